@@ -15,6 +15,9 @@ Names mirror the C ABI in ``include/rk_paged.h``:
 (rk_paged_decode_balanced_scratch_bytes), ``attn_decode_balanced``
 (rk_paged_attn_decode_balanced), ``kv_append`` (rk_paged_kv_append),
 ``plan_ragged`` (rk_paged_plan_ragged), ``attn_ragged`` (rk_paged_attn_ragged),
+``tables_extend`` (rk_paged_tables_extend), ``kv_append_q8`` (rk_paged_kv_append_q8),
+``decode_q8_scratch_bytes`` (rk_paged_decode_q8_scratch_bytes), ``attn_decode_q8``
+(rk_paged_attn_decode_q8), ``attn_prefill_q8`` (rk_paged_attn_prefill_q8),
 ``last_error``, ``policy``, ``abi_version``.
 """
 from __future__ import annotations
@@ -33,6 +36,7 @@ ERRORS = {
 }
 CODES = {v: k for k, v in ERRORS.items()}
 STATUS_PAGE_OOB, STATUS_KVLEN, STATUS_POSITION, STATUS_TIMEOUT, STATUS_RANGE = 1, 2, 4, 8, 16
+STATUS_SCALE, STATUS_POOL = 32, 64
 ABI_VERSION = 3
 SPLIT_STATIC_SCRATCH_BYTES = 16 << 20  # RK_PAGED_SPLIT_STATIC_SCRATCH_BYTES
 BALANCED_SCRATCH_BYTES = 4096 + 512 * 3088 * 4  # RK_PAGED_BALANCED_SCRATCH_BYTES
@@ -108,6 +112,19 @@ def load(path: str | None = None):
             [ctypes.c_uint64, vp, vp]
         lib.rk_paged_prefill_backward_workspace_bytes.restype = ctypes.c_int
         lib.rk_paged_prefill_backward_workspace_bytes.argtypes = [ctypes.POINTER(Plan), ctypes.POINTER(ctypes.c_uint64)]
+        lib.rk_paged_tables_extend.restype = ctypes.c_int
+        lib.rk_paged_tables_extend.argtypes = [ctypes.POINTER(Plan), vp, vp, vp, ctypes.c_int32] + [vp] * 7 + \
+            [ctypes.c_int32, vp, vp]
+        lib.rk_paged_kv_append_q8.restype = ctypes.c_int
+        lib.rk_paged_kv_append_q8.argtypes = [ctypes.POINTER(Plan), ctypes.c_int32] + [vp] * 10
+        lib.rk_paged_decode_q8_scratch_bytes.restype = ctypes.c_int
+        lib.rk_paged_decode_q8_scratch_bytes.argtypes = [ctypes.POINTER(Plan), ctypes.c_int32,
+                                                         ctypes.POINTER(ctypes.c_uint64)]
+        lib.rk_paged_attn_decode_q8.restype = ctypes.c_int
+        lib.rk_paged_attn_decode_q8.argtypes = [ctypes.POINTER(Plan), ctypes.c_int32] + [vp] * 11 + \
+            [ctypes.c_uint64, vp, vp]
+        lib.rk_paged_attn_prefill_q8.restype = ctypes.c_int
+        lib.rk_paged_attn_prefill_q8.argtypes = [ctypes.POINTER(Plan)] + [vp] * 12
         lib.rk_last_error.restype = ctypes.c_char_p
         lib.rk_last_error.argtypes = []
         lib.rk_paged_policy.restype = ctypes.c_char_p
@@ -403,6 +420,122 @@ def attn_ragged(p: Plan, max_q_len, qo_indptr, q, k_cache, v_cache, block_table,
     _expect(qo_indptr, (p.B + 1,), "qo_indptr")
     _launch(lambda pp, *r: load().rk_paged_attn_ragged(pp, int(max_q_len), _dptr(qo_indptr), *r), p, q,
             k_cache, v_cache, block_table, kv_lens, position_ids, out, lse, status, stream, ragged=True)
+
+
+def _pointers(tensors):
+    """Device pointers of ``(tensor, dtype, shape, name)`` entries, each checked:
+    type, shape (None: any), contiguous, on the current CUDA device (the one
+    that the call launches on)."""
+    import torch
+    for t, dt, shape, name in tensors:
+        if t.dtype != dt:
+            raise TypeError("%s must be %s (got %s)" % (name, dt, t.dtype))
+        if shape is not None and t.shape != shape:
+            raise ValueError("%s has shape %s, the call needs %s" % (name, tuple(t.shape), tuple(shape)))
+        if not t.is_cuda:
+            raise ValueError("%s: expected a CUDA tensor" % name)
+        if not t.is_contiguous():
+            raise ValueError("%s: expected a contiguous tensor" % name)
+    dev = torch.cuda.current_device()
+    ptrs = []
+    for t, _, _, name in tensors:
+        if t.get_device() != dev:
+            raise ValueError("%s is on device %d, the current device is %d" % (name, t.get_device(), dev))
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _status(status):
+    """Entry list of the optional status word."""
+    import torch
+    if status is None:
+        return []
+    if status.numel() < 1:
+        raise ValueError("status must hold at least one int32")
+    return [(status, torch.int32, None, "status")]
+
+
+def tables_extend(p: Plan, n_new, kv_lens, pool, taken, block_table, kv_lens_out, taken_out, qo_indptr,
+                  position_ids, slot_map, status=None, stream=None):
+    """rk_paged_tables_extend: the tables of a step from the rows' lengths ``kv_lens``
+    [B] and token counts ``n_new`` [B].  ``pool`` holds free page ids, of which
+    ``taken`` [1] are handed out; ``block_table`` [B, W] is written in place;
+    ``kv_lens_out`` and ``taken_out`` may be ``kv_lens`` and ``taken``.  All int32."""
+    import torch
+    i32 = torch.int32
+    B = p.B
+    if pool.dim() != 1 or position_ids.dim() != 1:
+        raise ValueError("pool and position_ids must have one dimension")
+    ptr = _pointers([(n_new, i32, (B,), "n_new"), (kv_lens, i32, (B,), "kv_lens"), (pool, i32, None, "pool"),
+                     (taken, i32, (1,), "taken"), (block_table, i32, (B, p.W), "block_table"),
+                     (kv_lens_out, i32, (B,), "kv_lens_out"), (taken_out, i32, (1,), "taken_out"),
+                     (qo_indptr, i32, (B + 1,), "qo_indptr"), (position_ids, i32, None, "position_ids"),
+                     (slot_map, i32, position_ids.shape, "slot_map")] + _status(status))
+    _check(load().rk_paged_tables_extend(ctypes.byref(p), ptr[0], ptr[1], ptr[2], pool.shape[0], *ptr[3:10],
+                                         slot_map.shape[0], ptr[10] if status is not None else None, _stream(stream)))
+
+
+def _q8_cache(p: Plan, k_cache, v_cache, k_scale, v_scale):
+    import torch
+    cache, scale = (p.num_pages, p.Hkv, p.page_size, p.D), (p.num_pages, p.Hkv)
+    return [(k_cache, torch.float8_e4m3fn, cache, "k_cache"), (v_cache, torch.float8_e4m3fn, cache, "v_cache"),
+            (k_scale, torch.float32, scale, "k_scale"), (v_scale, torch.float32, scale, "v_scale")]
+
+
+def kv_append_q8(p: Plan, k_new, v_new, slot_map, position_ids, k_cache, v_cache, k_scale, v_scale, status=None,
+                 stream=None):
+    """rk_paged_kv_append_q8: rotate (K), quantise and write k_new / v_new (bf16
+    [n, Hkv, D]) at the slots and positions of ``slot_map`` / ``position_ids`` (int32
+    [n]) into the e4m3 caches [num_pages, Hkv, 16, D] with their scales (float32
+    [num_pages, Hkv])."""
+    import torch
+    n = slot_map.numel()
+    new = (n, p.Hkv, p.D)
+    ptr = _pointers([(k_new, torch.bfloat16, new, "k_new"), (v_new, torch.bfloat16, new, "v_new"),
+                     (slot_map, torch.int32, (n,), "slot_map"),
+                     (position_ids, torch.int32, (n,), "position_ids")] +
+                    _q8_cache(p, k_cache, v_cache, k_scale, v_scale) + _status(status))
+    _check(load().rk_paged_kv_append_q8(ctypes.byref(p), n, *ptr[:8], ptr[8] if status is not None else None,
+                                        _stream(stream)))
+
+
+def decode_q8_scratch_bytes(p: Plan, split_tokens: int = 0) -> int:
+    """rk_paged_decode_q8_scratch_bytes: device scratch bytes of the 8-bit decode (0: none needed)."""
+    n = ctypes.c_uint64(0)
+    _check(load().rk_paged_decode_q8_scratch_bytes(ctypes.byref(p), int(split_tokens), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _attn_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse, status):
+    import torch
+    qs = (p.B, p.Hq, p.Sq, p.D)
+    return _pointers([(q, torch.bfloat16, qs, "q")] + _q8_cache(p, k_cache, v_cache, k_scale, v_scale) +
+                     [(block_table, torch.int32, (p.B, p.W), "block_table"), (kv_lens, torch.int32, (p.B,), "kv_lens"),
+                      (position_ids, torch.int32, (p.B, p.Sq), "position_ids"), (out, torch.bfloat16, qs, "out"),
+                      (lse, torch.float32, qs[:3], "lse")] + _status(status))
+
+
+def attn_decode_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse,
+                   scratch=None, split_tokens=0, status=None, stream=None):
+    """rk_paged_attn_decode_q8 on device tensors: decode over the 8-bit cache, in
+    fixed splits of ``split_tokens`` (0: the library's own) merged in order.
+    ``scratch`` is a CUDA tensor of at least ``decode_q8_scratch_bytes`` bytes (any
+    dtype; None where that is 0)."""
+    ptr = _attn_q8(p, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse, status)
+    sp, nbytes = None, 0
+    if scratch is not None:
+        sp = _pointers([(scratch, scratch.dtype, None, "scratch")])[0]
+        nbytes = scratch.numel() * scratch.element_size()
+    _check(load().rk_paged_attn_decode_q8(ctypes.byref(p), int(split_tokens), *ptr[:10], sp, nbytes,
+                                          ptr[10] if status is not None else None, _stream(stream)))
+
+
+def attn_prefill_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse,
+                    status=None, stream=None):
+    """rk_paged_attn_prefill_q8 on device tensors: causal chunked prefill over the 8-bit cache."""
+    ptr = _attn_q8(p, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse, status)
+    _check(load().rk_paged_attn_prefill_q8(ctypes.byref(p), *ptr[:10], ptr[10] if status is not None else None,
+                                           _stream(stream)))
 
 
 def run(mode: str, q, k_cache, v_cache, block_table, kv_lens, position_ids, plan_obj=None,

@@ -29,6 +29,9 @@ cudaError_t launch_backward_dkdv_tc(const CUtensorMap& qm, const CUtensorMap& om
 cudaError_t launch_backward_dq_tc(const CUtensorMap& qm, const CUtensorMap& om, const CUtensorMap& km,
                                   const CUtensorMap& vm, const BackwardArgs& a, cudaStream_t stream);
 cudaError_t launch_backward_rotate(const BackwardArgs& a, cudaStream_t stream);
+cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream);
+cudaError_t launch_append_q8(const AppendQ8Args& a, cudaStream_t stream);
+cudaError_t launch_attn_q8(const AttnQ8Args& a, cudaStream_t stream);
 }  // namespace rk
 
 namespace {
@@ -874,6 +877,201 @@ int rk_paged_attn_ragged(const rk_paged_plan_t* plan, int32_t max_q_len, const i
     // started while the decode launch drains: the two write disjoint rows
     cudaError_t e = rk::launch_prefill(qm, km, vm, a, st, true);
     if (e != cudaSuccess) return fail(RK_E_CUDA, "ragged prefill launch: %s", cudaGetErrorString(e));
+    return RK_OK;
+}
+
+}  // extern "C"
+
+// --------------------------------------------------------- 8-bit cache ----
+
+namespace {
+
+int check_plan(const rk_paged_plan_t* plan) {
+    if (!plan) return fail(RK_E_ARG, "plan is NULL");
+    if (plan->abi != RK_PAGED_ABI_VERSION)
+        return fail(RK_E_ARG, "plan ABI %u does not match library ABI %u (plan not filled by rk_paged_plan?)",
+                    plan->abi, RK_PAGED_ABI_VERSION);
+    return check_shape(plan->B, plan->Sq, plan->Hq, plan->Hkv, plan->D, plan->page_size, plan->num_pages, plan->W,
+                       plan->rope_theta, plan->rope_scale);
+}
+
+// Checks and arguments that the two attention calls share.
+int attn_q8_args(const rk_paged_plan_t* plan, const void* q, const void* k_cache, const void* v_cache,
+                 const float* k_scale, const float* v_scale, const int32_t* block_table_d, const int32_t* kv_lens_d,
+                 const int32_t* position_ids_d, void* out, float* lse, int32_t* status_d, rk::AttnQ8Args* a) {
+    int rc = check_plan(plan);
+    if (rc) return rc;
+    if (plan->B > 0 && plan->num_pages > 0 && (!k_scale || !v_scale)) return fail(RK_E_ARG, "k_scale / v_scale is NULL");
+    if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(status_d, 4))
+        return fail(RK_E_ARG, "k_scale, v_scale and status must be 4-byte aligned");
+    if ((rc = check_launch_common(plan, q, k_cache, v_cache, block_table_d, kv_lens_d, position_ids_d, out, lse))) return rc;
+    std::memset(a, 0, sizeof *a);
+    a->q = q;
+    a->k_cache = static_cast<const uint8_t*>(k_cache);
+    a->v_cache = static_cast<const uint8_t*>(v_cache);
+    a->k_scale = k_scale;
+    a->v_scale = v_scale;
+    a->block_table = block_table_d;
+    a->kv_lens = kv_lens_d;
+    a->position_ids = position_ids_d;
+    a->out = out;
+    a->lse = lse;
+    a->status = status_d;
+    a->B = plan->B;
+    a->Sq = plan->Sq;
+    a->Hq = plan->Hq;
+    a->Hkv = plan->Hkv;
+    a->G = plan->Hq / plan->Hkv;
+    a->W = plan->W;
+    a->num_pages = plan->num_pages;
+    a->qk_scale_log2 = (float)((1.0 / std::sqrt((double)plan->D)) * 1.4426950408889634074);
+    a->wait_limit_ns = plan->wait_limit_ns;
+    a->timeout_drill = plan->timeout_drill;
+    std::memcpy(a->rope_turns, plan->rope_turns, sizeof a->rope_turns);
+    return RK_OK;
+}
+
+int q8_split(int32_t* split_tokens) {
+    if (*split_tokens == 0) *split_tokens = RK_PAGED_Q8_SPLIT_TOKENS;
+    if (*split_tokens < 0 || *split_tokens % rk::PAGE != 0)
+        return fail(RK_E_ARG, "split_tokens must be 0 or a positive multiple of %d (got %d)", rk::PAGE, *split_tokens);
+    return RK_OK;
+}
+
+// Scratch of the 8-bit decode: none where the table holds one split at most.
+int64_t q8_scratch_need(const rk_paged_plan_t* plan, int32_t split_tokens) {
+    return split_count(plan, split_tokens) > 1 ? split_scratch_need(plan, split_tokens) : 0;
+}
+
+}  // namespace
+
+extern "C" {
+
+int rk_paged_tables_extend(const rk_paged_plan_t* plan, const int32_t* n_new_d, const int32_t* kv_lens_d,
+                           const int32_t* pool_d, int32_t n_pool, const int32_t* taken_d, int32_t* block_table_d,
+                           int32_t* kv_lens_out_d, int32_t* taken_out_d, int32_t* qo_indptr_d, int32_t* position_ids_d,
+                           int32_t* slot_map_d, int32_t cap, int32_t* status_d, rk_stream_t stream) {
+    g_err.clear();
+    int rc = check_plan(plan);
+    if (rc) return rc;
+    if (n_pool < 0 || cap < 0) return fail(RK_E_ARG, "n_pool and cap must be >= 0 (got %d, %d)", n_pool, cap);
+    if (plan->B > rk::TAB_MAX_ROWS)
+        return fail(RK_E_UNSUPPORTED, "%d rows: at most %d are supported", plan->B, rk::TAB_MAX_ROWS);
+    if (!taken_d || !taken_out_d || !qo_indptr_d || (n_pool > 0 && !pool_d) || (cap > 0 && (!position_ids_d || !slot_map_d)) ||
+        (plan->B > 0 && (!n_new_d || !kv_lens_d || !kv_lens_out_d || (plan->W > 0 && !block_table_d))))
+        return fail(RK_E_ARG, "null device pointer");
+    const void* all[] = {n_new_d,     kv_lens_d,   pool_d,         taken_d,    block_table_d, kv_lens_out_d,
+                         taken_out_d, qo_indptr_d, position_ids_d, slot_map_d, status_d};
+    for (const void* p : all)
+        if (!aligned(p, 4)) return fail(RK_E_ARG, "every array must be 4-byte aligned");
+    if ((rc = check_device())) return rc;
+    rk::TablesArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.n_new = n_new_d;
+    a.kv_lens = kv_lens_d;
+    a.pool = pool_d;
+    a.taken = taken_d;
+    a.block_table = block_table_d;
+    a.kv_lens_out = kv_lens_out_d;
+    a.taken_out = taken_out_d;
+    a.qo_indptr = qo_indptr_d;
+    a.position_ids = position_ids_d;
+    a.slot_map = slot_map_d;
+    a.status = status_d;
+    a.B = plan->B;
+    a.W = plan->W;
+    a.num_pages = plan->num_pages;
+    a.n_pool = n_pool;
+    a.cap = cap;
+    cudaError_t e = rk::launch_tables(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(RK_E_CUDA, "tables launch: %s", cudaGetErrorString(e));
+    return RK_OK;
+}
+
+int rk_paged_kv_append_q8(const rk_paged_plan_t* plan, int32_t n, const void* k_new, const void* v_new,
+                          const int32_t* slot_map_d, const int32_t* position_ids_d, void* k_cache, void* v_cache,
+                          float* k_scale, float* v_scale, int32_t* status_d, rk_stream_t stream) {
+    g_err.clear();
+    int rc = check_plan(plan);
+    if (rc) return rc;
+    if (n < 0) return fail(RK_E_ARG, "n must be >= 0 (got %d)", n);
+    if (n == 0) return RK_OK;
+    if (plan->num_pages == 0) return fail(RK_E_KVLEN, "appending %d tokens needs a non-empty page pool", n);
+    if (!k_new || !v_new || !slot_map_d || !position_ids_d || !k_cache || !v_cache || !k_scale || !v_scale)
+        return fail(RK_E_ARG, "null device pointer");
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return fail(RK_E_ARG, "k_new, v_new, k_cache and v_cache must be 16-byte aligned");
+    if (!aligned(slot_map_d, 4) || !aligned(position_ids_d, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+        !aligned(status_d, 4))
+        return fail(RK_E_ARG, "slots, positions and scales must be 4-byte aligned");
+    if ((rc = check_device())) return rc;
+    rk::AppendQ8Args a;
+    std::memset(&a, 0, sizeof a);
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.slot_map = slot_map_d;
+    a.position_ids = position_ids_d;
+    a.k_cache = static_cast<uint8_t*>(k_cache);
+    a.v_cache = static_cast<uint8_t*>(v_cache);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.status = status_d;
+    a.n = n;
+    a.Hkv = plan->Hkv;
+    a.num_pages = plan->num_pages;
+    std::memcpy(a.rope_turns, plan->rope_turns, sizeof a.rope_turns);
+    cudaError_t e = rk::launch_append_q8(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(RK_E_CUDA, "8-bit append launch: %s", cudaGetErrorString(e));
+    return RK_OK;
+}
+
+int rk_paged_decode_q8_scratch_bytes(const rk_paged_plan_t* plan, int32_t split_tokens, uint64_t* bytes) {
+    g_err.clear();
+    if (!plan || !bytes) return fail(RK_E_ARG, "plan and bytes must be non-null");
+    if (plan->abi != RK_PAGED_ABI_VERSION) return fail(RK_E_ARG, "plan ABI %u != %u", plan->abi, RK_PAGED_ABI_VERSION);
+    int rc = q8_split(&split_tokens);
+    if (rc) return rc;
+    *bytes = (uint64_t)q8_scratch_need(plan, split_tokens);
+    return RK_OK;
+}
+
+int rk_paged_attn_decode_q8(const rk_paged_plan_t* plan, int32_t split_tokens, const void* q, const void* k_cache,
+                            const void* v_cache, const float* k_scale, const float* v_scale, const int32_t* block_table_d,
+                            const int32_t* kv_lens_d, const int32_t* position_ids_d, void* out, float* lse, void* scratch,
+                            uint64_t scratch_bytes, int32_t* status_d, rk_stream_t stream) {
+    g_err.clear();
+    int rc = check_plan(plan);
+    if (rc) return rc;
+    if (plan->Sq != 1) return fail(RK_E_ARG, "decode needs a plan with Sq == 1 (got %d)", plan->Sq);
+    if ((rc = q8_split(&split_tokens))) return rc;
+    const int64_t need = q8_scratch_need(plan, split_tokens);
+    if (need > 0) {
+        if (!scratch || !aligned(scratch, 16))
+            return fail(RK_E_ARG, "8-bit decode scratch must be a non-null 16-byte aligned device pointer");
+        if ((uint64_t)need > scratch_bytes)
+            return fail(RK_E_ARG, "8-bit decode scratch too small: %lld bytes needed, %llu given", (long long)need,
+                        (unsigned long long)scratch_bytes);
+    }
+    rk::AttnQ8Args a;
+    rc = attn_q8_args(plan, q, k_cache, v_cache, k_scale, v_scale, block_table_d, kv_lens_d, position_ids_d, out, lse, status_d,
+                      &a);
+    if (rc || plan->B == 0) return rc;
+    cudaError_t e = rk::launch_attn_q8(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(RK_E_CUDA, "8-bit decode launch: %s", cudaGetErrorString(e));
+    return RK_OK;
+}
+
+int rk_paged_attn_prefill_q8(const rk_paged_plan_t* plan, const void* q, const void* k_cache, const void* v_cache,
+                             const float* k_scale, const float* v_scale, const int32_t* block_table_d,
+                             const int32_t* kv_lens_d, const int32_t* position_ids_d, void* out, float* lse,
+                             int32_t* status_d, rk_stream_t stream) {
+    g_err.clear();
+    rk::AttnQ8Args a;
+    int rc = attn_q8_args(plan, q, k_cache, v_cache, k_scale, v_scale, block_table_d, kv_lens_d, position_ids_d, out, lse,
+                          status_d, &a);
+    if (rc || plan->B == 0) return rc;
+    cudaError_t e = rk::launch_attn_q8(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(RK_E_CUDA, "8-bit prefill launch: %s", cudaGetErrorString(e));
     return RK_OK;
 }
 

@@ -81,7 +81,11 @@ enum rk_status {
 #define RK_STATUS_POSITION (1 << 2) /* a negative query position */
 #define RK_STATUS_TIMEOUT (1 << 3)  /* an internal pipeline wait gave up (kernel returned early) */
 #define RK_STATUS_RANGE (1 << 4)    /* decode, prefill, ragged, backward: a pre-RoPE q or k element the
-                                       kernel reads has |x| >= 2^15 (the FP16 score operand limit) */
+                                       kernel reads has |x| >= 2^15 (the FP16 score operand limit);
+                                       8-bit cache calls: see there */
+#define RK_STATUS_SCALE (1 << 5)   /* a scale of the 8-bit cache that is not a positive normal number (append:
+                                       not a power of two in [2^-64, 2^57]) */
+#define RK_STATUS_POOL (1 << 6)    /* rk_paged_tables_extend: a row's tokens or new pages do not fit */
 
 /* Opaque stream handle; identical to cudaStream_t / CUstream. */
 typedef struct CUstream_st *rk_stream_t;
@@ -453,6 +457,139 @@ int rk_paged_attn_prefill_backward(const rk_paged_plan_t *plan, const void *q, c
  * Hkv W 16 D + 4 B Hq Sq bytes, each part rounded up to 256).  Host only;
  * RK_E_ARG for a null plan / bytes or a plan of another ABI. */
 int rk_paged_prefill_backward_workspace_bytes(const rk_paged_plan_t *plan, uint64_t *bytes);
+
+/*
+ * The 8-bit cache: four calls that make up a serving step over a page cache
+ * held in 8 bits, half the bytes of the BF16 cache.
+ *
+ *   rk_paged_tables_extend   the step's block table, lengths, indptr, positions
+ *                            and slots from the rows' token counts
+ *   rk_paged_kv_append_q8    rotate K, quantise K and V, write them
+ *   rk_paged_attn_decode_q8, rk_paged_attn_prefill_q8
+ *                            the attention calls over that cache
+ *
+ * Semantics shared by the three cache calls (B, Hq, Hkv, D, W, num_pages and
+ * the RoPE constants from the plan, as everywhere):
+ *   k_cache, v_cache  e4m3 codes [num_pages, Hkv, 16, D]: the 16 tokens of a
+ *                page and one KV head are one contiguous 2 KiB block (unlike the
+ *                NHD BF16 cache); 16-byte aligned
+ *   k_scale, v_scale  fp32 [num_pages, Hkv]; a value is code * scale
+ *   K is stored ROTATED at its token's position (the BF16 cache holds it
+ *   pre-RoPE): the append rotates once, the attention calls rotate only q.
+ * The page table, positions, visibility rule (t <= position, t < kv_len), GQA
+ * grouping, out and lse are those of the BF16 calls.
+ */
+
+/*
+ * rk_paged_tables_extend -- the tables of a step, built on the device: every
+ * row b gets n_new_d[b] tokens behind its kv_lens_d[b], with new pages from a
+ * pool where it needs them.  Everything is device memory, so a captured graph
+ * of steps advances by itself.
+ *   n_new_d       int32 [B], >= 0
+ *   kv_lens_d     int32 [B], lengths before the step
+ *   pool_d, n_pool  int32 [n_pool]: ids of free pages, all different and in no
+ *                row's table; pool_d[taken ..] are handed out in order, row by row
+ *   taken_d       int32 [1]: how many are handed out already
+ *   block_table_d int32 [B, W], in place: entries ceil(len / 16) .. of the new
+ *                pages are written, no other entry is touched
+ *   kv_lens_out_d int32 [B], taken_out_d int32 [1]: after the step (each may be
+ *                the array that it follows: everything is read first)
+ *   qo_indptr_d   int32 [B + 1]: row b's tokens are qo_indptr[b] ..
+ *                qo_indptr[b + 1] - 1 of the packed order
+ *   position_ids_d, slot_map_d  int32 [cap]: position in the row and slot (page
+ *                * 16 + position % 16) of each token; -1 behind the last one
+ *   cap           >= 0, the arrays' size (the most tokens that a step can have)
+ * The other arrays must not overlap each other.  A row stays as it was, without
+ * tokens, and the status word says why, if its length is negative or would
+ * pass W * 16 or its count is negative (RK_STATUS_KVLEN), or if the tokens of the
+ * rows up to it (rows without a place left out) pass cap or their new pages
+ * pass the pool while it needs one (RK_STATUS_POOL; also taken outside
+ * [0, n_pool], which leaves no page).  A page id outside [0, num_pages), from the
+ * pool or in a started page's entry, gives slot -1 and RK_STATUS_PAGE_OOB.
+ * Plan: B, W, num_pages (B at most 16384, else RK_E_UNSUPPORTED).  One launch, no
+ * allocation, no host synchronisation.  Errors: RK_E_ARG (null or misaligned
+ * pointer, negative n_pool or cap), RK_E_DEVICE, RK_E_CUDA.
+ */
+int rk_paged_tables_extend(const rk_paged_plan_t *plan, const int32_t *n_new_d, const int32_t *kv_lens_d,
+                           const int32_t *pool_d, int32_t n_pool, const int32_t *taken_d,
+                           int32_t *block_table_d, int32_t *kv_lens_out_d, int32_t *taken_out_d,
+                           int32_t *qo_indptr_d, int32_t *position_ids_d, int32_t *slot_map_d, int32_t cap,
+                           int32_t *status_d, rk_stream_t stream);
+
+/*
+ * rk_paged_kv_append_q8 -- quantise n tokens' K and V into the 8-bit cache.
+ *   k_new, v_new  bf16 [n, Hkv, D] DEVICE, pre-RoPE, contiguous, 16-byte aligned
+ *   slot_map_d    int32 [n]: page * 16 + slot of each token, -1 to skip it
+ *   position_ids_d  int32 [n]: the position K is rotated at
+ *   k_cache, v_cache, k_scale, v_scale  written in place
+ * Tokens of a page come in the order of its slots, in one run of neighbours per
+ * call (as rk_paged_tables_extend lays them out); a token at slot 0 starts its
+ * page anew, a token at another slot follows those that the page holds.  A
+ * block's scale is 2^E with E the largest, over its tokens, of
+ * floor(log2 max|x|) - 7 of the token's bf16 inputs, at least -64; codes are the
+ * values over that scale rounded to 4 significant bits (half to even), 0 below
+ * 2^-6.  When a later token raises E the block's earlier codes move along, and
+ * the block is bit for bit the same as if all its tokens had come in one call.
+ * Slots behind a page's last token are left as they are.  Two runs of one call
+ * on the same page (a page in two rows, a slot twice) give unspecified codes
+ * and scales for that page.
+ * Status: RK_STATUS_PAGE_OOB (slot outside [-1, num_pages * 16)), RK_STATUS_POSITION
+ * (negative position): the token is not written; RK_STATUS_RANGE (an input of 2^64
+ * or more, or not finite): that token's codes of the tensor become NaN, which the
+ * attention calls report, and the scale goes without it; RK_STATUS_SCALE (a started
+ * page whose scale is no power of two in [2^-64, 2^57]): none of the run's tokens is
+ * written for that head.
+ * Plan: Hkv, D, num_pages and the RoPE constants.  n = 0 is a no-op.  One launch, no
+ * allocation, no host synchronisation.  Errors: RK_E_ARG (null or misaligned pointer,
+ * n < 0), RK_E_KVLEN (tokens but no page pool), RK_E_DEVICE, RK_E_CUDA.
+ */
+int rk_paged_kv_append_q8(const rk_paged_plan_t *plan, int32_t n, const void *k_new, const void *v_new,
+                          const int32_t *slot_map_d, const int32_t *position_ids_d, void *k_cache,
+                          void *v_cache, float *k_scale, float *v_scale, int32_t *status_d,
+                          rk_stream_t stream);
+
+/*
+ * rk_paged_attn_decode_q8 -- one query per row (plan->Sq must be 1) over the
+ * 8-bit cache: q, block_table, kv_lens, position_ids, out, lse as in
+ * rk_paged_attn_decode.  Every row's keys are cut at fixed logical offsets
+ * s * split_tokens; the splits are reduced apart and merged in ascending order
+ * in FP32 (the policy of rk_paged_attn_decode_split), so a row's result depends on
+ * split_tokens and not on the batch, the table width or the grid.
+ *   split_tokens  a positive multiple of 16, or 0 for RK_PAGED_Q8_SPLIT_TOKENS
+ *   scratch       DEVICE, 16-byte aligned, at least
+ *                rk_paged_decode_q8_scratch_bytes bytes; nothing in it needs
+ *                initialising; may be NULL where that is 0 (the table holds no
+ *                more than one split).  Two calls in flight at once must not share
+ *                it (two captured graphs that may run at once included).
+ * Status and failed rows (out = 0, lse = NaN): RK_STATUS_KVLEN, _POSITION, _PAGE_OOB
+ * as in the BF16 call; RK_STATUS_SCALE (a scale of a visible page that is not a
+ * positive normal number) and RK_STATUS_RANGE (a q element of 2^64 or more or not
+ * finite, a NaN code among the visible tokens, scores or sums beyond FP32) fail the
+ * query heads that meet them, and may fail the other query heads of that KV head.
+ * What lies past kv_len or the position is not read as a value (it may be anything).
+ * Errors: as rk_paged_attn_decode_split.
+ */
+#define RK_PAGED_Q8_SPLIT_TOKENS 512
+int rk_paged_decode_q8_scratch_bytes(const rk_paged_plan_t *plan, int32_t split_tokens, uint64_t *bytes);
+int rk_paged_attn_decode_q8(const rk_paged_plan_t *plan, int32_t split_tokens, const void *q,
+                            const void *k_cache, const void *v_cache, const float *k_scale,
+                            const float *v_scale, const int32_t *block_table_d, const int32_t *kv_lens_d,
+                            const int32_t *position_ids_d, void *out, float *lse, void *scratch,
+                            uint64_t scratch_bytes, int32_t *status_d, rk_stream_t stream);
+
+/*
+ * rk_paged_attn_prefill_q8 -- causal chunked prefill (any plan->Sq >= 1) over the
+ * 8-bit cache, which already holds the chunk's own K and V: the arguments of
+ * rk_paged_attn_prefill with the scales.  One ascending pass over the keys per
+ * query, no split.  Status and failed rows as in rk_paged_attn_decode_q8, where what a
+ * query meets is what its q-tile reads (keys up to the largest position of the
+ * tile's queries).  Errors: as rk_paged_attn_prefill.
+ */
+int rk_paged_attn_prefill_q8(const rk_paged_plan_t *plan, const void *q, const void *k_cache,
+                             const void *v_cache, const float *k_scale, const float *v_scale,
+                             const int32_t *block_table_d, const int32_t *kv_lens_d,
+                             const int32_t *position_ids_d, void *out, float *lse, int32_t *status_d,
+                             rk_stream_t stream);
 
 /* Message of the last failing call on this thread ("" if none).  The
  * pointer stays valid until the next library call on the same thread. */
