@@ -16,6 +16,9 @@
 // of the block's tokens.  Leaving subnormals out costs at most 2^-7 2^E, below
 // 2^-14 of the block's largest value; the 4-bit rounding of that value is 2^-5.
 // E comes from the inputs' exponent bits, never from a rounded product.
+// The rotation is in FP32; a pair with a result that FP32 cannot place on one
+// side of a rounding border is done again in FP64, so that codes are those of
+// the real number (a few in a million would be one step off otherwise).
 //
 // Work: a run is the tokens of one call on one page (slots that follow one
 // another).  A CTA takes one KV head of the runs that start in a window of 16
@@ -23,7 +26,7 @@
 // 64 + 8u ..), so a thread's loads are 16 bytes and 8 lanes cover 128.  A run
 // may go on for 15 tokens past the window, in a second pass.  Bound by latency at
 // decode sizes, by bytes (512 in, 256 out a token and head) at chunk sizes.
-#include "rk_device.cuh"
+#include "q8_device.cuh"
 
 namespace rk {
 
@@ -32,12 +35,6 @@ namespace {
 constexpr int AQ_THREADS = 128;
 constexpr int AQ_WINDOW = 16;
 
-// Two floats -> packed e4m3 (lo in the low byte), half to even.
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ float flush_code(float v) { return fabsf(v) < 31.0f / 2048.0f ? 0.0f : v; }
 
 // Lower the exponent of four codes by `by` > 0; below the smallest normal: 0.
@@ -69,8 +66,30 @@ __device__ __forceinline__ uint32_t token_amax(const Half8& x) {
     for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     return m;
 }
-__device__ __forceinline__ int exponent_of(uint32_t amax_bits) { return max((int)(amax_bits >> 7) - 127 - 7, Q8_E_MIN); }
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// What FP32 may be off by in a rotated value, relative to |lo| + |hi|: the angle
+// of rope_cos_sin is off by at most 2 pi 2^-32 and 2^-24 of itself (2^-22.3 at
+// pi), its sine and cosine by 2^-21.2, the two products and the sum by 2^-23.
+constexpr float ROT_ERR = 1.0f / (1 << 19);
+
+// A double as a float that rounds to 4 bits as the double does: cut off, and the
+// last bit set if something was lost.
+__device__ __forceinline__ float to_odd(double x) {
+    const float r = __double2float_rz(x);
+    return (double)r != x ? __int_as_float(__float_as_int(r) | 1) : r;
+}
+
+// The rotation of one pair in FP64 (angle in turns from the 0.64 fixed-point rate).
+__device__ __noinline__ float2 rotate_exact(float lo, float hi, uint32_t pos, uint64_t turns) {
+    double sn, c;
+    sincospi(ldexp((double)(long long)(pos * turns), -63), &sn, &c);
+    return make_float2(to_odd((double)lo * c - (double)hi * sn), to_odd((double)hi * c + (double)lo * sn));
+}
+
+// Whether codes of v 2^-E and of a value up to d away may differ.
+__device__ __forceinline__ bool near_border(float v0, float v1, float d) {
+    return cvt_e4m3x2(flush_code(v0 - d), flush_code(v1 - d)) != cvt_e4m3x2(flush_code(v0 + d), flush_code(v1 + d));
+}
 
 __device__ __forceinline__ uint2 pack8(const float (&y)[8], float inv) {
     uint32_t w[4];
@@ -154,8 +173,8 @@ __global__ void __launch_bounds__(AQ_THREADS) append_q8_kernel(const __grid_cons
             if (bk) ok_k &= ~(1 << p); else ok_k |= 1 << p;
             if (bv) ok_v &= ~(1 << p); else ok_v |= 1 << p;
             if (u == 0) {
-                s_ek[t] = bk ? Q8_E_MIN : exponent_of(mk);
-                s_ev[t] = bv ? Q8_E_MIN : exponent_of(mv);
+                s_ek[t] = bk ? Q8_E_MIN : q8_exponent(mk);
+                s_ev[t] = bv ? Q8_E_MIN : q8_exponent(mv);
                 if ((bk || bv) && a.status) atomicOr(a.status, RK_STATUS_RANGE);
             }
         }
@@ -235,6 +254,7 @@ __global__ void __launch_bounds__(AQ_THREADS) append_q8_kernel(const __grid_cons
             const uint32_t lw[4] = {k[p].lo.x, k[p].lo.y, k[p].lo.z, k[p].lo.w};
             const uint32_t hw[4] = {k[p].hi.x, k[p].hi.y, k[p].hi.z, k[p].hi.w};
             float yl[8], yh[8];
+            const float inv = pow2(-ek);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float lo = (i & 1) ? bf16hi(lw[i >> 1]) : bf16lo(lw[i >> 1]);
@@ -243,8 +263,13 @@ __global__ void __launch_bounds__(AQ_THREADS) append_q8_kernel(const __grid_cons
                 rope_cos_sin(pos, a.rope_turns[8 * u + i], c, sn);
                 yl[i] = fmaf(-hi, sn, lo * c);
                 yh[i] = fmaf(lo, sn, hi * c);
+                const float d = (fabsf(lo) + fabsf(hi)) * ROT_ERR * inv;
+                if (near_border(yl[i] * inv, yh[i] * inv, d)) {
+                    const float2 y = rotate_exact(lo, hi, pos, a.rope_turns[8 * u + i]);
+                    yl[i] = y.x;
+                    yh[i] = y.y;
+                }
             }
-            const float inv = pow2(-ek);
             const bool good = (ok_k >> p) & 1;
             *reinterpret_cast<uint2*>(kb + s * HEAD_DIM + 8 * u) = good ? pack8(yl, inv) : nan8;
             *reinterpret_cast<uint2*>(kb + s * HEAD_DIM + 64 + 8 * u) = good ? pack8(yh, inv) : nan8;

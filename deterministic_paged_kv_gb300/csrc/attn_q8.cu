@@ -2,20 +2,11 @@
 // and query head: the simplest kernel that serves every case.  Keys in chunks
 // of 128, one key's score per thread, one pass with the running maximum and
 // sum, then one output dimension per thread.
-#include <cuda_fp16.h>
-
-#include "rk_device.cuh"
+#include "q8_device.cuh"
 
 namespace rk {
 
 namespace {
-
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t w) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(w));
-    const __half2 x = *reinterpret_cast<__half2*>(&h);
-    return __half22float2(x);
-}
 
 __global__ void __launch_bounds__(128) attn_q8_kernel(const __grid_constant__ AttnQ8Args a) {
     __shared__ float qs[HEAD_DIM], ps[128], red[4];
@@ -65,7 +56,7 @@ __global__ void __launch_bounds__(128) attn_q8_kernel(const __grid_constant__ At
                     const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 p0 = e4m3x2_to_float2((uint16_t)ww[e]), p1 = e4m3x2_to_float2((uint16_t)(ww[e] >> 16));
+                        const float2 p0 = e4m3x2_to_float2(ww[e]), p1 = e4m3x2_to_float2(ww[e] >> 16);
                         const float* qq = qs + c * 16 + e * 4;
                         acc += qq[0] * p0.x + qq[1] * p0.y + qq[2] * p1.x + qq[3] * p1.y;
                     }

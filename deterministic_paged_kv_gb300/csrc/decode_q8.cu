@@ -1,0 +1,774 @@
+// decode_q8.cu -- one-query attention over the 8-bit page cache (tcgen05, TMA).
+//
+// Operation: the paged decode of "flashinfer_fa2 backend for Ada (SM89)" with a
+// fixed split of each row's keys ("WS2 PR7 Fused Attention Backend Alignment",
+// "Split-KV Policy", fixed:<N> in logical tokens), over e4m3 codes whose K was
+// rotated when it was written.
+//
+// What bounds it: the cache's bytes (256 a token and KV head).  At half the
+// bytes of a BF16 cache there is no time to convert codes, so none is converted:
+// K and V go by TMA from the cache into swizzled shared memory and from there
+// into kind::f8f6f4 MMAs as they are.  What multiplies them is split into e4m3
+// parts instead, which is cheap because it is small:
+//   q, rotated and scaled to below 362 by a power of two per head, is four parts
+//   (two at 1, two at 2^-8), the G heads' parts being columns of one operand;
+//   the softmax weights, scaled to at most 256, are three parts.
+// Products of e4m3 values are exact and the sums are FP32, so a score has the
+// precision of q in about 16 bits and a weight in 12.
+//
+// With S^T = K q^T [128 tokens x 4 G] and O^T = V^T p^T [128 dims x 3 G] both
+// operands that come from the cache are A operands in the layout they land in:
+// K K-major, V MN-major.  V's page scale enters as an addition to the exponent,
+//   w_t = z_t + log2(vs_t),  p'_t = 2^(w_t - max w),  l = sum p'_t / vs_t,
+//   o = sum p'_t vcode_t,  out = o / l,
+// with z_t the score in the log2 domain.
+//
+// Work: an item is a split of one (row, KV head), taken in steps of up to 512
+// tokens (4 tiles of 128); within a step the softmax is plain (one maximum over
+// its tokens), steps and splits are joined with the running maximum in FP32.
+// A persistent grid of one CTA per SM takes items c, c + grid, ... of the list
+// ordered by row, split, KV head, so neighbouring CTAs read neighbouring blocks.
+// Roles (8 warps):
+//   warp 0     TMA producer: lane p loads page p of a step's K, then of its V;
+//   warp 1     MMA issuer;
+//   warp 2     q: rotates the item's query heads, splits them into parts;
+//   warp 3     metadata: walks the items, page ids and scales of each step;
+//   warps 4-7  softmax: thread t has token t of every tile, and output dim t.
+// Nothing depends on B, W or the grid.
+#include <atomic>
+#include <cstring>
+
+#include "q8_device.cuh"
+
+namespace rk {
+
+namespace {
+
+constexpr int DQ_THREADS = 256;
+constexpr int DQ_TILE = 128;                      // tokens of a tile
+constexpr int DQ_TILE_BYTES = DQ_TILE * HEAD_DIM;  // 16 KiB
+constexpr int DQ_TILES = 4;                       // tiles of a step
+constexpr int DQ_STEP = DQ_TILE * DQ_TILES;
+constexpr int DQ_PAGES = DQ_STEP / PAGE;          // 32: one lane each
+constexpr int DQ_STAGES = 12;                     // 192 KiB on the way or in use
+constexpr int DQ_SLOTS = 4;                       // steps the metadata runs ahead
+constexpr int DQ_PRE = 1024;                      // row groups of the item list
+constexpr int DQ_TMEM_COLS = 256;
+constexpr int DQ_TMEM_O = 128;                    // S in columns [0, 128), O behind it
+
+template <int G>
+struct DqShape {
+    static constexpr int NS = 4 * G < 16 ? 16 : 4 * G;  // columns of S: part * G + head
+    static constexpr int NP = 3 * G <= 16 ? 16 : 32;    // columns of O
+};
+constexpr int DQ_Q_BYTES = 32 * 128, DQ_P_BYTES = 32 * 128;
+constexpr int DQ_OFF_Q = DQ_STAGES * DQ_TILE_BYTES;      // two q operands
+constexpr int DQ_OFF_P = DQ_OFF_Q + 2 * DQ_Q_BYTES;      // a step's weights, one operand per tile
+constexpr int DQ_OFF_CTRL = DQ_OFF_P + DQ_TILES * DQ_P_BYTES;
+
+struct DqStep {
+    int b, h, split;   // row, KV head, split
+    int n_splits;      // of the row
+    int cnt;           // tokens of the step (0: nothing to compute)
+    int first, last;   // of the item
+    int item;          // index in the item list; -1: no more
+    int bad;           // RK_STATUS_* bits
+};
+
+struct DqCtrl {
+    uint64_t full[DQ_STAGES], empty[DQ_STAGES];
+    uint64_t id_full[DQ_SLOTS], sc_full[DQ_SLOTS], slot_empty[DQ_SLOTS];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full, p_ready, o_full;
+    uint64_t never;
+    uint32_t tmem_base;
+    PipeCtl pipe;
+    int total;                       // row splits of the batch
+    int scan[DQ_THREADS / 32];
+    DqStep step[DQ_SLOTS];
+    int ids[DQ_SLOTS][DQ_PAGES];
+    alignas(16) float4 sc[DQ_SLOTS][DQ_PAGES];  // k scale, log2 of v's, 1 / v's
+    float qscale[2][8];              // score factor of each head (log2 domain)
+    int qbad[2];                     // heads whose query is out of range, a bit each
+    float red[4][8];
+    float lred[4][8];
+    int fred[4];
+    int pre[DQ_PRE + 1];             // row splits before each group of rows
+};
+constexpr int DQ_SMEM_BYTES = DQ_OFF_CTRL + (int)sizeof(DqCtrl);
+static_assert(DQ_SMEM_BYTES <= 232448, "8-bit decode shared memory above the 227 KiB opt-in limit");
+
+// Visible keys of a row (0 where its metadata is unsafe) and its status bits.
+__device__ __forceinline__ int row_keys(const AttnQ8Args& a, int b, int& bad) {
+    const int kv = a.kv_lens[b], pos = a.position_ids[b];
+    bad = (kv < 0 || kv > a.W * PAGE) ? RK_STATUS_KVLEN : 0;
+    if (pos < 0) bad |= RK_STATUS_POSITION;
+    return bad ? 0 : (pos < kv ? pos + 1 : kv);
+}
+__device__ __forceinline__ int splits_of(int n, int split) { return n > 0 ? (n + split - 1) / split : 1; }
+
+// Row and split of entry rs of the list of row splits.
+__device__ __forceinline__ void find_row(const AttnQ8Args& a, const DqCtrl* c, int rs, int& b, int& s, int& n, int& bad) {
+    const int per = (a.B + DQ_PRE - 1) / DQ_PRE, groups = (a.B + per - 1) / per;
+    int lo = 0, hi = groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (c->pre[mid] <= rs) lo = mid;
+        else hi = mid;
+    }
+    b = lo * per;
+    s = rs - c->pre[lo];
+    while (true) {
+        n = row_keys(a, b, bad);
+        const int k = splits_of(n, a.split_tokens);
+        if (s < k || b + 1 >= a.B) return;
+        s -= k;
+        ++b;
+    }
+}
+
+// An item's result: head g of the KV head, dim d (one thread each); o over l.
+__device__ __forceinline__ void write_item(const AttnQ8Args& a, const DqStep& st, int g, int d, float o, float lse2) {
+    const size_t bh = (size_t)st.b * a.Hq + st.h * a.G + g;
+    if (a.n_splits > 1) {
+        a.o_part[(bh * a.n_splits + st.split) * HEAD_DIM + d] = o;
+        if (d == 0) a.lse_part[bh * a.n_splits + st.split] = lse2;
+    } else {
+        reinterpret_cast<__nv_bfloat16*>(a.out)[bh * HEAD_DIM + d] = __float2bfloat16_rn(o);
+        if (d == 0) a.lse[bh] = lse2 * 0.693147180559945309f;
+    }
+}
+
+template <int G>
+__global__ void __launch_bounds__(DQ_THREADS, 1)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const __grid_constant__ AttnQ8Args a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw;
+    DqCtrl* c = reinterpret_cast<DqCtrl*>(sm + DQ_OFF_CTRL);
+    const uint32_t s_base = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int NS = DqShape<G>::NS, NP = DqShape<G>::NP;
+    griddep_launch_dependents();  // the merge may become resident; it waits for this grid's end
+
+    // ---- set-up: barriers, tensor memory, operands that stay zero, the item list ----
+    if (tid == 0) {
+        c->pipe.abort = 0;
+        c->pipe.limit_ns = wait_limit(a.wait_limit_ns);
+        for (int i = 0; i < DQ_STAGES; ++i) {
+            mbar_init(smem_u32(&c->full[i]), 1);
+            mbar_init(smem_u32(&c->empty[i]), 1);
+        }
+        for (int i = 0; i < DQ_SLOTS; ++i) {
+            mbar_init(smem_u32(&c->id_full[i]), 1);
+            mbar_init(smem_u32(&c->sc_full[i]), 1);
+            mbar_init(smem_u32(&c->slot_empty[i]), 7);  // producer, issuer, q, four softmax warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&c->q_full[i]), 1);
+            mbar_init(smem_u32(&c->q_empty[i]), 5);     // issuer's commit, four softmax warps
+        }
+        mbar_init(smem_u32(&c->s_full), 1);
+        mbar_init(smem_u32(&c->p_ready), 128);
+        mbar_init(smem_u32(&c->o_full), 1);
+        mbar_init(smem_u32(&c->never), 1);
+        fence_mbar_init();
+    }
+    for (int i = tid; i < (2 * DQ_Q_BYTES + DQ_TILES * DQ_P_BYTES) / 16; i += DQ_THREADS)
+        reinterpret_cast<uint4*>(sm + DQ_OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&c->tmem_base), DQ_TMEM_COLS);
+        tmem_relinquish();
+    }
+    {
+        // Row splits before each group of `per` rows.  Threads take DQ_PRE / 256 groups each.
+        const int per = (a.B + DQ_PRE - 1) / DQ_PRE, groups = (a.B + per - 1) / per;
+        constexpr int MINE = DQ_PRE / DQ_THREADS;
+        int cnt[MINE], sum = 0;
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+            cnt[i] = 0;
+            const int gr = tid * MINE + i;
+            if (gr < groups) {
+                for (int b = gr * per; b < min(a.B, gr * per + per); ++b) {
+                    int bad;
+                    const int n = row_keys(a, b, bad);
+                    cnt[i] += splits_of(n, a.split_tokens);
+                }
+            }
+            sum += cnt[i];
+        }
+        int v = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += t;
+        }
+        if (lane == 31) c->scan[warp] = v;
+        __syncthreads();
+        int base = v - sum;
+        for (int w = 0; w < warp; ++w) base += c->scan[w];
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+            c->pre[tid * MINE + i] = base;
+            base += cnt[i];
+        }
+        if (tid == DQ_THREADS - 1) c->total = base;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c->tmem_base;
+    PipeCtl* pc = &c->pipe;
+    const long long items = (long long)c->total * a.Hkv;
+
+    if (warp == 3) {
+        // ==================================================== metadata ====
+        int slot = 0, use = 0;  // ring position and how often it went round
+        bool ok = true;
+        for (long long it = blockIdx.x; ok; it += gridDim.x) {
+            DqStep st{};
+            st.item = -1;
+            int n = 0, t0 = 0, t1 = 0;
+            if (it < items) {
+                st.item = (int)it;
+                st.h = (int)(it % a.Hkv);
+                find_row(a, c, (int)(it / a.Hkv), st.b, st.split, n, st.bad);
+                st.n_splits = splits_of(n, a.split_tokens);
+                t0 = st.split * a.split_tokens;
+                t1 = min(n, t0 + a.split_tokens);
+            }
+            const int32_t* bt = a.block_table + (size_t)st.b * a.W;
+            int id = lane * PAGE < t1 - t0 ? __ldg(bt + t0 / PAGE + lane) : 0;
+            for (int t = t0; ok; t += DQ_STEP) {
+                const int cnt = max(0, min(DQ_STEP, t1 - t));
+                const bool mine = lane * PAGE < cnt;
+                const bool oob = mine && (id < 0 || id >= a.num_pages);
+                st.first = t == t0;
+                st.last = t + DQ_STEP >= t1;
+                st.cnt = cnt;
+                if (__any_sync(0xffffffffu, oob)) {
+                    st.bad |= RK_STATUS_PAGE_OOB;
+                    st.cnt = 0;
+                }
+                int good = 1;
+                if (lane == 0) good = mbar_wait(smem_u32(&c->slot_empty[slot]), (uint32_t)((use & 1) ^ 1), pc);
+                if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
+                c->ids[slot][lane] = id;
+                if (lane == 0) c->step[slot] = st;  // bad scales are added below, before sc_full
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c->id_full[slot]));
+                // the next step's page ids travel while this step's scales do
+                const int cur = id;
+                id = !st.last && lane * PAGE < t1 - t - DQ_STEP ? __ldg(bt + (t + DQ_STEP) / PAGE + lane) : 0;
+                float ks = 1.0f, vs = 1.0f;
+                if (mine && st.cnt > 0) {
+                    const size_t block = (size_t)cur * a.Hkv + st.h;
+                    ks = __ldg(a.k_scale + block);
+                    vs = __ldg(a.v_scale + block);
+                }
+                const bool odd = !scale_ok(ks) || !scale_ok(vs);
+                if (odd) ks = vs = 1.0f;
+                c->sc[slot][lane] = make_float4(ks, __log2f(vs), 1.0f / vs, 0.0f);
+                if (__any_sync(0xffffffffu, odd) && lane == 0) c->step[slot].bad = st.bad | RK_STATUS_SCALE;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c->sc_full[slot]));
+                if (++slot == DQ_SLOTS) {
+                    slot = 0;
+                    ++use;
+                }
+                st.bad = 0;  // reported once
+                if (st.last) break;
+            }
+            if (st.item < 0) break;
+        }
+    } else if (warp == 0) {
+        // ==================================================== producer ====
+        if (lane == 0) {
+            prefetch_tmap(&kmap);
+            prefetch_tmap(&vmap);
+        }
+        int slot = 0, use = 0, n = 0;  // n: tiles issued
+        bool ok = true;
+        while (ok) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->id_full[slot]), (uint32_t)(use & 1), pc)))) break;
+            const volatile DqStep* st = &c->step[slot];
+            const int cnt = st->cnt, h = st->h;
+            if (st->item < 0) break;
+            const int id = c->ids[slot][lane];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
+            if (++slot == DQ_SLOTS) {
+                slot = 0;
+                ++use;
+            }
+            const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE, pages = (cnt + PAGE - 1) / PAGE;
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+                for (int j = 0; j < tiles; ++j, ++n) {
+                    const int stg = n % DQ_STAGES;
+                    int good = 1;
+                    if (lane == 0) {
+                        good = mbar_wait(smem_u32(&c->empty[stg]), (uint32_t)(((n / DQ_STAGES) & 1) ^ 1), pc);
+                        if (good)
+                            mbar_arrive_expect_tx(smem_u32(&c->full[stg]), (uint32_t)min(8, pages - 8 * j) * Q8_BLOCK_BYTES);
+                    }
+                    if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
+                    if ((lane >> 3) == j && lane < pages)
+                        tma_load_3d(s_base + stg * DQ_TILE_BYTES + (lane & 7) * Q8_BLOCK_BYTES, kv ? &vmap : &kmap,
+                                    smem_u32(&c->full[stg]), 0, 0, id * a.Hkv + h);
+                }
+            }
+        }
+        if (lane == 0 && pipe_aborted(pc))  // copies in flight land before the CTA's shared memory is released
+            for (int i = max(0, n - DQ_STAGES); i < n; ++i)
+                mbar_wait_drain(smem_u32(&c->full[i % DQ_STAGES]), (uint32_t)((i / DQ_STAGES) & 1));
+    } else if (warp == 2) {
+        // =========================================================== q ====
+        int slot = 0, use = 0, nq = 0;
+        bool ok = true;
+        const uint64_t turn0 = a.rope_turns[2 * lane], turn1 = a.rope_turns[2 * lane + 1];
+        while (ok) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->id_full[slot]), (uint32_t)(use & 1), pc)))) break;
+            const volatile DqStep* st = &c->step[slot];
+            const int b = st->b, h = st->h, first = st->first;
+            if (st->item < 0) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
+            if (++slot == DQ_SLOTS) {
+                slot = 0;
+                ++use;
+            }
+            if (!first) continue;
+            const int buf = nq & 1;
+            uint32_t lo[G], hi[G];
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + ((size_t)b * a.Hq + h * G) * (HEAD_DIM / 2);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {  // dims 2 lane, 2 lane + 1 and the 64 above
+                lo[g] = __ldg(q + g * 64 + lane);
+                hi[g] = __ldg(q + g * 64 + 32 + lane);
+            }
+            const uint32_t pos = (uint32_t)max(0, a.position_ids[b]);
+            float c0, s0, c1, s1;
+            rope_cos_sin(pos, turn0, c0, s0);
+            rope_cos_sin(pos, turn1, c1, s1);
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->q_empty[buf]), (uint32_t)(((nq >> 1) & 1) ^ 1), pc)))) break;
+            uint8_t* qt = sm + DQ_OFF_Q + buf * DQ_Q_BYTES;
+            uint32_t badq = 0;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                uint32_t m = __vmaxu2(lo[g] & 0x7fff7fffu, hi[g] & 0x7fff7fffu);
+                m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+                const bool bad = m >= Q8_LIMIT_BF16;
+                if (bad) badq |= 1u << g;
+                const int e = bad ? 0 : q8_exponent(m);
+                const float inv = bad ? 0.0f : pow2(-e);
+                const float2 l = make_float2(bf16lo(lo[g]), bf16hi(lo[g])), u = make_float2(bf16lo(hi[g]), bf16hi(hi[g]));
+                float2 x = make_float2((l.x * c0 - u.x * s0) * inv, (l.y * c1 - u.y * s1) * inv);
+                float2 y = make_float2((u.x * c0 + l.x * s0) * inv, (u.y * c1 + l.y * s1) * inv);
+                if (bad) x = y = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    if (p == 2) {
+                        x = make_float2(x.x * 256.0f, x.y * 256.0f);
+                        y = make_float2(y.x * 256.0f, y.y * 256.0f);
+                    }
+                    const int row = p * G + g;
+                    *reinterpret_cast<uint16_t*>(qt + sw128_off(row, lane >> 3) + (2 * lane & 15)) = (uint16_t)take_part(x);
+                    *reinterpret_cast<uint16_t*>(qt + sw128_off(row, 4 + (lane >> 3)) + (2 * lane & 15)) = (uint16_t)take_part(y);
+                }
+                if (lane == 0) c->qscale[buf][g] = a.qk_scale_log2 * pow2(e);
+            }
+            if (lane == 0) c->qbad[buf] = (int)badq;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c->q_full[buf]));
+            ++nq;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ============================================== MMA issuer ====
+            constexpr uint32_t idS = idesc_e4m3_f32(DQ_TILE, NS, 0, 0);
+            constexpr uint32_t idO = idesc_e4m3_f32(HEAD_DIM, NP, 1, 0);
+            const uint32_t dT = desc_lo(s_base, 16), dQ = desc_lo(s_base + DQ_OFF_Q, 16), dP = desc_lo(s_base + DQ_OFF_P, 16);
+            constexpr uint32_t TILE = DQ_TILE_BYTES >> 4;
+            int slot = 0, use = 0, n = 0, nq = 0, ns = 0;  // tiles, items, steps done
+            bool ok = !a.timeout_drill || drill_wait(smem_u32(&c->never), pc);
+            while (ok) {
+                if (!(ok = mbar_wait(smem_u32(&c->id_full[slot]), (uint32_t)(use & 1), pc))) break;
+                const volatile DqStep* st = &c->step[slot];
+                const int cnt = st->cnt, first = st->first, last = st->last;
+                if (st->item < 0) break;
+                mbar_arrive(smem_u32(&c->slot_empty[slot]));
+                if (++slot == DQ_SLOTS) {
+                    slot = 0;
+                    ++use;
+                }
+                const int buf = nq & 1;
+                if (first && !(ok = mbar_wait(smem_u32(&c->q_full[buf]), (uint32_t)((nq >> 1) & 1), pc))) break;
+                const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE;
+                for (int j = 0; j < tiles; ++j, ++n) {
+                    const int stg = n % DQ_STAGES;
+                    if (!(ok = mbar_wait(smem_u32(&c->full[stg]), (uint32_t)((n / DQ_STAGES) & 1), pc))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f8(tmem + j * NS, dT + stg * TILE + 2 * k, dQ + buf * (DQ_Q_BYTES >> 4) + 2 * k, idS, k > 0);
+                    umma_commit(smem_u32(&c->empty[stg]));
+                }
+                if (!ok) break;
+                if (tiles > 0) umma_commit(smem_u32(&c->s_full));
+                if (last) {
+                    umma_commit(smem_u32(&c->q_empty[buf]));
+                    ++nq;
+                }
+                if (tiles == 0) continue;
+                if (!(ok = mbar_wait(smem_u32(&c->p_ready), (uint32_t)(ns & 1), pc))) break;
+                tc_fence_after();
+                for (int j = 0; j < tiles; ++j, ++n) {
+                    const int stg = n % DQ_STAGES;
+                    if (!(ok = mbar_wait(smem_u32(&c->full[stg]), (uint32_t)((n / DQ_STAGES) & 1), pc))) break;
+                    tc_fence_after();
+                    const int ks = min(4, (cnt - j * DQ_TILE + 31) / 32);  // k-steps that hold tokens
+                    for (int k = 0; k < ks; ++k)
+                        mma_f8(tmem + DQ_TMEM_O, dT + stg * TILE + 256 * k, dP + j * (DQ_P_BYTES >> 4) + 2 * k, idO, j + k > 0);
+                    umma_commit(smem_u32(&c->empty[stg]));
+                }
+                if (!ok) break;
+                umma_commit(smem_u32(&c->o_full));
+                ++ns;
+            }
+            if (!ok) {  // issued MMAs drain before tensor memory is released
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000000ull) {
+                }
+            }
+        }
+    } else {
+        // ===================================================== softmax ====
+        const int t = tid - 128, w4 = warp & 3;  // token of each tile, output dim
+        const uint32_t lane_addr = (uint32_t)(w4 * 32) << 16;
+        uint8_t* pt = sm + DQ_OFF_P;
+        int slot = 0, use = 0, n = 0, nq = 0, ns = 0;
+        float M[G], l[G], o[G], sc[G];
+        int bad = 0;       // the item's status bits
+        uint32_t range = 0;  // heads that met a value FP32 cannot hold
+        long long resume = blockIdx.x;  // first item not written
+        // The warpgroup leaves the loop together: a warp whose wait gave up goes on to
+        // the next barrier, which tells the others.
+        bool ok = true;
+        auto wait = [&](uint64_t& bar, int parity) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), (uint32_t)(parity & 1), pc));
+        };
+        while (true) {
+            wait(c->id_full[slot], use);
+            wait(c->sc_full[slot], use);
+            DqStep st{};
+            float4 ps[DQ_TILES];
+            if (ok) {
+                const volatile DqStep* s = &c->step[slot];
+                st.b = s->b;
+                st.h = s->h;
+                st.split = s->split;
+                st.n_splits = s->n_splits;
+                st.cnt = s->cnt;
+                st.first = s->first;
+                st.last = s->last;
+                st.item = s->item;
+                st.bad = s->bad;
+#pragma unroll
+                for (int j = 0; j < DQ_TILES; ++j) ps[j] = c->sc[slot][8 * j + (t >> 4)];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
+                if (++slot == DQ_SLOTS) {
+                    slot = 0;
+                    ++use;
+                }
+                if (st.first && st.item >= 0) {
+                    const int buf = nq & 1;
+                    wait(c->q_full[buf], nq >> 1);
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        M[g] = -INFINITY;
+                        l[g] = o[g] = 0.0f;
+                        sc[g] = c->qscale[buf][g];
+                    }
+                    bad = 0;
+                    range = (uint32_t)c->qbad[buf];
+                    __syncwarp();
+                    if (ok && lane == 0) mbar_arrive(smem_u32(&c->q_empty[buf]));
+                    ++nq;
+                }
+            }
+            const int tiles = (st.cnt + DQ_TILE - 1) / DQ_TILE;
+            // scores of the thread's tokens: w = z + log2 vs (-inf past the last token)
+            float w[DQ_TILES][G], mx[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) mx[g] = -INFINITY;
+            if (st.cnt > 0) {
+                wait(c->s_full, ns);
+                tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < DQ_TILES; ++j) {
+                    uint32_t r[NS];
+                    if (j < tiles) {
+                        if constexpr (NS == 16) tmem_ld16(tmem + lane_addr + j * NS, r);
+                        else tmem_ld32(tmem + lane_addr + j * NS, r);
+                        tmem_ld_wait();
+                    }
+                    const bool in = j * DQ_TILE + t < st.cnt;
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        w[j][g] = -INFINITY;
+                        if (in) {
+                            const float hi = __uint_as_float(r[g]) + __uint_as_float(r[G + g]);
+                            const float lo = __uint_as_float(r[2 * G + g]) + __uint_as_float(r[3 * G + g]);
+                            const float z = fmaf(lo, 1.0f / 256.0f, hi) * (ps[j].x * sc[g]);
+                            if (!(fabsf(z) < INFINITY)) range |= 1u << g;
+                            w[j][g] = z + ps[j].y;
+                            mx[g] = fmaxf(mx[g], w[j][g]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float x = warp_max(mx[g]);
+                    if (lane == 0) c->red[w4][g] = x;
+                }
+            }
+            if (named_bar_or(1, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            if (st.item < 0) break;
+            bad |= st.bad;
+            if (st.cnt > 0) {
+                float beta[G];
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float m = fmaxf(fmaxf(c->red[0][g], c->red[1][g]), fmaxf(c->red[2][g], c->red[3][g]));
+                    mx[g] = m > -INFINITY && m < INFINITY ? m : 0.0f;  // otherwise the head fails (range)
+                    const float top = fmaxf(M[g], mx[g]);
+                    const float alpha = ex2(M[g] - top);
+                    beta[g] = ex2(mx[g] - top);
+                    M[g] = top;
+                    l[g] *= alpha;
+                    o[g] *= alpha;
+                }
+                // weights p' = 2^(w - m + 8) as three e4m3 parts; rows part * G + head of tile j's operand
+#pragma unroll
+                for (int j = 0; j < DQ_TILES; j += 2) {
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        float2 p = make_float2(ex2(w[j][g] - mx[g] + 8.0f), ex2(w[j + 1][g] - mx[g] + 8.0f));
+                        l[g] = fmaf(beta[g], fmaf(p.x, ps[j].z, p.y * ps[j + 1].z), l[g]);
+#pragma unroll
+                        for (int e = 0; e < 3; ++e) {
+                            const uint32_t k = take_part(p);
+                            const uint32_t at = sw128_off(e * G + g, t >> 4) + (t & 15);
+                            pt[j * DQ_P_BYTES + at] = (uint8_t)k;
+                            pt[(j + 1) * DQ_P_BYTES + at] = (uint8_t)(k >> 8);
+                        }
+                    }
+                }
+                if (st.cnt & 31) {
+                    // the k-step that the last token is in: V rows behind it hold anything, and 0 times a NaN
+                    // is not 0
+                    const int j = tiles - 1, stg = (n + 2 * tiles - 1) % DQ_STAGES;
+                    wait(c->full[stg], (n + 2 * tiles - 1) / DQ_STAGES);
+                    const int r0 = st.cnt - j * DQ_TILE, r1 = (r0 + 31) & ~31;
+                    for (int i = t; ok && i < (r1 - r0) * 8; i += 128)
+                        reinterpret_cast<uint4*>(sm + stg * DQ_TILE_BYTES + r0 * 128)[i] = make_uint4(0, 0, 0, 0);
+                }
+                n += 2 * tiles;
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&c->p_ready));
+                wait(c->o_full, ns);
+                tc_fence_after();
+                {
+                    uint32_t r[NP];
+                    if constexpr (NP == 16) tmem_ld16(tmem + lane_addr + DQ_TMEM_O, r);
+                    else tmem_ld32(tmem + lane_addr + DQ_TMEM_O, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const float x = (__uint_as_float(r[2 * G + g]) + __uint_as_float(r[G + g])) + __uint_as_float(r[g]);
+                        o[g] = fmaf(x, beta[g], o[g]);
+                    }
+                }
+                ++ns;
+            }
+            if (st.last) {
+                // sums over the warpgroup in a fixed order, and what went wrong anywhere
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    float x = l[g];
+#pragma unroll
+                    for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
+                    if (lane == 0) c->lred[w4][g] = x;
+                    if (!(fabsf(o[g]) < INFINITY)) range |= 1u << g;
+                }
+                range = __reduce_or_sync(0xffffffffu, range);
+                if (lane == 0) c->fred[w4] = (int)range;
+                if (named_bar_or(1, 128, !ok)) {
+                    ok = false;
+                    break;
+                }
+                range = (uint32_t)(c->fred[0] | c->fred[1] | c->fred[2] | c->fred[3]);
+                const bool none = M[0] == -INFINITY;  // no visible key
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float sum = (c->lred[0][g] + c->lred[1][g]) + (c->lred[2][g] + c->lred[3][g]);
+                    if (!none && !(sum > 0.0f && sum < INFINITY)) range |= 1u << g;
+                    const bool fail = bad || (!none && ((range >> g) & 1u));
+                    const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : M[g] - 8.0f + log2f(sum);
+                    write_item(a, st, g, t, fail || none ? 0.0f : o[g] / sum, lse2);
+                }
+                if (t == 0 && a.status) {
+                    const int say = bad | (!none && !bad && range ? RK_STATUS_RANGE : 0);
+                    if (say) atomicOr(a.status, say);
+                }
+                resume = (long long)st.item + gridDim.x;
+                named_bar_sync(1, 128);  // lred and fred may be written again
+            }
+        }
+        if (!ok) {  // a wait gave up: this CTA's items from here on are written as failed
+            for (long long it = resume; it < items; it += gridDim.x) {
+                DqStep st{};
+                int nk, bd;
+                st.h = (int)(it % a.Hkv);
+                find_row(a, c, (int)(it / a.Hkv), st.b, st.split, nk, bd);
+                for (int g = 0; g < G; ++g) write_item(a, st, g, t, 0.0f, __int_as_float(0x7fc00000));
+            }
+            if (t == 0 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, DQ_TMEM_COLS);
+    }
+}
+
+// Merge of the split partials of one (row, query head).  Warp w takes splits w,
+// w + 8, ... with the weights 2^(lse_s - max lse), a lane four dims; the warps'
+// sums are added in order.  Fixed by the row's split count alone.  A NaN partial
+// fails the row, no visible key gives out = 0, lse = -inf.
+constexpr int MERGE_WARPS = 8;
+__global__ void __launch_bounds__(32 * MERGE_WARPS) merge_q8_kernel(const __grid_constant__ AttnQ8Args a) {
+    __shared__ float4 acc_s[MERGE_WARPS][32];
+    __shared__ float sum_s[MERGE_WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const size_t bh = blockIdx.x;
+    int bad0;
+    const int ns = splits_of(row_keys(a, (int)(bh / a.Hq), bad0), a.split_tokens);
+    griddep_wait();  // the partials are complete and visible
+    const float* lp = a.lse_part + bh * a.n_splits;
+    const float4* op = reinterpret_cast<const float4*>(a.o_part + bh * a.n_splits * HEAD_DIM) + lane;
+    float m = -INFINITY;
+    bool bad = false;
+    for (int s = lane; s < ns; s += 32) {
+        const float v = lp[s];
+        bad |= v != v;
+        m = fmaxf(m, v);
+    }
+    m = warp_max(m);
+    bad = __any_sync(0xffffffffu, bad);
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + bh * HEAD_DIM;
+    if (bad || m == -INFINITY) {
+        if (warp == 0) {
+            reinterpret_cast<uint2*>(out)[lane] = make_uint2(0, 0);
+            if (lane == 0) a.lse[bh] = bad ? __int_as_float(0x7fc00000) : -INFINITY;
+        }
+        return;
+    }
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f;
+    constexpr int AHEAD = 4;
+    for (int s0 = warp; s0 < ns; s0 += MERGE_WARPS * AHEAD) {
+        float4 x[AHEAD];
+        float wt[AHEAD];
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+            const int s = s0 + e * MERGE_WARPS;
+            wt[e] = s < ns ? lp[s] : -INFINITY;
+            x[e] = s < ns ? op[(size_t)s * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int e = 0; e < AHEAD; ++e) {
+            const float w = ex2(wt[e] - m);
+            sum += w;
+            acc.x = fmaf(w, x[e].x, acc.x);
+            acc.y = fmaf(w, x[e].y, acc.y);
+            acc.z = fmaf(w, x[e].z, acc.z);
+            acc.w = fmaf(w, x[e].w, acc.w);
+        }
+    }
+    acc_s[warp][lane] = acc;
+    if (lane == 0) sum_s[warp] = sum;
+    __syncthreads();
+    if (warp) return;
+    for (int w = 1; w < MERGE_WARPS; ++w) {
+        const float4 x = acc_s[w][lane];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+        sum += sum_s[w];
+    }
+    const float inv = 1.0f / sum;
+    reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0) a.lse[bh] = (m + log2f(sum)) * 0.693147180559945309f;
+}
+
+std::atomic<uint64_t> g_configured{0};
+std::atomic<int> g_sms[64];
+
+template <int G>
+cudaError_t configure_one() {
+    return cudaFuncSetAttribute(decode_q8_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, DQ_SMEM_BYTES);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
+    if (!bit || !(g_configured.load() & bit)) {
+        if ((e = configure_one<1>()) != cudaSuccess || (e = configure_one<2>()) != cudaSuccess ||
+            (e = configure_one<4>()) != cudaSuccess || (e = configure_one<8>()) != cudaSuccess)
+            return e;
+        if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        if (bit) g_sms[dev].store(sms);
+        g_configured.fetch_or(bit);
+    } else {
+        sms = g_sms[dev].load();
+    }
+    const long long most = (long long)a.B * a.Hkv * a.n_splits;
+    const unsigned grid = (unsigned)(most < sms ? most : sms);
+    switch (a.G) {
+        case 1: decode_q8_kernel<1><<<grid, DQ_THREADS, DQ_SMEM_BYTES, stream>>>(km, vm, a); break;
+        case 2: decode_q8_kernel<2><<<grid, DQ_THREADS, DQ_SMEM_BYTES, stream>>>(km, vm, a); break;
+        case 4: decode_q8_kernel<4><<<grid, DQ_THREADS, DQ_SMEM_BYTES, stream>>>(km, vm, a); break;
+        default: decode_q8_kernel<8><<<grid, DQ_THREADS, DQ_SMEM_BYTES, stream>>>(km, vm, a); break;
+    }
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.n_splits <= 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hq));
+    cfg.blockDim = dim3(32 * MERGE_WARPS);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, merge_q8_kernel, a);
+}
+
+}  // namespace rk

@@ -32,6 +32,7 @@ cudaError_t launch_backward_rotate(const BackwardArgs& a, cudaStream_t stream);
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream);
 cudaError_t launch_append_q8(const AppendQ8Args& a, cudaStream_t stream);
 cudaError_t launch_attn_q8(const AttnQ8Args& a, cudaStream_t stream);
+cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream);
 }  // namespace rk
 
 namespace {
@@ -183,11 +184,11 @@ EncodeTiledFn encode_fn() {
 
 int make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims,
              const cuuint64_t* strides_bytes, const cuuint32_t* box, CUtensorMapSwizzle swz,
-             const char* what) {
+             const char* what, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(RK_E_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims,
+    CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims,
                     strides_bytes, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(RK_E_CUDA, "cuTensorMapEncodeTiled(%s) failed: %d", what, (int)r);
@@ -212,6 +213,15 @@ int make_page_map(CUtensorMap* m, const void* cache, int num_pages, int Hkv, con
     const cuuint64_t strides[3] = {(cuuint64_t)Hkv * rk::HEAD_DIM * 2, 128, (cuuint64_t)rk::HEAD_DIM * 2};
     const cuuint32_t box[4] = {64, (cuuint32_t)rk::PAGE, 2, 1};
     return make_map(m, cache, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what);
+}
+
+// 8-bit cache [num_pages, Hkv, 16, 128] as 3-D (byte, token, block): one box is
+// a page of one head, 2 KiB, landing as 16 swizzled rows of 128 bytes.
+int make_q8_map(CUtensorMap* m, const void* cache, int num_pages, int Hkv, const char* what) {
+    const cuuint64_t dims[3] = {(cuuint64_t)rk::HEAD_DIM, (cuuint64_t)rk::PAGE, (cuuint64_t)num_pages * Hkv};
+    const cuuint64_t strides[2] = {(cuuint64_t)rk::HEAD_DIM, (cuuint64_t)rk::Q8_BLOCK_BYTES};
+    const cuuint32_t box[3] = {(cuuint32_t)rk::HEAD_DIM, (cuuint32_t)rk::PAGE, 1};
+    return make_map(m, cache, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -895,12 +905,20 @@ int check_plan(const rk_paged_plan_t* plan) {
                        plan->rope_theta, plan->rope_scale);
 }
 
+// Blocks of the 8-bit cache are counted in 32 bits.
+int check_q8_blocks(const rk_paged_plan_t* plan) {
+    if ((int64_t)plan->num_pages * plan->Hkv > INT32_MAX)
+        return fail(RK_E_UNSUPPORTED, "num_pages %d x Hkv %d: too many blocks", plan->num_pages, plan->Hkv);
+    return RK_OK;
+}
+
 // Checks and arguments that the two attention calls share.
 int attn_q8_args(const rk_paged_plan_t* plan, const void* q, const void* k_cache, const void* v_cache,
                  const float* k_scale, const float* v_scale, const int32_t* block_table_d, const int32_t* kv_lens_d,
                  const int32_t* position_ids_d, void* out, float* lse, int32_t* status_d, rk::AttnQ8Args* a) {
     int rc = check_plan(plan);
     if (rc) return rc;
+    if ((rc = check_q8_blocks(plan))) return rc;
     if (plan->B > 0 && plan->num_pages > 0 && (!k_scale || !v_scale)) return fail(RK_E_ARG, "k_scale / v_scale is NULL");
     if (!aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(status_d, 4))
         return fail(RK_E_ARG, "k_scale, v_scale and status must be 4-byte aligned");
@@ -1044,6 +1062,9 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t* plan, int32_t split_tokens, c
     if (rc) return rc;
     if (plan->Sq != 1) return fail(RK_E_ARG, "decode needs a plan with Sq == 1 (got %d)", plan->Sq);
     if ((rc = q8_split(&split_tokens))) return rc;
+    if ((double)plan->B * plan->Hkv * (double)split_count(plan, split_tokens) > 2147483647.0)
+        return fail(RK_E_UNSUPPORTED, "B %d x Hkv %d x %lld splits: too many", plan->B, plan->Hkv,
+                    (long long)split_count(plan, split_tokens));
     const int64_t need = q8_scratch_need(plan, split_tokens);
     if (need > 0) {
         if (!scratch || !aligned(scratch, 16))
@@ -1056,7 +1077,16 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t* plan, int32_t split_tokens, c
     rc = attn_q8_args(plan, q, k_cache, v_cache, k_scale, v_scale, block_table_d, kv_lens_d, position_ids_d, out, lse, status_d,
                       &a);
     if (rc || plan->B == 0) return rc;
-    cudaError_t e = rk::launch_attn_q8(a, reinterpret_cast<cudaStream_t>(stream));
+    a.split_tokens = split_tokens;
+    a.n_splits = (int32_t)split_count(plan, split_tokens);
+    a.o_part = static_cast<float*>(scratch);
+    if (need > 0) a.lse_part = a.o_part + (int64_t)plan->B * plan->Hq * a.n_splits * rk::HEAD_DIM;
+    // without a pool no row has a page to read: the map of the (16-byte aligned) query stands in
+    CUtensorMap km, vm;
+    const bool have = plan->num_pages > 0;
+    if ((rc = make_q8_map(&km, have ? k_cache : q, have ? plan->num_pages : 1, have ? plan->Hkv : 1, "k_cache"))) return rc;
+    if ((rc = make_q8_map(&vm, have ? v_cache : q, have ? plan->num_pages : 1, have ? plan->Hkv : 1, "v_cache"))) return rc;
+    cudaError_t e = rk::launch_decode_q8(km, vm, a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(RK_E_CUDA, "8-bit decode launch: %s", cudaGetErrorString(e));
     return RK_OK;
 }
