@@ -28,12 +28,18 @@
 // its tokens), steps and splits are joined with the running maximum in FP32.
 // A persistent grid of one CTA per SM takes items c, c + grid, ... of the list
 // ordered by row, split, KV head, so neighbouring CTAs read neighbouring blocks.
-// Roles (8 warps):
-//   warp 0     TMA producer: lane p loads page p of a step's K, then of its V;
-//   warp 1     MMA issuer;
-//   warp 2     q: rotates the item's query heads, splits them into parts;
-//   warp 3     metadata: walks the items, page ids and scales of each step;
-//   warps 4-7  softmax: thread t has token t of every tile, and output dim t.
+// Roles (12 warps):
+//   warp 0      TMA producer: lane p loads page p of a step's K, then of its V;
+//   warp 1      MMA issuer: S of step k + 1 before PV of step k, so that it
+//               never waits for a softmax with work at hand;
+//   warp 2      q: rotates the item's query heads, splits them into parts;
+//   warp 3      metadata: walks the items, page ids and scales of each step;
+//   warps 4-11  two softmax warpgroups, items in turn: thread t has token t of
+//               every tile, and output dim t.  S, P and O have two buffers, by
+//               the parity of the step.
+// One warpgroup and one buffer took 4.9 us a step (64 x 4096), a chain of S MMAs
+// 1.1, scores and maximum 0.7, weights 0.7, PV 1.5 and the item's end 1.3 us,
+// where the step's bytes take 3.0 us of this SM's share of the bandwidth.
 // Nothing depends on B, W or the grid.
 #include <atomic>
 #include <cstring>
@@ -44,27 +50,30 @@ namespace rk {
 
 namespace {
 
-constexpr int DQ_THREADS = 256;
+constexpr int DQ_THREADS = 384;
 constexpr int DQ_TILE = 128;                      // tokens of a tile
 constexpr int DQ_TILE_BYTES = DQ_TILE * HEAD_DIM;  // 16 KiB
 constexpr int DQ_TILES = 4;                       // tiles of a step
 constexpr int DQ_STEP = DQ_TILE * DQ_TILES;
 constexpr int DQ_PAGES = DQ_STEP / PAGE;          // 32: one lane each
-constexpr int DQ_STAGES = 12;                     // 192 KiB on the way or in use
 constexpr int DQ_SLOTS = 4;                       // steps the metadata runs ahead
 constexpr int DQ_PRE = 1024;                      // row groups of the item list
-constexpr int DQ_TMEM_COLS = 256;
-constexpr int DQ_TMEM_O = 128;                    // S in columns [0, 128), O behind it
 
 template <int G>
 struct DqShape {
     static constexpr int NS = 4 * G < 16 ? 16 : 4 * G;  // columns of S: part * G + head
     static constexpr int NP = 3 * G <= 16 ? 16 : 32;    // columns of O
+    // tensor memory: two S buffers of DQ_TILES x NS columns, two O buffers
+    static constexpr int TMEM_S = DQ_TILES * NS, TMEM_O = 2 * TMEM_S;
+    static constexpr int TMEM_COLS = TMEM_O + 2 * NP <= 256 ? 256 : 512;
+    // shared memory: tiles on the way or in use (192 or 176 KiB), two q operands, two
+    // steps' weights (an operand per tile)
+    static constexpr int STAGES = G == 8 ? 11 : 12;
+    static constexpr int Q_BYTES = NS * 128, P_BYTES = NP * 128;
+    static constexpr int OFF_Q = STAGES * DQ_TILE_BYTES;
+    static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
+    static constexpr int OFF_CTRL = OFF_P + 2 * DQ_TILES * P_BYTES;
 };
-constexpr int DQ_Q_BYTES = 32 * 128, DQ_P_BYTES = 32 * 128;
-constexpr int DQ_OFF_Q = DQ_STAGES * DQ_TILE_BYTES;      // two q operands
-constexpr int DQ_OFF_P = DQ_OFF_Q + 2 * DQ_Q_BYTES;      // a step's weights, one operand per tile
-constexpr int DQ_OFF_CTRL = DQ_OFF_P + DQ_TILES * DQ_P_BYTES;
 
 struct DqStep {
     int b, h, split;   // row, KV head, split
@@ -76,10 +85,10 @@ struct DqStep {
 };
 
 struct DqCtrl {
-    uint64_t full[DQ_STAGES], empty[DQ_STAGES];
+    uint64_t full[12], empty[12];
     uint64_t id_full[DQ_SLOTS], sc_full[DQ_SLOTS], slot_empty[DQ_SLOTS];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full, p_ready, o_full;
+    uint64_t s_full[2], p_ready[2], o_full[2], o_read[2];  // by the parity of the step
     uint64_t never;
     uint32_t tmem_base;
     PipeCtl pipe;
@@ -90,13 +99,16 @@ struct DqCtrl {
     alignas(16) float4 sc[DQ_SLOTS][DQ_PAGES];  // k scale, log2 of v's, 1 / v's
     float qscale[2][8];              // score factor of each head (log2 domain)
     int qbad[2];                     // heads whose query is out of range, a bit each
-    float red[4][8];
-    float lred[4][8];
-    int fred[4];
+    float red[2][4][8];              // of each softmax warpgroup
+    float lred[2][4][8];
+    int fred[2][4];
     int pre[DQ_PRE + 1];             // row splits before each group of rows
 };
-constexpr int DQ_SMEM_BYTES = DQ_OFF_CTRL + (int)sizeof(DqCtrl);
-static_assert(DQ_SMEM_BYTES <= 232448, "8-bit decode shared memory above the 227 KiB opt-in limit");
+template <int G>
+constexpr int dq_smem_bytes() {
+    static_assert(DqShape<G>::OFF_CTRL + sizeof(DqCtrl) <= 232448, "8-bit decode shared memory above the 227 KiB opt-in limit");
+    return DqShape<G>::OFF_CTRL + (int)sizeof(DqCtrl);
+}
 
 // Visible keys of a row (0 where its metadata is unsafe) and its status bits.
 __device__ __forceinline__ int row_keys(const AttnQ8Args& a, int b, int& bad) {
@@ -145,76 +157,74 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                      const __grid_constant__ AttnQ8Args a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw;
-    DqCtrl* c = reinterpret_cast<DqCtrl*>(sm + DQ_OFF_CTRL);
+    using Sh = DqShape<G>;
+    DqCtrl* c = reinterpret_cast<DqCtrl*>(sm + Sh::OFF_CTRL);
     const uint32_t s_base = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int NS = DqShape<G>::NS, NP = DqShape<G>::NP;
+    constexpr int NS = Sh::NS, NP = Sh::NP, STAGES = Sh::STAGES;
     griddep_launch_dependents();  // the merge may become resident; it waits for this grid's end
 
     // ---- set-up: barriers, tensor memory, operands that stay zero, the item list ----
     if (tid == 0) {
         c->pipe.abort = 0;
         c->pipe.limit_ns = wait_limit(a.wait_limit_ns);
-        for (int i = 0; i < DQ_STAGES; ++i) {
+        for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&c->full[i]), 1);
             mbar_init(smem_u32(&c->empty[i]), 1);
         }
         for (int i = 0; i < DQ_SLOTS; ++i) {
             mbar_init(smem_u32(&c->id_full[i]), 1);
             mbar_init(smem_u32(&c->sc_full[i]), 1);
-            mbar_init(smem_u32(&c->slot_empty[i]), 7);  // producer, issuer, q, four softmax warps
+            mbar_init(smem_u32(&c->slot_empty[i]), 11);  // producer, issuer, q, eight softmax warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&c->q_full[i]), 1);
-            mbar_init(smem_u32(&c->q_empty[i]), 5);     // issuer's commit, four softmax warps
+            mbar_init(smem_u32(&c->q_empty[i]), 5);      // issuer's commit, four softmax warps
+            mbar_init(smem_u32(&c->s_full[i]), 1);
+            mbar_init(smem_u32(&c->p_ready[i]), 128);
+            mbar_init(smem_u32(&c->o_full[i]), 1);
+            mbar_init(smem_u32(&c->o_read[i]), 128);
         }
-        mbar_init(smem_u32(&c->s_full), 1);
-        mbar_init(smem_u32(&c->p_ready), 128);
-        mbar_init(smem_u32(&c->o_full), 1);
         mbar_init(smem_u32(&c->never), 1);
         fence_mbar_init();
     }
-    for (int i = tid; i < (2 * DQ_Q_BYTES + DQ_TILES * DQ_P_BYTES) / 16; i += DQ_THREADS)
-        reinterpret_cast<uint4*>(sm + DQ_OFF_Q)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < (Sh::OFF_CTRL - Sh::OFF_Q) / 16; i += DQ_THREADS)
+        reinterpret_cast<uint4*>(sm + Sh::OFF_Q)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     if (warp == 1) {
-        tmem_alloc(smem_u32(&c->tmem_base), DQ_TMEM_COLS);
+        tmem_alloc(smem_u32(&c->tmem_base), Sh::TMEM_COLS);
         tmem_relinquish();
     }
     {
-        // Row splits before each group of `per` rows.  Threads take DQ_PRE / 256 groups each.
+        // Row splits before each group of `per` rows, a group to a thread and pass.
         const int per = (a.B + DQ_PRE - 1) / DQ_PRE, groups = (a.B + per - 1) / per;
-        constexpr int MINE = DQ_PRE / DQ_THREADS;
-        int cnt[MINE], sum = 0;
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-            cnt[i] = 0;
-            const int gr = tid * MINE + i;
-            if (gr < groups) {
-                for (int b = gr * per; b < min(a.B, gr * per + per); ++b) {
-                    int bad;
-                    const int n = row_keys(a, b, bad);
-                    cnt[i] += splits_of(n, a.split_tokens);
-                }
+        int base = 0;
+        for (int g0 = 0; g0 < groups; g0 += DQ_THREADS) {
+            const int gr = g0 + tid;
+            int cnt = 0;
+            for (int b = gr * per; gr < groups && b < min(a.B, gr * per + per); ++b) {
+                int bad;
+                const int n = row_keys(a, b, bad);
+                cnt += splits_of(n, a.split_tokens);
             }
-            sum += cnt[i];
-        }
-        int v = sum;
+            int v = cnt;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += t;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += t;
+            }
+            __syncthreads();
+            if (lane == 31) c->scan[warp] = v;
+            __syncthreads();
+            int before = base;
+            for (int w = 0; w < DQ_THREADS / 32; ++w) {
+                const int x = c->scan[w];
+                before += w < warp ? x : 0;
+                base += x;
+            }
+            if (gr < groups) c->pre[gr] = before + v - cnt;
         }
-        if (lane == 31) c->scan[warp] = v;
-        __syncthreads();
-        int base = v - sum;
-        for (int w = 0; w < warp; ++w) base += c->scan[w];
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-            c->pre[tid * MINE + i] = base;
-            base += cnt[i];
-        }
-        if (tid == DQ_THREADS - 1) c->total = base;
+        if (tid == 0) c->total = base;
     }
     tc_fence_before();
     __syncthreads();
@@ -306,10 +316,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE, pages = (cnt + PAGE - 1) / PAGE;
             for (int kv = 0; kv < 2 && ok; ++kv) {
                 for (int j = 0; j < tiles; ++j, ++n) {
-                    const int stg = n % DQ_STAGES;
+                    const int stg = n % STAGES;
                     int good = 1;
                     if (lane == 0) {
-                        good = mbar_wait(smem_u32(&c->empty[stg]), (uint32_t)(((n / DQ_STAGES) & 1) ^ 1), pc);
+                        good = mbar_wait(smem_u32(&c->empty[stg]), (uint32_t)(((n / STAGES) & 1) ^ 1), pc);
                         if (good)
                             mbar_arrive_expect_tx(smem_u32(&c->full[stg]), (uint32_t)min(8, pages - 8 * j) * Q8_BLOCK_BYTES);
                     }
@@ -321,8 +331,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             }
         }
         if (lane == 0 && pipe_aborted(pc))  // copies in flight land before the CTA's shared memory is released
-            for (int i = max(0, n - DQ_STAGES); i < n; ++i)
-                mbar_wait_drain(smem_u32(&c->full[i % DQ_STAGES]), (uint32_t)((i / DQ_STAGES) & 1));
+            for (int i = max(0, n - STAGES); i < n; ++i)
+                mbar_wait_drain(smem_u32(&c->full[i % STAGES]), (uint32_t)((i / STAGES) & 1));
     } else if (warp == 2) {
         // =========================================================== q ====
         int slot = 0, use = 0, nq = 0;
@@ -353,7 +363,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             rope_cos_sin(pos, turn0, c0, s0);
             rope_cos_sin(pos, turn1, c1, s1);
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->q_empty[buf]), (uint32_t)(((nq >> 1) & 1) ^ 1), pc)))) break;
-            uint8_t* qt = sm + DQ_OFF_Q + buf * DQ_Q_BYTES;
+            uint8_t* qt = sm + Sh::OFF_Q + buf * Sh::Q_BYTES;
             uint32_t badq = 0;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
@@ -390,53 +400,83 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             // ============================================== MMA issuer ====
             constexpr uint32_t idS = idesc_e4m3_f32(DQ_TILE, NS, 0, 0);
             constexpr uint32_t idO = idesc_e4m3_f32(HEAD_DIM, NP, 1, 0);
-            const uint32_t dT = desc_lo(s_base, 16), dQ = desc_lo(s_base + DQ_OFF_Q, 16), dP = desc_lo(s_base + DQ_OFF_P, 16);
+            const uint32_t dT = desc_lo(s_base, 16), dQ = desc_lo(s_base + Sh::OFF_Q, 16), dP = desc_lo(s_base + Sh::OFF_P, 16);
             constexpr uint32_t TILE = DQ_TILE_BYTES >> 4;
-            int slot = 0, use = 0, n = 0, nq = 0, ns = 0;  // tiles, items, steps done
+            // Tiles arrive step by step, K before V: with S one step ahead of PV, the K
+            // tiles are counted from nk and the V tiles of the step before from nv.
+            int slot = 0, use = 0, nk = 0, nq = 0, ks = 0;  // next tile, items, steps (S)
+            int pv_cnt = 0, nv = 0;                         // the step whose PV is due: tokens, first V tile
             bool ok = !a.timeout_drill || drill_wait(smem_u32(&c->never), pc);
+            auto tile_in = [&](int n) { return mbar_wait(smem_u32(&c->full[n % STAGES]), (uint32_t)((n / STAGES) & 1), pc); };
+            // PV of step k
+            auto issue_pv = [&](int k) -> bool {
+                const int buf = k & 1;
+                const uint32_t par = (uint32_t)((k >> 1) & 1);
+                if (!mbar_wait(smem_u32(&c->o_read[buf]), par ^ 1u, pc)) return false;  // step k - 2's result is read
+                if (!mbar_wait(smem_u32(&c->p_ready[buf]), par, pc)) return false;
+                const uint32_t d = tmem + Sh::TMEM_O + buf * NP;
+                for (int j = 0; j * DQ_TILE < pv_cnt; ++j) {
+                    const int n = nv + j;
+                    if (!tile_in(n)) return false;
+                    tc_fence_after();
+                    const uint32_t dv = dT + (n % STAGES) * TILE, dp = dP + (buf * DQ_TILES + j) * (Sh::P_BYTES >> 4);
+                    const int kn = min(4, (pv_cnt - j * DQ_TILE + 31) / 32);  // k-steps that hold tokens
+                    if (kn == 4) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) mma_f8(d, dv + 256 * i, dp + 2 * i, idO, i > 0 || j > 0);
+                    } else {
+                        for (int i = 0; i < kn; ++i) mma_f8(d, dv + 256 * i, dp + 2 * i, idO, i > 0 || j > 0);
+                    }
+                    umma_commit(smem_u32(&c->empty[n % STAGES]));
+                }
+                umma_commit(smem_u32(&c->o_full[buf]));
+                return true;
+            };
             while (ok) {
                 if (!(ok = mbar_wait(smem_u32(&c->id_full[slot]), (uint32_t)(use & 1), pc))) break;
                 const volatile DqStep* st = &c->step[slot];
-                const int cnt = st->cnt, first = st->first, last = st->last;
-                if (st->item < 0) break;
-                mbar_arrive(smem_u32(&c->slot_empty[slot]));
-                if (++slot == DQ_SLOTS) {
-                    slot = 0;
-                    ++use;
-                }
-                const int buf = nq & 1;
-                if (first && !(ok = mbar_wait(smem_u32(&c->q_full[buf]), (uint32_t)((nq >> 1) & 1), pc))) break;
-                const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE;
-                for (int j = 0; j < tiles; ++j, ++n) {
-                    const int stg = n % DQ_STAGES;
-                    if (!(ok = mbar_wait(smem_u32(&c->full[stg]), (uint32_t)((n / DQ_STAGES) & 1), pc))) break;
-                    tc_fence_after();
+                const int cnt = st->cnt, first = st->first, last = st->last, end = st->item < 0;
+                if (!end) {
+                    mbar_arrive(smem_u32(&c->slot_empty[slot]));
+                    if (++slot == DQ_SLOTS) {
+                        slot = 0;
+                        ++use;
+                    }
+                    const int qb = nq & 1;
+                    if (first && !(ok = mbar_wait(smem_u32(&c->q_full[qb]), (uint32_t)((nq >> 1) & 1), pc))) break;
+                    const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE;
+                    for (int j = 0; j < tiles; ++j) {
+                        if (!(ok = tile_in(nk + j))) break;
+                        tc_fence_after();
+                        const uint32_t dk = dT + ((nk + j) % STAGES) * TILE, dq = dQ + qb * (Sh::Q_BYTES >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f8(tmem + j * NS, dT + stg * TILE + 2 * k, dQ + buf * (DQ_Q_BYTES >> 4) + 2 * k, idS, k > 0);
-                    umma_commit(smem_u32(&c->empty[stg]));
+                        for (int i = 0; i < 4; ++i)
+                            mma_f8(tmem + (ks & 1) * Sh::TMEM_S + j * NS, dk + 2 * i, dq + 2 * i, idS, i > 0);
+                        umma_commit(smem_u32(&c->empty[(nk + j) % STAGES]));
+                    }
+                    if (!ok) break;
+                    if (tiles > 0) umma_commit(smem_u32(&c->s_full[ks & 1]));
+                    if (last) {
+                        umma_commit(smem_u32(&c->q_empty[qb]));
+                        ++nq;
+                    }
+                    if (tiles == 0) {
+                        // nothing to run ahead of: the step before must not wait for what
+                        // comes (its softmax holds descriptor slots up)
+                        if (pv_cnt > 0 && !(ok = issue_pv(ks - 1))) break;
+                        pv_cnt = 0;
+                        continue;
+                    }
                 }
-                if (!ok) break;
-                if (tiles > 0) umma_commit(smem_u32(&c->s_full));
-                if (last) {
-                    umma_commit(smem_u32(&c->q_empty[buf]));
-                    ++nq;
-                }
-                if (tiles == 0) continue;
-                if (!(ok = mbar_wait(smem_u32(&c->p_ready), (uint32_t)(ns & 1), pc))) break;
-                tc_fence_after();
-                for (int j = 0; j < tiles; ++j, ++n) {
-                    const int stg = n % DQ_STAGES;
-                    if (!(ok = mbar_wait(smem_u32(&c->full[stg]), (uint32_t)((n / DQ_STAGES) & 1), pc))) break;
-                    tc_fence_after();
-                    const int ks = min(4, (cnt - j * DQ_TILE + 31) / 32);  // k-steps that hold tokens
-                    for (int k = 0; k < ks; ++k)
-                        mma_f8(tmem + DQ_TMEM_O, dT + stg * TILE + 256 * k, dP + j * (DQ_P_BYTES >> 4) + 2 * k, idO, j + k > 0);
-                    umma_commit(smem_u32(&c->empty[stg]));
-                }
-                if (!ok) break;
-                umma_commit(smem_u32(&c->o_full));
-                ++ns;
+                // S of this step is under way (its buffer was read by step k - 2's softmax, whose
+                // weights the PV before last waited for); now the PV of the step before
+                if (pv_cnt > 0 && !(ok = issue_pv(ks - 1))) break;
+                if (end) break;
+                const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE;
+                pv_cnt = cnt;
+                nv = nk + tiles;
+                nk += 2 * tiles;
+                ++ks;
             }
             if (!ok) {  // issued MMAs drain before tensor memory is released
                 const uint64_t t0 = global_timer_ns();
@@ -446,14 +486,14 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         }
     } else {
         // ===================================================== softmax ====
-        const int t = tid - 128, w4 = warp & 3;  // token of each tile, output dim
+        const int wg = (warp >> 2) - 1;                // takes items wg, wg + 2, ... of the CTA
+        const int t = tid & 127, w4 = warp & 3;        // token of each tile, output dim
         const uint32_t lane_addr = (uint32_t)(w4 * 32) << 16;
-        uint8_t* pt = sm + DQ_OFF_P;
-        int slot = 0, use = 0, n = 0, nq = 0, ns = 0;
+        int slot = 0, use = 0, n = 0, nq = 0, ks = 0;  // tiles, items, steps before this one (both warpgroups')
         float M[G], l[G], o[G], sc[G];
         int bad = 0;       // the item's status bits
         uint32_t range = 0;  // heads that met a value FP32 cannot hold
-        long long resume = blockIdx.x;  // first item not written
+        long long resume = blockIdx.x + (long long)wg * gridDim.x;  // first item not written
         // The warpgroup leaves the loop together: a warp whose wait gave up goes on to
         // the next barrier, which tells the others.
         bool ok = true;
@@ -484,9 +524,15 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     slot = 0;
                     ++use;
                 }
+                nq += st.first;
+                if (st.item >= 0 && ((nq - 1) & 1) != wg) {  // the other warpgroup's
+                    ks += st.cnt > 0;
+                    n += 2 * ((st.cnt + DQ_TILE - 1) / DQ_TILE);
+                    continue;
+                }
                 if (st.first && st.item >= 0) {
-                    const int buf = nq & 1;
-                    wait(c->q_full[buf], nq >> 1);
+                    const int buf = (nq - 1) & 1;
+                    wait(c->q_full[buf], (nq - 1) >> 1);
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
                         M[g] = -INFINITY;
@@ -497,7 +543,6 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     range = (uint32_t)c->qbad[buf];
                     __syncwarp();
                     if (ok && lane == 0) mbar_arrive(smem_u32(&c->q_empty[buf]));
-                    ++nq;
                 }
             }
             const int tiles = (st.cnt + DQ_TILE - 1) / DQ_TILE;
@@ -506,14 +551,15 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
 #pragma unroll
             for (int g = 0; g < G; ++g) mx[g] = -INFINITY;
             if (st.cnt > 0) {
-                wait(c->s_full, ns);
+                wait(c->s_full[ks & 1], ks >> 1);
                 tc_fence_after();
+                const uint32_t ts = tmem + lane_addr + (ks & 1) * Sh::TMEM_S;
 #pragma unroll
                 for (int j = 0; j < DQ_TILES; ++j) {
                     uint32_t r[NS];
                     if (j < tiles) {
-                        if constexpr (NS == 16) tmem_ld16(tmem + lane_addr + j * NS, r);
-                        else tmem_ld32(tmem + lane_addr + j * NS, r);
+                        if constexpr (NS == 16) tmem_ld16(ts + j * NS, r);
+                        else tmem_ld32(ts + j * NS, r);
                         tmem_ld_wait();
                     }
                     const bool in = j * DQ_TILE + t < st.cnt;
@@ -533,10 +579,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     const float x = warp_max(mx[g]);
-                    if (lane == 0) c->red[w4][g] = x;
+                    if (lane == 0) c->red[wg][w4][g] = x;
                 }
             }
-            if (named_bar_or(1, 128, !ok)) {
+            if (named_bar_or(1 + wg, 128, !ok)) {
                 ok = false;
                 break;
             }
@@ -546,7 +592,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 float beta[G];
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float m = fmaxf(fmaxf(c->red[0][g], c->red[1][g]), fmaxf(c->red[2][g], c->red[3][g]));
+                    const float m = fmaxf(fmaxf(c->red[wg][0][g], c->red[wg][1][g]), fmaxf(c->red[wg][2][g], c->red[wg][3][g]));
                     mx[g] = m > -INFINITY && m < INFINITY ? m : 0.0f;  // otherwise the head fails (range)
                     const float top = fmaxf(M[g], mx[g]);
                     const float alpha = ex2(M[g] - top);
@@ -555,6 +601,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     l[g] *= alpha;
                     o[g] *= alpha;
                 }
+                // the weights' buffer is free once the PV of step k - 2 is done
+                wait(c->o_full[ks & 1], (ks >> 1) + 1);
+                uint8_t* pt = sm + Sh::OFF_P + (ks & 1) * DQ_TILES * Sh::P_BYTES;
                 // weights p' = 2^(w - m + 8) as three e4m3 parts; rows part * G + head of tile j's operand
 #pragma unroll
                 for (int j = 0; j < DQ_TILES; j += 2) {
@@ -566,16 +615,16 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                         for (int e = 0; e < 3; ++e) {
                             const uint32_t k = take_part(p);
                             const uint32_t at = sw128_off(e * G + g, t >> 4) + (t & 15);
-                            pt[j * DQ_P_BYTES + at] = (uint8_t)k;
-                            pt[(j + 1) * DQ_P_BYTES + at] = (uint8_t)(k >> 8);
+                            pt[j * Sh::P_BYTES + at] = (uint8_t)k;
+                            pt[(j + 1) * Sh::P_BYTES + at] = (uint8_t)(k >> 8);
                         }
                     }
                 }
                 if (st.cnt & 31) {
                     // the k-step that the last token is in: V rows behind it hold anything, and 0 times a NaN
                     // is not 0
-                    const int j = tiles - 1, stg = (n + 2 * tiles - 1) % DQ_STAGES;
-                    wait(c->full[stg], (n + 2 * tiles - 1) / DQ_STAGES);
+                    const int j = tiles - 1, stg = (n + 2 * tiles - 1) % STAGES;
+                    wait(c->full[stg], (n + 2 * tiles - 1) / STAGES);
                     const int r0 = st.cnt - j * DQ_TILE, r1 = (r0 + 31) & ~31;
                     for (int i = t; ok && i < (r1 - r0) * 8; i += 128)
                         reinterpret_cast<uint4*>(sm + stg * DQ_TILE_BYTES + r0 * 128)[i] = make_uint4(0, 0, 0, 0);
@@ -583,21 +632,23 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 n += 2 * tiles;
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(smem_u32(&c->p_ready));
-                wait(c->o_full, ns);
+                mbar_arrive(smem_u32(&c->p_ready[ks & 1]));
+                wait(c->o_full[ks & 1], ks >> 1);
                 tc_fence_after();
                 {
                     uint32_t r[NP];
-                    if constexpr (NP == 16) tmem_ld16(tmem + lane_addr + DQ_TMEM_O, r);
-                    else tmem_ld32(tmem + lane_addr + DQ_TMEM_O, r);
+                    if constexpr (NP == 16) tmem_ld16(tmem + lane_addr + Sh::TMEM_O + (ks & 1) * NP, r);
+                    else tmem_ld32(tmem + lane_addr + Sh::TMEM_O + (ks & 1) * NP, r);
                     tmem_ld_wait();
+                    tc_fence_before();
+                    mbar_arrive(smem_u32(&c->o_read[ks & 1]));
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
                         const float x = (__uint_as_float(r[2 * G + g]) + __uint_as_float(r[G + g])) + __uint_as_float(r[g]);
                         o[g] = fmaf(x, beta[g], o[g]);
                     }
                 }
-                ++ns;
+                ++ks;
             }
             if (st.last) {
                 // sums over the warpgroup in a fixed order, and what went wrong anywhere
@@ -606,20 +657,20 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     float x = l[g];
 #pragma unroll
                     for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-                    if (lane == 0) c->lred[w4][g] = x;
+                    if (lane == 0) c->lred[wg][w4][g] = x;
                     if (!(fabsf(o[g]) < INFINITY)) range |= 1u << g;
                 }
                 range = __reduce_or_sync(0xffffffffu, range);
-                if (lane == 0) c->fred[w4] = (int)range;
-                if (named_bar_or(1, 128, !ok)) {
+                if (lane == 0) c->fred[wg][w4] = (int)range;
+                if (named_bar_or(1 + wg, 128, !ok)) {
                     ok = false;
                     break;
                 }
-                range = (uint32_t)(c->fred[0] | c->fred[1] | c->fred[2] | c->fred[3]);
+                range = (uint32_t)(c->fred[wg][0] | c->fred[wg][1] | c->fred[wg][2] | c->fred[wg][3]);
                 const bool none = M[0] == -INFINITY;  // no visible key
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float sum = (c->lred[0][g] + c->lred[1][g]) + (c->lred[2][g] + c->lred[3][g]);
+                    const float sum = (c->lred[wg][0][g] + c->lred[wg][1][g]) + (c->lred[wg][2][g] + c->lred[wg][3][g]);
                     if (!none && !(sum > 0.0f && sum < INFINITY)) range |= 1u << g;
                     const bool fail = bad || (!none && ((range >> g) & 1u));
                     const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : M[g] - 8.0f + log2f(sum);
@@ -629,12 +680,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     const int say = bad | (!none && !bad && range ? RK_STATUS_RANGE : 0);
                     if (say) atomicOr(a.status, say);
                 }
-                resume = (long long)st.item + gridDim.x;
-                named_bar_sync(1, 128);  // lred and fred may be written again
+                resume = (long long)st.item + 2ll * gridDim.x;
+                named_bar_sync(1 + wg, 128);  // lred and fred may be written again
             }
         }
         if (!ok) {  // a wait gave up: this CTA's items from here on are written as failed
-            for (long long it = resume; it < items; it += gridDim.x) {
+            for (long long it = resume; it < items; it += 2ll * gridDim.x) {
                 DqStep st{};
                 int nk, bd;
                 st.h = (int)(it % a.Hkv);
@@ -649,7 +700,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem, DQ_TMEM_COLS);
+        tmem_dealloc(tmem, Sh::TMEM_COLS);
     }
 }
 
@@ -729,7 +780,7 @@ std::atomic<int> g_sms[64];
 
 template <int G>
 cudaError_t configure_one() {
-    return cudaFuncSetAttribute(decode_q8_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, DQ_SMEM_BYTES);
+    return cudaFuncSetAttribute(decode_q8_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem_bytes<G>());
 }
 
 }  // namespace
@@ -752,10 +803,10 @@ cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const
     const long long most = (long long)a.B * a.Hkv * a.n_splits;
     const unsigned grid = (unsigned)(most < sms ? most : sms);
     switch (a.G) {
-        case 1: decode_q8_kernel<1><<<grid, DQ_THREADS, DQ_SMEM_BYTES, stream>>>(km, vm, a); break;
-        case 2: decode_q8_kernel<2><<<grid, DQ_THREADS, DQ_SMEM_BYTES, stream>>>(km, vm, a); break;
-        case 4: decode_q8_kernel<4><<<grid, DQ_THREADS, DQ_SMEM_BYTES, stream>>>(km, vm, a); break;
-        default: decode_q8_kernel<8><<<grid, DQ_THREADS, DQ_SMEM_BYTES, stream>>>(km, vm, a); break;
+        case 1: decode_q8_kernel<1><<<grid, DQ_THREADS, dq_smem_bytes<1>(), stream>>>(km, vm, a); break;
+        case 2: decode_q8_kernel<2><<<grid, DQ_THREADS, dq_smem_bytes<2>(), stream>>>(km, vm, a); break;
+        case 4: decode_q8_kernel<4><<<grid, DQ_THREADS, dq_smem_bytes<4>(), stream>>>(km, vm, a); break;
+        default: decode_q8_kernel<8><<<grid, DQ_THREADS, dq_smem_bytes<8>(), stream>>>(km, vm, a); break;
     }
     e = cudaGetLastError();
     if (e != cudaSuccess || a.n_splits <= 1) return e;
