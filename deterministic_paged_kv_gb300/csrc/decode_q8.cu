@@ -28,18 +28,19 @@
 // its tokens), steps and splits are joined with the running maximum in FP32.
 // A persistent grid of one CTA per SM takes items c, c + grid, ... of the list
 // ordered by row, split, KV head, so neighbouring CTAs read neighbouring blocks.
-// Roles (12 warps):
+// Roles (20 warps):
 //   warp 0      TMA producer: lane p loads page p of a step's K, then of its V;
 //   warp 1      MMA issuer: S of step k + 1 before PV of step k, so that it
 //               never waits for a softmax with work at hand;
 //   warp 2      q: rotates the item's query heads, splits them into parts;
 //   warp 3      metadata: walks the items, page ids and scales of each step;
-//   warps 4-11  two softmax warpgroups, items in turn: thread t has token t of
-//               every tile, and output dim t.  S, P and O have two buffers, by
-//               the parity of the step.
-// One warpgroup and one buffer took 4.9 us a step (64 x 4096), a chain of S MMAs
-// 1.1, scores and maximum 0.7, weights 0.7, PV 1.5 and the item's end 1.3 us,
-// where the step's bytes take 3.0 us of this SM's share of the bandwidth.
+//   warps 4-19  softmax: warpgroup j has tile j of a step, a thread one token, and
+//               in the accumulation heads j, j + 4, a thread one output dim.
+// S, P and O have two buffers, by the parity of the step; O of step k is added
+// up after the weights of step k + 1 are out.  With a step's four tiles in one
+// thread (two warpgroups in turn) each warp ran through 1000 straight
+// instructions a step and waited for instruction fetches a third of its time:
+// 4.4 us a step where its bytes take 3.0 us of this SM's share of the bandwidth.
 // Nothing depends on B, W or the grid.
 #include <atomic>
 #include <cstring>
@@ -50,7 +51,8 @@ namespace rk {
 
 namespace {
 
-constexpr int DQ_THREADS = 384;
+constexpr int DQ_SOFTMAX = 512;                   // softmax threads
+constexpr int DQ_THREADS = 128 + DQ_SOFTMAX;
 constexpr int DQ_TILE = 128;                      // tokens of a tile
 constexpr int DQ_TILE_BYTES = DQ_TILE * HEAD_DIM;  // 16 KiB
 constexpr int DQ_TILES = 4;                       // tiles of a step
@@ -62,14 +64,16 @@ constexpr int DQ_PRE = 1024;                      // row groups of the item list
 template <int G>
 struct DqShape {
     static constexpr int NS = 4 * G < 16 ? 16 : 4 * G;  // columns of S: part * G + head
-    static constexpr int NP = 3 * G <= 16 ? 16 : 32;    // columns of O
+    static constexpr int NP = 3 * G <= 16 ? 16 : 32;    // columns of O: part * G + head
+    static constexpr int OWN = G <= 4 ? 1 : 2;          // heads that a softmax warpgroup adds up
     // tensor memory: two S buffers of DQ_TILES x NS columns, two O buffers
     static constexpr int TMEM_S = DQ_TILES * NS, TMEM_O = 2 * TMEM_S;
     static constexpr int TMEM_COLS = TMEM_O + 2 * NP <= 256 ? 256 : 512;
     // shared memory: tiles on the way or in use (192 or 176 KiB), two q operands, two
     // steps' weights (an operand per tile)
     static constexpr int STAGES = G == 8 ? 11 : 12;
-    static constexpr int Q_BYTES = NS * 128, P_BYTES = NP * 128;
+    // weights of a tile: 16 columns of O to a 16-byte row per token, MN-major without swizzle
+    static constexpr int Q_BYTES = NS * 128, P_BYTES = NP * DQ_TILE;
     static constexpr int OFF_Q = STAGES * DQ_TILE_BYTES;
     static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
     static constexpr int OFF_CTRL = OFF_P + 2 * DQ_TILES * P_BYTES;
@@ -99,9 +103,9 @@ struct DqCtrl {
     alignas(16) float4 sc[DQ_SLOTS][DQ_PAGES];  // k scale, log2 of v's, 1 / v's
     float qscale[2][8];              // score factor of each head (log2 domain)
     int qbad[2];                     // heads whose query is out of range, a bit each
-    float red[2][4][8];              // of each softmax warpgroup
-    float lred[2][4][8];
-    int fred[2][4];
+    float red[2][16][8];             // a step's maximum of each softmax warp, by parity
+    float lred[2][16][8];            // an item's sums of each softmax warp, by parity
+    uint32_t fred[2][16];            // heads out of range
     int pre[DQ_PRE + 1];             // row splits before each group of rows
 };
 template <int G>
@@ -175,15 +179,15 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         for (int i = 0; i < DQ_SLOTS; ++i) {
             mbar_init(smem_u32(&c->id_full[i]), 1);
             mbar_init(smem_u32(&c->sc_full[i]), 1);
-            mbar_init(smem_u32(&c->slot_empty[i]), 11);  // producer, issuer, q, eight softmax warps
+            mbar_init(smem_u32(&c->slot_empty[i]), 19);  // producer, issuer, q, softmax warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&c->q_full[i]), 1);
-            mbar_init(smem_u32(&c->q_empty[i]), 5);      // issuer's commit, four softmax warps
+            mbar_init(smem_u32(&c->q_empty[i]), 17);     // issuer's commit, softmax warps
             mbar_init(smem_u32(&c->s_full[i]), 1);
-            mbar_init(smem_u32(&c->p_ready[i]), 128);
+            mbar_init(smem_u32(&c->p_ready[i]), 16);
             mbar_init(smem_u32(&c->o_full[i]), 1);
-            mbar_init(smem_u32(&c->o_read[i]), 128);
+            mbar_init(smem_u32(&c->o_read[i]), 16);
         }
         mbar_init(smem_u32(&c->never), 1);
         fence_mbar_init();
@@ -399,8 +403,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         if (lane == 0) {
             // ============================================== MMA issuer ====
             constexpr uint32_t idS = idesc_e4m3_f32(DQ_TILE, NS, 0, 0);
-            constexpr uint32_t idO = idesc_e4m3_f32(HEAD_DIM, NP, 1, 0);
-            const uint32_t dT = desc_lo(s_base, 16), dQ = desc_lo(s_base + Sh::OFF_Q, 16), dP = desc_lo(s_base + Sh::OFF_P, 16);
+            constexpr uint32_t idO = idesc_e4m3_f32(HEAD_DIM, NP, 1, 1);
+            const uint32_t dT = desc_lo(s_base, 16), dQ = desc_lo(s_base + Sh::OFF_Q, 16), dP = desc_lo(s_base + Sh::OFF_P, 128);
             constexpr uint32_t TILE = DQ_TILE_BYTES >> 4;
             // Tiles arrive step by step, K before V: with S one step ahead of PV, the K
             // tiles are counted from nk and the V tiles of the step before from nv.
@@ -423,9 +427,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     const int kn = min(4, (pv_cnt - j * DQ_TILE + 31) / 32);  // k-steps that hold tokens
                     if (kn == 4) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mma_f8(d, dv + 256 * i, dp + 2 * i, idO, i > 0 || j > 0);
+                        for (int i = 0; i < 4; ++i) mma_f8_pv(d, dv + 256 * i, dp + 32 * i, idO, i > 0 || j > 0);
                     } else {
-                        for (int i = 0; i < kn; ++i) mma_f8(d, dv + 256 * i, dp + 2 * i, idO, i > 0 || j > 0);
+                        for (int i = 0; i < kn; ++i) mma_f8_pv(d, dv + 256 * i, dp + 32 * i, idO, i > 0 || j > 0);
                     }
                     umma_commit(smem_u32(&c->empty[n % STAGES]));
                 }
@@ -486,213 +490,259 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         }
     } else {
         // ===================================================== softmax ====
-        const int wg = (warp >> 2) - 1;                // takes items wg, wg + 2, ... of the CTA
-        const int t = tid & 127, w4 = warp & 3;        // token of each tile, output dim
-        const uint32_t lane_addr = (uint32_t)(w4 * 32) << 16;
-        int slot = 0, use = 0, n = 0, nq = 0, ks = 0;  // tiles, items, steps before this one (both warpgroups')
-        float M[G], l[G], o[G], sc[G];
-        int bad = 0;       // the item's status bits
+        const int sw = warp - 4, wg = sw >> 2;         // softmax warp, warpgroup (tile)
+        const int t = tid & 127;                       // token of the tile, output dim
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        constexpr int OWN = Sh::OWN;                   // heads wg, wg + 4 are this warpgroup's
+        int slot = 0, use = 0, n = 0, nq = 0, ks = 0;  // tiles, items, steps so far
+        float M[G], l[G], sc[G];
+        int bad = 0;         // the item's status bits
         uint32_t range = 0;  // heads that met a value FP32 cannot hold
-        long long resume = blockIdx.x + (long long)wg * gridDim.x;  // first item not written
-        // The warpgroup leaves the loop together: a warp whose wait gave up goes on to
-        // the next barrier, which tells the others.
+        float o[OWN];
+        // the step whose O is due: scales of what is summed so far and of O, the item's end
+        int due = 0;
+        float al[OWN], be[OWN], Mo[OWN];
+        DqStep dst{};
+        int dbad = 0, dpar = 0;
+        long long resume = blockIdx.x;  // first item not written
+        // The warps leave the loop together: one whose wait gave up goes on to the
+        // next barrier, which tells the others.
         bool ok = true;
         auto wait = [&](uint64_t& bar, int parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), (uint32_t)(parity & 1), pc));
+        };
+        // Results of an item from the warps' sums (behind a barrier).
+        auto finish = [&](const DqStep& st, int par, int status, bool none) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int w = 0; w < 16; ++w) any |= c->fred[par][w];
+#pragma unroll
+            for (int i = 0; i < OWN; ++i) {
+                const int g = wg + 4 * i;
+                if (g < G) {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < 16; ++w) sum += c->lred[par][w][g];
+                    const bool over = !none && (((any >> g) & 1u) || !(sum > 0.0f && sum < INFINITY));
+                    const bool fail = status || over;
+                    // dims that come out beyond FP32 fail the head too, all 128 of them
+                    const float x = o[i] * (1.0f / sum);
+                    const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : Mo[i] - 8.0f + log2f(sum);
+                    write_item(a, st, g, t, fail || none ? 0.0f : x, lse2);
+                    if (t == 0 && a.status && (over || status)) atomicOr(a.status, status ? status : RK_STATUS_RANGE);
+                }
+            }
+            resume = (long long)st.item + gridDim.x;
         };
         while (true) {
             wait(c->id_full[slot], use);
             wait(c->sc_full[slot], use);
             DqStep st{};
-            float4 ps[DQ_TILES];
+            float4 ps = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
             if (ok) {
                 const volatile DqStep* s = &c->step[slot];
                 st.b = s->b;
                 st.h = s->h;
                 st.split = s->split;
-                st.n_splits = s->n_splits;
                 st.cnt = s->cnt;
                 st.first = s->first;
                 st.last = s->last;
                 st.item = s->item;
                 st.bad = s->bad;
-#pragma unroll
-                for (int j = 0; j < DQ_TILES; ++j) ps[j] = c->sc[slot][8 * j + (t >> 4)];
+                ps = c->sc[slot][8 * wg + (t >> 4)];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
                 if (++slot == DQ_SLOTS) {
                     slot = 0;
                     ++use;
                 }
-                nq += st.first;
-                if (st.item >= 0 && ((nq - 1) & 1) != wg) {  // the other warpgroup's
-                    ks += st.cnt > 0;
-                    n += 2 * ((st.cnt + DQ_TILE - 1) / DQ_TILE);
-                    continue;
-                }
                 if (st.first && st.item >= 0) {
-                    const int buf = (nq - 1) & 1;
-                    wait(c->q_full[buf], (nq - 1) >> 1);
+                    const int buf = nq & 1;
+                    wait(c->q_full[buf], nq >> 1);
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
                         M[g] = -INFINITY;
-                        l[g] = o[g] = 0.0f;
+                        l[g] = 0.0f;
                         sc[g] = c->qscale[buf][g];
                     }
                     bad = 0;
                     range = (uint32_t)c->qbad[buf];
                     __syncwarp();
                     if (ok && lane == 0) mbar_arrive(smem_u32(&c->q_empty[buf]));
+                    ++nq;
                 }
             }
-            const int tiles = (st.cnt + DQ_TILE - 1) / DQ_TILE;
-            // scores of the thread's tokens: w = z + log2 vs (-inf past the last token)
-            float w[DQ_TILES][G], mx[G];
-#pragma unroll
-            for (int g = 0; g < G; ++g) mx[g] = -INFINITY;
+            const int tiles = (st.cnt + DQ_TILE - 1) / DQ_TILE, par = ks & 1;
+            // scores of the thread's token: w = z + log2 vs (-inf past the last one)
+            float w[G];
             if (st.cnt > 0) {
-                wait(c->s_full[ks & 1], ks >> 1);
+#pragma unroll
+                for (int g = 0; g < G; ++g) w[g] = -INFINITY;
+                wait(c->s_full[par], ks >> 1);
                 tc_fence_after();
-                const uint32_t ts = tmem + lane_addr + (ks & 1) * Sh::TMEM_S;
-#pragma unroll
-                for (int j = 0; j < DQ_TILES; ++j) {
+                if (wg < tiles) {
                     uint32_t r[NS];
-                    if (j < tiles) {
-                        if constexpr (NS == 16) tmem_ld16(ts + j * NS, r);
-                        else tmem_ld32(ts + j * NS, r);
-                        tmem_ld_wait();
-                    }
-                    const bool in = j * DQ_TILE + t < st.cnt;
+                    const uint32_t ts = tmem + lane_addr + par * Sh::TMEM_S + wg * NS;
+                    if constexpr (NS == 16) tmem_ld16(ts, r);
+                    else tmem_ld32(ts, r);
+                    tmem_ld_wait();
+                    if (wg * DQ_TILE + t < st.cnt) {
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        w[j][g] = -INFINITY;
-                        if (in) {
+                        for (int g = 0; g < G; ++g) {
                             const float hi = __uint_as_float(r[g]) + __uint_as_float(r[G + g]);
                             const float lo = __uint_as_float(r[2 * G + g]) + __uint_as_float(r[3 * G + g]);
-                            const float z = fmaf(lo, 1.0f / 256.0f, hi) * (ps[j].x * sc[g]);
+                            const float z = fmaf(lo, 1.0f / 256.0f, hi) * (ps.x * sc[g]);
                             if (!(fabsf(z) < INFINITY)) range |= 1u << g;
-                            w[j][g] = z + ps[j].y;
-                            mx[g] = fmaxf(mx[g], w[j][g]);
+                            w[g] = z + ps.y;
                         }
                     }
                 }
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float x = warp_max(mx[g]);
-                    if (lane == 0) c->red[wg][w4][g] = x;
+                    const float x = warp_max(w[g]);
+                    if (lane == 0) c->red[par][sw][g] = x;
                 }
             }
-            if (named_bar_or(1 + wg, 128, !ok)) {
+            if (named_bar_or(1, DQ_SOFTMAX, !ok)) {
                 ok = false;
                 break;
             }
-            if (st.item < 0) break;
-            bad |= st.bad;
+            float aln[OWN], ben[OWN];  // this step's scales of o and O
             if (st.cnt > 0) {
-                float beta[G];
+                float p[G], beta[G];
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float m = fmaxf(fmaxf(c->red[wg][0][g], c->red[wg][1][g]), fmaxf(c->red[wg][2][g], c->red[wg][3][g]));
-                    mx[g] = m > -INFINITY && m < INFINITY ? m : 0.0f;  // otherwise the head fails (range)
-                    const float top = fmaxf(M[g], mx[g]);
+                    float m = warp_max(c->red[par][lane & 15][g]);
+                    m = fabsf(m) < INFINITY ? m : 0.0f;  // otherwise the head fails (range)
+                    const float top = fmaxf(M[g], m);
                     const float alpha = ex2(M[g] - top);
-                    beta[g] = ex2(mx[g] - top);
+                    beta[g] = ex2(m - top);
                     M[g] = top;
-                    l[g] *= alpha;
-                    o[g] *= alpha;
+                    p[g] = ex2(w[g] - m + 8.0f);
+                    l[g] = fmaf(l[g], alpha, p[g] * ps.z * beta[g]);
+                    if ((g & 3) == wg) {
+                        aln[g >> 2] = alpha;
+                        ben[g >> 2] = beta[g];
+                    }
                 }
                 // the weights' buffer is free once the PV of step k - 2 is done
-                wait(c->o_full[ks & 1], (ks >> 1) + 1);
-                uint8_t* pt = sm + Sh::OFF_P + (ks & 1) * DQ_TILES * Sh::P_BYTES;
-                // weights p' = 2^(w - m + 8) as three e4m3 parts; rows part * G + head of tile j's operand
+                wait(c->o_full[par], (ks >> 1) + 1);
+                if (wg < tiles) {
+                    // p' = 2^(w - m + 8) as three e4m3 parts, part * G + head of the token's row
+                    uint32_t wd[NP / 4];
 #pragma unroll
-                for (int j = 0; j < DQ_TILES; j += 2) {
+                    for (int i = 0; i < NP / 4; ++i) wd[i] = 0;
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        float2 p = make_float2(ex2(w[j][g] - mx[g] + 8.0f), ex2(w[j + 1][g] - mx[g] + 8.0f));
-                        l[g] = fmaf(beta[g], fmaf(p.x, ps[j].z, p.y * ps[j + 1].z), l[g]);
+                    for (int g = 0; g < G; g += 2) {
+                        float2 x = make_float2(p[g], g + 1 < G ? p[g + 1 < G ? g + 1 : g] : 0.0f);
 #pragma unroll
                         for (int e = 0; e < 3; ++e) {
-                            const uint32_t k = take_part(p);
-                            const uint32_t at = sw128_off(e * G + g, t >> 4) + (t & 15);
-                            pt[j * Sh::P_BYTES + at] = (uint8_t)k;
-                            pt[(j + 1) * Sh::P_BYTES + at] = (uint8_t)(k >> 8);
+                            const int col = e * G + g;
+                            wd[col >> 2] |= take_part(x) << (8 * (col & 3));
                         }
                     }
+                    uint8_t* pt = sm + Sh::OFF_P + (par * DQ_TILES + wg) * Sh::P_BYTES + t * 16;
+#pragma unroll
+                    for (int i = 0; i < NP / 16; ++i)
+                        *reinterpret_cast<uint4*>(pt + i * DQ_TILE * 16) = make_uint4(wd[4 * i], wd[4 * i + 1], wd[4 * i + 2], wd[4 * i + 3]);
                 }
                 if (st.cnt & 31) {
                     // the k-step that the last token is in: V rows behind it hold anything, and 0 times a NaN
                     // is not 0
-                    const int j = tiles - 1, stg = (n + 2 * tiles - 1) % STAGES;
-                    wait(c->full[stg], (n + 2 * tiles - 1) / STAGES);
-                    const int r0 = st.cnt - j * DQ_TILE, r1 = (r0 + 31) & ~31;
-                    for (int i = t; ok && i < (r1 - r0) * 8; i += 128)
+                    const int j = tiles - 1, last = n + 2 * tiles - 1, stg = last % STAGES;
+                    wait(c->full[stg], last / STAGES);
+                    const int r0 = st.cnt - j * DQ_TILE, r1 = (r0 + 31) & ~31, i = tid - 128;
+                    if (ok && i < (r1 - r0) * 8)
                         reinterpret_cast<uint4*>(sm + stg * DQ_TILE_BYTES + r0 * 128)[i] = make_uint4(0, 0, 0, 0);
                 }
                 n += 2 * tiles;
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(smem_u32(&c->p_ready[ks & 1]));
-                wait(c->o_full[ks & 1], ks >> 1);
-                tc_fence_after();
-                {
-                    uint32_t r[NP];
-                    if constexpr (NP == 16) tmem_ld16(tmem + lane_addr + Sh::TMEM_O + (ks & 1) * NP, r);
-                    else tmem_ld32(tmem + lane_addr + Sh::TMEM_O + (ks & 1) * NP, r);
-                    tmem_ld_wait();
-                    tc_fence_before();
-                    mbar_arrive(smem_u32(&c->o_read[ks & 1]));
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const float x = (__uint_as_float(r[2 * G + g]) + __uint_as_float(r[G + g])) + __uint_as_float(r[g]);
-                        o[g] = fmaf(x, beta[g], o[g]);
-                    }
-                }
-                ++ks;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c->p_ready[par]));
             }
-            if (st.last) {
-                // sums over the warpgroup in a fixed order, and what went wrong anywhere
+            // the item's sums, at its last step
+            const int ipar = (nq + 1) & 1;
+            bad |= st.bad;
+            if (st.last && st.item >= 0) {
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     float x = l[g];
 #pragma unroll
                     for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-                    if (lane == 0) c->lred[wg][w4][g] = x;
-                    if (!(fabsf(o[g]) < INFINITY)) range |= 1u << g;
+                    if (lane == 0) c->lred[ipar][sw][g] = x;
                 }
                 range = __reduce_or_sync(0xffffffffu, range);
-                if (lane == 0) c->fred[wg][w4] = (int)range;
-                if (named_bar_or(1 + wg, 128, !ok)) {
+                if (lane == 0) c->fred[ipar][sw] = range;
+            }
+            // O of the step before
+            if (due) {
+                const int k = ks - 1, db = k & 1;
+                wait(c->o_full[db], k >> 1);
+                tc_fence_after();
+                uint32_t r[OWN][3];
+                const uint32_t to = tmem + lane_addr + Sh::TMEM_O + db * NP;
+#pragma unroll
+                for (int i = 0; i < OWN; ++i)
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) tmem_ld1(to + e * G + (G > wg + 4 * i ? wg + 4 * i : 0), r[i][e]);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c->o_read[db]));
+                uint32_t over = 0;
+#pragma unroll
+                for (int i = 0; i < OWN; ++i) {
+                    const float x = (__uint_as_float(r[i][2]) + __uint_as_float(r[i][1])) + __uint_as_float(r[i][0]);
+                    o[i] = fmaf(x, be[i], o[i] * al[i]);
+                    if (!(fabsf(o[i]) < INFINITY)) over |= 1u << (wg + 4 * i);
+                }
+                if (dst.last) {
+                    // o may be beyond FP32 (a NaN code in V) in a dim only; the head's 128 threads agree on it
+                    over = __reduce_or_sync(0xffffffffu, over);
+                    if (over && lane == 0) atomicOr(&c->fred[dpar][sw], over);
+                    if (named_bar_or(1, DQ_SOFTMAX, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    finish(dst, dpar, dbad, false);
+                }
+                due = 0;
+            }
+            if (st.item < 0) break;
+            if (st.cnt > 0) {
+                due = 1;
+                dst = st;
+                dbad = bad;
+                dpar = ipar;
+#pragma unroll
+                for (int i = 0; i < OWN; ++i) {
+                    al[i] = aln[i];
+                    be[i] = ben[i];
+                    if (st.first) o[i] = 0.0f;
+#pragma unroll
+                    for (int g = i * 4; g < G && g < i * 4 + 4; ++g)
+                        if ((g & 3) == wg) Mo[i] = M[g];
+                }
+                ++ks;
+            } else if (st.last) {
+                // nothing in this step: an empty row, or one that fails
+                if (named_bar_or(1, DQ_SOFTMAX, !ok)) {
                     ok = false;
                     break;
                 }
-                range = (uint32_t)(c->fred[wg][0] | c->fred[wg][1] | c->fred[wg][2] | c->fred[wg][3]);
-                const bool none = M[0] == -INFINITY;  // no visible key
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const float sum = (c->lred[wg][0][g] + c->lred[wg][1][g]) + (c->lred[wg][2][g] + c->lred[wg][3][g]);
-                    if (!none && !(sum > 0.0f && sum < INFINITY)) range |= 1u << g;
-                    const bool fail = bad || (!none && ((range >> g) & 1u));
-                    const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : M[g] - 8.0f + log2f(sum);
-                    write_item(a, st, g, t, fail || none ? 0.0f : o[g] / sum, lse2);
-                }
-                if (t == 0 && a.status) {
-                    const int say = bad | (!none && !bad && range ? RK_STATUS_RANGE : 0);
-                    if (say) atomicOr(a.status, say);
-                }
-                resume = (long long)st.item + 2ll * gridDim.x;
-                named_bar_sync(1 + wg, 128);  // lred and fred may be written again
+                finish(st, ipar, bad, M[0] == -INFINITY);
             }
         }
         if (!ok) {  // a wait gave up: this CTA's items from here on are written as failed
-            for (long long it = resume; it < items; it += 2ll * gridDim.x) {
+            for (long long it = resume; it < items; it += gridDim.x) {
                 DqStep st{};
                 int nk, bd;
                 st.h = (int)(it % a.Hkv);
                 find_row(a, c, (int)(it / a.Hkv), st.b, st.split, nk, bd);
-                for (int g = 0; g < G; ++g) write_item(a, st, g, t, 0.0f, __int_as_float(0x7fc00000));
+                for (int g = wg; g < G; g += 4) write_item(a, st, g, t, 0.0f, __int_as_float(0x7fc00000));
             }
-            if (t == 0 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
+            if (tid == 128 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
         }
     }
     __syncwarp();

@@ -66,4 +66,23 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a_lo, uint32_t b_lo,
         : "memory");
 }
 
+// The same with B an MN-major tile without swizzle: 16 values of a row of K in 16
+// bytes, rows 16 bytes apart, so groups of 8 rows (the leading byte offset, in
+// b_lo) are 128 bytes apart and blocks of 16 columns 2 KiB (128 rows).
+constexpr uint32_t DESC_HI_ROWS16 = (2048u >> 4) | (1u << 14);
+__device__ __forceinline__ void mma_f8_pv(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %6};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(DESC_HI), "r"(acc), "r"(DESC_HI_ROWS16)
+        : "memory");
+}
+
+// 32 lanes x one 32-bit column.
+__device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
+
 }  // namespace rk
