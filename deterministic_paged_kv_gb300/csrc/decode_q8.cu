@@ -30,8 +30,8 @@
 // ordered by row, split, KV head, so neighbouring CTAs read neighbouring blocks.
 // Roles (20 warps):
 //   warp 0      TMA producer: lane p loads page p of a step's K, then of its V;
-//   warp 1      MMA issuer: S of step k + 1 before PV of step k, so that it
-//               never waits for a softmax with work at hand;
+//   warp 1      MMA issuer: S and PV of each step, S of step k + 1 first where
+//               its K is here before the weights of step k are;
 //   warp 2      q: rotates the item's query heads, splits them into parts;
 //   warp 3      metadata: walks the items, page ids and scales of each step;
 //   warps 4-19  softmax: warpgroup j has tile j of a step, a thread one token, and
@@ -81,7 +81,6 @@ struct DqShape {
 
 struct DqStep {
     int b, h, split;   // row, KV head, split
-    int n_splits;      // of the row
     int cnt;           // tokens of the step (0: nothing to compute)
     int first, last;   // of the item
     int item;          // index in the item list; -1: no more
@@ -241,61 +240,70 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         // ==================================================== metadata ====
         int slot = 0, use = 0;  // ring position and how often it went round
         bool ok = true;
-        for (long long it = blockIdx.x; ok; it += gridDim.x) {
-            DqStep st{};
+        DqStep st{};
+        int t = 0, t1 = 0, id = 0;  // the step's first token, the item's end, the lane's page id
+        long long it = blockIdx.x;
+        auto item = [&]() {  // the item `it` and its first page ids
+            st = DqStep{};
             st.item = -1;
-            int n = 0, t0 = 0, t1 = 0;
+            st.first = 1;
+            t = t1 = 0;
             if (it < items) {
+                int n;
                 st.item = (int)it;
                 st.h = (int)(it % a.Hkv);
                 find_row(a, c, (int)(it / a.Hkv), st.b, st.split, n, st.bad);
-                st.n_splits = splits_of(n, a.split_tokens);
-                t0 = st.split * a.split_tokens;
-                t1 = min(n, t0 + a.split_tokens);
+                t = st.split * a.split_tokens;
+                t1 = min(n, t + a.split_tokens);
             }
-            const int32_t* bt = a.block_table + (size_t)st.b * a.W;
-            int id = lane * PAGE < t1 - t0 ? __ldg(bt + t0 / PAGE + lane) : 0;
-            for (int t = t0; ok; t += DQ_STEP) {
-                const int cnt = max(0, min(DQ_STEP, t1 - t));
-                const bool mine = lane * PAGE < cnt;
-                const bool oob = mine && (id < 0 || id >= a.num_pages);
-                st.first = t == t0;
-                st.last = t + DQ_STEP >= t1;
-                st.cnt = cnt;
-                if (__any_sync(0xffffffffu, oob)) {
-                    st.bad |= RK_STATUS_PAGE_OOB;
-                    st.cnt = 0;
-                }
-                int good = 1;
-                if (lane == 0) good = mbar_wait(smem_u32(&c->slot_empty[slot]), (uint32_t)((use & 1) ^ 1), pc);
-                if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
-                c->ids[slot][lane] = id;
-                if (lane == 0) c->step[slot] = st;  // bad scales are added below, before sc_full
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&c->id_full[slot]));
-                // the next step's page ids travel while this step's scales do
-                const int cur = id;
-                id = !st.last && lane * PAGE < t1 - t - DQ_STEP ? __ldg(bt + (t + DQ_STEP) / PAGE + lane) : 0;
-                float ks = 1.0f, vs = 1.0f;
-                if (mine && st.cnt > 0) {
-                    const size_t block = (size_t)cur * a.Hkv + st.h;
-                    ks = __ldg(a.k_scale + block);
-                    vs = __ldg(a.v_scale + block);
-                }
-                const bool odd = !scale_ok(ks) || !scale_ok(vs);
-                if (odd) ks = vs = 1.0f;
-                c->sc[slot][lane] = make_float4(ks, __log2f(vs), 1.0f / vs, 0.0f);
-                if (__any_sync(0xffffffffu, odd) && lane == 0) c->step[slot].bad = st.bad | RK_STATUS_SCALE;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&c->sc_full[slot]));
-                if (++slot == DQ_SLOTS) {
-                    slot = 0;
-                    ++use;
-                }
-                st.bad = 0;  // reported once
-                if (st.last) break;
+            id = lane * PAGE < t1 - t ? __ldg(a.block_table + (size_t)st.b * a.W + t / PAGE + lane) : 0;
+        };
+        item();
+        while (ok) {
+            const int cnt = max(0, min(DQ_STEP, t1 - t));
+            const bool mine = lane * PAGE < cnt;
+            const bool oob = mine && (id < 0 || id >= a.num_pages);
+            st.last = t + DQ_STEP >= t1;
+            st.cnt = cnt;
+            if (__any_sync(0xffffffffu, oob)) {
+                st.bad |= RK_STATUS_PAGE_OOB;
+                st.cnt = 0;
             }
-            if (st.item < 0) break;
+            int good = 1;
+            if (lane == 0) good = mbar_wait(smem_u32(&c->slot_empty[slot]), (uint32_t)((use & 1) ^ 1), pc);
+            if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
+            c->ids[slot][lane] = id;
+            if (lane == 0) c->step[slot] = st;  // bad scales are added below, before sc_full
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c->id_full[slot]));
+            float ks = 1.0f, vs = 1.0f;
+            if (mine && st.cnt > 0) {
+                const size_t block = (size_t)id * a.Hkv + st.h;
+                ks = __ldg(a.k_scale + block);
+                vs = __ldg(a.v_scale + block);
+            }
+            // the next step's page ids travel while this step's scales do
+            const bool end = st.item < 0;
+            const int bad = st.bad;
+            st.bad = st.first = 0;  // reported once
+            if (st.last) {
+                it += gridDim.x;
+                if (!end) item();
+            } else {
+                t += DQ_STEP;
+                id = lane * PAGE < t1 - t ? __ldg(a.block_table + (size_t)st.b * a.W + t / PAGE + lane) : 0;
+            }
+            const bool odd = !scale_ok(ks) || !scale_ok(vs);
+            if (odd) ks = vs = 1.0f;
+            c->sc[slot][lane] = make_float4(ks, __log2f(vs), 1.0f / vs, 0.0f);
+            if (__any_sync(0xffffffffu, odd) && lane == 0) c->step[slot].bad = bad | RK_STATUS_SCALE;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c->sc_full[slot]));
+            if (++slot == DQ_SLOTS) {
+                slot = 0;
+                ++use;
+            }
+            if (end) break;
         }
     } else if (warp == 0) {
         // ==================================================== producer ====
@@ -400,92 +408,93 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             ++nq;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ============================================== MMA issuer ====
-            constexpr uint32_t idS = idesc_e4m3_f32(DQ_TILE, NS, 0, 0);
-            constexpr uint32_t idO = idesc_e4m3_f32(HEAD_DIM, NP, 1, 1);
-            const uint32_t dT = desc_lo(s_base, 16), dQ = desc_lo(s_base + Sh::OFF_Q, 16), dP = desc_lo(s_base + Sh::OFF_P, 128);
-            constexpr uint32_t TILE = DQ_TILE_BYTES >> 4;
-            // Tiles arrive step by step, K before V: with S one step ahead of PV, the K
-            // tiles are counted from nk and the V tiles of the step before from nv.
-            int slot = 0, use = 0, nk = 0, nq = 0, ks = 0;  // next tile, items, steps (S)
-            int pv_cnt = 0, nv = 0;                         // the step whose PV is due: tokens, first V tile
-            bool ok = !a.timeout_drill || drill_wait(smem_u32(&c->never), pc);
-            auto tile_in = [&](int n) { return mbar_wait(smem_u32(&c->full[n % STAGES]), (uint32_t)((n / STAGES) & 1), pc); };
-            // PV of step k
-            auto issue_pv = [&](int k) -> bool {
-                const int buf = k & 1;
-                const uint32_t par = (uint32_t)((k >> 1) & 1);
-                if (!mbar_wait(smem_u32(&c->o_read[buf]), par ^ 1u, pc)) return false;  // step k - 2's result is read
-                if (!mbar_wait(smem_u32(&c->p_ready[buf]), par, pc)) return false;
-                const uint32_t d = tmem + Sh::TMEM_O + buf * NP;
-                for (int j = 0; j * DQ_TILE < pv_cnt; ++j) {
-                    const int n = nv + j;
-                    if (!tile_in(n)) return false;
-                    tc_fence_after();
-                    const uint32_t dv = dT + (n % STAGES) * TILE, dp = dP + (buf * DQ_TILES + j) * (Sh::P_BYTES >> 4);
-                    const int kn = min(4, (pv_cnt - j * DQ_TILE + 31) / 32);  // k-steps that hold tokens
-                    if (kn == 4) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mma_f8_pv(d, dv + 256 * i, dp + 32 * i, idO, i > 0 || j > 0);
-                    } else {
-                        for (int i = 0; i < kn; ++i) mma_f8_pv(d, dv + 256 * i, dp + 32 * i, idO, i > 0 || j > 0);
-                    }
-                    umma_commit(smem_u32(&c->empty[n % STAGES]));
-                }
-                umma_commit(smem_u32(&c->o_full[buf]));
-                return true;
-            };
-            while (ok) {
-                if (!(ok = mbar_wait(smem_u32(&c->id_full[slot]), (uint32_t)(use & 1), pc))) break;
-                const volatile DqStep* st = &c->step[slot];
-                const int cnt = st->cnt, first = st->first, last = st->last, end = st->item < 0;
-                if (!end) {
-                    mbar_arrive(smem_u32(&c->slot_empty[slot]));
-                    if (++slot == DQ_SLOTS) {
-                        slot = 0;
-                        ++use;
-                    }
-                    const int qb = nq & 1;
-                    if (first && !(ok = mbar_wait(smem_u32(&c->q_full[qb]), (uint32_t)((nq >> 1) & 1), pc))) break;
-                    const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE;
-                    for (int j = 0; j < tiles; ++j) {
-                        if (!(ok = tile_in(nk + j))) break;
-                        tc_fence_after();
-                        const uint32_t dk = dT + ((nk + j) % STAGES) * TILE, dq = dQ + qb * (Sh::Q_BYTES >> 4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_f8(tmem + (ks & 1) * Sh::TMEM_S + j * NS, dk + 2 * i, dq + 2 * i, idS, i > 0);
-                        umma_commit(smem_u32(&c->empty[(nk + j) % STAGES]));
-                    }
-                    if (!ok) break;
-                    if (tiles > 0) umma_commit(smem_u32(&c->s_full[ks & 1]));
-                    if (last) {
-                        umma_commit(smem_u32(&c->q_empty[qb]));
-                        ++nq;
-                    }
-                    if (tiles == 0) {
-                        // nothing to run ahead of: the step before must not wait for what
-                        // comes (its softmax holds descriptor slots up)
-                        if (pv_cnt > 0 && !(ok = issue_pv(ks - 1))) break;
-                        pv_cnt = 0;
-                        continue;
-                    }
-                }
-                // S of this step is under way (its buffer was read by step k - 2's softmax, whose
-                // weights the PV before last waited for); now the PV of the step before
-                if (pv_cnt > 0 && !(ok = issue_pv(ks - 1))) break;
-                if (end) break;
-                const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE;
-                pv_cnt = cnt;
-                nv = nk + tiles;
-                nk += 2 * tiles;
-                ++ks;
+        // ================================================== MMA issuer ====
+        // The whole warp, converged, so that the operands stay in uniform registers
+        // (one lane alone took 130 cycles an MMA, most of it moving descriptors).
+        constexpr uint32_t idS = idesc_e4m3_f32(DQ_TILE, NS, 0, 0);
+        constexpr uint32_t idO = idesc_e4m3_f32(HEAD_DIM, NP, 1, 1);
+        const uint32_t dT = desc_lo(s_base, 16), dQ = desc_lo(s_base + Sh::OFF_Q, 16), dP = desc_lo(s_base + Sh::OFF_P, 128);
+        constexpr uint32_t TILE = DQ_TILE_BYTES >> 4;
+        int slot = 0, use = 0, nk = 0, nq = 0, ks = 0;  // next tile, items, steps (S)
+        int pv_cnt = 0, nv = 0;                         // the step whose PV is due: tokens, first V tile
+        auto wait = [&](uint64_t& bar, int parity) {
+            return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), (uint32_t)(parity & 1), pc)) != 0;
+        };
+        bool ok = !a.timeout_drill || __all_sync(0xffffffffu, drill_wait(smem_u32(&c->never), pc));
+        // PV of step k
+        auto issue_pv = [&](int k) -> bool {
+            const int buf = k & 1;
+            if (!wait(c->o_read[buf], (k >> 1) + 1)) return false;  // step k - 2's result is read
+            if (!wait(c->p_ready[buf], k >> 1)) return false;
+            const uint32_t d = tmem + Sh::TMEM_O + buf * NP;
+#pragma unroll 1
+            for (int j = 0; j * DQ_TILE < pv_cnt; ++j) {
+                const int n = nv + j, stg = n % STAGES;
+                if (!wait(c->full[stg], n / STAGES)) return false;
+                tc_fence_after();
+                const uint32_t dv = dT + stg * TILE, dp = dP + (buf * DQ_TILES + j) * (Sh::P_BYTES >> 4);
+                const uint32_t acc = j > 0;
+                const int kn = (pv_cnt - j * DQ_TILE + 31) / 32;  // k-steps that hold tokens
+                if (kn >= 4) mma_f8_steps<0, 4, 256, 32, DESC_HI_ROWS16>(d, dv, dp, idO, acc);
+                else if (kn == 3) mma_f8_steps<0, 3, 256, 32, DESC_HI_ROWS16>(d, dv, dp, idO, acc);
+                else if (kn == 2) mma_f8_steps<0, 2, 256, 32, DESC_HI_ROWS16>(d, dv, dp, idO, acc);
+                else mma_f8_steps<0, 1, 256, 32, DESC_HI_ROWS16>(d, dv, dp, idO, acc);
+                umma_commit_elect(smem_u32(&c->empty[stg]));
             }
-            if (!ok) {  // issued MMAs drain before tensor memory is released
-                const uint64_t t0 = global_timer_ns();
-                while (global_timer_ns() - t0 < 1000000ull) {
-                }
+            umma_commit_elect(smem_u32(&c->o_full[buf]));
+            pv_cnt = 0;
+            return true;
+        };
+        while (ok) {
+            if (!(ok = wait(c->id_full[slot], use))) break;
+            const int cnt = __shfl_sync(0xffffffffu, c->step[slot].cnt, 0);
+            const int flags = __shfl_sync(0xffffffffu, c->step[slot].first | (c->step[slot].last << 1) | (c->step[slot].item < 0 ? 4 : 0), 0);
+            const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE;
+            if (flags & 4) {
+                if (pv_cnt > 0) ok = issue_pv(ks - 1);
+                break;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
+            if (++slot == DQ_SLOTS) {
+                slot = 0;
+                ++use;
+            }
+            // The PV that is due goes before this step's S, unless all of this step's K is
+            // here already: then the loads are ahead of the softmax, and S need not wait for
+            // it.  (Where the loads are behind, the V tiles' room is what they wait for.)
+            if (pv_cnt > 0) {
+                const int n = nk + tiles - 1;
+                const bool ahead = tiles > 0 && __all_sync(0xffffffffu, mbar_test(smem_u32(&c->full[n % STAGES]), (uint32_t)((n / STAGES) & 1)));
+                if (!ahead && !(ok = issue_pv(ks - 1))) break;
+            }
+            const int qb = nq & 1;
+            if ((flags & 1) && !(ok = wait(c->q_full[qb], nq >> 1))) break;
+            const uint32_t dq = dQ + qb * (Sh::Q_BYTES >> 4), ds = tmem + (ks & 1) * Sh::TMEM_S;
+#pragma unroll 1
+            for (int j = 0; j < tiles; ++j) {
+                const int n = nk + j, stg = n % STAGES;
+                if (!(ok = wait(c->full[stg], n / STAGES))) break;
+                tc_fence_after();
+                mma_f8_steps<0, 4, 2, 2, DESC_HI>(ds + j * NS, dT + stg * TILE, dq, idS, 0u);
+                umma_commit_elect(smem_u32(&c->empty[stg]));
+            }
+            if (!ok) break;
+            if (tiles > 0) umma_commit_elect(smem_u32(&c->s_full[ks & 1]));
+            if (flags & 2) {
+                umma_commit_elect(smem_u32(&c->q_empty[qb]));
+                ++nq;
+            }
+            if (tiles == 0) continue;
+            if (pv_cnt > 0 && !(ok = issue_pv(ks - 1))) break;
+            pv_cnt = cnt;
+            nv = nk + tiles;
+            nk += 2 * tiles;
+            ++ks;
+        }
+        if (!ok) {  // issued MMAs drain before tensor memory is released
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 1000000ull) {
             }
         }
     } else {

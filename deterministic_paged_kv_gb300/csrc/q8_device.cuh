@@ -54,31 +54,28 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn_maj
     return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }
-// D[tmem] (+)= A[smem] * B[smem], one k-step of 32 e4m3 values; both operands in
-// 128-byte-swizzled tiles whose rows are 128 bytes (descriptor high word DESC_HI).
-__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+// D[tmem] (+)= A[smem] * B[smem], k-steps KS .. END - 1 of 32 e4m3 values,
+// accumulating from k-step 1 on, and at k-step 0 iff acc0.  Called by a whole
+// converged warp with uniform operands; one elected lane issues.  a_lo, b_lo:
+// descriptor low words of k-step 0, A_STEP / B_STEP added for each (16-byte units,
+// immediates, so that a step costs the issuing warp no arithmetic).  A lies in a
+// 128-byte-swizzled tile (high word DESC_HI), B in one with high word B_HI.
+template <int KS, int END, uint32_t A_STEP, uint32_t B_STEP, uint32_t B_HI>
+__device__ __forceinline__ void mma_f8_steps(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc0) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(DESC_HI), "r"(acc)
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 al, bl;\n\t.reg .b64 da, db;\n\t"
+        "add.u32 al, %1, %5;\n\tadd.u32 bl, %2, %6;\n\t"
+        "mov.b64 da, {al, %4};\n\tmov.b64 db, {bl, %8};\n\t"
+        "setp.ne.b32 p, %7, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(DESC_HI), "n"(KS * A_STEP), "n"(KS * B_STEP), "r"(KS > 0 ? 1u : acc0), "r"(B_HI)
         : "memory");
+    if constexpr (KS + 1 < END) mma_f8_steps<KS + 1, END, A_STEP, B_STEP, B_HI>(d, a_lo, b_lo, idesc, acc0);
 }
-
-// The same with B an MN-major tile without swizzle: 16 values of a row of K in 16
-// bytes, rows 16 bytes apart, so groups of 8 rows (the leading byte offset, in
-// b_lo) are 128 bytes apart and blocks of 16 columns 2 KiB (128 rows).
+// High word of an MN-major tile without swizzle: 16 values of a row of K in 16
+// bytes, rows 16 bytes apart, so groups of 8 rows (the leading byte offset, in the
+// low word) are 128 bytes apart and blocks of 16 columns 2 KiB (128 rows).
 constexpr uint32_t DESC_HI_ROWS16 = (2048u >> 4) | (1u << 14);
-__device__ __forceinline__ void mma_f8_pv(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-        "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %6};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(DESC_HI), "r"(acc), "r"(DESC_HI_ROWS16)
-        : "memory");
-}
 
 // 32 lanes x one 32-bit column.
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
