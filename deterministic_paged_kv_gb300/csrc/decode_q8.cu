@@ -23,24 +23,29 @@
 //   o = sum p'_t vcode_t,  out = o / l,
 // with z_t the score in the log2 domain.
 //
-// Work: an item is a split of one (row, KV head), taken in steps of up to 512
-// tokens (4 tiles of 128); within a step the softmax is plain (one maximum over
-// its tokens), steps and splits are joined with the running maximum in FP32.
+// Work: an item is a split of a row for a bundle of H neighbouring KV heads (4, 2 or
+// 1, the most that divide Hkv).  A TMA copy takes a page's blocks of the whole
+// bundle: copies of 2 KiB (one head) get 4.36 TB/s out of a bare load loop, 4 KiB
+// 5.0, 8 KiB 5.93, and 64 x 4096 took 123 us to load head by head where a bundle
+// of four takes 91.  A step is 512 / H tokens of the bundle, four tiles of 128 tokens and
+// one head; in it the softmax is plain (one maximum over its tokens), steps and splits
+// are joined with the running maximum in FP32.  The copies leave the bundle as
+// [page][half][head][8 tokens][128 B] in shared memory, so that the 16 groups of 8
+// tokens of a head's tile lie at one stride and make one operand.
 // A persistent grid of one CTA per SM takes items c, c + grid, ... of the list
-// ordered by row, split, KV head, so neighbouring CTAs read neighbouring blocks.
+// ordered by row, split, bundle, so neighbouring CTAs read neighbouring blocks.
 // Roles (20 warps):
-//   warp 0      TMA producer: lane p loads page p of a step's K, then of its V;
-//   warp 1      MMA issuer: S and PV of each step, S of step k + 1 first where
-//               its K is here before the weights of step k are;
+//   warp 0      TMA producer: a step's K, then its V, 64 KiB each, in a ring of three;
+//   warp 1      MMA issuer: S and PV of each step;
 //   warp 2      q: rotates the item's query heads, splits them into parts;
 //   warp 3      metadata: walks the items, page ids and scales of each step;
 //   warps 4-19  softmax: warpgroup j has tile j of a step, a thread one token, and
-//               in the accumulation heads j, j + 4, a thread one output dim.
-// S, P and O have two buffers, by the parity of the step; O of step k is added
-// up after the weights of step k + 1 are out.  With a step's four tiles in one
-// thread (two warpgroups in turn) each warp ran through 1000 straight
-// instructions a step and waited for instruction fetches a third of its time:
-// 4.4 us a step where its bytes take 3.0 us of this SM's share of the bandwidth.
+//               in the accumulation its share of that KV head's queries, a thread one
+//               output dim.
+// S and O have two buffers, by the parity of the step; O of step k is added up after
+// the weights of step k + 1 are out.  (With a step's four tiles in one thread each
+// warp ran through 1000 straight instructions a step and waited for instruction
+// fetches a third of its time.)
 // Nothing depends on B, W or the grid.
 #include <atomic>
 #include <cstring>
@@ -54,43 +59,43 @@ namespace {
 constexpr int DQ_SOFTMAX = 512;                   // softmax threads
 constexpr int DQ_THREADS = 128 + DQ_SOFTMAX;
 constexpr int DQ_TILE = 128;                      // tokens of a tile
-constexpr int DQ_TILE_BYTES = DQ_TILE * HEAD_DIM;  // 16 KiB
 constexpr int DQ_TILES = 4;                       // tiles of a step
-constexpr int DQ_STEP = DQ_TILE * DQ_TILES;
-constexpr int DQ_PAGES = DQ_STEP / PAGE;          // 32: one lane each
+constexpr int DQ_STEP_BYTES = DQ_TILES * DQ_TILE * HEAD_DIM;  // K (or V) of a step: 64 KiB
 constexpr int DQ_SLOTS = 4;                       // steps the metadata runs ahead
 constexpr int DQ_PRE = 1024;                      // row groups of the item list
 
-template <int G>
+template <int G, int H>
 struct DqShape {
-    static constexpr int NS = 4 * G < 16 ? 16 : 4 * G;  // columns of S: part * G + head
-    static constexpr int NP = 3 * G <= 16 ? 16 : 32;    // columns of O: part * G + head
-    static constexpr int OWN = G <= 4 ? 1 : 2;          // heads that a softmax warpgroup adds up
-    // tensor memory: two S buffers of DQ_TILES x NS columns, two O buffers
-    static constexpr int TMEM_S = DQ_TILES * NS, TMEM_O = 2 * TMEM_S;
-    static constexpr int TMEM_COLS = TMEM_O + 2 * NP <= 256 ? 256 : 512;
-    // shared memory: tiles on the way or in use (192 or 176 KiB), two q operands, two
-    // steps' weights (an operand per tile)
-    static constexpr int STAGES = G == 8 ? 11 : 12;
-    // weights of a tile: 16 columns of O to a 16-byte row per token, MN-major without swizzle
+    static constexpr int NS = 4 * G < 16 ? 16 : 4 * G;  // columns of S: part * G + query
+    static constexpr int NP = 3 * G <= 16 ? 16 : 32;    // columns of O: part * G + query
+    static constexpr int TOKENS = DQ_TILES * DQ_TILE / H;  // of a step
+    static constexpr int SHARE = 4 / H;                 // warpgroups to a KV head
+    static constexpr int OWN = G > SHARE ? G / SHARE : 1;  // queries that one of them adds up
+    // tensor memory: two buffers of S (4 tiles) and of O (H heads)
+    static constexpr int TMEM_S = DQ_TILES * NS, TMEM_O = 2 * TMEM_S, TMEM_OBUF = H * NP;
+    static constexpr int TMEM_COLS = TMEM_O + 2 * TMEM_OBUF <= 256 ? 256 : 512;
+    // shared memory: the ring (a step's K or V to a stage), q operands (one per head of the
+    // bundle), weights (one per tile: 16 columns of O to a 16-byte row per token, MN-major
+    // without swizzle)
+    static constexpr int STAGES = G == 8 && H == 4 ? 2 : 3, PBUF = G == 8 ? 1 : 2;  // as room allows
     static constexpr int Q_BYTES = NS * 128, P_BYTES = NP * DQ_TILE;
-    static constexpr int OFF_Q = STAGES * DQ_TILE_BYTES;
-    static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
-    static constexpr int OFF_CTRL = OFF_P + 2 * DQ_TILES * P_BYTES;
+    static constexpr int OFF_Q = STAGES * DQ_STEP_BYTES;
+    static constexpr int OFF_P = OFF_Q + H * Q_BYTES;
+    static constexpr int OFF_CTRL = OFF_P + PBUF * DQ_TILES * P_BYTES;
 };
 
 struct DqStep {
-    int b, h, split;   // row, KV head, split
+    int b, h, split;   // row, bundle of KV heads, split
     int cnt;           // tokens of the step (0: nothing to compute)
     int first, last;   // of the item
     int item;          // index in the item list; -1: no more
-    int bad;           // RK_STATUS_* bits
+    int bad;           // RK_STATUS_* bits of the row
 };
 
 struct DqCtrl {
-    uint64_t full[12], empty[12];
+    uint64_t full[3], empty[3];      // the ring
     uint64_t id_full[DQ_SLOTS], sc_full[DQ_SLOTS], slot_empty[DQ_SLOTS];
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full, q_empty;
     uint64_t s_full[2], p_ready[2], o_full[2], o_read[2];  // by the parity of the step
     uint64_t never;
     uint32_t tmem_base;
@@ -98,19 +103,20 @@ struct DqCtrl {
     int total;                       // row splits of the batch
     int scan[DQ_THREADS / 32];
     DqStep step[DQ_SLOTS];
-    int ids[DQ_SLOTS][DQ_PAGES];
-    alignas(16) float4 sc[DQ_SLOTS][DQ_PAGES];  // k scale, log2 of v's, 1 / v's
-    float qscale[2][8];              // score factor of each head (log2 domain)
-    int qbad[2];                     // heads whose query is out of range, a bit each
+    int ids[DQ_SLOTS][32];           // page of lane p's block: page p / H, head p % H of the step
+    uint32_t odd[DQ_SLOTS];          // blocks whose scale is not one
+    alignas(16) float4 sc[DQ_SLOTS][32];  // k scale, log2 of v's, 1 / v's of those blocks
+    float qscale[32];                // score factor of each query head (log2 domain)
+    uint32_t qbad;                   // query heads out of range
     float red[2][16][8];             // a step's maximum of each softmax warp, by parity
     float lred[2][16][8];            // an item's sums of each softmax warp, by parity
-    uint32_t fred[2][16];            // heads out of range
+    uint32_t fred[2][16];            // queries out of range; bit 31: a scale
     int pre[DQ_PRE + 1];             // row splits before each group of rows
 };
-template <int G>
+template <int G, int H>
 constexpr int dq_smem_bytes() {
-    static_assert(DqShape<G>::OFF_CTRL + sizeof(DqCtrl) <= 232448, "8-bit decode shared memory above the 227 KiB opt-in limit");
-    return DqShape<G>::OFF_CTRL + (int)sizeof(DqCtrl);
+    static_assert(DqShape<G, H>::OFF_CTRL + sizeof(DqCtrl) <= 232448, "8-bit decode shared memory above the 227 KiB opt-in limit");
+    return DqShape<G, H>::OFF_CTRL + (int)sizeof(DqCtrl);
 }
 
 // Visible keys of a row (0 where its metadata is unsafe) and its status bits.
@@ -142,9 +148,9 @@ __device__ __forceinline__ void find_row(const AttnQ8Args& a, const DqCtrl* c, i
     }
 }
 
-// An item's result: head g of the KV head, dim d (one thread each); o over l.
-__device__ __forceinline__ void write_item(const AttnQ8Args& a, const DqStep& st, int g, int d, float o, float lse2) {
-    const size_t bh = (size_t)st.b * a.Hq + st.h * a.G + g;
+// An item's result: query head hq, dim d (one thread each); o over l.
+__device__ __forceinline__ void write_item(const AttnQ8Args& a, const DqStep& st, int hq, int d, float o, float lse2) {
+    const size_t bh = (size_t)st.b * a.Hq + hq;
     if (a.n_splits > 1) {
         a.o_part[(bh * a.n_splits + st.split) * HEAD_DIM + d] = o;
         if (d == 0) a.lse_part[bh * a.n_splits + st.split] = lse2;
@@ -154,13 +160,13 @@ __device__ __forceinline__ void write_item(const AttnQ8Args& a, const DqStep& st
     }
 }
 
-template <int G>
+template <int G, int H>
 __global__ void __launch_bounds__(DQ_THREADS, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ AttnQ8Args a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw;
-    using Sh = DqShape<G>;
+    using Sh = DqShape<G, H>;
     DqCtrl* c = reinterpret_cast<DqCtrl*>(sm + Sh::OFF_CTRL);
     const uint32_t s_base = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     if (tid == 0) {
         c->pipe.abort = 0;
         c->pipe.limit_ns = wait_limit(a.wait_limit_ns);
-        for (int i = 0; i < STAGES; ++i) {
+        for (int i = 0; i < Sh::STAGES; ++i) {
             mbar_init(smem_u32(&c->full[i]), 1);
             mbar_init(smem_u32(&c->empty[i]), 1);
         }
@@ -181,13 +187,13 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             mbar_init(smem_u32(&c->slot_empty[i]), 19);  // producer, issuer, q, softmax warps
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&c->q_full[i]), 1);
-            mbar_init(smem_u32(&c->q_empty[i]), 17);     // issuer's commit, softmax warps
             mbar_init(smem_u32(&c->s_full[i]), 1);
             mbar_init(smem_u32(&c->p_ready[i]), 16);
             mbar_init(smem_u32(&c->o_full[i]), 1);
             mbar_init(smem_u32(&c->o_read[i]), 16);
         }
+        mbar_init(smem_u32(&c->q_full), 1);
+        mbar_init(smem_u32(&c->q_empty), 17);            // issuer's commit, softmax warps
         mbar_init(smem_u32(&c->never), 1);
         fence_mbar_init();
     }
@@ -234,15 +240,21 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = c->tmem_base;
     PipeCtl* pc = &c->pipe;
-    const long long items = (long long)c->total * a.Hkv;
+    const int bundles = a.Hkv / H;
+    const long long items = (long long)c->total * bundles;
 
     if (warp == 3) {
         // ==================================================== metadata ====
+        // lane p: block p of the step, page p / H and head p % H of the bundle
         int slot = 0, use = 0;  // ring position and how often it went round
         bool ok = true;
         DqStep st{};
         int t = 0, t1 = 0, id = 0;  // the step's first token, the item's end, the lane's page id
         long long it = blockIdx.x;
+        const int my_page = lane / H;
+        auto page_id = [&]() {
+            return my_page * PAGE < t1 - t ? __ldg(a.block_table + (size_t)st.b * a.W + t / PAGE + my_page) : 0;
+        };
         auto item = [&]() {  // the item `it` and its first page ids
             st = DqStep{};
             st.item = -1;
@@ -251,19 +263,19 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             if (it < items) {
                 int n;
                 st.item = (int)it;
-                st.h = (int)(it % a.Hkv);
-                find_row(a, c, (int)(it / a.Hkv), st.b, st.split, n, st.bad);
+                st.h = (int)(it % bundles);
+                find_row(a, c, (int)(it / bundles), st.b, st.split, n, st.bad);
                 t = st.split * a.split_tokens;
                 t1 = min(n, t + a.split_tokens);
             }
-            id = lane * PAGE < t1 - t ? __ldg(a.block_table + (size_t)st.b * a.W + t / PAGE + lane) : 0;
+            id = page_id();
         };
         item();
         while (ok) {
-            const int cnt = max(0, min(DQ_STEP, t1 - t));
-            const bool mine = lane * PAGE < cnt;
+            const int cnt = max(0, min(Sh::TOKENS, t1 - t));
+            const bool mine = my_page * PAGE < cnt;
             const bool oob = mine && (id < 0 || id >= a.num_pages);
-            st.last = t + DQ_STEP >= t1;
+            st.last = t + Sh::TOKENS >= t1;
             st.cnt = cnt;
             if (__any_sync(0xffffffffu, oob)) {
                 st.bad |= RK_STATUS_PAGE_OOB;
@@ -273,30 +285,30 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             if (lane == 0) good = mbar_wait(smem_u32(&c->slot_empty[slot]), (uint32_t)((use & 1) ^ 1), pc);
             if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
             c->ids[slot][lane] = id;
-            if (lane == 0) c->step[slot] = st;  // bad scales are added below, before sc_full
+            if (lane == 0) c->step[slot] = st;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&c->id_full[slot]));
             float ks = 1.0f, vs = 1.0f;
             if (mine && st.cnt > 0) {
-                const size_t block = (size_t)id * a.Hkv + st.h;
+                const size_t block = (size_t)id * a.Hkv + st.h * H + lane % H;
                 ks = __ldg(a.k_scale + block);
                 vs = __ldg(a.v_scale + block);
             }
             // the next step's page ids travel while this step's scales do
             const bool end = st.item < 0;
-            const int bad = st.bad;
             st.bad = st.first = 0;  // reported once
             if (st.last) {
                 it += gridDim.x;
                 if (!end) item();
             } else {
-                t += DQ_STEP;
-                id = lane * PAGE < t1 - t ? __ldg(a.block_table + (size_t)st.b * a.W + t / PAGE + lane) : 0;
+                t += Sh::TOKENS;
+                id = page_id();
             }
             const bool odd = !scale_ok(ks) || !scale_ok(vs);
             if (odd) ks = vs = 1.0f;
             c->sc[slot][lane] = make_float4(ks, __log2f(vs), 1.0f / vs, 0.0f);
-            if (__any_sync(0xffffffffu, odd) && lane == 0) c->step[slot].bad = bad | RK_STATUS_SCALE;
+            const uint32_t odds = __ballot_sync(0xffffffffu, odd);
+            if (lane == 0) c->odd[slot] = odds;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&c->sc_full[slot]));
             if (++slot == DQ_SLOTS) {
@@ -311,34 +323,38 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             prefetch_tmap(&kmap);
             prefetch_tmap(&vmap);
         }
-        int slot = 0, use = 0, n = 0;  // n: tiles issued
+        // The whole warp, converged: the copies' operands stay in uniform registers and one
+        // elected lane issues.  Loops stay rolled: a step's worth of straight code is
+        // fetched anew each time, and that, not the copies, set the pace (450 ns for 16 KiB).
+        int slot = 0, use = 0, n = 0;  // n: stages filled
+        uint32_t stg = 0, phase = 1;
         bool ok = true;
+#pragma unroll 1
         while (ok) {
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->id_full[slot]), (uint32_t)(use & 1), pc)))) break;
-            const volatile DqStep* st = &c->step[slot];
-            const int cnt = st->cnt, h = st->h;
-            if (st->item < 0) break;
+            const int cnt = __shfl_sync(0xffffffffu, c->step[slot].cnt, 0), head = __shfl_sync(0xffffffffu, c->step[slot].h, 0) * H;
             const int id = c->ids[slot][lane];
-            __syncwarp();
+            if (__any_sync(0xffffffffu, c->step[slot].item < 0)) break;
             if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
             if (++slot == DQ_SLOTS) {
                 slot = 0;
                 ++use;
             }
-            const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE, pages = (cnt + PAGE - 1) / PAGE;
-            for (int kv = 0; kv < 2 && ok; ++kv) {
-                for (int j = 0; j < tiles; ++j, ++n) {
-                    const int stg = n % STAGES;
-                    int good = 1;
-                    if (lane == 0) {
-                        good = mbar_wait(smem_u32(&c->empty[stg]), (uint32_t)(((n / STAGES) & 1) ^ 1), pc);
-                        if (good)
-                            mbar_arrive_expect_tx(smem_u32(&c->full[stg]), (uint32_t)min(8, pages - 8 * j) * Q8_BLOCK_BYTES);
-                    }
-                    if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
-                    if ((lane >> 3) == j && lane < pages)
-                        tma_load_3d(s_base + stg * DQ_TILE_BYTES + (lane & 7) * Q8_BLOCK_BYTES, kv ? &vmap : &kmap,
-                                    smem_u32(&c->full[stg]), 0, 0, id * a.Hkv + h);
+            if (cnt == 0) continue;
+            const int pages = (cnt + PAGE - 1) / PAGE;
+#pragma unroll 1
+            for (int kv = 0; kv < 2; ++kv, ++n) {
+                const uint32_t fb = smem_u32(&c->full[stg]);
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->empty[stg]), phase, pc)))) break;
+                arrive_expect_tx_elect(fb, (uint32_t)pages * H * Q8_BLOCK_BYTES);
+                uint32_t dst = s_base + stg * DQ_STEP_BYTES;
+                const CUtensorMap* map = kv ? &vmap : &kmap;
+#pragma unroll 1
+                for (int p = 0; p < pages; ++p, dst += H * Q8_BLOCK_BYTES)
+                    tma_load_5d_elect(dst, map, fb, 0, 0, head, 0, __shfl_sync(0xffffffffu, id, p * H));
+                if (++stg == STAGES) {
+                    stg = 0;
+                    phase ^= 1;
                 }
             }
         }
@@ -362,49 +378,64 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 ++use;
             }
             if (!first) continue;
-            const int buf = nq & 1;
-            uint32_t lo[G], hi[G];
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + ((size_t)b * a.Hq + h * G) * (HEAD_DIM / 2);
-#pragma unroll
-            for (int g = 0; g < G; ++g) {  // dims 2 lane, 2 lane + 1 and the 64 above
-                lo[g] = __ldg(q + g * 64 + lane);
-                hi[g] = __ldg(q + g * 64 + 32 + lane);
-            }
             const uint32_t pos = (uint32_t)max(0, a.position_ids[b]);
+            // dims 2 lane, 2 lane + 1 and the 64 above of G queries at a time, the next head's on the way
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + ((size_t)b * a.Hq + h * H * G) * (HEAD_DIM / 2) + lane;
+            uint32_t lo[G], hi[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                lo[g] = __ldg(q + g * 64);
+                hi[g] = __ldg(q + g * 64 + 32);
+            }
             float c0, s0, c1, s1;
             rope_cos_sin(pos, turn0, c0, s0);
             rope_cos_sin(pos, turn1, c1, s1);
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->q_empty[buf]), (uint32_t)(((nq >> 1) & 1) ^ 1), pc)))) break;
-            uint8_t* qt = sm + Sh::OFF_Q + buf * Sh::Q_BYTES;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->q_empty), (uint32_t)((nq & 1) ^ 1), pc)))) break;
             uint32_t badq = 0;
+#pragma unroll 1
+            for (int hj = 0; hj < H; ++hj) {
+                uint8_t* qt = sm + Sh::OFF_Q + hj * Sh::Q_BYTES;
+                uint32_t nlo[G], nhi[G];
+                const uint32_t* qn = q + (hj + 1 < H ? hj + 1 : hj) * G * 64;
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                uint32_t m = __vmaxu2(lo[g] & 0x7fff7fffu, hi[g] & 0x7fff7fffu);
-                m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-                const bool bad = m >= Q8_LIMIT_BF16;
-                if (bad) badq |= 1u << g;
-                const int e = bad ? 0 : q8_exponent(m);
-                const float inv = bad ? 0.0f : pow2(-e);
-                const float2 l = make_float2(bf16lo(lo[g]), bf16hi(lo[g])), u = make_float2(bf16lo(hi[g]), bf16hi(hi[g]));
-                float2 x = make_float2((l.x * c0 - u.x * s0) * inv, (l.y * c1 - u.y * s1) * inv);
-                float2 y = make_float2((u.x * c0 + l.x * s0) * inv, (u.y * c1 + l.y * s1) * inv);
-                if (bad) x = y = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    if (p == 2) {
-                        x = make_float2(x.x * 256.0f, x.y * 256.0f);
-                        y = make_float2(y.x * 256.0f, y.y * 256.0f);
-                    }
-                    const int row = p * G + g;
-                    *reinterpret_cast<uint16_t*>(qt + sw128_off(row, lane >> 3) + (2 * lane & 15)) = (uint16_t)take_part(x);
-                    *reinterpret_cast<uint16_t*>(qt + sw128_off(row, 4 + (lane >> 3)) + (2 * lane & 15)) = (uint16_t)take_part(y);
+                for (int g = 0; g < G; ++g) {
+                    nlo[g] = __ldg(qn + g * 64);
+                    nhi[g] = __ldg(qn + g * 64 + 32);
                 }
-                if (lane == 0) c->qscale[buf][g] = a.qk_scale_log2 * pow2(e);
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    uint32_t m = __vmaxu2(lo[g] & 0x7fff7fffu, hi[g] & 0x7fff7fffu);
+                    m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+                    const bool bad = m >= Q8_LIMIT_BF16;
+                    if (bad) badq |= 1u << (hj * G + g);
+                    const int e = bad ? 0 : q8_exponent(m);
+                    const float inv = pow2(-e);
+                    const float2 l = make_float2(bf16lo(lo[g]), bf16hi(lo[g])), u = make_float2(bf16lo(hi[g]), bf16hi(hi[g]));
+                    float2 x = make_float2((l.x * c0 - u.x * s0) * inv, (l.y * c1 - u.y * s1) * inv);
+                    float2 y = make_float2((u.x * c0 + l.x * s0) * inv, (u.y * c1 + l.y * s1) * inv);
+                    if (bad) x = y = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        if (p == 2) {
+                            x = make_float2(x.x * 256.0f, x.y * 256.0f);
+                            y = make_float2(y.x * 256.0f, y.y * 256.0f);
+                        }
+                        const int row = p * G + g;
+                        *reinterpret_cast<uint16_t*>(qt + sw128_off(row, lane >> 3) + (2 * lane & 15)) = (uint16_t)take_part(x);
+                        *reinterpret_cast<uint16_t*>(qt + sw128_off(row, 4 + (lane >> 3)) + (2 * lane & 15)) = (uint16_t)take_part(y);
+                    }
+                    if (lane == 0) c->qscale[hj * G + g] = a.qk_scale_log2 * pow2(e);
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    lo[g] = nlo[g];
+                    hi[g] = nhi[g];
+                }
             }
-            if (lane == 0) c->qbad[buf] = (int)badq;
+            if (lane == 0) c->qbad = badq;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c->q_full[buf]));
+            if (lane == 0) mbar_arrive(smem_u32(&c->q_full));
             ++nq;
         }
     } else if (warp == 1) {
@@ -413,84 +444,73 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         // (one lane alone took 130 cycles an MMA, most of it moving descriptors).
         constexpr uint32_t idS = idesc_e4m3_f32(DQ_TILE, NS, 0, 0);
         constexpr uint32_t idO = idesc_e4m3_f32(HEAD_DIM, NP, 1, 1);
-        const uint32_t dT = desc_lo(s_base, 16), dQ = desc_lo(s_base + Sh::OFF_Q, 16), dP = desc_lo(s_base + Sh::OFF_P, 128);
-        constexpr uint32_t TILE = DQ_TILE_BYTES >> 4;
-        int slot = 0, use = 0, nk = 0, nq = 0, ks = 0;  // next tile, items, steps (S)
-        int pv_cnt = 0, nv = 0;                         // the step whose PV is due: tokens, first V tile
+        // operands from the cache: a head's groups of 8 tokens are H KiB apart
+        constexpr uint32_t HI_KV = ((H * 1024u) >> 4) | (1u << 14) | (2u << 29);
+        const uint32_t dT = desc_lo(s_base, 16);
+        const uint32_t dQ = desc_lo(s_base + Sh::OFF_Q, 16), dP = desc_lo(s_base + Sh::OFF_P, 128);
+        int slot = 0, use = 0, nq = 0, ks = 0;  // items, steps (S; a step fills two stages)
+        int pv_cnt = 0;                         // tokens of the step whose PV is due
         auto wait = [&](uint64_t& bar, int parity) {
             return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), (uint32_t)(parity & 1), pc)) != 0;
         };
         bool ok = !a.timeout_drill || __all_sync(0xffffffffu, drill_wait(smem_u32(&c->never), pc));
         // PV of step k
         auto issue_pv = [&](int k) -> bool {
-            const int buf = k & 1;
+            const int buf = k & 1, n = 2 * k + 1, stg = n % STAGES;
             if (!wait(c->o_read[buf], (k >> 1) + 1)) return false;  // step k - 2's result is read
             if (!wait(c->p_ready[buf], k >> 1)) return false;
-            const uint32_t d = tmem + Sh::TMEM_O + buf * NP;
+            if (!wait(c->full[stg], n / STAGES)) return false;
+            tc_fence_after();
 #pragma unroll 1
-            for (int j = 0; j * DQ_TILE < pv_cnt; ++j) {
-                const int n = nv + j, stg = n % STAGES;
-                if (!wait(c->full[stg], n / STAGES)) return false;
-                tc_fence_after();
-                const uint32_t dv = dT + stg * TILE, dp = dP + (buf * DQ_TILES + j) * (Sh::P_BYTES >> 4);
-                const uint32_t acc = j > 0;
-                const int kn = (pv_cnt - j * DQ_TILE + 31) / 32;  // k-steps that hold tokens
-                if (kn >= 4) mma_f8_steps<0, 4, 256, 32, DESC_HI_ROWS16>(d, dv, dp, idO, acc);
-                else if (kn == 3) mma_f8_steps<0, 3, 256, 32, DESC_HI_ROWS16>(d, dv, dp, idO, acc);
-                else if (kn == 2) mma_f8_steps<0, 2, 256, 32, DESC_HI_ROWS16>(d, dv, dp, idO, acc);
-                else mma_f8_steps<0, 1, 256, 32, DESC_HI_ROWS16>(d, dv, dp, idO, acc);
-                umma_commit_elect(smem_u32(&c->empty[stg]));
+            for (int j = 0; j < DQ_TILES; ++j) {
+                const int left = pv_cnt - (j / H) * DQ_TILE, kn = (left + 31) / 32;  // k-steps that hold tokens
+                if (left <= 0) break;
+                const uint32_t d = tmem + Sh::TMEM_O + buf * Sh::TMEM_OBUF + (j % H) * NP;
+                const uint32_t dv = dT + stg * (DQ_STEP_BYTES >> 4) + (j / H) * H * 1024 + (j % H) * 64;
+                const uint32_t dp = dP + ((k % Sh::PBUF) * DQ_TILES + j) * (Sh::P_BYTES >> 4);
+                // a k-step is 4 groups of 8 tokens
+                mma_f8_x4<256 * H, 32>(d, dv, dp, HI_KV, DESC_HI_ROWS16, idO, j >= H, kn);
             }
+            umma_commit_elect(smem_u32(&c->empty[stg]));
             umma_commit_elect(smem_u32(&c->o_full[buf]));
             pv_cnt = 0;
             return true;
         };
+#pragma unroll 1
         while (ok) {
             if (!(ok = wait(c->id_full[slot], use))) break;
             const int cnt = __shfl_sync(0xffffffffu, c->step[slot].cnt, 0);
             const int flags = __shfl_sync(0xffffffffu, c->step[slot].first | (c->step[slot].last << 1) | (c->step[slot].item < 0 ? 4 : 0), 0);
-            const int tiles = (cnt + DQ_TILE - 1) / DQ_TILE;
-            if (flags & 4) {
-                if (pv_cnt > 0) ok = issue_pv(ks - 1);
-                break;
+            if (!(flags & 4)) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
+                if (++slot == DQ_SLOTS) {
+                    slot = 0;
+                    ++use;
+                }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
-            if (++slot == DQ_SLOTS) {
-                slot = 0;
-                ++use;
-            }
-            // The PV that is due goes before this step's S, unless all of this step's K is
-            // here already: then the loads are ahead of the softmax, and S need not wait for
-            // it.  (Where the loads are behind, the V tiles' room is what they wait for.)
-            if (pv_cnt > 0) {
-                const int n = nk + tiles - 1;
-                const bool ahead = tiles > 0 && __all_sync(0xffffffffu, mbar_test(smem_u32(&c->full[n % STAGES]), (uint32_t)((n / STAGES) & 1)));
-                if (!ahead && !(ok = issue_pv(ks - 1))) break;
-            }
-            const int qb = nq & 1;
-            if ((flags & 1) && !(ok = wait(c->q_full[qb], nq >> 1))) break;
-            const uint32_t dq = dQ + qb * (Sh::Q_BYTES >> 4), ds = tmem + (ks & 1) * Sh::TMEM_S;
-#pragma unroll 1
-            for (int j = 0; j < tiles; ++j) {
-                const int n = nk + j, stg = n % STAGES;
+            // The PV that is due goes before this step's S.  (S first, where this step's K is
+            // here before the weights are, gained nothing.)
+            if (pv_cnt > 0 && !(ok = issue_pv(ks - 1))) break;
+            if (flags & 4) break;
+            if ((flags & 1) && !(ok = wait(c->q_full, nq))) break;
+            if (cnt > 0) {
+                const int n = 2 * ks, stg = n % STAGES, kb = ks & 1;
                 if (!(ok = wait(c->full[stg], n / STAGES))) break;
                 tc_fence_after();
-                mma_f8_steps<0, 4, 2, 2, DESC_HI>(ds + j * NS, dT + stg * TILE, dq, idS, 0u);
+#pragma unroll 1
+                for (int j = 0; j < DQ_TILES && (j / H) * DQ_TILE < cnt; ++j)
+                    mma_f8_x4<2, 2>(tmem + kb * Sh::TMEM_S + j * NS, dT + stg * (DQ_STEP_BYTES >> 4) + (j / H) * H * 1024 + (j % H) * 64,
+                                    dQ + (j % H) * (Sh::Q_BYTES >> 4), HI_KV, DESC_HI, idS, 0u, 4);
+                umma_commit_elect(smem_u32(&c->s_full[kb]));
                 umma_commit_elect(smem_u32(&c->empty[stg]));
+                pv_cnt = cnt;
+                ++ks;
             }
-            if (!ok) break;
-            if (tiles > 0) umma_commit_elect(smem_u32(&c->s_full[ks & 1]));
             if (flags & 2) {
-                umma_commit_elect(smem_u32(&c->q_empty[qb]));
+                umma_commit_elect(smem_u32(&c->q_empty));
                 ++nq;
             }
-            if (tiles == 0) continue;
-            if (pv_cnt > 0 && !(ok = issue_pv(ks - 1))) break;
-            pv_cnt = cnt;
-            nv = nk + tiles;
-            nk += 2 * tiles;
-            ++ks;
         }
         if (!ok) {  // issued MMAs drain before tensor memory is released
             const uint64_t t0 = global_timer_ns();
@@ -500,13 +520,14 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     } else {
         // ===================================================== softmax ====
         const int sw = warp - 4, wg = sw >> 2;         // softmax warp, warpgroup (tile)
+        const int hj = wg % H, blk = wg / H;           // KV head of the bundle, token block of the step
         const int t = tid & 127;                       // token of the tile, output dim
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-        constexpr int OWN = Sh::OWN;                   // heads wg, wg + 4 are this warpgroup's
-        int slot = 0, use = 0, n = 0, nq = 0, ks = 0;  // tiles, items, steps so far
-        float M[G], l[G], sc[G];
+        constexpr int OWN = Sh::OWN, SHARE = Sh::SHARE;  // queries blk, blk + SHARE, ... are this warpgroup's
+        int slot = 0, use = 0, nq = 0, ks = 0;         // items, steps so far
+        float M[G], l[G];
         int bad = 0;         // the item's status bits
-        uint32_t range = 0;  // heads that met a value FP32 cannot hold
+        uint32_t range = 0;  // queries that met a value FP32 cannot hold; bit 31: a scale that is none
         float o[OWN];
         // the step whose O is due: scales of what is summed so far and of O, the item's end
         int due = 0;
@@ -524,21 +545,23 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         auto finish = [&](const DqStep& st, int par, int status, bool none) {
             uint32_t any = 0;
 #pragma unroll
-            for (int w = 0; w < 16; ++w) any |= c->fred[par][w];
+            for (int w = 0; w < 16; ++w)
+                if ((w >> 2) % H == hj) any |= c->fred[par][w];
+            if (any >> 31) status |= RK_STATUS_SCALE;
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
-                const int g = wg + 4 * i;
+                const int g = blk + SHARE * i;
                 if (g < G) {
                     float sum = 0.0f;
 #pragma unroll
-                    for (int w = 0; w < 16; ++w) sum += c->lred[par][w][g];
+                    for (int w = 0; w < 16; ++w)
+                        if ((w >> 2) % H == hj) sum += c->lred[par][w][g];
                     const bool over = !none && (((any >> g) & 1u) || !(sum > 0.0f && sum < INFINITY));
                     const bool fail = status || over;
-                    // dims that come out beyond FP32 fail the head too, all 128 of them
                     const float x = o[i] * (1.0f / sum);
                     const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : Mo[i] - 8.0f + log2f(sum);
-                    write_item(a, st, g, t, fail || none ? 0.0f : x, lse2);
-                    if (t == 0 && a.status && (over || status)) atomicOr(a.status, status ? status : RK_STATUS_RANGE);
+                    write_item(a, st, (st.h * H + hj) * G + g, t, fail || none ? 0.0f : x, lse2);
+                    if (t == 0 && fail && a.status) atomicOr(a.status, status ? status : RK_STATUS_RANGE);
                 }
             }
             resume = (long long)st.item + gridDim.x;
@@ -548,6 +571,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             wait(c->sc_full[slot], use);
             DqStep st{};
             float4 ps = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+            float sc[G];
             if (ok) {
                 const volatile DqStep* s = &c->step[slot];
                 st.b = s->b;
@@ -558,7 +582,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 st.last = s->last;
                 st.item = s->item;
                 st.bad = s->bad;
-                ps = c->sc[slot][8 * wg + (t >> 4)];
+                ps = c->sc[slot][(8 * blk + (t >> 4)) * H + hj];
+                const uint32_t odd = c->odd[slot];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
                 if (++slot == DQ_SLOTS) {
@@ -566,22 +591,27 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     ++use;
                 }
                 if (st.first && st.item >= 0) {
-                    const int buf = nq & 1;
-                    wait(c->q_full[buf], nq >> 1);
+                    wait(c->q_full, nq);
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
                         M[g] = -INFINITY;
                         l[g] = 0.0f;
-                        sc[g] = c->qscale[buf][g];
                     }
                     bad = 0;
-                    range = (uint32_t)c->qbad[buf];
+                    range = (c->qbad >> (hj * G)) & ((1u << G) - 1u);
+                }
+#pragma unroll
+                for (int g = 0; g < G; ++g) sc[g] = c->qscale[hj * G + g];
+                constexpr uint32_t EACH = H == 1 ? 0xffffffffu : H == 2 ? 0x55555555u : 0x11111111u;
+                if (odd & (EACH << hj)) range |= 0x80000000u;
+                if (st.last && st.item >= 0) {
                     __syncwarp();
-                    if (ok && lane == 0) mbar_arrive(smem_u32(&c->q_empty[buf]));
+                    if (ok && lane == 0) mbar_arrive(smem_u32(&c->q_empty));
                     ++nq;
                 }
             }
-            const int tiles = (st.cnt + DQ_TILE - 1) / DQ_TILE, par = ks & 1;
+            const int par = ks & 1;
+            const bool have = blk * DQ_TILE < st.cnt;  // the tile holds tokens
             // scores of the thread's token: w = z + log2 vs (-inf past the last one)
             float w[G];
             if (st.cnt > 0) {
@@ -589,13 +619,13 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 for (int g = 0; g < G; ++g) w[g] = -INFINITY;
                 wait(c->s_full[par], ks >> 1);
                 tc_fence_after();
-                if (wg < tiles) {
+                if (have) {
                     uint32_t r[NS];
                     const uint32_t ts = tmem + lane_addr + par * Sh::TMEM_S + wg * NS;
                     if constexpr (NS == 16) tmem_ld16(ts, r);
                     else tmem_ld32(ts, r);
                     tmem_ld_wait();
-                    if (wg * DQ_TILE + t < st.cnt) {
+                    if (blk * DQ_TILE + t < st.cnt) {
 #pragma unroll
                         for (int g = 0; g < G; ++g) {
                             const float hi = __uint_as_float(r[g]) + __uint_as_float(r[G + g]);
@@ -618,26 +648,27 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             }
             float aln[OWN], ben[OWN];  // this step's scales of o and O
             if (st.cnt > 0) {
-                float p[G], beta[G];
+                float p[G];
+                const int rw = ((lane & 15) >> 2) % H == hj ? lane & 15 : 4 * hj;  // a warp of this head
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    float m = warp_max(c->red[par][lane & 15][g]);
-                    m = fabsf(m) < INFINITY ? m : 0.0f;  // otherwise the head fails (range)
+                    float m = warp_max(c->red[par][rw][g]);
+                    m = fabsf(m) < INFINITY ? m : 0.0f;  // otherwise the query fails (range)
                     const float top = fmaxf(M[g], m);
-                    const float alpha = ex2(M[g] - top);
-                    beta[g] = ex2(m - top);
+                    const float alpha = ex2(M[g] - top), beta = ex2(m - top);
                     M[g] = top;
                     p[g] = ex2(w[g] - m + 8.0f);
-                    l[g] = fmaf(l[g], alpha, p[g] * ps.z * beta[g]);
-                    if ((g & 3) == wg) {
-                        aln[g >> 2] = alpha;
-                        ben[g >> 2] = beta[g];
+                    l[g] = fmaf(l[g], alpha, p[g] * ps.z * beta);
+                    if (g % SHARE == blk) {
+                        aln[g / SHARE] = alpha;
+                        ben[g / SHARE] = beta;
                     }
                 }
-                // the weights' buffer is free once the PV of step k - 2 is done
-                wait(c->o_full[par], (ks >> 1) + 1);
-                if (wg < tiles) {
-                    // p' = 2^(w - m + 8) as three e4m3 parts, part * G + head of the token's row
+                // the weights' buffer is free once the PV that read it last is done
+                if (Sh::PBUF == 2) wait(c->o_full[par], (ks >> 1) + 1);
+                else if (ks > 0) wait(c->o_full[par ^ 1], (ks - 1) >> 1);
+                if (have) {
+                    // p' = 2^(w - m + 8) as three e4m3 parts, part * G + query of the token's row
                     uint32_t wd[NP / 4];
 #pragma unroll
                     for (int i = 0; i < NP / 4; ++i) wd[i] = 0;
@@ -650,21 +681,24 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                             wd[col >> 2] |= take_part(x) << (8 * (col & 3));
                         }
                     }
-                    uint8_t* pt = sm + Sh::OFF_P + (par * DQ_TILES + wg) * Sh::P_BYTES + t * 16;
+                    uint8_t* pt = sm + Sh::OFF_P + ((ks % Sh::PBUF) * DQ_TILES + wg) * Sh::P_BYTES + t * 16;
 #pragma unroll
                     for (int i = 0; i < NP / 16; ++i)
                         *reinterpret_cast<uint4*>(pt + i * DQ_TILE * 16) = make_uint4(wd[4 * i], wd[4 * i + 1], wd[4 * i + 2], wd[4 * i + 3]);
                 }
                 if (st.cnt & 31) {
                     // the k-step that the last token is in: V rows behind it hold anything, and 0 times a NaN
-                    // is not 0
-                    const int j = tiles - 1, last = n + 2 * tiles - 1, stg = last % STAGES;
-                    wait(c->full[stg], last / STAGES);
-                    const int r0 = st.cnt - j * DQ_TILE, r1 = (r0 + 31) & ~31, i = tid - 128;
-                    if (ok && i < (r1 - r0) * 8)
-                        reinterpret_cast<uint4*>(sm + stg * DQ_TILE_BYTES + r0 * 128)[i] = make_uint4(0, 0, 0, 0);
+                    // is not 0.  (The stage's use before this one is known to be over.)
+                    const int nv = 2 * ks + 1, stg = nv % STAGES;
+                    wait(c->full[stg], nv / STAGES);
+                    const int r1 = (st.cnt + 31) & ~31;
+                    uint8_t* vt = sm + stg * DQ_STEP_BYTES;
+                    for (int i = tid - 128; ok && i < (r1 - st.cnt) * H * 8; i += DQ_SOFTMAX) {
+                        const int tok = st.cnt + i / (8 * H), rest = i % (8 * H);
+                        *reinterpret_cast<uint4*>(vt + (tok >> 3) * H * 1024 + (rest >> 3) * 1024 + (tok & 7) * 128 + (rest & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
                 }
-                n += 2 * tiles;
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
@@ -690,11 +724,11 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 wait(c->o_full[db], k >> 1);
                 tc_fence_after();
                 uint32_t r[OWN][3];
-                const uint32_t to = tmem + lane_addr + Sh::TMEM_O + db * NP;
+                const uint32_t to = tmem + lane_addr + Sh::TMEM_O + db * Sh::TMEM_OBUF + hj * NP;
 #pragma unroll
                 for (int i = 0; i < OWN; ++i)
 #pragma unroll
-                    for (int e = 0; e < 3; ++e) tmem_ld1(to + e * G + (G > wg + 4 * i ? wg + 4 * i : 0), r[i][e]);
+                    for (int e = 0; e < 3; ++e) tmem_ld1(to + e * G + min(blk + SHARE * i, G - 1), r[i][e]);
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -704,7 +738,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 for (int i = 0; i < OWN; ++i) {
                     const float x = (__uint_as_float(r[i][2]) + __uint_as_float(r[i][1])) + __uint_as_float(r[i][0]);
                     o[i] = fmaf(x, be[i], o[i] * al[i]);
-                    if (!(fabsf(o[i]) < INFINITY)) over |= 1u << (wg + 4 * i);
+                    if (!(fabsf(o[i]) < INFINITY) && blk + SHARE * i < G) over |= 1u << (blk + SHARE * i);
                 }
                 if (dst.last) {
                     // o may be beyond FP32 (a NaN code in V) in a dim only; the head's 128 threads agree on it
@@ -730,8 +764,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     be[i] = ben[i];
                     if (st.first) o[i] = 0.0f;
 #pragma unroll
-                    for (int g = i * 4; g < G && g < i * 4 + 4; ++g)
-                        if ((g & 3) == wg) Mo[i] = M[g];
+                    for (int g = i * SHARE; g < G && g < (i + 1) * SHARE; ++g)
+                        if (g % SHARE == blk) Mo[i] = M[g];
                 }
                 ++ks;
             } else if (st.last) {
@@ -747,9 +781,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             for (long long it = resume; it < items; it += gridDim.x) {
                 DqStep st{};
                 int nk, bd;
-                st.h = (int)(it % a.Hkv);
-                find_row(a, c, (int)(it / a.Hkv), st.b, st.split, nk, bd);
-                for (int g = wg; g < G; g += 4) write_item(a, st, g, t, 0.0f, __int_as_float(0x7fc00000));
+                st.h = (int)(it % bundles);
+                find_row(a, c, (int)(it / bundles), st.b, st.split, nk, bd);
+                for (int g = blk; g < G; g += SHARE) write_item(a, st, (st.h * H + hj) * G + g, t, 0.0f, __int_as_float(0x7fc00000));
             }
             if (tid == 128 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
         }
@@ -837,37 +871,55 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) merge_q8_kernel(const __grid
 std::atomic<uint64_t> g_configured{0};
 std::atomic<int> g_sms[64];
 
+template <int G, int H>
+cudaError_t launch_one(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, unsigned grid, cudaStream_t stream,
+                       bool configure) {
+    if (configure)
+        return cudaFuncSetAttribute(decode_q8_kernel<G, H>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem_bytes<G, H>());
+    decode_q8_kernel<G, H><<<grid, DQ_THREADS, dq_smem_bytes<G, H>(), stream>>>(km, vm, a);
+    return cudaGetLastError();
+}
 template <int G>
-cudaError_t configure_one() {
-    return cudaFuncSetAttribute(decode_q8_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, dq_smem_bytes<G>());
+cudaError_t launch_bundle(int bundle, const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, unsigned grid,
+                          cudaStream_t stream, bool configure) {
+    return bundle == 4   ? launch_one<G, 4>(km, vm, a, grid, stream, configure)
+           : bundle == 2 ? launch_one<G, 2>(km, vm, a, grid, stream, configure)
+                         : launch_one<G, 1>(km, vm, a, grid, stream, configure);
+}
+cudaError_t launch_any(int group, int bundle, const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, unsigned grid,
+                       cudaStream_t stream, bool configure) {
+    switch (group) {
+        case 1: return launch_bundle<1>(bundle, km, vm, a, grid, stream, configure);
+        case 2: return launch_bundle<2>(bundle, km, vm, a, grid, stream, configure);
+        case 4: return launch_bundle<4>(bundle, km, vm, a, grid, stream, configure);
+        default: return launch_bundle<8>(bundle, km, vm, a, grid, stream, configure);
+    }
 }
 
 }  // namespace
+
+// KV heads to an item (and to a TMA box): the most of 4, 2, 1 that divide Hkv.
+int decode_q8_bundle(int Hkv) { return Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1; }
 
 cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const int bundle = decode_q8_bundle(a.Hkv);
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(g_configured.load() & bit)) {
-        if ((e = configure_one<1>()) != cudaSuccess || (e = configure_one<2>()) != cudaSuccess ||
-            (e = configure_one<4>()) != cudaSuccess || (e = configure_one<8>()) != cudaSuccess)
-            return e;
+        for (int g = 1; g <= 8; g *= 2)
+            for (int h = 1; h <= 4; h *= 2)
+                if ((e = launch_any(g, h, km, vm, a, 0, stream, true)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if (bit) g_sms[dev].store(sms);
         g_configured.fetch_or(bit);
     } else {
         sms = g_sms[dev].load();
     }
-    const long long most = (long long)a.B * a.Hkv * a.n_splits;
+    const long long most = (long long)a.B * (a.Hkv / bundle) * a.n_splits;
     const unsigned grid = (unsigned)(most < sms ? most : sms);
-    switch (a.G) {
-        case 1: decode_q8_kernel<1><<<grid, DQ_THREADS, dq_smem_bytes<1>(), stream>>>(km, vm, a); break;
-        case 2: decode_q8_kernel<2><<<grid, DQ_THREADS, dq_smem_bytes<2>(), stream>>>(km, vm, a); break;
-        case 4: decode_q8_kernel<4><<<grid, DQ_THREADS, dq_smem_bytes<4>(), stream>>>(km, vm, a); break;
-        default: decode_q8_kernel<8><<<grid, DQ_THREADS, dq_smem_bytes<8>(), stream>>>(km, vm, a); break;
-    }
-    e = cudaGetLastError();
+    e = launch_any(a.G, bundle, km, vm, a, grid, stream, false);
     if (e != cudaSuccess || a.n_splits <= 1) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hq));

@@ -54,28 +54,55 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, int a_mn_maj
     return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }
-// D[tmem] (+)= A[smem] * B[smem], k-steps KS .. END - 1 of 32 e4m3 values,
-// accumulating from k-step 1 on, and at k-step 0 iff acc0.  Called by a whole
-// converged warp with uniform operands; one elected lane issues.  a_lo, b_lo:
-// descriptor low words of k-step 0, A_STEP / B_STEP added for each (16-byte units,
-// immediates, so that a step costs the issuing warp no arithmetic).  A lies in a
-// 128-byte-swizzled tile (high word DESC_HI), B in one with high word B_HI.
-template <int KS, int END, uint32_t A_STEP, uint32_t B_STEP, uint32_t B_HI>
-__device__ __forceinline__ void mma_f8_steps(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc0) {
+// D[tmem] (+)= A[smem] * B[smem], the first kn of 4 k-steps of 32 e4m3 values,
+// accumulating from the second on, and at the first iff acc0.  Called by a whole
+// converged warp with uniform operands; one elected lane issues.  a_lo, b_lo and
+// A_HI, B_HI: descriptor words of the first k-step; A_STEP, B_STEP (16-byte units)
+// lead to the next.
+template <uint32_t A_STEP, uint32_t B_STEP>
+__device__ __forceinline__ void mma_f8_x4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi, uint32_t b_hi, uint32_t idesc,
+                                          uint32_t acc0, int kn) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b32 al, bl;\n\t.reg .b64 da, db;\n\t"
-        "add.u32 al, %1, %5;\n\tadd.u32 bl, %2, %6;\n\t"
-        "mov.b64 da, {al, %4};\n\tmov.b64 db, {bl, %8};\n\t"
-        "setp.ne.b32 p, %7, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(DESC_HI), "n"(KS * A_STEP), "n"(KS * B_STEP), "r"(KS > 0 ? 1u : acc0), "r"(B_HI)
+        "{\n\t.reg .pred p, e, t, k;\n\t.reg .b32 al, bl;\n\t.reg .b64 da, db;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %6, %6;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t"
+        "add.u32 al, %1, %8;\n\tadd.u32 bl, %2, %9;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"
+        "setp.gt.and.s32 k, %7, 1, e;\n\t"
+        "@k tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, t;\n\t"
+        "add.u32 al, al, %8;\n\tadd.u32 bl, bl, %9;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"
+        "setp.gt.and.s32 k, %7, 2, e;\n\t"
+        "@k tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, t;\n\t"
+        "add.u32 al, al, %8;\n\tadd.u32 bl, bl, %9;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %4};\n\t"
+        "setp.gt.and.s32 k, %7, 3, e;\n\t"
+        "@k tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, t;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "r"(acc0), "r"(kn), "n"(A_STEP), "n"(B_STEP)
         : "memory");
-    if constexpr (KS + 1 < END) mma_f8_steps<KS + 1, END, A_STEP, B_STEP, B_HI>(d, a_lo, b_lo, idesc, acc0);
 }
 // High word of an MN-major tile without swizzle: 16 values of a row of K in 16
 // bytes, rows 16 bytes apart, so groups of 8 rows (the leading byte offset, in the
 // low word) are 128 bytes apart and blocks of 16 columns 2 KiB (128 rows).
 constexpr uint32_t DESC_HI_ROWS16 = (2048u >> 4) | (1u << 14);
+
+// By one elected lane of a converged warp, operands uniform: a 5-D box copy, and an
+// arrival that expects `bytes` of copies (0: the arrival alone).
+__device__ __forceinline__ void tma_load_5d_elect(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, int c3,
+                                                  int c4) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+        : "memory");
+}
+__device__ __forceinline__ void arrive_expect_tx_elect(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes)
+        : "memory");
+}
 
 // 32 lanes x one 32-bit column.
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {

@@ -32,6 +32,7 @@ cudaError_t launch_backward_rotate(const BackwardArgs& a, cudaStream_t stream);
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream);
 cudaError_t launch_append_q8(const AppendQ8Args& a, cudaStream_t stream);
 cudaError_t launch_attn_q8(const AttnQ8Args& a, cudaStream_t stream);
+int decode_q8_bundle(int Hkv);
 cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream);
 }  // namespace rk
 
@@ -215,13 +216,15 @@ int make_page_map(CUtensorMap* m, const void* cache, int num_pages, int Hkv, con
     return make_map(m, cache, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what);
 }
 
-// 8-bit cache [num_pages, Hkv, 16, 128] as 3-D (byte, token, block): one box is
-// a page of one head, 2 KiB, landing as 16 swizzled rows of 128 bytes.
-int make_q8_map(CUtensorMap* m, const void* cache, int num_pages, int Hkv, const char* what) {
-    const cuuint64_t dims[3] = {(cuuint64_t)rk::HEAD_DIM, (cuuint64_t)rk::PAGE, (cuuint64_t)num_pages * Hkv};
-    const cuuint64_t strides[2] = {(cuuint64_t)rk::HEAD_DIM, (cuuint64_t)rk::Q8_BLOCK_BYTES};
-    const cuuint32_t box[3] = {(cuuint32_t)rk::HEAD_DIM, (cuuint32_t)rk::PAGE, 1};
-    return make_map(m, cache, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+// 8-bit cache [num_pages, Hkv, 16, 128] as 5-D (byte, token of a half, head, half,
+// page): one box is a page of `heads` neighbouring heads, landing as [half][head]
+// blocks of 8 swizzled rows of 128 bytes.
+int make_q8_map(CUtensorMap* m, const void* cache, int num_pages, int Hkv, int heads, const char* what) {
+    const cuuint64_t dims[5] = {(cuuint64_t)rk::HEAD_DIM, 8, (cuuint64_t)Hkv, 2, (cuuint64_t)num_pages};
+    const cuuint64_t strides[4] = {(cuuint64_t)rk::HEAD_DIM, (cuuint64_t)rk::Q8_BLOCK_BYTES,
+                                   (cuuint64_t)rk::Q8_BLOCK_BYTES / 2, (cuuint64_t)Hkv * rk::Q8_BLOCK_BYTES};
+    const cuuint32_t box[5] = {(cuuint32_t)rk::HEAD_DIM, 8, (cuuint32_t)heads, 2, 1};
+    return make_map(m, cache, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -1084,8 +1087,9 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t* plan, int32_t split_tokens, c
     // without a pool no row has a page to read: the map of the (16-byte aligned) query stands in
     CUtensorMap km, vm;
     const bool have = plan->num_pages > 0;
-    if ((rc = make_q8_map(&km, have ? k_cache : q, have ? plan->num_pages : 1, have ? plan->Hkv : 1, "k_cache"))) return rc;
-    if ((rc = make_q8_map(&vm, have ? v_cache : q, have ? plan->num_pages : 1, have ? plan->Hkv : 1, "v_cache"))) return rc;
+    const int pages = have ? plan->num_pages : 1, heads = rk::decode_q8_bundle(plan->Hkv);
+    if ((rc = make_q8_map(&km, have ? k_cache : q, pages, plan->Hkv, heads, "k_cache"))) return rc;
+    if ((rc = make_q8_map(&vm, have ? v_cache : q, pages, plan->Hkv, heads, "v_cache"))) return rc;
     cudaError_t e = rk::launch_decode_q8(km, vm, a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(RK_E_CUDA, "8-bit decode launch: %s", cudaGetErrorString(e));
     return RK_OK;
