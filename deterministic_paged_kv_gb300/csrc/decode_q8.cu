@@ -74,14 +74,14 @@ struct DqShape {
     // tensor memory: two buffers of S (4 tiles) and of O (H heads)
     static constexpr int TMEM_S = DQ_TILES * NS, TMEM_O = 2 * TMEM_S, TMEM_OBUF = H * NP;
     static constexpr int TMEM_COLS = TMEM_O + 2 * TMEM_OBUF <= 256 ? 256 : 512;
-    // shared memory: the ring (a step's K or V to a stage), q operands (one per head of the
-    // bundle), weights (one per tile: 16 columns of O to a 16-byte row per token, MN-major
-    // without swizzle)
-    static constexpr int STAGES = G == 8 && H == 4 ? 2 : 3, PBUF = G == 8 ? 1 : 2;  // as room allows
+    // shared memory: the ring (a step's K or V to a stage), two buffers of q operands (one per
+    // head of the bundle), weights (one per tile: 16 columns of O to a 16-byte row per token,
+    // MN-major without swizzle)
+    static constexpr int STAGES = G == 8 && H > 1 ? 2 : 3;  // as room allows
     static constexpr int Q_BYTES = NS * 128, P_BYTES = NP * DQ_TILE;
     static constexpr int OFF_Q = STAGES * DQ_STEP_BYTES;
-    static constexpr int OFF_P = OFF_Q + H * Q_BYTES;
-    static constexpr int OFF_CTRL = OFF_P + PBUF * DQ_TILES * P_BYTES;
+    static constexpr int OFF_P = OFF_Q + 2 * H * Q_BYTES;
+    static constexpr int OFF_CTRL = OFF_P + DQ_TILES * P_BYTES;
 };
 
 struct DqStep {
@@ -95,7 +95,7 @@ struct DqStep {
 struct DqCtrl {
     uint64_t full[3], empty[3];      // the ring
     uint64_t id_full[DQ_SLOTS], sc_full[DQ_SLOTS], slot_empty[DQ_SLOTS];
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_ready[2], o_full[2], o_read[2];  // by the parity of the step
     uint64_t never;
     uint32_t tmem_base;
@@ -106,8 +106,8 @@ struct DqCtrl {
     int ids[DQ_SLOTS][32];           // page of lane p's block: page p / H, head p % H of the step
     uint32_t odd[DQ_SLOTS];          // blocks whose scale is not one
     alignas(16) float4 sc[DQ_SLOTS][32];  // k scale, log2 of v's, 1 / v's of those blocks
-    float qscale[32];                // score factor of each query head (log2 domain)
-    uint32_t qbad;                   // query heads out of range
+    float qscale[2][32];             // score factor of each query head (log2 domain)
+    uint32_t qbad[2];                // query heads out of range
     float red[2][16][8];             // a step's maximum of each softmax warp, by parity
     float lred[2][16][8];            // an item's sums of each softmax warp, by parity
     uint32_t fred[2][16];            // queries out of range; bit 31: a scale
@@ -148,18 +148,6 @@ __device__ __forceinline__ void find_row(const AttnQ8Args& a, const DqCtrl* c, i
     }
 }
 
-// An item's result: query head hq, dim d (one thread each); o over l.
-__device__ __forceinline__ void write_item(const AttnQ8Args& a, const DqStep& st, int hq, int d, float o, float lse2) {
-    const size_t bh = (size_t)st.b * a.Hq + hq;
-    if (a.n_splits > 1) {
-        a.o_part[(bh * a.n_splits + st.split) * HEAD_DIM + d] = o;
-        if (d == 0) a.lse_part[bh * a.n_splits + st.split] = lse2;
-    } else {
-        reinterpret_cast<__nv_bfloat16*>(a.out)[bh * HEAD_DIM + d] = __float2bfloat16_rn(o);
-        if (d == 0) a.lse[bh] = lse2 * 0.693147180559945309f;
-    }
-}
-
 template <int G, int H>
 __global__ void __launch_bounds__(DQ_THREADS, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -187,13 +175,13 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             mbar_init(smem_u32(&c->slot_empty[i]), 19);  // producer, issuer, q, softmax warps
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&c->q_full[i]), 1);
+            mbar_init(smem_u32(&c->q_empty[i]), 17);     // issuer's commit, softmax warps
             mbar_init(smem_u32(&c->s_full[i]), 1);
             mbar_init(smem_u32(&c->p_ready[i]), 16);
             mbar_init(smem_u32(&c->o_full[i]), 1);
             mbar_init(smem_u32(&c->o_read[i]), 16);
         }
-        mbar_init(smem_u32(&c->q_full), 1);
-        mbar_init(smem_u32(&c->q_empty), 17);            // issuer's commit, softmax warps
         mbar_init(smem_u32(&c->never), 1);
         fence_mbar_init();
     }
@@ -378,64 +366,72 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 ++use;
             }
             if (!first) continue;
+            const int buf = nq & 1;
             const uint32_t pos = (uint32_t)max(0, a.position_ids[b]);
-            // dims 2 lane, 2 lane + 1 and the 64 above of G queries at a time, the next head's on the way
-            const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + ((size_t)b * a.Hq + h * H * G) * (HEAD_DIM / 2) + lane;
-            uint32_t lo[G], hi[G];
+            // A query head per turn of a rolled loop (100 instructions that stay in the
+            // instruction buffer; four heads unrolled took 5.5 us an item of 16), the next
+            // four on the way.  Lane: dims 2 lane, 2 lane + 1 and the 64 above.
+            constexpr int N = H * G, AHEAD = 4;
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + ((size_t)b * a.Hq + h * N) * (HEAD_DIM / 2) + lane;
+            uint32_t lo[AHEAD], hi[AHEAD];
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                lo[g] = __ldg(q + g * 64);
-                hi[g] = __ldg(q + g * 64 + 32);
+            for (int i = 0; i < N * 2; i += 32)  // all of it on its way to L2, 128 bytes a lane
+                if (i + lane < N * 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(q - lane + (i + lane) * 32));
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                lo[i] = i < N ? __ldg(q + i * 64) : 0;
+                hi[i] = i < N ? __ldg(q + i * 64 + 32) : 0;
             }
             float c0, s0, c1, s1;
             rope_cos_sin(pos, turn0, c0, s0);
             rope_cos_sin(pos, turn1, c1, s1);
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->q_empty), (uint32_t)((nq & 1) ^ 1), pc)))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->q_empty[buf]), (uint32_t)(((nq >> 1) & 1) ^ 1), pc)))) break;
             uint32_t badq = 0;
+            uint8_t* qt = sm + Sh::OFF_Q + buf * H * Sh::Q_BYTES + (2 * lane & 15);
+            int g = 0;
 #pragma unroll 1
-            for (int hj = 0; hj < H; ++hj) {
-                uint8_t* qt = sm + Sh::OFF_Q + hj * Sh::Q_BYTES;
-                uint32_t nlo[G], nhi[G];
-                const uint32_t* qn = q + (hj + 1 < H ? hj + 1 : hj) * G * 64;
+            for (int i = 0; i < N; ++i) {
+                const uint32_t wl = lo[0], wh = hi[0];
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    nlo[g] = __ldg(qn + g * 64);
-                    nhi[g] = __ldg(qn + g * 64 + 32);
+                for (int e = 0; e + 1 < AHEAD; ++e) {
+                    lo[e] = lo[e + 1];
+                    hi[e] = hi[e + 1];
                 }
+                if (i + AHEAD < N) {
+                    lo[AHEAD - 1] = __ldg(q + (i + AHEAD) * 64);
+                    hi[AHEAD - 1] = __ldg(q + (i + AHEAD) * 64 + 32);
+                }
+                uint32_t m = __vmaxu2(wl & 0x7fff7fffu, wh & 0x7fff7fffu);
+                m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+                const bool bad = m >= Q8_LIMIT_BF16;
+                if (bad) badq |= 1u << i;
+                const int e = bad ? 0 : q8_exponent(m);
+                const float inv = pow2(-e);
+                const float2 l = make_float2(bf16lo(wl) * inv, bf16hi(wl) * inv), u = make_float2(bf16lo(wh) * inv, bf16hi(wh) * inv);
+                float2 x = make_float2(l.x * c0 - u.x * s0, l.y * c1 - u.y * s1);
+                float2 y = make_float2(u.x * c0 + l.x * s0, u.y * c1 + l.y * s1);
+                if (bad) x = y = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    uint32_t m = __vmaxu2(lo[g] & 0x7fff7fffu, hi[g] & 0x7fff7fffu);
-                    m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-                    const bool bad = m >= Q8_LIMIT_BF16;
-                    if (bad) badq |= 1u << (hj * G + g);
-                    const int e = bad ? 0 : q8_exponent(m);
-                    const float inv = pow2(-e);
-                    const float2 l = make_float2(bf16lo(lo[g]), bf16hi(lo[g])), u = make_float2(bf16lo(hi[g]), bf16hi(hi[g]));
-                    float2 x = make_float2((l.x * c0 - u.x * s0) * inv, (l.y * c1 - u.y * s1) * inv);
-                    float2 y = make_float2((u.x * c0 + l.x * s0) * inv, (u.y * c1 + l.y * s1) * inv);
-                    if (bad) x = y = make_float2(0.0f, 0.0f);
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        if (p == 2) {
-                            x = make_float2(x.x * 256.0f, x.y * 256.0f);
-                            y = make_float2(y.x * 256.0f, y.y * 256.0f);
-                        }
-                        const int row = p * G + g;
-                        *reinterpret_cast<uint16_t*>(qt + sw128_off(row, lane >> 3) + (2 * lane & 15)) = (uint16_t)take_part(x);
-                        *reinterpret_cast<uint16_t*>(qt + sw128_off(row, 4 + (lane >> 3)) + (2 * lane & 15)) = (uint16_t)take_part(y);
+                for (int p = 0; p < 4; ++p) {
+                    if (p == 2) {
+                        x = make_float2(x.x * 256.0f, x.y * 256.0f);
+                        y = make_float2(y.x * 256.0f, y.y * 256.0f);
                     }
-                    if (lane == 0) c->qscale[hj * G + g] = a.qk_scale_log2 * pow2(e);
+                    const int row = p * G + g;
+                    const uint32_t at = sw128_off(row, lane >> 3);
+                    *reinterpret_cast<uint16_t*>(qt + at) = (uint16_t)take_part(x);
+                    *reinterpret_cast<uint16_t*>(qt + (at ^ 64)) = (uint16_t)take_part(y);  // chunk + 4
                 }
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    lo[g] = nlo[g];
-                    hi[g] = nhi[g];
+                if (lane == 0) c->qscale[buf][i] = a.qk_scale_log2 * pow2(e);
+                if (++g == G) {
+                    g = 0;
+                    qt += Sh::Q_BYTES;
                 }
             }
-            if (lane == 0) c->qbad = badq;
+            if (lane == 0) c->qbad[buf] = badq;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c->q_full));
+            if (lane == 0) mbar_arrive(smem_u32(&c->q_full[buf]));
             ++nq;
         }
     } else if (warp == 1) {
@@ -467,7 +463,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 if (left <= 0) break;
                 const uint32_t d = tmem + Sh::TMEM_O + buf * Sh::TMEM_OBUF + (j % H) * NP;
                 const uint32_t dv = dT + stg * (DQ_STEP_BYTES >> 4) + (j / H) * H * 1024 + (j % H) * 64;
-                const uint32_t dp = dP + ((k % Sh::PBUF) * DQ_TILES + j) * (Sh::P_BYTES >> 4);
+                const uint32_t dp = dP + j * (Sh::P_BYTES >> 4);
                 // a k-step is 4 groups of 8 tokens
                 mma_f8_x4<256 * H, 32>(d, dv, dp, HI_KV, DESC_HI_ROWS16, idO, j >= H, kn);
             }
@@ -493,7 +489,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             // here before the weights are, gained nothing.)
             if (pv_cnt > 0 && !(ok = issue_pv(ks - 1))) break;
             if (flags & 4) break;
-            if ((flags & 1) && !(ok = wait(c->q_full, nq))) break;
+            if ((flags & 1) && !(ok = wait(c->q_full[nq & 1], nq >> 1))) break;
             if (cnt > 0) {
                 const int n = 2 * ks, stg = n % STAGES, kb = ks & 1;
                 if (!(ok = wait(c->full[stg], n / STAGES))) break;
@@ -501,14 +497,14 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
 #pragma unroll 1
                 for (int j = 0; j < DQ_TILES && (j / H) * DQ_TILE < cnt; ++j)
                     mma_f8_x4<2, 2>(tmem + kb * Sh::TMEM_S + j * NS, dT + stg * (DQ_STEP_BYTES >> 4) + (j / H) * H * 1024 + (j % H) * 64,
-                                    dQ + (j % H) * (Sh::Q_BYTES >> 4), HI_KV, DESC_HI, idS, 0u, 4);
+                                    dQ + ((nq & 1) * H + j % H) * (Sh::Q_BYTES >> 4), HI_KV, DESC_HI, idS, 0u, 4);
                 umma_commit_elect(smem_u32(&c->s_full[kb]));
                 umma_commit_elect(smem_u32(&c->empty[stg]));
                 pv_cnt = cnt;
                 ++ks;
             }
             if (flags & 2) {
-                umma_commit_elect(smem_u32(&c->q_empty));
+                umma_commit_elect(smem_u32(&c->q_empty[nq & 1]));
                 ++nq;
             }
         }
@@ -543,25 +539,33 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         };
         // Results of an item from the warps' sums (behind a barrier).
         auto finish = [&](const DqStep& st, int par, int status, bool none) {
+            // softmax warp i of this head: the head's warpgroups are hj, hj + H, ...
+            auto of_head = [&](int i) { return ((i >> 2) * H + hj) * 4 + (i & 3); };
             uint32_t any = 0;
 #pragma unroll
-            for (int w = 0; w < 16; ++w)
-                if ((w >> 2) % H == hj) any |= c->fred[par][w];
+            for (int i = 0; i < 16 / H; ++i) any |= c->fred[par][of_head(i)];
+            if (status == RK_STATUS_TIMEOUT) any = 0;  // nothing was summed up
             if (any >> 31) status |= RK_STATUS_SCALE;
+            const size_t row = (size_t)st.b * a.Hq + (st.h * H + hj) * G;
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
                 const int g = blk + SHARE * i;
                 if (g < G) {
                     float sum = 0.0f;
 #pragma unroll
-                    for (int w = 0; w < 16; ++w)
-                        if ((w >> 2) % H == hj) sum += c->lred[par][w][g];
+                    for (int w = 0; w < 16 / H; ++w) sum += c->lred[par][of_head(w)][g];
                     const bool over = !none && (((any >> g) & 1u) || !(sum > 0.0f && sum < INFINITY));
                     const bool fail = status || over;
-                    const float x = o[i] * (1.0f / sum);
-                    const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : Mo[i] - 8.0f + log2f(sum);
-                    write_item(a, st, (st.h * H + hj) * G + g, t, fail || none ? 0.0f : x, lse2);
-                    if (t == 0 && fail && a.status) atomicOr(a.status, status ? status : RK_STATUS_RANGE);
+                    const float x = fail || none ? 0.0f : o[i] * rcp(sum);
+                    const size_t bh = row + g;
+                    if (a.n_splits > 1) a.o_part[(bh * a.n_splits + st.split) * HEAD_DIM + t] = x;
+                    else reinterpret_cast<__nv_bfloat16*>(a.out)[bh * HEAD_DIM + t] = __float2bfloat16_rn(x);
+                    if (t == 0) {
+                        const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : Mo[i] - 8.0f + __log2f(sum);
+                        if (a.n_splits > 1) a.lse_part[bh * a.n_splits + st.split] = lse2;
+                        else a.lse[bh] = lse2 * 0.693147180559945309f;
+                        if (fail && a.status) atomicOr(a.status, status ? status : RK_STATUS_RANGE);
+                    }
                 }
             }
             resume = (long long)st.item + gridDim.x;
@@ -590,23 +594,24 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     slot = 0;
                     ++use;
                 }
+                const int qb = nq & 1;
                 if (st.first && st.item >= 0) {
-                    wait(c->q_full, nq);
+                    wait(c->q_full[qb], nq >> 1);
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
                         M[g] = -INFINITY;
                         l[g] = 0.0f;
                     }
                     bad = 0;
-                    range = (c->qbad >> (hj * G)) & ((1u << G) - 1u);
+                    range = (c->qbad[qb] >> (hj * G)) & ((1u << G) - 1u);
                 }
 #pragma unroll
-                for (int g = 0; g < G; ++g) sc[g] = c->qscale[hj * G + g];
+                for (int g = 0; g < G; ++g) sc[g] = c->qscale[qb][hj * G + g];
                 constexpr uint32_t EACH = H == 1 ? 0xffffffffu : H == 2 ? 0x55555555u : 0x11111111u;
                 if (odd & (EACH << hj)) range |= 0x80000000u;
                 if (st.last && st.item >= 0) {
                     __syncwarp();
-                    if (ok && lane == 0) mbar_arrive(smem_u32(&c->q_empty));
+                    if (ok && lane == 0) mbar_arrive(smem_u32(&c->q_empty[qb]));
                     ++nq;
                 }
             }
@@ -664,9 +669,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                         ben[g / SHARE] = beta;
                     }
                 }
-                // the weights' buffer is free once the PV that read it last is done
-                if (Sh::PBUF == 2) wait(c->o_full[par], (ks >> 1) + 1);
-                else if (ks > 0) wait(c->o_full[par ^ 1], (ks - 1) >> 1);
+                // the weights' buffer is free once the PV of the step before is done
+                if (ks > 0) wait(c->o_full[par ^ 1], (ks - 1) >> 1);
                 if (have) {
                     // p' = 2^(w - m + 8) as three e4m3 parts, part * G + query of the token's row
                     uint32_t wd[NP / 4];
@@ -681,7 +685,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                             wd[col >> 2] |= take_part(x) << (8 * (col & 3));
                         }
                     }
-                    uint8_t* pt = sm + Sh::OFF_P + ((ks % Sh::PBUF) * DQ_TILES + wg) * Sh::P_BYTES + t * 16;
+                    uint8_t* pt = sm + Sh::OFF_P + wg * Sh::P_BYTES + t * 16;
 #pragma unroll
                     for (int i = 0; i < NP / 16; ++i)
                         *reinterpret_cast<uint4*>(pt + i * DQ_TILE * 16) = make_uint4(wd[4 * i], wd[4 * i + 1], wd[4 * i + 2], wd[4 * i + 3]);
@@ -783,7 +787,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 int nk, bd;
                 st.h = (int)(it % bundles);
                 find_row(a, c, (int)(it / bundles), st.b, st.split, nk, bd);
-                for (int g = blk; g < G; g += SHARE) write_item(a, st, (st.h * H + hj) * G + g, t, 0.0f, __int_as_float(0x7fc00000));
+                finish(st, 0, RK_STATUS_TIMEOUT, false);
             }
             if (tid == 128 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
         }

@@ -34,6 +34,13 @@ __device__ __forceinline__ uint32_t take_part(float2& x) {
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
+// 1 / x, off by at most one unit in the last place.
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Scale exponent of a set of bf16 values from the largest |x| as a bit pattern:
 // floor(log2) - 7, at least Q8_E_MIN, so that values over 2^E stay below 2^8
 // and their rotation below 362.
