@@ -32,12 +32,15 @@
 // are joined with the running maximum in FP32.  The copies leave the bundle as
 // [page][half][head][8 tokens][128 B] in shared memory, so that the 16 groups of 8
 // tokens of a head's tile lie at one stride and make one operand.
-// A persistent grid of one CTA per SM takes items c, c + grid, ... of the list
-// ordered by row, split, bundle, so neighbouring CTAs read neighbouring blocks.
+// The items in order of row, bundle, split are dealt to a persistent grid of one CTA per
+// SM in runs of equal numbers of steps, so a CTA changes its queries a few times only.
+// (Dealt in turn, 64 x 4096 gave 112 CTAs seven items of four steps and 40 six: they
+// ended between 78 and 98 us.)
 // Roles (20 warps):
 //   warp 0      TMA producer: a step's K, then its V, 64 KiB each, in a ring of three;
 //   warp 1      MMA issuer: S and PV of each step;
-//   warp 2      q: rotates the item's query heads, splits them into parts;
+//   warp 2      q: rotates the query heads of the next row and bundle, splits them into parts
+//               (the softmax warps do the first ones, together: they have nothing else to do);
 //   warp 3      metadata: walks the items, page ids and scales of each step;
 //   warps 4-19  softmax: warpgroup j has tile j of a step, a thread one token, and
 //               in the accumulation its share of that KV head's queries, a thread one
@@ -84,11 +87,13 @@ struct DqShape {
     static constexpr int OFF_CTRL = OFF_P + DQ_TILES * P_BYTES;
 };
 
+// Step flags: first and last of its item, first and last of its queries, no step any more.
+constexpr int DQ_FIRST = 1, DQ_LAST = 2, DQ_NEWQ = 4, DQ_ENDQ = 8, DQ_END = 16;
+
 struct DqStep {
     int b, h, split;   // row, bundle of KV heads, split
     int cnt;           // tokens of the step (0: nothing to compute)
-    int first, last;   // of the item
-    int item;          // index in the item list; -1: no more
+    int flags;         // DQ_*
     int bad;           // RK_STATUS_* bits of the row
 };
 
@@ -100,7 +105,7 @@ struct DqCtrl {
     uint64_t never;
     uint32_t tmem_base;
     PipeCtl pipe;
-    int total;                       // row splits of the batch
+    int total;                       // steps of the batch's rows (of one bundle)
     int scan[DQ_THREADS / 32];
     DqStep step[DQ_SLOTS];
     int ids[DQ_SLOTS][32];           // page of lane p's block: page p / H, head p % H of the step
@@ -110,8 +115,10 @@ struct DqCtrl {
     uint32_t qbad[2];                // query heads out of range
     float red[2][16][8];             // a step's maximum of each softmax warp, by parity
     float lred[2][16][8];            // an item's sums of each softmax warp, by parity
+    float2 ab[2][4][8];              // a step's scales of the sum so far and of its O, by parity, head, query
+    float top[2][4][8];              // an item's maximum, by parity, head, query
     uint32_t fred[2][16];            // queries out of range; bit 31: a scale
-    int pre[DQ_PRE + 1];             // row splits before each group of rows
+    int pre[DQ_PRE];                 // steps before each group of rows
 };
 template <int G, int H>
 constexpr int dq_smem_bytes() {
@@ -126,26 +133,137 @@ __device__ __forceinline__ int row_keys(const AttnQ8Args& a, int b, int& bad) {
     if (pos < 0) bad |= RK_STATUS_POSITION;
     return bad ? 0 : (pos < kv ? pos + 1 : kv);
 }
-__device__ __forceinline__ int splits_of(int n, int split) { return n > 0 ? (n + split - 1) / split : 1; }
+// ---- split geometry: up to three zones of equal splits (AttnQ8Args::zone) ----
 
-// Row and split of entry rs of the list of row splits.
-__device__ __forceinline__ void find_row(const AttnQ8Args& a, const DqCtrl* c, int rs, int& b, int& s, int& n, int& bad) {
-    const int per = (a.B + DQ_PRE - 1) / DQ_PRE, groups = (a.B + per - 1) / per;
-    int lo = 0, hi = groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (c->pre[mid] <= rs) lo = mid;
-        else hi = mid;
+// Splits of a row of n keys (one for an empty row).
+__device__ __forceinline__ int splits_of(const AttnQ8Args& a, int n) {
+    if (n <= 0) return 1;
+    const int z = n > a.zone[2].token ? 2 : n > a.zone[1].token ? 1 : 0;
+    return a.zone[z].split + (n - a.zone[z].token + a.zone[z].size - 1) / a.zone[z].size;
+}
+// Tokens [first, end) of split s.
+__device__ __forceinline__ void split_range(const AttnQ8Args& a, int s, int n, int& first, int& end) {
+    const int z = s >= a.zone[2].split ? 2 : s >= a.zone[1].split ? 1 : 0;
+    first = a.zone[z].token + (s - a.zone[z].split) * a.zone[z].size;
+    end = min(n, first + a.zone[z].size);
+}
+// Steps of T tokens of a row (one for an empty row).
+template <int T>
+__device__ __forceinline__ int row_steps(const AttnQ8Args& a, int n) {
+    if (n <= 0) return 1;
+    int sum = 0;
+#pragma unroll
+    for (int z = 0; z < 3; ++z) {
+        const int len = (z < 2 ? min(n, a.zone[z + 1].token) : n) - a.zone[z].token, size = a.zone[z].size;
+        if (len > 0) sum += len / size * ((size + T - 1) / T) + (len % size + T - 1) / T;
     }
-    b = lo * per;
-    s = rs - c->pre[lo];
-    while (true) {
-        n = row_keys(a, b, bad);
-        const int k = splits_of(n, a.split_tokens);
-        if (s < k || b + 1 >= a.B) return;
-        s -= k;
-        ++b;
+    return sum;
+}
+// First split of a row that starts at its step r or later; r becomes that split's first step.
+template <int T>
+__device__ __forceinline__ int split_at(const AttnQ8Args& a, int& r) {
+    int before = 0;
+#pragma unroll
+    for (int z = 0; z < 3; ++z) {
+        const int per = (a.zone[z].size + T - 1) / T;
+        const int count = z < 2 ? a.zone[z + 1].split - a.zone[z].split : 0x7fffffff;
+        const int k = r <= before ? 0 : (r - before + per - 1) / per;
+        if (z == 2 || k < count || count > (0x7fffffff - before) / per) {
+            r = before + k * per;
+            return a.zone[z].split + k;
+        }
+        before += count * per;
     }
+    return 0;
+}
+
+// A CTA's items: the splits whose first step, in the order of row, bundle, split, lies in the
+// CTA's share of all steps.
+template <int T>
+struct DqItems {
+    int b, h, s, n, ns, bad;  // the item: row, bundle, split; the row's keys, splits, status
+    int at, hi;               // its first step, the share's end (the host bounds all steps by INT32_MAX)
+
+    __device__ __forceinline__ bool valid(const AttnQ8Args& a) const { return b < a.B && at < hi; }
+    __device__ __forceinline__ void row(const AttnQ8Args& a) {
+        if (b < a.B) {
+            n = row_keys(a, b, bad);
+            ns = splits_of(a, n);
+        }
+    }
+    __device__ void start(const AttnQ8Args& a, const DqCtrl* c, int bundles) {
+        const unsigned all = (unsigned)(c->total * bundles), each = all / gridDim.x, rest = all % gridDim.x;
+        at = (int)(each * blockIdx.x + rest * blockIdx.x / gridDim.x);
+        hi = (int)(each * (blockIdx.x + 1) + rest * (blockIdx.x + 1) / gridDim.x);
+        const int per = (a.B + DQ_PRE - 1) / DQ_PRE, groups = (a.B + per - 1) / per;
+        int lo = 0, top = groups;
+        while (top - lo > 1) {
+            const int mid = (lo + top) >> 1;
+            if (c->pre[mid] * bundles <= at) lo = mid;
+            else top = mid;
+        }
+        b = lo * per;
+        int base = c->pre[lo] * bundles;
+        while (true) {
+            row(a);
+            const int sr = row_steps<T>(a, n);
+            const int in = at - base;
+            if (in < sr * bundles || b + 1 >= a.B) {
+                h = in / sr;
+                int r = in % sr;
+                s = split_at<T>(a, r);
+                at = base + h * sr + min(r, sr);
+                if (s >= ns) wrap(a, bundles);
+                return;
+            }
+            base += sr * bundles;
+            ++b;
+        }
+    }
+    __device__ __forceinline__ void wrap(const AttnQ8Args& a, int bundles) {  // the row's next bundle, or the next row
+        s = 0;
+        if (++h == bundles) {
+            h = 0;
+            ++b;
+            row(a);
+        }
+    }
+    __device__ __forceinline__ void next(const AttnQ8Args& a, int bundles) {
+        int t0, t1;
+        split_range(a, s, n, t0, t1);
+        at += max(1, (t1 - t0 + T - 1) / T);
+        if (++s == ns) wrap(a, bundles);
+    }
+};
+
+// One query head of a row (a warp): rotated, over a power of two, as four e4m3 parts in rows
+// part * G + g of the operand qt.  wl, wh: dims 2 lane, 2 lane + 1 and the 64 above.
+// Returns whether it is out of range (then zeros).
+template <int G>
+__device__ __forceinline__ bool prepare_query(uint8_t* qt, int g, uint32_t wl, uint32_t wh, float c0, float s0, float c1, float s1,
+                                              float scale, float* factor, int lane) {
+    uint32_t m = __vmaxu2(wl & 0x7fff7fffu, wh & 0x7fff7fffu);
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+    const bool bad = m >= Q8_LIMIT_BF16;
+    const int e = bad ? 0 : q8_exponent(m);
+    const float inv = pow2(-e);
+    const float2 l = make_float2(bf16lo(wl) * inv, bf16hi(wl) * inv), u = make_float2(bf16lo(wh) * inv, bf16hi(wh) * inv);
+    float2 x = make_float2(l.x * c0 - u.x * s0, l.y * c1 - u.y * s1);
+    float2 y = make_float2(u.x * c0 + l.x * s0, u.y * c1 + l.y * s1);
+    if (bad) x = y = make_float2(0.0f, 0.0f);
+    qt += 2 * lane & 15;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        if (p == 2) {
+            x = make_float2(x.x * 256.0f, x.y * 256.0f);
+            y = make_float2(y.x * 256.0f, y.y * 256.0f);
+        }
+        const uint32_t at = sw128_off(p * G + g, lane >> 3);
+        *reinterpret_cast<uint16_t*>(qt + at) = (uint16_t)take_part(x);
+        *reinterpret_cast<uint16_t*>(qt + (at ^ 64)) = (uint16_t)take_part(y);  // chunk + 4
+    }
+    if (lane == 0) *factor = scale * pow2(e);
+    return bad;
 }
 
 template <int G, int H>
@@ -164,6 +282,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     // ---- set-up: barriers, tensor memory, operands that stay zero, the item list ----
     if (tid == 0) {
         c->pipe.abort = 0;
+        c->qbad[0] = 0;
         c->pipe.limit_ns = wait_limit(a.wait_limit_ns);
         for (int i = 0; i < Sh::STAGES; ++i) {
             mbar_init(smem_u32(&c->full[i]), 1);
@@ -175,7 +294,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             mbar_init(smem_u32(&c->slot_empty[i]), 19);  // producer, issuer, q, softmax warps
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&c->q_full[i]), 1);
+            mbar_init(smem_u32(&c->q_full[i]), 16);      // lanes of the q warp, or the softmax warps
             mbar_init(smem_u32(&c->q_empty[i]), 17);     // issuer's commit, softmax warps
             mbar_init(smem_u32(&c->s_full[i]), 1);
             mbar_init(smem_u32(&c->p_ready[i]), 16);
@@ -193,7 +312,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         tmem_relinquish();
     }
     {
-        // Row splits before each group of `per` rows, a group to a thread and pass.
+        // Steps before each group of `per` rows, a group to a thread and pass.
         const int per = (a.B + DQ_PRE - 1) / DQ_PRE, groups = (a.B + per - 1) / per;
         int base = 0;
         for (int g0 = 0; g0 < groups; g0 += DQ_THREADS) {
@@ -202,7 +321,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             for (int b = gr * per; gr < groups && b < min(a.B, gr * per + per); ++b) {
                 int bad;
                 const int n = row_keys(a, b, bad);
-                cnt += splits_of(n, a.split_tokens);
+                cnt += row_steps<Sh::TOKENS>(a, n);
             }
             int v = cnt;
 #pragma unroll
@@ -229,7 +348,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     const uint32_t tmem = c->tmem_base;
     PipeCtl* pc = &c->pipe;
     const int bundles = a.Hkv / H;
-    const long long items = (long long)c->total * bundles;
+    using Items = DqItems<Sh::TOKENS>;
 
     if (warp == 3) {
         // ==================================================== metadata ====
@@ -237,24 +356,25 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         int slot = 0, use = 0;  // ring position and how often it went round
         bool ok = true;
         DqStep st{};
+        Items it;
+        it.start(a, c, bundles);
         int t = 0, t1 = 0, id = 0;  // the step's first token, the item's end, the lane's page id
-        long long it = blockIdx.x;
         const int my_page = lane / H;
+        bool newq = true;
         auto page_id = [&]() {
             return my_page * PAGE < t1 - t ? __ldg(a.block_table + (size_t)st.b * a.W + t / PAGE + my_page) : 0;
         };
-        auto item = [&]() {  // the item `it` and its first page ids
+        auto item = [&]() {  // the first step of the item `it` and its page ids
             st = DqStep{};
-            st.item = -1;
-            st.first = 1;
+            st.flags = DQ_END;
             t = t1 = 0;
-            if (it < items) {
-                int n;
-                st.item = (int)it;
-                st.h = (int)(it % bundles);
-                find_row(a, c, (int)(it / bundles), st.b, st.split, n, st.bad);
-                t = st.split * a.split_tokens;
-                t1 = min(n, t + a.split_tokens);
+            if (it.valid(a)) {
+                st.b = it.b;
+                st.h = it.h;
+                st.split = it.s;
+                st.bad = it.bad;
+                st.flags = DQ_FIRST | (newq ? DQ_NEWQ : 0);
+                split_range(a, it.s, it.n, t, t1);
             }
             id = page_id();
         };
@@ -263,7 +383,13 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             const int cnt = max(0, min(Sh::TOKENS, t1 - t));
             const bool mine = my_page * PAGE < cnt;
             const bool oob = mine && (id < 0 || id >= a.num_pages);
-            st.last = t + Sh::TOKENS >= t1;
+            const bool end = st.flags & DQ_END, last = t + Sh::TOKENS >= t1;
+            if (last && !end) {  // the next item, before this step is told: it may have the same queries
+                const int b = it.b, h = it.h;
+                it.next(a, bundles);
+                newq = !it.valid(a) || it.b != b || it.h != h;
+                st.flags |= DQ_LAST | (newq ? DQ_ENDQ : 0);
+            }
             st.cnt = cnt;
             if (__any_sync(0xffffffffu, oob)) {
                 st.bad |= RK_STATUS_PAGE_OOB;
@@ -283,10 +409,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 vs = __ldg(a.v_scale + block);
             }
             // the next step's page ids travel while this step's scales do
-            const bool end = st.item < 0;
-            st.bad = st.first = 0;  // reported once
-            if (st.last) {
-                it += gridDim.x;
+            st.bad = st.flags = 0;  // said once
+            if (last) {
                 if (!end) item();
             } else {
                 t += Sh::TOKENS;
@@ -294,7 +418,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             }
             const bool odd = !scale_ok(ks) || !scale_ok(vs);
             if (odd) ks = vs = 1.0f;
-            c->sc[slot][lane] = make_float4(ks, __log2f(vs), 1.0f / vs, 0.0f);
+            c->sc[slot][lane] = make_float4(ks, __log2f(vs), rcp(vs), 0.0f);
             const uint32_t odds = __ballot_sync(0xffffffffu, odd);
             if (lane == 0) c->odd[slot] = odds;
             __syncwarp();
@@ -322,7 +446,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->id_full[slot]), (uint32_t)(use & 1), pc)))) break;
             const int cnt = __shfl_sync(0xffffffffu, c->step[slot].cnt, 0), head = __shfl_sync(0xffffffffu, c->step[slot].h, 0) * H;
             const int id = c->ids[slot][lane];
-            if (__any_sync(0xffffffffu, c->step[slot].item < 0)) break;
+            if (__any_sync(0xffffffffu, c->step[slot].flags & DQ_END)) break;
             if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
             if (++slot == DQ_SLOTS) {
                 slot = 0;
@@ -354,23 +478,28 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         int slot = 0, use = 0, nq = 0;
         bool ok = true;
         const uint64_t turn0 = a.rope_turns[2 * lane], turn1 = a.rope_turns[2 * lane + 1];
+#pragma unroll 1
         while (ok) {
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->id_full[slot]), (uint32_t)(use & 1), pc)))) break;
             const volatile DqStep* st = &c->step[slot];
-            const int b = st->b, h = st->h, first = st->first;
-            if (st->item < 0) break;
+            const int b = st->b, h = st->h, flags = st->flags;
+            if (flags & DQ_END) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
             if (++slot == DQ_SLOTS) {
                 slot = 0;
                 ++use;
             }
-            if (!first) continue;
+            if (!(flags & DQ_NEWQ)) continue;
+            if (nq == 0) {  // the softmax warps'
+                ++nq;
+                continue;
+            }
             const int buf = nq & 1;
             const uint32_t pos = (uint32_t)max(0, a.position_ids[b]);
             // A query head per turn of a rolled loop (100 instructions that stay in the
-            // instruction buffer; four heads unrolled took 5.5 us an item of 16), the next
-            // four on the way.  Lane: dims 2 lane, 2 lane + 1 and the 64 above.
+            // instruction buffer; four heads unrolled took 5.5 us a bundle of 16), the next
+            // four on the way.
             constexpr int N = H * G, AHEAD = 4;
             const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + ((size_t)b * a.Hq + h * N) * (HEAD_DIM / 2) + lane;
             uint32_t lo[AHEAD], hi[AHEAD];
@@ -387,7 +516,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             rope_cos_sin(pos, turn1, c1, s1);
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&c->q_empty[buf]), (uint32_t)(((nq >> 1) & 1) ^ 1), pc)))) break;
             uint32_t badq = 0;
-            uint8_t* qt = sm + Sh::OFF_Q + buf * H * Sh::Q_BYTES + (2 * lane & 15);
+            uint8_t* qt = sm + Sh::OFF_Q + buf * H * Sh::Q_BYTES;
             int g = 0;
 #pragma unroll 1
             for (int i = 0; i < N; ++i) {
@@ -401,28 +530,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     lo[AHEAD - 1] = __ldg(q + (i + AHEAD) * 64);
                     hi[AHEAD - 1] = __ldg(q + (i + AHEAD) * 64 + 32);
                 }
-                uint32_t m = __vmaxu2(wl & 0x7fff7fffu, wh & 0x7fff7fffu);
-                m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-                const bool bad = m >= Q8_LIMIT_BF16;
-                if (bad) badq |= 1u << i;
-                const int e = bad ? 0 : q8_exponent(m);
-                const float inv = pow2(-e);
-                const float2 l = make_float2(bf16lo(wl) * inv, bf16hi(wl) * inv), u = make_float2(bf16lo(wh) * inv, bf16hi(wh) * inv);
-                float2 x = make_float2(l.x * c0 - u.x * s0, l.y * c1 - u.y * s1);
-                float2 y = make_float2(u.x * c0 + l.x * s0, u.y * c1 + l.y * s1);
-                if (bad) x = y = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    if (p == 2) {
-                        x = make_float2(x.x * 256.0f, x.y * 256.0f);
-                        y = make_float2(y.x * 256.0f, y.y * 256.0f);
-                    }
-                    const int row = p * G + g;
-                    const uint32_t at = sw128_off(row, lane >> 3);
-                    *reinterpret_cast<uint16_t*>(qt + at) = (uint16_t)take_part(x);
-                    *reinterpret_cast<uint16_t*>(qt + (at ^ 64)) = (uint16_t)take_part(y);  // chunk + 4
-                }
-                if (lane == 0) c->qscale[buf][i] = a.qk_scale_log2 * pow2(e);
+                if (prepare_query<G>(qt, g, wl, wh, c0, s0, c1, s1, a.qk_scale_log2, &c->qscale[buf][i], lane)) badq |= 1u << i;
                 if (++g == G) {
                     g = 0;
                     qt += Sh::Q_BYTES;
@@ -431,7 +539,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             if (lane == 0) c->qbad[buf] = badq;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&c->q_full[buf]));
+            if (lane < 16) mbar_arrive(smem_u32(&c->q_full[buf]));
             ++nq;
         }
     } else if (warp == 1) {
@@ -476,8 +584,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         while (ok) {
             if (!(ok = wait(c->id_full[slot], use))) break;
             const int cnt = __shfl_sync(0xffffffffu, c->step[slot].cnt, 0);
-            const int flags = __shfl_sync(0xffffffffu, c->step[slot].first | (c->step[slot].last << 1) | (c->step[slot].item < 0 ? 4 : 0), 0);
-            if (!(flags & 4)) {
+            const int flags = __shfl_sync(0xffffffffu, c->step[slot].flags, 0);
+            if (!(flags & DQ_END)) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
                 if (++slot == DQ_SLOTS) {
@@ -488,8 +596,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             // The PV that is due goes before this step's S.  (S first, where this step's K is
             // here before the weights are, gained nothing.)
             if (pv_cnt > 0 && !(ok = issue_pv(ks - 1))) break;
-            if (flags & 4) break;
-            if ((flags & 1) && !(ok = wait(c->q_full[nq & 1], nq >> 1))) break;
+            if (flags & DQ_END) break;
+            if ((flags & DQ_NEWQ) && !(ok = wait(c->q_full[nq & 1], nq >> 1))) break;
             if (cnt > 0) {
                 const int n = 2 * ks, stg = n % STAGES, kb = ks & 1;
                 if (!(ok = wait(c->full[stg], n / STAGES))) break;
@@ -503,7 +611,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 pv_cnt = cnt;
                 ++ks;
             }
-            if (flags & 2) {
+            if (flags & DQ_ENDQ) {
                 umma_commit_elect(smem_u32(&c->q_empty[nq & 1]));
                 ++nq;
             }
@@ -520,17 +628,16 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         const int t = tid & 127;                       // token of the tile, output dim
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         constexpr int OWN = Sh::OWN, SHARE = Sh::SHARE;  // queries blk, blk + SHARE, ... are this warpgroup's
-        int slot = 0, use = 0, nq = 0, ks = 0;         // items, steps so far
+        int slot = 0, use = 0, ni = 0, nq = 0, ks = 0;  // items, queries, steps so far
         float M[G], l[G];
         int bad = 0;         // the item's status bits
         uint32_t range = 0;  // queries that met a value FP32 cannot hold; bit 31: a scale that is none
         float o[OWN];
-        // the step whose O is due: scales of what is summed so far and of O, the item's end
+        // the step whose O is due
         int due = 0;
-        float al[OWN], be[OWN], Mo[OWN];
         DqStep dst{};
         int dbad = 0, dpar = 0;
-        long long resume = blockIdx.x;  // first item not written
+        int done = 0;        // items written
         // The warps leave the loop together: one whose wait gave up goes on to the
         // next barrier, which tells the others.
         bool ok = true;
@@ -561,15 +668,39 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     if (a.n_splits > 1) a.o_part[(bh * a.n_splits + st.split) * HEAD_DIM + t] = x;
                     else reinterpret_cast<__nv_bfloat16*>(a.out)[bh * HEAD_DIM + t] = __float2bfloat16_rn(x);
                     if (t == 0) {
-                        const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : Mo[i] - 8.0f + __log2f(sum);
+                        const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : c->top[par][hj][g] - 8.0f + __log2f(sum);
                         if (a.n_splits > 1) a.lse_part[bh * a.n_splits + st.split] = lse2;
                         else a.lse[bh] = lse2 * 0.693147180559945309f;
                         if (fail && a.status) atomicOr(a.status, status ? status : RK_STATUS_RANGE);
                     }
                 }
             }
-            resume = (long long)st.item + gridDim.x;
+            ++done;
         };
+        // the first queries, a head to a warp
+        {
+            Items it;
+            it.start(a, c, bundles);
+            if (it.valid(a)) {
+                constexpr int N = H * G;
+                float c0, s0, c1, s1;
+                const uint32_t pos = (uint32_t)max(0, a.position_ids[it.b]);
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + ((size_t)it.b * a.Hq + it.h * N) * (HEAD_DIM / 2) + lane;
+#pragma unroll 1
+                for (int i = sw; i < N; i += 16) {
+                    const uint32_t wl = __ldg(q + i * 64), wh = __ldg(q + i * 64 + 32);
+                    rope_cos_sin(pos, a.rope_turns[2 * lane], c0, s0);
+                    rope_cos_sin(pos, a.rope_turns[2 * lane + 1], c1, s1);
+                    if (prepare_query<G>(sm + Sh::OFF_Q + i / G * Sh::Q_BYTES, i % G, wl, wh, c0, s0, c1, s1, a.qk_scale_log2,
+                                         &c->qscale[0][i], lane) &&
+                        lane == 0)
+                        atomicOr(&c->qbad[0], 1u << i);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c->q_full[0]));
+            }
+        }
         while (true) {
             wait(c->id_full[slot], use);
             wait(c->sc_full[slot], use);
@@ -582,9 +713,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 st.h = s->h;
                 st.split = s->split;
                 st.cnt = s->cnt;
-                st.first = s->first;
-                st.last = s->last;
-                st.item = s->item;
+                st.flags = s->flags;
                 st.bad = s->bad;
                 ps = c->sc[slot][(8 * blk + (t >> 4)) * H + hj];
                 const uint32_t odd = c->odd[slot];
@@ -595,8 +724,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     ++use;
                 }
                 const int qb = nq & 1;
-                if (st.first && st.item >= 0) {
-                    wait(c->q_full[qb], nq >> 1);
+                if (st.flags & DQ_NEWQ) wait(c->q_full[qb], nq >> 1);
+                if (st.flags & DQ_FIRST) {
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
                         M[g] = -INFINITY;
@@ -609,11 +738,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 for (int g = 0; g < G; ++g) sc[g] = c->qscale[qb][hj * G + g];
                 constexpr uint32_t EACH = H == 1 ? 0xffffffffu : H == 2 ? 0x55555555u : 0x11111111u;
                 if (odd & (EACH << hj)) range |= 0x80000000u;
-                if (st.last && st.item >= 0) {
+                if (st.flags & DQ_ENDQ) {
                     __syncwarp();
                     if (ok && lane == 0) mbar_arrive(smem_u32(&c->q_empty[qb]));
                     ++nq;
                 }
+                ni += (st.flags & DQ_LAST) != 0;
             }
             const int par = ks & 1;
             const bool have = blk * DQ_TILE < st.cnt;  // the tile holds tokens
@@ -651,7 +781,6 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 ok = false;
                 break;
             }
-            float aln[OWN], ben[OWN];  // this step's scales of o and O
             if (st.cnt > 0) {
                 float p[G];
                 const int rw = ((lane & 15) >> 2) % H == hj ? lane & 15 : 4 * hj;  // a warp of this head
@@ -664,10 +793,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                     M[g] = top;
                     p[g] = ex2(w[g] - m + 8.0f);
                     l[g] = fmaf(l[g], alpha, p[g] * ps.z * beta);
-                    if (g % SHARE == blk) {
-                        aln[g / SHARE] = alpha;
-                        ben[g / SHARE] = beta;
-                    }
+                    if (blk == 0 && t == 0) c->ab[par][hj][g] = make_float2(alpha, beta);
                 }
                 // the weights' buffer is free once the PV of the step before is done
                 if (ks > 0) wait(c->o_full[par ^ 1], (ks - 1) >> 1);
@@ -709,11 +835,12 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&c->p_ready[par]));
             }
             // the item's sums, at its last step
-            const int ipar = (nq + 1) & 1;
+            const int ipar = (ni + 1) & 1;
             bad |= st.bad;
-            if (st.last && st.item >= 0) {
+            if (st.flags & DQ_LAST) {
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
+                    if (blk == 0 && t == 0) c->top[ipar][hj][g] = M[g];
                     float x = l[g];
 #pragma unroll
                     for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
@@ -741,10 +868,11 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < OWN; ++i) {
                     const float x = (__uint_as_float(r[i][2]) + __uint_as_float(r[i][1])) + __uint_as_float(r[i][0]);
-                    o[i] = fmaf(x, be[i], o[i] * al[i]);
+                    const float2 ab = c->ab[db][hj][min(blk + SHARE * i, G - 1)];
+                    o[i] = fmaf(x, ab.y, o[i] * ab.x);
                     if (!(fabsf(o[i]) < INFINITY) && blk + SHARE * i < G) over |= 1u << (blk + SHARE * i);
                 }
-                if (dst.last) {
+                if (dst.flags & DQ_LAST) {
                     // o may be beyond FP32 (a NaN code in V) in a dim only; the head's 128 threads agree on it
                     over = __reduce_or_sync(0xffffffffu, over);
                     if (over && lane == 0) atomicOr(&c->fred[dpar][sw], over);
@@ -756,7 +884,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 }
                 due = 0;
             }
-            if (st.item < 0) break;
+            if (st.flags & DQ_END) break;
             if (st.cnt > 0) {
                 due = 1;
                 dst = st;
@@ -764,15 +892,10 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 dpar = ipar;
 #pragma unroll
                 for (int i = 0; i < OWN; ++i) {
-                    al[i] = aln[i];
-                    be[i] = ben[i];
-                    if (st.first) o[i] = 0.0f;
-#pragma unroll
-                    for (int g = i * SHARE; g < G && g < (i + 1) * SHARE; ++g)
-                        if (g % SHARE == blk) Mo[i] = M[g];
+                    if (st.flags & DQ_FIRST) o[i] = 0.0f;
                 }
                 ++ks;
-            } else if (st.last) {
+            } else if (st.flags & DQ_LAST) {
                 // nothing in this step: an empty row, or one that fails
                 if (named_bar_or(1, DQ_SOFTMAX, !ok)) {
                     ok = false;
@@ -782,11 +905,14 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             }
         }
         if (!ok) {  // a wait gave up: this CTA's items from here on are written as failed
-            for (long long it = resume; it < items; it += gridDim.x) {
+            Items it;
+            it.start(a, c, bundles);
+            for (int i = 0, skip = done; it.valid(a); ++i, it.next(a, bundles)) {
+                if (i < skip) continue;
                 DqStep st{};
-                int nk, bd;
-                st.h = (int)(it % bundles);
-                find_row(a, c, (int)(it / bundles), st.b, st.split, nk, bd);
+                st.b = it.b;
+                st.h = it.h;
+                st.split = it.s;
                 finish(st, 0, RK_STATUS_TIMEOUT, false);
             }
             if (tid == 128 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
@@ -801,21 +927,35 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
     }
 }
 
-// Merge of the split partials of one (row, query head).  Warp w takes splits w,
-// w + 8, ... with the weights 2^(lse_s - max lse), a lane four dims; the warps'
-// sums are added in order.  Fixed by the row's split count alone.  A NaN partial
-// fails the row, no visible key gives out = 0, lse = -inf.
-constexpr int MERGE_WARPS = 8;
-__global__ void __launch_bounds__(32 * MERGE_WARPS) merge_q8_kernel(const __grid_constant__ AttnQ8Args a) {
-    __shared__ float4 acc_s[MERGE_WARPS][32];
-    __shared__ float sum_s[MERGE_WARPS];
+// Merge of the split partials of one (row, query head): weights 2^(lse_s - max lse), eight
+// sums over the splits s = e, e + 8, ... in ascending order, added up in order of e: fixed by
+// the row's split count alone.  A lane has four dims.  A NaN partial fails the row, no visible
+// key gives out = 0, lse = -inf.  WARPS = 1: a warp has all eight sums (one round of loads for
+// up to eight splits, four rows to a block); 8: a warp has one, for long rows.  Both add in the
+// same order, so which one runs (a choice by the table's width) does not show in the result.
+// Bound by latency: length of the row, a round of loads, one of stores.
+template <int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 256) merge_q8_kernel(const __grid_constant__ AttnQ8Args a) {
+    constexpr int SUMS = 8 / WARPS;
+    __shared__ float4 acc_s[WARPS == 1 ? 1 : 8][32];
+    __shared__ float sum_s[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const size_t bh = blockIdx.x;
+    const size_t bh = WARPS == 1 ? (size_t)blockIdx.x * 4 + warp : blockIdx.x;
+    if (WARPS == 1 && bh >= (size_t)a.B * a.Hq) return;
+    const int e0 = WARPS == 1 ? 0 : warp;
     int bad0;
-    const int ns = splits_of(row_keys(a, (int)(bh / a.Hq), bad0), a.split_tokens);
+    const int ns = splits_of(a, row_keys(a, (int)(bh / a.Hq), bad0));
     griddep_wait();  // the partials are complete and visible
     const float* lp = a.lse_part + bh * a.n_splits;
     const float4* op = reinterpret_cast<const float4*>(a.o_part + bh * a.n_splits * HEAD_DIM) + lane;
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 x[SUMS];
+    float wt[SUMS];
+#pragma unroll
+    for (int e = 0; e < SUMS; ++e) {
+        x[e] = e0 + e < ns ? op[(size_t)(e0 + e) * 32] : zero;
+        wt[e] = e0 + e < ns ? lp[e0 + e] : -INFINITY;
+    }
     float m = -INFINITY;
     bool bad = false;
     for (int s = lane; s < ns; s += 32) {
@@ -827,49 +967,60 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) merge_q8_kernel(const __grid
     bad = __any_sync(0xffffffffu, bad);
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + bh * HEAD_DIM;
     if (bad || m == -INFINITY) {
-        if (warp == 0) {
+        if (e0 == 0) {
             reinterpret_cast<uint2*>(out)[lane] = make_uint2(0, 0);
             if (lane == 0) a.lse[bh] = bad ? __int_as_float(0x7fc00000) : -INFINITY;
         }
         return;
     }
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float sum = 0.0f;
-    constexpr int AHEAD = 4;
-    for (int s0 = warp; s0 < ns; s0 += MERGE_WARPS * AHEAD) {
-        float4 x[AHEAD];
-        float wt[AHEAD];
+    float4 acc[SUMS];
+    float sum[SUMS];
 #pragma unroll
-        for (int e = 0; e < AHEAD; ++e) {
-            const int s = s0 + e * MERGE_WARPS;
-            wt[e] = s < ns ? lp[s] : -INFINITY;
-            x[e] = s < ns ? op[(size_t)s * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int e = 0; e < SUMS; ++e) {
+        acc[e] = zero;
+        sum[e] = 0.0f;
+    }
+    for (int s0 = 0; s0 < ns; s0 += 8) {
+        float4 nx[SUMS];
+        float nw[SUMS];
+#pragma unroll
+        for (int e = 0; e < SUMS; ++e) {  // the next round's loads
+            const int s = s0 + 8 + e0 + e;
+            nx[e] = s < ns ? op[(size_t)s * 32] : zero;
+            nw[e] = s < ns ? lp[s] : -INFINITY;
         }
 #pragma unroll
-        for (int e = 0; e < AHEAD; ++e) {
+        for (int e = 0; e < SUMS; ++e) {
             const float w = ex2(wt[e] - m);
-            sum += w;
-            acc.x = fmaf(w, x[e].x, acc.x);
-            acc.y = fmaf(w, x[e].y, acc.y);
-            acc.z = fmaf(w, x[e].z, acc.z);
-            acc.w = fmaf(w, x[e].w, acc.w);
+            sum[e] += w;
+            acc[e].x = fmaf(w, x[e].x, acc[e].x);
+            acc[e].y = fmaf(w, x[e].y, acc[e].y);
+            acc[e].z = fmaf(w, x[e].z, acc[e].z);
+            acc[e].w = fmaf(w, x[e].w, acc[e].w);
+            x[e] = nx[e];
+            wt[e] = nw[e];
         }
     }
-    acc_s[warp][lane] = acc;
-    if (lane == 0) sum_s[warp] = sum;
-    __syncthreads();
-    if (warp) return;
-    for (int w = 1; w < MERGE_WARPS; ++w) {
-        const float4 x = acc_s[w][lane];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
-        sum += sum_s[w];
+    float4 r = acc[0];
+    float l = sum[0];
+    if constexpr (WARPS == 8) {
+        acc_s[warp][lane] = acc[0];
+        if (lane == 0) sum_s[warp] = sum[0];
+        __syncthreads();
+        if (warp) return;
     }
-    const float inv = 1.0f / sum;
-    reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (lane == 0) a.lse[bh] = (m + log2f(sum)) * 0.693147180559945309f;
+#pragma unroll
+    for (int e = 1; e < 8; ++e) {
+        const float4 y = WARPS == 1 ? acc[e % SUMS] : acc_s[WARPS == 1 ? 0 : e][lane];
+        r.x += y.x;
+        r.y += y.y;
+        r.z += y.z;
+        r.w += y.w;
+        l += WARPS == 1 ? sum[e % SUMS] : sum_s[e];
+    }
+    const float inv = 1.0f / l;
+    reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv));
+    if (lane == 0) a.lse[bh] = (m + log2f(l)) * 0.693147180559945309f;
 }
 
 std::atomic<uint64_t> g_configured{0};
@@ -925,16 +1076,18 @@ cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const
     const unsigned grid = (unsigned)(most < sms ? most : sms);
     e = launch_any(a.G, bundle, km, vm, a, grid, stream, false);
     if (e != cudaSuccess || a.n_splits <= 1) return e;
+    const long long rows = (long long)a.B * a.Hq;
+    const bool few = a.n_splits <= 16;  // 64 x 4096 (10 splits): a warp each; from some tens of splits on eight share one
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hq));
-    cfg.blockDim = dim3(32 * MERGE_WARPS);
+    cfg.gridDim = dim3((unsigned)(few ? (rows + 3) / 4 : rows));
+    cfg.blockDim = dim3(few ? 128 : 256);
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, merge_q8_kernel, a);
+    return few ? cudaLaunchKernelEx(&cfg, merge_q8_kernel<1>, a) : cudaLaunchKernelEx(&cfg, merge_q8_kernel<8>, a);
 }
 
 }  // namespace rk

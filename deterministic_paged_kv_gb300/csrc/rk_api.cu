@@ -952,16 +952,35 @@ int attn_q8_args(const rk_paged_plan_t* plan, const void* q, const void* k_cache
     return RK_OK;
 }
 
-int q8_split(int32_t* split_tokens) {
-    if (*split_tokens == 0) *split_tokens = RK_PAGED_Q8_SPLIT_TOKENS;
-    if (*split_tokens < 0 || *split_tokens % rk::PAGE != 0)
-        return fail(RK_E_ARG, "split_tokens must be 0 or a positive multiple of %d (got %d)", rk::PAGE, *split_tokens);
+// Split geometry of the 8-bit decode.  split_tokens = 0: short splits where a row starts
+// (a short row then has several CTAs at work), longer ones further on (fewer partial
+// results of a long row); which token is in which split never depends on the row's length.
+int q8_zones(int32_t split_tokens, rk::AttnQ8Args* a) {
+    if (split_tokens < 0 || split_tokens % rk::PAGE != 0)
+        return fail(RK_E_ARG, "split_tokens must be 0 or a positive multiple of %d (got %d)", rk::PAGE, split_tokens);
+    const int32_t far = INT32_MAX;
+    if (split_tokens > 0) {
+        a->zone[0] = {0, 0, split_tokens};
+        a->zone[1] = a->zone[2] = {far, far, split_tokens};
+    } else {
+        a->zone[0] = {0, 0, 256};
+        a->zone[1] = {4, 1024, 512};
+        a->zone[2] = {18, 8192, 2048};
+    }
     return RK_OK;
 }
 
+// Splits of the longest row that the table can hold, at least one.
+int64_t q8_split_count(const rk_paged_plan_t* plan, const rk::AttnQ8Args& a) {
+    const int64_t cap = (int64_t)plan->W * rk::PAGE;
+    if (cap <= 0) return 1;
+    const int z = cap > a.zone[2].token ? 2 : cap > a.zone[1].token ? 1 : 0;
+    return a.zone[z].split + (cap - a.zone[z].token + a.zone[z].size - 1) / a.zone[z].size;
+}
+
 // Scratch of the 8-bit decode: none where the table holds one split at most.
-int64_t q8_scratch_need(const rk_paged_plan_t* plan, int32_t split_tokens) {
-    return split_count(plan, split_tokens) > 1 ? split_scratch_need(plan, split_tokens) : 0;
+int64_t q8_scratch_need(const rk_paged_plan_t* plan, int64_t splits) {
+    return splits > 1 ? (int64_t)plan->B * plan->Hq * splits * (rk::HEAD_DIM + 1) * 4 : 0;
 }
 
 }  // namespace
@@ -1050,9 +1069,10 @@ int rk_paged_decode_q8_scratch_bytes(const rk_paged_plan_t* plan, int32_t split_
     g_err.clear();
     if (!plan || !bytes) return fail(RK_E_ARG, "plan and bytes must be non-null");
     if (plan->abi != RK_PAGED_ABI_VERSION) return fail(RK_E_ARG, "plan ABI %u != %u", plan->abi, RK_PAGED_ABI_VERSION);
-    int rc = q8_split(&split_tokens);
+    rk::AttnQ8Args a;
+    int rc = q8_zones(split_tokens, &a);
     if (rc) return rc;
-    *bytes = (uint64_t)q8_scratch_need(plan, split_tokens);
+    *bytes = (uint64_t)q8_scratch_need(plan, q8_split_count(plan, a));
     return RK_OK;
 }
 
@@ -1064,11 +1084,14 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t* plan, int32_t split_tokens, c
     int rc = check_plan(plan);
     if (rc) return rc;
     if (plan->Sq != 1) return fail(RK_E_ARG, "decode needs a plan with Sq == 1 (got %d)", plan->Sq);
-    if ((rc = q8_split(&split_tokens))) return rc;
-    if ((double)plan->B * plan->Hkv * (double)split_count(plan, split_tokens) > 2147483647.0)
-        return fail(RK_E_UNSUPPORTED, "B %d x Hkv %d x %lld splits: too many", plan->B, plan->Hkv,
-                    (long long)split_count(plan, split_tokens));
-    const int64_t need = q8_scratch_need(plan, split_tokens);
+    rk::AttnQ8Args a;
+    if ((rc = q8_zones(split_tokens, &a))) return rc;
+    const int64_t splits = q8_split_count(plan, a);
+    // steps and items are counted in 32 bits
+    if ((double)plan->B * plan->Hkv * ((double)plan->W + (double)splits) > 2147483647.0)
+        return fail(RK_E_UNSUPPORTED, "B %d x Hkv %d x (W %d + %lld splits): too many", plan->B, plan->Hkv, plan->W,
+                    (long long)splits);
+    const int64_t need = q8_scratch_need(plan, splits);
     if (need > 0) {
         if (!scratch || !aligned(scratch, 16))
             return fail(RK_E_ARG, "8-bit decode scratch must be a non-null 16-byte aligned device pointer");
@@ -1076,12 +1099,11 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t* plan, int32_t split_tokens, c
             return fail(RK_E_ARG, "8-bit decode scratch too small: %lld bytes needed, %llu given", (long long)need,
                         (unsigned long long)scratch_bytes);
     }
-    rk::AttnQ8Args a;
     rc = attn_q8_args(plan, q, k_cache, v_cache, k_scale, v_scale, block_table_d, kv_lens_d, position_ids_d, out, lse, status_d,
                       &a);
     if (rc || plan->B == 0) return rc;
-    a.split_tokens = split_tokens;
-    a.n_splits = (int32_t)split_count(plan, split_tokens);
+    q8_zones(split_tokens, &a);
+    a.n_splits = (int32_t)splits;
     a.o_part = static_cast<float*>(scratch);
     if (need > 0) a.lse_part = a.o_part + (int64_t)plan->B * plan->Hq * a.n_splits * rk::HEAD_DIM;
     // without a pool no row has a page to read: the map of the (16-byte aligned) query stands in

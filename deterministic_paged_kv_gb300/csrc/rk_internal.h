@@ -222,9 +222,13 @@ struct AttnQ8Args {
     float qk_scale_log2;          // sm_scale * log2(e)
     uint32_t wait_limit_ns;
     int32_t timeout_drill;
-    // decode: splits of split_tokens keys, n_splits to a row of the scratch; with more than
-    // one, partial o / l [B, Hq, n_splits, D] and log2-domain LSE [B, Hq, n_splits]
-    int32_t split_tokens, n_splits;
+    // decode: where a row's keys are split, zones of equal splits from a token (and split) on
+    // (a zone that is not used starts at INT32_MAX); n_splits to a row of the scratch: with
+    // more than one, partial o / l [B, Hq, n_splits, D] and log2-domain LSE [B, Hq, n_splits]
+    struct {
+        int32_t split, token, size;
+    } zone[3];
+    int32_t n_splits;
     float* o_part;
     float* lse_part;
     uint64_t rope_turns[ROPE_PAIRS];

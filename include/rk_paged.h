@@ -551,11 +551,13 @@ int rk_paged_kv_append_q8(const rk_paged_plan_t *plan, int32_t n, const void *k_
 /*
  * rk_paged_attn_decode_q8 -- one query per row (plan->Sq must be 1) over the
  * 8-bit cache: q, block_table, kv_lens, position_ids, out, lse as in
- * rk_paged_attn_decode.  Every row's keys are cut at fixed logical offsets
- * s * split_tokens; the splits are reduced apart and merged in ascending order
- * in FP32 (the policy of rk_paged_attn_decode_split), so a row's result depends on
- * split_tokens and not on the batch, the table width or the grid.
- *   split_tokens  a positive multiple of 16, or 0 for RK_PAGED_Q8_SPLIT_TOKENS
+ * rk_paged_attn_decode.  Every row's keys are cut at fixed logical offsets; the
+ * splits are reduced apart and merged in FP32 in an order that the row's length alone
+ * sets (the policy of rk_paged_attn_decode_split), so a row's result depends on where
+ * it is cut and not on the batch, the table width or the grid.
+ *   split_tokens  a positive multiple of 16: splits start at its multiples; 0: at
+ *                multiples of 256 below token 1024, of 512 below 8192, of 2048
+ *                from there on
  *   scratch       DEVICE, 16-byte aligned, at least
  *                rk_paged_decode_q8_scratch_bytes bytes; nothing in it needs
  *                initialising; may be NULL where that is 0 (the table holds no
@@ -569,7 +571,6 @@ int rk_paged_kv_append_q8(const rk_paged_plan_t *plan, int32_t n, const void *k_
  * What lies past kv_len or the position is not read as a value (it may be anything).
  * Errors: as rk_paged_attn_decode_split.
  */
-#define RK_PAGED_Q8_SPLIT_TOKENS 512
 int rk_paged_decode_q8_scratch_bytes(const rk_paged_plan_t *plan, int32_t split_tokens, uint64_t *bytes);
 int rk_paged_attn_decode_q8(const rk_paged_plan_t *plan, int32_t split_tokens, const void *q,
                             const void *k_cache, const void *v_cache, const float *k_scale,
