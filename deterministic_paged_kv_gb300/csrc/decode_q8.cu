@@ -151,30 +151,16 @@ __device__ __forceinline__ void split_range(const AttnQ8Args& a, int s, int n, i
 template <int T>
 __device__ __forceinline__ int row_steps(const AttnQ8Args& a, int n) {
     if (n <= 0) return 1;
-    int sum = 0;
-#pragma unroll
-    for (int z = 0; z < 3; ++z) {
-        const int len = (z < 2 ? min(n, a.zone[z + 1].token) : n) - a.zone[z].token, size = a.zone[z].size;
-        if (len > 0) sum += len / size * ((size + T - 1) / T) + (len % size + T - 1) / T;
-    }
-    return sum;
+    const int z = n > a.zone[2].token ? 2 : n > a.zone[1].token ? 1 : 0;
+    const int len = n - a.zone[z].token, full = len / a.zone[z].size;
+    return a.zone[z].step + full * a.zone[z].steps + (len - full * a.zone[z].size + T - 1) / T;
 }
 // First split of a row that starts at its step r or later; r becomes that split's first step.
-template <int T>
 __device__ __forceinline__ int split_at(const AttnQ8Args& a, int& r) {
-    int before = 0;
-#pragma unroll
-    for (int z = 0; z < 3; ++z) {
-        const int per = (a.zone[z].size + T - 1) / T;
-        const int count = z < 2 ? a.zone[z + 1].split - a.zone[z].split : 0x7fffffff;
-        const int k = r <= before ? 0 : (r - before + per - 1) / per;
-        if (z == 2 || k < count || count > (0x7fffffff - before) / per) {
-            r = before + k * per;
-            return a.zone[z].split + k;
-        }
-        before += count * per;
-    }
-    return 0;
+    const int z = r >= a.zone[2].step ? 2 : r >= a.zone[1].step ? 1 : 0;
+    const int k = (r - a.zone[z].step + a.zone[z].steps - 1) / a.zone[z].steps;
+    r = a.zone[z].step + k * a.zone[z].steps;
+    return a.zone[z].split + k;
 }
 
 // A CTA's items: the splits whose first step, in the order of row, bundle, split, lies in the
@@ -211,7 +197,7 @@ struct DqItems {
             if (in < sr * bundles || b + 1 >= a.B) {
                 h = in / sr;
                 int r = in % sr;
-                s = split_at<T>(a, r);
+                s = split_at(a, r);
                 at = base + h * sr + min(r, sr);
                 if (s >= ns) wrap(a, bundles);
                 return;
@@ -332,12 +318,15 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             __syncthreads();
             if (lane == 31) c->scan[warp] = v;
             __syncthreads();
-            int before = base;
-            for (int w = 0; w < DQ_THREADS / 32; ++w) {
-                const int x = c->scan[w];
-                before += w < warp ? x : 0;
-                base += x;
+            int x = lane < DQ_THREADS / 32 ? c->scan[lane] : 0;
+            const int own = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += t;
             }
+            const int before = base + __shfl_sync(0xffffffffu, x - own, warp);
+            base += __shfl_sync(0xffffffffu, x, 31);
             if (gr < groups) c->pre[gr] = before + v - cnt;
         }
         if (tid == 0) c->total = base;
@@ -678,14 +667,14 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             ++done;
         };
         // the first queries, a head to a warp
+        wait(c->id_full[0], 0);
         {
-            Items it;
-            it.start(a, c, bundles);
-            if (it.valid(a)) {
+            const int qrow = c->step[0].b, qh = c->step[0].h;
+            if (ok && !(c->step[0].flags & DQ_END)) {
                 constexpr int N = H * G;
                 float c0, s0, c1, s1;
-                const uint32_t pos = (uint32_t)max(0, a.position_ids[it.b]);
-                const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + ((size_t)it.b * a.Hq + it.h * N) * (HEAD_DIM / 2) + lane;
+                const uint32_t pos = (uint32_t)max(0, a.position_ids[qrow]);
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q) + ((size_t)qrow * a.Hq + qh * N) * (HEAD_DIM / 2) + lane;
 #pragma unroll 1
                 for (int i = sw; i < N; i += 16) {
                     const uint32_t wl = __ldg(q + i * 64), wh = __ldg(q + i * 64 + 32);
@@ -930,13 +919,14 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
 // Merge of the split partials of one (row, query head): weights 2^(lse_s - max lse), eight
 // sums over the splits s = e, e + 8, ... in ascending order, added up in order of e: fixed by
 // the row's split count alone.  A lane has four dims.  A NaN partial fails the row, no visible
-// key gives out = 0, lse = -inf.  WARPS = 1: a warp has all eight sums (one round of loads for
-// up to eight splits, four rows to a block); 8: a warp has one, for long rows.  Both add in the
-// same order, so which one runs (a choice by the table's width) does not show in the result.
-// Bound by latency: length of the row, a round of loads, one of stores.
+// key gives out = 0, lse = -inf.  WARPS = 1: a warp has all eight sums (four rows to a
+// block); 8: a warp has one, for long rows.  Both add in the same order, so which one runs (a
+// choice by the table's width) does not show in the result.  Bound by latency: the row's
+// length, a round of loads of AHEAD splits a sum (for long rows two rounds at a time took
+// 10 us and more of 2 rows of 114 splits), one of stores.
 template <int WARPS>
 __global__ void __launch_bounds__(WARPS == 1 ? 128 : 256) merge_q8_kernel(const __grid_constant__ AttnQ8Args a) {
-    constexpr int SUMS = 8 / WARPS;
+    constexpr int SUMS = 8 / WARPS, AHEAD = WARPS == 1 ? 1 : 8;
     __shared__ float4 acc_s[WARPS == 1 ? 1 : 8][32];
     __shared__ float sum_s[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -949,13 +939,19 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 256) merge_q8_kernel(const 
     const float* lp = a.lse_part + bh * a.n_splits;
     const float4* op = reinterpret_cast<const float4*>(a.o_part + bh * a.n_splits * HEAD_DIM) + lane;
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float4 x[SUMS];
-    float wt[SUMS];
+    float4 x[AHEAD][SUMS];
+    float wt[AHEAD][SUMS];
+    auto load = [&](int s0) {  // AHEAD rounds of eight splits from s0 on
 #pragma unroll
-    for (int e = 0; e < SUMS; ++e) {
-        x[e] = e0 + e < ns ? op[(size_t)(e0 + e) * 32] : zero;
-        wt[e] = e0 + e < ns ? lp[e0 + e] : -INFINITY;
-    }
+        for (int r = 0; r < AHEAD; ++r)
+#pragma unroll
+            for (int e = 0; e < SUMS; ++e) {
+                const int s = s0 + 8 * r + e0 + e;
+                x[r][e] = s < ns ? op[(size_t)s * 32] : zero;
+                wt[r][e] = s < ns ? lp[s] : -INFINITY;
+            }
+    };
+    load(0);
     float m = -INFINITY;
     bool bad = false;
     for (int s = lane; s < ns; s += 32) {
@@ -980,26 +976,20 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 256) merge_q8_kernel(const 
         acc[e] = zero;
         sum[e] = 0.0f;
     }
-    for (int s0 = 0; s0 < ns; s0 += 8) {
-        float4 nx[SUMS];
-        float nw[SUMS];
+    for (int s0 = 0; s0 < ns;) {
 #pragma unroll
-        for (int e = 0; e < SUMS; ++e) {  // the next round's loads
-            const int s = s0 + 8 + e0 + e;
-            nx[e] = s < ns ? op[(size_t)s * 32] : zero;
-            nw[e] = s < ns ? lp[s] : -INFINITY;
-        }
+        for (int r = 0; r < AHEAD; ++r)
 #pragma unroll
-        for (int e = 0; e < SUMS; ++e) {
-            const float w = ex2(wt[e] - m);
-            sum[e] += w;
-            acc[e].x = fmaf(w, x[e].x, acc[e].x);
-            acc[e].y = fmaf(w, x[e].y, acc[e].y);
-            acc[e].z = fmaf(w, x[e].z, acc[e].z);
-            acc[e].w = fmaf(w, x[e].w, acc[e].w);
-            x[e] = nx[e];
-            wt[e] = nw[e];
-        }
+            for (int e = 0; e < SUMS; ++e) {
+                const float w = ex2(wt[r][e] - m);
+                sum[e] += w;
+                acc[e].x = fmaf(w, x[r][e].x, acc[e].x);
+                acc[e].y = fmaf(w, x[r][e].y, acc[e].y);
+                acc[e].z = fmaf(w, x[r][e].z, acc[e].z);
+                acc[e].w = fmaf(w, x[r][e].w, acc[e].w);
+            }
+        s0 += 8 * AHEAD;
+        if (s0 < ns) load(s0);
     }
     float4 r = acc[0];
     float l = sum[0];
@@ -1077,7 +1067,7 @@ cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const
     e = launch_any(a.G, bundle, km, vm, a, grid, stream, false);
     if (e != cudaSuccess || a.n_splits <= 1) return e;
     const long long rows = (long long)a.B * a.Hq;
-    const bool few = a.n_splits <= 16;  // 64 x 4096 (10 splits): a warp each; from some tens of splits on eight share one
+    const bool few = a.n_splits <= 32;  // 64 x 4096 (10 splits): a warp each; from some tens of splits on eight share one
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(few ? (rows + 3) / 4 : rows));
     cfg.blockDim = dim3(few ? 128 : 256);

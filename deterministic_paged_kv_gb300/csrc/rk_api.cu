@@ -955,17 +955,23 @@ int attn_q8_args(const rk_paged_plan_t* plan, const void* q, const void* k_cache
 // Split geometry of the 8-bit decode.  split_tokens = 0: short splits where a row starts
 // (a short row then has several CTAs at work), longer ones further on (fewer partial
 // results of a long row); which token is in which split never depends on the row's length.
-int q8_zones(int32_t split_tokens, rk::AttnQ8Args* a) {
+int q8_zones(const rk_paged_plan_t* plan, int32_t split_tokens, rk::AttnQ8Args* a) {
     if (split_tokens < 0 || split_tokens % rk::PAGE != 0)
         return fail(RK_E_ARG, "split_tokens must be 0 or a positive multiple of %d (got %d)", rk::PAGE, split_tokens);
     const int32_t far = INT32_MAX;
     if (split_tokens > 0) {
-        a->zone[0] = {0, 0, split_tokens};
-        a->zone[1] = a->zone[2] = {far, far, split_tokens};
+        a->zone[0] = {0, 0, split_tokens, 0, 0};
+        a->zone[1] = a->zone[2] = {far, far, split_tokens, far, 0};
     } else {
-        a->zone[0] = {0, 0, 256};
-        a->zone[1] = {4, 1024, 512};
-        a->zone[2] = {18, 8192, 2048};
+        a->zone[0] = {0, 0, 256, 0, 0};
+        a->zone[1] = {4, 1024, 512, 0, 0};
+        a->zone[2] = {18, 8192, 2048, 0, 0};
+    }
+    const int32_t step_tokens = 512 / rk::decode_q8_bundle(plan->Hkv);
+    for (int z = 0; z < 3; ++z) {
+        a->zone[z].steps = (a->zone[z].size + step_tokens - 1) / step_tokens;
+        if (z > 0 && a->zone[z].split != far)
+            a->zone[z].step = a->zone[z - 1].step + (a->zone[z].split - a->zone[z - 1].split) * a->zone[z - 1].steps;
     }
     return RK_OK;
 }
@@ -1070,7 +1076,7 @@ int rk_paged_decode_q8_scratch_bytes(const rk_paged_plan_t* plan, int32_t split_
     if (!plan || !bytes) return fail(RK_E_ARG, "plan and bytes must be non-null");
     if (plan->abi != RK_PAGED_ABI_VERSION) return fail(RK_E_ARG, "plan ABI %u != %u", plan->abi, RK_PAGED_ABI_VERSION);
     rk::AttnQ8Args a;
-    int rc = q8_zones(split_tokens, &a);
+    int rc = q8_zones(plan, split_tokens, &a);
     if (rc) return rc;
     *bytes = (uint64_t)q8_scratch_need(plan, q8_split_count(plan, a));
     return RK_OK;
@@ -1085,7 +1091,7 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t* plan, int32_t split_tokens, c
     if (rc) return rc;
     if (plan->Sq != 1) return fail(RK_E_ARG, "decode needs a plan with Sq == 1 (got %d)", plan->Sq);
     rk::AttnQ8Args a;
-    if ((rc = q8_zones(split_tokens, &a))) return rc;
+    if ((rc = q8_zones(plan, split_tokens, &a))) return rc;
     const int64_t splits = q8_split_count(plan, a);
     // steps and items are counted in 32 bits
     if ((double)plan->B * plan->Hkv * ((double)plan->W + (double)splits) > 2147483647.0)
@@ -1102,7 +1108,7 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t* plan, int32_t split_tokens, c
     rc = attn_q8_args(plan, q, k_cache, v_cache, k_scale, v_scale, block_table_d, kv_lens_d, position_ids_d, out, lse, status_d,
                       &a);
     if (rc || plan->B == 0) return rc;
-    q8_zones(split_tokens, &a);
+    q8_zones(plan, split_tokens, &a);
     a.n_splits = (int32_t)splits;
     a.o_part = static_cast<float*>(scratch);
     if (need > 0) a.lse_part = a.o_part + (int64_t)plan->B * plan->Hq * a.n_splits * rk::HEAD_DIM;
