@@ -1,0 +1,723 @@
+// prefill_q8.cu -- causal chunked prefill over the 8-bit page cache (tcgen05, TMA).
+//
+// Operation: the paged prefill of "WS2 PR7 Fused Attention Backend Alignment",
+// "Current Implementation", over e4m3 codes whose K was rotated when it was written.
+// Work units (two q-tiles of one row and KV head), their heaviest-first order, the
+// persistent grid and the online softmax are those of the BF16 prefill kernel.
+//
+// What is different is what the operands are:
+//   scores   K goes from the cache into the MMA as it is (e4m3); q, rotated and scaled to
+//            below 362 by a power of two per query, is three e4m3 parts, added up in the
+//            FP32 accumulator: 12 MMAs of K = 32 for 8 of FP16 (768 cycles of the tensor
+//            pipe for 512), but no K tile is rewritten, and a score keeps q to 2^-12 at
+//            worst and 2^-16 on average, where one FP16 operand keeps 2^-12.3 on average
+//            (0.0002 off the LSE of a query that sees one key).
+//   P V      V is converted to FP16 (exact) by the transform warpgroup; P is FP16, scaled to
+//            at most 2^15 (it keeps 2^-11 of a weight down to 2^-21 of the largest).
+//            (P as two e4m3 parts would take as many tensor cycles and put the splitting on
+//            the softmax, which sets the pace.)
+//   scales   a page's scales are constants of 16 columns: the softmax folds K's into its
+//            multiplier and V's into the exponent, w = z + log2(vs), and divides the row sum's
+//            page partials by vs: some 40 instructions of 600 a tile and row.
+// What bounds it: the chain softmax -> PV -> S of each q-tile (two q-tiles overlap), then the
+// tensor pipe, 2560 cycles a pair of q-tiles and KV tile.
+//
+// Roles (512 threads, registers rebalanced with setmaxnreg):
+//   warp 15      scheduler: each unit's metadata, published as a descriptor (two slots);
+//   warpgroup 0  transform: q of both q-tiles of a unit as e4m3 parts (as soon as the unit
+//                before has read its own), V tiles to FP16 (zeros past the last key);
+//   warpgroups 1, 2  softmax of q-tile 0, 1: a thread per accumulator row;
+//   warp 12      K producer: K tiles by TMA, the pages' scales;
+//   warp 14      V producer: V tiles by TMA (codes);
+//   warp 13      MMA issuer (converged).
+// Nothing depends on B, W or the grid.
+#include <atomic>
+
+#include "q8_device.cuh"
+
+namespace rk {
+
+namespace {
+
+constexpr int PQ_THREADS = 512;
+constexpr int WARP_K = 12, WARP_MMA = 13, WARP_V = 14, WARP_SCHED = 15;
+constexpr int PQ_PARTS = 3;
+constexpr int PQ_CODES = PF_BN * HEAD_DIM;      // a tile of codes: 16 KiB
+constexpr int KST = 2, VST = 2;                 // K stages, V stages (codes and FP16)
+constexpr int SCST = 4;                         // scale slots: one more than K stages at least
+constexpr uint32_t TMEM_COLS = 512;             // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512)
+constexpr float RESCALE_SLACK = 8.0f, P_BIAS = 7.0f;
+constexpr uint32_t UNIT_READERS = 3 * 32 + 128 + 256;
+
+// setmaxnreg split (sum 4 x 128 = the 512 x 128 registers the CTA launches with)
+constexpr int REG_XFORM = 88, REG_SOFTMAX = 184, REG_CTRL = 56;
+static_assert(REG_XFORM + 2 * REG_SOFTMAX + REG_CTRL == 4 * 128, "register split must sum to the launch budget");
+
+constexpr int OFF_Q = 0;                                     // [q-tile][part][128 rows][128 B]
+constexpr int OFF_K = OFF_Q + 2 * PQ_PARTS * PQ_CODES;
+constexpr int OFF_VC = OFF_K + KST * PQ_CODES;               // V codes
+constexpr int OFF_V = OFF_VC + VST * PQ_CODES;               // V FP16, [page][64-dim half][16 rows][128 B]
+constexpr int OFF_BAR = OFF_V + VST * PF_TILE_BYTES;
+
+struct PqUnit {
+    int end, b, kvh, pair;
+    int kv_len, nt0, nt1, n_keys;  // keys, KV tiles of q-tile 0 / 1, keys that the pair reads
+    int bad;
+};
+
+struct PqBars {
+    uint64_t q_ready[2], q_empty;
+    uint64_t k_full[KST], k_empty[KST], sc_full[SCST];
+    uint64_t c_full[VST], c_empty[VST];  // V codes
+    uint64_t v_full[VST], v_empty[VST];  // V FP16
+    uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
+    uint64_t u_full[2], u_empty[2];
+    uint64_t r_full[2], r_empty[2];      // a unit's verdict: transform threads and K producer -> softmax
+    uint64_t never;
+    uint32_t tmem_base;
+    PipeCtl pipe;
+    PqUnit unit[2];
+    alignas(16) uint8_t r_flag[2][144];  // [0, 128) NaN code in V; [128] a scale that is none
+    alignas(16) float4 sc[SCST][PF_PAGES_PER_TILE];  // k scale, log2 of v's, 1 / v's
+    float qscale[2][PF_BM];              // score factor of each query (log2 domain); NaN: out of range
+};
+constexpr int PQ_SMEM_BYTES = OFF_BAR + (int)sizeof(PqBars);
+static_assert(PQ_SMEM_BYTES <= 232448, "8-bit prefill shared memory above the 227 KiB opt-in limit");
+
+// Unit k of this CTA in the heaviest-first order (positions c, 2 G - 1 - c, 2 G + c, ...).
+__device__ __forceinline__ long long cta_unit(int k, int c, int g) {
+    return (k & 1) ? (long long)(k + 1) * g - 1 - c : (long long)k * g + c;
+}
+__device__ __forceinline__ void unit_place(const AttnQ8Args& a, int n_qtiles, long long u, int& b, int& kvh, int& pair) {
+    const int units = a.B * a.Hkv;
+    pair = (n_qtiles + 1) / 2 - 1 - (int)(u / units);
+    const int rem = (int)(u % units);
+    b = rem / a.Hkv;
+    kvh = rem % a.Hkv;
+}
+
+// Row r of a q-tile from query s0 on: query head kvh * G + r / rph, query s0 + r % rph.
+__device__ __forceinline__ size_t query_row(const AttnQ8Args& a, int b, int kvh, int rph, int s0, int r) {
+    return ((size_t)b * a.Hq + kvh * a.G + r / rph) * a.Sq + s0 + r % rph;
+}
+
+__device__ __forceinline__ void write_row(const AttnQ8Args& a, size_t row, float lse) {
+    uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + row * HEAD_DIM);
+#pragma unroll 1
+    for (int d = 0; d < HEAD_DIM / 8; ++d) o[d] = make_uint4(0, 0, 0, 0);
+    a.lse[row] = lse;
+}
+
+// Unit k's metadata checks (one warp): kv_len, positions (the largest of each q-tile sets
+// the keys it reads), every page id of the row's keys.
+__device__ __forceinline__ PqUnit unit_meta(const AttnQ8Args& a, int n_qtiles, int rph, int k, int cta, int grid, long long total,
+                                            int lane) {
+    PqUnit d;
+    d.b = d.kvh = d.pair = d.kv_len = d.nt0 = d.nt1 = d.n_keys = d.bad = 0;
+    const long long u = cta_unit(k, cta, grid);
+    d.end = u >= total;
+    if (d.end) return d;
+    unit_place(a, n_qtiles, u, d.b, d.kvh, d.pair);
+    const int kv_len = a.kv_lens[d.b];
+    int bad = (kv_len < 0 || kv_len > a.W * PAGE) ? RK_STATUS_KVLEN : 0;
+    const int32_t* pos = a.position_ids + (size_t)d.b * a.Sq;
+    const int s00 = 2 * d.pair * rph;
+    int pm0 = -1, pm1 = -1, neg = 0;
+#pragma unroll 1
+    for (int r = lane; r < rph; r += 32) {
+        if (s00 + r < a.Sq) {
+            const int p = pos[s00 + r];
+            neg |= p < 0;
+            pm0 = max(pm0, p);
+        }
+        if (s00 + rph + r < a.Sq) {
+            const int p = pos[s00 + rph + r];
+            neg |= p < 0;
+            pm1 = max(pm1, p);
+        }
+    }
+    pm0 = __reduce_max_sync(0xffffffffu, pm0);
+    pm1 = __reduce_max_sync(0xffffffffu, pm1);
+    if (__reduce_or_sync(0xffffffffu, (unsigned)neg)) bad |= RK_STATUS_POSITION;
+    const int row_pages = (bad & RK_STATUS_KVLEN) ? 0 : (kv_len + PAGE - 1) / PAGE;
+    const int32_t* bt = a.block_table + (size_t)d.b * a.W;
+    int oob = 0;
+#pragma unroll 4
+    for (int i = lane; i < row_pages; i += 32) {
+        const int pg = __ldg(bt + i);
+        oob |= (pg < 0) | (pg >= a.num_pages);
+    }
+    if (__reduce_or_sync(0xffffffffu, (unsigned)oob)) bad |= RK_STATUS_PAGE_OOB;
+    const int nk0 = (bad || pm0 < 0) ? 0 : (pm0 >= kv_len ? kv_len : pm0 + 1);
+    const int nk1 = (bad || pm1 < 0) ? 0 : (pm1 >= kv_len ? kv_len : pm1 + 1);
+    d.kv_len = kv_len;
+    d.nt0 = (nk0 + PF_BN - 1) / PF_BN;
+    d.nt1 = (nk1 + PF_BN - 1) / PF_BN;
+    d.n_keys = max(nk0, nk1);
+    d.bad = bad;
+    return d;
+}
+
+__device__ __forceinline__ bool read_unit(PqBars* bars, int k, PipeCtl* pc, PqUnit& u) {
+    const int slot = k & 1;
+    if (!mbar_wait(smem_u32(&bars->u_full[slot]), (uint32_t)((k >> 1) & 1), pc)) return false;
+    const volatile PqUnit* src = &bars->unit[slot];
+    u.end = src->end;
+    u.b = src->b;
+    u.kvh = src->kvh;
+    u.pair = src->pair;
+    u.kv_len = src->kv_len;
+    u.nt0 = src->nt0;
+    u.nt1 = src->nt1;
+    u.n_keys = src->n_keys;
+    u.bad = src->bad;
+    mbar_arrive(smem_u32(&bars->u_empty[slot]));
+    return true;
+}
+
+__global__ void __launch_bounds__(PQ_THREADS, 1)
+    prefill_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const __grid_constant__ AttnQ8Args a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw;
+    PqBars* bars = reinterpret_cast<PqBars*>(sm + OFF_BAR);
+    const uint32_t s_base = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+    const int rph = PF_BM / a.G, n_qtiles = (a.Sq + rph - 1) / rph;
+    const int cta = (int)blockIdx.x, grid = (int)gridDim.x;
+    const long long total = (long long)a.B * a.Hkv * ((n_qtiles + 1) / 2);
+    PqUnit first{};
+    if (warp == WARP_SCHED) first = unit_meta(a, n_qtiles, rph, 0, cta, grid, total, lane);
+    if (tid == 0) {
+        bars->pipe.abort = 0;
+        bars->pipe.limit_ns = wait_limit(a.wait_limit_ns);
+        mbar_init(smem_u32(&bars->never), 1);
+        mbar_init(smem_u32(&bars->q_empty), 1);
+        for (int k = 0; k < KST; ++k) {
+            mbar_init(smem_u32(&bars->k_full[k]), 1);
+            mbar_init(smem_u32(&bars->k_empty[k]), 1);
+        }
+        for (int k = 0; k < SCST; ++k) mbar_init(smem_u32(&bars->sc_full[k]), 1);
+        for (int k = 0; k < VST; ++k) {
+            mbar_init(smem_u32(&bars->c_full[k]), 1);
+            mbar_init(smem_u32(&bars->c_empty[k]), 128);
+            mbar_init(smem_u32(&bars->v_full[k]), 128);
+            mbar_init(smem_u32(&bars->v_empty[k]), 1);
+        }
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(smem_u32(&bars->q_ready[j]), 128);
+            mbar_init(smem_u32(&bars->s_full[j]), 1);
+            mbar_init(smem_u32(&bars->p_ready[j]), 128);
+            mbar_init(smem_u32(&bars->o_done[j]), 1);
+            mbar_init(smem_u32(&bars->o_free[j]), 128);
+            mbar_init(smem_u32(&bars->u_full[j]), 1);
+            mbar_init(smem_u32(&bars->u_empty[j]), UNIT_READERS);
+            mbar_init(smem_u32(&bars->r_full[j]), 129);
+            mbar_init(smem_u32(&bars->r_empty[j]), 256);
+        }
+        fence_mbar_init();
+    }
+    for (int i = tid; i < (int)sizeof(bars->r_flag) / 4; i += PQ_THREADS) reinterpret_cast<uint32_t*>(&bars->r_flag[0][0])[i] = 0;
+    if (warp == WARP_MMA) {
+        tmem_alloc(smem_u32(&bars->tmem_base), TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    PipeCtl* pc = &bars->pipe;
+
+    if (wg == 3) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_CTRL));
+        if (warp == WARP_SCHED) {
+            // ============================================== scheduler ====
+            bool ok = true;
+#pragma unroll 1
+            for (int k = 0; ok; ++k) {
+                const int slot = k & 1;
+                const PqUnit m = k == 0 ? first : unit_meta(a, n_qtiles, rph, k, cta, grid, total, lane);
+                ok = __shfl_sync(0xffffffffu,
+                                 lane == 0 ? (int)mbar_wait(smem_u32(&bars->u_empty[slot]), (uint32_t)(((k >> 1) & 1) ^ 1), pc) : 0,
+                                 0) != 0;
+                if (!ok) break;
+                if (lane == 0) {
+                    bars->unit[slot] = m;
+                    if (m.bad && a.status) atomicOr(a.status, m.bad);
+                    mbar_arrive(smem_u32(&bars->u_full[slot]));
+                }
+                if (m.end) break;
+            }
+        } else if (warp == WARP_K || warp == WARP_V) {
+            // ============================================== producers ====
+            // lane p: page p of a tile.  n: tiles over the CTA's units.
+            const bool is_k = warp == WARP_K;
+            const CUtensorMap* map = is_k ? &kmap : &vmap;
+            if (lane == 0) prefetch_tmap(map);
+            constexpr int nst = KST;
+            static_assert(KST == VST, "one stage count for both producers");
+            int n = 0, wu = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int k = 0; ok; ++k) {
+                PqUnit u;
+                if (!(ok = __all_sync(0xffffffffu, read_unit(bars, k, pc, u))) || u.end) break;
+                const int n_tiles = max(u.nt0, u.nt1);
+                if (u.bad || n_tiles == 0) continue;
+                const int32_t* bt = a.block_table + (size_t)u.b * a.W;
+                const int n_pages = (u.n_keys + PAGE - 1) / PAGE;
+                int pg = lane < min(PF_PAGES_PER_TILE, n_pages) ? __ldg(bt + lane) : 0;
+                bool odd = false;
+#pragma unroll 1
+                for (int i = 0; i < n_tiles; ++i, ++n) {
+                    const int st = n % nst, p0 = i * PF_PAGES_PER_TILE, np = min(PF_PAGES_PER_TILE, n_pages - p0);
+                    const uint32_t eb = smem_u32(is_k ? &bars->k_empty[st] : &bars->c_empty[st]);
+                    const uint32_t fb = smem_u32(is_k ? &bars->k_full[st] : &bars->c_full[st]);
+                    int good = 1;
+                    if (lane == 0) {
+                        good = mbar_wait(eb, (uint32_t)(((n / nst) & 1) ^ 1), pc);
+                        if (good) mbar_arrive_expect_tx(fb, (uint32_t)np * Q8_BLOCK_BYTES);
+                    }
+                    if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
+                    const uint32_t dst = s_base + (is_k ? OFF_K : OFF_VC) + st * PQ_CODES;
+#pragma unroll 1
+                    for (int p = 0; p < np; ++p)
+                        tma_load_5d_elect(dst + p * Q8_BLOCK_BYTES, map, fb, 0, 0, u.kvh, 0, __shfl_sync(0xffffffffu, pg, p));
+                    const int cur = pg;
+                    if (i + 1 < n_tiles) pg = lane < min(PF_PAGES_PER_TILE, n_pages - p0 - 8) ? __ldg(bt + p0 + 8 + lane) : 0;
+                    if (is_k) {
+                        // The slot's reader of SCST tiles ago is done: the stage of K was free, so S of tile
+                        // n - KST is, and with it the softmax of the tile before that.
+                        float ks = 1.0f, vs = 1.0f;
+                        if (lane < np) {
+                            const size_t block = (size_t)cur * a.Hkv + u.kvh;
+                            ks = __ldg(a.k_scale + block);
+                            vs = __ldg(a.v_scale + block);
+                        }
+                        if (!scale_ok(ks) || !scale_ok(vs)) {
+                            odd = true;
+                            ks = vs = 1.0f;
+                        }
+                        if (lane < PF_PAGES_PER_TILE) bars->sc[n % SCST][lane] = make_float4(ks, __log2f(vs), rcp(vs), 0.0f);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&bars->sc_full[n % SCST]));
+                    }
+                }
+                if (!ok) break;
+                if (is_k) {
+                    odd = __any_sync(0xffffffffu, odd);
+                    const int slot = wu & 1;
+                    int good = 1;
+                    if (lane == 0) {
+                        good = mbar_wait(smem_u32(&bars->r_empty[slot]), (uint32_t)(((wu >> 1) & 1) ^ 1), pc);
+                        if (good) {
+                            bars->r_flag[slot][128] = odd ? 1 : 0;
+                            mbar_arrive(smem_u32(&bars->r_full[slot]));
+                        }
+                    }
+                    if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
+                    ++wu;
+                }
+            }
+            if (lane == 0 && pipe_aborted(pc))  // copies in flight land before the CTA's shared memory is released
+                for (int i = max(0, n - nst); i < n; ++i)
+                    mbar_wait_drain(smem_u32(is_k ? &bars->k_full[i % nst] : &bars->c_full[i % nst]), (uint32_t)((i / nst) & 1));
+        } else {
+            // ============================================= MMA issuer ====
+            constexpr uint32_t idS = idesc_e4m3_f32(PF_BM, PF_BN, 0, 0);
+            constexpr uint32_t idO = idesc_f16_f32(PF_BM, HEAD_DIM) | (1u << 16);  // FP16, V MN-major
+            const uint32_t dQ = desc_lo(s_base + OFF_Q, 16), dK = desc_lo(s_base + OFF_K, 16), dV = desc_lo(s_base + OFF_V, 2048);
+            constexpr uint32_t TILE8 = PQ_CODES >> 4, TILE16 = PF_TILE_BYTES >> 4;
+            // g0: KV tiles before the unit; ph bit 0 work units, bits 2 + j s_full / p_ready of
+            // q-tile j, bits 4 + j o_free
+            int g0 = 0;
+            uint32_t ph = 0;
+            auto wait = [&](uint64_t& bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), parity & 1u, pc)) != 0;
+            };
+            bool ok = !a.timeout_drill || __all_sync(0xffffffffu, drill_wait(smem_u32(&bars->never), pc));
+#pragma unroll 1
+            for (int kk = 0; ok; ++kk) {
+                PqUnit u;
+                if (!(ok = __all_sync(0xffffffffu, read_unit(bars, kk, pc, u))) || __any_sync(0xffffffffu, u.end)) break;
+                const int nt0 = __shfl_sync(0xffffffffu, u.nt0, 0), nt1 = __shfl_sync(0xffffffffu, u.nt1, 0);
+                const int n_tiles = max(nt0, nt1);
+                if (__any_sync(0xffffffffu, u.bad != 0) || n_tiles == 0) continue;
+                // O_j (+)= P_j(i) V(i); the unit's first PV into O_j waits for the epilogue before it
+                auto issue_pv = [&](int j, int i) -> bool {
+                    const int g = g0 + i;
+                    if (i == 0 && !wait(bars->o_free[j], (ph >> (4 + j)) ^ 1u)) return false;
+                    if (!wait(bars->v_full[g % VST], (uint32_t)(g / VST))) return false;
+                    if (!wait(bars->p_ready[j], (ph >> (2 + j)) ^ (uint32_t)i)) return false;
+                    tc_fence_after();
+                    mma_ts_steps<0, 8, MN_MAJOR_PAGE, true>(tmem + 256 + j * 128, tmem + j * 128, dV + (uint32_t)(g % VST) * TILE16, idO,
+                                                            i > 0 ? 1u : 0u);
+                    return true;
+                };
+#pragma unroll 1
+                for (int i = 0; i < n_tiles && ok; ++i) {
+                    const int g = g0 + i;
+#pragma unroll 1
+                    for (int j = 0; j < 2 && ok; ++j) {
+                        const int nt = j ? nt1 : nt0;
+                        if (i > nt || nt == 0) continue;
+                        if (i > 0 && !(ok = issue_pv(j, i - 1))) break;
+                        if (i == nt) {
+                            umma_commit_elect(smem_u32(&bars->o_done[j]));
+                            continue;
+                        }
+                        if (i == 0 && !(ok = wait(bars->q_ready[j], ph))) break;
+                        if (!(ok = wait(bars->k_full[g % KST], (uint32_t)(g / KST)))) break;
+                        tc_fence_after();
+                        const uint32_t d = tmem + j * 128, dk = dK + (uint32_t)(g % KST) * TILE8, dq = dQ + (uint32_t)(j * PQ_PARTS) * TILE8;
+#pragma unroll
+                        for (int p = 0; p < PQ_PARTS; ++p)
+                            mma_f8_x4<2, 2>(d, dq + p * TILE8, dk, DESC_HI, DESC_HI, idS, p > 0, 4);
+                        umma_commit_elect(smem_u32(&bars->s_full[j]));
+                    }
+                    if (!ok) break;
+                    umma_commit_elect(smem_u32(&bars->k_empty[g % KST]));                       // K(i) read by S(i)
+                    if (i > 0) umma_commit_elect(smem_u32(&bars->v_empty[(g - 1) % VST]));      // V(i-1) read by PV(i-1)
+                    if (i == n_tiles - 1) umma_commit_elect(smem_u32(&bars->q_empty));          // the unit's last S read q
+                }
+#pragma unroll 1
+                for (int j = 0; j < 2 && ok; ++j) {
+                    if ((j ? nt1 : nt0) != n_tiles) continue;
+                    if (!(ok = issue_pv(j, n_tiles - 1))) break;
+                    umma_commit_elect(smem_u32(&bars->o_done[j]));
+                }
+                if (!ok) break;
+                umma_commit_elect(smem_u32(&bars->v_empty[(g0 + n_tiles - 1) % VST]));
+                ph ^= 1u | ((uint32_t)(nt0 & 1) << 2) | ((uint32_t)(nt1 & 1) << 3) | (nt0 > 0 ? 16u : 0u) | (nt1 > 0 ? 32u : 0u);
+                g0 += n_tiles;
+            }
+            if (!ok) {  // issued MMAs drain before tensor memory is released
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000000ull) {
+                }
+            }
+        }
+        __syncwarp();
+        named_bar_sync(2, PQ_THREADS);
+    } else if (wg == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_XFORM));
+        // ================================================ transform WG ====
+        int g0 = 0, wu = 0;  // KV tiles before the unit, work units
+        bool ok = true;
+#pragma unroll 1
+        for (int kk = 0; ok; ++kk) {
+            PqUnit u;
+            if (!(ok = read_unit(bars, kk, pc, u)) || u.end) break;
+            const int n_tiles = max(u.nt0, u.nt1);
+            if (u.bad || n_tiles == 0) continue;
+            // ---- q: thread r rotates row r of both q-tiles and splits it into parts ----
+            if (!(ok = mbar_wait(smem_u32(&bars->q_empty), (uint32_t)((wu & 1) ^ 1), pc))) break;
+#pragma unroll 1
+            for (int j = 0; j < 2; ++j) {
+                const int s0 = (2 * u.pair + j) * rph, s = s0 + tid % rph;
+                const bool valid = s < a.Sq;
+                const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
+                                                                (valid ? query_row(a, u.b, u.kvh, rph, s0, tid) : 0) * HEAD_DIM);
+                const uint32_t pos = valid ? (uint32_t)a.position_ids[(size_t)u.b * a.Sq + s] : 0;
+                uint32_t m = 0;
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    const uint4 w = __ldg(q + i);
+                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+                }
+                m = max(m & 0xffffu, m >> 16);
+                const bool bad = m >= Q8_LIMIT_BF16, zero = bad || !valid;
+                const int e = zero ? 0 : q8_exponent(m);
+                const float inv = pow2(-e);
+                bars->qscale[j][tid] = bad && valid ? __int_as_float(0x7fc00000) : a.qk_scale_log2 * pow2(e);
+                uint8_t* qt = sm + OFF_Q + j * PQ_PARTS * PQ_CODES;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {  // pairs 8 c .. 8 c + 7: dims 8 c .. and 64 + 8 c ..
+                    const uint4 lo = __ldg(q + c), hi = __ldg(q + 8 + c);
+                    const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+                    uint32_t pl[PQ_PARTS][2] = {}, ph[PQ_PARTS][2] = {};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float c0, n0, c1, n1;
+                        rope_cos_sin(pos, a.rope_turns[8 * c + 2 * i], c0, n0);
+                        rope_cos_sin(pos, a.rope_turns[8 * c + 2 * i + 1], c1, n1);
+                        const float2 l = make_float2(bf16lo(lw[i]) * inv, bf16hi(lw[i]) * inv);
+                        const float2 h = make_float2(bf16lo(hw[i]) * inv, bf16hi(hw[i]) * inv);
+                        float2 x = make_float2(l.x * c0 - h.x * n0, l.y * c1 - h.y * n1);
+                        float2 y = make_float2(h.x * c0 + l.x * n0, h.y * c1 + l.y * n1);
+                        if (zero) x = y = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int p = 0; p < PQ_PARTS; ++p) {
+                            pl[p][i >> 1] |= take_part(x) << (16 * (i & 1));
+                            ph[p][i >> 1] |= take_part(y) << (16 * (i & 1));
+                        }
+                    }
+#pragma unroll
+                    for (int p = 0; p < PQ_PARTS; ++p) {
+                        const uint32_t at = p * PQ_CODES + sw128_off(tid, c >> 1) + (c & 1) * 8;
+                        *reinterpret_cast<uint2*>(qt + at) = make_uint2(pl[p][0], pl[p][1]);
+                        *reinterpret_cast<uint2*>(qt + (at ^ 64)) = make_uint2(ph[p][0], ph[p][1]);  // chunk + 4
+                    }
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(&bars->q_ready[j]));
+            }
+            // ---- V tiles: thread t has 16 codes (chunk c) of every 16th token ----
+            uint32_t nan = 0;
+            const int c = tid & 7, r0 = tid >> 3;
+#pragma unroll 1
+            for (int i = 0; i < n_tiles; ++i) {
+                const int g = g0 + i, st = g % VST;
+                if (!(ok = mbar_wait(smem_u32(&bars->c_full[st]), (uint32_t)((g / VST) & 1), pc))) break;
+                if (!(ok = mbar_wait(smem_u32(&bars->v_empty[st]), (uint32_t)(((g / VST) & 1) ^ 1), pc))) break;
+                const uint8_t* vc = sm + OFF_VC + st * PQ_CODES;
+                uint8_t* vt = sm + OFF_V + st * PF_TILE_BYTES;
+                uint4 w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int t = r0 + 16 * e;
+                    w[e] = i * PF_BN + t < u.n_keys ? *reinterpret_cast<const uint4*>(vc + sw128_off(t, c)) : make_uint4(0, 0, 0, 0);
+                }
+                mbar_arrive(smem_u32(&bars->c_empty[st]));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // token r0 + 16 e: row r0 of page e; 16 codes: two 16-byte chunks of its half
+                    const uint32_t cw[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[2 * k] = e4m3x2_to_f16x2(cw[k]);
+                        o[2 * k + 1] = e4m3x2_to_f16x2(cw[k] >> 16);
+                        // a byte of 0x7f or 0xff: NaN
+                        const uint32_t all = cw[k] & 0x7f7f7f7fu;
+                        nan |= (all + 0x01010101u) & 0x80808080u;
+                    }
+                    uint8_t* row = vt + e * 4096 + (c >> 2) * 2048;
+                    *reinterpret_cast<uint4*>(row + sw128_off(r0, (2 * c) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(row + sw128_off(r0, (2 * c + 1) & 7)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(&bars->v_full[st]));
+            }
+            if (!ok) break;
+            const int slot = wu & 1;
+            if (!(ok = mbar_wait(smem_u32(&bars->r_empty[slot]), (uint32_t)(((wu >> 1) & 1) ^ 1), pc))) break;
+            bars->r_flag[slot][tid] = nan ? 1 : 0;
+            mbar_arrive(smem_u32(&bars->r_full[slot]));
+            g0 += n_tiles;
+            ++wu;
+        }
+        named_bar_sync(2, PQ_THREADS);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
+        // =========================================== softmax WG j ======
+        const int j = wg - 1;
+        const int r = tid - 128 * wg;  // accumulator row == TMEM lane
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + j * 128, tO = tmem + 256 + j * 128;
+        const float nanv = __int_as_float(0x7fc00000);
+        int g0 = 0;        // KV tiles before the unit
+        uint32_t ph = 0;   // bit 0 s_full (this q-tile's tiles), bit 1 o_done, bits 2-3 work units
+        bool ok = true;
+#pragma unroll 1
+        for (int kk = 0;; ++kk) {
+            const int uslot = kk & 1;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->u_full[uslot]), (uint32_t)((kk >> 1) & 1), pc)))) break;
+            const volatile PqUnit* un = &bars->unit[uslot];
+            if (un->end) break;
+            const int s0 = (2 * un->pair + j) * rph, s = s0 + r % rph;
+            const bool valid = s < a.Sq;
+            const int n_tiles = max(un->nt0, un->nt1), nt = j ? un->nt1 : un->nt0;
+            const size_t row = query_row(a, un->b, un->kvh, rph, s0, r);
+            if (un->bad || n_tiles == 0) {
+                if (valid) write_row(a, row, un->bad ? nanv : -INFINITY);
+                mbar_arrive(smem_u32(&bars->u_empty[uslot]));
+                continue;
+            }
+            int n_vis;
+            {
+                const int p = valid ? a.position_ids[(size_t)un->b * a.Sq + s] : -1, kv_len = un->kv_len;
+                n_vis = p < 0 ? 0 : (p >= kv_len ? kv_len : p + 1);
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->q_ready[j]), (ph >> 2) & 1u, pc));
+            const float scr = bars->qscale[j][r];
+            float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < nt && ok; ++i) {
+                const int g = g0 + i;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->s_full[j]), (ph ^ (uint32_t)i) & 1u, pc)))) break;
+                // (behind s_full: the scales of every tile before this one are told, so the slot is in
+                // this use or the one before, as a wait by parity needs)
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->sc_full[g % SCST]), (uint32_t)((g / SCST) & 1), pc)))) break;
+                tc_fence_after();
+                const float4* sc = bars->sc[g % SCST];
+                uint32_t xr[128];
+#pragma unroll
+                for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(tS + lane_addr + c4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&xr[c4 * 32]));
+                tmem_ld_wait();
+                const int lim = n_vis - i * PF_BN;  // columns < lim are visible
+                if (__any_sync(0xffffffffu, lim < PF_BN)) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) xr[c] = c < lim ? xr[c] : 0xff800000u;  // -inf
+                }
+                // Row max of w = z + log2(vs): per page on the raw scores (its factor is positive).
+                float mt = -INFINITY;
+#pragma unroll
+                for (int p = 0; p < PF_PAGES_PER_TILE; ++p) {
+                    float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) {
+                        x0 = fmaxf(x0, __uint_as_float(xr[16 * p + c]));
+                        x1 = fmaxf(x1, __uint_as_float(xr[16 * p + c + 1]));
+                    }
+                    const float4 f = sc[p];
+                    mt = fmaxf(mt, fmaf(fmaxf(x0, x1), f.x * scr, f.y));
+                }
+                float alpha = 1.0f;
+                bool resc = false;
+                if (mt > m + RESCALE_SLACK) {
+                    alpha = ex2(m - mt);  // 0 when m = -inf
+                    m = mt;
+                    resc = true;
+                }
+                // p' = 2^(w - m + 7), packed as FP16 pairs into xr[0..63]; the sum divides vs out
+                const float nm = (m == -INFINITY) ? 0.0f : P_BIAS - m;
+                float rs = 0.0f;
+#pragma unroll
+                for (int p = 0; p < PF_PAGES_PER_TILE; ++p) {
+                    const float4 f = sc[p];
+                    const float mul = f.x * scr, add = f.y + nm;
+                    const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
+                    float2 acc2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int c = 16 * p; c < 16 * p + 16; c += 2) {
+                        const float2 t = ffma2(make_float2(__uint_as_float(xr[c]), __uint_as_float(xr[c + 1])), mul2, add2);
+                        const float2 e = make_float2(ex2(t.x), ex2(t.y));
+                        acc2 = fadd2(acc2, e);
+                        xr[c >> 1] = pack_f16x2(e.x, e.y);
+                    }
+                    rs = fmaf(acc2.x + acc2.y, f.z, rs);
+                }
+                l = fmaf(l, alpha, rs);
+                // S_j(i) complete implies PV_j(i-1) complete (MMAs of one issuer retire in order), so O_j is
+                // stable and S_j's columns may take P_j(i).
+                if (i > 0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        uint32_t rr[32];
+                        tmem_ld32(tO + lane_addr + c4 * 32, rr);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) rr[q] = __float_as_uint(__uint_as_float(rr[q]) * alpha);
+                        tmem_st32(tO + lane_addr + c4 * 32, rr);
+                    }
+                }
+                tmem_st32(tS + lane_addr, *reinterpret_cast<uint32_t(*)[32]>(&xr[0]));
+                tmem_st32(tS + lane_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&xr[32]));
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&bars->p_ready[j]));
+            }
+            // ---- epilogue ----
+            if (ok && nt > 0) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->o_done[j]), (ph >> 1) & 1u, pc));
+            int unit_bad = 0;
+            if (ok) {  // the verdict on the unit's V codes and scales
+                const int slot = (ph >> 2) & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->r_full[slot]), (ph >> 3) & 1u, pc));
+                if (ok) {
+                    const uint4* f = reinterpret_cast<const uint4*>(bars->r_flag[slot]);
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) any |= f[q].x | f[q].y | f[q].z | f[q].w;
+                    unit_bad = (any ? RK_STATUS_RANGE : 0) | (bars->r_flag[slot][128] ? RK_STATUS_SCALE : 0);
+                    mbar_arrive(smem_u32(&bars->r_empty[slot]));
+                }
+            }
+            if (!ok) {  // a wait gave up: this unit's rows and the CTA's later units are written as failed
+                if (valid) write_row(a, row, nanv);
+                for (int k2 = kk + 1;; ++k2) {
+                    const long long u2 = cta_unit(k2, cta, grid);
+                    if (u2 >= total) break;
+                    int b2, kvh2, pair2;
+                    unit_place(a, n_qtiles, u2, b2, kvh2, pair2);
+                    const int t0 = (2 * pair2 + j) * rph;
+                    if (t0 + r % rph < a.Sq) write_row(a, query_row(a, b2, kvh2, rph, t0, r), nanv);
+                }
+                if (r == 0 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
+                break;
+            }
+            // a query that sees a key fails if its unit does or its sum is beyond FP32 (which a NaN
+            // code in K, a query out of range or an overflowing score make it)
+            const bool seen = n_vis > 0;
+            const int fail = !valid || !seen ? 0 : unit_bad ? unit_bad : (l > 0.0f && l < INFINITY) ? 0 : RK_STATUS_RANGE;
+            if (nt > 0) {
+                tc_fence_after();
+                const float inv_l = fail || !seen ? 0.0f : 1.0f / l;
+                uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (valid ? row : 0) * HEAD_DIM);
+#pragma unroll 1
+                for (int c4 = 0; c4 < 4; ++c4) {
+                    uint32_t rr[32];
+                    tmem_ld32(tO + lane_addr + c4 * 32, rr);
+                    tmem_ld_wait();
+                    if (valid) {
+#pragma unroll
+                        for (int q = 0; q < 32; q += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = fail || !seen ? 0u
+                                                     : pack_bf16x2(__uint_as_float(rr[q + 2 * e]) * inv_l, __uint_as_float(rr[q + 2 * e + 1]) * inv_l);
+                            o[(c4 * 32 + q) / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                // O_j has been read: the next unit's first PV may overwrite it
+                tc_fence_before();
+                mbar_arrive(smem_u32(&bars->o_free[j]));
+                if (valid) a.lse[row] = fail ? nanv : seen ? (m - P_BIAS + log2f(l)) * 0.693147180559945309f : -INFINITY;
+            } else if (valid) {
+                write_row(a, row, fail ? nanv : -INFINITY);
+            }
+            const unsigned any_fail = __reduce_or_sync(0xffffffffu, (unsigned)fail);
+            if (any_fail && lane == 0 && a.status) atomicOr(a.status, (int)any_fail);
+            mbar_arrive(smem_u32(&bars->u_empty[uslot]));
+            g0 += n_tiles;
+            ph ^= (uint32_t)(nt & 1) | (nt > 0 ? 2u : 0u);
+            ph = (ph & 3u) | ((((ph >> 2) + 1u) & 3u) << 2);
+        }
+        named_bar_sync(2, PQ_THREADS);
+    }
+
+    // ---- teardown: every role has passed barrier 2; no MMA or TMEM access is in flight ----
+    if (warp == WARP_MMA) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream) {
+    static std::atomic<uint64_t> configured{0};
+    static std::atomic<int> sm_count[64];
+    int dev = 0, nsm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
+    if (!bit || !(configured.load() & bit)) {
+        e = cudaFuncSetAttribute(prefill_q8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PQ_SMEM_BYTES);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) return e;
+        if (bit) sm_count[dev].store(nsm);
+        configured.fetch_or(bit);
+    } else {
+        nsm = sm_count[dev].load();
+    }
+    const int rph = PF_BM / a.G, n_qtiles = (a.Sq + rph - 1) / rph;
+    const long long units = (long long)a.B * a.Hkv * ((n_qtiles + 1) / 2);
+    if (units <= 0) return cudaSuccess;
+    prefill_q8_kernel<<<(unsigned)(units < nsm ? units : nsm), PQ_THREADS, PQ_SMEM_BYTES, stream>>>(km, vm, a);
+    return cudaGetLastError();
+}
+
+}  // namespace rk

@@ -14,11 +14,15 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Packed e4m3 -> two floats (exact).
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t w) {
+// The two e4m3 in the low half -> packed FP16, two floats (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)w));
-    return __half22float2(*reinterpret_cast<__half2*>(&h));
+    return h;
+}
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t w) {
+    const uint32_t h = e4m3x2_to_f16x2(w);
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // x (two values) as a sum of e4m3 parts: the part, and x reduced to what is left

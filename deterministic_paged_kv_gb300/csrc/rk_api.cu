@@ -31,9 +31,9 @@ cudaError_t launch_backward_dq_tc(const CUtensorMap& qm, const CUtensorMap& om, 
 cudaError_t launch_backward_rotate(const BackwardArgs& a, cudaStream_t stream);
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream);
 cudaError_t launch_append_q8(const AppendQ8Args& a, cudaStream_t stream);
-cudaError_t launch_attn_q8(const AttnQ8Args& a, cudaStream_t stream);
 int decode_q8_bundle(int Hkv);
 cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream);
+cudaError_t launch_prefill_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream);
 }  // namespace rk
 
 namespace {
@@ -952,6 +952,16 @@ int attn_q8_args(const rk_paged_plan_t* plan, const void* q, const void* k_cache
     return RK_OK;
 }
 
+// Maps of both caches; without a pool no row has a page to read, and the (16-byte aligned)
+// query's address stands in.
+int make_q8_maps(CUtensorMap* km, CUtensorMap* vm, const rk_paged_plan_t* plan, const void* q, const void* k_cache,
+                 const void* v_cache, int heads) {
+    const bool have = plan->num_pages > 0;
+    const int pages = have ? plan->num_pages : 1;
+    const int rc = make_q8_map(km, have ? k_cache : q, pages, plan->Hkv, heads, "k_cache");
+    return rc ? rc : make_q8_map(vm, have ? v_cache : q, pages, plan->Hkv, heads, "v_cache");
+}
+
 // Split geometry of the 8-bit decode.  split_tokens = 0: short splits where a row starts
 // (a short row then has several CTAs at work), longer ones further on (fewer partial
 // results of a long row); which token is in which split never depends on the row's length.
@@ -1112,12 +1122,8 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t* plan, int32_t split_tokens, c
     a.n_splits = (int32_t)splits;
     a.o_part = static_cast<float*>(scratch);
     if (need > 0) a.lse_part = a.o_part + (int64_t)plan->B * plan->Hq * a.n_splits * rk::HEAD_DIM;
-    // without a pool no row has a page to read: the map of the (16-byte aligned) query stands in
     CUtensorMap km, vm;
-    const bool have = plan->num_pages > 0;
-    const int pages = have ? plan->num_pages : 1, heads = rk::decode_q8_bundle(plan->Hkv);
-    if ((rc = make_q8_map(&km, have ? k_cache : q, pages, plan->Hkv, heads, "k_cache"))) return rc;
-    if ((rc = make_q8_map(&vm, have ? v_cache : q, pages, plan->Hkv, heads, "v_cache"))) return rc;
+    if ((rc = make_q8_maps(&km, &vm, plan, q, k_cache, v_cache, rk::decode_q8_bundle(plan->Hkv)))) return rc;
     cudaError_t e = rk::launch_decode_q8(km, vm, a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(RK_E_CUDA, "8-bit decode launch: %s", cudaGetErrorString(e));
     return RK_OK;
@@ -1132,7 +1138,9 @@ int rk_paged_attn_prefill_q8(const rk_paged_plan_t* plan, const void* q, const v
     int rc = attn_q8_args(plan, q, k_cache, v_cache, k_scale, v_scale, block_table_d, kv_lens_d, position_ids_d, out, lse,
                           status_d, &a);
     if (rc || plan->B == 0) return rc;
-    cudaError_t e = rk::launch_attn_q8(a, reinterpret_cast<cudaStream_t>(stream));
+    CUtensorMap km, vm;
+    if ((rc = make_q8_maps(&km, &vm, plan, q, k_cache, v_cache, 1))) return rc;
+    cudaError_t e = rk::launch_prefill_q8(km, vm, a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(RK_E_CUDA, "8-bit prefill launch: %s", cudaGetErrorString(e));
     return RK_OK;
 }
