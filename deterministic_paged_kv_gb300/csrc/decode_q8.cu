@@ -452,7 +452,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 const CUtensorMap* map = kv ? &vmap : &kmap;
 #pragma unroll 1
                 for (int p = 0; p < pages; ++p, dst += H * Q8_BLOCK_BYTES)
-                    tma_load_5d_elect(dst, map, fb, 0, 0, head, 0, __shfl_sync(0xffffffffu, id, p * H));
+                    if constexpr (H == 1) tma_load_3d_elect(dst, map, fb, 0, 0, __shfl_sync(0xffffffffu, id, p) * a.Hkv + head);
+                    else tma_load_5d_elect(dst, map, fb, 0, 0, head, 0, __shfl_sync(0xffffffffu, id, p * H));
                 if (++stg == STAGES) {
                     stg = 0;
                     phase ^= 1;

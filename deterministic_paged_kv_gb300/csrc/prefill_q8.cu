@@ -1,35 +1,31 @@
-// prefill_q8.cu -- causal chunked prefill over the 8-bit page cache (tcgen05, TMA).
+// prefill_q8.cu -- causal chunked prefill over the 8-bit page cache (tcgen05).
 //
 // Operation: the paged prefill of "WS2 PR7 Fused Attention Backend Alignment",
 // "Current Implementation", over e4m3 codes whose K was rotated when it was written.
 // Work units (two q-tiles of one row and KV head), their heaviest-first order, the
 // persistent grid and the online softmax are those of the BF16 prefill kernel.
 //
-// What is different is what the operands are:
-//   scores   K goes from the cache into the MMA as it is (e4m3); q, rotated and scaled to
-//            below 362 by a power of two per query, is three e4m3 parts, added up in the
-//            FP32 accumulator: 12 MMAs of K = 32 for 8 of FP16 (768 cycles of the tensor
-//            pipe for 512), but no K tile is rewritten, and a score keeps q to 2^-12 at
-//            worst and 2^-16 on average, where one FP16 operand keeps 2^-12.3 on average
-//            (0.0002 off the LSE of a query that sees one key).
-//   P V      V is converted to FP16 (exact) by the transform warpgroup; P is FP16, scaled to
-//            at most 2^15 (it keeps 2^-11 of a weight down to 2^-21 of the largest).
-//            (P as two e4m3 parts would take as many tensor cycles and put the splitting on
-//            the softmax, which sets the pace.)
-//   scales   a page's scales are constants of 16 columns: the softmax folds K's into its
-//            multiplier and V's into the exponent, w = z + log2(vs), and divides the row sum's
-//            page partials by vs: some 40 instructions of 600 a tile and row.
+// Operands: the codes of K and V become FP16 (exact) on their way into shared memory; q is
+// rotated, scaled to below 362 by a power of two per query, and rounded to FP16 (2^-11 at
+// most, the precision of the BF16 kernel's scores); P is FP16, scaled to at most 2^15 (it
+// keeps 2^-11 of a weight down to 2^-21 of the largest).  A page's scales are constants of
+// 16 columns: the softmax folds K's into its multiplier and V's into the exponent,
+// w = z + log2(vs), and divides the row sum's page partials by vs, some 40 instructions of 600
+// a tile and row.
+// (K as it is, in fp8 MMAs against q in three e4m3 parts, needs no conversion and keeps q to
+// 2^-16, but its 12 MMAs a tile read 96 KiB of operands where 8 of FP16 read 64, took 125
+// cycles each, and left the copies no room in the shared memory's bandwidth: 925 us for
+// S = 8192, 137 us for the chunk.)
 // What bounds it: the chain softmax -> PV -> S of each q-tile (two q-tiles overlap), then the
-// tensor pipe, 2560 cycles a pair of q-tiles and KV tile.
+// tensor pipe, 2048 cycles a pair of q-tiles and KV tile.
 //
 // Roles (512 threads, registers rebalanced with setmaxnreg):
 //   warp 15      scheduler: each unit's metadata, published as a descriptor (two slots);
-//   warpgroup 0  transform: q of both q-tiles of a unit as e4m3 parts (as soon as the unit
-//                before has read its own), V tiles to FP16 (zeros past the last key);
+//   warpgroup 0  transform: q of both q-tiles of a unit (as soon as the unit before has read
+//                its own), K and V tiles from the cache to FP16 operands (V zero past the last
+//                key), a tile's codes in registers while the one before is in use; scales;
 //   warpgroups 1, 2  softmax of q-tile 0, 1: a thread per accumulator row;
-//   warp 12      K producer: K tiles by TMA, the pages' scales;
-//   warp 14      V producer: V tiles by TMA (codes);
-//   warp 13      MMA issuer (converged).
+//   warp 13      MMA issuer (converged); warps 12, 14 have nothing to do.
 // Nothing depends on B, W or the grid.
 #include <atomic>
 
@@ -40,23 +36,20 @@ namespace rk {
 namespace {
 
 constexpr int PQ_THREADS = 512;
-constexpr int WARP_K = 12, WARP_MMA = 13, WARP_V = 14, WARP_SCHED = 15;
-constexpr int PQ_PARTS = 3;
-constexpr int PQ_CODES = PF_BN * HEAD_DIM;      // a tile of codes: 16 KiB
-constexpr int KST = 2, VST = 2;                 // K stages, V stages (codes and FP16)
+constexpr int WARP_MMA = 13, WARP_SCHED = 15;
+constexpr int KST = 2, VST = 3;                 // K stages, V stages
 constexpr int SCST = 4;                         // scale slots: one more than K stages at least
 constexpr uint32_t TMEM_COLS = 512;             // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512)
 constexpr float RESCALE_SLACK = 8.0f, P_BIAS = 7.0f;
-constexpr uint32_t UNIT_READERS = 3 * 32 + 128 + 256;
+constexpr uint32_t UNIT_READERS = 32 + 128 + 256;
 
 // setmaxnreg split (sum 4 x 128 = the 512 x 128 registers the CTA launches with)
-constexpr int REG_XFORM = 88, REG_SOFTMAX = 184, REG_CTRL = 56;
+constexpr int REG_XFORM = 104, REG_SOFTMAX = 176, REG_CTRL = 56;
 static_assert(REG_XFORM + 2 * REG_SOFTMAX + REG_CTRL == 4 * 128, "register split must sum to the launch budget");
 
-constexpr int OFF_Q = 0;                                     // [q-tile][part][128 rows][128 B]
-constexpr int OFF_K = OFF_Q + 2 * PQ_PARTS * PQ_CODES;
-constexpr int OFF_VC = OFF_K + KST * PQ_CODES;               // V codes
-constexpr int OFF_V = OFF_VC + VST * PQ_CODES;               // V FP16, [page][64-dim half][16 rows][128 B]
+constexpr int OFF_Q = 0;                             // [q-tile][64-dim half][128 rows][128 B]
+constexpr int OFF_K = OFF_Q + 2 * PF_TILE_BYTES;     // [64-dim half][128 rows][128 B]
+constexpr int OFF_V = OFF_K + KST * PF_TILE_BYTES;   // [page][64-dim half][16 rows][128 B]
 constexpr int OFF_BAR = OFF_V + VST * PF_TILE_BYTES;
 
 struct PqUnit {
@@ -67,18 +60,17 @@ struct PqUnit {
 
 struct PqBars {
     uint64_t q_ready[2], q_empty;
-    uint64_t k_full[KST], k_empty[KST], sc_full[SCST];
-    uint64_t c_full[VST], c_empty[VST];  // V codes
-    uint64_t v_full[VST], v_empty[VST];  // V FP16
+    uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], sc_full[SCST];
     uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
     uint64_t u_full[2], u_empty[2];
-    uint64_t r_full[2], r_empty[2];      // a unit's verdict: transform threads and K producer -> softmax
+    uint64_t r_full[2], r_empty[2];      // a unit's verdict: transform threads -> softmax
     uint64_t never;
     uint32_t tmem_base;
     PipeCtl pipe;
     PqUnit unit[2];
-    alignas(16) uint8_t r_flag[2][144];  // [0, 128) NaN code in V; [128] a scale that is none
+    alignas(16) uint8_t r_flag[2][128];  // 1: NaN code in V, 2: a scale that is none
     alignas(16) float4 sc[SCST][PF_PAGES_PER_TILE];  // k scale, log2 of v's, 1 / v's
+    float qinv[PF_BM];                   // a query's power of two, inverted
     float qscale[2][PF_BM];              // score factor of each query (log2 domain); NaN: out of range
 };
 constexpr int PQ_SMEM_BYTES = OFF_BAR + (int)sizeof(PqBars);
@@ -176,8 +168,7 @@ __device__ __forceinline__ bool read_unit(PqBars* bars, int k, PipeCtl* pc, PqUn
 }
 
 __global__ void __launch_bounds__(PQ_THREADS, 1)
-    prefill_q8_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                      const __grid_constant__ AttnQ8Args a) {
+    prefill_q8_kernel(const __grid_constant__ AttnQ8Args a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw;
     PqBars* bars = reinterpret_cast<PqBars*>(sm + OFF_BAR);
@@ -194,13 +185,11 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
         mbar_init(smem_u32(&bars->never), 1);
         mbar_init(smem_u32(&bars->q_empty), 1);
         for (int k = 0; k < KST; ++k) {
-            mbar_init(smem_u32(&bars->k_full[k]), 1);
+            mbar_init(smem_u32(&bars->k_full[k]), 128);
             mbar_init(smem_u32(&bars->k_empty[k]), 1);
         }
         for (int k = 0; k < SCST; ++k) mbar_init(smem_u32(&bars->sc_full[k]), 1);
         for (int k = 0; k < VST; ++k) {
-            mbar_init(smem_u32(&bars->c_full[k]), 1);
-            mbar_init(smem_u32(&bars->c_empty[k]), 128);
             mbar_init(smem_u32(&bars->v_full[k]), 128);
             mbar_init(smem_u32(&bars->v_empty[k]), 1);
         }
@@ -212,12 +201,11 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
             mbar_init(smem_u32(&bars->o_free[j]), 128);
             mbar_init(smem_u32(&bars->u_full[j]), 1);
             mbar_init(smem_u32(&bars->u_empty[j]), UNIT_READERS);
-            mbar_init(smem_u32(&bars->r_full[j]), 129);
+            mbar_init(smem_u32(&bars->r_full[j]), 128);
             mbar_init(smem_u32(&bars->r_empty[j]), 256);
         }
         fence_mbar_init();
     }
-    for (int i = tid; i < (int)sizeof(bars->r_flag) / 4; i += PQ_THREADS) reinterpret_cast<uint32_t*>(&bars->r_flag[0][0])[i] = 0;
     if (warp == WARP_MMA) {
         tmem_alloc(smem_u32(&bars->tmem_base), TMEM_COLS);
         tmem_relinquish();
@@ -248,86 +236,12 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 }
                 if (m.end) break;
             }
-        } else if (warp == WARP_K || warp == WARP_V) {
-            // ============================================== producers ====
-            // lane p: page p of a tile.  n: tiles over the CTA's units.
-            const bool is_k = warp == WARP_K;
-            const CUtensorMap* map = is_k ? &kmap : &vmap;
-            if (lane == 0) prefetch_tmap(map);
-            constexpr int nst = KST;
-            static_assert(KST == VST, "one stage count for both producers");
-            int n = 0, wu = 0;
-            bool ok = true;
-#pragma unroll 1
-            for (int k = 0; ok; ++k) {
-                PqUnit u;
-                if (!(ok = __all_sync(0xffffffffu, read_unit(bars, k, pc, u))) || u.end) break;
-                const int n_tiles = max(u.nt0, u.nt1);
-                if (u.bad || n_tiles == 0) continue;
-                const int32_t* bt = a.block_table + (size_t)u.b * a.W;
-                const int n_pages = (u.n_keys + PAGE - 1) / PAGE;
-                int pg = lane < min(PF_PAGES_PER_TILE, n_pages) ? __ldg(bt + lane) : 0;
-                bool odd = false;
-#pragma unroll 1
-                for (int i = 0; i < n_tiles; ++i, ++n) {
-                    const int st = n % nst, p0 = i * PF_PAGES_PER_TILE, np = min(PF_PAGES_PER_TILE, n_pages - p0);
-                    const uint32_t eb = smem_u32(is_k ? &bars->k_empty[st] : &bars->c_empty[st]);
-                    const uint32_t fb = smem_u32(is_k ? &bars->k_full[st] : &bars->c_full[st]);
-                    int good = 1;
-                    if (lane == 0) {
-                        good = mbar_wait(eb, (uint32_t)(((n / nst) & 1) ^ 1), pc);
-                        if (good) mbar_arrive_expect_tx(fb, (uint32_t)np * Q8_BLOCK_BYTES);
-                    }
-                    if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
-                    const uint32_t dst = s_base + (is_k ? OFF_K : OFF_VC) + st * PQ_CODES;
-#pragma unroll 1
-                    for (int p = 0; p < np; ++p)
-                        tma_load_5d_elect(dst + p * Q8_BLOCK_BYTES, map, fb, 0, 0, u.kvh, 0, __shfl_sync(0xffffffffu, pg, p));
-                    const int cur = pg;
-                    if (i + 1 < n_tiles) pg = lane < min(PF_PAGES_PER_TILE, n_pages - p0 - 8) ? __ldg(bt + p0 + 8 + lane) : 0;
-                    if (is_k) {
-                        // The slot's reader of SCST tiles ago is done: the stage of K was free, so S of tile
-                        // n - KST is, and with it the softmax of the tile before that.
-                        float ks = 1.0f, vs = 1.0f;
-                        if (lane < np) {
-                            const size_t block = (size_t)cur * a.Hkv + u.kvh;
-                            ks = __ldg(a.k_scale + block);
-                            vs = __ldg(a.v_scale + block);
-                        }
-                        if (!scale_ok(ks) || !scale_ok(vs)) {
-                            odd = true;
-                            ks = vs = 1.0f;
-                        }
-                        if (lane < PF_PAGES_PER_TILE) bars->sc[n % SCST][lane] = make_float4(ks, __log2f(vs), rcp(vs), 0.0f);
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&bars->sc_full[n % SCST]));
-                    }
-                }
-                if (!ok) break;
-                if (is_k) {
-                    odd = __any_sync(0xffffffffu, odd);
-                    const int slot = wu & 1;
-                    int good = 1;
-                    if (lane == 0) {
-                        good = mbar_wait(smem_u32(&bars->r_empty[slot]), (uint32_t)(((wu >> 1) & 1) ^ 1), pc);
-                        if (good) {
-                            bars->r_flag[slot][128] = odd ? 1 : 0;
-                            mbar_arrive(smem_u32(&bars->r_full[slot]));
-                        }
-                    }
-                    if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
-                    ++wu;
-                }
-            }
-            if (lane == 0 && pipe_aborted(pc))  // copies in flight land before the CTA's shared memory is released
-                for (int i = max(0, n - nst); i < n; ++i)
-                    mbar_wait_drain(smem_u32(is_k ? &bars->k_full[i % nst] : &bars->c_full[i % nst]), (uint32_t)((i / nst) & 1));
-        } else {
+        } else if (warp == WARP_MMA) {
             // ============================================= MMA issuer ====
-            constexpr uint32_t idS = idesc_e4m3_f32(PF_BM, PF_BN, 0, 0);
+            constexpr uint32_t idS = idesc_f16_f32(PF_BM, PF_BN);
             constexpr uint32_t idO = idesc_f16_f32(PF_BM, HEAD_DIM) | (1u << 16);  // FP16, V MN-major
             const uint32_t dQ = desc_lo(s_base + OFF_Q, 16), dK = desc_lo(s_base + OFF_K, 16), dV = desc_lo(s_base + OFF_V, 2048);
-            constexpr uint32_t TILE8 = PQ_CODES >> 4, TILE16 = PF_TILE_BYTES >> 4;
+            constexpr uint32_t TILE = PF_TILE_BYTES >> 4;
             // g0: KV tiles before the unit; ph bit 0 work units, bits 2 + j s_full / p_ready of
             // q-tile j, bits 4 + j o_free
             int g0 = 0;
@@ -350,7 +264,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                     if (!wait(bars->v_full[g % VST], (uint32_t)(g / VST))) return false;
                     if (!wait(bars->p_ready[j], (ph >> (2 + j)) ^ (uint32_t)i)) return false;
                     tc_fence_after();
-                    mma_ts_steps<0, 8, MN_MAJOR_PAGE, true>(tmem + 256 + j * 128, tmem + j * 128, dV + (uint32_t)(g % VST) * TILE16, idO,
+                    mma_ts_steps<0, 8, MN_MAJOR_PAGE, true>(tmem + 256 + j * 128, tmem + j * 128, dV + (uint32_t)(g % VST) * TILE, idO,
                                                             i > 0 ? 1u : 0u);
                     return true;
                 };
@@ -369,10 +283,8 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                         if (i == 0 && !(ok = wait(bars->q_ready[j], ph))) break;
                         if (!(ok = wait(bars->k_full[g % KST], (uint32_t)(g / KST)))) break;
                         tc_fence_after();
-                        const uint32_t d = tmem + j * 128, dk = dK + (uint32_t)(g % KST) * TILE8, dq = dQ + (uint32_t)(j * PQ_PARTS) * TILE8;
-#pragma unroll
-                        for (int p = 0; p < PQ_PARTS; ++p)
-                            mma_f8_x4<2, 2>(d, dq + p * TILE8, dk, DESC_HI, DESC_HI, idS, p > 0, 4);
+                        mma_ss_steps<0, 8, K_MAJOR_128, K_MAJOR_128, true>(tmem + j * 128, dQ + (uint32_t)j * TILE,
+                                                                           dK + (uint32_t)(g % KST) * TILE, idS, 0u);
                         umma_commit_elect(smem_u32(&bars->s_full[j]));
                     }
                     if (!ok) break;
@@ -402,108 +314,187 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
     } else if (wg == 0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_XFORM));
         // ================================================ transform WG ====
+        // Tiles: the thread has 16 codes (chunk c) of rows r0 + 16 e, a row of each page.
+        const int c = tid & 7, r0 = tid >> 3;
         int g0 = 0, wu = 0;  // KV tiles before the unit, work units
+        // The warpgroup leaves the loop together: a warp whose wait gave up goes on to the next
+        // barrier, which tells the others.
         bool ok = true;
+        auto wait = [&](uint64_t& bar, int parity) {
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), (uint32_t)(parity & 1), pc));
+            return ok;
+        };
 #pragma unroll 1
-        for (int kk = 0; ok; ++kk) {
+        for (int kk = 0;; ++kk) {
             PqUnit u;
-            if (!(ok = read_unit(bars, kk, pc, u)) || u.end) break;
+            if (ok) ok = __all_sync(0xffffffffu, read_unit(bars, kk, pc, u));
+            if (named_bar_or(3, 128, !ok)) {
+                ok = false;
+                break;
+            }
+            if (u.end) break;
             const int n_tiles = max(u.nt0, u.nt1);
             if (u.bad || n_tiles == 0) continue;
-            // ---- q: thread r rotates row r of both q-tiles and splits it into parts ----
-            if (!(ok = mbar_wait(smem_u32(&bars->q_empty), (uint32_t)((wu & 1) ^ 1), pc))) break;
+            const int32_t* bt = a.block_table + (size_t)u.b * a.W;
+            const int n_pages = (u.n_keys + PAGE - 1) / PAGE;
+            const size_t in_block = (size_t)u.kvh * Q8_BLOCK_BYTES + r0 * HEAD_DIM + c * 16, page_bytes = (size_t)a.Hkv * Q8_BLOCK_BYTES;
+            auto page_ids = [&](int i) {  // lane e (of 8): page e of tile i, -1 past the last
+                const int p = i * PF_PAGES_PER_TILE + (lane & 7);
+                return p < n_pages ? __ldg(bt + p) : -1;
+            };
+            uint32_t odd = 0;  // 1: NaN code in V, 2: a scale that is none
+            uint4 kw[8], vw[8];
+            float ks = 1.0f, vs = 1.0f;
+            auto load = [&](int ids) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int id = __shfl_sync(0xffffffffu, ids, e);
+                    const size_t at = (size_t)id * page_bytes + in_block;
+                    kw[e] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.k_cache + at)) : make_uint4(0, 0, 0, 0);
+                    vw[e] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.v_cache + at)) : make_uint4(0, 0, 0, 0);
+                }
+                ks = vs = 1.0f;
+                if (tid < 8 && ids >= 0) {
+                    ks = __ldg(a.k_scale + (size_t)ids * a.Hkv + u.kvh);
+                    vs = __ldg(a.v_scale + (size_t)ids * a.Hkv + u.kvh);
+                }
+            };
+            // Tile i of the unit from the registers to its operands.
+            auto convert = [&](int i) {
+                const int g = g0 + i, kst = g % KST, vst = g % VST;
+                if (!wait(bars->k_empty[kst], (g / KST) ^ 1)) return;
+                uint8_t* kt = sm + OFF_K + kst * PF_TILE_BYTES + (c >> 2) * 16384;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t w[4] = {kw[e].x, kw[e].y, kw[e].z, kw[e].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[2 * k] = e4m3x2_to_f16x2(w[k]);
+                        o[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
+                    }
+                    *reinterpret_cast<uint4*>(kt + sw128_off(r0 + 16 * e, (2 * c) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(kt + sw128_off(r0 + 16 * e, (2 * c + 1) & 7)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                if (tid < 8) {
+                    // The slot's readers of SCST tiles ago are done: the stage of K was free, so S of tile
+                    // g - KST is, and with it the softmax of the tile before that.
+                    const bool none = !scale_ok(ks) || !scale_ok(vs);
+                    if (none) odd |= 2;
+                    bars->sc[g % SCST][tid] = none ? make_float4(1.0f, 0.0f, 1.0f, 0.0f) : make_float4(ks, __log2f(vs), rcp(vs), 0.0f);
+                }
+                if (warp == 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&bars->sc_full[g % SCST]));
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(&bars->k_full[kst]));
+                if (!wait(bars->v_empty[vst], (g / VST) ^ 1)) return;
+                uint8_t* vt = sm + OFF_V + vst * PF_TILE_BYTES + (c >> 2) * 2048;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool in = i * PF_BN + 16 * e + r0 < u.n_keys;  // zeros past the last key: 0 times a NaN is not 0
+                    const uint32_t w[4] = {vw[e].x, vw[e].y, vw[e].z, vw[e].w};
+                    uint32_t o[8], nan = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t x = in ? w[k] : 0u;
+                        o[2 * k] = e4m3x2_to_f16x2(x);
+                        o[2 * k + 1] = e4m3x2_to_f16x2(x >> 16);
+                        nan |= (x & 0x7f7f7f7fu) + 0x01010101u;  // a byte of 0x7f or 0xff: NaN
+                    }
+                    if (nan & 0x80808080u) odd |= 1;
+                    *reinterpret_cast<uint4*>(vt + e * 4096 + sw128_off(r0, (2 * c) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(vt + e * 4096 + sw128_off(r0, (2 * c + 1) & 7)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(&bars->v_full[vst]));
+            };
+            // ---- the unit's first tile, while the unit before is still at work ----
+            load(page_ids(0));
+            int next = page_ids(1);
+            convert(0);
+            // ---- q ----
+            wait(bars->q_empty, wu ^ 1);
+            if (named_bar_or(3, 128, !ok)) {
+                ok = false;
+                break;
+            }
 #pragma unroll 1
             for (int j = 0; j < 2; ++j) {
-                const int s0 = (2 * u.pair + j) * rph, s = s0 + tid % rph;
-                const bool valid = s < a.Sq;
-                const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                                                (valid ? query_row(a, u.b, u.kvh, rph, s0, tid) : 0) * HEAD_DIM);
-                const uint32_t pos = valid ? (uint32_t)a.position_ids[(size_t)u.b * a.Sq + s] : 0;
-                uint32_t m = 0;
-#pragma unroll 4
-                for (int i = 0; i < 16; ++i) {
-                    const uint4 w = __ldg(q + i);
-                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-                }
-                m = max(m & 0xffffu, m >> 16);
-                const bool bad = m >= Q8_LIMIT_BF16, zero = bad || !valid;
-                const int e = zero ? 0 : q8_exponent(m);
-                const float inv = pow2(-e);
-                bars->qscale[j][tid] = bad && valid ? __int_as_float(0x7fc00000) : a.qk_scale_log2 * pow2(e);
-                uint8_t* qt = sm + OFF_Q + j * PQ_PARTS * PQ_CODES;
-#pragma unroll 1
-                for (int c = 0; c < 8; ++c) {  // pairs 8 c .. 8 c + 7: dims 8 c .. and 64 + 8 c ..
-                    const uint4 lo = __ldg(q + c), hi = __ldg(q + 8 + c);
-                    const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
-                    uint32_t pl[PQ_PARTS][2] = {}, ph[PQ_PARTS][2] = {};
+                const int s0 = (2 * u.pair + j) * rph;
+                const __nv_bfloat16* qb = reinterpret_cast<const __nv_bfloat16*>(a.q);
+                {   // the largest element of row tid
+                    const bool valid = s0 + tid % rph < a.Sq;
+                    const uint4* q = reinterpret_cast<const uint4*>(qb + (valid ? query_row(a, u.b, u.kvh, rph, s0, tid) : 0) * HEAD_DIM);
+                    uint32_t m = 0;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float c0, n0, c1, n1;
-                        rope_cos_sin(pos, a.rope_turns[8 * c + 2 * i], c0, n0);
-                        rope_cos_sin(pos, a.rope_turns[8 * c + 2 * i + 1], c1, n1);
-                        const float2 l = make_float2(bf16lo(lw[i]) * inv, bf16hi(lw[i]) * inv);
-                        const float2 h = make_float2(bf16lo(hw[i]) * inv, bf16hi(hw[i]) * inv);
-                        float2 x = make_float2(l.x * c0 - h.x * n0, l.y * c1 - h.y * n1);
-                        float2 y = make_float2(h.x * c0 + l.x * n0, h.y * c1 + l.y * n1);
-                        if (zero) x = y = make_float2(0.0f, 0.0f);
-#pragma unroll
-                        for (int p = 0; p < PQ_PARTS; ++p) {
-                            pl[p][i >> 1] |= take_part(x) << (16 * (i & 1));
-                            ph[p][i >> 1] |= take_part(y) << (16 * (i & 1));
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        const uint4 w = __ldg(q + i);
+                        m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
                     }
+                    m = max(m & 0xffffu, m >> 16);
+                    const bool bad = m >= Q8_LIMIT_BF16;
+                    const int e = bad ? 0 : q8_exponent(m);
+                    bars->qinv[tid] = bad || !valid ? 0.0f : pow2(-e);
+                    bars->qscale[j][tid] = bad && valid ? __int_as_float(0x7fc00000) : a.qk_scale_log2 * pow2(e);
+                }
+                named_bar_sync(3, 128);
+                // A thread has a position and 8 rotation pairs (dims 8 u .. and 64 + 8 u ..) of its G query
+                // heads, so an angle is computed once for all of them.
+                const int si = tid % rph;
+                const bool valid = s0 + si < a.Sq;
+                const uint32_t pos = valid ? (uint32_t)a.position_ids[(size_t)u.b * a.Sq + s0 + si] : 0;
+                uint8_t* qt = sm + OFF_Q + j * PF_TILE_BYTES;
+#pragma unroll 1
+                for (int ch = tid / rph; ch < 8; ch += a.G) {
+                    float cs[8], sn[8];
 #pragma unroll
-                    for (int p = 0; p < PQ_PARTS; ++p) {
-                        const uint32_t at = p * PQ_CODES + sw128_off(tid, c >> 1) + (c & 1) * 8;
-                        *reinterpret_cast<uint2*>(qt + at) = make_uint2(pl[p][0], pl[p][1]);
-                        *reinterpret_cast<uint2*>(qt + (at ^ 64)) = make_uint2(ph[p][0], ph[p][1]);  // chunk + 4
+                    for (int i = 0; i < 8; ++i) rope_cos_sin(pos, a.rope_turns[8 * ch + i], cs[i], sn[i]);
+                    const uint4* q = reinterpret_cast<const uint4*>(qb + (valid ? query_row(a, u.b, u.kvh, rph, s0, si) : 0) * HEAD_DIM) + ch;
+                    const size_t head = valid ? (size_t)a.Sq * (HEAD_DIM / 8) : 0;  // 16-byte chunks to the next head's row
+                    uint4 lo = __ldg(q), hi = __ldg(q + 8);
+#pragma unroll 1
+                    for (int h = 0; h < a.G; ++h) {
+                        const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+                        q += head;
+                        if (h + 1 < a.G) {
+                            lo = __ldg(q);
+                            hi = __ldg(q + 8);
+                        }
+                        const int r = h * rph + si;
+                        const float inv = bars->qinv[r];
+                        uint32_t ol[4], oh[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float l0 = bf16lo(lw[i]) * inv, l1 = bf16hi(lw[i]) * inv, h0 = bf16lo(hw[i]) * inv, h1 = bf16hi(hw[i]) * inv;
+                            ol[i] = pack_f16x2(l0 * cs[2 * i] - h0 * sn[2 * i], l1 * cs[2 * i + 1] - h1 * sn[2 * i + 1]);
+                            oh[i] = pack_f16x2(h0 * cs[2 * i] + l0 * sn[2 * i], h1 * cs[2 * i + 1] + l1 * sn[2 * i + 1]);
+                        }
+                        // a row that is out of range has 0 times what may be infinite: zeros instead
+                        const bool zero = inv == 0.0f;
+                        const uint32_t at = sw128_off(r, ch);
+                        *reinterpret_cast<uint4*>(qt + at) = zero ? make_uint4(0, 0, 0, 0) : make_uint4(ol[0], ol[1], ol[2], ol[3]);
+                        *reinterpret_cast<uint4*>(qt + 16384 + at) = zero ? make_uint4(0, 0, 0, 0) : make_uint4(oh[0], oh[1], oh[2], oh[3]);
                     }
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(smem_u32(&bars->q_ready[j]));
+                named_bar_sync(3, 128);  // qinv may be written again
             }
-            // ---- V tiles: thread t has 16 codes (chunk c) of every 16th token ----
-            uint32_t nan = 0;
-            const int c = tid & 7, r0 = tid >> 3;
+            // ---- the other tiles ----
 #pragma unroll 1
-            for (int i = 0; i < n_tiles; ++i) {
-                const int g = g0 + i, st = g % VST;
-                if (!(ok = mbar_wait(smem_u32(&bars->c_full[st]), (uint32_t)((g / VST) & 1), pc))) break;
-                if (!(ok = mbar_wait(smem_u32(&bars->v_empty[st]), (uint32_t)(((g / VST) & 1) ^ 1), pc))) break;
-                const uint8_t* vc = sm + OFF_VC + st * PQ_CODES;
-                uint8_t* vt = sm + OFF_V + st * PF_TILE_BYTES;
-                uint4 w[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int t = r0 + 16 * e;
-                    w[e] = i * PF_BN + t < u.n_keys ? *reinterpret_cast<const uint4*>(vc + sw128_off(t, c)) : make_uint4(0, 0, 0, 0);
-                }
-                mbar_arrive(smem_u32(&bars->c_empty[st]));
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // token r0 + 16 e: row r0 of page e; 16 codes: two 16-byte chunks of its half
-                    const uint32_t cw[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        o[2 * k] = e4m3x2_to_f16x2(cw[k]);
-                        o[2 * k + 1] = e4m3x2_to_f16x2(cw[k] >> 16);
-                        // a byte of 0x7f or 0xff: NaN
-                        const uint32_t all = cw[k] & 0x7f7f7f7fu;
-                        nan |= (all + 0x01010101u) & 0x80808080u;
-                    }
-                    uint8_t* row = vt + e * 4096 + (c >> 2) * 2048;
-                    *reinterpret_cast<uint4*>(row + sw128_off(r0, (2 * c) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(row + sw128_off(r0, (2 * c + 1) & 7)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(smem_u32(&bars->v_full[st]));
+            for (int i = 1; i < n_tiles; ++i) {
+                load(next);
+                next = page_ids(i + 1);
+                convert(i);
+                if (!ok) break;
             }
-            if (!ok) break;
             const int slot = wu & 1;
-            if (!(ok = mbar_wait(smem_u32(&bars->r_empty[slot]), (uint32_t)(((wu >> 1) & 1) ^ 1), pc))) break;
-            bars->r_flag[slot][tid] = nan ? 1 : 0;
-            mbar_arrive(smem_u32(&bars->r_full[slot]));
+            if (wait(bars->r_empty[slot], (wu >> 1) ^ 1)) {
+                bars->r_flag[slot][tid] = (uint8_t)odd;
+                mbar_arrive(smem_u32(&bars->r_full[slot]));
+            }
             g0 += n_tiles;
             ++wu;
         }
@@ -629,7 +620,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                     uint32_t any = 0;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) any |= f[q].x | f[q].y | f[q].z | f[q].w;
-                    unit_bad = (any ? RK_STATUS_RANGE : 0) | (bars->r_flag[slot][128] ? RK_STATUS_SCALE : 0);
+                    unit_bad = (any & 0x01010101u ? RK_STATUS_RANGE : 0) | (any & 0x02020202u ? RK_STATUS_SCALE : 0);
                     mbar_arrive(smem_u32(&bars->r_empty[slot]));
                 }
             }
@@ -697,7 +688,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
 
 }  // namespace
 
-cudaError_t launch_prefill_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream) {
+cudaError_t launch_prefill_q8(const AttnQ8Args& a, cudaStream_t stream) {
     static std::atomic<uint64_t> configured{0};
     static std::atomic<int> sm_count[64];
     int dev = 0, nsm = 0;
@@ -716,7 +707,7 @@ cudaError_t launch_prefill_q8(const CUtensorMap& km, const CUtensorMap& vm, cons
     const int rph = PF_BM / a.G, n_qtiles = (a.Sq + rph - 1) / rph;
     const long long units = (long long)a.B * a.Hkv * ((n_qtiles + 1) / 2);
     if (units <= 0) return cudaSuccess;
-    prefill_q8_kernel<<<(unsigned)(units < nsm ? units : nsm), PQ_THREADS, PQ_SMEM_BYTES, stream>>>(km, vm, a);
+    prefill_q8_kernel<<<(unsigned)(units < nsm ? units : nsm), PQ_THREADS, PQ_SMEM_BYTES, stream>>>(a);
     return cudaGetLastError();
 }
 

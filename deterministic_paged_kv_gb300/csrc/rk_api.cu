@@ -33,7 +33,7 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream);
 cudaError_t launch_append_q8(const AppendQ8Args& a, cudaStream_t stream);
 int decode_q8_bundle(int Hkv);
 cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream);
-cudaError_t launch_prefill_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream);
+cudaError_t launch_prefill_q8(const AttnQ8Args& a, cudaStream_t stream);
 }  // namespace rk
 
 namespace {
@@ -220,6 +220,12 @@ int make_page_map(CUtensorMap* m, const void* cache, int num_pages, int Hkv, con
 // page): one box is a page of `heads` neighbouring heads, landing as [half][head]
 // blocks of 8 swizzled rows of 128 bytes.
 int make_q8_map(CUtensorMap* m, const void* cache, int num_pages, int Hkv, int heads, const char* what) {
+    if (heads == 1) {  // a block is 2 KiB in a row
+        const cuuint64_t dims[3] = {(cuuint64_t)rk::HEAD_DIM, (cuuint64_t)rk::PAGE, (cuuint64_t)num_pages * Hkv};
+        const cuuint64_t strides[2] = {(cuuint64_t)rk::HEAD_DIM, (cuuint64_t)rk::Q8_BLOCK_BYTES};
+        const cuuint32_t box[3] = {(cuuint32_t)rk::HEAD_DIM, (cuuint32_t)rk::PAGE, 1};
+        return make_map(m, cache, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, what, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+    }
     const cuuint64_t dims[5] = {(cuuint64_t)rk::HEAD_DIM, 8, (cuuint64_t)Hkv, 2, (cuuint64_t)num_pages};
     const cuuint64_t strides[4] = {(cuuint64_t)rk::HEAD_DIM, (cuuint64_t)rk::Q8_BLOCK_BYTES,
                                    (cuuint64_t)rk::Q8_BLOCK_BYTES / 2, (cuuint64_t)Hkv * rk::Q8_BLOCK_BYTES};
@@ -1138,9 +1144,7 @@ int rk_paged_attn_prefill_q8(const rk_paged_plan_t* plan, const void* q, const v
     int rc = attn_q8_args(plan, q, k_cache, v_cache, k_scale, v_scale, block_table_d, kv_lens_d, position_ids_d, out, lse,
                           status_d, &a);
     if (rc || plan->B == 0) return rc;
-    CUtensorMap km, vm;
-    if ((rc = make_q8_maps(&km, &vm, plan, q, k_cache, v_cache, 1))) return rc;
-    cudaError_t e = rk::launch_prefill_q8(km, vm, a, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = rk::launch_prefill_q8(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(RK_E_CUDA, "8-bit prefill launch: %s", cudaGetErrorString(e));
     return RK_OK;
 }

@@ -17,9 +17,10 @@ i32 = torch.int32
 # a part is exact to 2^-10, of at least 2^7 for the largest q (two parts at 2^-8: 2^-25) and
 # 2^8 for the largest weight of a split of 512: 512 2^-18.
 DECODE = dict(q_rel=2.0 ** -14, q_abs=2.0 ** -24, p_rel=2.0 ** -11, p_abs=2.0 ** -9)
-# Prefill: q as three parts (2^-12; 2^-10 of 2^7), weights in 16 bits (2^-9 with their sums),
-# to 2^-25 of the largest weight for each of up to 2^13 keys.
-PREFILL = dict(q_rel=2.0 ** -11, q_abs=2.0 ** -16, p_rel=2.0 ** -8, p_abs=2.0 ** -12)
+# Prefill: q in FP16 (2^-11, with the FP32 rotation and exponent 2^-16 more), weights in FP16
+# (2^-11, with their sums 2^-10; their least step, 2^-25 of weights of which the largest is at least
+# 2^7, for each of up to 2^13 keys: 2^-19).
+PREFILL = dict(q_rel=2.0 ** -11 + 2.0 ** -16, q_abs=2.0 ** -24, p_rel=2.0 ** -10, p_abs=2.0 ** -19)
 
 
 @pytest.fixture(scope="module", autouse=True)
