@@ -23,7 +23,10 @@
 //   warp 15      scheduler: each unit's metadata, published as a descriptor (two slots);
 //   warpgroup 0  transform: q of both q-tiles of a unit (as soon as the unit before has read
 //                its own), K and V tiles from the cache to FP16 operands (V zero past the last
-//                key), a tile's codes in registers while the one before is in use; scales;
+//                key), scales.  Codes come by cp.async, a thread's own 16 bytes of each page,
+//                a tile ahead, and are converted in a rolled loop (with the codes in
+//                registers and the loop unrolled the code pushed the softmax's out of the
+//                instruction cache: 615 us, the softmax twice as slow);
 //   warpgroups 1, 2  softmax of q-tile 0, 1: a thread per accumulator row;
 //   warp 13      MMA issuer (converged); warps 12, 14 have nothing to do.
 // Nothing depends on B, W or the grid.
@@ -37,20 +40,21 @@ namespace {
 
 constexpr int PQ_THREADS = 512;
 constexpr int WARP_MMA = 13, WARP_SCHED = 15;
-constexpr int KST = 2, VST = 3;                 // K stages, V stages
+constexpr int KST = 2, VST = 2;                 // K stages, V stages
 constexpr int SCST = 4;                         // scale slots: one more than K stages at least
 constexpr uint32_t TMEM_COLS = 512;             // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512)
 constexpr float RESCALE_SLACK = 8.0f, P_BIAS = 7.0f;
 constexpr uint32_t UNIT_READERS = 32 + 128 + 256;
 
 // setmaxnreg split (sum 4 x 128 = the 512 x 128 registers the CTA launches with)
-constexpr int REG_XFORM = 104, REG_SOFTMAX = 176, REG_CTRL = 56;
+constexpr int REG_XFORM = 88, REG_SOFTMAX = 184, REG_CTRL = 56;
 static_assert(REG_XFORM + 2 * REG_SOFTMAX + REG_CTRL == 4 * 128, "register split must sum to the launch budget");
 
 constexpr int OFF_Q = 0;                             // [q-tile][64-dim half][128 rows][128 B]
 constexpr int OFF_K = OFF_Q + 2 * PF_TILE_BYTES;     // [64-dim half][128 rows][128 B]
 constexpr int OFF_V = OFF_K + KST * PF_TILE_BYTES;   // [page][64-dim half][16 rows][128 B]
-constexpr int OFF_BAR = OFF_V + VST * PF_TILE_BYTES;
+constexpr int OFF_C = OFF_V + VST * PF_TILE_BYTES;   // codes of the next tile: K, V (128 rows of 128 B each)
+constexpr int OFF_BAR = OFF_C + 2 * PF_BN * HEAD_DIM;
 
 struct PqUnit {
     int end, b, kvh, pair;
@@ -165,6 +169,25 @@ __device__ __forceinline__ bool read_unit(PqBars* bars, int k, PipeCtl* pc, PqUn
     u.bad = src->bad;
     mbar_arrive(smem_u32(&bars->u_empty[slot]));
     return true;
+}
+
+// Transpose of 16-byte elements among lanes 4 k .. 4 k + 3: lane i's element q becomes lane
+// q's element i.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4][4], int i) {
+#pragma unroll
+    for (int b = 1; b < 4; b <<= 1)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (!(q & b)) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool up = i & b;  // keeps q | b, gives q
+                    const uint32_t give = up ? w[q][e] : w[q | b][e];
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, b);
+                    if (up) w[q][e] = got;
+                    else w[q | b][e] = got;
+                }
+            }
 }
 
 __global__ void __launch_bounds__(PQ_THREADS, 1)
@@ -343,38 +366,41 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 return p < n_pages ? __ldg(bt + p) : -1;
             };
             uint32_t odd = 0;  // 1: NaN code in V, 2: a scale that is none
-            uint4 kw[8], vw[8];
             float ks = 1.0f, vs = 1.0f;
-            auto load = [&](int ids) {
+            uint8_t* codes = sm + OFF_C + r0 * HEAD_DIM + c * 16;  // the thread's chunk of page 0, K; pages 2 KiB, V 16 KiB on
+            const uint32_t codes_s = smem_u32(codes);
+            auto load_part = [&](int ids, int part) {  // K (0) or V (1) codes of a tile
+                const uint8_t* cache = part ? a.v_cache : a.k_cache;
+                const uint32_t dst = codes_s + part * PF_BN * HEAD_DIM;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int id = __shfl_sync(0xffffffffu, ids, e);
-                    const size_t at = (size_t)id * page_bytes + in_block;
-                    kw[e] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.k_cache + at)) : make_uint4(0, 0, 0, 0);
-                    vw[e] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.v_cache + at)) : make_uint4(0, 0, 0, 0);
+                    if (id >= 0) cp_async16(dst + e * Q8_BLOCK_BYTES, cache + (size_t)id * page_bytes + in_block);
                 }
+                cp_async_commit();
+            };
+            auto load_scales = [&](int ids) {
                 ks = vs = 1.0f;
                 if (tid < 8 && ids >= 0) {
                     ks = __ldg(a.k_scale + (size_t)ids * a.Hkv + u.kvh);
                     vs = __ldg(a.v_scale + (size_t)ids * a.Hkv + u.kvh);
                 }
             };
-            // Tile i of the unit from the registers to its operands.
-            auto convert = [&](int i) {
+            // Tile i of the unit from its codes to its operands; `next`: the pages of the tile after it,
+            // whose codes are fetched as soon as this tile's have been read.
+            auto convert = [&](int i, int next) {
                 const int g = g0 + i, kst = g % KST, vst = g % VST;
                 if (!wait(bars->k_empty[kst], (g / KST) ^ 1)) return;
-                uint8_t* kt = sm + OFF_K + kst * PF_TILE_BYTES + (c >> 2) * 16384;
-#pragma unroll
+                cp_async_wait<1>();  // K is here (V, committed after it, may not be)
+                uint8_t* kt = sm + OFF_K + kst * PF_TILE_BYTES + (c >> 2) * 16384 + r0 * 128;
+                const uint32_t c0 = ((2 * c & 7) ^ (r0 & 7)) << 4, c1 = c0 ^ 16;  // swizzled 16-byte chunks of the row
+#pragma unroll 1
                 for (int e = 0; e < 8; ++e) {
-                    const uint32_t w[4] = {kw[e].x, kw[e].y, kw[e].z, kw[e].w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        o[2 * k] = e4m3x2_to_f16x2(w[k]);
-                        o[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
-                    }
-                    *reinterpret_cast<uint4*>(kt + sw128_off(r0 + 16 * e, (2 * c) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(kt + sw128_off(r0 + 16 * e, (2 * c + 1) & 7)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    const uint4 w = *reinterpret_cast<const uint4*>(codes + e * Q8_BLOCK_BYTES);
+                    *reinterpret_cast<uint4*>(kt + e * 2048 + c0) =
+                        make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
+                    *reinterpret_cast<uint4*>(kt + e * 2048 + c1) =
+                        make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w), e4m3x2_to_f16x2(w.w >> 16));
                 }
                 if (tid < 8) {
                     // The slot's readers of SCST tiles ago are done: the stage of K was free, so S of tile
@@ -389,80 +415,89 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(smem_u32(&bars->k_full[kst]));
+                load_part(next, 0);
+                load_scales(next);
                 if (!wait(bars->v_empty[vst], (g / VST) ^ 1)) return;
-                uint8_t* vt = sm + OFF_V + vst * PF_TILE_BYTES + (c >> 2) * 2048;
-#pragma unroll
+                cp_async_wait<1>();
+                uint8_t* vt = sm + OFF_V + vst * PF_TILE_BYTES + (c >> 2) * 2048 + r0 * 128;
+                uint32_t nan = 0;
+#pragma unroll 1
                 for (int e = 0; e < 8; ++e) {
-                    const bool in = i * PF_BN + 16 * e + r0 < u.n_keys;  // zeros past the last key: 0 times a NaN is not 0
-                    const uint32_t w[4] = {vw[e].x, vw[e].y, vw[e].z, vw[e].w};
-                    uint32_t o[8], nan = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t x = in ? w[k] : 0u;
-                        o[2 * k] = e4m3x2_to_f16x2(x);
-                        o[2 * k + 1] = e4m3x2_to_f16x2(x >> 16);
-                        nan |= (x & 0x7f7f7f7fu) + 0x01010101u;  // a byte of 0x7f or 0xff: NaN
-                    }
-                    if (nan & 0x80808080u) odd |= 1;
-                    *reinterpret_cast<uint4*>(vt + e * 4096 + sw128_off(r0, (2 * c) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(vt + e * 4096 + sw128_off(r0, (2 * c + 1) & 7)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    uint4 w = *reinterpret_cast<const uint4*>(codes + PF_BN * HEAD_DIM + e * Q8_BLOCK_BYTES);
+                    if (i * PF_BN + 16 * e + r0 >= u.n_keys) w = make_uint4(0, 0, 0, 0);  // 0 times a NaN is not 0
+                    // a byte of 0x7f or 0xff: NaN
+                    nan |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
+                           ((w.z & 0x7f7f7f7fu) + 0x01010101u) | ((w.w & 0x7f7f7f7fu) + 0x01010101u);
+                    *reinterpret_cast<uint4*>(vt + e * 4096 + c0) =
+                        make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
+                    *reinterpret_cast<uint4*>(vt + e * 4096 + c1) =
+                        make_uint4(e4m3x2_to_f16x2(w.z), e4m3x2_to_f16x2(w.z >> 16), e4m3x2_to_f16x2(w.w), e4m3x2_to_f16x2(w.w >> 16));
                 }
+                if (nan & 0x80808080u) odd |= 1;
                 fence_proxy_async_smem();
                 mbar_arrive(smem_u32(&bars->v_full[vst]));
+                load_part(next, 1);
             };
             // ---- the unit's first tile, while the unit before is still at work ----
-            load(page_ids(0));
-            int next = page_ids(1);
-            convert(0);
+            int next = page_ids(0);
+            load_part(next, 0);
+            load_part(next, 1);
+            load_scales(next);
+            next = page_ids(1);
+            convert(0, next);
+            next = page_ids(2);
             // ---- q ----
             wait(bars->q_empty, wu ^ 1);
             if (named_bar_or(3, 128, !ok)) {
                 ok = false;
                 break;
             }
+            // Both q-tiles by cp.async (rows past the last query as zeros), then rewritten in place.
+            cp_async_wait_all();  // (the next tile's codes too)
+#pragma unroll 1
+            for (int i = tid; i < 2 * PF_BM * 16; i += 128) {
+                const int j = i >> 11, r = (i >> 4) & 127, ch = i & 15, s0 = (2 * u.pair + j) * rph;
+                const bool in = s0 + r % rph < a.Sq;
+                const __nv_bfloat16* src =
+                    reinterpret_cast<const __nv_bfloat16*>(a.q) + (in ? query_row(a, u.b, u.kvh, rph, s0, r) : 0) * HEAD_DIM + ch * 8;
+                cp_async16_or_zero(s_base + OFF_Q + j * PF_TILE_BYTES + (ch >> 3) * 16384 + sw128_off(r, ch & 7), src, in);
+            }
+            cp_async_commit();
+            cp_async_wait_all();
+            named_bar_sync(3, 128);
 #pragma unroll 1
             for (int j = 0; j < 2; ++j) {
                 const int s0 = (2 * u.pair + j) * rph;
-                const __nv_bfloat16* qb = reinterpret_cast<const __nv_bfloat16*>(a.q);
+                uint8_t* qt = sm + OFF_Q + j * PF_TILE_BYTES;
                 {   // the largest element of row tid
-                    const bool valid = s0 + tid % rph < a.Sq;
-                    const uint4* q = reinterpret_cast<const uint4*>(qb + (valid ? query_row(a, u.b, u.kvh, rph, s0, tid) : 0) * HEAD_DIM);
                     uint32_t m = 0;
-#pragma unroll
+#pragma unroll 4
                     for (int i = 0; i < 16; ++i) {
-                        const uint4 w = __ldg(q + i);
+                        const uint4 w = *reinterpret_cast<const uint4*>(qt + (i >> 3) * 16384 + sw128_off(tid, i & 7));
                         m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
                     }
                     m = max(m & 0xffffu, m >> 16);
                     const bool bad = m >= Q8_LIMIT_BF16;
                     const int e = bad ? 0 : q8_exponent(m);
-                    bars->qinv[tid] = bad || !valid ? 0.0f : pow2(-e);
-                    bars->qscale[j][tid] = bad && valid ? __int_as_float(0x7fc00000) : a.qk_scale_log2 * pow2(e);
+                    bars->qinv[tid] = bad ? 0.0f : pow2(-e);
+                    bars->qscale[j][tid] = bad ? __int_as_float(0x7fc00000) : a.qk_scale_log2 * pow2(e);
                 }
                 named_bar_sync(3, 128);
-                // A thread has a position and 8 rotation pairs (dims 8 u .. and 64 + 8 u ..) of its G query
+                // A thread has a position and 8 rotation pairs (dims 8 ch .. and 64 + 8 ch ..) of its G query
                 // heads, so an angle is computed once for all of them.
                 const int si = tid % rph;
-                const bool valid = s0 + si < a.Sq;
-                const uint32_t pos = valid ? (uint32_t)a.position_ids[(size_t)u.b * a.Sq + s0 + si] : 0;
-                uint8_t* qt = sm + OFF_Q + j * PF_TILE_BYTES;
+                const uint32_t pos = s0 + si < a.Sq ? (uint32_t)a.position_ids[(size_t)u.b * a.Sq + s0 + si] : 0;
 #pragma unroll 1
                 for (int ch = tid / rph; ch < 8; ch += a.G) {
                     float cs[8], sn[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) rope_cos_sin(pos, a.rope_turns[8 * ch + i], cs[i], sn[i]);
-                    const uint4* q = reinterpret_cast<const uint4*>(qb + (valid ? query_row(a, u.b, u.kvh, rph, s0, si) : 0) * HEAD_DIM) + ch;
-                    const size_t head = valid ? (size_t)a.Sq * (HEAD_DIM / 8) : 0;  // 16-byte chunks to the next head's row
-                    uint4 lo = __ldg(q), hi = __ldg(q + 8);
 #pragma unroll 1
-                    for (int h = 0; h < a.G; ++h) {
+                    for (int r = si; r < PF_BM; r += rph) {
+                        uint4* pl = reinterpret_cast<uint4*>(qt + sw128_off(r, ch));
+                        uint4* ph = reinterpret_cast<uint4*>(qt + 16384 + sw128_off(r, ch));
+                        const uint4 lo = *pl, hi = *ph;
                         const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
-                        q += head;
-                        if (h + 1 < a.G) {
-                            lo = __ldg(q);
-                            hi = __ldg(q + 8);
-                        }
-                        const int r = h * rph + si;
                         const float inv = bars->qinv[r];
                         uint32_t ol[4], oh[4];
 #pragma unroll
@@ -473,9 +508,8 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                         }
                         // a row that is out of range has 0 times what may be infinite: zeros instead
                         const bool zero = inv == 0.0f;
-                        const uint32_t at = sw128_off(r, ch);
-                        *reinterpret_cast<uint4*>(qt + at) = zero ? make_uint4(0, 0, 0, 0) : make_uint4(ol[0], ol[1], ol[2], ol[3]);
-                        *reinterpret_cast<uint4*>(qt + 16384 + at) = zero ? make_uint4(0, 0, 0, 0) : make_uint4(oh[0], oh[1], oh[2], oh[3]);
+                        *pl = zero ? make_uint4(0, 0, 0, 0) : make_uint4(ol[0], ol[1], ol[2], ol[3]);
+                        *ph = zero ? make_uint4(0, 0, 0, 0) : make_uint4(oh[0], oh[1], oh[2], oh[3]);
                     }
                 }
                 fence_proxy_async_smem();
@@ -485,11 +519,12 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
             // ---- the other tiles ----
 #pragma unroll 1
             for (int i = 1; i < n_tiles; ++i) {
-                load(next);
-                next = page_ids(i + 1);
-                convert(i);
+                const int after = next;
+                next = page_ids(i + 2);
+                convert(i, after);
                 if (!ok) break;
             }
+            cp_async_wait_all();
             const int slot = wu & 1;
             if (wait(bars->r_empty[slot], (wu >> 1) ^ 1)) {
                 bars->r_flag[slot][tid] = (uint8_t)odd;
@@ -644,23 +679,36 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
             if (nt > 0) {
                 tc_fence_after();
                 const float inv_l = fail || !seen ? 0.0f : 1.0f / l;
-                uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (valid ? row : 0) * HEAD_DIM);
+                // A thread has a row, so its 16-byte stores would meet 32 lines a warp; four lanes swap their
+                // four chunks of 32 columns first and write 64 bytes of a row at a time.
+                const int l4 = lane & 3;
+                size_t rows[4];
+                bool in[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int re = (r & ~3) + e;
+                    in[e] = s0 + re % rph < a.Sq;
+                    rows[e] = in[e] ? query_row(a, un->b, un->kvh, rph, s0, re) : 0;
+                }
 #pragma unroll 1
                 for (int c4 = 0; c4 < 4; ++c4) {
                     uint32_t rr[32];
                     tmem_ld32(tO + lane_addr + c4 * 32, rr);
                     tmem_ld_wait();
-                    if (valid) {
+                    uint32_t w[4][4];  // [chunk][word], after the swap [row of the four][word]
 #pragma unroll
-                        for (int q = 0; q < 32; q += 8) {
-                            uint32_t w[4];
+                    for (int q = 0; q < 4; ++q)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = fail || !seen ? 0u
-                                                     : pack_bf16x2(__uint_as_float(rr[q + 2 * e]) * inv_l, __uint_as_float(rr[q + 2 * e + 1]) * inv_l);
-                            o[(c4 * 32 + q) / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    }
+                        for (int e = 0; e < 4; ++e)
+                            w[q][e] = fail || !seen ? 0u
+                                                    : pack_bf16x2(__uint_as_float(rr[8 * q + 2 * e]) * inv_l,
+                                                                  __uint_as_float(rr[8 * q + 2 * e + 1]) * inv_l);
+                    transpose4(w, l4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (in[e])
+                            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + rows[e] * HEAD_DIM + c4 * 32 + l4 * 8) =
+                                make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
                 }
                 // O_j has been read: the next unit's first PV may overwrite it
                 tc_fence_before();

@@ -123,6 +123,11 @@ __device__ __forceinline__ void arrive_expect_tx_elect(uint32_t bar, uint32_t by
         : "memory");
 }
 
+// 16-byte asynchronous copy, or 16 zero bytes.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool copy) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(copy ? 16 : 0) : "memory");
+}
+
 // 32 lanes x one 32-bit column.
 __device__ __forceinline__ void tmem_ld1(uint32_t taddr, uint32_t& r) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
