@@ -92,9 +92,10 @@ __device__ __forceinline__ void unit_place(const AttnQ8Args& a, int n_qtiles, lo
     kvh = rem % a.Hkv;
 }
 
-// Row r of a q-tile from query s0 on: query head kvh * G + r / rph, query s0 + r % rph.
-__device__ __forceinline__ size_t query_row(const AttnQ8Args& a, int b, int kvh, int rph, int s0, int r) {
-    return ((size_t)b * a.Hq + kvh * a.G + r / rph) * a.Sq + s0 + r % rph;
+// Row r of a q-tile from query s0 on: query head kvh * G + r / rph, query s0 + (r & (rph - 1)), with
+// rph = 128 / G = 1 << rsh queries to a tile.
+__device__ __forceinline__ size_t query_row(const AttnQ8Args& a, int b, int kvh, int rsh, int s0, int r) {
+    return ((size_t)b * a.Hq + kvh * a.G + (r >> rsh)) * a.Sq + s0 + (r & ((1 << rsh) - 1));
 }
 
 __device__ __forceinline__ void write_row(const AttnQ8Args& a, size_t row, float lse) {
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
     PqBars* bars = reinterpret_cast<PqBars*>(sm + OFF_BAR);
     const uint32_t s_base = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
-    const int rph = PF_BM / a.G, n_qtiles = (a.Sq + rph - 1) / rph;
+    const int rph = PF_BM / a.G, rsh = 31 - __clz(rph), n_qtiles = (a.Sq + rph - 1) >> rsh;
     const int cta = (int)blockIdx.x, grid = (int)gridDim.x;
     const long long total = (long long)a.B * a.Hkv * ((n_qtiles + 1) / 2);
     PqUnit first{};
@@ -280,32 +281,34 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 const int nt0 = __shfl_sync(0xffffffffu, u.nt0, 0), nt1 = __shfl_sync(0xffffffffu, u.nt1, 0);
                 const int n_tiles = max(nt0, nt1);
                 if (__any_sync(0xffffffffu, u.bad != 0) || n_tiles == 0) continue;
-                // O_j (+)= P_j(i) V(i); the unit's first PV into O_j waits for the epilogue before it
+                // O_j (+)= P_j(i) V(i); the unit's first PV into O_j waits for the epilogue before it.
+                // P comes last: what follows it (PV, then S of the next tile) is the q-tile's chain,
+                // and K and V are there long before.
                 auto issue_pv = [&](int j, int i) -> bool {
-                    const int g = g0 + i;
                     if (i == 0 && !wait(bars->o_free[j], (ph >> (4 + j)) ^ 1u)) return false;
-                    if (!wait(bars->v_full[g % VST], (uint32_t)(g / VST))) return false;
                     if (!wait(bars->p_ready[j], (ph >> (2 + j)) ^ (uint32_t)i)) return false;
                     tc_fence_after();
-                    mma_ts_steps<0, 8, MN_MAJOR_PAGE, true>(tmem + 256 + j * 128, tmem + j * 128, dV + (uint32_t)(g % VST) * TILE, idO,
-                                                            i > 0 ? 1u : 0u);
+                    mma_ts_steps<0, 8, MN_MAJOR_PAGE, true>(tmem + 256 + j * 128, tmem + j * 128, dV + (uint32_t)((g0 + i) % VST) * TILE,
+                                                            idO, i > 0 ? 1u : 0u);
                     return true;
                 };
 #pragma unroll 1
                 for (int i = 0; i < n_tiles && ok; ++i) {
                     const int g = g0 + i;
+                    if (i > 0 && !(ok = wait(bars->v_full[(g - 1) % VST], (uint32_t)((g - 1) / VST)))) break;
+                    if (!(ok = wait(bars->k_full[g % KST], (uint32_t)(g / KST)))) break;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int j = 0; j < 2 && ok; ++j) {
                         const int nt = j ? nt1 : nt0;
                         if (i > nt || nt == 0) continue;
+                        if (i == 0 && !(ok = wait(bars->q_ready[j], ph))) break;
                         if (i > 0 && !(ok = issue_pv(j, i - 1))) break;
                         if (i == nt) {
                             umma_commit_elect(smem_u32(&bars->o_done[j]));
                             continue;
                         }
-                        if (i == 0 && !(ok = wait(bars->q_ready[j], ph))) break;
-                        if (!(ok = wait(bars->k_full[g % KST], (uint32_t)(g / KST)))) break;
-                        tc_fence_after();
+                        if (i == 0) tc_fence_after();
                         mma_ss_steps<0, 8, K_MAJOR_128, K_MAJOR_128, true>(tmem + j * 128, dQ + (uint32_t)j * TILE,
                                                                            dK + (uint32_t)(g % KST) * TILE, idS, 0u);
                         umma_commit_elect(smem_u32(&bars->s_full[j]));
@@ -315,6 +318,8 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                     if (i > 0) umma_commit_elect(smem_u32(&bars->v_empty[(g - 1) % VST]));      // V(i-1) read by PV(i-1)
                     if (i == n_tiles - 1) umma_commit_elect(smem_u32(&bars->q_empty));          // the unit's last S read q
                 }
+                if (!ok || !(ok = wait(bars->v_full[(g0 + n_tiles - 1) % VST], (uint32_t)((g0 + n_tiles - 1) / VST)))) break;
+                tc_fence_after();
 #pragma unroll 1
                 for (int j = 0; j < 2 && ok; ++j) {
                     if ((j ? nt1 : nt0) != n_tiles) continue;
@@ -457,9 +462,9 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
 #pragma unroll 1
             for (int i = tid; i < 2 * PF_BM * 16; i += 128) {
                 const int j = i >> 11, r = (i >> 4) & 127, ch = i & 15, s0 = (2 * u.pair + j) * rph;
-                const bool in = s0 + r % rph < a.Sq;
+                const bool in = s0 + (r & (rph - 1)) < a.Sq;
                 const __nv_bfloat16* src =
-                    reinterpret_cast<const __nv_bfloat16*>(a.q) + (in ? query_row(a, u.b, u.kvh, rph, s0, r) : 0) * HEAD_DIM + ch * 8;
+                    reinterpret_cast<const __nv_bfloat16*>(a.q) + (in ? query_row(a, u.b, u.kvh, rsh, s0, r) : 0) * HEAD_DIM + ch * 8;
                 cp_async16_or_zero(s_base + OFF_Q + j * PF_TILE_BYTES + (ch >> 3) * 16384 + sw128_off(r, ch & 7), src, in);
             }
             cp_async_commit();
@@ -485,10 +490,10 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 named_bar_sync(3, 128);
                 // A thread has a position and 8 rotation pairs (dims 8 ch .. and 64 + 8 ch ..) of its G query
                 // heads, so an angle is computed once for all of them.
-                const int si = tid % rph;
+                const int si = tid & (rph - 1);
                 const uint32_t pos = s0 + si < a.Sq ? (uint32_t)a.position_ids[(size_t)u.b * a.Sq + s0 + si] : 0;
 #pragma unroll 1
-                for (int ch = tid / rph; ch < 8; ch += a.G) {
+                for (int ch = tid >> rsh; ch < 8; ch += a.G) {
                     float cs[8], sn[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) rope_cos_sin(pos, a.rope_turns[8 * ch + i], cs[i], sn[i]);
@@ -551,10 +556,10 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->u_full[uslot]), (uint32_t)((kk >> 1) & 1), pc)))) break;
             const volatile PqUnit* un = &bars->unit[uslot];
             if (un->end) break;
-            const int s0 = (2 * un->pair + j) * rph, s = s0 + r % rph;
+            const int s0 = (2 * un->pair + j) * rph, s = s0 + (r & (rph - 1));
             const bool valid = s < a.Sq;
             const int n_tiles = max(un->nt0, un->nt1), nt = j ? un->nt1 : un->nt0;
-            const size_t row = query_row(a, un->b, un->kvh, rph, s0, r);
+            const size_t row = query_row(a, un->b, un->kvh, rsh, s0, r);
             if (un->bad || n_tiles == 0) {
                 if (valid) write_row(a, row, un->bad ? nanv : -INFINITY);
                 mbar_arrive(smem_u32(&bars->u_empty[uslot]));
@@ -667,7 +672,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                     int b2, kvh2, pair2;
                     unit_place(a, n_qtiles, u2, b2, kvh2, pair2);
                     const int t0 = (2 * pair2 + j) * rph;
-                    if (t0 + r % rph < a.Sq) write_row(a, query_row(a, b2, kvh2, rph, t0, r), nanv);
+                    if (t0 + (r & (rph - 1)) < a.Sq) write_row(a, query_row(a, b2, kvh2, rsh, t0, r), nanv);
                 }
                 if (r == 0 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
                 break;
@@ -687,8 +692,8 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int re = (r & ~3) + e;
-                    in[e] = s0 + re % rph < a.Sq;
-                    rows[e] = in[e] ? query_row(a, un->b, un->kvh, rph, s0, re) : 0;
+                    in[e] = s0 + (re & (rph - 1)) < a.Sq;
+                    rows[e] = in[e] ? query_row(a, un->b, un->kvh, rsh, s0, re) : 0;
                 }
 #pragma unroll 1
                 for (int c4 = 0; c4 < 4; ++c4) {
