@@ -398,10 +398,15 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 if (!wait(bars->k_empty[kst], (g / KST) ^ 1)) return;
                 cp_async_wait<1>();  // K is here (V, committed after it, may not be)
                 uint8_t* kt = sm + OFF_K + kst * PF_TILE_BYTES + (c >> 2) * 16384 + r0 * 128;
-                const uint32_t c0 = ((2 * c & 7) ^ (r0 & 7)) << 4, c1 = c0 ^ 16;  // swizzled 16-byte chunks of the row
+                // The 16 codes are chunks 2 c, 2 c + 1 (of 16 bytes, swizzled) of a half's row; lanes of the
+                // upper half store theirs the other way round, so that 8 lanes meet 8 chunks.
+                const bool up = c >= 4;
+                const uint32_t c0 = (((2 * c & 7) ^ (r0 & 7)) << 4) ^ (up ? 16u : 0u), c1 = c0 ^ 16;
+                uint4 ahead = *reinterpret_cast<const uint4*>(codes);
 #pragma unroll 1
                 for (int e = 0; e < 8; ++e) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(codes + e * Q8_BLOCK_BYTES);
+                    const uint4 w = up ? make_uint4(ahead.z, ahead.w, ahead.x, ahead.y) : ahead;
+                    ahead = *reinterpret_cast<const uint4*>(codes + min(e + 1, 7) * Q8_BLOCK_BYTES);
                     *reinterpret_cast<uint4*>(kt + e * 2048 + c0) =
                         make_uint4(e4m3x2_to_f16x2(w.x), e4m3x2_to_f16x2(w.x >> 16), e4m3x2_to_f16x2(w.y), e4m3x2_to_f16x2(w.y >> 16));
                     *reinterpret_cast<uint4*>(kt + e * 2048 + c1) =
@@ -426,9 +431,11 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 cp_async_wait<1>();
                 uint8_t* vt = sm + OFF_V + vst * PF_TILE_BYTES + (c >> 2) * 2048 + r0 * 128;
                 uint32_t nan = 0;
+                ahead = *reinterpret_cast<const uint4*>(codes + PF_BN * HEAD_DIM);
 #pragma unroll 1
                 for (int e = 0; e < 8; ++e) {
-                    uint4 w = *reinterpret_cast<const uint4*>(codes + PF_BN * HEAD_DIM + e * Q8_BLOCK_BYTES);
+                    uint4 w = up ? make_uint4(ahead.z, ahead.w, ahead.x, ahead.y) : ahead;
+                    ahead = *reinterpret_cast<const uint4*>(codes + PF_BN * HEAD_DIM + min(e + 1, 7) * Q8_BLOCK_BYTES);
                     if (i * PF_BN + 16 * e + r0 >= u.n_keys) w = make_uint4(0, 0, 0, 0);  // 0 times a NaN is not 0
                     // a byte of 0x7f or 0xff: NaN
                     nan |= ((w.x & 0x7f7f7f7fu) + 0x01010101u) | ((w.y & 0x7f7f7f7fu) + 0x01010101u) |
@@ -460,12 +467,16 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
             // Both q-tiles by cp.async (rows past the last query as zeros), then rewritten in place.
             cp_async_wait_all();  // (the next tile's codes too)
 #pragma unroll 1
-            for (int i = tid; i < 2 * PF_BM * 16; i += 128) {
-                const int j = i >> 11, r = (i >> 4) & 127, ch = i & 15, s0 = (2 * u.pair + j) * rph;
-                const bool in = s0 + (r & (rph - 1)) < a.Sq;
-                const __nv_bfloat16* src =
-                    reinterpret_cast<const __nv_bfloat16*>(a.q) + (in ? query_row(a, u.b, u.kvh, rsh, s0, r) : 0) * HEAD_DIM + ch * 8;
-                cp_async16_or_zero(s_base + OFF_Q + j * PF_TILE_BYTES + (ch >> 3) * 16384 + sw128_off(r, ch & 7), src, in);
+            for (int j = 0; j < 2; ++j) {
+                const int s0 = (2 * u.pair + j) * rph, ch = tid & 15;  // 16-byte chunk ch of rows tid / 16 + 8 i
+                const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q) + query_row(a, u.b, u.kvh, rsh, s0, 0) * HEAD_DIM + ch * 8;
+                const uint32_t dst = s_base + OFF_Q + j * PF_TILE_BYTES + (ch >> 3) * 16384;
+#pragma unroll 4
+                for (int r = tid >> 4; r < PF_BM; r += 8) {
+                    const int si = r & (rph - 1);
+                    const bool in = s0 + si < a.Sq;
+                    cp_async16_or_zero(dst + sw128_off(r, ch & 7), src + (in ? ((size_t)(r >> rsh) * a.Sq + si) * HEAD_DIM : 0), in);
+                }
             }
             cp_async_commit();
             cp_async_wait_all();
@@ -494,22 +505,29 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 const uint32_t pos = s0 + si < a.Sq ? (uint32_t)a.position_ids[(size_t)u.b * a.Sq + s0 + si] : 0;
 #pragma unroll 1
                 for (int ch = tid >> rsh; ch < 8; ch += a.G) {
-                    float cs[8], sn[8];
+                    float2 cs[4], sn[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) rope_cos_sin(pos, a.rope_turns[8 * ch + i], cs[i], sn[i]);
-#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        rope_cos_sin(pos, a.rope_turns[8 * ch + 2 * i], cs[i].x, sn[i].x);
+                        rope_cos_sin(pos, a.rope_turns[8 * ch + 2 * i + 1], cs[i].y, sn[i].y);
+                    }
+#pragma unroll 2
                     for (int r = si; r < PF_BM; r += rph) {
                         uint4* pl = reinterpret_cast<uint4*>(qt + sw128_off(r, ch));
                         uint4* ph = reinterpret_cast<uint4*>(qt + 16384 + sw128_off(r, ch));
                         const uint4 lo = *pl, hi = *ph;
                         const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
                         const float inv = bars->qinv[r];
+                        const float2 inv2 = make_float2(inv, inv);
                         uint32_t ol[4], oh[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float l0 = bf16lo(lw[i]) * inv, l1 = bf16hi(lw[i]) * inv, h0 = bf16lo(hw[i]) * inv, h1 = bf16hi(hw[i]) * inv;
-                            ol[i] = pack_f16x2(l0 * cs[2 * i] - h0 * sn[2 * i], l1 * cs[2 * i + 1] - h1 * sn[2 * i + 1]);
-                            oh[i] = pack_f16x2(h0 * cs[2 * i] + l0 * sn[2 * i], h1 * cs[2 * i + 1] + l1 * sn[2 * i + 1]);
+                            const float2 l = fmul2(make_float2(bf16lo(lw[i]), bf16hi(lw[i])), inv2);
+                            const float2 h = fmul2(make_float2(bf16lo(hw[i]), bf16hi(hw[i])), inv2);
+                            const float2 x = ffma2(make_float2(-h.x, -h.y), sn[i], fmul2(l, cs[i]));
+                            const float2 y = ffma2(l, sn[i], fmul2(h, cs[i]));
+                            ol[i] = pack_f16x2(x.x, x.y);
+                            oh[i] = pack_f16x2(y.x, y.y);
                         }
                         // a row that is out of range has 0 times what may be infinite: zeros instead
                         const bool zero = inv == 0.0f;
