@@ -425,24 +425,41 @@ def attn_ragged(p: Plan, max_q_len, qo_indptr, q, k_cache, v_cache, block_table,
 def _pointers(tensors):
     """Device pointers of ``(tensor, dtype, shape, name)`` entries, each checked:
     type, shape (None: any), contiguous, on the current CUDA device (the one
-    that the call launches on)."""
-    import torch
+    that the call launches on).  This runs for every call, so it asks each
+    tensor for no more than that."""
+    ptrs = []
+    dev = -1
     for t, dt, shape, name in tensors:
-        if t.dtype != dt:
+        if t.dtype is not dt:
             raise TypeError("%s must be %s (got %s)" % (name, dt, t.dtype))
         if shape is not None and t.shape != shape:
             raise ValueError("%s has shape %s, the call needs %s" % (name, tuple(t.shape), tuple(shape)))
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise ValueError("%s: expected a CUDA tensor" % name)
+        if d != dev:
+            if dev < 0:
+                dev = _cuda_device()
+            if d != dev:
+                raise ValueError("%s is on device %d, the current device is %d" % (name, d, dev))
         if not t.is_contiguous():
             raise ValueError("%s: expected a contiguous tensor" % name)
-    dev = torch.cuda.current_device()
-    ptrs = []
-    for t, _, _, name in tensors:
-        if t.get_device() != dev:
-            raise ValueError("%s is on device %d, the current device is %d" % (name, t.get_device(), dev))
         ptrs.append(t.data_ptr())
     return ptrs
+
+
+def _cuda_device():
+    """Index of the current CUDA device."""
+    import torch
+    return torch._C._cuda_getDevice()
+
+
+def _raw_stream(stream):
+    """As ``_stream``, without making a stream object of the current one."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _stream(stream)
 
 
 def _status(status):
@@ -472,7 +489,7 @@ def tables_extend(p: Plan, n_new, kv_lens, pool, taken, block_table, kv_lens_out
                      (qo_indptr, i32, (B + 1,), "qo_indptr"), (position_ids, i32, None, "position_ids"),
                      (slot_map, i32, position_ids.shape, "slot_map")] + _status(status))
     _check(load().rk_paged_tables_extend(ctypes.byref(p), ptr[0], ptr[1], ptr[2], pool.shape[0], *ptr[3:10],
-                                         slot_map.shape[0], ptr[10] if status is not None else None, _stream(stream)))
+                                         slot_map.shape[0], ptr[10] if status is not None else None, _raw_stream(stream)))
 
 
 def _q8_cache(p: Plan, k_cache, v_cache, k_scale, v_scale):
@@ -496,7 +513,7 @@ def kv_append_q8(p: Plan, k_new, v_new, slot_map, position_ids, k_cache, v_cache
                      (position_ids, torch.int32, (n,), "position_ids")] +
                     _q8_cache(p, k_cache, v_cache, k_scale, v_scale) + _status(status))
     _check(load().rk_paged_kv_append_q8(ctypes.byref(p), n, *ptr[:8], ptr[8] if status is not None else None,
-                                        _stream(stream)))
+                                        _raw_stream(stream)))
 
 
 def decode_q8_scratch_bytes(p: Plan, split_tokens: int = 0) -> int:
@@ -527,7 +544,7 @@ def attn_decode_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table, 
         sp = _pointers([(scratch, scratch.dtype, None, "scratch")])[0]
         nbytes = scratch.numel() * scratch.element_size()
     _check(load().rk_paged_attn_decode_q8(ctypes.byref(p), int(split_tokens), *ptr[:10], sp, nbytes,
-                                          ptr[10] if status is not None else None, _stream(stream)))
+                                          ptr[10] if status is not None else None, _raw_stream(stream)))
 
 
 def attn_prefill_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse,
@@ -535,7 +552,7 @@ def attn_prefill_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table,
     """rk_paged_attn_prefill_q8 on device tensors: causal chunked prefill over the 8-bit cache."""
     ptr = _attn_q8(p, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse, status)
     _check(load().rk_paged_attn_prefill_q8(ctypes.byref(p), *ptr[:10], ptr[10] if status is not None else None,
-                                           _stream(stream)))
+                                           _raw_stream(stream)))
 
 
 def run(mode: str, q, k_cache, v_cache, block_table, kv_lens, position_ids, plan_obj=None,

@@ -17,23 +17,29 @@
 // 2^-14 of the block's largest value; the 4-bit rounding of that value is 2^-5.
 // E comes from the inputs' exponent bits, never from a rounded product.
 // The rotation is in FP32; a pair with a result that FP32 cannot place on one
-// side of a rounding border is done again in FP64, so that codes are those of
+// side of a rounding border is done again with 44 bits, so that codes are those of
 // the real number (a few in a million would be one step off otherwise).
 //
-// Work: a run is the tokens of one call on one page (slots that follow one
-// another).  A CTA takes one KV head of the runs that start in a window of 16
-// tokens: 8 threads to a token, each with 8 rotation pairs (dims 8u .. 8u+7 and
-// 64 + 8u ..), so a thread's loads are 16 bytes and 8 lanes cover 128.  A run
-// may go on for 15 tokens past the window, in a second pass.  Bound by latency at
-// decode sizes, by bytes (512 in, 256 out a token and head) at chunk sizes.
+// Work: a run is the tokens of one call on one page (slots that follow one another).  The
+// runs that start in a window of tokens belong to one warp (window 4) or to the four warps of a
+// CTA (window 16), for one KV head: lane t of each warp has slot, position and exponent of the
+// window's t-th token (a run goes on for 15 past the window at most), the values go by 8 lanes
+// to a token, four tokens to a warp's turn, once for the exponents and once more (mostly still
+// in registers, else out of L1) for the codes.
+// 64 single tokens x 8 heads: 4.7 us a launch (latency: launch, slots, values, stores); 2048
+// tokens in runs of 16: 6.8 us; 15600 tokens of 24 ragged rows: 30 us (bound by instructions:
+// the bytes alone would take 12).
 #include "q8_device.cuh"
 
 namespace rk {
 
 namespace {
 
-constexpr int AQ_THREADS = 128;
-constexpr int AQ_WINDOW = 16;
+constexpr int AQ_THREADS = 128, AQ_WARPS = AQ_THREADS / 32;
+// Four warps to a window once there is a CTA of them per SM: the warps of a long run then work
+// side by side (2048 tokens of 8 heads: 6.8 us, 15.9 with a warp to each run); below, a warp
+// alone needs no barrier and spreads single tokens wider (64 tokens: 4.7 us, 5.2 in fours).
+constexpr long long AQ_MANY = 152;
 
 __device__ __forceinline__ float flush_code(float v) { return fabsf(v) < 31.0f / 2048.0f ? 0.0f : v; }
 
@@ -50,14 +56,9 @@ __device__ __forceinline__ uint32_t lower4(uint32_t w, int by) {
     return r;
 }
 
-// What a token's 8 threads hold of one tensor: dims 8u .. 8u+7 and 64+8u ..
-struct Half8 {
-    uint4 lo, hi;
-};
-
 // Largest |x| of the token as a bf16 bit pattern (the 8 lanes of a group agree).
-__device__ __forceinline__ uint32_t token_amax(const Half8& x) {
-    const uint32_t w[8] = {x.lo.x, x.lo.y, x.lo.z, x.lo.w, x.hi.x, x.hi.y, x.hi.z, x.hi.w};
+__device__ __forceinline__ uint32_t token_amax(const uint4& lo, const uint4& hi) {
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
@@ -72,221 +73,293 @@ __device__ __forceinline__ uint32_t token_amax(const Half8& x) {
 // pi), its sine and cosine by 2^-21.2, the two products and the sum by 2^-23.
 constexpr float ROT_ERR = 1.0f / (1 << 19);
 
-// A double as a float that rounds to 4 bits as the double does: cut off, and the
-// last bit set if something was lost.
-__device__ __forceinline__ float to_odd(double x) {
-    const float r = __double2float_rz(x);
-    return (double)r != x ? __int_as_float(__float_as_int(r) | 1) : r;
+// A value as the unevaluated sum of two floats, about 47 bits; sums and products after
+// Dekker ("A floating-point technique for extending the available precision", 1971).
+struct Two {
+    float h, l;
+};
+// x z + c for |c| >= |x z|
+__device__ __forceinline__ Two two_fma(Two x, Two z, float ch, float cl) {
+    const float m = __fmul_rn(x.h, z.h);
+    const float e = __fmaf_rn(x.h, z.h, -m) + fmaf(x.h, z.l, x.l * z.h);
+    const float h = __fadd_rn(ch, m);
+    return {h, __fsub_rn(m, __fsub_rn(h, ch)) + (e + cl)};
 }
+// a x + b y for floats a, b, as one float that rounds to fewer bits as the sum does: the
+// neighbour with its last bit set, on the side that the rest points to.
+__device__ __forceinline__ float two_dot(float a, Two x, float b, Two y) {
+    const float p = __fmul_rn(a, x.h), q = __fmul_rn(b, y.h);
+    const float e = (__fmaf_rn(a, x.h, -p) + a * x.l) + (__fmaf_rn(b, y.h, -q) + b * y.l);
+    const float s = __fadd_rn(p, q), t = __fsub_rn(s, p);
+    const float r = __fadd_rn(__fadd_rn(__fsub_rn(p, __fsub_rn(s, t)), __fsub_rn(q, t)), e);
+    const float h = __fadd_rn(s, r), l = __fsub_rn(r, __fsub_rn(h, s));
+    const int bits = __float_as_int(h);
+    return l != 0.0f && !(bits & 1) ? __int_as_float(bits + ((l > 0.0f) == (h > 0.0f) ? 1 : -1)) : h;
+}
+// Taylor coefficients of sin and cos of pi / 4 t, |t| <= 1, in powers of t^2; the next is below 2^-49.
+struct TurnSeries {
+    float sin2[5][2], cos2[5][2], sin1[3], cos1[3];
+};
+__constant__ TurnSeries turn_series = {
+    {{7.853981853e-01f, -2.185569414e-08f}, {-8.074551076e-02f, -1.431311292e-09f}, {2.490394516e-03f, 5.427601424e-11f}, {-3.657620255e-05f, -1.635465201e-12f}, {3.133616815e-07f, 7.545715084e-15f}},
+    {{1.000000000e+00f, 0.000000000e+00f}, {-3.084251285e-01f, -9.074112128e-09f}, {1.585434377e-02f, 4.718809787e-10f}, {-3.259918885e-04f, 1.603162373e-12f}, {3.590860388e-06f, 6.088822480e-14f}},
+    {-1.757247681e-09f, 6.948453098e-12f, -2.041026345e-14f},
+    {-2.461136894e-08f, 1.150115905e-10f, -3.898073270e-13f}};
 
-// The rotation of one pair in FP64 (angle in turns from the 0.64 fixed-point rate).
+// The rotation of one pair, to about 2^-44 of its length (in FP64 the same took 3 us; that
+// pipe is slow here): a quarter turn's share of the angle by the two series, the rest by swaps.
 __device__ __noinline__ float2 rotate_exact(float lo, float hi, uint32_t pos, uint64_t turns) {
-    double sn, c;
-    sincospi(ldexp((double)(long long)(pos * turns), -63), &sn, &c);
-    return make_float2(to_odd((double)lo * c - (double)hi * sn), to_odd((double)hi * c + (double)lo * sn));
+    const uint64_t frac = pos * turns;
+    const uint32_t quarter = (uint32_t)((frac + (1ull << 61)) >> 62);
+    const long long r = (long long)(frac - ((uint64_t)quarter << 62));  // of [-2^61, 2^61)
+    Two t;
+    t.h = (float)r;
+    t.l = (float)(r - (long long)t.h) * 0x1p-61f;
+    t.h *= 0x1p-61f;
+    Two z;
+    z.h = __fmul_rn(t.h, t.h);
+    z.l = fmaf(2.0f * t.h, t.l, __fmaf_rn(t.h, t.h, -z.h));
+    const TurnSeries& c = turn_series;
+    Two sn = {fmaf(fmaf(c.sin1[2], z.h, c.sin1[1]), z.h, c.sin1[0]), 0.0f};
+    Two cn = {fmaf(fmaf(c.cos1[2], z.h, c.cos1[1]), z.h, c.cos1[0]), 0.0f};
+#pragma unroll
+    for (int k = 4; k >= 0; --k) {
+        sn = two_fma(sn, z, c.sin2[k][0], c.sin2[k][1]);
+        cn = two_fma(cn, z, c.cos2[k][0], c.cos2[k][1]);
+    }
+    const float m = __fmul_rn(sn.h, t.h);
+    sn = {m, __fmaf_rn(sn.h, t.h, -m) + fmaf(sn.h, t.l, sn.l * t.h)};
+    if (quarter & 1) {  // a quarter turn on: (cos, sin) -> (-sin, cos)
+        const Two x = sn;
+        sn = cn;
+        cn = {-x.h, -x.l};
+    }
+    if (quarter & 2) {
+        lo = -lo;
+        hi = -hi;
+    }
+    return make_float2(two_dot(lo, cn, -hi, sn), two_dot(hi, cn, lo, sn));
 }
 
-// Whether codes of v 2^-E and of a value up to d away may differ.
+// Whether the codes of two scaled values and of values up to d away may differ.
 __device__ __forceinline__ bool near_border(float v0, float v1, float d) {
     return cvt_e4m3x2(flush_code(v0 - d), flush_code(v1 - d)) != cvt_e4m3x2(flush_code(v0 + d), flush_code(v1 + d));
 }
+// The cheap half of it: whether a border of 4 bits (the upper 12 of the word, half up) lies
+// between v - d and v + d, at any size.
+__device__ __forceinline__ bool maybe_border(float v, float d) {
+    return ((__float_as_uint(v - d) + 0x80000u) ^ (__float_as_uint(v + d) + 0x80000u)) & 0xfff00000u;
+}
 
-__device__ __forceinline__ uint2 pack8(const float (&y)[8], float inv) {
+__device__ __forceinline__ uint2 pack8(const float (&y)[8]) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = cvt_e4m3x2(flush_code(y[2 * i] * inv), flush_code(y[2 * i + 1] * inv));
+    for (int i = 0; i < 4; ++i) w[i] = cvt_e4m3x2(flush_code(y[2 * i]), flush_code(y[2 * i + 1]));
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
+// The codes of one token's 16 dims lo / hi (8 each, dims 8u .. and 64 + 8u ..).
+__device__ __forceinline__ void store_codes(uint8_t* row, int u, uint2 lo, uint2 hi) {
+    *reinterpret_cast<uint2*>(row + 8 * u) = lo;
+    *reinterpret_cast<uint2*>(row + 64 + 8 * u) = hi;
+}
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (i & 1) ? bf16hi(v[i >> 1]) : bf16lo(v[i >> 1]);
+}
+
+// Move the codes of slots [0, n) of a block to a scale 2^by larger (a warp's work).
+__device__ __forceinline__ void lower_block(uint8_t* block, int n, int lane, int by) {
+#pragma unroll 1
+    for (int i = lane; i < n * (HEAD_DIM / 16); i += 32) {
+        uint4* c = reinterpret_cast<uint4*>(block) + i;
+        const uint4 x = *c;
+        *c = make_uint4(lower4(x.x, by), lower4(x.y, by), lower4(x.z, by), lower4(x.w, by));
+    }
+}
+
+// TEAM: the CTA's warps share one window of 16 tokens, turn by turn; else each has its own of 4.
+template <bool TEAM>
 __global__ void __launch_bounds__(AQ_THREADS) append_q8_kernel(const __grid_constant__ AppendQ8Args a) {
-    __shared__ int s_slot[32], s_pos[32];
-    __shared__ uint32_t s_lead, s_live;
-    __shared__ int s_ek[32], s_ev[32];
-    const int tid = threadIdx.x, g = tid >> 3, u = tid & 7;
-    const int h = (int)(blockIdx.x % a.Hkv);
-    const long long w0 = (long long)(blockIdx.x / a.Hkv) * AQ_WINDOW;  // first token of the window
+    const int lane = threadIdx.x & 31, g = lane >> 3, u = lane & 7;
+    constexpr int STEP = TEAM ? AQ_WARPS : 1, WINDOW = 4 * STEP;
+    const int wid = TEAM ? threadIdx.x >> 5 : 0;
+    const long long work = TEAM ? blockIdx.x : (long long)blockIdx.x * AQ_WARPS + (threadIdx.x >> 5);
+    const int h = (int)(work % a.Hkv);
+    const long long w0 = work / a.Hkv * WINDOW;  // first token of the window
+    if (w0 >= a.n) return;
 
-    // ---- the window's slots and the 15 after it; which of them start a run ----
-    if (tid < 32) {
-        const long long i = w0 + tid;
-        int slot = -1, pos = -1, bad = 0;
-        if (i < a.n) {
-            slot = a.slot_map[i];
-            pos = a.position_ids[i];
-            if (slot < -1 || slot >= a.num_pages * PAGE) bad |= RK_STATUS_PAGE_OOB;
-            else if (slot >= 0 && pos < 0) bad |= RK_STATUS_POSITION;
-            if (bad) slot = -1;
-        }
-        if (bad && tid < AQ_WINDOW && h == 0 && a.status) atomicOr(a.status, bad);
-        // the token before: as the run rule sees it (a refused one starts no run and carries none on)
-        int prev = __shfl_up_sync(0xffffffffu, slot, 1);
-        if (tid == 0) {
-            prev = -1;
-            if (w0 > 0) {
-                prev = a.slot_map[w0 - 1];
-                if (prev < -1 || prev >= a.num_pages * PAGE || a.position_ids[w0 - 1] < 0) prev = -1;
-            }
-        }
-        const bool live = slot >= 0;
-        const bool lead = live && !(prev >= 0 && slot == prev + 1 && slot % PAGE != 0);
-        s_slot[tid] = slot;
-        s_pos[tid] = pos;
-        const uint32_t ml = __ballot_sync(0xffffffffu, lead), mv = __ballot_sync(0xffffffffu, live);
-        if (tid == 0) {
-            s_lead = ml;
-            s_live = mv;
-        }
-    }
-    __syncthreads();
-    const uint32_t lead = s_lead, live = s_live;
-    if ((lead & 0xffffu) == 0) return;  // no run starts here
-    // the last run that starts in the window may reach past it
-    const int last = 31 - __clz(lead & 0xffffu);
-    const uint32_t stop = (lead | ~live) & ~((2u << last) - 1u);  // first token after `last` that is not of its run
-    const int end = stop ? __ffs(stop) - 1 : 32;                  // a run has at most 16 tokens: <= 31
-    const bool two = end > AQ_WINDOW;
+    __shared__ uint32_t s_raw[TEAM ? 32 : 1];
+    struct Token {
+        uint4 kl, kh, vl, vh;
+    };
+    auto load = [&](long long i, Token& x) {
+        const size_t at = ((size_t)i * a.Hkv + h) * HEAD_DIM + 8 * u;
+        const uint4* ks = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.k_new) + at);
+        const uint4* vs = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.v_new) + at);
+        x.kl = __ldg(ks);
+        x.kh = __ldg(ks + 8);
+        x.vl = __ldg(vs);
+        x.vh = __ldg(vs + 8);
+    };
+    // The window's first tokens travel while the slots do (in a decode step they are the work).
+    Token x;
+    x.kl = x.kh = x.vl = x.vh = make_uint4(0, 0, 0, 0);
+    if (w0 + 4 * wid + g < a.n) load(w0 + 4 * wid + g, x);
 
-    Half8 k[2], v[2];
-    int run[2];   // the run's first token, -1: not ours
-    int ok_k = 1, ok_v = 1;  // per pass, bits
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const int t = g + AQ_WINDOW * p;
-        run[p] = -1;
-        const uint32_t before = lead & ((2u << t) - 1u) & 0xffffu;
-        if ((p == 0 || two) && t < end && ((live >> t) & 1u) && before) run[p] = 31 - __clz(before);
-        uint32_t mk = 0, mv = 0;
-        k[p].lo = k[p].hi = v[p].lo = v[p].hi = make_uint4(0, 0, 0, 0);
-        if (run[p] >= 0) {
-            const size_t at = ((size_t)(w0 + t) * a.Hkv + h) * HEAD_DIM + 8 * u;
-            const uint4* ks = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.k_new) + at);
-            const uint4* vs = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.v_new) + at);
-            k[p].lo = __ldcs(ks);
-            k[p].hi = __ldcs(ks + 8);
-            v[p].lo = __ldcs(vs);
-            v[p].hi = __ldcs(vs + 8);
+    // ---- lane = token: slots, positions, where runs start and end ----
+    const long long i = w0 + lane;
+    int slot = -1, pos = -1, prev = -1, bad = 0;
+    const int slots = a.num_pages * PAGE;
+    if (i < a.n) {
+        slot = a.slot_map[i];
+        pos = a.position_ids[i];
+        if (lane == 0 && w0 > 0) {
+            prev = a.slot_map[i - 1];
+            if (prev < -1 || prev >= slots || a.position_ids[i - 1] < 0) prev = -1;
         }
-        if (p == 0 || two) {
-            mk = token_amax(k[p]);
-            mv = token_amax(v[p]);
-            const bool bk = mk >= Q8_LIMIT_BF16, bv = mv >= Q8_LIMIT_BF16;
-            if (bk) ok_k &= ~(1 << p); else ok_k |= 1 << p;
-            if (bv) ok_v &= ~(1 << p); else ok_v |= 1 << p;
-            if (u == 0) {
-                s_ek[t] = bk ? Q8_E_MIN : q8_exponent(mk);
-                s_ev[t] = bv ? Q8_E_MIN : q8_exponent(mv);
-                if ((bk || bv) && a.status) atomicOr(a.status, RK_STATUS_RANGE);
-            }
-        }
+        if (slot < -1 || slot >= slots) bad = RK_STATUS_PAGE_OOB;
+        else if (slot >= 0 && pos < 0) bad = RK_STATUS_POSITION;
+        if (bad) slot = -1;
     }
-    // the scales of pages that had tokens before this call, read before any is written
-    float sk[2] = {1.0f, 1.0f}, sv[2] = {1.0f, 1.0f};
-    int off[2];  // the run's first slot in its page
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        off[p] = 0;
-        if (run[p] < 0) continue;
-        const int slot = s_slot[run[p]];
-        off[p] = slot % PAGE;
-        if (off[p] > 0) {
-            const size_t at = (size_t)(slot / PAGE) * a.Hkv + h;
-            sk[p] = a.k_scale[at];
-            sv[p] = a.v_scale[at];
-        }
-    }
-    __syncthreads();
+    if (bad && lane < WINDOW && h == 0 && wid == 0 && a.status) atomicOr(a.status, bad);
+    // the token before, as the run rule sees it: a refused one starts no run and carries none on
+    const int up = __shfl_up_sync(0xffffffffu, slot, 1);
+    if (lane > 0) prev = up;
+    const uint32_t live = __ballot_sync(0xffffffffu, slot >= 0);
+    const uint32_t lead = __ballot_sync(0xffffffffu, slot >= 0 && !(prev >= 0 && slot == prev + 1 && slot % PAGE != 0));
+    const uint32_t ours = lead & ((1u << WINDOW) - 1u);
+    if (ours == 0) return;  // no run starts here
+    const uint32_t after = ~((2u << lane) - 1u);  // the lanes behind this one
+    const int first = __ffs(ours) - 1, last = 31 - __clz(ours);
+    const int start = (lead & ~after) ? 31 - __clz(lead & ~after) : 0;  // of this lane's run
+    const uint32_t next = (lead | ~live) & after;
+    const int close = next ? __ffs(next) - 2 : 31;  // its last token
+    const int end = __shfl_sync(0xffffffffu, close, last) + 1;
+    const int turns = (end - first + 3) >> 2;
 
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        if (run[p] < 0) continue;
-        const int t = g + AQ_WINDOW * p, first = run[p];
-        const int page = s_slot[first] / PAGE;
-        const size_t block = (size_t)page * a.Hkv + h;
-        int ek = Q8_E_MIN, ev = Q8_E_MIN;
-        for (int j = first; j < 32 && ((live >> j) & 1u) && (j == first || !((lead >> j) & 1u)); ++j) {
-            ek = max(ek, s_ek[j]);
-            ev = max(ev, s_ev[j]);
+    // ---- the block's scales, where it had tokens before this call ----
+    const bool head = (ours >> lane) & 1u;
+    const int off = slot % PAGE;
+    const size_t block = (size_t)(max(slot, 0) / PAGE) * a.Hkv + h;
+    int sk = 0, sv = 0;
+    if (head && off > 0) {
+        sk = __float_as_int(a.k_scale[block]);
+        sv = __float_as_int(a.v_scale[block]);
+    }
+    // ---- exponents: K in bits 0-7, V in bits 16-23 (plus 128); bits 8 and 24: out of range ----
+    uint32_t raw = 0;
+#pragma unroll 1
+    for (int r = wid; r < turns; r += STEP) {
+        const int t = first + 4 * r + g;
+        if (r > wid || first > 0) {
+            if (t < end && ((live >> t) & 1u)) load(w0 + t, x);
         }
-        int ek_old = ek, ev_old = ev;
-        if (off[p] > 0) {
-            const int bk = __float_as_int(sk[p]), bv = __float_as_int(sv[p]);
-            ek_old = (bk >> 23) - 127;
-            ev_old = (bv >> 23) - 127;
+        const uint32_t mk = token_amax(x.kl, x.kh), mv = token_amax(x.vl, x.vh);
+        const uint32_t e = (mk >= Q8_LIMIT_BF16 ? 0x100u + (uint32_t)(128 + Q8_E_MIN) : (uint32_t)(q8_exponent(mk) + 128)) |
+                           (mv >= Q8_LIMIT_BF16 ? 0x100u + (uint32_t)(128 + Q8_E_MIN) : (uint32_t)(q8_exponent(mv) + 128)) << 16;
+        const uint32_t v = __shfl_sync(0xffffffffu, e, ((lane - first) & 3) * 8);
+        if (lane - first >= 4 * r && lane - first < 4 * r + 4) raw = v;
+    }
+    if constexpr (TEAM) {  // each token's exponents from the warp that has them
+        if (lane >= first && lane < end && ((lane - first) >> 2) % AQ_WARPS == wid) s_raw[lane] = raw;
+        __syncthreads();
+        raw = s_raw[lane];
+    }
+    // largest of the run: up to its last token, and back from there
+    uint32_t m = raw & 0x00ff00ffu;
+#pragma unroll
+    for (int o = 1; o < PAGE; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, m, o);
+        if (lane - o >= start) m = __vmaxu2(m, v);
+    }
+    m = __shfl_sync(0xffffffffu, m, close);
+    int ek = (int)(m & 0xff) - 128, ev = (int)(m >> 16) - 128;
+    bool ok = true;
+    int up_k = 0, up_v = 0;
+    if (head) {
+        if (off > 0) {
+            const int ek_old = (sk >> 23) - 127, ev_old = (sv >> 23) - 127;
             // not a power of two that this kernel writes: the block's codes cannot be moved to another scale
-            if ((bk & 0x7fffff) || (bv & 0x7fffff) || ek_old < Q8_E_MIN || ek_old > Q8_E_MAX || ev_old < Q8_E_MIN ||
-                ev_old > Q8_E_MAX) {
-                if (u == 0 && a.status) atomicOr(a.status, RK_STATUS_SCALE);
-                continue;
-            }
+            ok = !((sk | sv) & 0x7fffff) && ek_old >= Q8_E_MIN && ek_old <= Q8_E_MAX && ev_old >= Q8_E_MIN && ev_old <= Q8_E_MAX;
+            up_k = max(0, ek - ek_old);
+            up_v = max(0, ev - ev_old);
             ek = max(ek, ek_old);
             ev = max(ev, ev_old);
         }
-        uint8_t* kb = a.k_cache + block * Q8_BLOCK_BYTES;
-        uint8_t* vb = a.v_cache + block * Q8_BLOCK_BYTES;
-        if (t == first) {
-            if (off[p] == 0 || ek > ek_old || ev > ev_old) {
-                if (u == 0) {
-                    a.k_scale[block] = pow2(ek);
-                    a.v_scale[block] = pow2(ev);
-                }
-                for (int s = 0; s < off[p]; ++s) {  // old codes: lane u has 16 bytes of each slot
-                    if (ek > ek_old) {
-                        uint4* c = reinterpret_cast<uint4*>(kb + s * HEAD_DIM) + u;
-                        uint4 x = *c;
-                        x = make_uint4(lower4(x.x, ek - ek_old), lower4(x.y, ek - ek_old), lower4(x.z, ek - ek_old),
-                                       lower4(x.w, ek - ek_old));
-                        *c = x;
-                    }
-                    if (ev > ev_old) {
-                        uint4* c = reinterpret_cast<uint4*>(vb + s * HEAD_DIM) + u;
-                        uint4 x = *c;
-                        x = make_uint4(lower4(x.x, ev - ev_old), lower4(x.y, ev - ev_old), lower4(x.z, ev - ev_old),
-                                       lower4(x.w, ev - ev_old));
-                        *c = x;
-                    }
-                }
-            }
+        if (wid > 0) {
+        } else if (ok) {
+            a.k_scale[block] = pow2(ek);
+            a.v_scale[block] = pow2(ev);
+        } else if (a.status) {
+            atomicOr(a.status, RK_STATUS_SCALE);
         }
-        const int s = s_slot[t] % PAGE;
-        const uint32_t pos = (uint32_t)s_pos[t];
+    }
+    // earlier codes of the block move along
+    uint32_t grown = __ballot_sync(0xffffffffu, head && ok && (up_k | up_v));
+    while (wid == 0 && grown) {
+        const int src = __ffs(grown) - 1;
+        grown &= grown - 1;
+        const int n = __shfl_sync(0xffffffffu, off, src);
+        const int bk = __shfl_sync(0xffffffffu, up_k, src), bv = __shfl_sync(0xffffffffu, up_v, src);
+        const size_t at = ((size_t)(__shfl_sync(0xffffffffu, slot, src) / PAGE) * a.Hkv + h) * Q8_BLOCK_BYTES;
+        if (bk) lower_block(a.k_cache + at, n, lane, bk);
+        if (bv) lower_block(a.v_cache + at, n, lane, bv);
+    }
+    // the run's exponents to each of its tokens, with the token's own two bits
+    m = (uint32_t)(ek + 128) | (uint32_t)(ev + 128) << 16 | (ok ? 0u : 1u << 31);
+    m = __shfl_sync(0xffffffffu, m, start);
+    m |= raw & 0x01000100u;
+    if (slot >= 0 && lane >= first && lane < end && !(m >> 31) && (m & 0x01000100u) && wid == 0 && a.status) atomicOr(a.status, RK_STATUS_RANGE);
+
+    // ---- codes; the last turn's values are still here ----
+    const int top = wid + (turns - 1 - wid) / STEP * STEP;
+#pragma unroll 1
+    for (int r = top; r >= wid && turns > wid; r -= STEP) {
+        const int t = first + 4 * r + g;
+        const uint32_t e = __shfl_sync(0xffffffffu, m, t & 31);
+        const int at = __shfl_sync(0xffffffffu, slot, t & 31);
+        const uint32_t p = (uint32_t)__shfl_sync(0xffffffffu, pos, t & 31);
+        if (t >= end || at < 0 || (e >> 31)) continue;
+        if (r < top) load(w0 + t, x);
+        const size_t row = ((size_t)(at / PAGE) * a.Hkv + h) * Q8_BLOCK_BYTES + (at % PAGE) * HEAD_DIM;
         const uint2 nan8 = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
         {
-            const uint32_t lw[4] = {k[p].lo.x, k[p].lo.y, k[p].lo.z, k[p].lo.w};
-            const uint32_t hw[4] = {k[p].hi.x, k[p].hi.y, k[p].hi.z, k[p].hi.w};
-            float yl[8], yh[8];
-            const float inv = pow2(-ek);
+            float lo[8], hi[8], yl[8], yh[8];
+            unpack8(x.kl, lo);
+            unpack8(x.kh, hi);
+            const float inv = pow2(128 - (int)(e & 0xff));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float lo = (i & 1) ? bf16hi(lw[i >> 1]) : bf16lo(lw[i >> 1]);
-                const float hi = (i & 1) ? bf16hi(hw[i >> 1]) : bf16lo(hw[i >> 1]);
-                float c, sn;
-                rope_cos_sin(pos, a.rope_turns[8 * u + i], c, sn);
-                yl[i] = fmaf(-hi, sn, lo * c);
-                yh[i] = fmaf(lo, sn, hi * c);
-                const float d = (fabsf(lo) + fabsf(hi)) * ROT_ERR * inv;
-                if (near_border(yl[i] * inv, yh[i] * inv, d)) {
-                    const float2 y = rotate_exact(lo, hi, pos, a.rope_turns[8 * u + i]);
-                    yl[i] = y.x;
-                    yh[i] = y.y;
+                float c, s;
+                rope_cos_sin(p, a.rope_turns[8 * u + i], c, s);
+                yl[i] = fmaf(-hi[i], s, lo[i] * c) * inv;
+                yh[i] = fmaf(lo[i], s, hi[i] * c) * inv;
+                const float d = (fabsf(lo[i]) + fabsf(hi[i])) * (ROT_ERR * inv);
+                if (maybe_border(yl[i], d) | maybe_border(yh[i], d)) {
+                    if (near_border(yl[i], yh[i], d)) {
+                        const float2 y = rotate_exact(lo[i], hi[i], p, a.rope_turns[8 * u + i]);
+                        yl[i] = y.x * inv;
+                        yh[i] = y.y * inv;
+                    }
                 }
             }
-            const bool good = (ok_k >> p) & 1;
-            *reinterpret_cast<uint2*>(kb + s * HEAD_DIM + 8 * u) = good ? pack8(yl, inv) : nan8;
-            *reinterpret_cast<uint2*>(kb + s * HEAD_DIM + 64 + 8 * u) = good ? pack8(yh, inv) : nan8;
+            const bool good = !(e & 0x100u);
+            store_codes(a.k_cache + row, u, good ? pack8(yl) : nan8, good ? pack8(yh) : nan8);
         }
         {
-            const uint32_t lw[4] = {v[p].lo.x, v[p].lo.y, v[p].lo.z, v[p].lo.w};
-            const uint32_t hw[4] = {v[p].hi.x, v[p].hi.y, v[p].hi.z, v[p].hi.w};
-            float yl[8], yh[8];
+            float lo[8], hi[8];
+            unpack8(x.vl, lo);
+            unpack8(x.vh, hi);
+            const float inv = pow2(128 - (int)((e >> 16) & 0xff));
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                yl[i] = (i & 1) ? bf16hi(lw[i >> 1]) : bf16lo(lw[i >> 1]);
-                yh[i] = (i & 1) ? bf16hi(hw[i >> 1]) : bf16lo(hw[i >> 1]);
+                lo[i] *= inv;
+                hi[i] *= inv;
             }
-            const float inv = pow2(-ev);
-            const bool good = (ok_v >> p) & 1;
-            *reinterpret_cast<uint2*>(vb + s * HEAD_DIM + 8 * u) = good ? pack8(yl, inv) : nan8;
-            *reinterpret_cast<uint2*>(vb + s * HEAD_DIM + 64 + 8 * u) = good ? pack8(yh, inv) : nan8;
+            const bool good = !(e & 0x1000000u);
+            store_codes(a.v_cache + row, u, good ? pack8(lo) : nan8, good ? pack8(hi) : nan8);
         }
     }
 }
@@ -295,9 +368,12 @@ __global__ void __launch_bounds__(AQ_THREADS) append_q8_kernel(const __grid_cons
 
 cudaError_t launch_append_q8(const AppendQ8Args& a, cudaStream_t stream) {
     if (a.n <= 0) return cudaSuccess;
-    const long long blocks = (((long long)a.n + AQ_WINDOW - 1) / AQ_WINDOW) * a.Hkv;
+    const long long teams = ((long long)a.n + 4 * AQ_WARPS - 1) / (4 * AQ_WARPS) * a.Hkv;
+    const bool team = teams >= AQ_MANY;
+    const long long blocks = team ? teams : (((long long)a.n + 3) / 4 * a.Hkv + AQ_WARPS - 1) / AQ_WARPS;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    append_q8_kernel<<<(unsigned)blocks, AQ_THREADS, 0, stream>>>(a);
+    if (team) append_q8_kernel<true><<<(unsigned)blocks, AQ_THREADS, 0, stream>>>(a);
+    else append_q8_kernel<false><<<(unsigned)blocks, AQ_THREADS, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
