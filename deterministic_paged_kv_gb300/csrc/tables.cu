@@ -9,11 +9,14 @@
 // the new pages ceil((len + n) / 16) - ceil(len / 16); then each token finds
 // its row by bisection of qo_indptr, and everything else is arithmetic.
 //
-// One cluster of 1 or 8 CTAs: every CTA sums over all rows itself (a few
-// loads per thread; no traffic between CTAs), the cluster barrier separates
-// every read of kv_lens / taken from the writes (they may be the same arrays),
-// then the CTAs share the tokens.  Bound by latency: launch, one round of loads,
-// the scan, one round of stores.
+// Up to 4096 tokens one CTA does all of it.  Beyond, that CTA leaves the tokens to a second
+// launch, which has all it needs in the first one's outputs: every CTA of it sums the rows'
+// pages once more (a few loads per thread) and takes a share of the tokens.  (kv_lens and taken
+// may be updated in place, so the CTAs of one launch could not read them and write them
+// without a barrier over all; a cluster of 8 CTAs has one, and took 36 us where this takes
+// 8.7.)  Bound by latency: launch, one round of loads, the scan, one round of stores; 64 rows of one
+// token 5.2 us, 1024 rows of 520000 tokens 8.7 us.
+#include <algorithm>
 #include <atomic>
 
 #include "rk_device.cuh"
@@ -21,15 +24,6 @@
 namespace rk {
 
 namespace {
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
-    return r;
-}
 
 // Exclusive prefix sums over the block of two values per thread (all threads
 // call it); totals in *ta, *tb.
@@ -68,12 +62,66 @@ __device__ void scan2(long long& a, long long& b, long long* ta, long long* tb, 
 
 __device__ __forceinline__ int pages_of(int n) { return (int)(((unsigned)n + PAGE - 1) / PAGE); }
 
+// What the rows' part leaves in shared memory, [B] each: a row's first token, its first new
+// page's place in the pool, its length before.
+struct Rows {
+    int32_t *tok, *page, *len;
+};
+
+// This CTA's share of the tokens, four neighbours to a thread.  Returns status bits.
+__device__ int fill_tokens(const TablesArgs& a, const Rows& rows, int total) {
+    int bad = 0;
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.position_ids) | reinterpret_cast<uintptr_t>(a.slot_map)) & 15) == 0;
+    const long long step = 4ll * TAB_THREADS * gridDim.x;
+    for (long long i0 = 4ll * ((long long)blockIdx.x * TAB_THREADS + threadIdx.x); i0 < a.cap; i0 += step) {
+        int pos[4], slot[4];
+        int r = -1, next = -1, start = 0, len = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const long long i = i0 + k;
+            pos[k] = slot[k] = -1;
+            if (i >= total) continue;
+            if (i >= next) {  // the last row that starts at or before token i (rows without tokens share a start)
+                int lo = r < 0 ? 0 : r, hi = a.B;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (rows.tok[mid] <= i) lo = mid;
+                    else hi = mid;
+                }
+                r = lo;
+                start = rows.tok[r];
+                len = rows.len[r];
+                next = r + 1 < a.B ? rows.tok[r + 1] : total;
+            }
+            const int p = len + (int)i - start, j = p / PAGE, have = pages_of(len);
+            const int page = j < have ? a.block_table[(size_t)r * a.W + j] : a.pool[rows.page[r] + j - have];
+            if (j >= have && (p % PAGE) == 0) a.block_table[(size_t)r * a.W + j] = page;
+            pos[k] = p;
+            if (page < 0 || page >= a.num_pages) bad |= RK_STATUS_PAGE_OOB;
+            else slot[k] = page * PAGE + p % PAGE;
+        }
+        if (wide && i0 + 4 <= a.cap) {
+            *reinterpret_cast<int4*>(a.position_ids + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4*>(a.slot_map + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+        } else {
+            for (int k = 0; k < 4 && i0 + k < a.cap; ++k) {
+                a.position_ids[i0 + k] = pos[k];
+                a.slot_map[i0 + k] = slot[k];
+            }
+        }
+    }
+    return bad;
+}
+
+// The rows; ALL: and the tokens.
+template <bool ALL>
 __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const __grid_constant__ TablesArgs a) {
-    extern __shared__ int32_t rows[];  // [B] first token, [B] first new page's place in the pool, [B] length before
+    extern __shared__ int32_t rows[];
     __shared__ long long sh[64];
     int32_t* s_tok = rows;
     int32_t* s_page = rows + a.B;
     int32_t* s_len = rows + 2 * a.B;
+    if constexpr (!ALL) griddep_launch_dependents();
     const int tid = threadIdx.x;
     const int per = (a.B + TAB_THREADS - 1) / TAB_THREADS;
     const int r0 = min(a.B, tid * per), r1 = min(a.B, r0 + per);
@@ -141,60 +189,50 @@ __global__ void __launch_bounds__(TAB_THREADS) tables_kernel(const __grid_consta
     }
     __syncthreads();
     const int total = (int)tok_all;
-    cluster_sync();  // every CTA has read kv_lens and taken
-    const int rank = (int)blockIdx.x;
-    if (rank == 0) {
-        for (int r = tid; r < a.B; r += TAB_THREADS) {
-            const int t = s_tok[r], e = r + 1 < a.B ? s_tok[r + 1] : total;
-            a.qo_indptr[r] = t;
-            a.kv_lens_out[r] = s_len[r] + (e - t);
-        }
-        if (tid == 0) {
-            a.qo_indptr[a.B] = total;
-            *a.taken_out = taken + (int)pg_all;
-        }
+    for (int r = tid; r < a.B; r += TAB_THREADS) {
+        const int t = s_tok[r], e = r + 1 < a.B ? s_tok[r + 1] : total;
+        a.qo_indptr[r] = t;
+        a.kv_lens_out[r] = s_len[r] + (e - t);
+    }
+    if (tid == 0) {
+        a.qo_indptr[a.B] = total;
+        *a.taken_out = taken + (int)pg_all;
     }
 
-    // ---- the tokens: four neighbours to a thread ----
-    const bool wide = ((reinterpret_cast<uintptr_t>(a.position_ids) | reinterpret_cast<uintptr_t>(a.slot_map)) & 15) == 0;
-    const long long step = 4ll * TAB_THREADS * cluster_size();
-    for (long long i0 = 4ll * (rank * TAB_THREADS + tid); i0 < a.cap; i0 += step) {
-        int pos[4], slot[4];
-        int r = -1, next = -1, start = 0, len = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const long long i = i0 + k;
-            pos[k] = slot[k] = -1;
-            if (i >= total) continue;
-            if (i >= next) {  // the last row that starts at or before token i (rows without tokens share a start)
-                int lo = r < 0 ? 0 : r, hi = a.B;
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (s_tok[mid] <= i) lo = mid;
-                    else hi = mid;
-                }
-                r = lo;
-                start = s_tok[r];
-                len = s_len[r];
-                next = r + 1 < a.B ? s_tok[r + 1] : total;
-            }
-            const int p = len + (int)i - start, j = p / PAGE, have = pages_of(len);
-            const int page = j < have ? a.block_table[(size_t)r * a.W + j] : a.pool[s_page[r] + j - have];
-            if (j >= have && (p % PAGE) == 0) a.block_table[(size_t)r * a.W + j] = page;
-            pos[k] = p;
-            if (page < 0 || page >= a.num_pages) bad |= RK_STATUS_PAGE_OOB;
-            else slot[k] = page * PAGE + p % PAGE;
-        }
-        if (wide && i0 + 4 <= a.cap) {
-            *reinterpret_cast<int4*>(a.position_ids + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-            *reinterpret_cast<int4*>(a.slot_map + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-        } else {
-            for (int k = 0; k < 4 && i0 + k < a.cap; ++k) {
-                a.position_ids[i0 + k] = pos[k];
-                a.slot_map[i0 + k] = slot[k];
-            }
-        }
+    if constexpr (ALL) {
+        bad |= fill_tokens(a, {s_tok, s_page, s_len}, total);
     }
+    if (bad && a.status) atomicOr(a.status, bad);
+}
+
+// The tokens, after tables_kernel<false>: lengths and pages of the rows from its outputs.
+__global__ void __launch_bounds__(TAB_THREADS) tokens_kernel(const __grid_constant__ TablesArgs a) {
+    extern __shared__ int32_t rows[];
+    __shared__ long long sh[64];
+    const Rows s = {rows, rows + a.B, rows + 2 * a.B};
+    const int per = (a.B + TAB_THREADS - 1) / TAB_THREADS;
+    const int r0 = min(a.B, (int)threadIdx.x * per), r1 = min(a.B, r0 + per);
+    griddep_wait();
+    const int total = a.qo_indptr[a.B];
+    int t = r0 < r1 ? a.qo_indptr[r0] : total;
+    long long pg = 0, none = 0, pg_all, t0;
+    for (int r = r0; r < r1; ++r) {
+        const int e = a.qo_indptr[r + 1], n = e - t, len = a.kv_lens_out[r] - n;
+        s.tok[r] = t;
+        s.len[r] = len;
+        s.page[r] = n > 0 ? pages_of(len + n) - pages_of(len) : 0;
+        pg += s.page[r];
+        t = e;
+    }
+    scan2(none, pg, &t0, &pg_all, sh);
+    int p = *a.taken_out - (int)pg_all + (int)pg;
+    for (int r = r0; r < r1; ++r) {
+        const int need = s.page[r];
+        s.page[r] = p;
+        p += need;
+    }
+    __syncthreads();
+    const int bad = fill_tokens(a, s, total);
     if (bad && a.status) atomicOr(a.status, bad);
 }
 
@@ -208,23 +246,30 @@ cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(configured.load() & bit)) {
-        e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * TAB_MAX_ROWS * 4);
-        if (e != cudaSuccess) return e;
+        for (const void* f : {(const void*)tables_kernel<true>, (const void*)tables_kernel<false>, (const void*)tokens_kernel}) {
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * TAB_MAX_ROWS * 4);
+            if (e != cudaSuccess) return e;
+        }
         configured.fetch_or(bit);
     }
+    if (a.cap <= 4 * TAB_THREADS) {
+        tables_kernel<true><<<1, TAB_THREADS, smem, stream>>>(a);
+        return cudaGetLastError();
+    }
+    tables_kernel<false><<<1, TAB_THREADS, smem, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    const int ctas = a.cap > 4 * TAB_THREADS ? 8 : 1;
-    cfg.gridDim = dim3(ctas);
+    cfg.gridDim = dim3((unsigned)std::min<long long>(152, (a.cap + 4ll * TAB_THREADS - 1) / (4ll * TAB_THREADS)));
     cfg.blockDim = dim3(TAB_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ctas;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tables_kernel, a);
+    return cudaLaunchKernelEx(&cfg, tokens_kernel, a);
 }
 
 }  // namespace rk
