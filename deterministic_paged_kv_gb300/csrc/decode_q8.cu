@@ -36,6 +36,8 @@
 // SM in runs of equal numbers of steps, so a CTA changes its queries a few times only.
 // (Dealt in turn, 64 x 4096 gave 112 CTAs seven items of four steps and 40 six: they
 // ended between 78 and 98 us.)
+// The copies carry an evict-first hint: the cache is read once and passes by, while the
+// partials of many splits stay in L2 until the merge (64 x 4096: 102 us without, 94 with).
 // Roles (20 warps):
 //   warp 0      TMA producer: a step's K, then its V, 64 KiB each, in a ring of three;
 //   warp 1      MMA issuer: S and PV of each step;
@@ -429,6 +431,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         // fetched anew each time, and that, not the copies, set the pace (450 ns for 16 KiB).
         int slot = 0, use = 0, n = 0;  // n: stages filled
         uint32_t stg = 0, phase = 1;
+        const uint64_t once = evict_first_policy();  // the cache passes by; the partials stay in L2 for the merge
         bool ok = true;
 #pragma unroll 1
         while (ok) {
@@ -452,8 +455,8 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 const CUtensorMap* map = kv ? &vmap : &kmap;
 #pragma unroll 1
                 for (int p = 0; p < pages; ++p, dst += H * Q8_BLOCK_BYTES)
-                    if constexpr (H == 1) tma_load_3d_elect(dst, map, fb, 0, 0, __shfl_sync(0xffffffffu, id, p) * a.Hkv + head);
-                    else tma_load_5d_elect(dst, map, fb, 0, 0, head, 0, __shfl_sync(0xffffffffu, id, p * H));
+                    if constexpr (H == 1) tma_load_3d_elect(dst, map, fb, 0, 0, __shfl_sync(0xffffffffu, id, p) * a.Hkv + head, once);
+                    else tma_load_5d_elect(dst, map, fb, 0, 0, head, 0, __shfl_sync(0xffffffffu, id, p * H), once);
                 if (++stg == STAGES) {
                     stg = 0;
                     phase ^= 1;
@@ -634,35 +637,39 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         auto wait = [&](uint64_t& bar, int parity) {
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), (uint32_t)(parity & 1), pc));
         };
-        // Results of an item from the warps' sums (behind a barrier).
+        // Results of an item from the warps' sums (behind a barrier): a query's verdict and sum
+        // in lane g of each warp, its dims by the threads.  (Each thread on its own for every
+        // query took 300 ns a query, 2.4 us of an item of eight.)
         auto finish = [&](const DqStep& st, int par, int status, bool none) {
             // softmax warp i of this head: the head's warpgroups are hj, hj + H, ...
             auto of_head = [&](int i) { return ((i >> 2) * H + hj) * 4 + (i & 3); };
-            uint32_t any = 0;
-#pragma unroll
-            for (int i = 0; i < 16 / H; ++i) any |= c->fred[par][of_head(i)];
+            uint32_t any = __reduce_or_sync(0xffffffffu, c->fred[par][of_head(lane % (16 / H))]);
             if (status == RK_STATUS_TIMEOUT) any = 0;  // nothing was summed up
             if (any >> 31) status |= RK_STATUS_SCALE;
+            const int mine = lane % G;
+            float sum = 0.0f;
+#pragma unroll 4
+            for (int w = 0; w < 16 / H; ++w) sum += c->lred[par][of_head(w)][mine];
+            const bool over = !none && (((any >> mine) & 1u) || !(sum > 0.0f && sum < INFINITY));
+            const bool fail = status || over, zero = fail || none;
+            const float inv = zero ? 0.0f : rcp(sum);
+            const uint32_t zeros = __ballot_sync(0xffffffffu, zero);
             const size_t row = (size_t)st.b * a.Hq + (st.h * H + hj) * G;
+            if ((warp & 3) == 0 && lane < G && lane % SHARE == blk) {
+                const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : c->top[par][hj][lane] - 8.0f + __log2f(sum);
+                if (a.n_splits > 1) a.lse_part[(row + lane) * a.n_splits + st.split] = lse2;
+                else a.lse[row + lane] = lse2 * 0.693147180559945309f;
+                if (fail && a.status) atomicOr(a.status, status ? status : RK_STATUS_RANGE);
+            }
+            float* part = a.o_part + ((row + blk) * a.n_splits + st.split) * HEAD_DIM + t;
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + (row + blk) * HEAD_DIM + t;
 #pragma unroll
             for (int i = 0; i < OWN; ++i) {
                 const int g = blk + SHARE * i;
+                const float x = (zeros >> (g & 31)) & 1u ? 0.0f : o[i] * __shfl_sync(0xffffffffu, inv, g & 31);
                 if (g < G) {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < 16 / H; ++w) sum += c->lred[par][of_head(w)][g];
-                    const bool over = !none && (((any >> g) & 1u) || !(sum > 0.0f && sum < INFINITY));
-                    const bool fail = status || over;
-                    const float x = fail || none ? 0.0f : o[i] * rcp(sum);
-                    const size_t bh = row + g;
-                    if (a.n_splits > 1) a.o_part[(bh * a.n_splits + st.split) * HEAD_DIM + t] = x;
-                    else reinterpret_cast<__nv_bfloat16*>(a.out)[bh * HEAD_DIM + t] = __float2bfloat16_rn(x);
-                    if (t == 0) {
-                        const float lse2 = fail ? __int_as_float(0x7fc00000) : none ? -INFINITY : c->top[par][hj][g] - 8.0f + __log2f(sum);
-                        if (a.n_splits > 1) a.lse_part[bh * a.n_splits + st.split] = lse2;
-                        else a.lse[bh] = lse2 * 0.693147180559945309f;
-                        if (fail && a.status) atomicOr(a.status, status ? status : RK_STATUS_RANGE);
-                    }
+                    if (a.n_splits > 1) part[(size_t)(SHARE * i) * a.n_splits * HEAD_DIM] = x;
+                    else out[SHARE * i * HEAD_DIM] = __float2bfloat16_rn(x);
                 }
             }
             ++done;
@@ -919,26 +926,27 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
 
 // Merge of the split partials of one (row, query head): weights 2^(lse_s - max lse), eight
 // sums over the splits s = e, e + 8, ... in ascending order, added up in order of e: fixed by
-// the row's split count alone.  A lane has four dims.  A NaN partial fails the row, no visible
-// key gives out = 0, lse = -inf.  WARPS = 1: a warp has all eight sums (four rows to a
-// block); 8: a warp has one, for long rows.  Both add in the same order, so which one runs (a
-// choice by the table's width) does not show in the result.  Bound by latency: the row's
-// length, a round of loads of AHEAD splits a sum (for long rows two rounds at a time took
-// 10 us and more of 2 rows of 114 splits), one of stores.
-template <int WARPS>
-__global__ void __launch_bounds__(WARPS == 1 ? 128 : 256) merge_q8_kernel(const __grid_constant__ AttnQ8Args a) {
-    constexpr int SUMS = 8 / WARPS, AHEAD = WARPS == 1 ? 1 : 8;
-    __shared__ float4 acc_s[WARPS == 1 ? 1 : 8][32];
+// the row's split count alone.  A NaN partial fails the row, no visible key gives out = 0,
+// lse = -inf.  MANY = false: a warp has a row, four dims to a lane and all eight sums (four rows
+// to a block).  MANY = true: a block of two warps has a quarter of a row's dims, eight lanes to
+// a sum, and asks for sixteen splits of each sum at a time.  Both add in the same order, so which
+// one runs (a choice by the table's width) does not show in the result.  Bound by latency: the
+// row's length, a round or two of loads, one of stores.
+template <bool MANY>
+__global__ void __launch_bounds__(MANY ? 64 : 128) merge_q8_kernel(const __grid_constant__ AttnQ8Args a) {
+    constexpr int SUMS = MANY ? 1 : 8, AHEAD = MANY ? 16 : 1;
+    __shared__ float4 acc_s[MANY ? 8 : 1][8];
     __shared__ float sum_s[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const size_t bh = WARPS == 1 ? (size_t)blockIdx.x * 4 + warp : blockIdx.x;
-    if (WARPS == 1 && bh >= (size_t)a.B * a.Hq) return;
-    const int e0 = WARPS == 1 ? 0 : warp;
+    const size_t bh = MANY ? blockIdx.x >> 2 : (size_t)blockIdx.x * 4 + warp;
+    if (!MANY && bh >= (size_t)a.B * a.Hq) return;
+    const int e0 = MANY ? (int)(threadIdx.x >> 3) : 0;                     // this thread's (first) sum
+    const int d4 = MANY ? (int)((blockIdx.x & 3) * 8) + (lane & 7) : lane;  // its four dims
     int bad0;
     const int ns = splits_of(a, row_keys(a, (int)(bh / a.Hq), bad0));
     griddep_wait();  // the partials are complete and visible
     const float* lp = a.lse_part + bh * a.n_splits;
-    const float4* op = reinterpret_cast<const float4*>(a.o_part + bh * a.n_splits * HEAD_DIM) + lane;
+    const float4* op = reinterpret_cast<const float4*>(a.o_part + bh * a.n_splits * HEAD_DIM) + d4;
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float4 x[AHEAD][SUMS];
     float wt[AHEAD][SUMS];
@@ -955,6 +963,7 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 256) merge_q8_kernel(const 
     load(0);
     float m = -INFINITY;
     bool bad = false;
+#pragma unroll 4
     for (int s = lane; s < ns; s += 32) {
         const float v = lp[s];
         bad |= v != v;
@@ -963,10 +972,11 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 256) merge_q8_kernel(const 
     m = warp_max(m);
     bad = __any_sync(0xffffffffu, bad);
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + bh * HEAD_DIM;
+    const bool first = !MANY || (blockIdx.x & 3) == 0;  // says the row's lse
     if (bad || m == -INFINITY) {
-        if (e0 == 0) {
-            reinterpret_cast<uint2*>(out)[lane] = make_uint2(0, 0);
-            if (lane == 0) a.lse[bh] = bad ? __int_as_float(0x7fc00000) : -INFINITY;
+        if (!MANY || e0 == 0) {
+            reinterpret_cast<uint2*>(out)[d4] = make_uint2(0, 0);
+            if (first && lane == 0) a.lse[bh] = bad ? __int_as_float(0x7fc00000) : -INFINITY;
         }
         return;
     }
@@ -994,24 +1004,24 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 256) merge_q8_kernel(const 
     }
     float4 r = acc[0];
     float l = sum[0];
-    if constexpr (WARPS == 8) {
-        acc_s[warp][lane] = acc[0];
-        if (lane == 0) sum_s[warp] = sum[0];
+    if constexpr (MANY) {
+        acc_s[e0][lane & 7] = acc[0];
+        if ((lane & 7) == 0) sum_s[e0] = sum[0];
         __syncthreads();
-        if (warp) return;
+        if (e0) return;
     }
 #pragma unroll
     for (int e = 1; e < 8; ++e) {
-        const float4 y = WARPS == 1 ? acc[e % SUMS] : acc_s[WARPS == 1 ? 0 : e][lane];
+        const float4 y = MANY ? acc_s[MANY ? e : 0][lane & 7] : acc[e % SUMS];
         r.x += y.x;
         r.y += y.y;
         r.z += y.z;
         r.w += y.w;
-        l += WARPS == 1 ? sum[e % SUMS] : sum_s[e];
+        l += MANY ? sum_s[e] : sum[e % SUMS];
     }
     const float inv = 1.0f / l;
-    reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv));
-    if (lane == 0) a.lse[bh] = (m + log2f(l)) * 0.693147180559945309f;
+    reinterpret_cast<uint2*>(out)[d4] = make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv));
+    if (first && lane == 0) a.lse[bh] = (m + log2f(l)) * 0.693147180559945309f;
 }
 
 std::atomic<uint64_t> g_configured{0};
@@ -1068,17 +1078,19 @@ cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const
     e = launch_any(a.G, bundle, km, vm, a, grid, stream, false);
     if (e != cudaSuccess || a.n_splits <= 1) return e;
     const long long rows = (long long)a.B * a.Hq;
-    const bool few = a.n_splits <= 32;  // 64 x 4096 (10 splits): a warp each; from some tens of splits on eight share one
+    // Long rows in quarters: 32 rows and heads of 82 splits take 2.5 us (4.1 by a block of eight
+    // warps to a row, with the partials gone from L2).
+    const bool many = a.n_splits > 32 && rows <= 0x1fffffff;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(few ? (rows + 3) / 4 : rows));
-    cfg.blockDim = dim3(few ? 128 : 256);
+    cfg.gridDim = dim3((unsigned)(many ? rows * 4 : (rows + 3) / 4));
+    cfg.blockDim = dim3(many ? 64 : 128);
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return few ? cudaLaunchKernelEx(&cfg, merge_q8_kernel<1>, a) : cudaLaunchKernelEx(&cfg, merge_q8_kernel<8>, a);
+    return many ? cudaLaunchKernelEx(&cfg, merge_q8_kernel<true>, a) : cudaLaunchKernelEx(&cfg, merge_q8_kernel<false>, a);
 }
 
 }  // namespace rk
