@@ -296,8 +296,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 for (int i = 0; i < n_tiles && ok; ++i) {
                     const int g = g0 + i;
                     if (i > 0 && !(ok = wait(bars->v_full[(g - 1) % VST], (uint32_t)((g - 1) / VST)))) break;
-                    if (!(ok = wait(bars->k_full[g % KST], (uint32_t)(g / KST)))) break;
-                    tc_fence_after();
+                    bool have_k = false;
 #pragma unroll 1
                     for (int j = 0; j < 2 && ok; ++j) {
                         const int nt = j ? nt1 : nt0;
@@ -308,7 +307,11 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                             umma_commit_elect(smem_u32(&bars->o_done[j]));
                             continue;
                         }
-                        if (i == 0) tc_fence_after();
+                        if (!have_k) {  // (not before PV, which does without)
+                            if (!(ok = wait(bars->k_full[g % KST], (uint32_t)(g / KST)))) break;
+                            have_k = true;
+                        }
+                        tc_fence_after();
                         mma_ss_steps<0, 8, K_MAJOR_128, K_MAJOR_128, true>(tmem + j * 128, dQ + (uint32_t)j * TILE,
                                                                            dK + (uint32_t)(g % KST) * TILE, idS, 0u);
                         umma_commit_elect(smem_u32(&bars->s_full[j]));
@@ -403,7 +406,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 const bool up = c >= 4;
                 const uint32_t c0 = (((2 * c & 7) ^ (r0 & 7)) << 4) ^ (up ? 16u : 0u), c1 = c0 ^ 16;
                 uint4 ahead = *reinterpret_cast<const uint4*>(codes);
-#pragma unroll 1
+#pragma unroll 2
                 for (int e = 0; e < 8; ++e) {
                     const uint4 w = up ? make_uint4(ahead.z, ahead.w, ahead.x, ahead.y) : ahead;
                     ahead = *reinterpret_cast<const uint4*>(codes + min(e + 1, 7) * Q8_BLOCK_BYTES);
@@ -432,7 +435,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 uint8_t* vt = sm + OFF_V + vst * PF_TILE_BYTES + (c >> 2) * 2048 + r0 * 128;
                 uint32_t nan = 0;
                 ahead = *reinterpret_cast<const uint4*>(codes + PF_BN * HEAD_DIM);
-#pragma unroll 1
+#pragma unroll 2
                 for (int e = 0; e < 8; ++e) {
                     uint4 w = up ? make_uint4(ahead.z, ahead.w, ahead.x, ahead.y) : ahead;
                     ahead = *reinterpret_cast<const uint4*>(codes + PF_BN * HEAD_DIM + min(e + 1, 7) * Q8_BLOCK_BYTES);
@@ -450,102 +453,99 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 mbar_arrive(smem_u32(&bars->v_full[vst]));
                 load_part(next, 1);
             };
-            // ---- the unit's first tile, while the unit before is still at work ----
             int next = page_ids(0);
             load_part(next, 0);
             load_part(next, 1);
             load_scales(next);
             next = page_ids(1);
-            convert(0, next);
-            next = page_ids(2);
-            // ---- q ----
-            wait(bars->q_empty, wu ^ 1);
-            if (named_bar_or(3, 128, !ok)) {
-                ok = false;
-                break;
-            }
-            // Both q-tiles by cp.async (rows past the last query as zeros), then rewritten in place.
-            cp_async_wait_all();  // (the next tile's codes too)
 #pragma unroll 1
-            for (int j = 0; j < 2; ++j) {
-                const int s0 = (2 * u.pair + j) * rph, ch = tid & 15;  // 16-byte chunk ch of rows tid / 16 + 8 i
-                const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q) + query_row(a, u.b, u.kvh, rsh, s0, 0) * HEAD_DIM + ch * 8;
-                const uint32_t dst = s_base + OFF_Q + j * PF_TILE_BYTES + (ch >> 3) * 16384;
-#pragma unroll 4
-                for (int r = tid >> 4; r < PF_BM; r += 8) {
-                    const int si = r & (rph - 1);
-                    const bool in = s0 + si < a.Sq;
-                    cp_async16_or_zero(dst + sw128_off(r, ch & 7), src + (in ? ((size_t)(r >> rsh) * a.Sq + si) * HEAD_DIM : 0), in);
-                }
-            }
-            cp_async_commit();
-            cp_async_wait_all();
-            named_bar_sync(3, 128);
-#pragma unroll 1
-            for (int j = 0; j < 2; ++j) {
-                const int s0 = (2 * u.pair + j) * rph;
-                uint8_t* qt = sm + OFF_Q + j * PF_TILE_BYTES;
-                {   // the largest element of row tid
-                    uint32_t m = 0;
-#pragma unroll 4
-                    for (int i = 0; i < 16; ++i) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(qt + (i >> 3) * 16384 + sw128_off(tid, i & 7));
-                        m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-                    }
-                    m = max(m & 0xffffu, m >> 16);
-                    const bool bad = m >= Q8_LIMIT_BF16;
-                    const int e = bad ? 0 : q8_exponent(m);
-                    bars->qinv[tid] = bad ? 0.0f : pow2(-e);
-                    bars->qscale[j][tid] = bad ? __int_as_float(0x7fc00000) : a.qk_scale_log2 * pow2(e);
-                }
-                named_bar_sync(3, 128);
-                // A thread has a position and 8 rotation pairs (dims 8 ch .. and 64 + 8 ch ..) of its G query
-                // heads, so an angle is computed once for all of them.
-                const int si = tid & (rph - 1);
-                const uint32_t pos = s0 + si < a.Sq ? (uint32_t)a.position_ids[(size_t)u.b * a.Sq + s0 + si] : 0;
-#pragma unroll 1
-                for (int ch = tid >> rsh; ch < 8; ch += a.G) {
-                    float2 cs[4], sn[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        rope_cos_sin(pos, a.rope_turns[8 * ch + 2 * i], cs[i].x, sn[i].x);
-                        rope_cos_sin(pos, a.rope_turns[8 * ch + 2 * i + 1], cs[i].y, sn[i].y);
-                    }
-#pragma unroll 2
-                    for (int r = si; r < PF_BM; r += rph) {
-                        uint4* pl = reinterpret_cast<uint4*>(qt + sw128_off(r, ch));
-                        uint4* ph = reinterpret_cast<uint4*>(qt + 16384 + sw128_off(r, ch));
-                        const uint4 lo = *pl, hi = *ph;
-                        const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
-                        const float inv = bars->qinv[r];
-                        const float2 inv2 = make_float2(inv, inv);
-                        uint32_t ol[4], oh[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 l = fmul2(make_float2(bf16lo(lw[i]), bf16hi(lw[i])), inv2);
-                            const float2 h = fmul2(make_float2(bf16lo(hw[i]), bf16hi(hw[i])), inv2);
-                            const float2 x = ffma2(make_float2(-h.x, -h.y), sn[i], fmul2(l, cs[i]));
-                            const float2 y = ffma2(l, sn[i], fmul2(h, cs[i]));
-                            ol[i] = pack_f16x2(x.x, x.y);
-                            oh[i] = pack_f16x2(y.x, y.y);
-                        }
-                        // a row that is out of range has 0 times what may be infinite: zeros instead
-                        const bool zero = inv == 0.0f;
-                        *pl = zero ? make_uint4(0, 0, 0, 0) : make_uint4(ol[0], ol[1], ol[2], ol[3]);
-                        *ph = zero ? make_uint4(0, 0, 0, 0) : make_uint4(oh[0], oh[1], oh[2], oh[3]);
-                    }
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(smem_u32(&bars->q_ready[j]));
-                named_bar_sync(3, 128);  // qinv may be written again
-            }
-            // ---- the other tiles ----
-#pragma unroll 1
-            for (int i = 1; i < n_tiles; ++i) {
+            for (int i = 0; i < n_tiles; ++i) {
                 const int after = next;
                 next = page_ids(i + 2);
                 convert(i, after);
-                if (!ok) break;
+                if (i > 0 && !ok) break;
+                if (i > 0) continue;
+                // ---- q, with the unit's first tile done while the unit before was still at work ----
+                wait(bars->q_empty, wu ^ 1);
+                if (named_bar_or(3, 128, !ok)) {
+                    ok = false;
+                    break;
+                }
+                // Both q-tiles by cp.async (rows past the last query as zeros), then rewritten in place.
+                cp_async_wait_all();  // (the next tile's codes too)
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) {
+                    const int s0 = (2 * u.pair + j) * rph, ch = tid & 15;  // 16-byte chunk ch of rows tid / 16 + 8 i
+                    const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q) + query_row(a, u.b, u.kvh, rsh, s0, 0) * HEAD_DIM + ch * 8;
+                    const uint32_t dst = s_base + OFF_Q + j * PF_TILE_BYTES + (ch >> 3) * 16384;
+#pragma unroll 4
+                    for (int r = tid >> 4; r < PF_BM; r += 8) {
+                        const int si = r & (rph - 1);
+                        const bool in = s0 + si < a.Sq;
+                        cp_async16_or_zero(dst + sw128_off(r, ch & 7), src + (in ? ((size_t)(r >> rsh) * a.Sq + si) * HEAD_DIM : 0), in);
+                    }
+                }
+                cp_async_commit();
+                cp_async_wait_all();
+                named_bar_sync(3, 128);
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j) {
+                    const int s0 = (2 * u.pair + j) * rph;
+                    uint8_t* qt = sm + OFF_Q + j * PF_TILE_BYTES;
+                    {   // the largest element of row tid
+                        uint32_t m = 0;
+#pragma unroll 4
+                        for (int i = 0; i < 16; ++i) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(qt + (i >> 3) * 16384 + sw128_off(tid, i & 7));
+                            m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+                        }
+                        m = max(m & 0xffffu, m >> 16);
+                        const bool bad = m >= Q8_LIMIT_BF16;
+                        const int e = bad ? 0 : q8_exponent(m);
+                        bars->qinv[tid] = bad ? 0.0f : pow2(-e);
+                        bars->qscale[j][tid] = bad ? __int_as_float(0x7fc00000) : a.qk_scale_log2 * pow2(e);
+                    }
+                    named_bar_sync(3, 128);
+                    // A thread has a position and 8 rotation pairs (dims 8 ch .. and 64 + 8 ch ..) of its G query
+                    // heads, so an angle is computed once for all of them.
+                    const int si = tid & (rph - 1);
+                    const uint32_t pos = s0 + si < a.Sq ? (uint32_t)a.position_ids[(size_t)u.b * a.Sq + s0 + si] : 0;
+#pragma unroll 1
+                    for (int ch = tid >> rsh; ch < 8; ch += a.G) {
+                        float2 cs[4], sn[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            rope_cos_sin(pos, a.rope_turns[8 * ch + 2 * i], cs[i].x, sn[i].x);
+                            rope_cos_sin(pos, a.rope_turns[8 * ch + 2 * i + 1], cs[i].y, sn[i].y);
+                        }
+#pragma unroll 2
+                        for (int r = si; r < PF_BM; r += rph) {
+                            uint4* pl = reinterpret_cast<uint4*>(qt + sw128_off(r, ch));
+                            uint4* ph = reinterpret_cast<uint4*>(qt + 16384 + sw128_off(r, ch));
+                            const uint4 lo = *pl, hi = *ph;
+                            const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+                            const float inv = bars->qinv[r];
+                            const float2 inv2 = make_float2(inv, inv);
+                            uint32_t ol[4], oh[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 l = fmul2(make_float2(bf16lo(lw[i]), bf16hi(lw[i])), inv2);
+                                const float2 h = fmul2(make_float2(bf16lo(hw[i]), bf16hi(hw[i])), inv2);
+                                const float2 x = ffma2(make_float2(-h.x, -h.y), sn[i], fmul2(l, cs[i]));
+                                const float2 y = ffma2(l, sn[i], fmul2(h, cs[i]));
+                                ol[i] = pack_f16x2(x.x, x.y);
+                                oh[i] = pack_f16x2(y.x, y.y);
+                            }
+                            // a row that is out of range has 0 times what may be infinite: zeros instead
+                            const bool zero = inv == 0.0f;
+                            *pl = zero ? make_uint4(0, 0, 0, 0) : make_uint4(ol[0], ol[1], ol[2], ol[3]);
+                            *ph = zero ? make_uint4(0, 0, 0, 0) : make_uint4(oh[0], oh[1], oh[2], oh[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(smem_u32(&bars->q_ready[j]));
+                    named_bar_sync(3, 128);  // qinv may be written again
+                }
             }
             cp_async_wait_all();
             const int slot = wu & 1;
