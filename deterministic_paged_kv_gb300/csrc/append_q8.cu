@@ -27,7 +27,7 @@
 // to a token, four tokens to a warp's turn, once for the exponents and once more (mostly still
 // in registers, else out of L1) for the codes.
 // 64 single tokens x 8 heads: 4.7 us a launch (latency: launch, slots, values, stores); 2048
-// tokens in runs of 16: 6.8 us; 15600 tokens of 24 ragged rows: 30 us (bound by instructions:
+// tokens in runs of 16: 6.7 us; 12700 tokens of 24 ragged rows: 29 us (bound by instructions, a quarter of them for the borders:
 // the bytes alone would take 12).
 #include "q8_device.cuh"
 
@@ -141,14 +141,16 @@ __device__ __noinline__ float2 rotate_exact(float lo, float hi, uint32_t pos, ui
     return make_float2(two_dot(lo, cn, -hi, sn), two_dot(hi, cn, lo, sn));
 }
 
-// Whether the codes of two scaled values and of values up to d away may differ.
-__device__ __forceinline__ bool near_border(float v0, float v1, float d) {
-    return cvt_e4m3x2(flush_code(v0 - d), flush_code(v1 - d)) != cvt_e4m3x2(flush_code(v0 + d), flush_code(v1 + d));
+// Whether two values y may have other codes than what is known of them says: they lie from y0 to y1.
+__device__ __forceinline__ bool near_border(float2 y0, float2 y1) {
+    return cvt_e4m3x2(flush_code(y0.x), flush_code(y0.y)) != cvt_e4m3x2(flush_code(y1.x), flush_code(y1.y));
 }
 // The cheap half of it: whether a border of 4 bits (the upper 12 of the word, half up) lies
-// between v - d and v + d, at any size.
-__device__ __forceinline__ bool maybe_border(float v, float d) {
-    return ((__float_as_uint(v - d) + 0x80000u) ^ (__float_as_uint(v + d) + 0x80000u)) & 0xfff00000u;
+// between them, at any size.
+__device__ __forceinline__ bool maybe_border(float2 y0, float2 y1) {
+    const uint32_t h = 0x80000u;
+    return (((__float_as_uint(y0.x) + h) ^ (__float_as_uint(y1.x) + h)) | ((__float_as_uint(y0.y) + h) ^ (__float_as_uint(y1.y) + h))) &
+           0xfff00000u;
 }
 
 __device__ __forceinline__ uint2 pack8(const float (&y)[8]) {
@@ -334,16 +336,16 @@ __global__ void __launch_bounds__(AQ_THREADS) append_q8_kernel(const __grid_cons
             for (int i = 0; i < 8; ++i) {
                 float c, s;
                 rope_cos_sin(p, a.rope_turns[8 * u + i], c, s);
-                yl[i] = fmaf(-hi[i], s, lo[i] * c) * inv;
-                yh[i] = fmaf(lo[i], s, hi[i] * c) * inv;
+                float2 y = fmul2(make_float2(lo[i], hi[i]), make_float2(c, c));
+                y = fmul2(ffma2(make_float2(-hi[i], lo[i]), make_float2(s, s), y), make_float2(inv, inv));
                 const float d = (fabsf(lo[i]) + fabsf(hi[i])) * (ROT_ERR * inv);
-                if (maybe_border(yl[i], d) | maybe_border(yh[i], d)) {
-                    if (near_border(yl[i], yh[i], d)) {
-                        const float2 y = rotate_exact(lo[i], hi[i], p, a.rope_turns[8 * u + i]);
-                        yl[i] = y.x * inv;
-                        yh[i] = y.y * inv;
-                    }
+                const float2 y0 = fadd2(y, make_float2(-d, -d)), y1 = fadd2(y, make_float2(d, d));
+                if (maybe_border(y0, y1) && near_border(y0, y1)) {
+                    y = rotate_exact(lo[i], hi[i], p, a.rope_turns[8 * u + i]);
+                    y = fmul2(y, make_float2(inv, inv));
                 }
+                yl[i] = y.x;
+                yh[i] = y.y;
             }
             const bool good = !(e & 0x100u);
             store_codes(a.k_cache + row, u, good ? pack8(yl) : nan8, good ? pack8(yh) : nan8);
