@@ -506,8 +506,8 @@ int rk_paged_prefill_backward_workspace_bytes(const rk_paged_plan_t *plan, uint6
  * pass the pool while it needs one (RK_STATUS_POOL; also taken outside
  * [0, n_pool], which leaves no page).  A page id outside [0, num_pages), from the
  * pool or in a started page's entry, gives slot -1 and RK_STATUS_PAGE_OOB.
- * Plan: B, W, num_pages (B at most 16384, else RK_E_UNSUPPORTED).  One launch, no
- * allocation, no host synchronisation.  Errors: RK_E_ARG (null or misaligned
+ * Plan: B, W, num_pages (B at most 16384, else RK_E_UNSUPPORTED).  One launch, two
+ * where cap is above 4096; no allocation, no host synchronisation.  Errors: RK_E_ARG (null or misaligned
  * pointer, negative n_pool or cap), RK_E_DEVICE, RK_E_CUDA.
  */
 int rk_paged_tables_extend(const rk_paged_plan_t *plan, const int32_t *n_new_d, const int32_t *kv_lens_d,
@@ -582,9 +582,13 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t *plan, int32_t split_tokens, c
  * rk_paged_attn_prefill_q8 -- causal chunked prefill (any plan->Sq >= 1) over the
  * 8-bit cache, which already holds the chunk's own K and V: the arguments of
  * rk_paged_attn_prefill with the scales.  One ascending pass over the keys per
- * query, no split.  Status and failed rows as in rk_paged_attn_decode_q8, where what a
- * query meets is what its q-tile reads (keys up to the largest position of the
- * tile's queries).  Errors: as rk_paged_attn_prefill.
+ * query, no split.  Status and failed rows as in rk_paged_attn_decode_q8; queries go
+ * through the kernel in units of 256 / (Hq / Hkv) neighbours, and a unit's queries that
+ * see a key fail together for metadata, a scale, or a NaN code of V among the keys
+ * that any of them reads (a NaN code of K fails those that see it).
+ * Precision: q is rounded to FP16 after its rotation (2^-11 of each element, as
+ * in the BF16 call), which moves lse by some 1e-5 (the decode call keeps 2^-16).
+ * Errors: as rk_paged_attn_prefill.
  */
 int rk_paged_attn_prefill_q8(const rk_paged_plan_t *plan, const void *q, const void *k_cache,
                              const void *v_cache, const float *k_scale, const float *v_scale,
