@@ -16,17 +16,23 @@
 // 2^-16, but its 12 MMAs a tile read 96 KiB of operands where 8 of FP16 read 64, took 125
 // cycles each, and left the copies no room in the shared memory's bandwidth: 925 us for
 // S = 8192, 137 us for the chunk.)
-// What bounds it: the chain softmax -> PV -> S of each q-tile (two q-tiles overlap), then the
-// tensor pipe, 2048 cycles a pair of q-tiles and KV tile.
-//
+// What bounds it: the chain softmax (1760 cycles) -> hand-over (250) -> PV and S of the next
+// tile (16 MMAs of 108 cycles) of each q-tile, two of which overlap: 3700 cycles a KV tile.  The
+// MMAs would take 64 each, but S reads both operands from shared memory at all of its bandwidth,
+// and the conversions take 40% of what they leave.  (An issuer to each q-tile: 538 us, as the
+// MMAs of the two then share the pipe and both chains grow; a maximum found along with the
+// exponentials and the tile done again where it rose: 500 us.)
+// S = 8192 of 32 heads: 468 us, tensor pipe 49% active; 4 chunks of 512 behind 1536: 71 us
+// (256 units on 152 CTAs: two units where 1.68 would be even); 33 queries: 22 us.
 // Roles (512 threads, registers rebalanced with setmaxnreg):
 //   warp 15      scheduler: each unit's metadata, published as a descriptor (two slots);
-//   warpgroup 0  transform: q of both q-tiles of a unit (as soon as the unit before has read
-//                its own), K and V tiles from the cache to FP16 operands (V zero past the last
-//                key), scales.  Codes come by cp.async, a thread's own 16 bytes of each page,
-//                a tile ahead, and are converted in a rolled loop (with the codes in
-//                registers and the loop unrolled the code pushed the softmax's out of the
-//                instruction cache: 615 us, the softmax twice as slow);
+//   warpgroup 0  transform: K and V tiles from the cache to FP16 operands (V zero past the last
+//                key), scales; q of both q-tiles of a unit, as soon as the unit before has read
+//                its own (the CTA's first are made by the softmax warpgroups, which have nothing
+//                to do yet: 2 us of a call).  Codes come by cp.async, a thread's own 16 bytes of
+//                each page, a tile ahead, and are converted two pages to a turn of a loop (with
+//                the codes in registers and all unrolled the code pushed the softmax's out of
+//                the instruction cache: 615 us of S = 8192 where it takes 468);
 //   warpgroups 1, 2  softmax of q-tile 0, 1: a thread per accumulator row;
 //   warp 13      MMA issuer (converged); warps 12, 14 have nothing to do.
 // Nothing depends on B, W or the grid.
@@ -47,7 +53,7 @@ constexpr float RESCALE_SLACK = 8.0f, P_BIAS = 7.0f;
 constexpr uint32_t UNIT_READERS = 32 + 128 + 256;
 
 // setmaxnreg split (sum 4 x 128 = the 512 x 128 registers the CTA launches with)
-constexpr int REG_XFORM = 88, REG_SOFTMAX = 184, REG_CTRL = 56;
+constexpr int REG_XFORM = 96, REG_SOFTMAX = 184, REG_CTRL = 48;
 static_assert(REG_XFORM + 2 * REG_SOFTMAX + REG_CTRL == 4 * 128, "register split must sum to the launch budget");
 
 constexpr int OFF_Q = 0;                             // [q-tile][64-dim half][128 rows][128 B]
@@ -62,6 +68,7 @@ struct PqUnit {
     int bad;
 };
 
+constexpr int Q_BAD = -128;
 struct PqBars {
     uint64_t q_ready[2], q_empty;
     uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], sc_full[SCST];
@@ -74,7 +81,7 @@ struct PqBars {
     PqUnit unit[2];
     alignas(16) uint8_t r_flag[2][128];  // 1: NaN code in V, 2: a scale that is none
     alignas(16) float4 sc[SCST][PF_PAGES_PER_TILE];  // k scale, log2 of v's, 1 / v's
-    float qinv[PF_BM];                   // a query's power of two, inverted
+    int8_t qexp[2][PF_BM];               // exponent of a query's power of two; Q_BAD: out of range
     float qscale[2][PF_BM];              // score factor of each query (log2 domain); NaN: out of range
 };
 constexpr int PQ_SMEM_BYTES = OFF_BAR + (int)sizeof(PqBars);
@@ -189,6 +196,81 @@ __device__ __forceinline__ void transpose4(uint32_t (&w)[4][4], int i) {
                     else w[q | b][e] = got;
                 }
             }
+}
+
+// q-tile `tile` of a row and KV head into the operand j by cp.async (a warpgroup; rows past the
+// last query as zeros), as it is.
+__device__ __forceinline__ void load_q(const AttnQ8Args& a, uint32_t s_base, int b, int kvh, int tile, int j, int rsh, int t) {
+    const int rph = 1 << rsh, s0 = tile * rph, ch = t & 15;  // 16-byte chunk ch of rows t / 16 + 8 i
+    const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q) + query_row(a, b, kvh, rsh, s0, 0) * HEAD_DIM + ch * 8;
+    const uint32_t dst = s_base + OFF_Q + j * PF_TILE_BYTES + (ch >> 3) * 16384;
+#pragma unroll 4
+    for (int r = t >> 4; r < PF_BM; r += 8) {
+        const int si = r & (rph - 1);
+        const bool in = s0 + si < a.Sq;
+        cp_async16_or_zero(dst + sw128_off(r, ch & 7), src + (in ? ((size_t)(r >> rsh) * a.Sq + si) * HEAD_DIM : 0), in);
+    }
+    cp_async_commit();
+}
+
+// The operand j from bf16 to rotated FP16 in place (the warpgroup behind named barrier `bar`); its
+// threads arrive at q_ready.
+__device__ __forceinline__ void rotate_q(const AttnQ8Args& a, uint8_t* sm, PqBars* bars, int b, int tile, int j, int rsh, int t, int bar) {
+    const int rph = 1 << rsh, s0 = tile * rph;
+    uint8_t* qt = sm + OFF_Q + j * PF_TILE_BYTES;
+    {   // the largest element of row t
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+            const uint4 w = *reinterpret_cast<const uint4*>(qt + (i >> 3) * 16384 + sw128_off(t, i & 7));
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+        }
+        m = max(m & 0xffffu, m >> 16);
+        const bool bad = m >= Q8_LIMIT_BF16;
+        const int e = bad ? 0 : q8_exponent(m);
+        bars->qexp[j][t] = (int8_t)(bad ? Q_BAD : e);
+        bars->qscale[j][t] = bad ? __int_as_float(0x7fc00000) : a.qk_scale_log2 * pow2(e);
+    }
+    named_bar_sync(bar, 128);
+    // A thread has a position and 8 rotation pairs (dims 8 ch .. and 64 + 8 ch ..) of its G query
+    // heads, so an angle is computed once for all of them.
+    const int si = t & (rph - 1);
+    const uint32_t pos = s0 + si < a.Sq ? (uint32_t)a.position_ids[(size_t)b * a.Sq + s0 + si] : 0;
+#pragma unroll 1
+    for (int ch = t >> rsh; ch < 8; ch += a.G) {
+        float2 cs[4], sn[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            rope_cos_sin(pos, a.rope_turns[8 * ch + 2 * i], cs[i].x, sn[i].x);
+            rope_cos_sin(pos, a.rope_turns[8 * ch + 2 * i + 1], cs[i].y, sn[i].y);
+        }
+#pragma unroll 2
+        for (int r = si; r < PF_BM; r += rph) {
+            uint4* pl = reinterpret_cast<uint4*>(qt + sw128_off(r, ch));
+            uint4* ph = reinterpret_cast<uint4*>(qt + 16384 + sw128_off(r, ch));
+            const uint4 lo = *pl, hi = *ph;
+            const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+            const int e = bars->qexp[j][r];
+            const bool zero = e == Q_BAD;
+            const float inv = zero ? 0.0f : pow2(-e);
+            const float2 inv2 = make_float2(inv, inv);
+            uint32_t ol[4], oh[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 l = fmul2(make_float2(bf16lo(lw[i]), bf16hi(lw[i])), inv2);
+                const float2 h = fmul2(make_float2(bf16lo(hw[i]), bf16hi(hw[i])), inv2);
+                const float2 x = ffma2(make_float2(-h.x, -h.y), sn[i], fmul2(l, cs[i]));
+                const float2 y = ffma2(l, sn[i], fmul2(h, cs[i]));
+                ol[i] = pack_f16x2(x.x, x.y);
+                oh[i] = pack_f16x2(y.x, y.y);
+            }
+            // a row that is out of range has 0 times what may be infinite: zeros instead
+            *pl = zero ? make_uint4(0, 0, 0, 0) : make_uint4(ol[0], ol[1], ol[2], ol[3]);
+            *ph = zero ? make_uint4(0, 0, 0, 0) : make_uint4(oh[0], oh[1], oh[2], oh[3]);
+        }
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(smem_u32(&bars->q_ready[j]));
 }
 
 __global__ void __launch_bounds__(PQ_THREADS, 1)
@@ -465,87 +547,20 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 convert(i, after);
                 if (i > 0 && !ok) break;
                 if (i > 0) continue;
-                // ---- q, with the unit's first tile done while the unit before was still at work ----
+                // ---- q, with the unit's first tile done while the unit before was still at work
+                // (the CTA's first: the softmax warpgroups') ----
+                if (kk == 0) continue;
                 wait(bars->q_empty, wu ^ 1);
                 if (named_bar_or(3, 128, !ok)) {
                     ok = false;
                     break;
                 }
-                // Both q-tiles by cp.async (rows past the last query as zeros), then rewritten in place.
-                cp_async_wait_all();  // (the next tile's codes too)
 #pragma unroll 1
-                for (int j = 0; j < 2; ++j) {
-                    const int s0 = (2 * u.pair + j) * rph, ch = tid & 15;  // 16-byte chunk ch of rows tid / 16 + 8 i
-                    const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.q) + query_row(a, u.b, u.kvh, rsh, s0, 0) * HEAD_DIM + ch * 8;
-                    const uint32_t dst = s_base + OFF_Q + j * PF_TILE_BYTES + (ch >> 3) * 16384;
-#pragma unroll 4
-                    for (int r = tid >> 4; r < PF_BM; r += 8) {
-                        const int si = r & (rph - 1);
-                        const bool in = s0 + si < a.Sq;
-                        cp_async16_or_zero(dst + sw128_off(r, ch & 7), src + (in ? ((size_t)(r >> rsh) * a.Sq + si) * HEAD_DIM : 0), in);
-                    }
-                }
-                cp_async_commit();
-                cp_async_wait_all();
+                for (int j = 0; j < 2; ++j) load_q(a, s_base, u.b, u.kvh, 2 * u.pair + j, j, rsh, tid);
+                cp_async_wait_all();  // (the next tile's codes too)
                 named_bar_sync(3, 128);
 #pragma unroll 1
-                for (int j = 0; j < 2; ++j) {
-                    const int s0 = (2 * u.pair + j) * rph;
-                    uint8_t* qt = sm + OFF_Q + j * PF_TILE_BYTES;
-                    {   // the largest element of row tid
-                        uint32_t m = 0;
-#pragma unroll 4
-                        for (int i = 0; i < 16; ++i) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(qt + (i >> 3) * 16384 + sw128_off(tid, i & 7));
-                            m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-                        }
-                        m = max(m & 0xffffu, m >> 16);
-                        const bool bad = m >= Q8_LIMIT_BF16;
-                        const int e = bad ? 0 : q8_exponent(m);
-                        bars->qinv[tid] = bad ? 0.0f : pow2(-e);
-                        bars->qscale[j][tid] = bad ? __int_as_float(0x7fc00000) : a.qk_scale_log2 * pow2(e);
-                    }
-                    named_bar_sync(3, 128);
-                    // A thread has a position and 8 rotation pairs (dims 8 ch .. and 64 + 8 ch ..) of its G query
-                    // heads, so an angle is computed once for all of them.
-                    const int si = tid & (rph - 1);
-                    const uint32_t pos = s0 + si < a.Sq ? (uint32_t)a.position_ids[(size_t)u.b * a.Sq + s0 + si] : 0;
-#pragma unroll 1
-                    for (int ch = tid >> rsh; ch < 8; ch += a.G) {
-                        float2 cs[4], sn[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            rope_cos_sin(pos, a.rope_turns[8 * ch + 2 * i], cs[i].x, sn[i].x);
-                            rope_cos_sin(pos, a.rope_turns[8 * ch + 2 * i + 1], cs[i].y, sn[i].y);
-                        }
-#pragma unroll 2
-                        for (int r = si; r < PF_BM; r += rph) {
-                            uint4* pl = reinterpret_cast<uint4*>(qt + sw128_off(r, ch));
-                            uint4* ph = reinterpret_cast<uint4*>(qt + 16384 + sw128_off(r, ch));
-                            const uint4 lo = *pl, hi = *ph;
-                            const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
-                            const float inv = bars->qinv[r];
-                            const float2 inv2 = make_float2(inv, inv);
-                            uint32_t ol[4], oh[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 l = fmul2(make_float2(bf16lo(lw[i]), bf16hi(lw[i])), inv2);
-                                const float2 h = fmul2(make_float2(bf16lo(hw[i]), bf16hi(hw[i])), inv2);
-                                const float2 x = ffma2(make_float2(-h.x, -h.y), sn[i], fmul2(l, cs[i]));
-                                const float2 y = ffma2(l, sn[i], fmul2(h, cs[i]));
-                                ol[i] = pack_f16x2(x.x, x.y);
-                                oh[i] = pack_f16x2(y.x, y.y);
-                            }
-                            // a row that is out of range has 0 times what may be infinite: zeros instead
-                            const bool zero = inv == 0.0f;
-                            *pl = zero ? make_uint4(0, 0, 0, 0) : make_uint4(ol[0], ol[1], ol[2], ol[3]);
-                            *ph = zero ? make_uint4(0, 0, 0, 0) : make_uint4(oh[0], oh[1], oh[2], oh[3]);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    mbar_arrive(smem_u32(&bars->q_ready[j]));
-                    named_bar_sync(3, 128);  // qinv may be written again
-                }
+                for (int j = 0; j < 2; ++j) rotate_q(a, sm, bars, u.b, 2 * u.pair + j, j, rsh, tid, 3);
             }
             cp_async_wait_all();
             const int slot = wu & 1;
@@ -565,13 +580,32 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + j * 128, tO = tmem + 256 + j * 128;
         const float nanv = __int_as_float(0x7fc00000);
+        // A wait gave up: the rows of this q-tile from the CTA's unit k on are written as failed.
+        auto fail_from = [&](int k) {
+#pragma unroll 1
+            for (;; ++k) {
+                const long long u = cta_unit(k, cta, grid);
+                if (u >= total) break;
+                int b, kvh, pair;
+                unit_place(a, n_qtiles, u, b, kvh, pair);
+                const int t0 = (2 * pair + j) * rph;
+                if (t0 + (r & (rph - 1)) < a.Sq) write_row(a, query_row(a, b, kvh, rsh, t0, r), nanv);
+            }
+            if (r == 0 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
+        };
         int g0 = 0;        // KV tiles before the unit
         uint32_t ph = 0;   // bit 0 s_full (this q-tile's tiles), bit 1 o_done, bits 2-3 work units
         bool ok = true;
 #pragma unroll 1
         for (int kk = 0;; ++kk) {
             const int uslot = kk & 1;
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->u_full[uslot]), (uint32_t)((kk >> 1) & 1), pc)))) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->u_full[uslot]), (uint32_t)((kk >> 1) & 1), pc)) != 0;
+            // (at the first unit the warpgroup's warps go on or leave together: it makes its own operand)
+            if (kk == 0 && named_bar_or(4 + j, 128, !ok)) ok = false;
+            if (!ok) {
+                fail_from(kk);
+                break;
+            }
             const volatile PqUnit* un = &bars->unit[uslot];
             if (un->end) break;
             const int s0 = (2 * un->pair + j) * rph, s = s0 + (r & (rph - 1));
@@ -587,6 +621,12 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
             {
                 const int p = valid ? a.position_ids[(size_t)un->b * a.Sq + s] : -1, kv_len = un->kv_len;
                 n_vis = p < 0 ? 0 : (p >= kv_len ? kv_len : p + 1);
+            }
+            if (kk == 0) {
+                load_q(a, s_base, un->b, un->kvh, 2 * un->pair + j, j, rsh, r);
+                cp_async_wait_all();
+                named_bar_sync(4 + j, 128);
+                rotate_q(a, sm, bars, un->b, 2 * un->pair + j, j, rsh, r, 4 + j);
             }
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->q_ready[j]), (ph >> 2) & 1u, pc));
             const float scr = bars->qscale[j][r];
@@ -682,17 +722,8 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                     mbar_arrive(smem_u32(&bars->r_empty[slot]));
                 }
             }
-            if (!ok) {  // a wait gave up: this unit's rows and the CTA's later units are written as failed
-                if (valid) write_row(a, row, nanv);
-                for (int k2 = kk + 1;; ++k2) {
-                    const long long u2 = cta_unit(k2, cta, grid);
-                    if (u2 >= total) break;
-                    int b2, kvh2, pair2;
-                    unit_place(a, n_qtiles, u2, b2, kvh2, pair2);
-                    const int t0 = (2 * pair2 + j) * rph;
-                    if (t0 + (r & (rph - 1)) < a.Sq) write_row(a, query_row(a, b2, kvh2, rsh, t0, r), nanv);
-                }
-                if (r == 0 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
+            if (!ok) {
+                fail_from(kk);
                 break;
             }
             // a query that sees a key fails if its unit does or its sum is beyond FP32 (which a NaN
