@@ -422,24 +422,41 @@ def attn_ragged(p: Plan, max_q_len, qo_indptr, q, k_cache, v_cache, block_table,
             k_cache, v_cache, block_table, kv_lens, position_ids, out, lse, status, stream, ragged=True)
 
 
+class _Types:
+    """torch's types and device queries, looked up once: an import statement in each
+    helper costs a call more than the checks do."""
+    names = None
+
+    def __init__(self):
+        import torch
+        self.i32, self.f32, self.bf16, self.f8 = torch.int32, torch.float32, torch.bfloat16, torch.float8_e4m3fn
+        self.device, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _types():
+    if _Types.names is None:
+        _Types.names = _Types()
+    return _Types.names
+
+
 def _pointers(tensors):
     """Device pointers of ``(tensor, dtype, shape, name)`` entries, each checked:
     type, shape (None: any), contiguous, on the current CUDA device (the one
     that the call launches on).  This runs for every call, so it asks each
     tensor for no more than that."""
     ptrs = []
-    dev = -1
+    dev = -2
     for t, dt, shape, name in tensors:
         if t.dtype is not dt:
             raise TypeError("%s must be %s (got %s)" % (name, dt, t.dtype))
         if shape is not None and t.shape != shape:
             raise ValueError("%s has shape %s, the call needs %s" % (name, tuple(t.shape), tuple(shape)))
         d = t.get_device()
-        if d < 0:
-            raise ValueError("%s: expected a CUDA tensor" % name)
         if d != dev:
+            if d < 0:
+                raise ValueError("%s: expected a CUDA tensor" % name)
             if dev < 0:
-                dev = _cuda_device()
+                dev = _types().device()
             if d != dev:
                 raise ValueError("%s is on device %d, the current device is %d" % (name, d, dev))
         if not t.is_contiguous():
@@ -448,28 +465,24 @@ def _pointers(tensors):
     return ptrs
 
 
-def _cuda_device():
-    """Index of the current CUDA device."""
-    import torch
-    return torch._C._cuda_getDevice()
-
-
 def _raw_stream(stream):
     """As ``_stream``, without making a stream object of the current one."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        ty = _types()
+        return ty.stream(ty.device())
     return _stream(stream)
 
 
-def _status(status):
-    """Entry list of the optional status word."""
-    import torch
+def _with_status(tensors, status):
+    """Pointers of the entries and of the optional status word (None without one), last."""
     if status is None:
-        return []
+        ptr = _pointers(tensors)
+        ptr.append(None)
+        return ptr
     if status.numel() < 1:
         raise ValueError("status must hold at least one int32")
-    return [(status, torch.int32, None, "status")]
+    tensors.append((status, _types().i32, None, "status"))
+    return _pointers(tensors)
 
 
 def tables_extend(p: Plan, n_new, kv_lens, pool, taken, block_table, kv_lens_out, taken_out, qo_indptr,
@@ -478,25 +491,23 @@ def tables_extend(p: Plan, n_new, kv_lens, pool, taken, block_table, kv_lens_out
     [B] and token counts ``n_new`` [B].  ``pool`` holds free page ids, of which
     ``taken`` [1] are handed out; ``block_table`` [B, W] is written in place;
     ``kv_lens_out`` and ``taken_out`` may be ``kv_lens`` and ``taken``.  All int32."""
-    import torch
-    i32 = torch.int32
-    B = p.B
+    i32, B = _types().i32, p.B
     if pool.dim() != 1 or position_ids.dim() != 1:
         raise ValueError("pool and position_ids must have one dimension")
-    ptr = _pointers([(n_new, i32, (B,), "n_new"), (kv_lens, i32, (B,), "kv_lens"), (pool, i32, None, "pool"),
-                     (taken, i32, (1,), "taken"), (block_table, i32, (B, p.W), "block_table"),
-                     (kv_lens_out, i32, (B,), "kv_lens_out"), (taken_out, i32, (1,), "taken_out"),
-                     (qo_indptr, i32, (B + 1,), "qo_indptr"), (position_ids, i32, None, "position_ids"),
-                     (slot_map, i32, position_ids.shape, "slot_map")] + _status(status))
+    ptr = _with_status([(n_new, i32, (B,), "n_new"), (kv_lens, i32, (B,), "kv_lens"), (pool, i32, None, "pool"),
+                        (taken, i32, (1,), "taken"), (block_table, i32, (B, p.W), "block_table"),
+                        (kv_lens_out, i32, (B,), "kv_lens_out"), (taken_out, i32, (1,), "taken_out"),
+                        (qo_indptr, i32, (B + 1,), "qo_indptr"), (position_ids, i32, None, "position_ids"),
+                        (slot_map, i32, position_ids.shape, "slot_map")], status)
     _check(load().rk_paged_tables_extend(ctypes.byref(p), ptr[0], ptr[1], ptr[2], pool.shape[0], *ptr[3:10],
-                                         slot_map.shape[0], ptr[10] if status is not None else None, _raw_stream(stream)))
+                                         slot_map.shape[0], ptr[10], _raw_stream(stream)))
 
 
 def _q8_cache(p: Plan, k_cache, v_cache, k_scale, v_scale):
-    import torch
-    cache, scale = (p.num_pages, p.Hkv, p.page_size, p.D), (p.num_pages, p.Hkv)
-    return [(k_cache, torch.float8_e4m3fn, cache, "k_cache"), (v_cache, torch.float8_e4m3fn, cache, "v_cache"),
-            (k_scale, torch.float32, scale, "k_scale"), (v_scale, torch.float32, scale, "v_scale")]
+    ty, scale = _types(), (p.num_pages, p.Hkv)
+    cache = scale + (p.page_size, p.D)
+    return [(k_cache, ty.f8, cache, "k_cache"), (v_cache, ty.f8, cache, "v_cache"),
+            (k_scale, ty.f32, scale, "k_scale"), (v_scale, ty.f32, scale, "v_scale")]
 
 
 def kv_append_q8(p: Plan, k_new, v_new, slot_map, position_ids, k_cache, v_cache, k_scale, v_scale, status=None,
@@ -505,15 +516,11 @@ def kv_append_q8(p: Plan, k_new, v_new, slot_map, position_ids, k_cache, v_cache
     [n, Hkv, D]) at the slots and positions of ``slot_map`` / ``position_ids`` (int32
     [n]) into the e4m3 caches [num_pages, Hkv, 16, D] with their scales (float32
     [num_pages, Hkv])."""
-    import torch
-    n = slot_map.numel()
+    ty, n = _types(), slot_map.numel()
     new = (n, p.Hkv, p.D)
-    ptr = _pointers([(k_new, torch.bfloat16, new, "k_new"), (v_new, torch.bfloat16, new, "v_new"),
-                     (slot_map, torch.int32, (n,), "slot_map"),
-                     (position_ids, torch.int32, (n,), "position_ids")] +
-                    _q8_cache(p, k_cache, v_cache, k_scale, v_scale) + _status(status))
-    _check(load().rk_paged_kv_append_q8(ctypes.byref(p), n, *ptr[:8], ptr[8] if status is not None else None,
-                                        _raw_stream(stream)))
+    ptr = _with_status([(k_new, ty.bf16, new, "k_new"), (v_new, ty.bf16, new, "v_new"), (slot_map, ty.i32, (n,), "slot_map"),
+                        (position_ids, ty.i32, (n,), "position_ids")] + _q8_cache(p, k_cache, v_cache, k_scale, v_scale), status)
+    _check(load().rk_paged_kv_append_q8(ctypes.byref(p), n, *ptr, _raw_stream(stream)))
 
 
 def decode_q8_scratch_bytes(p: Plan, split_tokens: int = 0) -> int:
@@ -524,12 +531,12 @@ def decode_q8_scratch_bytes(p: Plan, split_tokens: int = 0) -> int:
 
 
 def _attn_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse, status):
-    import torch
-    qs = (p.B, p.Hq, p.Sq, p.D)
-    return _pointers([(q, torch.bfloat16, qs, "q")] + _q8_cache(p, k_cache, v_cache, k_scale, v_scale) +
-                     [(block_table, torch.int32, (p.B, p.W), "block_table"), (kv_lens, torch.int32, (p.B,), "kv_lens"),
-                      (position_ids, torch.int32, (p.B, p.Sq), "position_ids"), (out, torch.bfloat16, qs, "out"),
-                      (lse, torch.float32, qs[:3], "lse")] + _status(status))
+    ty, B = _types(), p.B
+    qs = (B, p.Hq, p.Sq, p.D)
+    return _with_status([(q, ty.bf16, qs, "q")] + _q8_cache(p, k_cache, v_cache, k_scale, v_scale) +
+                        [(block_table, ty.i32, (B, p.W), "block_table"), (kv_lens, ty.i32, (B,), "kv_lens"),
+                         (position_ids, ty.i32, (B, qs[2]), "position_ids"), (out, ty.bf16, qs, "out"),
+                         (lse, ty.f32, qs[:3], "lse")], status)
 
 
 def attn_decode_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse,
@@ -543,16 +550,15 @@ def attn_decode_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table, 
     if scratch is not None:
         sp = _pointers([(scratch, scratch.dtype, None, "scratch")])[0]
         nbytes = scratch.numel() * scratch.element_size()
-    _check(load().rk_paged_attn_decode_q8(ctypes.byref(p), int(split_tokens), *ptr[:10], sp, nbytes,
-                                          ptr[10] if status is not None else None, _raw_stream(stream)))
+    _check(load().rk_paged_attn_decode_q8(ctypes.byref(p), int(split_tokens), *ptr[:10], sp, nbytes, ptr[10],
+                                          _raw_stream(stream)))
 
 
 def attn_prefill_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse,
                     status=None, stream=None):
     """rk_paged_attn_prefill_q8 on device tensors: causal chunked prefill over the 8-bit cache."""
     ptr = _attn_q8(p, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse, status)
-    _check(load().rk_paged_attn_prefill_q8(ctypes.byref(p), *ptr[:10], ptr[10] if status is not None else None,
-                                           _raw_stream(stream)))
+    _check(load().rk_paged_attn_prefill_q8(ctypes.byref(p), *ptr, _raw_stream(stream)))
 
 
 def run(mode: str, q, k_cache, v_cache, block_table, kv_lens, position_ids, plan_obj=None,
