@@ -68,10 +68,11 @@ __device__ __forceinline__ uint32_t token_amax(const uint4& lo, const uint4& hi)
     return m;
 }
 
-// What FP32 may be off by in a rotated value, relative to |lo| + |hi|: the angle
-// of rope_cos_sin is off by at most 2 pi 2^-32 and 2^-24 of itself (2^-22.3 at
-// pi), its sine and cosine by 2^-21.2, the two products and the sum by 2^-23.
-constexpr float ROT_ERR = 1.0f / (1 << 19);
+// What FP32 may be off by in a rotated value, relative to |lo| + |hi|.  The angle: rounded as
+// an integer and as a product, 2 2^-24 of itself and 2^-25 for the constant, 4.7e-7 at pi, and
+// 2 pi 2^-32.  __sincosf on [-pi, pi]: 2^-21.19 by CUDA's documentation, 4.2e-7.  The product, the
+// fused sum and the border's own distance: 3 2^-24, 1.8e-7.
+constexpr float ROT_ERR = 1.1e-6f;
 
 // A value as the unevaluated sum of two floats, about 47 bits; sums and products after
 // Dekker ("A floating-point technique for extending the available precision", 1971).
