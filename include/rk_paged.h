@@ -531,8 +531,8 @@ int rk_paged_tables_extend(const rk_paged_plan_t *plan, const int32_t *n_new_d, 
  * 2^-6.  When a later token raises E the block's earlier codes move along, and
  * the block is bit for bit the same as if all its tokens had come in one call.
  * Slots behind a page's last token are left as they are.  Two runs of one call
- * on the same page (a page in two rows, a slot twice) give unspecified codes
- * and scales for that page.
+ * on the same page (a page in two rows, a slot twice, a token skipped or refused
+ * between others of its page) give unspecified codes and scales for that page.
  * Status: RK_STATUS_PAGE_OOB (slot outside [-1, num_pages * 16)), RK_STATUS_POSITION
  * (negative position): the token is not written; RK_STATUS_RANGE (an input of 2^64
  * or more, or not finite): that token's codes of the tensor become NaN, which the
