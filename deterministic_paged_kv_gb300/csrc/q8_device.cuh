@@ -4,6 +4,7 @@
 
 #include <cuda_fp16.h>
 
+#include "q8_args.h"
 #include "rk_device.cuh"
 
 namespace rk {

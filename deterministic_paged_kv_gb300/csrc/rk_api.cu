@@ -15,7 +15,7 @@
 #include <string>
 #include <vector>
 
-#include "rk_internal.h"
+#include "q8_args.h"
 #include "rk_paged.h"
 
 namespace rk {

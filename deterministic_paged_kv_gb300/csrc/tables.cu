@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "q8_args.h"
 #include "rk_device.cuh"
 
 namespace rk {
