@@ -172,6 +172,33 @@ def test_q8_cache_past_32_bit_offsets(mode):
     assert att._equal(want, att._run(o, plan=p, d=d))
 
 
+@pytest.mark.parametrize("split", [0, 16, 128, 1 << 20])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (32, 8), (16, 2), (3, 3)])
+def test_decode_q8_nan_codes(split, Hq, Hkv):
+    """A NaN code in one dim of one token fails that KV head's queries of that row in all dims, and nothing else."""
+    G = Hq // Hkv
+    lens = [900, 40, 17, 300, 1, 513] * 8
+    c = ref.case(81, lens, Hq, Hkv)
+    want = att._run(c, split)
+    r = np.random.RandomState(split % 1000 + Hq)
+    hit = set()
+    for n in ("k_cache", "v_cache"):
+        for b in r.permutation(len(lens))[:12]:
+            h, t = int(r.randint(Hkv)), int(r.choice([0, lens[b] - 1, r.randint(lens[b])]))
+            c[n].view(torch.uint8)[c["block_table"][b, t // 16].long(), h, t % 16, r.randint(128)] = r.choice([0x7F, 0xFF])
+            hit.add((int(b), h))
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    out, lse = att._run(c, split, status=st)
+    assert int(st.item()) == binding.STATUS_RANGE
+    for b in range(len(lens)):
+        for h in range(Hkv):
+            x, y = out[b, h * G:(h + 1) * G], lse[b, h * G:(h + 1) * G]
+            if (b, h) in hit:
+                assert (x == 0).all() and torch.isnan(y).all(), (b, h)
+            else:
+                assert torch.equal(x, want[0][b, h * G:(h + 1) * G]) and torch.equal(y, want[1][b, h * G:(h + 1) * G]), (b, h)
+
+
 # ----------------------------------------------------------- captured graphs ----
 
 class _Server:
