@@ -23,21 +23,19 @@
 //   o = sum p'_t vcode_t,  out = o / l,
 // with z_t the score in the log2 domain.
 //
-// Work: an item is a split of a row for a bundle of H neighbouring KV heads (4, 2 or
-// 1, the most that divide Hkv).  A TMA copy takes a page's blocks of the whole
-// bundle: copies of 2 KiB (one head) get 4.36 TB/s out of a bare load loop, 4 KiB
-// 5.0, 8 KiB 5.93, and 64 x 4096 took 123 us to load head by head where a bundle
-// of four takes 91.  A step is 512 / H tokens of the bundle, four tiles of 128 tokens and
-// one head; in it the softmax is plain (one maximum over its tokens), steps and splits
-// are joined with the running maximum in FP32.  The copies leave the bundle as
-// [page][half][head][8 tokens][128 B] in shared memory, so that the 16 groups of 8
-// tokens of a head's tile lie at one stride and make one operand.
+// Work: an item is a split of a row for a bundle of H neighbouring KV heads (2, or 1 where
+// Hkv is odd).  A TMA copy takes a page's blocks of the whole bundle: 64 x 4096 takes 125 us head
+// by head (copies of 2 KiB), 91 in bundles of two, 93 in bundles of four, whose items are
+// coarser (20 ragged rows of 8 heads a KV head: 54 us, 48 in twos).  A step is 512 / H tokens
+// of the bundle, four tiles of 128 tokens and one head; in it the softmax is plain (one
+// maximum over its tokens), steps and splits are joined with the running maximum in FP32.  The
+// copies leave the bundle as [page][half][head][8 tokens][128 B] in shared memory, so that
+// the 16 groups of 8 tokens of a head's tile lie at one stride and make one operand.
 // The items in order of row, bundle, split are dealt to a persistent grid of one CTA per
 // SM in runs of equal numbers of steps, so a CTA changes its queries a few times only.
-// (Dealt in turn, 64 x 4096 gave 112 CTAs seven items of four steps and 40 six: they
-// ended between 78 and 98 us.)
+// (Dealt in turn, with four heads to a bundle, CTAs of 64 x 4096 ended between 78 and 98 us.)
 // The copies carry an evict-first hint: the cache is read once and passes by, while the
-// partials of many splits stay in L2 until the merge (64 x 4096: 102 us without, 94 with).
+// partials of many splits stay in L2 until the merge (64 x 4096: 8 us less).
 // Roles (20 warps):
 //   warp 0      TMA producer: a step's K, then its V, 64 KiB each, in a ring of three;
 //   warp 1      MMA issuer: S and PV of each step;
@@ -82,7 +80,7 @@ struct DqShape {
     // shared memory: the ring (a step's K or V to a stage), two buffers of q operands (one per
     // head of the bundle), weights (one per tile: 16 columns of O to a 16-byte row per token,
     // MN-major without swizzle)
-    static constexpr int STAGES = G == 8 && H > 1 ? 2 : 3;  // as room allows
+    static constexpr int STAGES = G == 8 && H == 2 ? 2 : 3;  // as room allows (three, and one buffer of q: 54 us of the ragged rows, not 51)
     static constexpr int Q_BYTES = NS * 128, P_BYTES = NP * DQ_TILE;
     static constexpr int OFF_Q = STAGES * DQ_STEP_BYTES;
     static constexpr int OFF_P = OFF_Q + 2 * H * Q_BYTES;
@@ -113,12 +111,12 @@ struct DqCtrl {
     int ids[DQ_SLOTS][32];           // page of lane p's block: page p / H, head p % H of the step
     uint32_t odd[DQ_SLOTS];          // blocks whose scale is not one
     alignas(16) float4 sc[DQ_SLOTS][32];  // k scale, log2 of v's, 1 / v's of those blocks
-    float qscale[2][32];             // score factor of each query head (log2 domain)
+    float qscale[2][16];             // score factor of each query head (log2 domain)
     uint32_t qbad[2];                // query heads out of range
     float red[2][16][8];             // a step's maximum of each softmax warp, by parity
     float lred[2][16][8];            // an item's sums of each softmax warp, by parity
-    float2 ab[2][4][8];              // a step's scales of the sum so far and of its O, by parity, head, query
-    float top[2][4][8];              // an item's maximum, by parity, head, query
+    float2 ab[2][2][8];              // a step's scales of the sum so far and of its O, by parity, head, query
+    float top[2][2][8];              // an item's maximum, by parity, head, query
     uint32_t fred[2][16];            // queries out of range; bit 31: a scale
     int pre[DQ_PRE];                 // steps before each group of rows
 };
@@ -733,7 +731,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 }
 #pragma unroll
                 for (int g = 0; g < G; ++g) sc[g] = c->qscale[qb][hj * G + g];
-                constexpr uint32_t EACH = H == 1 ? 0xffffffffu : H == 2 ? 0x55555555u : 0x11111111u;
+                constexpr uint32_t EACH = H == 1 ? 0xffffffffu : 0x55555555u;
                 if (odd & (EACH << hj)) range |= 0x80000000u;
                 if (st.flags & DQ_ENDQ) {
                     __syncwarp();
@@ -1038,9 +1036,7 @@ cudaError_t launch_one(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ
 template <int G>
 cudaError_t launch_bundle(int bundle, const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, unsigned grid,
                           cudaStream_t stream, bool configure) {
-    return bundle == 4   ? launch_one<G, 4>(km, vm, a, grid, stream, configure)
-           : bundle == 2 ? launch_one<G, 2>(km, vm, a, grid, stream, configure)
-                         : launch_one<G, 1>(km, vm, a, grid, stream, configure);
+    return bundle == 2 ? launch_one<G, 2>(km, vm, a, grid, stream, configure) : launch_one<G, 1>(km, vm, a, grid, stream, configure);
 }
 cudaError_t launch_any(int group, int bundle, const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, unsigned grid,
                        cudaStream_t stream, bool configure) {
@@ -1054,8 +1050,8 @@ cudaError_t launch_any(int group, int bundle, const CUtensorMap& km, const CUten
 
 }  // namespace
 
-// KV heads to an item (and to a TMA box): the most of 4, 2, 1 that divide Hkv.
-int decode_q8_bundle(int Hkv) { return Hkv % 4 == 0 ? 4 : Hkv % 2 == 0 ? 2 : 1; }
+// KV heads to an item (and to a TMA box).
+int decode_q8_bundle(int Hkv) { return Hkv % 2 == 0 ? 2 : 1; }
 
 cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream) {
     int dev = 0, sms = 0;
@@ -1065,7 +1061,7 @@ cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(g_configured.load() & bit)) {
         for (int g = 1; g <= 8; g *= 2)
-            for (int h = 1; h <= 4; h *= 2)
+            for (int h = 1; h <= 2; ++h)
                 if ((e = launch_any(g, h, km, vm, a, 0, stream, true)) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if (bit) g_sms[dev].store(sms);

@@ -968,9 +968,11 @@ int make_q8_maps(CUtensorMap* km, CUtensorMap* vm, const rk_paged_plan_t* plan, 
     return rc ? rc : make_q8_map(vm, have ? v_cache : q, pages, plan->Hkv, heads, "v_cache");
 }
 
-// Split geometry of the 8-bit decode.  split_tokens = 0: short splits where a row starts
-// (a short row then has several CTAs at work), longer ones further on (fewer partial
-// results of a long row); which token is in which split never depends on the row's length.
+// Split geometry of the 8-bit decode.  split_tokens = 0: 512 tokens (two steps of a bundle of
+// heads), 1024 far into a row (fewer partial results); which token is in which split never
+// depends on the row's length.  In us, for 64 x 4096 / 20 ragged rows / 2 rows past 100000 / 1
+// row of 777: all 512 90 / 48 / 89 / 12.7, all 1024 87 / 50 / 88 / 15.6, 256 up to token
+// 1024 and 512 or 1024 behind 91 / 52 / 88 / 10.6.
 int q8_zones(const rk_paged_plan_t* plan, int32_t split_tokens, rk::AttnQ8Args* a) {
     if (split_tokens < 0 || split_tokens % rk::PAGE != 0)
         return fail(RK_E_ARG, "split_tokens must be 0 or a positive multiple of %d (got %d)", rk::PAGE, split_tokens);
@@ -979,9 +981,9 @@ int q8_zones(const rk_paged_plan_t* plan, int32_t split_tokens, rk::AttnQ8Args* 
         a->zone[0] = {0, 0, split_tokens, 0, 0};
         a->zone[1] = a->zone[2] = {far, far, split_tokens, far, 0};
     } else {
-        a->zone[0] = {0, 0, 256, 0, 0};
-        a->zone[1] = {4, 1024, 512, 0, 0};
-        a->zone[2] = {18, 8192, 2048, 0, 0};
+        a->zone[0] = {0, 0, 512, 0, 0};
+        a->zone[1] = {32, 16384, 1024, 0, 0};
+        a->zone[2] = {far, far, 1024, far, 0};
     }
     const int32_t step_tokens = 512 / rk::decode_q8_bundle(plan->Hkv);
     for (int z = 0; z < 3; ++z) {

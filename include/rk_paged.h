@@ -556,8 +556,7 @@ int rk_paged_kv_append_q8(const rk_paged_plan_t *plan, int32_t n, const void *k_
  * sets (the policy of rk_paged_attn_decode_split), so a row's result depends on where
  * it is cut and not on the batch, the table width or the grid.
  *   split_tokens  a positive multiple of 16: splits start at its multiples; 0: at
- *                multiples of 256 below token 1024, of 512 below 8192, of 2048
- *                from there on
+ *                multiples of 512 below token 16384, of 1024 from there on
  *   scratch       DEVICE, 16-byte aligned, at least
  *                rk_paged_decode_q8_scratch_bytes bytes; nothing in it needs
  *                initialising; may be NULL where that is 0 (the table holds no
