@@ -92,7 +92,7 @@ def test_attention_q8_refuses(rk):
         assert f(_plan(rk, B=0)) in ("RK_OK",)
     assert decode(_plan(rk, Sq=2)) != "RK_OK"
     n = rk.decode_q8_scratch_bytes(p)
-    assert n == 2 * 8 * 3 * 129 * 4 and rk.decode_q8_scratch_bytes(p, 640) == 0  # splits at 256, 512
+    assert n == 2 * 8 * 2 * 129 * 4 and rk.decode_q8_scratch_bytes(p, 640) == 0  # 640 tokens, a split at 512
     assert rk.decode_q8_scratch_bytes(_plan(rk, W=16)) == 0 and rk.decode_q8_scratch_bytes(_plan(rk, W=17)) == 2 * 8 * 2 * 129 * 4
     assert rk.decode_q8_scratch_bytes(_plan(rk, W=65)) == 2 * 8 * 5 * 129 * 4       # ..., 768, 1024
     assert rk.decode_q8_scratch_bytes(_plan(rk, W=513)) == 2 * 8 * 19 * 129 * 4     # 4 + 14 below 8192, one from there
