@@ -93,9 +93,10 @@ def test_attention_q8_refuses(rk):
     assert decode(_plan(rk, Sq=2)) != "RK_OK"
     n = rk.decode_q8_scratch_bytes(p)
     assert n == 2 * 8 * 2 * 129 * 4 and rk.decode_q8_scratch_bytes(p, 640) == 0  # 640 tokens, a split at 512
-    assert rk.decode_q8_scratch_bytes(_plan(rk, W=16)) == 0 and rk.decode_q8_scratch_bytes(_plan(rk, W=17)) == 2 * 8 * 2 * 129 * 4
-    assert rk.decode_q8_scratch_bytes(_plan(rk, W=65)) == 2 * 8 * 5 * 129 * 4       # ..., 768, 1024
-    assert rk.decode_q8_scratch_bytes(_plan(rk, W=513)) == 2 * 8 * 19 * 129 * 4     # 4 + 14 below 8192, one from there
+    assert rk.decode_q8_scratch_bytes(_plan(rk, W=32)) == 0 and rk.decode_q8_scratch_bytes(_plan(rk, W=33)) == 2 * 8 * 2 * 129 * 4
+    assert rk.decode_q8_scratch_bytes(_plan(rk, W=65)) == 2 * 8 * 3 * 129 * 4       # 512, 1024
+    assert rk.decode_q8_scratch_bytes(_plan(rk, W=1025)) == 2 * 8 * 33 * 129 * 4    # 32 below 16384, one from there
+    assert rk.decode_q8_scratch_bytes(_plan(rk, W=1089)) == 2 * 8 * 34 * 129 * 4
     assert rk.decode_q8_scratch_bytes(p, 16) == 2 * 8 * 40 * 129 * 4
     for split in (-16, 8, 17):
         assert decode(p, split=split) == "RK_E_ARG"
