@@ -80,7 +80,7 @@ struct DqShape {
     // shared memory: the ring (a step's K or V to a stage), two buffers of q operands (one per
     // head of the bundle), weights (one per tile: 16 columns of O to a 16-byte row per token,
     // MN-major without swizzle)
-    static constexpr int STAGES = G == 8 && H == 2 ? 2 : 3;  // as room allows (three, and one buffer of q: 54 us of the ragged rows, not 51)
+    static constexpr int STAGES = G == 8 && H == 2 ? 2 : 3;  // as room allows (three, and one buffer of q: 52 us of the ragged rows, not 47)
     static constexpr int Q_BYTES = NS * 128, P_BYTES = NP * DQ_TILE;
     static constexpr int OFF_Q = STAGES * DQ_STEP_BYTES;
     static constexpr int OFF_P = OFF_Q + 2 * H * Q_BYTES;
@@ -833,14 +833,27 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             const int ipar = (ni + 1) & 1;
             bad |= st.bad;
             if (st.flags & DQ_LAST) {
+                if (blk == 0 && t == 0) {
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    if (blk == 0 && t == 0) c->top[ipar][hj][g] = M[g];
-                    float x = l[g];
-#pragma unroll
-                    for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(0xffffffffu, x, k);
-                    if (lane == 0) c->lred[ipar][sw][g] = x;
+                    for (int g = 0; g < G; ++g) c->top[ipar][hj][g] = M[g];
                 }
+                // the lanes' sums: half of the queries to each half of the lanes, until a lane has one
+                float x[G];
+#pragma unroll
+                for (int g = 0; g < G; ++g) x[g] = l[g];
+                int mine = 0;
+#pragma unroll
+                for (int k = 1, m = G / 2; k < 32; k <<= 1, m >>= 1) {
+                    const bool up = lane & k;
+#pragma unroll
+                    for (int g = 0; g < m; ++g) {
+                        const float give = up ? x[g] : x[g + m];
+                        x[g] = (up ? x[g + m] : x[g]) + __shfl_xor_sync(0xffffffffu, give, k);
+                    }
+                    if (m == 0) x[0] += __shfl_xor_sync(0xffffffffu, x[0], k);
+                    else if (up) mine += m;
+                }
+                if (lane < G) c->lred[ipar][sw][mine] = x[0];
                 range = __reduce_or_sync(0xffffffffu, range);
                 if (lane == 0) c->fred[ipar][sw] = range;
             }
