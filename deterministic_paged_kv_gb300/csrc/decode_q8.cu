@@ -620,7 +620,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
         constexpr int OWN = Sh::OWN, SHARE = Sh::SHARE;  // queries blk, blk + SHARE, ... are this warpgroup's
         int slot = 0, use = 0, ni = 0, nq = 0, ks = 0;  // items, queries, steps so far
-        float M[G], l[G];
+        // the running maximum of each query; from four on a query's in the lanes lane % G
+        constexpr bool SPREAD = G >= 4;
+        float M[SPREAD ? 1 : G], l[G];
         int bad = 0;         // the item's status bits
         uint32_t range = 0;  // queries that met a value FP32 cannot hold; bit 31: a scale that is none
         float o[OWN];
@@ -723,7 +725,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 if (st.flags & DQ_FIRST) {
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
-                        M[g] = -INFINITY;
+                        M[SPREAD ? 0 : g] = -INFINITY;
                         l[g] = 0.0f;
                     }
                     bad = 0;
@@ -778,17 +780,38 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             }
             if (st.cnt > 0) {
                 float p[G];
-                const int rw = ((lane & 15) >> 2) % H == hj ? lane & 15 : 4 * hj;  // a warp of this head
+                if constexpr (SPREAD) {  // a query to a lane, then to all lanes
+                    float m = -INFINITY;
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    float m = warp_max(c->red[par][rw][g]);
+                    for (int i = 0; i < 16 / H; i += 32 / G) {  // softmax warp i of this head
+                        const int sw_i = i + lane / G;
+                        m = fmaxf(m, c->red[par][((sw_i >> 2) * H + hj) * 4 + (sw_i & 3)][lane % G]);
+                    }
+#pragma unroll
+                    for (int k = G; k < 32; k <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
                     m = fabsf(m) < INFINITY ? m : 0.0f;  // otherwise the query fails (range)
-                    const float top = fmaxf(M[g], m);
-                    const float alpha = ex2(M[g] - top), beta = ex2(m - top);
-                    M[g] = top;
-                    p[g] = ex2(w[g] - m + 8.0f);
-                    l[g] = fmaf(l[g], alpha, p[g] * ps.z * beta);
-                    if (blk == 0 && t == 0) c->ab[par][hj][g] = make_float2(alpha, beta);
+                    const float top = fmaxf(M[0], m);
+                    const float alpha = ex2(M[0] - top), beta = ex2(m - top);
+                    M[0] = top;
+                    if (blk == 0 && t < G) c->ab[par][hj][t] = make_float2(alpha, beta);
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        p[g] = ex2(w[g] - __shfl_sync(0xffffffffu, m, g) + 8.0f);
+                        l[g] = fmaf(l[g], __shfl_sync(0xffffffffu, alpha, g), p[g] * ps.z * __shfl_sync(0xffffffffu, beta, g));
+                    }
+                } else {
+                    const int rw = ((lane & 15) >> 2) % H == hj ? lane & 15 : 4 * hj;  // a warp of this head
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        float m = warp_max(c->red[par][rw][g]);
+                        m = fabsf(m) < INFINITY ? m : 0.0f;
+                        const float top = fmaxf(M[g], m);
+                        const float alpha = ex2(M[g] - top), beta = ex2(m - top);
+                        M[g] = top;
+                        p[g] = ex2(w[g] - m + 8.0f);
+                        l[g] = fmaf(l[g], alpha, p[g] * ps.z * beta);
+                        if (blk == 0 && t == 0) c->ab[par][hj][g] = make_float2(alpha, beta);
+                    }
                 }
                 // the weights' buffer is free once the PV of the step before is done
                 if (ks > 0) wait(c->o_full[par ^ 1], (ks - 1) >> 1);
@@ -833,7 +856,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             const int ipar = (ni + 1) & 1;
             bad |= st.bad;
             if (st.flags & DQ_LAST) {
-                if (blk == 0 && t == 0) {
+                if constexpr (SPREAD) {
+                    if (blk == 0 && t < G) c->top[ipar][hj][t] = M[0];
+                } else if (blk == 0 && t == 0) {
 #pragma unroll
                     for (int g = 0; g < G; ++g) c->top[ipar][hj][g] = M[g];
                 }
