@@ -26,7 +26,7 @@
 // Work: an item is a split of a row for a bundle of H neighbouring KV heads (2, or 1 where
 // Hkv is odd).  A TMA copy takes a page's blocks of the whole bundle: 64 x 4096 takes 125 us head
 // by head (copies of 2 KiB), 91 in bundles of two, 93 in bundles of four, whose items are
-// coarser (20 ragged rows of 8 heads a KV head: 54 us, 48 in twos).  A step is 512 / H tokens
+// coarser (20 ragged rows of 8 heads a KV head: 54 us, 48 in twos then, 44 now).  A step is 512 / H tokens
 // of the bundle, four tiles of 128 tokens and one head; in it the softmax is plain (one
 // maximum over its tokens), steps and splits are joined with the running maximum in FP32.  The
 // copies leave the bundle as [page][half][head][8 tokens][128 B] in shared memory, so that
@@ -80,7 +80,7 @@ struct DqShape {
     // shared memory: the ring (a step's K or V to a stage), two buffers of q operands (one per
     // head of the bundle), weights (one per tile: 16 columns of O to a 16-byte row per token,
     // MN-major without swizzle)
-    static constexpr int STAGES = G == 8 && H == 2 ? 2 : 3;  // as room allows (three, and one buffer of q: 52 us of the ragged rows, not 47)
+    static constexpr int STAGES = G == 8 && H == 2 ? 2 : 3;  // as room allows (three, and one buffer of q: 48.5 us of the ragged rows, not 44)
     static constexpr int Q_BYTES = NS * 128, P_BYTES = NP * DQ_TILE;
     static constexpr int OFF_Q = STAGES * DQ_STEP_BYTES;
     static constexpr int OFF_P = OFF_Q + 2 * H * Q_BYTES;

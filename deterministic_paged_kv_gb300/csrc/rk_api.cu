@@ -971,8 +971,8 @@ int make_q8_maps(CUtensorMap* km, CUtensorMap* vm, const rk_paged_plan_t* plan, 
 // Split geometry of the 8-bit decode.  split_tokens = 0: 512 tokens (two steps of a bundle of
 // heads), 1024 far into a row (fewer partial results); which token is in which split never
 // depends on the row's length.  In us, for 64 x 4096 / 20 ragged rows / 2 rows past 100000 / 1
-// row of 777: all 512 90 / 48 / 89 / 12.7, all 1024 87 / 50 / 88 / 15.6, 256 up to token
-// 1024 and 512 or 1024 behind 91 / 52 / 88 / 10.6.
+// row of 777: all 512 90 / 44 / 89 / 12.6, all 1024 87 / 48 / 88 / 15.4, all 256 91 / 46 / 96 /
+// 10.5 (and twice the scratch).
 int q8_zones(const rk_paged_plan_t* plan, int32_t split_tokens, rk::AttnQ8Args* a) {
     if (split_tokens < 0 || split_tokens % rk::PAGE != 0)
         return fail(RK_E_ARG, "split_tokens must be 0 or a positive multiple of %d (got %d)", rk::PAGE, split_tokens);
