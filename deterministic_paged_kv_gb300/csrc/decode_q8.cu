@@ -133,17 +133,17 @@ __device__ __forceinline__ int row_keys(const AttnQ8Args& a, int b, int& bad) {
     if (pos < 0) bad |= RK_STATUS_POSITION;
     return bad ? 0 : (pos < kv ? pos + 1 : kv);
 }
-// ---- split geometry: up to three zones of equal splits (AttnQ8Args::zone) ----
+// ---- split geometry: one or two zones of equal splits (AttnQ8Args::zone) ----
 
 // Splits of a row of n keys (one for an empty row).
 __device__ __forceinline__ int splits_of(const AttnQ8Args& a, int n) {
     if (n <= 0) return 1;
-    const int z = n > a.zone[2].token ? 2 : n > a.zone[1].token ? 1 : 0;
+    const int z = n > a.zone[1].token;
     return a.zone[z].split + (n - a.zone[z].token + a.zone[z].size - 1) / a.zone[z].size;
 }
 // Tokens [first, end) of split s.
 __device__ __forceinline__ void split_range(const AttnQ8Args& a, int s, int n, int& first, int& end) {
-    const int z = s >= a.zone[2].split ? 2 : s >= a.zone[1].split ? 1 : 0;
+    const int z = s >= a.zone[1].split;
     first = a.zone[z].token + (s - a.zone[z].split) * a.zone[z].size;
     end = min(n, first + a.zone[z].size);
 }
@@ -151,13 +151,13 @@ __device__ __forceinline__ void split_range(const AttnQ8Args& a, int s, int n, i
 template <int T>
 __device__ __forceinline__ int row_steps(const AttnQ8Args& a, int n) {
     if (n <= 0) return 1;
-    const int z = n > a.zone[2].token ? 2 : n > a.zone[1].token ? 1 : 0;
+    const int z = n > a.zone[1].token;
     const int len = n - a.zone[z].token, full = len / a.zone[z].size;
     return a.zone[z].step + full * a.zone[z].steps + (len - full * a.zone[z].size + T - 1) / T;
 }
 // First split of a row that starts at its step r or later; r becomes that split's first step.
 __device__ __forceinline__ int split_at(const AttnQ8Args& a, int& r) {
-    const int z = r >= a.zone[2].step ? 2 : r >= a.zone[1].step ? 1 : 0;
+    const int z = r >= a.zone[1].step;
     const int k = (r - a.zone[z].step + a.zone[z].steps - 1) / a.zone[z].steps;
     r = a.zone[z].step + k * a.zone[z].steps;
     return a.zone[z].split + k;

@@ -65,12 +65,12 @@ struct AttnQ8Args {
     uint32_t wait_limit_ns;
     int32_t timeout_drill;
     // decode: where a row's keys are split, zones of equal splits from a token (and split) on
-    // (a zone that is not used starts at INT32_MAX); n_splits to a row of the scratch: with
+    // (a second zone that is not used starts at INT32_MAX); n_splits to a row of the scratch: with
     // more than one, partial o / l [B, Hq, n_splits, D] and log2-domain LSE [B, Hq, n_splits]
     // (`step`, `steps`: where a zone starts and what a split of it takes, in steps of the kernel)
     struct {
         int32_t split, token, size, step, steps;
-    } zone[3];
+    } zone[2];
     int32_t n_splits;
     float* o_part;
     float* lse_part;

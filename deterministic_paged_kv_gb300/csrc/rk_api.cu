@@ -979,18 +979,14 @@ int q8_zones(const rk_paged_plan_t* plan, int32_t split_tokens, rk::AttnQ8Args* 
     const int32_t far = INT32_MAX;
     if (split_tokens > 0) {
         a->zone[0] = {0, 0, split_tokens, 0, 0};
-        a->zone[1] = a->zone[2] = {far, far, split_tokens, far, 0};
+        a->zone[1] = {far, far, split_tokens, far, 0};
     } else {
         a->zone[0] = {0, 0, 512, 0, 0};
         a->zone[1] = {32, 16384, 1024, 0, 0};
-        a->zone[2] = {far, far, 1024, far, 0};
     }
     const int32_t step_tokens = 512 / rk::decode_q8_bundle(plan->Hkv);
-    for (int z = 0; z < 3; ++z) {
-        a->zone[z].steps = (a->zone[z].size + step_tokens - 1) / step_tokens;
-        if (z > 0 && a->zone[z].split != far)
-            a->zone[z].step = a->zone[z - 1].step + (a->zone[z].split - a->zone[z - 1].split) * a->zone[z - 1].steps;
-    }
+    for (auto& z : a->zone) z.steps = (z.size + step_tokens - 1) / step_tokens;
+    if (a->zone[1].split != far) a->zone[1].step = a->zone[1].split * a->zone[0].steps;
     return RK_OK;
 }
 
@@ -998,7 +994,7 @@ int q8_zones(const rk_paged_plan_t* plan, int32_t split_tokens, rk::AttnQ8Args* 
 int64_t q8_split_count(const rk_paged_plan_t* plan, const rk::AttnQ8Args& a) {
     const int64_t cap = (int64_t)plan->W * rk::PAGE;
     if (cap <= 0) return 1;
-    const int z = cap > a.zone[2].token ? 2 : cap > a.zone[1].token ? 1 : 0;
+    const int z = cap > a.zone[1].token;
     return a.zone[z].split + (cap - a.zone[z].token + a.zone[z].size - 1) / a.zone[z].size;
 }
 
