@@ -978,8 +978,10 @@ int q8_zones(const rk_paged_plan_t* plan, int32_t split_tokens, rk::AttnQ8Args* 
         return fail(RK_E_ARG, "split_tokens must be 0 or a positive multiple of %d (got %d)", rk::PAGE, split_tokens);
     const int32_t far = INT32_MAX;
     if (split_tokens > 0) {
-        a->zone[0] = {0, 0, split_tokens, 0, 0};
-        a->zone[1] = {far, far, split_tokens, far, 0};
+        // (a split is at most what the table holds, so that sums with its size stay in 32 bits)
+        const int32_t size = std::min(split_tokens, std::max(plan->W, 1) * rk::PAGE);
+        a->zone[0] = {0, 0, size, 0, 0};
+        a->zone[1] = {far, far, size, far, 0};
     } else {
         a->zone[0] = {0, 0, 512, 0, 0};
         a->zone[1] = {32, 16384, 1024, 0, 0};

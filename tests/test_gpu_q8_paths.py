@@ -127,6 +127,13 @@ def test_decode_q8_does_not_depend_on_the_merge():
         assert att._equal(att._run(c, split), att._run(att._rows(c, rows, 700), split))
 
 
+def test_decode_q8_largest_split():
+    c = ref.case(67, [700, 0, 33, 1], 8, 2)
+    want = att._run(c, 1 << 20)
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    assert att._equal(want, att._run(c, 2 ** 31 - 16, status=st)) and int(st.item()) == 0
+
+
 @pytest.mark.parametrize("mode", ["decode", "prefill"])
 def test_q8_rows_share_pages(mode):
     c = ref.case(63, [600, 64, 350], 8, 2, Sq=1 if mode == "decode" else 40)
