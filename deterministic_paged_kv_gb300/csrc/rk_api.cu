@@ -1089,11 +1089,11 @@ int rk_paged_kv_append_q8(const rk_paged_plan_t* plan, int32_t n, const void* k_
 
 int rk_paged_decode_q8_scratch_bytes(const rk_paged_plan_t* plan, int32_t split_tokens, uint64_t* bytes) {
     g_err.clear();
-    if (!plan || !bytes) return fail(RK_E_ARG, "plan and bytes must be non-null");
-    if (plan->abi != RK_PAGED_ABI_VERSION) return fail(RK_E_ARG, "plan ABI %u != %u", plan->abi, RK_PAGED_ABI_VERSION);
-    rk::AttnQ8Args a;
-    int rc = q8_zones(plan, split_tokens, &a);
+    if (!bytes) return fail(RK_E_ARG, "bytes is NULL");
+    int rc = check_plan(plan);
     if (rc) return rc;
+    rk::AttnQ8Args a;
+    if ((rc = q8_zones(plan, split_tokens, &a))) return rc;
     *bytes = (uint64_t)q8_scratch_need(plan, q8_split_count(plan, a));
     return RK_OK;
 }
