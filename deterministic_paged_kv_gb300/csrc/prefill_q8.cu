@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
         bars->pipe.abort = 0;
         bars->pipe.limit_ns = wait_limit(a.wait_limit_ns);
         mbar_init(smem_u32(&bars->never), 1);
-        mbar_init(smem_u32(&bars->q_empty), 1);
+        mbar_init(smem_u32(&bars->q_empty), 1 + 8);  // issuer's commit, softmax warps
         for (int k = 0; k < KST; ++k) {
             mbar_init(smem_u32(&bars->k_full[k]), 128);
             mbar_init(smem_u32(&bars->k_empty[k]), 1);
@@ -630,6 +630,12 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
             }
             ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->q_ready[j]), (ph >> 2) & 1u, pc));
             const float scr = bars->qscale[j][r];
+            // The next unit's q may take the operand and the factors once every softmax warp has passed this
+            // point, those of a q-tile without keys too: no S waits for those, so nothing else would
+            // keep q_ready from completing twice before they look (a wait by parity then misses it), or q
+            // from being made where they still make the CTA's first.
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(smem_u32(&bars->q_empty));
             float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
             for (int i = 0; i < nt && ok; ++i) {
