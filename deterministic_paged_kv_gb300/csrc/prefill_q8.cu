@@ -50,6 +50,10 @@ constexpr int KST = 2, VST = 2;                 // K stages, V stages
 constexpr int SCST = 4;                         // scale slots: one more than K stages at least
 constexpr uint32_t TMEM_COLS = 512;             // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512)
 constexpr float RESCALE_SLACK = 8.0f, P_BIAS = 7.0f;
+// A running maximum from here on (log2 domain; one FP32 step is 1/8) is subtracted before the bias is
+// added: in one sum with it the bias and log2(vs) drown, and a weight may pass FP16's 2^16.  Below, the
+// sum's roundings are under 1/4 and a weight stays under 2^15.25.
+constexpr float FAR_MAX = 1048576.0f;
 constexpr uint32_t UNIT_READERS = 32 + 128 + 256;
 
 // setmaxnreg split (sum 4 x 128 = the 512 x 128 registers the CTA launches with)
@@ -670,18 +674,29 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 }
                 float alpha = 1.0f;
                 bool resc = false;
-                if (mt > m + RESCALE_SLACK) {
+                if (mt - m > RESCALE_SLACK) {  // (m + 8 may round up to mt)
                     alpha = ex2(m - mt);  // 0 when m = -inf
                     m = mt;
                     resc = true;
                 }
                 // p' = 2^(w - m + 7), packed as FP16 pairs into xr[0..63]; the sum divides vs out
-                const float nm = (m == -INFINITY) ? 0.0f : P_BIAS - m;
+                const float base = (m == -INFINITY) ? 0.0f : m;
+                const bool far = __any_sync(0xffffffffu, fabsf(base) >= FAR_MAX);
+                if (far) {  // w - m into xr; what follows adds the bias
+#pragma unroll
+                    for (int p = 0; p < PF_PAGES_PER_TILE; ++p) {
+                        const float4 f = sc[p];
+                        const float mul = f.x * scr;
+#pragma unroll
+                        for (int c = 16 * p; c < 16 * p + 16; ++c)
+                            xr[c] = __float_as_uint(fmaf(__uint_as_float(xr[c]), mul, f.y) - base);
+                    }
+                }
                 float rs = 0.0f;
 #pragma unroll
                 for (int p = 0; p < PF_PAGES_PER_TILE; ++p) {
                     const float4 f = sc[p];
-                    const float mul = f.x * scr, add = f.y + nm;
+                    const float mul = far ? 1.0f : f.x * scr, add = far ? P_BIAS : f.y + (P_BIAS - base);
                     const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
                     float2 acc2 = make_float2(0.0f, 0.0f);
 #pragma unroll
