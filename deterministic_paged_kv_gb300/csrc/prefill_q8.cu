@@ -54,6 +54,15 @@ constexpr float RESCALE_SLACK = 8.0f, P_BIAS = 7.0f;
 // added: in one sum with it the bias and log2(vs) drown, and a weight may pass FP16's 2^16.  Below, the
 // sum's roundings are under 1/4 and a weight stays under 2^15.25.
 constexpr float FAR_MAX = 1048576.0f;
+
+// A page's factor of raw scores (log2 domain) for one query.  Not 0 where the product underflows, as
+// masked scores are -inf: a raw score is below 2^25, so 2^-126 of it is as good as nothing.  NaN (a
+// query out of range) stays.
+__device__ __forceinline__ float score_factor(float k_scale, float q_scale) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(k_scale * q_scale), "f"(1.17549435e-38f));
+    return r;
+}
 constexpr uint32_t UNIT_READERS = 32 + 128 + 256;
 
 // setmaxnreg split (sum 4 x 128 = the 512 x 128 registers the CTA launches with)
@@ -670,7 +679,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                         x1 = fmaxf(x1, __uint_as_float(xr[16 * p + c + 1]));
                     }
                     const float4 f = sc[p];
-                    mt = fmaxf(mt, fmaf(fmaxf(x0, x1), f.x * scr, f.y));
+                    mt = fmaxf(mt, fmaf(fmaxf(x0, x1), score_factor(f.x, scr), f.y));
                 }
                 float alpha = 1.0f;
                 bool resc = false;
@@ -686,7 +695,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
 #pragma unroll
                     for (int p = 0; p < PF_PAGES_PER_TILE; ++p) {
                         const float4 f = sc[p];
-                        const float mul = f.x * scr;
+                        const float mul = score_factor(f.x, scr);
 #pragma unroll
                         for (int c = 16 * p; c < 16 * p + 16; ++c)
                             xr[c] = __float_as_uint(fmaf(__uint_as_float(xr[c]), mul, f.y) - base);
@@ -696,7 +705,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
 #pragma unroll
                 for (int p = 0; p < PF_PAGES_PER_TILE; ++p) {
                     const float4 f = sc[p];
-                    const float mul = far ? 1.0f : f.x * scr, add = far ? P_BIAS : f.y + (P_BIAS - base);
+                    const float mul = far ? 1.0f : score_factor(f.x, scr), add = far ? P_BIAS : f.y + (P_BIAS - base);
                     const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
                     float2 acc2 = make_float2(0.0f, 0.0f);
 #pragma unroll

@@ -79,3 +79,19 @@ def test_q8_large_scores_choose_one_key(mode, q_size, k_size):
     assert int(st.item()) == 0 and torch.isfinite(lse).all()
     want = torch.stack([(v[t[i], h] * vs) for h in range(Hkv) for i in range(G)])[None].to(torch.bfloat16)
     assert torch.equal(out.cpu(), want)
+
+
+# ------------------------------------------- products that vanish in 32 bits ----
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("k_exp", [-60, -83, -100, -126])
+@pytest.mark.parametrize("q_size", [0.0, 2.0 ** -70, 2.0 ** -57])
+def test_q8_scores_that_vanish(mode, k_exp, q_size):
+    """A query of (next to) nothing against small scales of K: equal scores, so the values' mean."""
+    c = ref.case(105, [300, 70, 16], 4, 2, Sq=1 if mode == "decode" else 30)
+    c["q"] = (c["q"].double() * q_size).to(torch.bfloat16)
+    c["k_scale"].fill_(2.0 ** k_exp)
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    got = att._run(c, status=st, mode=mode)
+    assert int(st.item()) == 0
+    att._check(c, got, TOL[mode])
