@@ -12,9 +12,12 @@
 // parts instead, which is cheap because it is small:
 //   q, rotated and scaled to below 362 by a power of two per head, is four parts
 //   (two at 1, two at 2^-8), the G heads' parts being columns of one operand;
-//   the softmax weights, scaled to at most 256, are three parts.
+//   the softmax weights, scaled to at most 256, are three parts at 1, 2^-5 and 2^-10.
 // Products of e4m3 values are exact and the sums are FP32, so a score has the
-// precision of q in about 16 bits and a weight in 12.
+// precision of q in about 16 bits.  A weight (with V's page scale in it) is good to 2^-14 of itself
+// or 2^-28 of its step's largest, whichever is more: a key that takes nearly all of a row's weight
+// for a value of nothing, or a page with an outlier in V, leave the other keys their bits.  (Three
+// parts at 1 are good to 2^-12 or 2^-18: a weight 2^-10 of the largest to 2^-8 only.)
 //
 // With S^T = K q^T [128 tokens x 4 G] and O^T = V^T p^T [128 dims x 3 G] both
 // operands that come from the cache are A operands in the layout they land in:
@@ -816,7 +819,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 // the weights' buffer is free once the PV of the step before is done
                 if (ks > 0) wait(c->o_full[par ^ 1], (ks - 1) >> 1);
                 if (have) {
-                    // p' = 2^(w - m + 8) as three e4m3 parts, part * G + query of the token's row
+                    // p' = 2^(w - m + 8) as three e4m3 parts at 1, 2^-5, 2^-10: part * G + query of the token's row
                     uint32_t wd[NP / 4];
 #pragma unroll
                     for (int i = 0; i < NP / 4; ++i) wd[i] = 0;
@@ -827,6 +830,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                         for (int e = 0; e < 3; ++e) {
                             const int col = e * G + g;
                             wd[col >> 2] |= take_part(x) << (8 * (col & 3));
+                            x = fmul2(x, make_float2(32.0f, 32.0f));  // at most 2^8 again: a part leaves 8 of 2^8
                         }
                     }
                     uint8_t* pt = sm + Sh::OFF_P + wg * Sh::P_BYTES + t * 16;
@@ -900,7 +904,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 uint32_t over = 0;
 #pragma unroll
                 for (int i = 0; i < OWN; ++i) {
-                    const float x = (__uint_as_float(r[i][2]) + __uint_as_float(r[i][1])) + __uint_as_float(r[i][0]);
+                    const float x = fmaf(fmaf(__uint_as_float(r[i][2]), 1.0f / 32.0f, __uint_as_float(r[i][1])), 1.0f / 32.0f, __uint_as_float(r[i][0]));
                     const float2 ab = c->ab[db][hj][min(blk + SHARE * i, G - 1)];
                     o[i] = fmaf(x, ab.y, o[i] * ab.x);
                     if (!(fabsf(o[i]) < INFINITY) && blk + SHARE * i < G) over |= 1u << (blk + SHARE * i);

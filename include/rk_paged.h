@@ -568,6 +568,9 @@ int rk_paged_kv_append_q8(const rk_paged_plan_t *plan, int32_t n, const void *k_
  * finite, a NaN code among the visible tokens, scores or sums beyond FP32) fail the
  * query heads that meet them, and may fail the other query heads of that KV head.
  * What lies past kv_len or the position is not read as a value (it may be anything).
+ * Precision: q is rounded to 2^-16 of each element; a softmax weight times its page's
+ * v_scale to 2^-14 of itself or 2^-28 of the largest such product among 512 neighbouring
+ * keys, whichever is more; sums are FP32.
  * Errors: as rk_paged_attn_decode_split.
  */
 int rk_paged_decode_q8_scratch_bytes(const rk_paged_plan_t *plan, int32_t split_tokens, uint64_t *bytes);
@@ -586,7 +589,8 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t *plan, int32_t split_tokens, c
  * see a key fail together for metadata, a scale, or a NaN code of V among the keys
  * that any of them reads (a NaN code of K fails those that see it).
  * Precision: q is rounded to FP16 after its rotation (2^-11 of each element, as
- * in the BF16 call), which moves lse by some 1e-5 (the decode call keeps 2^-16).
+ * in the BF16 call), which moves lse by some 1e-5 (the decode call keeps 2^-16); a softmax
+ * weight times its page's v_scale to FP16, 2^-11 of itself or 2^-32 of the largest such product.
  * Errors: as rk_paged_attn_prefill.
  */
 int rk_paged_attn_prefill_q8(const rk_paged_plan_t *plan, const void *q, const void *k_cache,

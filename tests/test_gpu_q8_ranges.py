@@ -95,3 +95,91 @@ def test_q8_scores_that_vanish(mode, k_exp, q_size):
     got = att._run(c, status=st, mode=mode)
     assert int(st.item()) == 0
     att._check(c, got, TOL[mode])
+
+
+# ------------------------------------------------- weights far below the largest ----
+
+# What a weight is off by: of itself, and of the largest product of a weight and its page's scale of V.
+# Decode: three e4m3 parts of 4 bits, each 32 times finer than the one before: 2^-12, and where a
+# part is below e4m3's normal numbers 2^-8 of its 2^-10 steps, on weights scaled to 2^8: 2^-26.
+# (An exponential and the FP32 sums: 2^-16 of it.)  Prefill: FP16, 2^-11 and steps of 2^-24 on
+# weights of which the largest is at least 2^7: 2^-32.
+SMALL = {"decode": (2.0 ** -12 + 2.0 ** -16, 2.0 ** -26), "prefill": (2.0 ** -11 + 2.0 ** -16, 2.0 ** -32)}
+
+
+def _small_weights_bound(c, b, h, g, s, mode):
+    """Answer and bound of one query in 64 bits, from each weight's error and each token's code."""
+    rel, part = SMALL[mode]
+    G = c["q"].shape[1] // c["k_cache"].shape[1]
+    n = min(int(c["kv_lens"][b]), int(c["position_ids"][b, s]) + 1)
+    pg = c["block_table"][b, :-(-n // 16)].long()
+    kc, vc = (c[i].to(torch.float32).double()[pg, h].reshape(-1, 128)[:n] for i in ("k_cache", "v_cache"))
+    ks, vs = (c[i].double()[pg, h].repeat_interleave(16)[:n] for i in ("k_scale", "v_scale"))
+    q = c["q"][b, h * G + g, s].double().numpy()
+    r = torch.from_numpy(ref.rotate(q, int(c["position_ids"][b, s])))
+    k = kc * ks[:, None]
+    x = k @ r / math.sqrt(128)
+    p = torch.exp(x - x.max())
+    p = p / p.sum()
+    pair = torch.from_numpy(np.tile(np.hypot(q[:64], q[64:]), 2))
+    t = TOL[mode]
+    d = (t["q_rel"] * (k.abs() @ pair).max() + t["q_abs"] * np.abs(q).max() * k.abs().sum(1).max()) / math.sqrt(128)
+    w = p * vs
+    out = w @ vc
+    off = (2 * d + rel) * (w @ vc.abs()) + part * w.max() * vc.abs().sum(0)
+    return out, 2.0 ** -8 * out.abs() + off + 1e-30
+
+
+def _small_weights_check(c, mode):
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    out = att._run(c, status=st, mode=mode)[0].double().cpu()
+    assert int(st.item()) == 0
+    B, Hq, Sq, _ = c["q"].shape
+    Hkv = c["k_cache"].shape[1]
+    worst = 0.0
+    for b in range(B):
+        for hq in range(Hq):
+            for s in {0, Sq // 2, Sq - 1}:
+                want, off = _small_weights_bound(c, b, hq // (Hq // Hkv), hq % (Hq // Hkv), s, mode)
+                worst = max(worst, float(((out[b, hq, s] - want).abs() / off).max()))
+    assert worst <= 1, "off by %.2f of what may be" % worst
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (8, 4), (8, 2), (8, 1)])
+@pytest.mark.parametrize("ratio", [8, 11, 15])
+def test_q8_a_page_of_large_values(mode, Hq, Hkv, ratio):
+    """One page of V has an outlier in one dim, and with it a scale 2^ratio of the others': what the
+    other pages give in the other dims keeps its bits."""
+    c = ref.case(111, [200, 47, 600], Hq, Hkv, Sq=1 if mode == "decode" else 20)
+    c["v_scale"] = torch.full_like(c["v_scale"], 2.0 ** -7)
+    for b in range(3):
+        pg = c["block_table"][b, 1].long()
+        c["v_scale"][pg] = 2.0 ** (ratio - 7)
+        codes = torch.zeros((Hkv, 16, 128))
+        codes[:, :, 5] = 240.0
+        c["v_cache"].view(torch.uint8)[pg] = codes.to(ref.F8).view(torch.uint8)
+    _small_weights_check(c, mode)
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (8, 4), (8, 2), (8, 1)])
+@pytest.mark.parametrize("lead", [4.0, 7.0, 10.0])
+def test_q8_a_key_that_takes_nearly_all(mode, Hq, Hkv, lead):
+    """A row's first key, whose value is zero, scores `lead` above the rest for every query: the
+    others' weights, down to e^-lead of it, are all of the result."""
+    Sq = 1 if mode == "decode" else 20
+    c = ref.case(113, [200, 47, 600], Hq, Hkv, Sq=Sq)
+    # (one query for all heads, and small keys, so that one key leads all of a head's queries)
+    c["q"] = c["q"][:, :1, :1].expand(-1, Hq, Sq, -1).contiguous()
+    c["k_scale"] = torch.full_like(c["k_scale"], 2.0 ** -9)
+    for b in range(3):
+        pg = c["block_table"][b, 0].long()
+        # at the middle query's position; its neighbours' rotations differ by a few steps
+        r = ref.rotate(c["q"][b, 0, 0].double().numpy(), int(c["position_ids"][b, Sq // 2]))
+        key = torch.from_numpy(r * (lead * math.sqrt(128) / (r @ r))).float() * 2.0 ** 9
+        c["k_scale"][pg] = 2.0 ** -7
+        codes = c["k_cache"].view(torch.uint8)
+        codes[pg, :, 0] = (key / 4).clamp(-448, 448).to(ref.F8).view(torch.uint8)
+        c["v_cache"].view(torch.uint8)[pg, :, 0] = 0
+    _small_weights_check(c, mode)
