@@ -992,12 +992,19 @@ int q8_zones(const rk_paged_plan_t* plan, int32_t split_tokens, rk::AttnQ8Args* 
     return RK_OK;
 }
 
-// Splits of the longest row that the table can hold, at least one.
-int64_t q8_split_count(const rk_paged_plan_t* plan, const rk::AttnQ8Args& a) {
+// Splits of the longest row that the table can hold, at least one.  Steps and items of a call are
+// counted in 32 bits (its scratch, 516 bytes to a split of a query head, then stays far below 2^63).
+int q8_split_count(const rk_paged_plan_t* plan, const rk::AttnQ8Args& a, int64_t* splits) {
     const int64_t cap = (int64_t)plan->W * rk::PAGE;
-    if (cap <= 0) return 1;
-    const int z = cap > a.zone[1].token;
-    return a.zone[z].split + (cap - a.zone[z].token + a.zone[z].size - 1) / a.zone[z].size;
+    *splits = 1;
+    if (cap > 0) {
+        const int z = cap > a.zone[1].token;
+        *splits = a.zone[z].split + (cap - a.zone[z].token + a.zone[z].size - 1) / a.zone[z].size;
+    }
+    if ((double)plan->B * plan->Hkv * ((double)plan->W + (double)*splits) > 2147483647.0)
+        return fail(RK_E_UNSUPPORTED, "B %d x Hkv %d x (W %d + %lld splits): too many", plan->B, plan->Hkv, plan->W,
+                    (long long)*splits);
+    return RK_OK;
 }
 
 // Scratch of the 8-bit decode: none where the table holds one split at most.
@@ -1094,7 +1101,9 @@ int rk_paged_decode_q8_scratch_bytes(const rk_paged_plan_t* plan, int32_t split_
     if (rc) return rc;
     rk::AttnQ8Args a;
     if ((rc = q8_zones(plan, split_tokens, &a))) return rc;
-    *bytes = (uint64_t)q8_scratch_need(plan, q8_split_count(plan, a));
+    int64_t splits;
+    if ((rc = q8_split_count(plan, a, &splits))) return rc;
+    *bytes = (uint64_t)q8_scratch_need(plan, splits);
     return RK_OK;
 }
 
@@ -1108,11 +1117,8 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t* plan, int32_t split_tokens, c
     if (plan->Sq != 1) return fail(RK_E_ARG, "decode needs a plan with Sq == 1 (got %d)", plan->Sq);
     rk::AttnQ8Args a;
     if ((rc = q8_zones(plan, split_tokens, &a))) return rc;
-    const int64_t splits = q8_split_count(plan, a);
-    // steps and items are counted in 32 bits
-    if ((double)plan->B * plan->Hkv * ((double)plan->W + (double)splits) > 2147483647.0)
-        return fail(RK_E_UNSUPPORTED, "B %d x Hkv %d x (W %d + %lld splits): too many", plan->B, plan->Hkv, plan->W,
-                    (long long)splits);
+    int64_t splits;
+    if ((rc = q8_split_count(plan, a, &splits))) return rc;
     const int64_t need = q8_scratch_need(plan, splits);
     if (need > 0) {
         if (!scratch || !aligned(scratch, 16))

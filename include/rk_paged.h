@@ -571,7 +571,8 @@ int rk_paged_kv_append_q8(const rk_paged_plan_t *plan, int32_t n, const void *k_
  * Precision: q is rounded to 2^-16 of each element; a softmax weight times its page's
  * v_scale to 2^-14 of itself or 2^-28 of the largest such product among 512 neighbouring
  * keys, whichever is more; sums are FP32.
- * Errors: as rk_paged_attn_decode_split.
+ * Errors: as rk_paged_attn_decode_split; RK_E_UNSUPPORTED, from both, for B * Hkv * (W + splits
+ * of a row) beyond 2^31.
  */
 int rk_paged_decode_q8_scratch_bytes(const rk_paged_plan_t *plan, int32_t split_tokens, uint64_t *bytes);
 int rk_paged_attn_decode_q8(const rk_paged_plan_t *plan, int32_t split_tokens, const void *q,
