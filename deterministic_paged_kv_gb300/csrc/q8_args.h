@@ -11,7 +11,7 @@ namespace rk {
 // stored rotated at its token's position.
 constexpr int Q8_BLOCK_BYTES = PAGE * HEAD_DIM;  // codes of one (page, KV head)
 constexpr int Q8_E_MIN = -64;                    // smallest scale exponent the append writes
-constexpr int Q8_E_MAX = 57;                     // largest: inputs of 2^64 and above are refused
+constexpr int Q8_E_MAX = 56;                     // largest: of inputs below 2^64 (63 - 7)
 constexpr uint32_t Q8_LIMIT_BF16 = (127u + 64u) << 7;  // bf16 bit pattern of 2^64
 
 // Build a step's tables from the rows' lengths and token counts.

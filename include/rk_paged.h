@@ -84,7 +84,7 @@ enum rk_status {
                                        kernel reads has |x| >= 2^15 (the FP16 score operand limit);
                                        8-bit cache calls: see there */
 #define RK_STATUS_SCALE (1 << 5)   /* a scale of the 8-bit cache that is not a positive normal number (append:
-                                       not a power of two in [2^-64, 2^57]) */
+                                       not a power of two in [2^-64, 2^56]) */
 #define RK_STATUS_POOL (1 << 6)    /* rk_paged_tables_extend: a row's tokens or new pages do not fit */
 
 /* Opaque stream handle; identical to cudaStream_t / CUstream. */
@@ -537,7 +537,7 @@ int rk_paged_tables_extend(const rk_paged_plan_t *plan, const int32_t *n_new_d, 
  * (negative position): the token is not written; RK_STATUS_RANGE (an input of 2^64
  * or more, or not finite): that token's codes of the tensor become NaN, which the
  * attention calls report, and the scale goes without it; RK_STATUS_SCALE (a started
- * page whose scale is no power of two in [2^-64, 2^57]): none of the run's tokens is
+ * page whose scale is no power of two in [2^-64, 2^56]): none of the run's tokens is
  * written for that head.
  * Plan: Hkv, D, num_pages and the RoPE constants.  n = 0 is a no-op.  One launch, no
  * allocation, no host synchronisation.  Errors: RK_E_ARG (null or misaligned pointer,

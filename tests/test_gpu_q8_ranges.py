@@ -9,6 +9,7 @@ import torch
 
 import q8_ref as ref
 import test_gpu_q8_attention as att
+import test_gpu_q8_tables_append as tab
 from deterministic_paged_kv_gb300 import binding
 
 pytestmark = pytest.mark.gpu
@@ -183,3 +184,20 @@ def test_q8_a_key_that_takes_nearly_all(mode, Hq, Hkv, lead):
         codes[pg, :, 0] = (key / 4).clamp(-448, 448).to(ref.F8).view(torch.uint8)
         c["v_cache"].view(torch.uint8)[pg, :, 0] = 0
     _small_weights_check(c, mode)
+
+
+# ------------------------------------------------------------- append's scales ----
+
+@pytest.mark.parametrize("e,taken", [(-65, False), (-64, True), (56, True), (57, False)])
+def test_append_q8_scales_that_it_writes(e, taken):
+    """A started page's scale is one that the append itself writes, 2^-64 to 2^56 (inputs below
+    2^64), or the run is refused and the page stays."""
+    c = tab._append_case(8, [(5, 4)], 2)
+    page = c["slots"][0] // 16
+    c["scale"][:, page] = 2.0 ** e
+    got = tab._dev(c)
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    tab._append(c, got, status=st)
+    assert int(st.item()) == (0 if taken else binding.STATUS_SCALE)
+    same = all(torch.equal(a, b) for a, b in zip(tab._bits(got), tab._bits(tab._dev(c))))
+    assert same == (not taken)
