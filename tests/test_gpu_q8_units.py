@@ -71,3 +71,27 @@ def test_prefill_q8_units_after_one_another(B, Sq, Hq, Hkv, lo, hi):
     good = [b for b in range(B) if b not in bad]
     for b, h in ((good[0], 0), (good[-1], Hkv - 1), (good[len(good) // 2], Hkv // 2)):
         att._check(_head(c, b, h), (out[b:b + 1, h * G:(h + 1) * G], lse[b:b + 1, h * G:(h + 1) * G]), att.PREFILL)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,split", [(700, 8, 2, 0), (2100, 4, 1, 0), (2100, 4, 2, 16), (1500, 6, 3, 1 << 20)])
+def test_decode_q8_large_batches(B, Hq, Hkv, split):
+    """More rows than the threads that count their steps (640), than the list's entries (1024) and
+    than twice those: each row as in a batch of fifty, and as in 64 bits."""
+    r = np.random.RandomState(B + Hkv)
+    lens = [int(x) for x in r.choice([0, 1, 15, 16, 17, 40, 100, 130, 300, 700], B, p=[.05, .1, .1, .1, .1, .2, .2, .1, .04, .01])]
+    c = ref.case(B, lens, Hq, Hkv)
+    bad, bits = _spoil(c, r)
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    out, lse = att._run(c, split, status=st)
+    assert int(st.item()) == bits
+    gone = torch.tensor(sorted(bad))
+    assert (out[gone] == 0).all() and torch.isnan(lse[gone]).all()
+    good = [b for b in range(B) if b not in bad]
+    d = [c[n].cuda() for n in ref.NAMES]
+    for at in range(0, len(good), 50):
+        rows = torch.tensor(good[at:at + 50], device="cuda")
+        part = [t if n in ("k_cache", "v_cache", "k_scale", "v_scale") else t[rows].contiguous() for t, n in zip(d, ref.NAMES)]
+        few = dict(c, q=part[0], block_table=part[5])
+        assert att._equal([out[rows], lse[rows]], att._run(few, split, d=part)), at
+    pick = good[::max(1, len(good) // 40)]
+    att._check(att._rows(c, pick), (out[pick], lse[pick]), att.DECODE)
