@@ -113,6 +113,7 @@ struct DqCtrl {
     DqStep step[DQ_SLOTS];
     int ids[DQ_SLOTS][32];           // page of lane p's block: page p / H, head p % H of the step
     uint32_t odd[DQ_SLOTS];          // blocks whose scale is not one
+    uint32_t wide[DQ_SLOTS];         // blocks of the heads whose scales of V lie too far apart in the item so far
     alignas(16) float4 sc[DQ_SLOTS][32];  // k scale, log2 of v's, 1 / v's of those blocks
     float qscale[2][16];             // score factor of each query head (log2 domain)
     uint32_t qbad[2];                // query heads out of range
@@ -353,6 +354,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
         int t = 0, t1 = 0, id = 0;  // the step's first token, the item's end, the lane's page id
         const int my_page = lane / H;
         bool newq = true;
+        VSpan span;  // of the lane's blocks of the item
         auto page_id = [&]() {
             return my_page * PAGE < t1 - t ? __ldg(a.block_table + (size_t)st.b * a.W + t / PAGE + my_page) : 0;
         };
@@ -400,7 +402,9 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 ks = __ldg(a.k_scale + block);
                 vs = __ldg(a.v_scale + block);
             }
+            if (st.flags & DQ_FIRST) span = VSpan();
             // the next step's page ids travel while this step's scales do
+            const bool scaled = mine && st.cnt > 0;
             st.bad = st.flags = 0;  // said once
             if (last) {
                 if (!end) item();
@@ -410,9 +414,19 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
             }
             const bool odd = !scale_ok(ks) || !scale_ok(vs);
             if (odd) ks = vs = 1.0f;
+            if (scaled) span.add(vs);
+            uint32_t wide = 0;
+            if (__any_sync(0xffffffffu, span.outside())) {
+                VSpan all = span;
+                all.join<H, 32>();
+                wide = __ballot_sync(0xffffffffu, all.too_wide());
+            }
             c->sc[slot][lane] = make_float4(ks, __log2f(vs), rcp(vs), 0.0f);
             const uint32_t odds = __ballot_sync(0xffffffffu, odd);
-            if (lane == 0) c->odd[slot] = odds;
+            if (lane == 0) {
+                c->odd[slot] = odds;
+                c->wide[slot] = wide;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&c->sc_full[slot]));
             if (++slot == DQ_SLOTS) {
@@ -716,7 +730,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 st.flags = s->flags;
                 st.bad = s->bad;
                 ps = c->sc[slot][(8 * blk + (t >> 4)) * H + hj];
-                const uint32_t odd = c->odd[slot];
+                const uint32_t odd = c->odd[slot], wide = c->wide[slot];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&c->slot_empty[slot]));
                 if (++slot == DQ_SLOTS) {
@@ -738,6 +752,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
                 for (int g = 0; g < G; ++g) sc[g] = c->qscale[qb][hj * G + g];
                 constexpr uint32_t EACH = H == 1 ? 0xffffffffu : 0x55555555u;
                 if (odd & (EACH << hj)) range |= 0x80000000u;
+                if (wide & (EACH << hj)) range |= (1u << G) - 1u;
                 if (st.flags & DQ_ENDQ) {
                     __syncwarp();
                     if (ok && lane == 0) mbar_arrive(smem_u32(&c->q_empty[qb]));

@@ -34,7 +34,10 @@
 //                the codes in registers and all unrolled the code pushed the softmax's out of
 //                the instruction cache: 615 us of S = 8192 where it takes 468);
 //   warpgroups 1, 2  softmax of q-tile 0, 1: a thread per accumulator row;
-//   warp 13      MMA issuer (converged); warps 12, 14 have nothing to do.
+//   warp 13      MMA issuer (converged);
+//   warp 14      how far V's scales of a unit lie apart (in the transform warps this took 3%: they have
+//                no register left);
+//   warp 12      nothing.
 // Nothing depends on B, W or the grid.
 #include <atomic>
 
@@ -45,7 +48,7 @@ namespace rk {
 namespace {
 
 constexpr int PQ_THREADS = 512;
-constexpr int WARP_MMA = 13, WARP_SCHED = 15;
+constexpr int WARP_MMA = 13, WARP_SPAN = 14, WARP_SCHED = 15;
 constexpr int KST = 2, VST = 2;                 // K stages, V stages
 constexpr int SCST = 4;                         // scale slots: one more than K stages at least
 constexpr uint32_t TMEM_COLS = 512;             // S0 [0,128) S1 [128,256) O0 [256,384) O1 [384,512)
@@ -63,7 +66,7 @@ __device__ __forceinline__ float score_factor(float k_scale, float q_scale) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(k_scale * q_scale), "f"(1.17549435e-38f));
     return r;
 }
-constexpr uint32_t UNIT_READERS = 32 + 128 + 256;
+constexpr uint32_t UNIT_READERS = 32 + 32 + 128 + 256;
 
 // setmaxnreg split (sum 4 x 128 = the 512 x 128 registers the CTA launches with)
 constexpr int REG_XFORM = 96, REG_SOFTMAX = 184, REG_CTRL = 48;
@@ -87,12 +90,13 @@ struct PqBars {
     uint64_t k_full[KST], k_empty[KST], v_full[VST], v_empty[VST], sc_full[SCST];
     uint64_t s_full[2], p_ready[2], o_done[2], o_free[2];
     uint64_t u_full[2], u_empty[2];
-    uint64_t r_full[2], r_empty[2];      // a unit's verdict: transform threads -> softmax
+    uint64_t r_full[2], r_empty[2];      // a unit's verdict: transform threads and warp 14 -> softmax
     uint64_t never;
     uint32_t tmem_base;
     PipeCtl pipe;
     PqUnit unit[2];
     alignas(16) uint8_t r_flag[2][128];  // 1: NaN code in V, 2: a scale that is none
+    int r_wide[2];                       // V's scales too far apart
     alignas(16) float4 sc[SCST][PF_PAGES_PER_TILE];  // k scale, log2 of v's, 1 / v's
     int8_t qexp[2][PF_BM];               // exponent of a query's power of two; Q_BAD: out of range
     float qscale[2][PF_BM];              // score factor of each query (log2 domain); NaN: out of range
@@ -320,7 +324,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
             mbar_init(smem_u32(&bars->o_free[j]), 128);
             mbar_init(smem_u32(&bars->u_full[j]), 1);
             mbar_init(smem_u32(&bars->u_empty[j]), UNIT_READERS);
-            mbar_init(smem_u32(&bars->r_full[j]), 128);
+            mbar_init(smem_u32(&bars->r_full[j]), 128 + 1);
             mbar_init(smem_u32(&bars->r_empty[j]), 256);
         }
         fence_mbar_init();
@@ -354,6 +358,31 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                     mbar_arrive(smem_u32(&bars->u_full[slot]));
                 }
                 if (m.end) break;
+            }
+        } else if (warp == WARP_SPAN) {
+            // ===================================== distance of V's scales ====
+            bool ok = true;
+            int wu = 0;  // work units
+#pragma unroll 1
+            for (int kk = 0; ok; ++kk) {
+                PqUnit u;
+                if (!(ok = __all_sync(0xffffffffu, read_unit(bars, kk, pc, u))) || __any_sync(0xffffffffu, u.end)) break;
+                if (u.bad || max(u.nt0, u.nt1) == 0) continue;
+                const int32_t* bt = a.block_table + (size_t)u.b * a.W;
+                VSpan span;
+#pragma unroll 1
+                for (int p = lane; p < (u.n_keys + PAGE - 1) / PAGE; p += 32) {
+                    const float vs = __ldg(a.v_scale + (size_t)__ldg(bt + p) * a.Hkv + u.kvh);
+                    if (scale_ok(vs)) span.add(vs);
+                }
+                span.join<1, 32>();
+                const int slot = wu & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->r_empty[slot]), (uint32_t)(((wu >> 1) & 1) ^ 1), pc)) != 0;
+                if (ok && lane == 0) {
+                    bars->r_wide[slot] = span.too_wide();
+                    mbar_arrive(smem_u32(&bars->r_full[slot]));
+                }
+                ++wu;
             }
         } else if (warp == WARP_MMA) {
             // ============================================= MMA issuer ====
@@ -748,7 +777,7 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                     uint32_t any = 0;
 #pragma unroll
                     for (int q = 0; q < 8; ++q) any |= f[q].x | f[q].y | f[q].z | f[q].w;
-                    unit_bad = (any & 0x01010101u ? RK_STATUS_RANGE : 0) | (any & 0x02020202u ? RK_STATUS_SCALE : 0);
+                    unit_bad = (any & 0x01010101u || bars->r_wide[slot] ? RK_STATUS_RANGE : 0) | (any & 0x02020202u ? RK_STATUS_SCALE : 0);
                     mbar_arrive(smem_u32(&bars->r_empty[slot]));
                 }
             }

@@ -54,6 +54,28 @@ __device__ __forceinline__ int q8_exponent(uint32_t amax_bits) { return max((int
 // A scale the attention calls accept: positive, normal, finite.
 __device__ __forceinline__ bool scale_ok(float s) { return s >= 1.17549435e-38f && s < INFINITY; }
 
+// Smallest and largest exponent of V's scales that weights of one running maximum have in them.
+// Weights have V's scale in their exponent and the sum takes it out again, so a key whose scale is far
+// below another's is lost to the sum where its weight passes FP32's 2^-126, which is 2^-133 of the
+// largest or less.  With exponents up to 80 apart 2^30 lost keys are 2^-22 of the sum at most; further
+// apart the query fails.  One word: the largest exponent, and the largest distance below 255.
+struct VSpan {
+    uint32_t w = 0;
+    __device__ __forceinline__ void add(float scale) {
+        const uint32_t e = __float_as_uint(scale) >> 23;
+        w = __vmaxu2(w, e << 16 | (255u - e));
+    }
+    // with the lanes that differ in the bits FROM .. TO / 2 of their number
+    template <int FROM, int TO>
+    __device__ __forceinline__ void join() {
+#pragma unroll
+        for (int o = FROM; o < TO; o <<= 1) w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, o));
+    }
+    __device__ __forceinline__ bool too_wide() const { return (w >> 16) + (w & 0xffffu) > 255u + 80u; }
+    // a set that may be too wide with others: not every exponent in [-40, 40]
+    __device__ __forceinline__ bool outside() const { return (w >> 16) > 127u + 40u || (w & 0xffffu) > 128u + 40u; }
+};
+
 // Largest of a warp's values (NaN left out), in every lane.
 __device__ __forceinline__ float warp_max(float x) {
     float r;

@@ -565,8 +565,9 @@ int rk_paged_kv_append_q8(const rk_paged_plan_t *plan, int32_t n, const void *k_
  * Status and failed rows (out = 0, lse = NaN): RK_STATUS_KVLEN, _POSITION, _PAGE_OOB
  * as in the BF16 call; RK_STATUS_SCALE (a scale of a visible page that is not a
  * positive normal number) and RK_STATUS_RANGE (a q element of 2^64 or more or not
- * finite, a NaN code among the visible tokens, scores or sums beyond FP32) fail the
- * query heads that meet them, and may fail the other query heads of that KV head.
+ * finite, a NaN code among the visible tokens, scores or sums beyond FP32, v_scales of a split's
+ * visible pages with exponents more than 80 apart) fail the query heads that meet them, and may
+ * fail the other query heads of that KV head.  Sums stay in FP32 for any v_scale from 2^-80 up.
  * What lies past kv_len or the position is not read as a value (it may be anything).
  * Precision: q is rounded to 2^-16 of each element; a softmax weight times its page's
  * v_scale to 2^-14 of itself or 2^-28 of the largest such product among 512 neighbouring
@@ -587,8 +588,8 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t *plan, int32_t split_tokens, c
  * rk_paged_attn_prefill with the scales.  One ascending pass over the keys per
  * query, no split.  Status and failed rows as in rk_paged_attn_decode_q8; queries go
  * through the kernel in units of 256 / (Hq / Hkv) neighbours, and a unit's queries that
- * see a key fail together for metadata, a scale, or a NaN code of V among the keys
- * that any of them reads (a NaN code of K fails those that see it).
+ * see a key fail together for metadata, a scale, v_scales too far apart, or a NaN code of
+ * V among the keys that any of them reads (a NaN code of K fails those that see it).
  * Precision: q is rounded to FP16 after its rotation (2^-11 of each element, as
  * in the BF16 call), which moves lse by some 1e-5 (the decode call keeps 2^-16); a softmax
  * weight times its page's v_scale to FP16, 2^-11 of itself or 2^-32 of the largest such product.

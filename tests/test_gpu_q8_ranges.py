@@ -201,3 +201,83 @@ def test_append_q8_scales_that_it_writes(e, taken):
     assert int(st.item()) == (0 if taken else binding.STATUS_SCALE)
     same = all(torch.equal(a, b) for a, b in zip(tab._bits(got), tab._bits(tab._dev(c))))
     assert same == (not taken)
+
+
+# -------------------------------------------------- V scales that lie far apart ----
+
+def _apart(mode, gap, low_page, n=200, Hq=8, Hkv=2):
+    """Rows of equal scores (q = 0), the first's KV head 1 with one page of V (None: no page) at 2^-gap of the others."""
+    c = ref.case(121, [n, 70], Hq, Hkv, Sq=1 if mode == "decode" else 20)
+    c["q"].zero_()
+    top = 20 if gap <= 100 else 60
+    c["v_scale"].fill_(2.0 ** top)
+    if low_page is not None:
+        c["v_scale"][c["block_table"][0, low_page].long(), 1] = 2.0 ** (top - gap)
+    return c
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("low_page", [0, 5, 11])
+@pytest.mark.parametrize("gap", [30, 79])
+def test_q8_v_scales_apart(mode, low_page, gap):
+    """Up to 2^80 apart every key is in the sum of the weights: equal ones here."""
+    c = _apart(mode, gap, low_page)
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    got = att._run(c, 1 << 20, status=st, mode=mode)
+    assert int(st.item()) == 0
+    att._check(c, got, TOL[mode])
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("low_page", [0, 5, 11])
+@pytest.mark.parametrize("gap", [82, 135, 150, 180])
+def test_q8_v_scales_too_far_apart(mode, low_page, gap):
+    """Further apart, where 32 bits lose the smaller ones' weights, that head fails; the rest does not."""
+    c = _apart(mode, gap, low_page)
+    want = att._run(_apart(mode, gap, None), 1 << 20, mode=mode)
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    out, lse = att._run(c, 1 << 20, status=st, mode=mode)
+    assert int(st.item()) == binding.STATUS_RANGE
+    s = c["q"].shape[2] - 1  # sees every page
+    assert (out[0, 4:, s] == 0).all() and torch.isnan(lse[0, 4:, s]).all()
+    assert torch.equal(out[0, :4], want[0][0, :4]) and torch.equal(lse[0, :4], want[1][0, :4])
+    assert att._equal((out[1], lse[1]), (want[0][1], want[1][1]))
+
+
+def test_decode_q8_v_scales_apart_in_other_splits():
+    """Splits are joined by their own sums, so what lies in different ones may be any distance apart
+    (as long as each sum is in FP32: 128 weights of up to 2^8 over scales of 2^-120 are not)."""
+    for gap in (150, 180):
+        c = _apart("decode", gap, 3, n=300)
+        c["v_scale"][c["block_table"][0].long(), 1] = 2.0 ** (60 - gap)
+        c["v_scale"][c["block_table"][0, 8:16].long(), 1] = 2.0 ** 60
+        st = torch.zeros(1, dtype=i32, device="cuda")
+        out, lse = att._run(c, 128, status=st)
+        if gap == 180:
+            assert int(st.item()) == binding.STATUS_RANGE
+            assert (out[0, 4:] == 0).all() and torch.isnan(lse[0, 4:]).all() and torch.isfinite(lse[0, :4]).all()
+        else:
+            assert int(st.item()) == 0
+            att._check(c, (out, lse), att.DECODE)
+
+
+@pytest.mark.parametrize("mode,split", [("decode", 0), ("decode", 1 << 20), ("prefill", 0)])
+def test_q8_v_scales_apart_in_other_steps(mode, split):
+    """Pages far apart that are read in different steps or tiles; a split of its own is no reason to fail,
+    and a row behind one that fails starts afresh."""
+    for low_page, high_page in ((1, 50), (70, 2)):
+        c = ref.case(123, [1200, 40, 300], 16, 2, Sq=1 if mode == "decode" else 20)
+        c["v_scale"].fill_(2.0 ** -6)
+        pages = c["block_table"][0].long()
+        c["v_scale"][pages[low_page], 0] = 2.0 ** -50
+        c["v_scale"][pages[high_page], 0] = 2.0 ** 40
+        st = torch.zeros(1, dtype=i32, device="cuda")
+        out, lse = att._run(c, split, status=st, mode=mode)
+        apart = mode == "decode" and split == 0  # pages 0 .. 31 are the first split, 32 .. 63 the next
+        assert int(st.item()) == (0 if apart else binding.STATUS_RANGE)
+        c["v_scale"][pages[low_page], 0] = c["v_scale"][pages[high_page], 0] = 2.0 ** -6
+        want = att._run(c, split, mode=mode)
+        assert torch.equal(out[0, 8:], want[0][0, 8:]) and torch.equal(lse[0, 8:], want[1][0, 8:])
+        assert att._equal((out[1:], lse[1:]), (want[0][1:], want[1][1:]))
+        if not apart:
+            assert (out[0, :8, -1] == 0).all() and torch.isnan(lse[0, :8, -1]).all()
