@@ -985,7 +985,7 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
 // lse = -inf.  MANY = false: a warp has a row, four dims to a lane and all eight sums (four rows
 // to a block).  MANY = true: a block of two warps has a quarter of a row's dims, eight lanes to
 // a sum, and asks for sixteen splits of each sum at a time.  Both add in the same order, so which
-// one runs (a choice by the table's width) does not show in the result.  Bound by latency: the
+// one runs (a choice by the table and the number of rows) does not show in the result.  Bound by latency: the
 // row's length, a round or two of loads, one of stores.
 template <bool MANY>
 __global__ void __launch_bounds__(MANY ? 64 : 128) merge_q8_kernel(const __grid_constant__ AttnQ8Args a) {
@@ -1131,9 +1131,11 @@ cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const
     e = launch_any(a.G, bundle, km, vm, a, grid, stream, false);
     if (e != cudaSuccess || a.n_splits <= 1) return e;
     const long long rows = (long long)a.B * a.Hq;
-    // Long rows in quarters: 32 rows and heads of 82 splits take 2.5 us (4.1 by a block of eight
-    // warps to a row, with the partials gone from L2).
-    const bool many = a.n_splits > 32 && rows <= 0x1fffffff;
+    // Rows in quarters where the table holds long ones, unless there are so many rows and heads that the
+    // quarters queue.  Whole calls in us, quarters / whole rows: 32 rows and heads past 100000 87.0 / 96.8,
+    // 128 of 20000 74.7 / 78.8, 512 of 16000 90.2 / 91.8; 1024 of 8000 91.9 / 89.6, 2048 of 4096 in a table of
+    // 131072 96.4 / 89.4, 2048 of 100 to 600 there 29.2 / 21.8.
+    const bool many = a.n_splits > 32 && rows <= 512;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(many ? rows * 4 : (rows + 3) / 4));
     cfg.blockDim = dim3(many ? 64 : 128);

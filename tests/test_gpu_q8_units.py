@@ -95,3 +95,17 @@ def test_decode_q8_large_batches(B, Hq, Hkv, split):
         assert att._equal([out[rows], lse[rows]], att._run(few, split, d=part)), at
     pick = good[::max(1, len(good) // 40)]
     att._check(att._rows(c, pick), (out[pick], lse[pick]), att.DECODE)
+
+
+def test_decode_q8_many_rows_in_a_wide_table():
+    """A table that holds long rows, with more rows and heads than the merge takes in quarters (512) and
+    with fewer: the bits of a table as wide as the longest row."""
+    lens = [33, 700, 1, 0, 513, 5000] + [40] * 60
+    c = ref.case(131, lens, 16, 2)
+    want = att._run(c)
+    rows = list(range(len(lens)))
+    assert len(rows) * 16 > 512
+    assert att._equal(want, att._run(att._rows(c, rows, 1300)))
+    few = [5, 1, 0]
+    assert att._equal([x[few] for x in want], att._run(att._rows(c, few, 1300)))
+    att._check(att._rows(c, few), [x[few] for x in want], att.DECODE)
