@@ -271,7 +271,12 @@ const char* rk_paged_policy(void) {
            "pv_mma=bf16_operands_fp32_acc,l_merge=fixed_tree;"
            "prefill_tile=2xq128xkv128,score_mma=fp16_operands_fp32_acc,pv_mma=bf16_operands_fp32_acc;"
            "batch_invariant=1;page_size=16;head_dim=128;"
-           "decode_split_entry=fixed_splits_of_16k_tokens,ordered_fp32_merge,separate_policy";
+           "decode_split_entry=fixed_splits_of_16k_tokens,ordered_fp32_merge,separate_policy;"
+           "q8_cache=e4m3_codes,pow2_scale_per_page_and_kv_head,k_rotated_at_append;"
+           "q8_decode=fixed_splits_of_512_tokens_and_1024_from_16384_or_of_split_tokens,ordered_fp32_merge,"
+           "score_mma=q_in_4_e4m3_parts_fp32_acc,pv_mma=weights_in_3_e4m3_parts_fp32_acc;"
+           "q8_prefill=split_kv_disabled,prefill_tile_as_above,score_mma=fp16_operands_fp32_acc,"
+           "pv_mma=fp16_operands_fp32_acc";
 }
 
 int rk_paged_plan(rk_paged_plan_t* plan, int32_t B, int32_t Sq, int32_t Hq, int32_t Hkv, int32_t D,

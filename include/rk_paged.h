@@ -608,7 +608,8 @@ const char *rk_last_error(void);
 /*
  * Fixed arithmetic policy of this library as "key=value;..." text: split-KV,
  * accumulation and LSE types, LSE base, downcast point and rounding, KV
- * reduction order, KV tile sizes.  Provenance in the sense of "WS2 PR7 ...",
+ * reduction order, KV tile sizes; q8_cache, q8_decode and q8_prefill: what differs
+ * for the 8-bit cache.  Provenance in the sense of "WS2 PR7 ...",
  * "P2P NCCL reference and strict arithmetic provenance" (FP32 accumulation,
  * FP32 LSE, downcast only at the final write).  Static string.
  */
