@@ -127,3 +127,64 @@ def test_q8_ragged_steps(room, captured):
                     val = c[("k_cache", "v_cache")[i]].to(torch.float32)[pg, :, t % 16].double() * sc
                     assert ((val - y).abs() <= 2.0 ** -4 * y.abs() * (1 + 2.0 ** -30) + 2.0 ** -6 * sc).all()
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("theta,scale", [(1e4, 1.0), (5e5, 8.0), (1e6, 0.5)])
+def test_q8_rope_constants(theta, scale):
+    """Append, decode and prefill rotate by the plan's constants, not by the usual ones."""
+    g = torch.Generator().manual_seed(9)
+    n, Hq, Hkv = 150, 4, 2
+    w = theta ** (-np.arange(0, 128, 2) / 128) / scale
+    turn = lambda x, pos: np.concatenate([(z := (x[..., :64] + 1j * x[..., 64:]) * np.exp(1j * np.asarray(pos, np.float64)[..., None] * w)).real,  # noqa: E731
+                                          z.imag], -1)
+    k, v = (torch.randn((n, Hkv, 128), generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((1, Hq, n, 128), generator=g).to(torch.bfloat16)
+    table = torch.randperm(12, generator=g).to(i32)[:10].view(1, 10).cuda()
+    pos = torch.arange(n, dtype=i32).cuda()
+    cache = [torch.zeros((12, Hkv, 16, 128), dtype=torch.uint8, device="cuda").view(ref.F8) for _ in range(2)]
+    cache += [torch.ones((12, Hkv), device="cuda") for _ in range(2)]
+    slot = (table[0, pos.long() // 16] * 16 + pos % 16).to(i32)
+    kv = tab._t([n])
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    plan = lambda Sq: binding.plan(1, Sq, Hq, Hkv, 128, 16, 12, 10, rope_theta=theta, rope_scale=scale)  # noqa: E731
+    binding.kv_append_q8(plan(1), k.cuda(), v.cuda(), slot, pos, *cache, status=st)
+    out, lse = torch.empty_like(q).cuda(), torch.empty((1, Hq, n), device="cuda")
+    binding.attn_prefill_q8(plan(n), q.cuda(), *cache, table, kv, pos.view(1, n), out, lse, status=st)
+    one, one_l = torch.empty((1, Hq, 1, 128), dtype=torch.bfloat16, device="cuda"), torch.empty((1, Hq, 1), device="cuda")
+    binding.attn_decode_q8(plan(1), q[:, :, -1:].contiguous().cuda(), *cache, table, kv, pos[-1:].view(1, 1), one, one_l, status=st)
+    assert int(st.item()) == 0
+    pg = table[0].long().cpu()
+    kc, vc = ((c.cpu().float()[pg] * s.cpu()[pg][..., None, None]).double().transpose(1, 2).reshape(-1, Hkv, 128)[:n].numpy()
+              for c, s in ((cache[0], cache[2]), (cache[1], cache[3])))
+    y = turn(k.double().numpy(), np.arange(n)[:, None])
+    sc = cache[2].cpu()[pg].double().numpy().repeat(16, 0)[:n, :, None]
+    assert (np.abs(kc - y) <= 2.0 ** -4 * np.abs(y) * (1 + 2.0 ** -30) + 2.0 ** -6 * sc).all()
+    for h in range(Hq):
+        r = turn(q[0, h].double().numpy(), np.arange(n))
+        x = r @ kc[:, h // 2].T / np.sqrt(128)
+        x[np.triu_indices(n, 1)] = -np.inf
+        p = np.exp(x - x.max(-1, keepdims=True))
+        want = p @ vc[:, h // 2] / p.sum(-1, keepdims=True)
+        pair = np.tile(np.hypot(q[0, h, :, :64].double().numpy(), q[0, h, :, 64:].double().numpy()), 2)
+        d = 2.0 ** -11 * 1.1 * (pair @ np.abs(kc[:, h // 2]).T / np.sqrt(128)).max(-1)[:, None]
+        bound = 2.0 ** -8 * np.abs(want) + (2 * d + 2.0 ** -10) * np.abs(vc).max() + 1e-30
+        assert (np.abs(out[0, h].double().cpu().numpy() - want) <= bound).all()
+        assert (np.abs(one[0, h, 0].double().cpu().numpy() - want[-1]) <= bound[-1]).all()
+
+
+@pytest.mark.parametrize("mode", ["decode", "prefill"])
+@pytest.mark.parametrize("NP,W", [(0, 0), (0, 3), (5, 0)])
+def test_q8_attention_without_pages_or_table(mode, NP, W):
+    """No pool, no table: empty rows are empty, rows that claim tokens fail."""
+    Sq = 1 if mode == "decode" else 3
+    p = binding.plan(2, Sq, 4, 2, 128, 16, NP, W)
+    q = torch.randn((2, 4, Sq, 128), device="cuda").to(torch.bfloat16)
+    cache = [torch.zeros((NP, 2, 16, 128), dtype=torch.uint8, device="cuda").view(ref.F8) for _ in range(2)]
+    cache += [torch.ones((NP, 2), device="cuda") for _ in range(2)]
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    out, lse = torch.full_like(q, 3), torch.full((2, 4, Sq), 3.0, device="cuda")
+    f = binding.attn_decode_q8 if mode == "decode" else binding.attn_prefill_q8
+    f(p, q, *cache, torch.full((2, W), -1, dtype=i32, device="cuda"), tab._t([0, 5]), torch.zeros((2, Sq), dtype=i32, device="cuda"),
+      out, lse, status=st)
+    assert int(st.item()) == (binding.STATUS_PAGE_OOB if W else binding.STATUS_KVLEN)
+    assert (out == 0).all() and torch.isneginf(lse[0]).all() and torch.isnan(lse[1]).all()
