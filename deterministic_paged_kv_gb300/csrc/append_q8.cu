@@ -18,7 +18,9 @@
 // E comes from the inputs' exponent bits, never from a rounded product.
 // The rotation is in FP32; a pair with a result that FP32 cannot place on one
 // side of a rounding border is done again with 44 bits, so that codes are those of
-// the real number (a few in a million would be one step off otherwise).
+// the rotation by the plan's rates (a few in a million would be one step off otherwise).
+// The rates are doubles, so that at position 131071 an angle is the real number's to
+// some 2^-35: one code in 2^30 may still be the neighbour of the real number's.
 //
 // Work: a run is the tokens of one call on one page (slots that follow one another).  The
 // runs that start in a window of tokens belong to one warp (window 4) or to the four warps of a
@@ -26,9 +28,10 @@
 // window's t-th token (a run goes on for 15 past the window at most), the values go by 8 lanes
 // to a token, four tokens to a warp's turn, once for the exponents and once more (mostly still
 // in registers, else out of L1) for the codes.
-// 64 single tokens x 8 heads: 4.7 us a launch (latency: launch, slots, values, stores); 2048
-// tokens in runs of 16: 6.7 us; 12700 tokens of 24 ragged rows: 29 us (bound by instructions, a quarter of them for the borders:
-// the bytes alone would take 12).
+// 64 single tokens x 8 heads: 4.8 us a launch (latency, and a longer chain of it than a copy has: slots,
+// runs, values, exponents by shuffles, scales, codes; the BF16 append of as many tokens takes 1.9); 2048
+// tokens in runs of 16: 6.8 us; 12700 tokens of 24 ragged rows: 29 us (bound by instructions, a quarter of
+// them for the borders: the bytes alone would take 12).
 #include "q8_device.cuh"
 
 namespace rk {

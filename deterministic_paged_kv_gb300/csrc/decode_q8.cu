@@ -28,7 +28,8 @@
 //
 // Work: an item is a split of a row for a bundle of H neighbouring KV heads (2, or 1 where
 // Hkv is odd).  A TMA copy takes a page's blocks of the whole bundle: 64 x 4096 takes 125 us head
-// by head (copies of 2 KiB), 91 in bundles of two, 93 in bundles of four, whose items are
+// by head (copies of 2 KiB, which is what an odd Hkv has: 123 us for the same bytes with Hkv 1 or 3 and
+// four queries a KV head, 134 with eight), 90 in bundles of two, 93 in bundles of four, whose items are
 // coarser (20 ragged rows of 8 heads a KV head: 54 us, 48 in twos then, 44 now).  A step is 512 / H tokens
 // of the bundle, four tiles of 128 tokens and one head; in it the softmax is plain (one
 // maximum over its tokens), steps and splits are joined with the running maximum in FP32.  The
@@ -44,7 +45,8 @@
 //   warp 1      MMA issuer: S and PV of each step;
 //   warp 2      q: rotates the query heads of the next row and bundle, splits them into parts
 //               (the softmax warps do the first ones, together: they have nothing else to do);
-//   warp 3      metadata: walks the items, page ids and scales of each step;
+//   warp 3      metadata: walks the items, page ids and scales of each step, and how far V's scales of
+//               an item lie apart;
 //   warps 4-19  softmax: warpgroup j has tile j of a step, a thread one token, and
 //               in the accumulation its share of that KV head's queries, a thread one
 //               output dim.

@@ -22,7 +22,7 @@
 // and the conversions take 40% of what they leave.  (An issuer to each q-tile: 538 us, as the
 // MMAs of the two then share the pipe and both chains grow; a maximum found along with the
 // exponentials and the tile done again where it rose: 500 us.)
-// S = 8192 of 32 heads: 468 us, tensor pipe 49% active; 4 chunks of 512 behind 1536: 71 us
+// S = 8192 of 32 heads: 472 us, tensor pipe 49% active; 4 chunks of 512 behind 1536: 73 us
 // (256 units on 152 CTAs: two units where 1.68 would be even); 33 queries: 22 us.
 // Roles (512 threads, registers rebalanced with setmaxnreg):
 //   warp 15      scheduler: each unit's metadata, published as a descriptor (two slots);
@@ -32,7 +32,7 @@
 //                to do yet: 2 us of a call).  Codes come by cp.async, a thread's own 16 bytes of
 //                each page, a tile ahead, and are converted two pages to a turn of a loop (with
 //                the codes in registers and all unrolled the code pushed the softmax's out of
-//                the instruction cache: 615 us of S = 8192 where it takes 468);
+//                the instruction cache: 615 us of S = 8192 where the loop took 468);
 //   warpgroups 1, 2  softmax of q-tile 0, 1: a thread per accumulator row;
 //   warp 13      MMA issuer (converged);
 //   warp 14      how far V's scales of a unit lie apart (in the transform warps this took 3%: they have

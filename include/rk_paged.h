@@ -569,9 +569,9 @@ int rk_paged_kv_append_q8(const rk_paged_plan_t *plan, int32_t n, const void *k_
  * visible pages with exponents more than 80 apart) fail the query heads that meet them, and may
  * fail the other query heads of that KV head.  Sums stay in FP32 for any v_scale from 2^-80 up.
  * What lies past kv_len or the position is not read as a value (it may be anything).
- * Precision: q is rounded to 2^-16 of each element; a softmax weight times its page's
- * v_scale to 2^-14 of itself or 2^-28 of the largest such product among 512 neighbouring
- * keys, whichever is more; sums are FP32.
+ * Precision: q is rounded to 2^-16 of each element or 2^-25 of the largest, whichever is
+ * more; a softmax weight times its page's v_scale to 2^-14 of itself or 2^-28 of the
+ * largest such product among 512 neighbouring keys; sums are FP32.
  * Errors: as rk_paged_attn_decode_split; RK_E_UNSUPPORTED, from both, for B * Hkv * (W + splits
  * of a row) beyond 2^31.
  */
@@ -591,8 +591,9 @@ int rk_paged_attn_decode_q8(const rk_paged_plan_t *plan, int32_t split_tokens, c
  * see a key fail together for metadata, a scale, v_scales too far apart, or a NaN code of
  * V among the keys that any of them reads (a NaN code of K fails those that see it).
  * Precision: q is rounded to FP16 after its rotation (2^-11 of each element, as
- * in the BF16 call), which moves lse by some 1e-5 (the decode call keeps 2^-16); a softmax
- * weight times its page's v_scale to FP16, 2^-11 of itself or 2^-32 of the largest such product.
+ * in the BF16 call), which moves lse by some 1e-5 (the decode call keeps 2^-16, and takes
+ * single queries of a chunk as rows that share their pages); a softmax weight times its
+ * page's v_scale to FP16, 2^-11 of itself or 2^-32 of the largest such product.
  * Errors: as rk_paged_attn_prefill.
  */
 int rk_paged_attn_prefill_q8(const rk_paged_plan_t *plan, const void *q, const void *k_cache,
