@@ -719,32 +719,42 @@ __global__ void __launch_bounds__(PQ_THREADS, 1)
                 }
                 // p' = 2^(w - m + 7), packed as FP16 pairs into xr[0..63]; the sum divides vs out
                 const float base = (m == -INFINITY) ? 0.0f : m;
-                const bool far = __any_sync(0xffffffffu, fabsf(base) >= FAR_MAX);
-                if (far) {  // w - m into xr; what follows adds the bias
+                const bool far = fabsf(base) >= FAR_MAX;
+                float rs = 0.0f;
+                if (__builtin_expect(!__any_sync(0xffffffffu, far), 1)) {
 #pragma unroll
                     for (int p = 0; p < PF_PAGES_PER_TILE; ++p) {
                         const float4 f = sc[p];
-                        const float mul = score_factor(f.x, scr);
+                        const float mul = score_factor(f.x, scr), add = f.y + (P_BIAS - base);
+                        const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
+                        float2 acc2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-                        for (int c = 16 * p; c < 16 * p + 16; ++c)
-                            xr[c] = __float_as_uint(fmaf(__uint_as_float(xr[c]), mul, f.y) - base);
+                        for (int c = 16 * p; c < 16 * p + 16; c += 2) {
+                            const float2 t = ffma2(make_float2(__uint_as_float(xr[c]), __uint_as_float(xr[c + 1])), mul2, add2);
+                            const float2 e = make_float2(ex2(t.x), ex2(t.y));
+                            acc2 = fadd2(acc2, e);
+                            xr[c >> 1] = pack_f16x2(e.x, e.y);
+                        }
+                        rs = fmaf(acc2.x + acc2.y, f.z, rs);
                     }
-                }
-                float rs = 0.0f;
+                } else {
+                    // the same with the maximum subtracted apart, in the rows that are far: a row's bits are its
+                    // own, whatever the rows beside it are
 #pragma unroll
-                for (int p = 0; p < PF_PAGES_PER_TILE; ++p) {
-                    const float4 f = sc[p];
-                    const float mul = far ? 1.0f : score_factor(f.x, scr), add = far ? P_BIAS : f.y + (P_BIAS - base);
-                    const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
-                    float2 acc2 = make_float2(0.0f, 0.0f);
+                    for (int p = 0; p < PF_PAGES_PER_TILE; ++p) {
+                        const float4 f = sc[p];
+                        const float mul = score_factor(f.x, scr), add = far ? f.y : f.y + (P_BIAS - base);
+                        const float less = far ? base : 0.0f, more = far ? P_BIAS : 0.0f;
+                        float2 acc2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int c = 16 * p; c < 16 * p + 16; c += 2) {
-                        const float2 t = ffma2(make_float2(__uint_as_float(xr[c]), __uint_as_float(xr[c + 1])), mul2, add2);
-                        const float2 e = make_float2(ex2(t.x), ex2(t.y));
-                        acc2 = fadd2(acc2, e);
-                        xr[c >> 1] = pack_f16x2(e.x, e.y);
+                        for (int c = 16 * p; c < 16 * p + 16; c += 2) {
+                            const float2 e = make_float2(ex2(fmaf(__uint_as_float(xr[c]), mul, add) - less + more),
+                                                         ex2(fmaf(__uint_as_float(xr[c + 1]), mul, add) - less + more));
+                            acc2 = fadd2(acc2, e);
+                            xr[c >> 1] = pack_f16x2(e.x, e.y);
+                        }
+                        rs = fmaf(acc2.x + acc2.y, f.z, rs);
                     }
-                    rs = fmaf(acc2.x + acc2.y, f.z, rs);
                 }
                 l = fmaf(l, alpha, rs);
                 // S_j(i) complete implies PV_j(i-1) complete (MMAs of one issuer retire in order), so O_j is

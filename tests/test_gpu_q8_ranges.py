@@ -281,3 +281,28 @@ def test_q8_v_scales_apart_in_other_steps(mode, split):
         assert att._equal((out[1:], lse[1:]), (want[0][1:], want[1][1:]))
         if not apart:
             assert (out[0, :8, -1] == 0).all() and torch.isnan(lse[0, :8, -1]).all()
+
+
+# ------------------------------------------------------------------- neighbours ----
+
+def test_prefill_q8_bits_do_not_depend_on_the_neighbours():
+    """A query beside queries with scores of any size (of its own row and KV head, in its tile) has
+    the bits that it has beside others, and in a chunk of its own."""
+    c = ref.case(141, [500, 300], 8, 2, Sq=64)
+    want = att._run(c)
+    big = {n: t.clone() for n, t in c.items()}
+    hit = [(b, h, s) for b in (0, 1) for h in (1, 6) for s in (3, 17, 40)]
+    for i, (b, h, s) in enumerate(hit):
+        big["q"][b, h, s] = (c["q"][b, h, s].double() * (1e7, 1e9, 2.0 ** 40)[i % 3]).to(torch.bfloat16)
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    out, lse = att._run(big, status=st)
+    assert int(st.item()) == 0
+    keep = torch.ones(c["q"].shape[:3], dtype=torch.bool)
+    for b, h, s in hit:
+        keep[b, h, s] = False
+    keep = keep.cuda()
+    assert torch.equal(out[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+    for lo, hi in ((0, 5), (5, 37), (37, 64)):
+        part = dict(big, q=big["q"][:, :, lo:hi].contiguous(), position_ids=big["position_ids"][:, lo:hi].contiguous())
+        o, l = att._run(part, mode="prefill")
+        assert torch.equal(o, out[:, :, lo:hi]) and torch.equal(l, lse[:, :, lo:hi])
