@@ -22,7 +22,7 @@
 // and the conversions take 40% of what they leave.  (An issuer to each q-tile: 538 us, as the
 // MMAs of the two then share the pipe and both chains grow; a maximum found along with the
 // exponentials and the tile done again where it rose: 500 us.)
-// S = 8192 of 32 heads: 472 us, tensor pipe 49% active; 4 chunks of 512 behind 1536: 73 us
+// S = 8192 of 32 heads: 474 us, tensor pipe 49% active; 4 chunks of 512 behind 1536: 72 us
 // (256 units on 152 CTAs: two units where 1.68 would be even); 33 queries: 22 us.
 // Roles (512 threads, registers rebalanced with setmaxnreg):
 //   warp 15      scheduler: each unit's metadata, published as a descriptor (two slots);
