@@ -18,6 +18,9 @@ Names mirror the C ABI in ``include/rk_paged.h``:
 ``tables_extend`` (rk_paged_tables_extend), ``kv_append_q8`` (rk_paged_kv_append_q8),
 ``decode_q8_scratch_bytes`` (rk_paged_decode_q8_scratch_bytes), ``attn_decode_q8``
 (rk_paged_attn_decode_q8), ``attn_prefill_q8`` (rk_paged_attn_prefill_q8),
+``tree_scratch_bytes`` (rk_paged_tree_scratch_bytes), ``attn_tree`` (rk_paged_attn_tree),
+``verify_tree`` (rk_paged_verify_tree), ``kv_compact`` (rk_paged_kv_compact),
+``tables_trim`` (rk_paged_tables_trim),
 ``last_error``, ``policy``, ``abi_version``.
 """
 from __future__ import annotations
@@ -36,7 +39,8 @@ ERRORS = {
 }
 CODES = {v: k for k, v in ERRORS.items()}
 STATUS_PAGE_OOB, STATUS_KVLEN, STATUS_POSITION, STATUS_TIMEOUT, STATUS_RANGE = 1, 2, 4, 8, 16
-STATUS_SCALE, STATUS_POOL = 32, 64
+STATUS_SCALE, STATUS_POOL, STATUS_TREE = 32, 64, 128
+TREE_MAX_NODES, TREE_UNUSED = 64, -2  # RK_PAGED_TREE_MAX_NODES, RK_PAGED_TREE_UNUSED
 ABI_VERSION = 3
 SPLIT_STATIC_SCRATCH_BYTES = 16 << 20  # RK_PAGED_SPLIT_STATIC_SCRATCH_BYTES
 BALANCED_SCRATCH_BYTES = 4096 + 512 * 3088 * 4  # RK_PAGED_BALANCED_SCRATCH_BYTES
@@ -125,6 +129,16 @@ def load(path: str | None = None):
             [ctypes.c_uint64, vp, vp]
         lib.rk_paged_attn_prefill_q8.restype = ctypes.c_int
         lib.rk_paged_attn_prefill_q8.argtypes = [ctypes.POINTER(Plan)] + [vp] * 12
+        lib.rk_paged_tree_scratch_bytes.restype = ctypes.c_int
+        lib.rk_paged_tree_scratch_bytes.argtypes = [ctypes.POINTER(Plan), ctypes.POINTER(ctypes.c_uint64)]
+        lib.rk_paged_attn_tree.restype = ctypes.c_int
+        lib.rk_paged_attn_tree.argtypes = [ctypes.POINTER(Plan)] + [vp] * 9 + [ctypes.c_uint64, vp, vp]
+        lib.rk_paged_verify_tree.restype = ctypes.c_int
+        lib.rk_paged_verify_tree.argtypes = [ctypes.POINTER(Plan), vp, ctypes.c_int32, ctypes.c_int32] + [vp] * 13
+        lib.rk_paged_kv_compact.restype = ctypes.c_int
+        lib.rk_paged_kv_compact.argtypes = [ctypes.POINTER(Plan)] + [vp] * 8
+        lib.rk_paged_tables_trim.restype = ctypes.c_int
+        lib.rk_paged_tables_trim.argtypes = [ctypes.POINTER(Plan), vp, vp, vp, ctypes.c_int32] + [vp] * 6
         lib.rk_last_error.restype = ctypes.c_char_p
         lib.rk_last_error.argtypes = []
         lib.rk_paged_policy.restype = ctypes.c_char_p
@@ -559,6 +573,80 @@ def attn_prefill_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table,
     """rk_paged_attn_prefill_q8 on device tensors: causal chunked prefill over the 8-bit cache."""
     ptr = _attn_q8(p, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse, status)
     _check(load().rk_paged_attn_prefill_q8(ctypes.byref(p), *ptr, _raw_stream(stream)))
+
+
+def tree_scratch_bytes(p: Plan) -> int:
+    """rk_paged_tree_scratch_bytes: device scratch bytes of the tree attention (0: none needed)."""
+    n = ctypes.c_uint64(0)
+    _check(load().rk_paged_tree_scratch_bytes(ctypes.byref(p), ctypes.byref(n)))
+    return int(n.value)
+
+
+def attn_tree(p: Plan, q, k_cache, v_cache, block_table, kv_lens, parents, out, lse, scratch=None, status=None,
+              stream=None):
+    """rk_paged_attn_tree on device tensors: attention of the ``p.Sq`` nodes of each row's
+    tree (``parents`` [B, Sq]; the nodes are the row's last tokens).  ``scratch`` is a CUDA
+    tensor of at least ``tree_scratch_bytes`` bytes (any dtype; None where that is 0)."""
+    ty, B, T = _types(), p.B, p.Sq
+    qs, cache = (B, p.Hq, T, p.D), (p.num_pages, p.page_size, p.Hkv, p.D)
+    ptr = _with_status([(q, ty.bf16, qs, "q"), (k_cache, ty.bf16, cache, "k_cache"), (v_cache, ty.bf16, cache, "v_cache"),
+                        (block_table, ty.i32, (B, p.W), "block_table"), (kv_lens, ty.i32, (B,), "kv_lens"),
+                        (parents, ty.i32, (B, T), "parents"), (out, ty.bf16, qs, "out"), (lse, ty.f32, qs[:3], "lse")], status)
+    sp, nbytes = None, 0
+    if scratch is not None:
+        sp = _pointers([(scratch, scratch.dtype, None, "scratch")])[0]
+        nbytes = scratch.numel() * scratch.element_size()
+    _check(load().rk_paged_attn_tree(ctypes.byref(p), *ptr[:8], sp, nbytes, ptr[8], _raw_stream(stream)))
+
+
+def verify_tree(p: Plan, logits, draft_tokens, parents, coins, race, temperature, n_accepted, n_drop, path, tokens,
+                logprobs, draft_probs=None, status=None, stream=None):
+    """rk_paged_verify_tree on device tensors: ``logits`` bfloat16 or float32 [B, Sq, V], ``draft_probs``
+    float32 [B, Sq, V] or None, ``race`` float32 [B, V], ``coins`` float32 [B, Sq], ``temperature`` float32 [B];
+    the results n_accepted, n_drop (int32 [B]), path, tokens (int32 [B, Sq]) and logprobs (float32 [B, Sq])."""
+    ty, B, T = _types(), p.B, p.Sq
+    if logits.dtype is not ty.bf16 and logits.dtype is not ty.f32:
+        raise TypeError("logits must be torch.bfloat16 or torch.float32 (got %s)" % logits.dtype)
+    if logits.dim() != 3:
+        raise ValueError("logits must have three dimensions")
+    V = logits.shape[2]
+    entries = [(logits, logits.dtype, (B, T, V), "logits"), (draft_tokens, ty.i32, (B, T), "draft_tokens"),
+               (parents, ty.i32, (B, T), "parents"), (coins, ty.f32, (B, T), "coins"), (race, ty.f32, (B, V), "race"),
+               (temperature, ty.f32, (B,), "temperature"), (n_accepted, ty.i32, (B,), "n_accepted"),
+               (n_drop, ty.i32, (B,), "n_drop"), (path, ty.i32, (B, T), "path"), (tokens, ty.i32, (B, T), "tokens"),
+               (logprobs, ty.f32, (B, T), "logprobs")]
+    if draft_probs is not None:
+        entries.insert(1, (draft_probs, ty.f32, (B, T, V), "draft_probs"))
+    ptr = _with_status(entries, status)
+    if draft_probs is None:
+        ptr.insert(1, None)
+    _check(load().rk_paged_verify_tree(ctypes.byref(p), ptr[0], 1 if logits.dtype is ty.f32 else 0, V, *ptr[1:],
+                                       _raw_stream(stream)))
+
+
+def kv_compact(p: Plan, path, n_keep, block_table, kv_lens, k_cache, v_cache, status=None, stream=None):
+    """rk_paged_kv_compact: K and V of the nodes ``path`` [B, Sq], the first ``n_keep`` [B] of them,
+    to the slots behind each row's prefix, in place (``kv_lens`` with the Sq nodes)."""
+    ty, B = _types(), p.B
+    cache = (p.num_pages, p.page_size, p.Hkv, p.D)
+    ptr = _with_status([(path, ty.i32, (B, p.Sq), "path"), (n_keep, ty.i32, (B,), "n_keep"),
+                        (block_table, ty.i32, (B, p.W), "block_table"), (kv_lens, ty.i32, (B,), "kv_lens"),
+                        (k_cache, ty.bf16, cache, "k_cache"), (v_cache, ty.bf16, cache, "v_cache")], status)
+    _check(load().rk_paged_kv_compact(ctypes.byref(p), *ptr, _raw_stream(stream)))
+
+
+def tables_trim(p: Plan, n_drop, kv_lens, pool, taken, block_table, kv_lens_out, taken_out, status=None, stream=None):
+    """rk_paged_tables_trim, the inverse of ``tables_extend``: each row's last ``n_drop`` [B] tokens leave
+    its length, and the pages that this empties leave ``block_table`` [B, W] for ``pool``, in place.
+    ``kv_lens_out`` and ``taken_out`` may be ``kv_lens`` and ``taken``.  All int32."""
+    i32, B = _types().i32, p.B
+    if pool.dim() != 1:
+        raise ValueError("pool must have one dimension")
+    ptr = _with_status([(n_drop, i32, (B,), "n_drop"), (kv_lens, i32, (B,), "kv_lens"), (pool, i32, None, "pool"),
+                        (taken, i32, (1,), "taken"), (block_table, i32, (B, p.W), "block_table"),
+                        (kv_lens_out, i32, (B,), "kv_lens_out"), (taken_out, i32, (1,), "taken_out")], status)
+    _check(load().rk_paged_tables_trim(ctypes.byref(p), ptr[0], ptr[1], ptr[2], pool.shape[0], *ptr[3:],
+                                       _raw_stream(stream)))
 
 
 def run(mode: str, q, k_cache, v_cache, block_table, kv_lens, position_ids, plan_obj=None,

@@ -17,6 +17,7 @@
 
 #include "q8_args.h"
 #include "rk_paged.h"
+#include "tree_args.h"
 
 namespace rk {
 cudaError_t launch_decode(const CUtensorMap& vm, const DecodeArgs& a, cudaStream_t stream);
@@ -34,6 +35,10 @@ cudaError_t launch_append_q8(const AppendQ8Args& a, cudaStream_t stream);
 int decode_q8_bundle(int Hkv);
 cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream);
 cudaError_t launch_prefill_q8(const AttnQ8Args& a, cudaStream_t stream);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_compact(const CompactArgs& a, cudaStream_t stream);
+cudaError_t launch_trim(const TrimArgs& a, cudaStream_t stream);
 }  // namespace rk
 
 namespace {
@@ -1157,6 +1162,185 @@ int rk_paged_attn_prefill_q8(const rk_paged_plan_t* plan, const void* q, const v
     if (rc || plan->B == 0) return rc;
     cudaError_t e = rk::launch_prefill_q8(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(RK_E_CUDA, "8-bit prefill launch: %s", cudaGetErrorString(e));
+    return RK_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------- speculative step ----
+
+namespace {
+
+static_assert(rk::TREE_MAX == RK_PAGED_TREE_MAX_NODES && rk::TREE_UNUSED == RK_PAGED_TREE_UNUSED, "tree constants");
+
+int check_tree_plan(const rk_paged_plan_t* plan) {
+    const int rc = check_plan(plan);
+    if (rc) return rc;
+    if (plan->Sq > RK_PAGED_TREE_MAX_NODES)
+        return fail(RK_E_UNSUPPORTED, "trees of %d nodes: at most %d are supported", plan->Sq, RK_PAGED_TREE_MAX_NODES);
+    return RK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int rk_paged_tree_scratch_bytes(const rk_paged_plan_t* plan, uint64_t* bytes) {
+    g_err.clear();
+    if (!bytes) return fail(RK_E_ARG, "bytes is NULL");
+    int rc = check_tree_plan(plan);
+    if (rc) return rc;
+    *bytes = 0;
+    return RK_OK;
+}
+
+int rk_paged_attn_tree(const rk_paged_plan_t* plan, const void* q, const void* k_cache, const void* v_cache,
+                       const int32_t* block_table_d, const int32_t* kv_lens_d, const int32_t* parents_d, void* out,
+                       float* lse, void* scratch, uint64_t scratch_bytes, int32_t* status_d, rk_stream_t stream) {
+    g_err.clear();
+    int rc = check_tree_plan(plan);
+    if (rc) return rc;
+    if (!aligned(status_d, 4)) return fail(RK_E_ARG, "status must be 4-byte aligned");
+    if ((rc = check_launch_common(plan, q, k_cache, v_cache, block_table_d, kv_lens_d, parents_d, out, lse))) return rc;
+    if (plan->B == 0) return RK_OK;
+    rk::TreeArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.block_table = block_table_d;
+    a.kv_lens = kv_lens_d;
+    a.parents = parents_d;
+    a.out = out;
+    a.lse = lse;
+    a.status = status_d;
+    a.B = plan->B;
+    a.T = plan->Sq;
+    a.Hq = plan->Hq;
+    a.Hkv = plan->Hkv;
+    a.G = plan->Hq / plan->Hkv;
+    a.W = plan->W;
+    a.num_pages = plan->num_pages;
+    a.qk_scale_log2 = (float)((1.0 / std::sqrt((double)plan->D)) * 1.4426950408889634074);
+    a.wait_limit_ns = plan->wait_limit_ns;
+    a.timeout_drill = plan->timeout_drill;
+    std::memcpy(a.rope_turns, plan->rope_turns, sizeof a.rope_turns);
+    cudaError_t e = rk::launch_tree(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(RK_E_CUDA, "tree attention launch: %s", cudaGetErrorString(e));
+    return RK_OK;
+}
+
+int rk_paged_verify_tree(const rk_paged_plan_t* plan, const void* logits, int32_t logits_type, int32_t V,
+                         const float* draft_probs, const int32_t* draft_tokens_d, const int32_t* parents_d,
+                         const float* coins_d, const float* race_d, const float* temperature_d, int32_t* n_accepted_d,
+                         int32_t* n_drop_d, int32_t* path_d, int32_t* tokens_d, float* logprobs_d, int32_t* status_d,
+                         rk_stream_t stream) {
+    g_err.clear();
+    int rc = check_tree_plan(plan);
+    if (rc) return rc;
+    if (logits_type != RK_LOGITS_BF16 && logits_type != RK_LOGITS_F32)
+        return fail(RK_E_ARG, "logits_type %d is neither RK_LOGITS_BF16 nor RK_LOGITS_F32", logits_type);
+    if (V < 1) return fail(RK_E_ARG, "V must be positive (got %d)", V);
+    if (plan->B == 0) return RK_OK;
+    if (!logits || !draft_tokens_d || !parents_d || !coins_d || !race_d || !temperature_d || !n_accepted_d || !n_drop_d ||
+        !path_d || !tokens_d || !logprobs_d)
+        return fail(RK_E_ARG, "null device pointer");
+    const void* all[] = {draft_probs, draft_tokens_d, parents_d, coins_d,  race_d,     temperature_d,
+                         n_accepted_d, n_drop_d,      path_d,    tokens_d, logprobs_d, status_d};
+    for (const void* p : all)
+        if (!aligned(p, 4)) return fail(RK_E_ARG, "every array must be 4-byte aligned");
+    if (!aligned(logits, logits_type == RK_LOGITS_F32 ? 4 : 2)) return fail(RK_E_ARG, "logits are not aligned to their type");
+    if ((rc = check_device())) return rc;
+    rk::VerifyArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.logits = logits;
+    a.draft_probs = draft_probs;
+    a.draft_tokens = draft_tokens_d;
+    a.parents = parents_d;
+    a.coins = coins_d;
+    a.race = race_d;
+    a.temperature = temperature_d;
+    a.n_accepted = n_accepted_d;
+    a.n_drop = n_drop_d;
+    a.path = path_d;
+    a.tokens = tokens_d;
+    a.logprobs = logprobs_d;
+    a.status = status_d;
+    a.B = plan->B;
+    a.T = plan->Sq;
+    a.V = V;
+    a.f32 = logits_type == RK_LOGITS_F32;
+    cudaError_t e = rk::launch_verify(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(RK_E_CUDA, "verification launch: %s", cudaGetErrorString(e));
+    return RK_OK;
+}
+
+int rk_paged_kv_compact(const rk_paged_plan_t* plan, const int32_t* path_d, const int32_t* n_keep_d,
+                        const int32_t* block_table_d, const int32_t* kv_lens_d, void* k_cache, void* v_cache,
+                        int32_t* status_d, rk_stream_t stream) {
+    g_err.clear();
+    int rc = check_tree_plan(plan);
+    if (rc) return rc;
+    if (plan->B == 0) return RK_OK;
+    if (plan->num_pages == 0 || plan->W == 0) return fail(RK_E_KVLEN, "moving tokens needs a table and a page pool");
+    if (!path_d || !n_keep_d || !block_table_d || !kv_lens_d || !k_cache || !v_cache)
+        return fail(RK_E_ARG, "null device pointer");
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(RK_E_ARG, "k_cache and v_cache must be 16-byte aligned");
+    if (!aligned(path_d, 4) || !aligned(n_keep_d, 4) || !aligned(block_table_d, 4) || !aligned(kv_lens_d, 4) ||
+        !aligned(status_d, 4))
+        return fail(RK_E_ARG, "metadata must be 4-byte aligned");
+    if ((rc = check_device())) return rc;
+    rk::CompactArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.path = path_d;
+    a.n_keep = n_keep_d;
+    a.block_table = block_table_d;
+    a.kv_lens = kv_lens_d;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.status = status_d;
+    a.B = plan->B;
+    a.T = plan->Sq;
+    a.Hkv = plan->Hkv;
+    a.W = plan->W;
+    a.num_pages = plan->num_pages;
+    cudaError_t e = rk::launch_kv_compact(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(RK_E_CUDA, "compaction launch: %s", cudaGetErrorString(e));
+    return RK_OK;
+}
+
+int rk_paged_tables_trim(const rk_paged_plan_t* plan, const int32_t* n_drop_d, const int32_t* kv_lens_d, int32_t* pool_d,
+                         int32_t n_pool, const int32_t* taken_d, int32_t* block_table_d, int32_t* kv_lens_out_d,
+                         int32_t* taken_out_d, int32_t* status_d, rk_stream_t stream) {
+    g_err.clear();
+    int rc = check_plan(plan);
+    if (rc) return rc;
+    if (n_pool < 0) return fail(RK_E_ARG, "n_pool must be >= 0 (got %d)", n_pool);
+    if (plan->B > rk::TAB_MAX_ROWS)
+        return fail(RK_E_UNSUPPORTED, "%d rows: at most %d are supported", plan->B, rk::TAB_MAX_ROWS);
+    if (!taken_d || !taken_out_d || (n_pool > 0 && !pool_d) ||
+        (plan->B > 0 && (!n_drop_d || !kv_lens_d || !kv_lens_out_d || (plan->W > 0 && !block_table_d))))
+        return fail(RK_E_ARG, "null device pointer");
+    const void* all[] = {n_drop_d, kv_lens_d, pool_d, taken_d, block_table_d, kv_lens_out_d, taken_out_d, status_d};
+    for (const void* p : all)
+        if (!aligned(p, 4)) return fail(RK_E_ARG, "every array must be 4-byte aligned");
+    if ((rc = check_device())) return rc;
+    rk::TrimArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.n_drop = n_drop_d;
+    a.kv_lens = kv_lens_d;
+    a.pool = pool_d;
+    a.taken = taken_d;
+    a.block_table = block_table_d;
+    a.kv_lens_out = kv_lens_out_d;
+    a.taken_out = taken_out_d;
+    a.status = status_d;
+    a.B = plan->B;
+    a.W = plan->W;
+    a.num_pages = plan->num_pages;
+    a.n_pool = n_pool;
+    cudaError_t e = rk::launch_trim(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(RK_E_CUDA, "trim launch: %s", cudaGetErrorString(e));
     return RK_OK;
 }
 

@@ -21,6 +21,7 @@
 
 #include "q8_args.h"
 #include "rk_device.cuh"
+#include "tree_args.h"
 
 namespace rk {
 
@@ -238,7 +239,118 @@ __global__ void __launch_bounds__(TAB_THREADS) tokens_kernel(const __grid_consta
     if (bad && a.status) atomicOr(a.status, bad);
 }
 
+// ---- the inverse: tokens leave the rows' ends, emptied pages go back to the pool ----
+//
+// One prefix sum over the rows, of the pages that come free; then each freed page finds its
+// row by bisection and moves to its place.  The CTAs of a launch are one cluster: each sums the
+// rows for itself and moves a share of the pages, and when all have read the lengths and taken,
+// the first writes the new ones (which may be the same arrays).
+__global__ void __launch_bounds__(TAB_THREADS) trim_kernel(const __grid_constant__ TrimArgs a) {
+    extern __shared__ int32_t rows[];
+    __shared__ long long sh[64];
+    int32_t* s_first = rows;        // a row's first freed page, counted over the batch
+    int32_t* s_left = rows + a.B;   // the pages that it keeps
+    int32_t* s_len = rows + 2 * a.B;  // its length after the drop
+    const int tid = threadIdx.x, ctas = (int)gridDim.x, cta = (int)blockIdx.x;
+    const int per = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;
+    const int r0 = min(a.B, tid * per), r1 = min(a.B, r0 + per);
+    const int taken = *a.taken;
+    const bool taken_ok = taken >= 0 && taken <= a.n_pool;
+    const long long room = taken_ok ? taken : 0;
+    int bad = taken_ok ? 0 : RK_STATUS_POOL;
+    // a row's length after the drop, or -1 where it is refused for its own numbers
+    auto after = [&](int r, int& len) {
+        len = a.kv_lens[r];
+        const int d = a.n_drop[r];
+        return (len < 0 || len > (long long)a.W * PAGE || d < 0 || d > len) ? -1 : len - d;
+    };
+    long long pg = 0, none = 0, all, t0;
+    for (int r = r0; r < r1; ++r) {
+        int len;
+        const int n = after(r, len);
+        s_left[r] = n;
+        if (n < 0) bad |= RK_STATUS_KVLEN;
+        else pg += pages_of(len) - pages_of(n);
+    }
+    scan2(none, pg, &t0, &all, sh);
+    if (all > room) {  // the same verdict in every thread: rows whose pages pass what was handed out are refused
+        long long run = pg;
+        pg = 0;
+        for (int r = r0; r < r1; ++r) {
+            if (s_left[r] < 0) continue;
+            const int need = pages_of(a.kv_lens[r]) - pages_of(s_left[r]);
+            run += need;
+            if (need > 0 && run > room) {
+                bad |= RK_STATUS_POOL;
+                s_left[r] = -1;
+            } else {
+                pg += need;
+            }
+        }
+        none = 0;
+        scan2(none, pg, &t0, &all, sh);
+    }
+    for (int r = r0; r < r1; ++r) {
+        const int n = s_left[r], len = a.kv_lens[r];
+        s_first[r] = (int)pg;
+        s_left[r] = n < 0 ? 0 : pages_of(n);
+        s_len[r] = n < 0 ? len : n;
+        if (n >= 0) pg += pages_of(len) - pages_of(n);
+    }
+    __syncthreads();
+    const int total = (int)all, base = taken - total;
+    for (int i = cta * (int)blockDim.x + tid; i < total; i += ctas * (int)blockDim.x) {
+        int lo = 0, hi = a.B;  // the last row that starts at or before page i (rows that free none share a start)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_first[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        int32_t* e = a.block_table + (size_t)lo * a.W + s_left[lo] + (i - s_first[lo]);
+        const int page = *e;
+        if (page < 0 || page >= a.num_pages) bad |= RK_STATUS_PAGE_OOB;
+        a.pool[base + i] = page;
+        *e = -1;
+    }
+    __syncthreads();
+    if (ctas > 1)  // every CTA has read the lengths and taken
+        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    if (cta == 0) {
+        for (int r = tid; r < a.B; r += (int)blockDim.x) a.kv_lens_out[r] = s_len[r];
+        if (tid == 0) *a.taken_out = taken - total;
+    }
+    // a status bit is one row's or one page's; the rows' are the same in every CTA
+    if (bad && a.status) atomicOr(a.status, bad);
+}
+
 }  // namespace
+
+cudaError_t launch_trim(const TrimArgs& a, cudaStream_t stream) {
+    const int smem = 3 * a.B * 4;
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
+    if (!bit || !(configured.load() & bit)) {
+        e = cudaFuncSetAttribute(trim_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * TAB_MAX_ROWS * 4);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit);
+    }
+    const bool small = (long long)a.B * a.W <= 4 * TAB_THREADS;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(small ? 1 : 8);
+    cfg.blockDim = dim3(small && a.B <= 128 ? 128 : TAB_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = small ? 1 : 8;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, trim_kernel, a);
+}
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {
     const int smem = 3 * a.B * 4;

@@ -85,7 +85,9 @@ enum rk_status {
                                        8-bit cache calls: see there */
 #define RK_STATUS_SCALE (1 << 5)   /* a scale of the 8-bit cache that is not a positive normal number (append:
                                        not a power of two in [2^-64, 2^56]) */
-#define RK_STATUS_POOL (1 << 6)    /* rk_paged_tables_extend: a row's tokens or new pages do not fit */
+#define RK_STATUS_POOL (1 << 6)    /* rk_paged_tables_extend: a row's tokens or new pages do not fit;
+                                      rk_paged_tables_trim: more pages come back than were handed out */
+#define RK_STATUS_TREE (1 << 7)    /* speculative step: a parent, path or drafted token that is none */
 
 /* Opaque stream handle; identical to cudaStream_t / CUstream. */
 typedef struct CUstream_st *rk_stream_t;
@@ -601,6 +603,147 @@ int rk_paged_attn_prefill_q8(const rk_paged_plan_t *plan, const void *q, const v
                              const int32_t *block_table_d, const int32_t *kv_lens_d,
                              const int32_t *position_ids_d, void *out, float *lse, int32_t *status_d,
                              rk_stream_t stream);
+
+/*
+ * The speculative step: a tree of T drafted tokens behind every row of the BF16
+ * cache, judged by the model in one pass, of which one path is kept.  In the order
+ * of a step:
+ *
+ *   rk_paged_tables_extend   pages for the T nodes of every row (n_new = T)
+ *   rk_paged_kv_append       a layer's K and V of the nodes, in their order
+ *   rk_paged_attn_tree       that layer's attention
+ *   rk_paged_verify_tree     which nodes are accepted, and the token behind them
+ *   rk_paged_kv_compact      a layer's accepted K and V to the slots behind the prefix
+ *   rk_paged_tables_trim     the dropped tokens' lengths and pages
+ *
+ * Everything is read on the device, so a captured step can be replayed.  K is pre-RoPE
+ * in this cache, so a node that moves to another slot keeps its bits, and the cache after
+ * a step is bit for bit what one token after the other would have left.
+ *
+ * Semantics shared by the calls (B, Hq, Hkv, D, W, num_pages from the plan; plan->Sq = T,
+ * at most RK_PAGED_TREE_MAX_NODES, else RK_E_UNSUPPORTED):
+ *   parents_d    int32 [B, T]: the node before node n that it follows (0 .. n - 1), -1 for
+ *                a root, RK_PAGED_TREE_UNUSED where the row has no node n.  Several children
+ *                of a node and several roots are fine; a node that follows an unused one is not.
+ *   Row b's node n lies in slot prefix + n with prefix = kv_lens_d[b] - T, and stands at
+ *   position prefix + depth(n); a root's depth is 0.  A row of kv_len 0 has no nodes.
+ * A row whose parents are not as above fails with RK_STATUS_TREE.
+ */
+#define RK_PAGED_TREE_MAX_NODES 64
+#define RK_PAGED_TREE_UNUSED (-2)
+
+/*
+ * rk_paged_attn_tree -- attention of the nodes: node n sees the prefix (keys 0 ..
+ * prefix - 1), its ancestors and itself.  For a chain this is rk_paged_attn_prefill's
+ * visibility.
+ *   q, out        bf16 [B, Hq, T, D], lse fp32 [B, Hq, T], caches, block_table_d: as in
+ *                rk_paged_attn_prefill
+ *   kv_lens_d     int32 [B], the nodes included
+ *   scratch       DEVICE, 16-byte aligned, at least rk_paged_tree_scratch_bytes bytes;
+ *                nothing in it needs initialising; may be NULL where that is 0.  Two calls
+ *                in flight at once must not share it (two captured graphs that may run at once
+ *                included).
+ * A row's keys are cut at fixed offsets, the parts are reduced apart and merged in FP32 in
+ * ascending order (the policy of rk_paged_attn_decode_split), so a row's result depends on
+ * its own length, tree and data, and not on the batch, the table's width or the grid.
+ * Unused nodes and rows of kv_len 0 get out = 0, lse = -inf; K and V of unused nodes and of
+ * slots past kv_len may be anything.
+ * Status and failed rows (out = 0, lse = NaN): RK_STATUS_KVLEN (kv_len outside [0, W * 16], or
+ * below T and not 0), RK_STATUS_PAGE_OOB, RK_STATUS_TREE fail the row.  RK_STATUS_RANGE: q or
+ * k elements of 2^15 or more, or NaN, fail the queries that they are of or that see them (the
+ * FP16 score operands of the other BF16 calls), and so does an element of a node's V that is
+ * not finite; no other query does.
+ * Errors: as rk_paged_attn_prefill, RK_E_ARG for a missing, small or misaligned scratch.
+ */
+int rk_paged_tree_scratch_bytes(const rk_paged_plan_t *plan, uint64_t *bytes);
+int rk_paged_attn_tree(const rk_paged_plan_t *plan, const void *q, const void *k_cache, const void *v_cache,
+                       const int32_t *block_table_d, const int32_t *kv_lens_d, const int32_t *parents_d, void *out,
+                       float *lse, void *scratch, uint64_t scratch_bytes, int32_t *status_d, rk_stream_t stream);
+
+/*
+ * rk_paged_verify_tree -- walk down each row's tree and keep what the target's
+ * distribution accepts, from given random numbers.
+ *   logits        [B, T, V] bf16 (logits_type RK_LOGITS_BF16) or fp32 (RK_LOGITS_F32): the
+ *                target's logits behind each node; -inf is a token of probability 0
+ *   draft_probs   fp32 [B, T, V] or NULL: the distribution that node n's children were drawn
+ *                from, independently of one another; NULL: the drafts were not drawn at random
+ *   draft_tokens_d  int32 [B, T]: the nodes' tokens, in [0, V) (node 0's is not read)
+ *   coins_d       fp32 [B, T]: uniform on [0, 1), one for each node's test
+ *   race_d        fp32 [B, V]: draws of the exponential distribution (mean 1), for the last token
+ *   temperature_d fp32 [B]: logits are divided by it; 0: greedy
+ * Node 0 is the root that the walk begins with (parent -1: the token before the drafted ones);
+ * other roots are never reached.  At a node with p = softmax(logits / temperature) and q =
+ * draft_probs behind it the children are tried in ascending order; r starts as p.  Child c with
+ * token x is accepted if coin[c] * q(x) * sum(r) < r(x), and the walk goes on there; otherwise
+ * r := max(r - sum(r) q, 0) (drafts without probabilities: q(x) counts as 1, and r(x) := 0).
+ * When no child is left the last token is the largest r(v) / race[v] (the lowest v of equal ones;
+ * p's where nothing of r is left), which draws it from r.  The tokens are then distributed as p
+ * says, whatever was drafted.  Greedy: a child is accepted if its token is the largest logit
+ * (the lowest of equal ones), which is also the last token.
+ *   n_accepted_d  int32 [B]: nodes of the path, the root included; 0 for a row without one
+ *   n_drop_d      int32 [B]: T - n_accepted (kv_len 0 is not known here: a row without a root
+ *                drops none)
+ *   path_d        int32 [B, T]: the path's nodes, ascending; -1 behind them
+ *   tokens_d      int32 [B, T]: the path's tokens behind the root, then the last token: n_accepted
+ *                of them; -1 behind
+ *   logprobs_d    fp32 [B, T]: ln p of those tokens (temperature 0: with 1); 0 behind
+ * Status: RK_STATUS_TREE (parents, a used node's token outside [0, V)), RK_STATUS_RANGE (a
+ * temperature that is negative, not finite or below 2^-64; at a node that the walk reaches, logits
+ * that are NaN, +inf or all -inf; draft probabilities that are NaN or not finite, where they are read): the row keeps
+ * nothing: n_accepted 0, n_drop T, tokens and path -1, logprobs NaN.
+ * A row whose node 0 is unused gives n_accepted 0, n_drop 0 without a status.
+ * Sums are FP32 in an order that V alone fixes: a row's results do not depend on the batch.
+ * Plan: B, Sq.  One launch, no allocation, no host synchronisation.  Errors: RK_E_ARG (V < 1,
+ * logits_type, null or misaligned pointer: 2 or 4 bytes), RK_E_UNSUPPORTED (T), RK_E_DEVICE, RK_E_CUDA.
+ */
+#define RK_LOGITS_BF16 0
+#define RK_LOGITS_F32 1
+int rk_paged_verify_tree(const rk_paged_plan_t *plan, const void *logits, int32_t logits_type, int32_t V,
+                         const float *draft_probs, const int32_t *draft_tokens_d, const int32_t *parents_d,
+                         const float *coins_d, const float *race_d, const float *temperature_d, int32_t *n_accepted_d,
+                         int32_t *n_drop_d, int32_t *path_d, int32_t *tokens_d, float *logprobs_d, int32_t *status_d,
+                         rk_stream_t stream);
+
+/*
+ * rk_paged_kv_compact -- K and V of the nodes path_d[b, i], i < n_keep_d[b], to the slots
+ * prefix + i, in place.
+ *   path_d        int32 [B, T], strictly ascending in [0, T) up to n_keep (the rest is not read)
+ *   n_keep_d      int32 [B], 0 .. T
+ *   kv_lens_d     int32 [B], the nodes included
+ * Other slots keep what they hold.  A row without nodes to keep is left alone, and so is one
+ * that is refused: RK_STATUS_TREE (path or n_keep), RK_STATUS_KVLEN (kv_len outside [T, W * 16]),
+ * RK_STATUS_PAGE_OOB (a page of its nodes).  Rows that share a page of their nodes give unspecified
+ * values on it.  One launch, no allocation, no host synchronisation.  Errors: RK_E_ARG (null or
+ * misaligned pointer), RK_E_UNSUPPORTED (T), RK_E_KVLEN (rows but an empty table or pool), RK_E_DEVICE,
+ * RK_E_CUDA.
+ */
+int rk_paged_kv_compact(const rk_paged_plan_t *plan, const int32_t *path_d, const int32_t *n_keep_d,
+                        const int32_t *block_table_d, const int32_t *kv_lens_d, void *k_cache, void *v_cache,
+                        int32_t *status_d, rk_stream_t stream);
+
+/*
+ * rk_paged_tables_trim -- the inverse of rk_paged_tables_extend: every row gives up
+ * the last n_drop_d[b] of its tokens, and the pages that hold none any more go back to
+ * the pool.  For either cache; a row that drops its whole length is freed.
+ *   n_drop_d      int32 [B], 0 .. kv_len
+ *   kv_lens_d     int32 [B], before the drop
+ *   pool_d        int32 [n_pool], written in place: the F freed ids take the places taken - F ..
+ *                taken - 1, row after row and page after page, so that rows which drop what an extend
+ *                gave them leave the pool as it was before that
+ *   taken_d       int32 [1]: how many are handed out; taken_out_d: that less F
+ *   block_table_d int32 [B, W], in place: the freed entries become -1, no other is touched
+ *   kv_lens_out_d int32 [B] (it and taken_out_d may be the array that they follow)
+ * The other arrays must not overlap each other.  A row stays as it was, and the status word says why, if its
+ * length is negative or passes W * 16 or its n_drop is not in [0, kv_len] (RK_STATUS_KVLEN), if a
+ * page id that it would free is outside [0, num_pages) (RK_STATUS_PAGE_OOB), or if the pages of the rows
+ * up to it (rows without a place left out) are more than taken while it frees one (RK_STATUS_POOL; also
+ * taken outside [0, n_pool], which leaves no place).
+ * Plan: B, W, num_pages (B at most 16384, else RK_E_UNSUPPORTED).  No allocation, no host synchronisation.
+ * Errors: RK_E_ARG (null or misaligned pointer, negative n_pool), RK_E_DEVICE, RK_E_CUDA.
+ */
+int rk_paged_tables_trim(const rk_paged_plan_t *plan, const int32_t *n_drop_d, const int32_t *kv_lens_d, int32_t *pool_d,
+                         int32_t n_pool, const int32_t *taken_d, int32_t *block_table_d, int32_t *kv_lens_out_d,
+                         int32_t *taken_out_d, int32_t *status_d, rk_stream_t stream);
 
 /* Message of the last failing call on this thread ("" if none).  The
  * pointer stays valid until the next library call on the same thread. */
