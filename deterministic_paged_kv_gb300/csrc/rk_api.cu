@@ -35,7 +35,7 @@ cudaError_t launch_append_q8(const AppendQ8Args& a, cudaStream_t stream);
 int decode_q8_bundle(int Hkv);
 cudaError_t launch_decode_q8(const CUtensorMap& km, const CUtensorMap& vm, const AttnQ8Args& a, cudaStream_t stream);
 cudaError_t launch_prefill_q8(const AttnQ8Args& a, cudaStream_t stream);
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+cudaError_t launch_tree(const CUtensorMap& km, const CUtensorMap& vm, const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_compact(const CompactArgs& a, cudaStream_t stream);
 cudaError_t launch_trim(const TrimArgs& a, cudaStream_t stream);
@@ -1181,6 +1181,24 @@ int check_tree_plan(const rk_paged_plan_t* plan) {
     return RK_OK;
 }
 
+// Where a row's prefix is cut, and the scratch for the parts of the widest row: none where the table holds
+// one part.  Tiles of a call are counted in 32 bits.
+int tree_parts(const rk_paged_plan_t* plan, rk::TreeArgs* a, uint64_t* bytes) {
+    a->zone[0] = {0, 0, 512};
+    a->zone[1] = {32, 16384, 1024};
+    const int64_t cap = (int64_t)plan->W * rk::PAGE;
+    const int z = cap > a->zone[1].token;
+    const int64_t parts = cap > 0 ? a->zone[z].split + (cap - a->zone[z].token + a->zone[z].size - 1) / a->zone[z].size : 1;
+    const int64_t R = (int64_t)plan->Sq * (plan->Hq / plan->Hkv), pairs = (R + 255) / 256;
+    if ((double)plan->B * plan->Hkv * pairs * ((double)cap / 128 + 2) > 2147483647.0 ||
+        (double)plan->B * plan->Hkv * parts * R > 2147483647.0)
+        return fail(RK_E_UNSUPPORTED, "B %d x Hkv %d x W %d: too many", plan->B, plan->Hkv, plan->W);
+    a->n_splits = (int32_t)parts;
+    a->Rp = (int32_t)((R + 7) & ~7);
+    *bytes = parts > 1 ? (uint64_t)plan->B * plan->Hkv * parts * a->Rp * (rk::HEAD_DIM + 1) * 4 : 0;
+    return RK_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1190,8 +1208,8 @@ int rk_paged_tree_scratch_bytes(const rk_paged_plan_t* plan, uint64_t* bytes) {
     if (!bytes) return fail(RK_E_ARG, "bytes is NULL");
     int rc = check_tree_plan(plan);
     if (rc) return rc;
-    *bytes = 0;
-    return RK_OK;
+    rk::TreeArgs a;
+    return tree_parts(plan, &a, bytes);
 }
 
 int rk_paged_attn_tree(const rk_paged_plan_t* plan, const void* q, const void* k_cache, const void* v_cache,
@@ -1201,13 +1219,22 @@ int rk_paged_attn_tree(const rk_paged_plan_t* plan, const void* q, const void* k
     int rc = check_tree_plan(plan);
     if (rc) return rc;
     if (!aligned(status_d, 4)) return fail(RK_E_ARG, "status must be 4-byte aligned");
-    if ((rc = check_launch_common(plan, q, k_cache, v_cache, block_table_d, kv_lens_d, parents_d, out, lse))) return rc;
-    if (plan->B == 0) return RK_OK;
     rk::TreeArgs a;
     std::memset(&a, 0, sizeof a);
+    uint64_t need;
+    if ((rc = tree_parts(plan, &a, &need))) return rc;
+    if (need > 0 && plan->B > 0) {
+        if (!scratch || !aligned(scratch, 16))
+            return fail(RK_E_ARG, "tree attention scratch must be a non-null 16-byte aligned device pointer");
+        if (need > scratch_bytes)
+            return fail(RK_E_ARG, "tree attention scratch too small: %llu bytes needed, %llu given", (unsigned long long)need,
+                        (unsigned long long)scratch_bytes);
+    }
+    if ((rc = check_launch_common(plan, q, k_cache, v_cache, block_table_d, kv_lens_d, parents_d, out, lse))) return rc;
+    if (plan->B == 0) return RK_OK;
     a.q = q;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
+    a.o_part = static_cast<float*>(scratch);
+    if (need > 0) a.lse_part = a.o_part + (int64_t)plan->B * plan->Hkv * a.n_splits * a.Rp * rk::HEAD_DIM;
     a.block_table = block_table_d;
     a.kv_lens = kv_lens_d;
     a.parents = parents_d;
@@ -1225,7 +1252,13 @@ int rk_paged_attn_tree(const rk_paged_plan_t* plan, const void* q, const void* k
     a.wait_limit_ns = plan->wait_limit_ns;
     a.timeout_drill = plan->timeout_drill;
     std::memcpy(a.rope_turns, plan->rope_turns, sizeof a.rope_turns);
-    cudaError_t e = rk::launch_tree(a, reinterpret_cast<cudaStream_t>(stream));
+    const bool have = plan->num_pages > 0;  // without a pool no row has a page to read
+    CUtensorMap km, vm;
+    if ((rc = make_cache_map(&km, have ? k_cache : q, have ? plan->num_pages : 1, have ? plan->Hkv : 1, 64,
+                             CU_TENSOR_MAP_SWIZZLE_128B, "k_cache")))
+        return rc;
+    if ((rc = make_page_map(&vm, have ? v_cache : q, have ? plan->num_pages : 1, have ? plan->Hkv : 1, "v_cache"))) return rc;
+    cudaError_t e = rk::launch_tree(km, vm, a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(RK_E_CUDA, "tree attention launch: %s", cudaGetErrorString(e));
     return RK_OK;
 }

@@ -12,8 +12,6 @@ constexpr int TREE_UNUSED = -2;    // parent of a node that the row does not hav
 // Attention of the T nodes behind each row's prefix.
 struct TreeArgs {
     const void* q;                // bf16 [B, Hq, T, D], pre-RoPE
-    const void* k_cache;          // bf16 [num_pages, 16, Hkv, D]
-    const void* v_cache;
     const int32_t* block_table;   // [B, W]
     const int32_t* kv_lens;       // [B], nodes included
     const int32_t* parents;       // [B, T]
@@ -24,6 +22,14 @@ struct TreeArgs {
     float qk_scale_log2;          // sm_scale * log2(e)
     uint32_t wait_limit_ns;
     int32_t timeout_drill;
+    // where a row's prefix is cut: zones of equal parts from a token (and part) on; with more than one part to
+    // the widest row: partial O / l [B, Hkv, n_splits, D, Rp] and log2-domain LSE [B, Hkv, n_splits, Rp]
+    struct {
+        int32_t split, token, size;
+    } zone[2];
+    int32_t n_splits, Rp;         // Rp: queries of a KV head (G T), rounded up to 8
+    float* o_part;
+    float* lse_part;
     uint64_t rope_turns[ROPE_PAIRS];
 };
 

@@ -308,3 +308,33 @@ def test_offsets_past_32_bits():
     binding.attn_tree(p, c["q"].cuda(), kc, vc, bt, c["kv_lens"].cuda(), c["parents"].cuda(), out, lse,
                       torch.empty(n, dtype=torch.uint8, device="cuda") if n else None)
     assert _equal(want, (out.cpu(), lse.cpu()))
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(5, 8, 2), (60, 8, 2), (40, 8, 1)])
+def test_tree_attention_timeout_exit(T, Hq, Hkv):
+    """A wait that nothing ends gives up: rows are written as failed, and a call after it is as before it."""
+    c = ref.case(43, [300, -T, 2500, 40], T, Hq, Hkv, ["tree", "forest"])
+    want = _run(c)
+    p = _plan(c)
+    p.wait_limit_ns, p.timeout_drill = 1, 1  # 1 us is the least limit that a launch takes
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    out, lse = _run(c, st, plan=p)
+    assert int(st.item()) & binding.STATUS_TIMEOUT
+    assert (out == 0).all() and torch.isnan(lse[[0, 2, 3]]).all() and (torch.isnan(lse[1]) | torch.isneginf(lse[1])).all()
+    st.zero_()
+    assert _equal(want, _run(c, st)) and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,hi", [(3000, 3, 4, 2, 40), (400, 20, 8, 1, 300), (1500, 1, 2, 2, 600)])
+def test_many_rows_are_those_of_small_batches(B, T, Hq, Hkv, hi):
+    r = np.random.RandomState(B)
+    lens = [-T if x < 0.1 else int(n) for x, n in zip(r.rand(B), r.randint(0, hi + 1, B))]
+    c = ref.case(B, lens, T, Hq, Hkv, ["tree", "forest", "chain"])
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    whole = _run(c, st)
+    assert int(st.item()) == 0
+    for lo in range(0, B, max(1, B // 7)):
+        part = {k: v[lo:lo + 9].contiguous() if k in ("q", "block_table", "kv_lens", "parents") else v for k, v in c.items()}
+        assert _equal([x[lo:lo + 9].contiguous() for x in whole], _run(part))
+    few = {k: v[-20:].contiguous() if k in ("q", "block_table", "kv_lens", "parents") else v for k, v in c.items()}
+    _near([x[-20:] for x in whole], ref.attention(few))
