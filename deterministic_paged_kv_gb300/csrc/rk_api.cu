@@ -1189,13 +1189,12 @@ int tree_parts(const rk_paged_plan_t* plan, rk::TreeArgs* a, uint64_t* bytes) {
     const int64_t cap = (int64_t)plan->W * rk::PAGE;
     const int z = cap > a->zone[1].token;
     const int64_t parts = cap > 0 ? a->zone[z].split + (cap - a->zone[z].token + a->zone[z].size - 1) / a->zone[z].size : 1;
-    const int64_t R = (int64_t)plan->Sq * (plan->Hq / plan->Hkv), pairs = (R + 255) / 256;
-    if ((double)plan->B * plan->Hkv * pairs * ((double)cap / 128 + 2) > 2147483647.0 ||
+    const int64_t R = (int64_t)plan->Sq * (plan->Hq / plan->Hkv), blocks = (R + 127) / 128;
+    if ((double)plan->B * plan->Hkv * blocks * ((double)cap / 128 + 2) > 2147483647.0 ||
         (double)plan->B * plan->Hkv * parts * R > 2147483647.0)
         return fail(RK_E_UNSUPPORTED, "B %d x Hkv %d x W %d: too many", plan->B, plan->Hkv, plan->W);
     a->n_splits = (int32_t)parts;
-    a->Rp = (int32_t)((R + 7) & ~7);
-    *bytes = parts > 1 ? (uint64_t)plan->B * plan->Hkv * parts * a->Rp * (rk::HEAD_DIM + 1) * 4 : 0;
+    *bytes = parts > 1 ? (uint64_t)plan->B * plan->Hkv * parts * R * (rk::HEAD_DIM + 1) * 4 : 0;
     return RK_OK;
 }
 
@@ -1234,7 +1233,7 @@ int rk_paged_attn_tree(const rk_paged_plan_t* plan, const void* q, const void* k
     if (plan->B == 0) return RK_OK;
     a.q = q;
     a.o_part = static_cast<float*>(scratch);
-    if (need > 0) a.lse_part = a.o_part + (int64_t)plan->B * plan->Hkv * a.n_splits * a.Rp * rk::HEAD_DIM;
+    if (need > 0) a.lse_part = a.o_part + (int64_t)plan->B * plan->Hq * plan->Sq * a.n_splits * rk::HEAD_DIM;
     a.block_table = block_table_d;
     a.kv_lens = kv_lens_d;
     a.parents = parents_d;

@@ -15,19 +15,26 @@
 // Splits: a row's prefix is cut at fixed tokens (TreeArgs::zone), the tree's tile belongs to the last
 // part; a part leaves O / l and a log2-domain LSE in FP32, and the merge adds the parts up in an
 // order that their number sets.  A row of one part writes its results itself.
-// Work: the items (row, KV head, pair of q-tiles, part) in that order are dealt to a persistent grid of
-// one CTA per SM in runs of equal numbers of tiles; a CTA keeps its queries over the items of one row
-// and head.  Which CTA runs an item never changes how.
+// Work: items (row, KV head, block of 128 queries, part) on a persistent grid of one CTA per SM.  A head's
+// items are dealt to its CTAs in runs of equal numbers of tiles (TrItems); a CTA keeps its queries over
+// the parts of a row.  Which CTA runs an item never changes how.
 //
-// Roles (512 threads), R <= 128 (TILES = 1) / R > 128 (TILES = 2, two q-tiles to an item):
-//   warpgroups 0-1 / 0   transform: rotate new queries and each K tile in place in shared memory
-//                        (FP32, angles from exact anchors and steps), FP16 for the score MMA;
-//   warpgroup  2 / 1-2   softmax, one thread per accumulator row: online softmax in the log2 domain,
-//                        P as BF16 into tensor memory over S; epilogue;
-//   warps 12, 14         TMA producers of K and V pages; warp 14 cleans the tree's V tile;
-//   warp 13              MMA issuer.  TILES = 1: S has two buffers, S of the next tile is issued before
-//                        PV of this one.  TILES = 2: a buffer to each q-tile;
-//   warp 15              scheduler: walks the items, checks their metadata, publishes them.
+// RR = 32, 64 or 128 is the number of queries that an item is padded to.  S = Q K^T has a query to each of
+// the 128 lanes of tensor memory: 128 / RR copies of the queries, so that with two warpgroups 256 / RR threads
+// share a query's row and each has RR / 2 of the tile's columns (a single copy of 32 queries took 5200
+// cycles a tile in the one warp that had rows, where the tile's bytes take 3034).  P^T goes to shared memory
+// as the N operand of O^T = V^T P^T, whose lanes are the output dims.
+//
+// Roles (640 threads):
+//   warps 0-7    transform: rotate new queries and each K tile in place in shared memory (FP32, angles
+//                from exact anchors and steps), FP16 for the score MMA;
+//   warps 8-15   softmax: online, in the log2 domain; the running maximum moves when some query's grows by
+//                more than 8 (a vote of the 256 threads says so; then the maxima are exchanged and O^T is
+//                rescaled); P as BF16; epilogue, a thread one dim of RR / 2 queries;
+//   warps 16, 18 TMA producers of K and V pages; warp 18 cleans the tree's V tile;
+//   warp 17      MMA issuer: S of the next tile before PV of this one (S, and O^T by item, have two buffers);
+//   warp 19      scheduler: walks the items, checks their metadata, publishes them.
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 
@@ -38,47 +45,53 @@ namespace rk {
 
 namespace {
 
-constexpr int TR_THREADS = 512;
-constexpr int WARP_K = 12, WARP_MMA = 13, WARP_V = 14, WARP_SCHED = 15;
+constexpr int TR_XW = 8, TR_SW = 8;                       // transform and softmax warps
+constexpr int TR_SOFTMAX = TR_SW * 32;
+constexpr int WARP_S0 = TR_XW, WARP_K = WARP_S0 + TR_SW, WARP_MMA = WARP_K + 1, WARP_V = WARP_K + 2, WARP_SCHED = WARP_K + 3;
+constexpr int TR_THREADS = (WARP_SCHED + 1) * 32;
+constexpr int TR_SPAN = 128;                              // queries of an item at most
 constexpr int TR_BN = 128;                                // keys of a prefix tile
 constexpr int TR_TILE_BYTES = TR_BN * HEAD_DIM * 2;       // 32 KiB
-constexpr int TR_KSTAGES = 3;
+constexpr int TR_KSTAGES = 3, TR_VSTAGES = 2;
 constexpr int TR_TREE_ROWS = 80;                          // keys of the tree's tile: 15 + 64, whole pages
-constexpr uint32_t TR_TMEM_COLS = 512;                    // S buffers at 0 and 128, O at 256 and 384
 constexpr float TR_SLACK = 8.0f;                          // the running max moves when it grows by more (log2)
 constexpr int TR_SLOTS = 2;                               // items published ahead
+constexpr int TR_ROW_STEP = TR_XW * 4;                    // rows between a transform thread's rows
 constexpr int TR_ANCHOR = 8;                              // tiles between exact angles
-constexpr int TR_GROUPS = 1024;                           // row groups of the item search
+constexpr int TR_GROUPS = 32;                             // row groups of the item search
+// setmaxnreg split of the 640 x 96 registers that the CTA launches with
+constexpr int REG_X = 88, REG_S = 120, REG_C = 64;
+static_assert(2 * REG_X + 2 * REG_S + REG_C <= 5 * 96, "register split above the launch's");
 
-template <int TILES>
+template <int RR>
 struct TrShape {
-    static constexpr int VSTAGES = TILES == 1 ? 3 : 2;
-    static constexpr int XW = TILES == 1 ? 8 : 4;         // transform warps
-    static constexpr int ROW_STEP = XW * 4;               // rows between a transform thread's rows
-    static constexpr int SW = 4 * TILES;                  // softmax warps
-    static constexpr int REG_X = TILES == 1 ? 104 : 88, REG_S = TILES == 1 ? 208 : 184, REG_C = 56;
-    static constexpr int OFF_K = TILES * TR_TILE_BYTES;
+    static constexpr int COPIES = TR_SPAN / RR;           // of the queries, in the lanes of S
+    static constexpr int PARTS = 2 * COPIES;              // threads of a query's row of S
+    static constexpr int COLS = TR_BN / PARTS;            // columns of each: RR / 2, and its queries in the epilogue
+    static constexpr int PBUF = RR == 128 ? 1 : 2;        // buffers of P^T, as room allows
+    static constexpr int P_BYTES = RR * TR_BN * 2;
+    static constexpr int OFF_K = TR_TILE_BYTES;           // queries first
     static constexpr int OFF_V = OFF_K + TR_KSTAGES * TR_TILE_BYTES;
-    static constexpr int OFF_CTRL = OFF_V + VSTAGES * TR_TILE_BYTES;
+    static constexpr int OFF_P = OFF_V + TR_VSTAGES * TR_TILE_BYTES;
+    static constexpr int OFF_CTRL = OFF_P + PBUF * P_BYTES;
+    // tensor memory: S at 0 and 128, O^T at 256 and 256 + RR
+    static constexpr uint32_t TMEM_COLS = 512;
 };
-static_assert(2 * TrShape<1>::REG_X + TrShape<1>::REG_S + TrShape<1>::REG_C <= 512, "register split above the launch's");
-static_assert(TrShape<2>::REG_X + 2 * TrShape<2>::REG_S + TrShape<2>::REG_C <= 512, "register split above the launch's");
 
 // An item as the scheduler publishes it.
 struct TrUnit {
     int end;                 // 1: no further item
-    int b, kvh, pair, split;
+    int b, kvh, block, split;
     int t0, n_keys;          // its prefix keys [t0, t0 + n_keys), whole pages
     int tree;                // 1: the tree's tile follows them
     int prefix;              // tokens before the tree
     int newq, endq, nq;      // first / last item of its queries, their number in this CTA
     int direct;              // 1: the row has one part
-    int rows;                // live accumulator rows of the item
+    int rows;                // live queries of the item
 };
 struct TrSlot {
     TrUnit u;
-    uint64_t sees[TREE_MAX];   // node's ancestors and itself
-    uint8_t depth[TREE_MAX];   // 255: unused
+    uint64_t sees[TREE_MAX];   // node's ancestors and itself (0: unused); its depth is one less than their number
 };
 
 // ------------------------------------------------------------ geometry ----
@@ -102,108 +115,108 @@ __device__ __forceinline__ int part_start(const TreeArgs& a, int s) {
 // Tiles of a row: its prefix's and the tree's (one for a row without keys, which is an item too).
 __device__ __forceinline__ int row_tiles(int n) { return n < 0 ? 1 : (n + TR_BN - 1) / TR_BN + 1; }
 
-// A CTA's items: the parts whose first tile, in the order of row, KV head and pair, part, lies in
-// the CTA's share of all tiles.
+// The items of a KV head and pair of q-tiles are its rows' parts in order of row and part; they are dealt
+// to `members` runs of equal numbers of tiles (a part belongs to the run that its first tile lies in), the same
+// for every head, so that the CTAs of a row's heads read its pages, in which a token's heads are
+// neighbours, at about the same time.  Run v of all is run v / heads of head v % heads; CTA c has the runs
+// c, c + grid, ...
 struct TrItems {
-    int b, h, s;            // row, KV head * pairs + pair, part
+    int v, b, s;            // run, row, part
     int kv, n, ns, bad;     // the row's length, prefix keys in whole pages, parts, status
-    int at, hi;             // the item's first tile, the share's end
-    __device__ __forceinline__ bool valid(const TreeArgs& a) const { return b < a.B && at < hi; }
+    int at, hi;             // the part's first tile, the run's end
+    __device__ __forceinline__ int head(int heads) const { return v % heads; }
+    __device__ __forceinline__ bool valid(const TreeArgs& a, int heads) const { return v < heads * a.members; }
     __device__ __forceinline__ void row(const TreeArgs& a) {
         if (b < a.B) {
             n = row_pages16(a, b, kv, bad);
             ns = parts_of(a, n);
         }
     }
-    __device__ void start(const TreeArgs& a, int total, const int* pre, int heads) {
-        const unsigned all = (unsigned)(total * heads), each = all / gridDim.x, rest = all % gridDim.x;
-        at = (int)(each * blockIdx.x + rest * blockIdx.x / gridDim.x);
-        hi = (int)(each * (blockIdx.x + 1) + rest * (blockIdx.x + 1) / gridDim.x);
-        const int per = (a.B + TR_GROUPS - 1) / TR_GROUPS, groups = (a.B + per - 1) / per;
-        int lo = 0, top = groups;
-        while (top - lo > 1) {
-            const int mid = (lo + top) >> 1;
-            if (pre[mid] * heads <= at) lo = mid;
-            else top = mid;
-        }
-        b = lo * per;
-        int base = pre[lo] * heads;
-        while (true) {
-            row(a);
-            const int rt = row_tiles(n), in = at - base;
-            if (in < rt * heads || b + 1 >= a.B) {
-                h = in / rt;
-                const int tile = in % rt;
-                // the first part that starts at this tile or later
-                for (s = tile ? parts_of(a, min(max(n, 0), tile * TR_BN)) : 0; s < ns && part_start(a, s) < tile * TR_BN; ++s) {
-                }
-                if (s < ns) {
-                    at = base + h * rt + part_start(a, s) / TR_BN;
-                } else {
-                    at = base + (h + 1) * rt;
-                    wrap(a, heads);
-                }
-                return;
+    // The first part of run v that there is, or of a later run of this CTA.
+    __device__ void start(const TreeArgs& a, int total, const int* pre, int heads, int run) {
+        for (v = run; v < heads * a.members; v += (int)gridDim.x) {
+            const unsigned m = (unsigned)(v / heads), each = (unsigned)total / a.members, rest = (unsigned)total % a.members;
+            at = (int)(each * m + rest * m / a.members);
+            hi = (int)(each * (m + 1) + rest * (m + 1) / a.members);
+            const int per = (a.B + TR_GROUPS - 1) / TR_GROUPS, groups = (a.B + per - 1) / per;
+            int lo = 0, top = groups;
+            while (top - lo > 1) {
+                const int mid = (lo + top) >> 1;
+                if (pre[mid] <= at) lo = mid;
+                else top = mid;
             }
-            base += rt * heads;
-            ++b;
+            b = lo * per;
+            int base = pre[lo];
+            for (;;) {
+                row(a);
+                const int rt = row_tiles(n);
+                if (at - base < rt || b + 1 >= a.B) break;
+                base += rt;
+                ++b;
+            }
+            const int tile = at - base;
+            s = tile ? parts_of(a, min(max(n, 0), tile * TR_BN)) : 0;  // the first part that starts at this tile or later
+            if (s < ns) {
+                at = base + part_start(a, s) / TR_BN;
+            } else {
+                at = base + row_tiles(n);
+                s = 0;
+                ++b;
+                row(a);
+            }
+            if (b < a.B && at < hi) return;
         }
     }
-    __device__ __forceinline__ void wrap(const TreeArgs& a, int heads) {
-        s = 0;
-        if (++h == heads) {
-            h = 0;
-            ++b;
-            row(a);
-        }
-    }
-    __device__ __forceinline__ void next(const TreeArgs& a, int heads) {
+    __device__ __forceinline__ void next(const TreeArgs& a, int total, const int* pre, int heads) {
         const int from = part_start(a, s) / TR_BN;
         if (++s == ns) {
             at += row_tiles(n) - from;
-            wrap(a, heads);
+            s = 0;
+            ++b;
+            row(a);
         } else {
             at += part_start(a, s) / TR_BN - from;
         }
+        if (b >= a.B || at >= hi) start(a, total, pre, heads, v + (int)gridDim.x);
     }
 };
 
 struct TrCtrl {
     uint64_t q_ready, q_empty;
     uint64_t k_full[TR_KSTAGES], k_ready[TR_KSTAGES], k_empty[TR_KSTAGES];
-    uint64_t v_full[3], v_empty[3], v_land;
-    uint64_t s_full[2], p_ready[2], pv_done[2], o_done[2], o_free[2];
+    uint64_t v_full[TR_VSTAGES], v_empty[TR_VSTAGES], v_land;
+    uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2], o_done[2], o_free[2];
     uint64_t u_full[TR_SLOTS], u_empty[TR_SLOTS];
     uint64_t r_full[2], r_empty[2];
     uint64_t never;
     uint32_t tmem_base;
     PipeCtl pipe;
-    int total;                        // tiles of the batch's rows (of one KV head and pair)
-    int first[sizeof(TrItems) / 4];   // the CTA's first item, for the way out after a failure
-    int scan[TR_THREADS / 32];
+    int total;                        // tiles of the batch's rows (of one KV head and block)
+    int pre[TR_GROUPS];               // tiles before each group of rows
     uint64_t vbad[2];                 // nodes whose V is not finite, by item parity
-    uint8_t xbad[2][8];               // a transform warp met a prefix key out of range
+    uint8_t xbad[2][TR_XW];           // a transform warp met a prefix key out of range
     uint8_t kbad[2][TR_TREE_ROWS];    // keys of the tree's tile out of range
-    uint8_t qbad[2][256];             // queries out of range, by the queries' parity
+    uint8_t qbad[2][TR_SPAN];         // queries out of range, by the queries' parity
     alignas(16) TrSlot slot[TR_SLOTS];
+    // exchange of the softmax threads: maxima, then scales of O^T; at the end sums, then factors
+    alignas(16) float ex[TR_SOFTMAX];
 };
-template <int TILES>
+template <int RR>
 constexpr int tr_smem_bytes() {
-    static_assert(TrShape<TILES>::OFF_CTRL + sizeof(TrCtrl) <= 232448, "tree attention shared memory above the 227 KiB opt-in limit");
-    return TrShape<TILES>::OFF_CTRL + (int)sizeof(TrCtrl);
+    static_assert(TrShape<RR>::OFF_CTRL + sizeof(TrCtrl) <= 232448, "tree attention shared memory above the 227 KiB opt-in limit");
+    return TrShape<RR>::OFF_CTRL + (int)sizeof(TrCtrl);
 }
-static_assert(TR_GROUPS * 4 <= TR_TILE_BYTES, "the item search's sums lie in a V stage");
 
-// First accumulator row of (row b, KV head kvh) in q, out and lse.
+// First query of (row b, KV head kvh) in q, out and lse: its G heads x T nodes follow one another.
 __device__ __forceinline__ size_t first_row(const TreeArgs& a, int b, int kvh) { return ((size_t)b * a.Hkv + kvh) * (size_t)(a.G * a.T); }
 
 // An item that nothing is computed for (count threads, i of them): a part that says NaN or -inf,
 // or the results themselves.
-__device__ void write_nothing(const TreeArgs& a, int b, int kvh, int pair, int split, bool direct, float lse, int i, int count, int span) {
-    const int R = a.G * a.T, r0 = pair * span, rows = min(span, R - r0);
+__device__ void write_nothing(const TreeArgs& a, int b, int kvh, int block, int split, bool direct, float lse, int i, int count) {
+    const int R = a.G * a.T, r0 = block * TR_SPAN, rows = min(TR_SPAN, R - r0);
     if (!direct) {
-        float* lp = a.lse_part + (((size_t)b * a.Hkv + kvh) * a.n_splits + split) * a.Rp + r0;
-        for (int r = i; r < rows; r += count) lp[r] = lse;
+        float* lp = a.lse_part + ((first_row(a, b, kvh) + r0) * a.n_splits + split);
+        for (int r = i; r < rows; r += count) lp[(size_t)r * a.n_splits] = lse;
         return;
     }
     uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (first_row(a, b, kvh) + r0) * HEAD_DIM);
@@ -211,13 +224,35 @@ __device__ void write_nothing(const TreeArgs& a, int b, int kvh, int pair, int s
     for (int r = i; r < rows; r += count) a.lse[first_row(a, b, kvh) + r0 + r] = lse * 0.693147180559945309f;
 }
 
-// PV of a tile: one k-step per page (P from tensor memory, V from shared memory).
-template <int KS>
-__device__ __forceinline__ void pv_steps(uint32_t d, uint32_t p, uint32_t v, uint32_t idesc, uint32_t acc0, int pages) {
+// PV of a tile, a whole warp: one k-step per page, O^T[dims x RR] += V^T P^T with V as the pages lie in shared
+// memory (MN-major) and P^T's rows as two blocks of 64 keys (K-major), RR * 128 bytes apart.
+template <int KS, int RR>
+__device__ __forceinline__ void pv_steps(uint32_t d, uint32_t v, uint32_t p, uint32_t idesc, uint32_t acc0, int pages) {
     if (KS < pages) {
-        mma_ts_steps<KS, KS + 1, MN_MAJOR_PAGE>(d, p, v, idesc, acc0);
-        if constexpr (KS + 1 < TR_BN / PAGE) pv_steps<KS + 1>(d, p, v, idesc, acc0, pages);
+        asm volatile(
+            "{\n\t.reg .pred q, e;\n\t.reg .b32 al, bl;\n\t.reg .b64 da, db;\n\t"
+            "add.u32 al, %1, %5;\n\tadd.u32 bl, %2, %6;\n\t"
+            "mov.b64 da, {al, %4};\n\tmov.b64 db, {bl, %4};\n\t"
+            "setp.ne.b32 q, %7, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, q;\n\t}" ::"r"(d),
+            "r"(v), "r"(p), "r"(idesc), "r"(DESC_HI), "n"(KS * (4096 >> 4)), "n"(((KS >> 2) * RR * 128 + (KS & 3) * 32) >> 4),
+            "r"(KS > 0 ? 1u : acc0)
+            : "memory");
+        if constexpr (KS + 1 < TR_BN / PAGE) pv_steps<KS + 1, RR>(d, v, p, idesc, acc0, pages);
     }
+}
+
+// N consecutive columns of the thread's lane (tensor memory), to be waited for.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N]) {
+    static_assert(N == 16 || N == 32, "tensor memory load");
+    if constexpr (N == 16) tmem_ld16(taddr, r);
+    else tmem_ld32(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[N]) {
+    if constexpr (N == 16) tmem_st16(taddr, r);
+    else tmem_st32(taddr, r);
 }
 
 // Keys of tile i of an item (whole pages).
@@ -226,112 +261,99 @@ __device__ __forceinline__ int tile_keys(int i, int n_keys, int prefix, int T) {
     return left > 0 ? min(TR_BN, left) : ((prefix & (PAGE - 1)) + T + PAGE - 1) & ~(PAGE - 1);
 }
 
-template <int TILES>
+template <int RR>
 __global__ void __launch_bounds__(TR_THREADS, 1)
     tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const __grid_constant__ TreeArgs a) {
     extern __shared__ __align__(1024) uint8_t sm[];
-    using Sh = TrShape<TILES>;
-    constexpr int VSTAGES = Sh::VSTAGES;
+    using Sh = TrShape<RR>;
     TrCtrl* c = reinterpret_cast<TrCtrl*>(sm + Sh::OFF_CTRL);
-    int* pre = reinterpret_cast<int*>(sm + Sh::OFF_V + (VSTAGES - 1) * TR_TILE_BYTES);
     const uint32_t s_base = smem_u32(sm);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int T = a.T, R = a.G * T;
-    constexpr int SPAN = 128 * TILES;                     // accumulator rows of an item
-    const int pairs = (R + SPAN - 1) / SPAN, heads = a.Hkv * pairs;
+    const int blocks = (R + TR_SPAN - 1) / TR_SPAN, heads = a.Hkv * blocks;
     griddep_launch_dependents();                          // the merge may become resident; it waits for this grid's end
 
     if (tid == 0) {
         c->pipe.abort = 0;
         c->pipe.limit_ns = wait_limit(a.wait_limit_ns);
         mbar_init(smem_u32(&c->never), 1);
-        mbar_init(smem_u32(&c->q_ready), Sh::XW);
+        mbar_init(smem_u32(&c->q_ready), TR_XW);
         mbar_init(smem_u32(&c->q_empty), 1);
         for (int k = 0; k < TR_KSTAGES; ++k) {
             mbar_init(smem_u32(&c->k_full[k]), 1);
-            mbar_init(smem_u32(&c->k_ready[k]), Sh::XW);
+            mbar_init(smem_u32(&c->k_ready[k]), TR_XW);
             mbar_init(smem_u32(&c->k_empty[k]), 1);
         }
-        for (int k = 0; k < VSTAGES; ++k) {
+        for (int k = 0; k < TR_VSTAGES; ++k) {
             mbar_init(smem_u32(&c->v_full[k]), 1);
             mbar_init(smem_u32(&c->v_empty[k]), 1);
         }
         mbar_init(smem_u32(&c->v_land), 1);
         for (int j = 0; j < 2; ++j) {
             mbar_init(smem_u32(&c->s_full[j]), 1);
-            mbar_init(smem_u32(&c->p_ready[j]), 4);
+            mbar_init(smem_u32(&c->s_free[j]), TR_SW);
+            mbar_init(smem_u32(&c->p_ready[j]), TR_SW);
             mbar_init(smem_u32(&c->pv_done[j]), 1);
             mbar_init(smem_u32(&c->o_done[j]), 1);
-            mbar_init(smem_u32(&c->o_free[j]), 4);
-            mbar_init(smem_u32(&c->r_full[j]), Sh::XW + 1);
-            mbar_init(smem_u32(&c->r_empty[j]), Sh::SW);
+            mbar_init(smem_u32(&c->o_free[j]), TR_SW);
+            mbar_init(smem_u32(&c->r_full[j]), TR_XW + 1);
+            mbar_init(smem_u32(&c->r_empty[j]), TR_SW);
         }
         for (int k = 0; k < TR_SLOTS; ++k) {
             mbar_init(smem_u32(&c->u_full[k]), 1);
-            mbar_init(smem_u32(&c->u_empty[k]), 3 + Sh::XW + Sh::SW);  // producers, issuer, transform, softmax warps
+            mbar_init(smem_u32(&c->u_empty[k]), 3 + TR_XW + TR_SW);  // producers, issuer, transform, softmax warps
         }
         fence_mbar_init();
     }
     if (warp == WARP_MMA) {
-        tmem_alloc(smem_u32(&c->tmem_base), TR_TMEM_COLS);
+        tmem_alloc(smem_u32(&c->tmem_base), Sh::TMEM_COLS);
         tmem_relinquish();
     }
     {
-        // Tiles before each group of `per` rows, a group to a thread and pass.
-        const int per = (a.B + TR_GROUPS - 1) / TR_GROUPS, groups = (a.B + per - 1) / per;
-        int base = 0;
-        for (int g0 = 0; g0 < groups; g0 += TR_THREADS) {
-            const int gr = g0 + tid;
-            int cnt = 0;
-            for (int b = gr * per; gr < groups && b < min(a.B, gr * per + per); ++b) {
-                int kv, bad;
-                cnt += row_tiles(row_pages16(a, b, kv, bad));
-            }
-            int v = cnt;
+        // Tiles before each group of `per` rows: a group to sixteen threads.
+        const int per = (a.B + TR_GROUPS - 1) / TR_GROUPS;
+        int cnt = 0;
+        for (int i = tid & 15, b = (tid >> 4) * per + i; i < per && b < a.B; i += 16, b += 16) {
+            int kv, bad;
+            cnt += row_tiles(row_pages16(a, b, kv, bad));
+        }
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
+        if ((tid & 15) == 0 && (tid >> 4) < TR_GROUPS) c->pre[tid >> 4] = cnt;
+        __syncthreads();
+        if (warp == 0) {
+            const int own = c->pre[lane];
+            int v = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int t = __shfl_up_sync(0xffffffffu, v, o);
                 if (lane >= o) v += t;
             }
-            __syncthreads();
-            if (lane == 31) c->scan[warp] = v;
-            __syncthreads();
-            int before = base;
-            for (int w = 0; w < TR_THREADS / 32; ++w) {
-                before += w < warp ? c->scan[w] : 0;
-                base += c->scan[w];
-            }
-            if (gr < groups) pre[gr] = before + v - cnt;
+            c->pre[lane] = v - own;
+            if (lane == 31) c->total = v;
         }
-        if (tid == 0) c->total = base;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c->tmem_base;
     PipeCtl* pc = &c->pipe;
-    if (warp == WARP_SCHED) {
-        TrItems first;
-        first.start(a, c->total, pre, heads);
-        if (lane == 0) *reinterpret_cast<TrItems*>(c->first) = first;
-        fence_proxy_async_smem();                         // the sums' memory is a V stage from here on
-    }
-    __syncthreads();
-    int done = 0;                                         // softmax: published items written
+    int done = 0;                                         // softmax: items written
 
     auto wait_all = [&](uint64_t& bar, int parity) {
         return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), (uint32_t)(parity & 1), pc)) != 0;
     };
 
-    if (wg == 3) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::REG_C));
+    if (warp >= WARP_K) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_C));
         if (warp == WARP_SCHED) {
             // ============================================== scheduler ====
-            TrItems it = *reinterpret_cast<const TrItems*>(c->first);
+            TrItems it;
+            it.start(a, c->total, c->pre, heads, (int)blockIdx.x);
             int k = 0, nq = -1, tree_row = -1;            // published items, queries; row whose tree is in registers
             uint64_t sees[2] = {0, 0};                    // of nodes lane, lane + 32
-            int deep[2] = {255, 255}, tree_bad = 0;
-            int lb = -1, lh = -1;                         // queries of the item before
+            int tree_bad = 0;
+            int lb = -1, lv = -1;                         // queries of the item before
             bool ok = true;
             // checks the item `it`; 0: to be published
             auto judge = [&]() -> int {
@@ -376,8 +398,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                             up[e] = up[e] >= 0 ? far[e] : -1;
                         }
                     }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) deep[e] = sees[e] ? __popcll(sees[e]) - 1 : 255;
                 }
                 bad |= tree_bad;
                 // page ids of the item's keys
@@ -393,40 +413,40 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             };
             // goes on to the next item that has something to compute, writing those that have not
             auto settle = [&]() {
-                while (it.valid(a)) {
+                while (it.valid(a, heads)) {
                     const int bad = judge();
                     if (!bad && it.n >= 0) return;
                     if (bad && lane == 0 && a.status) atomicOr(a.status, bad);
-                    write_nothing(a, it.b, it.h / pairs, it.h % pairs, it.s, it.ns == 1, bad ? __int_as_float(0x7fc00000) : -INFINITY, lane, 32, SPAN);
-                    it.next(a, heads);
+                    const int h = it.head(heads);
+                    write_nothing(a, it.b, h / blocks, h % blocks, it.s, it.ns == 1, bad ? __int_as_float(0x7fc00000) : -INFINITY, lane, 32);
+                    it.next(a, c->total, c->pre, heads);
                 }
             };
             settle();
             while (ok) {
                 TrUnit u;
                 std::memset(&u, 0, sizeof u);
-                u.end = !it.valid(a);
-                uint64_t s0 = sees[0], s1 = sees[1];
-                const int d0 = deep[0], d1 = deep[1];
+                u.end = !it.valid(a, heads);
+                const uint64_t s0 = sees[0], s1 = sees[1];
                 if (!u.end) {
                     u.b = it.b;
-                    u.kvh = it.h / pairs;
-                    u.pair = it.h % pairs;
+                    u.kvh = it.head(heads) / blocks;
+                    u.block = it.head(heads) % blocks;
                     u.split = it.s;
                     u.t0 = part_start(a, it.s);
                     u.tree = it.s + 1 == it.ns;
                     u.n_keys = (u.tree ? it.n : part_start(a, it.s + 1)) - u.t0;
                     u.prefix = it.kv - T;
                     u.direct = it.ns == 1;
-                    u.rows = min(SPAN, R - u.pair * SPAN);
-                    u.newq = it.b != lb || it.h != lh;
+                    u.rows = min(TR_SPAN, R - u.block * TR_SPAN);
+                    u.newq = it.b != lb || it.v != lv;
                     nq += u.newq;
                     u.nq = nq;
                     lb = it.b;
-                    lh = it.h;
-                    it.next(a, heads);
+                    lv = it.v;
+                    it.next(a, c->total, c->pre, heads);
                     settle();
-                    u.endq = !it.valid(a) || it.b != lb || it.h != lh;
+                    u.endq = !it.valid(a, heads) || it.b != lb || it.v != lv;
                 }
                 TrSlot* s = &c->slot[k % TR_SLOTS];
                 const int use = k / TR_SLOTS;
@@ -435,8 +455,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
                 s->sees[lane] = s0;
                 s->sees[lane + 32] = s1;
-                s->depth[lane] = (uint8_t)d0;
-                s->depth[lane + 32] = (uint8_t)d1;
                 if (lane == 0) s->u = u;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&c->u_full[k % TR_SLOTS]));
@@ -448,7 +466,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             const bool is_k = warp == WARP_K;
             const CUtensorMap* map = is_k ? &kmap : &vmap;
             if (lane == 0) prefetch_tmap(map);
-            const int nst = is_k ? TR_KSTAGES : VSTAGES;
+            const int nst = is_k ? TR_KSTAGES : TR_VSTAGES;
             int n = 0, nl = 0;          // tiles issued, tree tiles that went through v_land
             bool land_open = false, ok = true;
             for (int k = 0; ok; ++k) {
@@ -501,7 +519,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                         for (int r0 = off; r0 < keys; r0 += 2) {  // two rows a turn, 16 bytes a lane
                             const int r = r0 + (lane >> 4), ch = lane & 15, node = r - off;
                             uint4* x = reinterpret_cast<uint4*>(vt + (r >> 4) * 4096 + (ch >> 3) * 2048 + (r & 15) * 128 + (((ch & 7) ^ (r & 7)) << 4));
-                            const bool in = r < keys, real = in && node < T && s->depth[node & 63] != 255;
+                            const bool in = r < keys, real = in && node < T && s->sees[node & 63] != 0;
                             uint32_t m = 0;
                             if (real) {
                                 const uint4 y = *x;
@@ -539,70 +557,56 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 for (int i = max(0, n - nst); i < n; ++i)
                     mbar_wait_drain(smem_u32(is_k ? &c->k_full[i % nst] : &c->v_full[i % nst]), (uint32_t)((i / nst) & 1));
             }
-        } else if (warp == WARP_MMA && lane == 0) {
+        } else if (warp == WARP_MMA) {
             // ============================================= MMA issuer ====
-            const uint32_t idO = idesc_bf16_f32(128, HEAD_DIM, 0, 1);
+            // The whole warp, converged, so that the operands stay in uniform registers; one elected lane issues.
+            constexpr uint32_t idO = idesc_bf16_f32(HEAD_DIM, RR, 1, 0);
             constexpr uint32_t TILE_DESC = TR_TILE_BYTES >> 4;
-            const uint32_t dQ0 = desc_lo(s_base, 16), dK0 = desc_lo(s_base + Sh::OFF_K, 16), dV0 = desc_lo(s_base + Sh::OFF_V, 2048);
-            auto wait = [&](uint64_t& bar, int parity) { return mbar_wait(smem_u32(&bar), (uint32_t)(parity & 1), pc); };
-            int g0 = 0, nu[2] = {0, 0}, np[2] = {0, 0};  // tiles before the item; per q-tile: items, tiles
-            bool ok = !a.timeout_drill || drill_wait(smem_u32(&c->never), pc);
+            const uint32_t dQ = desc_lo(s_base, 16), dK0 = desc_lo(s_base + Sh::OFF_K, 16);
+            const uint32_t dV0 = desc_lo(s_base + Sh::OFF_V, 2048), dP0 = desc_lo(s_base + Sh::OFF_P, 16);
+            int g = 0;  // tiles so far
+            bool ok = !a.timeout_drill || __all_sync(0xffffffffu, drill_wait(smem_u32(&c->never), pc));
             for (int k = 0; ok; ++k) {
-                if (!(ok = wait(c->u_full[k % TR_SLOTS], k / TR_SLOTS))) break;
+                if (!(ok = wait_all(c->u_full[k % TR_SLOTS], k / TR_SLOTS))) break;
                 const volatile TrUnit* su = &c->slot[k % TR_SLOTS].u;
-                const int end = su->end, n_keys = su->n_keys, tree = su->tree, prefix = su->prefix;
-                const int newq = su->newq, endq = su->endq, nq = su->nq, live = TILES == 2 && su->rows > 128 ? 2 : 1;
-                mbar_arrive(smem_u32(&c->u_empty[k % TR_SLOTS]));
+                auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+                const int end = uni(su->end), n_keys = uni(su->n_keys), tree = uni(su->tree), prefix = uni(su->prefix);
+                const int newq = uni(su->newq), endq = uni(su->endq), nq = uni(su->nq);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&c->u_empty[k % TR_SLOTS]));
                 if (end) break;
-                const int npt = (n_keys + TR_BN - 1) / TR_BN, n_tiles = npt + tree;
-                if (newq && !(ok = wait(c->q_ready, nq))) break;
-                auto issue_s = [&](int j, int i) {
-                    const int g = g0 + i, keys = tile_keys(i, n_keys, prefix, T);
-                    const uint32_t idS = (1u << 4) | ((uint32_t)(keys >> 3) << 17) | (128u >> 4 << 24);
-                    const int buf = TILES == 1 ? g & 1 : j;
-                    mma_ss_steps<0, 8, K_MAJOR_128, K_MAJOR_128>(tmem + buf * 128, dQ0 + (uint32_t)j * TILE_DESC,
-                                                                 dK0 + (uint32_t)(g % TR_KSTAGES) * TILE_DESC, idS, 0u);
-                    umma_commit(smem_u32(&c->s_full[buf]));
-                };
-                // PV of tile i and q-tile j
-                auto issue_pv = [&](int j, int i) -> bool {
-                    const int g = g0 + i, buf = TILES == 1 ? g & 1 : j;
-                    if (i == 0 && !wait(c->o_free[j], nu[j] + 1)) return false;  // the item before has been read
-                    if (!wait(c->p_ready[buf], TILES == 1 ? g >> 1 : np[j] + i)) return false;
-                    if (!wait(c->v_full[g % VSTAGES], g / VSTAGES)) return false;
+                const int n_tiles = (n_keys + TR_BN - 1) / TR_BN + tree;
+                if (newq && !(ok = wait_all(c->q_ready, nq))) break;
+                // PV of tile i, number x of the CTA
+                auto issue_pv = [&](int i, int x) -> bool {
+                    if (i == 0 && !wait_all(c->o_free[k & 1], (k >> 1) + 1)) return false;  // the buffer's item before has been read
+                    if (!wait_all(c->p_ready[x % Sh::PBUF], x / Sh::PBUF)) return false;
+                    if (!wait_all(c->v_full[x % TR_VSTAGES], x / TR_VSTAGES)) return false;
                     tc_fence_after();
-                    pv_steps<0>(tmem + 256 + j * 128, tmem + buf * 128, dV0 + (uint32_t)(g % VSTAGES) * TILE_DESC, idO, i > 0 ? 1u : 0u,
-                                tile_keys(i, n_keys, prefix, T) / PAGE);
-                    if constexpr (TILES == 1) umma_commit(smem_u32(&c->pv_done[buf]));
-                    if (i == n_tiles - 1) umma_commit(smem_u32(&c->o_done[j]));
+                    pv_steps<0, RR>(tmem + 256 + (k & 1) * RR, dV0 + (uint32_t)(x % TR_VSTAGES) * TILE_DESC,
+                                    dP0 + (uint32_t)(x % Sh::PBUF) * (Sh::P_BYTES >> 4), idO, i > 0 ? 1u : 0u,
+                                    tile_keys(i, n_keys, prefix, T) / PAGE);
+                    umma_commit_elect(smem_u32(&c->pv_done[x & 1]));
+                    umma_commit_elect(smem_u32(&c->v_empty[x % TR_VSTAGES]));
+                    if (i == n_tiles - 1) umma_commit_elect(smem_u32(&c->o_done[k & 1]));
                     return true;
                 };
-                for (int i = 0; i < n_tiles; ++i) {
-                    const int g = g0 + i;
-                    if (!(ok = wait(c->k_ready[g % TR_KSTAGES], g / TR_KSTAGES))) break;
-                    tc_fence_after();
-                    if constexpr (TILES == 1) {
-                        issue_s(0, i);
-                    } else {
-                        for (int j = 0; j < live; ++j) {
-                            if (i > 0 && !(ok = issue_pv(j, i - 1))) break;
-                            issue_s(j, i);
-                        }
-                        if (!ok) break;
+#pragma unroll 1
+                for (int i = 0; i <= n_tiles; ++i, ++g) {
+                    if (i < n_tiles) {
+                        const uint32_t idS = idesc_f16_f32(128, tile_keys(i, n_keys, prefix, T));
+                        if (!(ok = wait_all(c->k_ready[g % TR_KSTAGES], g / TR_KSTAGES))) break;
+                        if (!(ok = wait_all(c->s_free[g & 1], (g >> 1) + 1))) break;
+                        tc_fence_after();
+                        mma_ss_steps<0, 8, K_MAJOR_128, K_MAJOR_128, true>(tmem + (g & 1) * 128, dQ,
+                                                                           dK0 + (uint32_t)(g % TR_KSTAGES) * TILE_DESC, idS, 0u);
+                        umma_commit_elect(smem_u32(&c->s_full[g & 1]));
+                        umma_commit_elect(smem_u32(&c->k_empty[g % TR_KSTAGES]));
+                        if (endq && i == n_tiles - 1) umma_commit_elect(smem_u32(&c->q_empty));
                     }
-                    umma_commit(smem_u32(&c->k_empty[g % TR_KSTAGES]));
-                    if (endq && i == n_tiles - 1) umma_commit(smem_u32(&c->q_empty));
-                    if (TILES == 1 && i > 0 && !(ok = issue_pv(0, i - 1))) break;
-                    if (i > 0) umma_commit(smem_u32(&c->v_empty[(g - 1) % VSTAGES]));
+                    if (i > 0 && !(ok = issue_pv(i - 1, g - 1))) break;
                 }
-                for (int j = 0; j < live && ok; ++j) ok = issue_pv(j, n_tiles - 1);
-                if (!ok) break;
-                umma_commit(smem_u32(&c->v_empty[(g0 + n_tiles - 1) % VSTAGES]));
-                g0 += n_tiles;
-                for (int j = 0; j < live; ++j) {
-                    ++nu[j];
-                    np[j] += n_tiles;
-                }
+                --g;  // the last turn had no tile
             }
             if (!ok) {  // issued MMAs drain before tensor memory is released
                 const uint64_t t0 = global_timer_ns();
@@ -611,17 +615,17 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (warp < Sh::XW) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Sh::REG_X));
+    } else if (warp < TR_XW) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_X));
         // ================================================ transform ====
         // thread: pair-chunk u8 (8 rotation pairs: 16 bytes of each 64-dim half) of rows r0 + ROW_STEP * m
         const int u8 = tid & 7, r0 = tid >> 3;
-        constexpr int ROWS = TR_BN / Sh::ROW_STEP;
+        constexpr int ROWS = TR_BN / TR_ROW_STEP;
         float2 dcs[4], dsn[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            rope_cos_sin((uint32_t)Sh::ROW_STEP, a.rope_turns[8 * u8 + 2 * e], dcs[e].x, dsn[e].x);
-            rope_cos_sin((uint32_t)Sh::ROW_STEP, a.rope_turns[8 * u8 + 2 * e + 1], dcs[e].y, dsn[e].y);
+            rope_cos_sin((uint32_t)TR_ROW_STEP, a.rope_turns[8 * u8 + 2 * e], dcs[e].x, dsn[e].x);
+            rope_cos_sin((uint32_t)TR_ROW_STEP, a.rope_turns[8 * u8 + 2 * e + 1], dcs[e].y, dsn[e].y);
         }
         auto angles = [&](uint32_t pos, float2 (&cs)[4], float2 (&sn)[4]) {
 #pragma unroll
@@ -646,27 +650,30 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             const int npt = (n_keys + TR_BN - 1) / TR_BN;
             float2 cs[4], sn[4];
             if (u->newq) {
-                // new queries, once the score MMAs have read the ones before
-                const int nq = u->nq, rows = u->rows;
+                // new queries, once the score MMAs have read the ones before: COPIES of them, zeros behind the last
+                const int nq = u->nq, rows = u->rows, base = u->block * TR_SPAN;
                 const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
-                                                                (first_row(a, u->b, u->kvh) + u->pair * SPAN) * HEAD_DIM);
+                                                                (first_row(a, u->b, u->kvh) + base) * HEAD_DIM);
                 if (!(ok = wait_all(c->q_empty, nq + 1))) break;
 #pragma unroll 1
-                for (int rr = 0; rr < SPAN && rr < ((rows + 31) & ~31); rr += Sh::ROW_STEP) {
-                    const int r = rr + r0, n = (u->pair * SPAN + r) % T;
+                for (int r = r0; r < RR; r += TR_ROW_STEP) {
                     const bool in = r < rows;
-                    uint32_t range = 0;
+                    uint32_t rg = 0;
+                    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
                     if (in) {
-                        uint4 lo = __ldg(q + r * 16 + u8), hi = __ldg(q + r * 16 + 8 + u8);
-                        const int d = s->depth[n];
-                        angles((uint32_t)(prefix + (d == 255 ? 0 : d)), cs, sn);
-                        range = rotate_regs_f16(lo, hi, cs, sn, 0);
-                        uint8_t* qt = sm + (r >> 7) * TR_TILE_BYTES + sw128_off(r & 127, u8);
+                        lo = __ldg(q + r * 16 + u8);
+                        hi = __ldg(q + r * 16 + 8 + u8);
+                        angles((uint32_t)(prefix + max(__popcll(s->sees[(base + r) % T]) - 1, 0)), cs, sn);
+                        rg = rotate_regs_f16(lo, hi, cs, sn, 0);
+                    }
+#pragma unroll
+                    for (int x = 0; x < Sh::COPIES; ++x) {
+                        uint8_t* qt = sm + sw128_off(x * RR + r, u8);
                         *reinterpret_cast<uint4*>(qt) = lo;
                         *reinterpret_cast<uint4*>(qt + 16384) = hi;
                     }
-                    const bool bad = any8(in && range_exceeded(range));
-                    if (in && u8 == 0) c->qbad[nq & 1][r] = bad;
+                    const bool bad = any8(range_exceeded(rg));
+                    if (u8 == 0) c->qbad[nq & 1][r] = bad;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -680,26 +687,23 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 if (!(ok = wait_all(c->k_full[kst], g / TR_KSTAGES))) break;
                 uint8_t* kt = sm + Sh::OFF_K + kst * TR_TILE_BYTES;
                 const int keys = min(TR_BN, n_keys - i * TR_BN);
+                uint4 lo[ROWS], hi[ROWS];  // all of the thread's rows are read before any is rotated
 #pragma unroll
-                for (int m0 = 0; m0 < ROWS; m0 += 4) {  // four rows are read before any is rotated
-                    uint4 lo[4], hi[4];
+                for (int m = 0; m < ROWS; ++m) {
+                    const uint32_t off = sw128_off(r0 + TR_ROW_STEP * m, u8);
+                    lo[m] = *reinterpret_cast<const uint4*>(kt + off);
+                    hi[m] = *reinterpret_cast<const uint4*>(kt + 16384 + off);
+                }
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const uint32_t off = sw128_off(r0 + Sh::ROW_STEP * (m0 + m), u8);
-                        lo[m] = *reinterpret_cast<const uint4*>(kt + off);
-                        hi[m] = *reinterpret_cast<const uint4*>(kt + 16384 + off);
+                for (int m = 0; m < ROWS; ++m) {
+                    const int r = r0 + TR_ROW_STEP * m;
+                    if (r < keys) {
+                        range = rotate_regs_f16(lo[m], hi[m], cs, sn, range);
+                        const uint32_t off = sw128_off(r, u8);
+                        *reinterpret_cast<uint4*>(kt + off) = lo[m];
+                        *reinterpret_cast<uint4*>(kt + 16384 + off) = hi[m];
                     }
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const int r = r0 + Sh::ROW_STEP * (m0 + m);
-                        if (r < keys) {
-                            range = rotate_regs_f16(lo[m], hi[m], cs, sn, range);
-                            const uint32_t off = sw128_off(r, u8);
-                            *reinterpret_cast<uint4*>(kt + off) = lo[m];
-                            *reinterpret_cast<uint4*>(kt + 16384 + off) = hi[m];
-                        }
-                        rope_step(cs, sn, dcs, dsn);
-                    }
+                    rope_step(cs, sn, dcs, dsn);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -712,11 +716,12 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 if (!(ok = wait_all(c->k_full[kst], g / TR_KSTAGES))) break;
                 uint8_t* kt = sm + Sh::OFF_K + kst * TR_TILE_BYTES;
 #pragma unroll 1
-                for (int rr = 0; rr < last; rr += Sh::ROW_STEP) {
+                for (int rr = 0; rr < last; rr += TR_ROW_STEP) {
                     const int r = rr + r0, node = r - off0;
-                    const int d = node < 0 ? node : r < last ? s->depth[node] : 255;
+                    // (d: how far from the end of the prefix; the page's own keys lie before it)
+                    const int d = node < 0 ? node : r < last ? __popcll(s->sees[node]) - 1 : -1;
                     bool bad = false;
-                    if (d != 255) {
+                    if (node < 0 || d >= 0) {
                         angles((uint32_t)(prefix + d), cs, sn);
                         const uint32_t off = sw128_off(r, u8);
                         const uint32_t rg = rotate_chunk_f16(kt + off, kt + 16384 + off, cs, sn, 0);
@@ -739,176 +744,217 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Sh::REG_S));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_S));
         // ================================================== softmax ====
-        const int j = TILES == 1 ? 0 : wg - 1;
-        const int rt = tid & 127, rj = 128 * j + rt;      // row of the q-tile (TMEM lane), of the item
+        constexpr int COLS = Sh::COLS, PARTS = Sh::PARTS, CH = COLS < 32 ? COLS : 32;  // CH: columns at a time
+        const int t = tid - 32 * WARP_S0, wg = t >> 7, ln = t & 127;  // warpgroup, lane of tensor memory
+        const int r = ln % RR, part = wg * Sh::COPIES + ln / RR;      // the thread's query, which of its threads it is
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tO = tmem + 256 + j * 128 + lane_addr;
         const float scl = a.qk_scale_log2;
-        int g0 = 0, nu = 0, np = 0;                       // tiles before the item (CTA), items and tiles of this q-tile
+        int g = 0;                                        // tiles so far
         bool ok = true;
-        for (int k = 0; ok; ++k) {
+        // The warps leave the loop together: one whose wait gave up goes on to the next barrier, which tells the others.
+        auto wait = [&](uint64_t& bar, int parity) {
+            if (ok) ok = wait_all(bar, parity);
+        };
+        for (int k = 0;; ++k) {
             TrSlot* s = &c->slot[k % TR_SLOTS];
-            if (!(ok = wait_all(c->u_full[k % TR_SLOTS], k / TR_SLOTS))) break;
+            wait(c->u_full[k % TR_SLOTS], k / TR_SLOTS);
+            if (named_bar_or(1, TR_SOFTMAX, !ok)) {
+                ok = false;
+                break;
+            }
             const volatile TrUnit* u = &s->u;
             if (u->end) break;
             const int n_keys = u->n_keys, prefix = u->prefix, tree = u->tree, rows = u->rows;
             const int npt = (n_keys + TR_BN - 1) / TR_BN, n_tiles = npt + tree;
-            if (128 * j >= rows) {  // this q-tile has no rows (the other one has)
-                ok = wait_all(c->r_full[k & 1], k >> 1);
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&c->r_empty[k & 1]));
-                    mbar_arrive(smem_u32(&c->u_empty[k % TR_SLOTS]));
-                }
-                g0 += n_tiles;
-                ++done;
-                continue;
-            }
-            const bool live_warp = 128 * j + (warp & 3) * 32 < rows;
-            const int node = (u->pair * SPAN + rj) % T;
-            const uint64_t sees = rj < rows ? s->sees[node] : 0ull;
+            const uint64_t sees = r < rows ? s->sees[(u->block * TR_SPAN + r) % T] : 0ull;
+            const uint32_t tO = tmem + 256 + (k & 1) * RR + wg * COLS + lane_addr;
             float m = -INFINITY, l = 0.0f;
-            for (int i = 0; i < n_tiles; ++i) {
-                const int g = g0 + i, buf = TILES == 1 ? g & 1 : j;
-                if (!(ok = wait_all(c->s_full[buf], TILES == 1 ? g >> 1 : np + i))) break;
-                if (live_warp) {
-                    tc_fence_after();
-                    const uint32_t tS = tmem + buf * 128 + lane_addr;
-                    uint32_t xr[128];
+            for (int i = 0; i < n_tiles; ++i, ++g) {
+                // the thread's visible columns: whole pages of the prefix, or the prefix's keys and the nodes that the
+                // query sees (tile_cols is the number of either)
+                const uint32_t tS = tmem + (g & 1) * 128 + part * COLS + lane_addr;
+                uint32_t see[COLS / CH];
 #pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4) tmem_ld32(tS + c4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&xr[c4 * 32]));
-                    tmem_ld_wait();
-                    if (i >= npt) {  // the tree's tile: the prefix's keys, then the nodes that this one sees
-                        const int off = prefix & (PAGE - 1);
-                        const uint32_t w0 = (uint32_t)((sees << off) | ((1ull << off) - 1ull)), w1 = (uint32_t)((sees << off) >> 32);
-                        const uint32_t w2 = off ? (uint32_t)(sees >> (64 - off)) : 0u;
-#pragma unroll
-                        for (int x = 0; x < 128; ++x) {
-                            const uint32_t w = x < 32 ? w0 : x < 64 ? w1 : x < 96 ? w2 : 0u;
-                            xr[x] = (w >> (x & 31)) & 1u ? xr[x] : 0xff800000u;
-                        }
+                for (int h = 0; h < COLS / CH; ++h) {
+                    const int c0 = part * COLS + h * CH;
+                    if (i < npt) {
+                        const int left = n_keys - i * TR_BN - c0;
+                        see[h] = left >= CH ? 0xffffffffu : left > 0 ? 0xffffu : 0u;
                     } else {
-                        const int lim = n_keys - i * TR_BN;
-                        if (lim < TR_BN) {
-#pragma unroll
-                            for (int x = 0; x < 128; ++x) xr[x] = x < lim ? xr[x] : 0xff800000u;
-                        }
+                        const int at = c0 - (prefix & (PAGE - 1));  // the node of the first column (before 0: prefix)
+                        see[h] = at >= 64 ? 0u : at >= 0 ? (uint32_t)(sees >> at) : (uint32_t)(sees << -at) | ((1u << -at) - 1u);
                     }
-                    float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-                    for (int x = 0; x < 128; x += 4) {
-                        mx0 = fmaxf(mx0, __uint_as_float(xr[x]));
-                        mx1 = fmaxf(mx1, __uint_as_float(xr[x + 1]));
-                        mx2 = fmaxf(mx2, __uint_as_float(xr[x + 2]));
-                        mx3 = fmaxf(mx3, __uint_as_float(xr[x + 3]));
-                    }
-                    const float mt = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * scl;
-                    float alpha = 1.0f;
-                    bool resc = false;
-                    if (mt > m + TR_SLACK) {
-                        alpha = ex2(m - mt);
-                        m = mt;
-                        resc = true;
-                    }
-                    const float nm = m == -INFINITY ? 0.0f : -m;
-                    const float2 sc2 = make_float2(scl, scl), nm2 = make_float2(nm, nm);
-                    float2 acc2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-                    for (int x = 0; x < 128; x += 2) {
-                        const float2 t = ffma2(make_float2(__uint_as_float(xr[x]), __uint_as_float(xr[x + 1])), sc2, nm2);
-                        const float2 e = make_float2(ex2(t.x), ex2(t.y));
-                        acc2 = fadd2(acc2, e);
-                        xr[x >> 1] = pack_bf16x2(e.x, e.y);
-                    }
-                    l = l * alpha + (acc2.x + acc2.y);
-                    if (i > 0 && __any_sync(0xffffffffu, resc)) {
-                        // PV of the tile before has to be in O (TILES = 2: S of this tile was issued behind it)
-                        if (TILES == 1 && !(ok = wait_all(c->pv_done[(g - 1) & 1], (g - 1) >> 1))) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c4 = 0; c4 < 4; ++c4) {
-                            uint32_t rr[32];
-                            tmem_ld32(tO + c4 * 32, rr);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int x = 0; x < 32; ++x) rr[x] = __float_as_uint(__uint_as_float(rr[x]) * alpha);
-                            tmem_st32(tO + c4 * 32, rr);
-                        }
-                    }
-                    tmem_st32(tS, *reinterpret_cast<uint32_t(*)[32]>(&xr[0]));
-                    tmem_st32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&xr[32]));
-                    tmem_st_wait();
-                    tc_fence_before();
                 }
+                wait(c->s_full[g & 1], g >> 1);
+                uint32_t xr[CH];
+                float mx = -INFINITY;
+                auto take = [&](int h) {  // columns h * CH .. of the thread, what is hidden at -inf
+                    tmem_load(tS + h * CH, xr);
+                    tmem_ld_wait();
+                    if (__any_sync(0xffffffffu, (~see[h] << (32 - CH)) != 0u)) {
+#pragma unroll
+                        for (int x = 0; x < CH; ++x) xr[x] = (see[h] >> x) & 1u ? xr[x] : 0xff800000u;
+                    }
+                };
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < COLS / CH; ++h) {
+                        take(h);
+                        float m0 = mx, m1 = __uint_as_float(xr[1]);
+#pragma unroll
+                        for (int x = 0; x < CH; x += 4) {
+                            m0 = fmaxf(fmaxf(m0, __uint_as_float(xr[x])), __uint_as_float(xr[x + 2]));
+                            m1 = fmaxf(fmaxf(m1, __uint_as_float(xr[x + 1])), __uint_as_float(xr[x + 3]));
+                        }
+                        mx = fmaxf(m0, m1);
+                    }
+                }
+                float mt = mx * scl;
+                if (named_bar_or(1, TR_SOFTMAX, mt > m + TR_SLACK || !ok)) {
+                    // some query's maximum moves (or a wait gave up)
+                    c->ex[part * RR + r] = mt;
+                    if (named_bar_or(1, TR_SOFTMAX, !ok)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int x = 0; x < PARTS; ++x) mt = fmaxf(mt, c->ex[x * RR + r]);
+                    float alpha = 1.0f;
+                    if (mt > m + TR_SLACK) {
+                        alpha = ex2(m - mt);  // 0 for the first
+                        m = mt;
+                    }
+                    l *= alpha;
+                    if (i > 0) {
+                        if (named_bar_or(1, TR_SOFTMAX, alpha != 1.0f)) {  // (and the maxima have been read)
+                            if (part == 0) c->ex[r] = alpha;
+                            wait(c->pv_done[(g - 1) & 1], (g - 1) >> 1);
+                            if (named_bar_or(1, TR_SOFTMAX, !ok)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll
+                            for (int h = 0; h < COLS / CH; ++h) {
+                                uint32_t rr[CH];
+                                tmem_load(tO + h * CH, rr);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int x = 0; x < CH; ++x) rr[x] = __float_as_uint(__uint_as_float(rr[x]) * c->ex[wg * COLS + h * CH + x]);
+                                tmem_store(tO + h * CH, rr);
+                            }
+                            tmem_st_wait();
+                        }
+                    }
+                    named_bar_sync(1, TR_SOFTMAX);  // the exchange may be written again
+                }
+                // P^T's buffer: read by PV of the tile PBUF before this one
+                if (g >= Sh::PBUF) wait(c->pv_done[(g - Sh::PBUF) & 1], (g - Sh::PBUF) >> 1);
+                if (!ok) continue;  // leaves at the next barrier, with the others
+                const float nm = m == -INFINITY ? 0.0f : -m;
+                const float2 sc2 = make_float2(scl, scl), nm2 = make_float2(nm, nm);
+                float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
+                uint8_t* prow = sm + Sh::OFF_P + (g % Sh::PBUF) * Sh::P_BYTES;
+#pragma unroll
+                for (int h = 0; h < COLS / CH; ++h) {
+                    if (COLS > CH) take(h);
+                    uint32_t pr[CH / 2];
+#pragma unroll
+                    for (int x = 0; x < CH; x += 4) {
+                        const float2 t0 = ffma2(make_float2(__uint_as_float(xr[x]), __uint_as_float(xr[x + 1])), sc2, nm2);
+                        const float2 t1 = ffma2(make_float2(__uint_as_float(xr[x + 2]), __uint_as_float(xr[x + 3])), sc2, nm2);
+                        const float2 e0 = make_float2(ex2(t0.x), ex2(t0.y)), e1 = make_float2(ex2(t1.x), ex2(t1.y));
+                        acc0 = fadd2(acc0, e0);
+                        acc1 = fadd2(acc1, e1);
+                        pr[x >> 1] = pack_bf16x2(e0.x, e0.y);
+                        pr[(x >> 1) + 1] = pack_bf16x2(e1.x, e1.y);
+                    }
+                    const int col = part * COLS + h * CH;  // chunks of 8 keys of the query's row of P^T
+#pragma unroll
+                    for (int x = 0; x < CH / 8; ++x)
+                        *reinterpret_cast<uint4*>(prow + (col >> 6) * (RR * 128) + sw128_off(r, ((col & 63) >> 3) + x)) =
+                            make_uint4(pr[4 * x], pr[4 * x + 1], pr[4 * x + 2], pr[4 * x + 3]);
+                }
+                l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                tc_fence_before();
+                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&c->p_ready[buf]));
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&c->s_free[g & 1]));
+                    mbar_arrive(smem_u32(&c->p_ready[g % Sh::PBUF]));
+                }
             }
-            if (ok) ok = wait_all(c->o_done[j], nu);
-            if (ok) ok = wait_all(c->r_full[k & 1], k >> 1);
-            if (!ok) break;
+            if (!ok) {
+                if (named_bar_or(1, TR_SOFTMAX, true)) break;
+            }
             // ---- the item's results ----
-            tc_fence_after();
-            bool fail = false;
-            {
-                const uint64_t xb = *reinterpret_cast<const uint64_t*>(c->xbad[k & 1]);
-                fail = (TILES == 1 ? xb : xb & 0xffffffffull) != 0;
+            wait(c->r_full[k & 1], k >> 1);
+            c->ex[part * RR + r] = l;
+            if (named_bar_or(1, TR_SOFTMAX, !ok)) {
+                ok = false;
+                break;
+            }
+            const size_t row0 = first_row(a, u->b, u->kvh) + u->block * TR_SPAN;
+            const int direct = u->direct, split = u->split, nqp = u->nq & 1;
+            float inv = 0.0f;
+            if (t < RR) {  // part 0 of query t, whole warps
+                float sum = 0.0f;
+#pragma unroll
+                for (int x = 0; x < PARTS; ++x) sum += c->ex[x * RR + r];
+                bool fail = *reinterpret_cast<const uint64_t*>(c->xbad[k & 1]) != 0;
                 if (tree) {
                     const int off = prefix & (PAGE - 1);
-                    const uint32_t b0 = __ballot_sync(0xffffffffu, lane < T && c->kbad[k & 1][off + lane]);
+                    const uint32_t b0 = __ballot_sync(0xffffffffu, lane < T && c->kbad[k & 1][off + min(lane, TREE_MAX - 1)]);
                     const uint32_t b1 = __ballot_sync(0xffffffffu, lane + 32 < T && c->kbad[k & 1][off + min(lane + 32, TREE_MAX - 1)]);
                     fail |= (sees & (((uint64_t)b1 << 32) | b0 | c->vbad[k & 1])) != 0;
                 }
-                if (rj < rows) fail |= c->qbad[u->nq & 1][rj] != 0;
-            }
-            const bool empty = sees == 0, direct = u->direct;
-            const size_t row = first_row(a, u->b, u->kvh) + u->pair * SPAN + rj;
-            const bool zero = empty || fail || !(l > 0.0f);
-            const float inv = zero ? 0.0f : 1.0f / l;
-            if (live_warp) {
-                const bool in = rj < rows;
-                const float lse2 = empty ? -INFINITY : fail ? __int_as_float(0x7fc00000) : m + log2f(l);
-                float* part = nullptr;
-                if (!direct) {
-                    const size_t p = ((size_t)u->b * a.Hkv + u->kvh) * a.n_splits + u->split;
-                    const int r = u->pair * SPAN + rj;
-                    if (in) a.lse_part[p * a.Rp + r] = lse2;
-                    part = a.o_part + p * a.Rp * HEAD_DIM + r;
-                } else if (in) {
-                    a.lse[row] = lse2 * 0.693147180559945309f;
+                fail |= c->qbad[nqp][r] != 0;
+                const bool empty = sees == 0;
+                if (!empty && !fail && sum > 0.0f) inv = 1.0f / sum;
+                if (r < rows) {
+                    const float lse2 = empty ? -INFINITY : fail ? __int_as_float(0x7fc00000) : m + log2f(sum);
+                    if (direct) a.lse[row0 + r] = lse2 * 0.693147180559945309f;
+                    else a.lse_part[(row0 + r) * a.n_splits + split] = lse2;
+                    if (fail && !empty && a.status) atomicOr(a.status, RK_STATUS_RANGE);
                 }
-                if (in && fail && !empty && a.status) atomicOr(a.status, RK_STATUS_RANGE);
-                uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + row * HEAD_DIM);
-#pragma unroll 1
-                for (int c4 = 0; c4 < 4; ++c4) {
-                    uint32_t rr[32];
-                    tmem_ld32(tO + c4 * 32, rr);
-                    tmem_ld_wait();
-                    if (!in) continue;
-                    float f[32];
+            }
+            named_bar_sync(1, TR_SOFTMAX);  // the sums have been read
+            if (t < RR) c->ex[r] = inv;
+            wait(c->o_done[k & 1], k >> 1);
+            if (named_bar_or(1, TR_SOFTMAX, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // thread: dim ln of queries wg * COLS ..
+            float* part_o = a.o_part + (row0 * a.n_splits + split) * HEAD_DIM + ln;
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + row0 * HEAD_DIM + ln;
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) f[x] = zero ? 0.0f : __uint_as_float(rr[x]) * inv;
-                    if (direct) {
+            for (int h = 0; h < COLS / CH; ++h) {
+                uint32_t rr[CH];
+                tmem_load(tO + h * CH, rr);
+                tmem_ld_wait();
 #pragma unroll
-                        for (int x = 0; x < 32; x += 8)
-                            o[(c4 * 32 + x) / 8] = make_uint4(pack_bf16x2(f[x], f[x + 1]), pack_bf16x2(f[x + 2], f[x + 3]),
-                                                              pack_bf16x2(f[x + 4], f[x + 5]), pack_bf16x2(f[x + 6], f[x + 7]));
-                    } else {  // a row to a lane: the warp writes a run of 32 rows of each dim
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) part[(size_t)(c4 * 32 + x) * a.Rp] = f[x];
+                for (int x = 0; x < CH; ++x) {
+                    const int qr = wg * COLS + h * CH + x;
+                    const float f = c->ex[qr];
+                    const float y = f == 0.0f ? 0.0f : __uint_as_float(rr[x]) * f;  // (a failed query's O may be NaN)
+                    if (qr < rows) {
+                        if (direct) out[(size_t)qr * HEAD_DIM] = __float2bfloat16_rn(y);
+                        else part_o[(size_t)qr * a.n_splits * HEAD_DIM] = y;
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(smem_u32(&c->o_free[j]));
+                mbar_arrive(smem_u32(&c->o_free[k & 1]));
                 mbar_arrive(smem_u32(&c->r_empty[k & 1]));
                 mbar_arrive(smem_u32(&c->u_empty[k % TR_SLOTS]));
             }
-            g0 += n_tiles;
-            np += n_tiles;
-            ++nu;
             ++done;
         }
     }
@@ -919,90 +965,115 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     __syncthreads();
     if (warp == WARP_MMA) {
         tc_fence_after();
-        tmem_dealloc(tmem, TR_TMEM_COLS);
+        tmem_dealloc(tmem, Sh::TMEM_COLS);
     }
     if (pipe_aborted(pc)) {
-        // A wait gave up.  What the first softmax warp has not written of this CTA's items (the others may
-        // be one further) is written as failed by all of it, rows without keys among them.
-        if (tid == 128 * (TILES == 1 ? 2 : 1)) c->total = done;
+        // A wait gave up.  What the softmax warps have not written of this CTA's items is written as failed,
+        // rows without keys among them.
+        if (tid == 32 * WARP_S0) *reinterpret_cast<int*>(c->ex) = done;
         __syncthreads();
-        int skip = c->total;
-        for (TrItems it = *reinterpret_cast<const TrItems*>(c->first); it.valid(a); it.next(a, heads)) {
+        int skip = *reinterpret_cast<const int*>(c->ex);
+        TrItems it;
+        for (it.start(a, c->total, c->pre, heads, (int)blockIdx.x); it.valid(a, heads); it.next(a, c->total, c->pre, heads)) {
             const bool publishes = it.n >= 0 && !it.bad;
             if (publishes && skip > 0) {
                 --skip;
                 continue;
             }
-            write_nothing(a, it.b, it.h / pairs, it.h % pairs, it.s, it.ns == 1, __int_as_float(0x7fc00000), tid, TR_THREADS, SPAN);
+            const int h = it.head(heads);
+            write_nothing(a, it.b, h / blocks, h % blocks, it.s, it.ns == 1, __int_as_float(0x7fc00000), tid, TR_THREADS);
         }
         if (tid == 0 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
     }
 }
 
-// Merge of the parts of 32 accumulator rows (a row to a lane) for 16 of the dims: weights
-// 2^(lse_s - max lse), eight sums over the parts s = w, w + 8, ... (one to a warp) in ascending
-// order, added up in order of w: fixed by the row's number of parts.  A NaN part fails the row, no visible
-// key gives out = 0, lse = -inf.
-constexpr int MG_DIMS = 16;
+// Merge of a query's parts: weights 2^(lse_s - max lse), eight sums over the parts s = e, e + 8, ... in
+// ascending order, added up in order of e: fixed by the row's number of parts.  A NaN part fails the query, no
+// visible key gives out = 0, lse = -inf.  WIDE = false: a warp has a query and all eight sums, four dims to a
+// lane; WIDE = true: a block has a query and a warp a sum.  Both add in the same order.
+template <bool WIDE>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeArgs a) {
-    __shared__ float acc_s[8][MG_DIMS][33], sum_s[8][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int R = a.G * a.T, groups = (R + 31) / 32;
-    const int d0 = (int)(blockIdx.x % (HEAD_DIM / MG_DIMS)) * MG_DIMS;
-    const int grp = (int)(blockIdx.x / (HEAD_DIM / MG_DIMS)) % groups;
-    const size_t bh = blockIdx.x / (HEAD_DIM / MG_DIMS) / groups;
+    constexpr int SUMS = WIDE ? 1 : 8;
+    __shared__ float4 acc_s[WIDE ? 8 : 1][32];
+    __shared__ float sum_s[8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = WIDE ? warp : 0;
+    const size_t row = WIDE ? blockIdx.x : (size_t)blockIdx.x * 8 + warp, all = (size_t)a.B * a.Hq * a.T;
     int kv, bad0;
-    const int ns = parts_of(a, row_pages16(a, (int)(bh / a.Hkv), kv, bad0));
+    const int ns = row < all ? parts_of(a, row_pages16(a, (int)(row / ((size_t)a.Hq * a.T)), kv, bad0)) : 1;
     griddep_wait();  // the parts are complete and visible
     if (ns <= 1) return;
-    const int r = grp * 32 + lane;
-    const bool in = r < R;
-    const float* lp = a.lse_part + bh * a.n_splits * a.Rp + (in ? r : 0);
-    const float* op = a.o_part + (bh * a.n_splits * HEAD_DIM + d0) * (size_t)a.Rp + (in ? r : 0);
+    const float* lp = a.lse_part + row * a.n_splits;
+    const float4* op = reinterpret_cast<const float4*>(a.o_part + row * a.n_splits * HEAD_DIM) + lane;
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4 x[SUMS];
+    float wt[SUMS];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int e = 0; e < SUMS; ++e) {
+            const int s = s0 + e0 + e;
+            x[e] = s < ns ? op[(size_t)s * 32] : zero;
+            wt[e] = s < ns ? lp[s] : -INFINITY;
+        }
+    };
+    load(0);
     float m = -INFINITY;
     bool bad = false;
-#pragma unroll 8
-    for (int s = 0; s < ns; ++s) {
-        const float v = lp[(size_t)s * a.Rp];
+    for (int s = lane; s < ns; s += 32) {
+        const float v = lp[s];
         bad |= v != v;
         m = fmaxf(m, v);
     }
-    float acc[MG_DIMS], sum = 0.0f;
 #pragma unroll
-    for (int d = 0; d < MG_DIMS; ++d) acc[d] = 0.0f;
-    if (!bad && m > -INFINITY) {
-        for (int s = warp; s < ns; s += 8) {
-            const float w = ex2(lp[(size_t)s * a.Rp] - m);
-            const float* o = op + (size_t)s * HEAD_DIM * a.Rp;
-            float x[MG_DIMS];
-#pragma unroll
-            for (int d = 0; d < MG_DIMS; ++d) x[d] = o[(size_t)d * a.Rp];
-            sum += w;
-#pragma unroll
-            for (int d = 0; d < MG_DIMS; ++d) acc[d] = fmaf(w, x[d], acc[d]);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    bad = __any_sync(0xffffffffu, bad);
+    uint2* out = reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + row * HEAD_DIM) + lane;
+    if (bad || m == -INFINITY) {  // (the same in every warp of a block)
+        if (e0 == 0) {
+            *out = make_uint2(0, 0);
+            if (lane == 0) a.lse[row] = bad ? __int_as_float(0x7fc00000) : -INFINITY;
         }
+        return;
+    }
+    float4 acc[SUMS];
+    float sum[SUMS];
+#pragma unroll
+    for (int e = 0; e < SUMS; ++e) {
+        acc[e] = zero;
+        sum[e] = 0.0f;
+    }
+    for (int s0 = 0; s0 < ns;) {
+#pragma unroll
+        for (int e = 0; e < SUMS; ++e) {
+            const float w = ex2(wt[e] - m);
+            sum[e] += w;
+            acc[e].x = fmaf(w, x[e].x, acc[e].x);
+            acc[e].y = fmaf(w, x[e].y, acc[e].y);
+            acc[e].z = fmaf(w, x[e].z, acc[e].z);
+            acc[e].w = fmaf(w, x[e].w, acc[e].w);
+        }
+        s0 += 8;
+        if (s0 < ns) load(s0);
+    }
+    float4 y = acc[0];
+    float l = sum[0];
+    if constexpr (WIDE) {
+        acc_s[e0][lane] = acc[0];
+        if (lane == 0) sum_s[e0] = sum[0];
+        __syncthreads();
+        if (e0) return;
     }
 #pragma unroll
-    for (int d = 0; d < MG_DIMS; ++d) acc_s[warp][d][lane] = acc[d];
-    sum_s[warp][lane] = sum;
-    __syncthreads();
-    float l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) l += sum_s[w][lane];
-    const float inv = bad || m == -INFINITY ? 0.0f : 1.0f / l;
-    // warp w: dims 2 w, 2 w + 1
-    float y[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) v += acc_s[w][2 * warp + e][lane];
-        y[e] = v * inv;
+    for (int e = 1; e < 8; ++e) {
+        const float4 z = WIDE ? acc_s[WIDE ? e : 0][lane] : acc[e % SUMS];
+        y.x += z.x;
+        y.y += z.y;
+        y.z += z.z;
+        y.w += z.w;
+        l += WIDE ? sum_s[e] : sum[e % SUMS];
     }
-    if (!in) return;
-    const size_t row = bh * R + r;
-    reinterpret_cast<uint32_t*>(a.out)[(row * HEAD_DIM + d0) / 2 + warp] = pack_bf16x2(y[0], y[1]);
-    if (d0 == 0 && warp == 0) a.lse[row] = bad ? __int_as_float(0x7fc00000) : m == -INFINITY ? m : (m + log2f(l)) * 0.693147180559945309f;
+    const float inv = 1.0f / l;
+    *out = make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+    if (lane == 0) a.lse[row] = (m + log2f(l)) * 0.693147180559945309f;
 }
 
 std::atomic<uint64_t> g_configured{0};
@@ -1016,24 +1087,28 @@ cudaError_t launch_tree(const CUtensorMap& km, const CUtensorMap& vm, const Tree
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(g_configured.load() & bit)) {
-        if ((e = cudaFuncSetAttribute(tree_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, tr_smem_bytes<1>())) != cudaSuccess) return e;
-        if ((e = cudaFuncSetAttribute(tree_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, tr_smem_bytes<2>())) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(tree_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize, tr_smem_bytes<32>())) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(tree_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, tr_smem_bytes<64>())) != cudaSuccess) return e;
+        if ((e = cudaFuncSetAttribute(tree_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, tr_smem_bytes<128>())) != cudaSuccess) return e;
         if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
         if (bit) g_sms[dev].store(sms);
         g_configured.fetch_or(bit);
     } else {
         sms = g_sms[dev].load();
     }
-    const int R = a.G * a.T, tiles = R > 128 ? 2 : 1;
-    const long long most = (long long)a.B * a.Hkv * ((R + 128 * tiles - 1) / (128 * tiles)) * a.n_splits;
-    const unsigned grid = (unsigned)(most < sms ? most : sms);
-    if (tiles == 1) tree_kernel<1><<<grid, TR_THREADS, tr_smem_bytes<1>(), stream>>>(km, vm, a);
-    else tree_kernel<2><<<grid, TR_THREADS, tr_smem_bytes<2>(), stream>>>(km, vm, a);
+    // as many runs to a KV head and block of queries as SMs, and no more than it can have parts
+    const int R = a.G * a.T, heads = a.Hkv * ((R + TR_SPAN - 1) / TR_SPAN);
+    TreeArgs r = a;
+    r.members = (int)std::min<long long>(std::max(1, sms / heads), (long long)a.B * a.n_splits);
+    const unsigned grid = (unsigned)std::min(sms, heads * r.members);
+    if (R <= 32) tree_kernel<32><<<grid, TR_THREADS, tr_smem_bytes<32>(), stream>>>(km, vm, r);
+    else if (R <= 64) tree_kernel<64><<<grid, TR_THREADS, tr_smem_bytes<64>(), stream>>>(km, vm, r);
+    else tree_kernel<128><<<grid, TR_THREADS, tr_smem_bytes<128>(), stream>>>(km, vm, r);
     if ((e = cudaGetLastError()) != cudaSuccess || a.n_splits <= 1) return e;
-    const long long blocks = (long long)a.B * a.Hkv * ((R + 31) / 32) * (HEAD_DIM / MG_DIMS);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const long long rows = (long long)a.B * a.Hq * a.T;
+    const bool wide = a.n_splits > 32;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 7) / 8));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
@@ -1041,7 +1116,7 @@ cudaError_t launch_tree(const CUtensorMap& km, const CUtensorMap& vm, const Tree
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel, a);
+    return wide ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<true>, a) : cudaLaunchKernelEx(&cfg, tree_merge_kernel<false>, a);
 }
 
 }  // namespace rk

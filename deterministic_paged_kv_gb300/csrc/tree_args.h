@@ -23,11 +23,12 @@ struct TreeArgs {
     uint32_t wait_limit_ns;
     int32_t timeout_drill;
     // where a row's prefix is cut: zones of equal parts from a token (and part) on; with more than one part to
-    // the widest row: partial O / l [B, Hkv, n_splits, D, Rp] and log2-domain LSE [B, Hkv, n_splits, Rp]
+    // the widest row: partial O / l [B, Hq, T, n_splits, D] and log2-domain LSE [B, Hq, T, n_splits]
     struct {
         int32_t split, token, size;
     } zone[2];
-    int32_t n_splits, Rp;         // Rp: queries of a KV head (G T), rounded up to 8
+    int32_t members;              // runs that a head's items are dealt to (set at the launch)
+    int32_t n_splits;
     float* o_part;
     float* lse_part;
     uint64_t rope_turns[ROPE_PAIRS];
