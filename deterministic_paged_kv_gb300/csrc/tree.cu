@@ -34,11 +34,14 @@
 //   warps 16, 18 TMA producers of K and V pages; warp 18 cleans the tree's V tile;
 //   warp 17      MMA issuer: S of the next tile before PV of this one (S, and O^T by item, have two buffers);
 //   warp 19      scheduler: walks the items, checks their metadata, publishes them.
+// Loops are rolled: twenty warps in six roles go through their code once a tile, and code of some hundred
+// instructions in a row was fetched anew each time (an MMA issued every 150 cycles, a wait on a barrier that had
+// completed took 300).
 #include <algorithm>
 #include <atomic>
 #include <cstring>
 
-#include "rk_device.cuh"
+#include "q8_device.cuh"
 #include "tree_args.h"
 
 namespace rk {
@@ -55,7 +58,7 @@ constexpr int TR_TILE_BYTES = TR_BN * HEAD_DIM * 2;       // 32 KiB
 constexpr int TR_KSTAGES = 3, TR_VSTAGES = 2;
 constexpr int TR_TREE_ROWS = 80;                          // keys of the tree's tile: 15 + 64, whole pages
 constexpr float TR_SLACK = 8.0f;                          // the running max moves when it grows by more (log2)
-constexpr int TR_SLOTS = 2;                               // items published ahead
+constexpr int TR_SLOTS = 3;                               // items published ahead
 constexpr int TR_ROW_STEP = TR_XW * 4;                    // rows between a transform thread's rows
 constexpr int TR_ANCHOR = 8;                              // tiles between exact angles
 constexpr int TR_GROUPS = 32;                             // row groups of the item search
@@ -85,13 +88,14 @@ struct TrUnit {
     int t0, n_keys;          // its prefix keys [t0, t0 + n_keys), whole pages
     int tree;                // 1: the tree's tile follows them
     int prefix;              // tokens before the tree
-    int newq, endq, nq;      // first / last item of its queries, their number in this CTA
+    int newq, nq;            // first item of its queries, their number in this CTA
     int direct;              // 1: the row has one part
     int rows;                // live queries of the item
 };
 struct TrSlot {
     TrUnit u;
-    uint64_t sees[TREE_MAX];   // node's ancestors and itself (0: unused); its depth is one less than their number
+    int8_t up[TREE_MAX];       // parents of the nodes (below 0: none)
+    uint8_t depth[TREE_MAX];   // 255: unused
 };
 
 // ------------------------------------------------------------ geometry ----
@@ -196,15 +200,17 @@ struct TrCtrl {
     uint64_t vbad[2];                 // nodes whose V is not finite, by item parity
     uint8_t xbad[2][TR_XW];           // a transform warp met a prefix key out of range
     uint8_t kbad[2][TR_TREE_ROWS];    // keys of the tree's tile out of range
-    uint8_t qbad[2][TR_SPAN];         // queries out of range, by the queries' parity
+    uint8_t qbad[2][TR_SPAN / 4];     // queries out of range, four to a byte, by the queries' parity
     alignas(16) TrSlot slot[TR_SLOTS];
-    // exchange of the softmax threads: maxima, then scales of O^T; at the end sums, then factors
+    // exchange of the softmax threads: maxima, or scales of O^T, or an item's factors (its sums, of all parts
+    // but the first, lie behind this block)
     alignas(16) float ex[TR_SOFTMAX];
 };
 template <int RR>
 constexpr int tr_smem_bytes() {
-    static_assert(TrShape<RR>::OFF_CTRL + sizeof(TrCtrl) <= 232448, "tree attention shared memory above the 227 KiB opt-in limit");
-    return TrShape<RR>::OFF_CTRL + (int)sizeof(TrCtrl);
+    constexpr int bytes = TrShape<RR>::OFF_CTRL + (int)sizeof(TrCtrl) + (TrShape<RR>::PARTS - 1) * RR * 4;
+    static_assert(bytes <= 232448, "tree attention shared memory above the 227 KiB opt-in limit");
+    return bytes;
 }
 
 // First query of (row b, KV head kvh) in q, out and lse: its G heads x T nodes follow one another.
@@ -224,35 +230,60 @@ __device__ void write_nothing(const TreeArgs& a, int b, int kvh, int block, int 
     for (int r = i; r < rows; r += count) a.lse[first_row(a, b, kvh) + r0 + r] = lse * 0.693147180559945309f;
 }
 
-// PV of a tile, a whole warp: one k-step per page, O^T[dims x RR] += V^T P^T with V as the pages lie in shared
-// memory (MN-major) and P^T's rows as two blocks of 64 keys (K-major), RR * 128 bytes apart.
-template <int KS, int RR>
-__device__ __forceinline__ void pv_steps(uint32_t d, uint32_t v, uint32_t p, uint32_t idesc, uint32_t acc0, int pages) {
-    if (KS < pages) {
-        asm volatile(
-            "{\n\t.reg .pred q, e;\n\t.reg .b32 al, bl;\n\t.reg .b64 da, db;\n\t"
-            "add.u32 al, %1, %5;\n\tadd.u32 bl, %2, %6;\n\t"
-            "mov.b64 da, {al, %4};\n\tmov.b64 db, {bl, %4};\n\t"
-            "setp.ne.b32 q, %7, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, q;\n\t}" ::"r"(d),
-            "r"(v), "r"(p), "r"(idesc), "r"(DESC_HI), "n"(KS * (4096 >> 4)), "n"(((KS >> 2) * RR * 128 + (KS & 3) * 32) >> 4),
-            "r"(KS > 0 ? 1u : acc0)
-            : "memory");
-        if constexpr (KS + 1 < TR_BN / PAGE) pv_steps<KS + 1, RR>(d, v, p, idesc, acc0, pages);
-    }
+// D[tmem] (+)= A[smem] * B[smem], the first kn of 4 k-steps of 16 values, accumulating from the second on, and at
+// the first iff acc0.  Called by a whole converged warp with uniform operands; one elected lane issues.  a_lo, b_lo:
+// low descriptor words of the first k-step; A_STEP, B_STEP (16-byte units) lead to the next.
+template <uint32_t A_STEP, uint32_t B_STEP>
+__device__ __forceinline__ void mma_f16_x4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc0, int kn) {
+    asm volatile(
+        "{\n\t.reg .pred p, e, t, k;\n\t.reg .b32 al, bl;\n\t.reg .b64 da, db;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, %5, %5;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t"
+        "add.u32 al, %1, %7;\n\tadd.u32 bl, %2, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %3};\n\t"
+        "setp.gt.and.s32 k, %6, 1, e;\n\t"
+        "@k tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, t;\n\t"
+        "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %3};\n\t"
+        "setp.gt.and.s32 k, %6, 2, e;\n\t"
+        "@k tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, t;\n\t"
+        "add.u32 al, al, %7;\n\tadd.u32 bl, bl, %8;\n\tmov.b64 da, {al, %3};\n\tmov.b64 db, {bl, %3};\n\t"
+        "setp.gt.and.s32 k, %6, 3, e;\n\t"
+        "@k tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, t;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(DESC_HI), "r"(idesc), "r"(acc0), "r"(kn), "n"(A_STEP), "n"(B_STEP)
+        : "memory");
 }
 
-// N consecutive columns of the thread's lane (tensor memory), to be waited for.
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[N]) {
-    static_assert(N == 16 || N == 32, "tensor memory load");
-    if constexpr (N == 16) tmem_ld16(taddr, r);
-    else tmem_ld32(taddr, r);
+// One box of a 4-D map, by one elected lane of a converged warp, operands uniform.
+__device__ __forceinline__ void tma_load_4d_elect(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2, int c3, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
+        : "memory");
 }
-template <int N>
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[N]) {
-    if constexpr (N == 16) tmem_st16(taddr, r);
-    else tmem_st32(taddr, r);
+
+// Eight rotation pairs (16 bf16) in FP32, to FP16 in place: (lo, hi) -> (lo c - hi s, hi c + lo s).  rs, ru: running
+// signed and unsigned maxima of the inputs' bits, the largest positive and (if any is below 0) negative one.
+__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2 (&c2)[4], const float2 (&s2)[4], uint32_t& rs, uint32_t& ru) {
+    uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        rs = __vimax3_s16x2(rs, x[k], y[k]);
+        ru = __vimax3_u16x2(ru, x[k], y[k]);
+        const float2 lo = make_float2(bf16lo(x[k]), bf16hi(x[k])), hi = make_float2(bf16lo(y[k]), bf16hi(y[k]));
+        const float2 ns = make_float2(-s2[k].x, -s2[k].y);
+        const float2 u = ffma2(hi, ns, fmul2(lo, c2[k])), v = ffma2(lo, s2[k], fmul2(hi, c2[k]));
+        x[k] = pack_f16x2(u.x, u.y);
+        y[k] = pack_f16x2(v.x, v.y);
+    }
+    a = make_uint4(x[0], x[1], x[2], x[3]);
+    b = make_uint4(y[0], y[1], y[2], y[3]);
+}
+// Did an input reach 2^15 (or was it no number)?
+__device__ __forceinline__ bool too_large(uint32_t rs, uint32_t ru) {
+    return max((int16_t)rs, (int16_t)(rs >> 16)) >= (int)RANGE_LIMIT_BF16 || max(ru & 0xffffu, ru >> 16) >= (RANGE_LIMIT_BF16 | 0x8000u);
 }
 
 // Keys of tile i of an item (whole pages).
@@ -351,7 +382,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             TrItems it;
             it.start(a, c->total, c->pre, heads, (int)blockIdx.x);
             int k = 0, nq = -1, tree_row = -1;            // published items, queries; row whose tree is in registers
-            uint64_t sees[2] = {0, 0};                    // of nodes lane, lane + 32
+            int up0[2] = {-1, -1}, deep[2] = {255, 255};  // of nodes lane, lane + 32
             int tree_bad = 0;
             int lb = -1, lv = -1;                         // queries of the item before
             bool ok = true;
@@ -376,28 +407,28 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                         wrong |= p[e] < TREE_UNUSED || (p[e] >= n && p[e] >= 0);
                         const int pp = of(p, p[e] & 63);
                         wrong |= p[e] >= 0 && pp == TREE_UNUSED;
-                        up[e] = p[e];
-                        sees[e] = p[e] == TREE_UNUSED ? 0ull : 1ull << n;
+                        up[e] = up0[e] = p[e];
+                        deep[e] = p[e] >= 0 ? 1 : 0;
                     }
                     tree_bad = __any_sync(0xffffffffu, wrong) ? RK_STATUS_TREE : 0;
-                    // ancestors: twice as far up with every step
+                    // depths: steps to `up`, twice as far up with every turn
 #pragma unroll 1
-                    for (int step = 0; step < 6 && !tree_bad; ++step) {
-                        uint64_t add[2];
-                        int far[2];
+                    for (int turn = 0; turn < 6 && !tree_bad; ++turn) {
+                        int add[2], far[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int n = up[e] & 63;
-                            const uint64_t lo = __shfl_sync(0xffffffffu, sees[0], n & 31), hi = __shfl_sync(0xffffffffu, sees[1], n & 31);
-                            add[e] = up[e] >= 0 ? (n & 32 ? hi : lo) : 0ull;
-                            far[e] = of(up, n);
+                            add[e] = of(deep, up[e] & 63);
+                            far[e] = of(up, up[e] & 63);
                         }
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            sees[e] |= add[e];
+                            deep[e] += up[e] >= 0 ? add[e] : 0;
                             up[e] = up[e] >= 0 ? far[e] : -1;
                         }
                     }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (p[e] == TREE_UNUSED) deep[e] = 255;
                 }
                 bad |= tree_bad;
                 // page ids of the item's keys
@@ -422,12 +453,12 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     it.next(a, c->total, c->pre, heads);
                 }
             };
-            settle();
             while (ok) {
+                settle();
                 TrUnit u;
                 std::memset(&u, 0, sizeof u);
                 u.end = !it.valid(a, heads);
-                const uint64_t s0 = sees[0], s1 = sees[1];
+                const int u0 = up0[0], u1 = up0[1], d0 = deep[0], d1 = deep[1];
                 if (!u.end) {
                     u.b = it.b;
                     u.kvh = it.head(heads) / blocks;
@@ -445,16 +476,16 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     lb = it.b;
                     lv = it.v;
                     it.next(a, c->total, c->pre, heads);
-                    settle();
-                    u.endq = !it.valid(a, heads) || it.b != lb || it.v != lv;
                 }
                 TrSlot* s = &c->slot[k % TR_SLOTS];
                 const int use = k / TR_SLOTS;
                 int good = 1;
                 if (lane == 0) good = mbar_wait(smem_u32(&c->u_empty[k % TR_SLOTS]), (uint32_t)((use & 1) ^ 1), pc);
                 if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
-                s->sees[lane] = s0;
-                s->sees[lane + 32] = s1;
+                s->up[lane] = (int8_t)u0;
+                s->up[lane + 32] = (int8_t)u1;
+                s->depth[lane] = (uint8_t)d0;
+                s->depth[lane + 32] = (uint8_t)d1;
                 if (lane == 0) s->u = u;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&c->u_full[k % TR_SLOTS]));
@@ -462,13 +493,19 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 if (u.end) break;
             }
         } else if (warp == WARP_K || warp == WARP_V) {
-            // ======================================= TMA producers ====
+            // ========================================= producers ====
+            // The whole warp, converged: the copies' operands stay in uniform registers, one elected lane issues.
             const bool is_k = warp == WARP_K;
-            const CUtensorMap* map = is_k ? &kmap : &vmap;
-            if (lane == 0) prefetch_tmap(map);
-            const int nst = is_k ? TR_KSTAGES : TR_VSTAGES;
-            int n = 0, nl = 0;          // tiles issued, tree tiles that went through v_land
+            if (lane == 0) prefetch_tmap(is_k ? &kmap : &vmap);
+            const int stages = is_k ? TR_KSTAGES : TR_VSTAGES;
+            uint64_t* full = is_k ? c->k_full : c->v_full;
+            uint64_t* empty = is_k ? c->k_empty : c->v_empty;
+            const uint32_t ring = s_base + (is_k ? Sh::OFF_K : Sh::OFF_V);
+            const uint64_t once = evict_first_policy();  // the cache passes by; the parts stay in L2 for the merge
+            int n = 0, st = 0, nl = 0;  // tiles issued, their stage, tree tiles that went through v_land
+            uint32_t phase = 1;
             bool land_open = false, ok = true;
+#pragma unroll 1
             for (int k = 0; ok; ++k) {
                 TrSlot* s = &c->slot[k % TR_SLOTS];
                 if (!(ok = wait_all(c->u_full[k % TR_SLOTS], k / TR_SLOTS))) break;
@@ -476,86 +513,86 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 if (u.end) break;
                 const int npt = (u.n_keys + TR_BN - 1) / TR_BN, n_tiles = npt + u.tree;
                 const int32_t* bt = a.block_table + (size_t)u.b * a.W + u.t0 / PAGE;
-                int st = n % nst;
+                auto page_ids = [&](int i) {  // lane p: page p of tile i (the tree's begins where the prefix's whole pages end)
+                    const int np = tile_keys(i, u.n_keys, u.prefix, T) / PAGE, p0 = i < npt ? i * (TR_BN / PAGE) : u.n_keys / PAGE;
+                    return i < n_tiles && lane < np ? __ldg(bt + p0 + lane) : 0;
+                };
+                int ids = page_ids(0);
+#pragma unroll 1
                 for (int i = 0; i < n_tiles; ++i, ++n) {
-                    const int keys = tile_keys(i, u.n_keys, u.prefix, T), np = keys / PAGE;
-                    // (the tree's tile begins where the prefix's whole pages end)
-                    const int p0 = i < npt ? i * (TR_BN / PAGE) : u.n_keys / PAGE;
-                    const int pg = lane < np ? __ldg(bt + p0 + lane) : 0;
-                    const uint32_t eb = smem_u32(is_k ? &c->k_empty[st] : &c->v_empty[st]);
-                    const uint32_t fb = smem_u32(is_k ? &c->k_full[st] : &c->v_full[st]);
-                    int good = 1;
-                    if (lane == 0) good = mbar_wait(eb, (uint32_t)((n / nst) & 1) ^ 1u, pc);
-                    if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
+                    const int keys = tile_keys(i, u.n_keys, u.prefix, T), np = __shfl_sync(0xffffffffu, keys / PAGE, 0);
+                    const int next = page_ids(i + 1);
+                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[st]), phase, pc)))) break;
                     const bool clean = !is_k && i >= npt;
-                    const uint32_t lb = clean ? smem_u32(&c->v_land) : fb;
-                    if (lane == 0) mbar_arrive_expect_tx(lb, (uint32_t)np * 4096);
-                    __syncwarp();
-                    if (lane < np) {
-                        if (is_k) {  // two 16 x 64 boxes per page: the K-major tile layout
-                            const uint32_t t = s_base + Sh::OFF_K + st * TR_TILE_BYTES + lane * 2048;
-                            tma_load_3d(t, map, lb, 0, u.kvh, pg * PAGE);
-                            tma_load_3d(t + 16384, map, lb, 64, u.kvh, pg * PAGE);
-                        } else {     // one 4 KiB box per page: [page][half][16 rows][128 B]
-                            tma_load_4d(s_base + Sh::OFF_V + st * TR_TILE_BYTES + lane * 4096, map, lb, 0, pg * PAGE, 0, u.kvh);
+                    const uint32_t lb = smem_u32(clean ? &c->v_land : &full[st]);
+                    arrive_expect_tx_elect(lb, (uint32_t)np * 4096);
+                    uint32_t dst = ring + st * TR_TILE_BYTES;
+                    const int head = __shfl_sync(0xffffffffu, u.kvh, 0);
+                    if (is_k) {  // two 16 x 64 boxes per page: the K-major tile layout
+#pragma unroll 1
+                        for (int p = 0; p < np; ++p, dst += 2048) {
+                            const int row = __shfl_sync(0xffffffffu, ids, p) * PAGE;
+                            tma_load_3d_elect(dst, &kmap, lb, 0, head, row, once);
+                            tma_load_3d_elect(dst + 16384, &kmap, lb, 64, head, row, once);
                         }
+                    } else {     // one 4 KiB box per page: [page][half][16 rows][128 B]
+#pragma unroll 1
+                        for (int p = 0; p < np; ++p, dst += 4096)
+                            tma_load_4d_elect(dst, &vmap, lb, 0, __shfl_sync(0xffffffffu, ids, p) * PAGE, 0, head, once);
                     }
-                    __syncwarp();
-                    if (clean) {
-                        // The tree's V: rows past the last node and unused nodes hold anything, and 0 times that need not
-                        // be 0; a node whose V is not finite is zeroed too and fails who sees it.
-                        int landed = 1;
-                        if (lane == 0) landed = mbar_wait(lb, (uint32_t)(nl & 1), pc);
-                        ++nl;
-                        if (!(ok = __shfl_sync(0xffffffffu, landed, 0) != 0)) {
-                            land_open = true;
-                            break;
-                        }
-                        const int off = u.prefix & (PAGE - 1);
-                        uint8_t* vt = sm + Sh::OFF_V + st * TR_TILE_BYTES;
-                        uint64_t bad = 0;
-                        if (lane == 0) ok = mbar_wait(smem_u32(&c->r_empty[k & 1]), (uint32_t)((k >> 1) & 1) ^ 1u, pc);
-                        if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
-                        for (int r0 = off; r0 < keys; r0 += 2) {  // two rows a turn, 16 bytes a lane
-                            const int r = r0 + (lane >> 4), ch = lane & 15, node = r - off;
-                            uint4* x = reinterpret_cast<uint4*>(vt + (r >> 4) * 4096 + (ch >> 3) * 2048 + (r & 15) * 128 + (((ch & 7) ^ (r & 7)) << 4));
-                            const bool in = r < keys, real = in && node < T && s->sees[node & 63] != 0;
-                            uint32_t m = 0;
-                            if (real) {
-                                const uint4 y = *x;
-                                m = __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
-                            }
-                            const bool off_range = (m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u;
-                            const uint32_t hit = __ballot_sync(0xffffffffu, off_range);
-                            const bool mine = (hit >> (lane & 16)) & 0xffffu;
-                            if (in && (!real || mine)) *x = make_uint4(0, 0, 0, 0);
-                            if (hit & 0xffffu) bad |= 1ull << ((r0 - off) & 63);
-                            if (hit >> 16) bad |= 1ull << ((r0 + 1 - off) & 63);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            c->vbad[k & 1] = bad;
-                            mbar_arrive(fb);
-                        }
+                    ids = next;
+                    const int here = st;
+                    if (++st == stages) {
+                        st = 0;
+                        phase ^= 1;
                     }
-                    if (++st == nst) st = 0;
+                    if (!clean) continue;
+                    // The tree's V: rows past the last node and unused nodes hold anything, and 0 times that need not
+                    // be 0; a node whose V is not finite is zeroed too and fails who sees it.
+                    if (!(ok = wait_all(c->v_land, nl))) {
+                        land_open = true;
+                        break;
+                    }
+                    ++nl;
+                    const int off = u.prefix & (PAGE - 1);
+                    uint8_t* vt = sm + Sh::OFF_V + here * TR_TILE_BYTES;
+                    uint64_t bad = 0;
+                    if (!(ok = wait_all(c->r_empty[k & 1], (k >> 1) + 1))) break;
+#pragma unroll 1
+                    for (int r0 = off; r0 < keys; r0 += 2) {  // two rows a turn, 16 bytes a lane
+                        const int r = r0 + (lane >> 4), ch = lane & 15, node = r - off;
+                        uint4* x = reinterpret_cast<uint4*>(vt + (r >> 4) * 4096 + (ch >> 3) * 2048 + (r & 15) * 128 + (((ch & 7) ^ (r & 7)) << 4));
+                        const bool in = r < keys, real = in && node < T && s->depth[node & 63] != 255;
+                        uint32_t m = 0;
+                        if (real) {
+                            const uint4 y = *x;
+                            m = __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
+                        }
+                        const bool off_range = (m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u;
+                        const uint32_t hit = __ballot_sync(0xffffffffu, off_range);
+                        const bool mine = (hit >> (lane & 16)) & 0xffffu;
+                        if (in && (!real || mine)) *x = make_uint4(0, 0, 0, 0);
+                        if (hit & 0xffffu) bad |= 1ull << ((r0 - off) & 63);
+                        if (hit >> 16) bad |= 1ull << ((r0 + 1 - off) & 63);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        c->vbad[k & 1] = bad;
+                        mbar_arrive(smem_u32(&c->v_full[here]));
+                    }
                 }
                 if (!ok) break;
-                if (!is_k && lane == 0) {
-                    if (!u.tree && !(ok = mbar_wait(smem_u32(&c->r_empty[k & 1]), (uint32_t)((k >> 1) & 1) ^ 1u, pc))) {
-                    } else {
-                        mbar_arrive(smem_u32(&c->r_full[k & 1]));
-                    }
+                if (!is_k && !u.tree && !(ok = wait_all(c->r_empty[k & 1], (k >> 1) + 1))) break;
+                if (lane == 0) {
+                    if (!is_k) mbar_arrive(smem_u32(&c->r_full[k & 1]));
+                    mbar_arrive(smem_u32(&c->u_empty[k % TR_SLOTS]));
                 }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-                if (lane == 0) mbar_arrive(smem_u32(&c->u_empty[k % TR_SLOTS]));
             }
             if (lane == 0 && pipe_aborted(pc)) {
                 // copies in flight land before the CTA's shared memory is released
-                if (land_open) mbar_wait_drain(smem_u32(&c->v_land), (uint32_t)((nl - 1) & 1));
-                for (int i = max(0, n - nst); i < n; ++i)
-                    mbar_wait_drain(smem_u32(is_k ? &c->k_full[i % nst] : &c->v_full[i % nst]), (uint32_t)((i / nst) & 1));
+                if (land_open) mbar_wait_drain(smem_u32(&c->v_land), (uint32_t)(nl & 1));
+                for (int i = max(0, n - stages); i < n; ++i) mbar_wait_drain(smem_u32(&full[i % stages]), (uint32_t)((i / stages) & 1));
             }
         } else if (warp == WARP_MMA) {
             // ============================================= MMA issuer ====
@@ -564,28 +601,38 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             constexpr uint32_t TILE_DESC = TR_TILE_BYTES >> 4;
             const uint32_t dQ = desc_lo(s_base, 16), dK0 = desc_lo(s_base + Sh::OFF_K, 16);
             const uint32_t dV0 = desc_lo(s_base + Sh::OFF_V, 2048), dP0 = desc_lo(s_base + Sh::OFF_P, 16);
-            int g = 0;  // tiles so far
+            int g = 0, freed = 0;  // tiles so far, sets of queries given back
             bool ok = !a.timeout_drill || __all_sync(0xffffffffu, drill_wait(smem_u32(&c->never), pc));
             for (int k = 0; ok; ++k) {
                 if (!(ok = wait_all(c->u_full[k % TR_SLOTS], k / TR_SLOTS))) break;
                 const volatile TrUnit* su = &c->slot[k % TR_SLOTS].u;
                 auto uni = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
                 const int end = uni(su->end), n_keys = uni(su->n_keys), tree = uni(su->tree), prefix = uni(su->prefix);
-                const int newq = uni(su->newq), endq = uni(su->endq), nq = uni(su->nq);
+                const int newq = uni(su->newq), nq = uni(su->nq);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&c->u_empty[k % TR_SLOTS]));
                 if (end) break;
                 const int n_tiles = (n_keys + TR_BN - 1) / TR_BN + tree;
-                if (newq && !(ok = wait_all(c->q_ready, nq))) break;
+                if (newq) {
+                    if (nq > freed) {  // the queries before have been read
+                        umma_commit_elect(smem_u32(&c->q_empty));
+                        freed = nq;
+                    }
+                    if (!(ok = wait_all(c->q_ready, nq))) break;
+                }
                 // PV of tile i, number x of the CTA
                 auto issue_pv = [&](int i, int x) -> bool {
                     if (i == 0 && !wait_all(c->o_free[k & 1], (k >> 1) + 1)) return false;  // the buffer's item before has been read
                     if (!wait_all(c->p_ready[x % Sh::PBUF], x / Sh::PBUF)) return false;
                     if (!wait_all(c->v_full[x % TR_VSTAGES], x / TR_VSTAGES)) return false;
                     tc_fence_after();
-                    pv_steps<0, RR>(tmem + 256 + (k & 1) * RR, dV0 + (uint32_t)(x % TR_VSTAGES) * TILE_DESC,
-                                    dP0 + (uint32_t)(x % Sh::PBUF) * (Sh::P_BYTES >> 4), idO, i > 0 ? 1u : 0u,
-                                    tile_keys(i, n_keys, prefix, T) / PAGE);
+                    const int pages = tile_keys(i, n_keys, prefix, T) / PAGE;
+                    const uint32_t dv = dV0 + (uint32_t)(x % TR_VSTAGES) * TILE_DESC, dp = dP0 + (uint32_t)(x % Sh::PBUF) * (Sh::P_BYTES >> 4);
+                    // O^T[dims x RR] += V^T P^T, a page to a k-step: V as the pages lie there (MN-major), P^T's rows as
+                    // two blocks of 64 keys (K-major)
+#pragma unroll 1
+                    for (int h = 0; 4 * h < pages; ++h)
+                        mma_f16_x4<256, 2>(tmem + 256 + (k & 1) * RR, dv + h * 1024, dp + h * (RR * 128 >> 4), idO, i > 0 || h > 0, pages - 4 * h);
                     umma_commit_elect(smem_u32(&c->pv_done[x & 1]));
                     umma_commit_elect(smem_u32(&c->v_empty[x % TR_VSTAGES]));
                     if (i == n_tiles - 1) umma_commit_elect(smem_u32(&c->o_done[k & 1]));
@@ -598,11 +645,21 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                         if (!(ok = wait_all(c->k_ready[g % TR_KSTAGES], g / TR_KSTAGES))) break;
                         if (!(ok = wait_all(c->s_free[g & 1], (g >> 1) + 1))) break;
                         tc_fence_after();
-                        mma_ss_steps<0, 8, K_MAJOR_128, K_MAJOR_128, true>(tmem + (g & 1) * 128, dQ,
-                                                                           dK0 + (uint32_t)(g % TR_KSTAGES) * TILE_DESC, idS, 0u);
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h)
+                            mma_f16_x4<2, 2>(tmem + (g & 1) * 128, dQ + h * 1024, dK0 + (uint32_t)(g % TR_KSTAGES) * TILE_DESC + h * 1024, idS, h, 4);
                         umma_commit_elect(smem_u32(&c->s_full[g & 1]));
                         umma_commit_elect(smem_u32(&c->k_empty[g % TR_KSTAGES]));
-                        if (endq && i == n_tiles - 1) umma_commit_elect(smem_u32(&c->q_empty));
+                        if (i == n_tiles - 1 &&
+                            __all_sync(0xffffffffu, mbar_test(smem_u32(&c->u_full[(k + 1) % TR_SLOTS]), (uint32_t)((k + 1) / TR_SLOTS) & 1u))) {
+                            // the next item is known: if it has other queries, these have been read by the scores so far
+                            const volatile TrUnit* nu = &c->slot[(k + 1) % TR_SLOTS].u;
+                            const int other = uni(nu->newq), num = uni(nu->nq), none = uni(nu->end);
+                            if (!none && other) {
+                                umma_commit_elect(smem_u32(&c->q_empty));
+                                freed = num;
+                            }
+                        }
                     }
                     if (i > 0 && !(ok = issue_pv(i - 1, g - 1))) break;
                 }
@@ -639,8 +696,8 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             const uint32_t b = __ballot_sync(0xffffffffu, x);
             return ((b >> (lane & 24)) & 0xffu) != 0;
         };
-        int g = 0;
         bool ok = true;
+        int g = 0;
         for (int k = 0; ok; ++k) {
             TrSlot* s = &c->slot[k % TR_SLOTS];
             if (!(ok = wait_all(c->u_full[k % TR_SLOTS], k / TR_SLOTS))) break;
@@ -654,32 +711,41 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 const int nq = u->nq, rows = u->rows, base = u->block * TR_SPAN;
                 const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(a.q) +
                                                                 (first_row(a, u->b, u->kvh) + base) * HEAD_DIM);
+                // (a row's data is asked for while the row before is rotated)
+                uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                auto row = [&](int r) {
+                    if (r < rows) {
+                        lo = __ldg(q + r * 16 + u8);
+                        hi = __ldg(q + r * 16 + 8 + u8);
+                    } else {
+                        lo = hi = make_uint4(0, 0, 0, 0);
+                    }
+                };
+                row(r0);
                 if (!(ok = wait_all(c->q_empty, nq + 1))) break;
 #pragma unroll 1
                 for (int r = r0; r < RR; r += TR_ROW_STEP) {
-                    const bool in = r < rows;
-                    uint32_t rg = 0;
-                    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-                    if (in) {
-                        lo = __ldg(q + r * 16 + u8);
-                        hi = __ldg(q + r * 16 + 8 + u8);
-                        angles((uint32_t)(prefix + max(__popcll(s->sees[(base + r) % T]) - 1, 0)), cs, sn);
-                        rg = rotate_regs_f16(lo, hi, cs, sn, 0);
-                    }
+                    uint4 x = lo, y = hi;
+                    row(r + TR_ROW_STEP);
+                    const int d = r < rows ? s->depth[(base + r) % T] : 255;
+                    angles((uint32_t)(prefix + (d == 255 ? 0 : d)), cs, sn);
+                    uint32_t rs = 0, ru = 0;
+                    rotate(x, y, cs, sn, rs, ru);
 #pragma unroll
-                    for (int x = 0; x < Sh::COPIES; ++x) {
-                        uint8_t* qt = sm + sw128_off(x * RR + r, u8);
-                        *reinterpret_cast<uint4*>(qt) = lo;
-                        *reinterpret_cast<uint4*>(qt + 16384) = hi;
+                    for (int e = 0; e < Sh::COPIES; ++e) {
+                        uint8_t* qt = sm + sw128_off(e * RR + r, u8);
+                        *reinterpret_cast<uint4*>(qt) = x;
+                        *reinterpret_cast<uint4*>(qt + 16384) = y;
                     }
-                    const bool bad = any8(range_exceeded(rg));
-                    if (u8 == 0) c->qbad[nq & 1][r] = bad;
+                    const uint32_t bad = __ballot_sync(0xffffffffu, too_large(rs, ru));
+                    if (lane == 0)
+                        c->qbad[nq & 1][r >> 2] = (uint8_t)(((bad & 0xffu) != 0) | ((bad & 0xff00u) != 0) << 1 | ((bad & 0xff0000u) != 0) << 2 | (bad >> 24 != 0) << 3);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&c->q_ready));
             }
-            uint32_t range = 0;
+            uint32_t rs = 0, ru = 0;       // largest positive, largest negative input (bits) of the prefix's keys
             if (!(ok = wait_all(c->r_empty[k & 1], (k >> 1) + 1))) break;
             for (int i = 0; i < npt; ++i, ++g) {
                 const int kst = g % TR_KSTAGES;
@@ -687,21 +753,20 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 if (!(ok = wait_all(c->k_full[kst], g / TR_KSTAGES))) break;
                 uint8_t* kt = sm + Sh::OFF_K + kst * TR_TILE_BYTES;
                 const int keys = min(TR_BN, n_keys - i * TR_BN);
-                uint4 lo[ROWS], hi[ROWS];  // all of the thread's rows are read before any is rotated
-#pragma unroll
-                for (int m = 0; m < ROWS; ++m) {
-                    const uint32_t off = sw128_off(r0 + TR_ROW_STEP * m, u8);
-                    lo[m] = *reinterpret_cast<const uint4*>(kt + off);
-                    hi[m] = *reinterpret_cast<const uint4*>(kt + 16384 + off);
-                }
-#pragma unroll
-                for (int m = 0; m < ROWS; ++m) {
-                    const int r = r0 + TR_ROW_STEP * m;
-                    if (r < keys) {
-                        range = rotate_regs_f16(lo[m], hi[m], cs, sn, range);
-                        const uint32_t off = sw128_off(r, u8);
-                        *reinterpret_cast<uint4*>(kt + off) = lo[m];
-                        *reinterpret_cast<uint4*>(kt + 16384 + off) = hi[m];
+                // row r0 + 32 m is chunk u8 ^ (r0 & 7) of its 128 bytes for every m
+                uint8_t* at = kt + sw128_off(r0, u8);
+                uint4 lo = *reinterpret_cast<const uint4*>(at), hi = *reinterpret_cast<const uint4*>(at + 16384);
+#pragma unroll 1
+                for (int m = 0; m < ROWS; ++m, at += TR_ROW_STEP * 128) {
+                    uint4 x = lo, y = hi;
+                    if (m + 1 < ROWS) {  // the next row is read while this one is rotated
+                        lo = *reinterpret_cast<const uint4*>(at + TR_ROW_STEP * 128);
+                        hi = *reinterpret_cast<const uint4*>(at + TR_ROW_STEP * 128 + 16384);
+                    }
+                    if (r0 + TR_ROW_STEP * m < keys) {
+                        rotate(x, y, cs, sn, rs, ru);
+                        *reinterpret_cast<uint4*>(at) = x;
+                        *reinterpret_cast<uint4*>(at + 16384) = y;
                     }
                     rope_step(cs, sn, dcs, dsn);
                 }
@@ -719,16 +784,21 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 for (int rr = 0; rr < last; rr += TR_ROW_STEP) {
                     const int r = rr + r0, node = r - off0;
                     // (d: how far from the end of the prefix; the page's own keys lie before it)
-                    const int d = node < 0 ? node : r < last ? __popcll(s->sees[node]) - 1 : -1;
-                    bool bad = false;
-                    if (node < 0 || d >= 0) {
+                    const int d = node < 0 ? node : r < last ? s->depth[node] : 255;
+                    uint32_t ns = 0, nu = 0;
+                    if (d != 255) {
                         angles((uint32_t)(prefix + d), cs, sn);
                         const uint32_t off = sw128_off(r, u8);
-                        const uint32_t rg = rotate_chunk_f16(kt + off, kt + 16384 + off, cs, sn, 0);
-                        if (node < 0) range = __vmaxu2(range, rg);
-                        else bad = range_exceeded(rg);
+                        uint4 lo = *reinterpret_cast<const uint4*>(kt + off), hi = *reinterpret_cast<const uint4*>(kt + 16384 + off);
+                        rotate(lo, hi, cs, sn, ns, nu);
+                        *reinterpret_cast<uint4*>(kt + off) = lo;
+                        *reinterpret_cast<uint4*>(kt + 16384 + off) = hi;
                     }
-                    bad = any8(bad);
+                    const bool bad = any8(node >= 0 && too_large(ns, nu));
+                    if (node < 0) {
+                        rs = __vmaxs2(rs, ns);
+                        ru = __vmaxu2(ru, nu);
+                    }
                     if (u8 == 0 && r < TR_TREE_ROWS) c->kbad[k & 1][r] = bad;
                 }
                 fence_proxy_async_smem();
@@ -736,7 +806,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 if (lane == 0) mbar_arrive(smem_u32(&c->k_ready[kst]));
                 ++g;
             }
-            const bool bad = __any_sync(0xffffffffu, range_exceeded(range));
+            const bool bad = __any_sync(0xffffffffu, too_large(rs, ru));
             if (lane == 0) {
                 c->xbad[k & 1][warp] = bad;
                 mbar_arrive(smem_u32(&c->r_full[k & 1]));
@@ -746,7 +816,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_S));
         // ================================================== softmax ====
-        constexpr int COLS = Sh::COLS, PARTS = Sh::PARTS, CH = COLS < 32 ? COLS : 32;  // CH: columns at a time
+        constexpr int COLS = Sh::COLS, PARTS = Sh::PARTS, CH = 16;    // CH: columns at a time
         const int t = tid - 32 * WARP_S0, wg = t >> 7, ln = t & 127;  // warpgroup, lane of tensor memory
         const int r = ln % RR, part = wg * Sh::COPIES + ln / RR;      // the thread's query, which of its threads it is
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
@@ -757,50 +827,49 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         auto wait = [&](uint64_t& bar, int parity) {
             if (ok) ok = wait_all(bar, parity);
         };
+        uint64_t sees = 0;                                // the query's node and its ancestors (0: unused)
         for (int k = 0;; ++k) {
             TrSlot* s = &c->slot[k % TR_SLOTS];
             wait(c->u_full[k % TR_SLOTS], k / TR_SLOTS);
-            if (named_bar_or(1, TR_SOFTMAX, !ok)) {
-                ok = false;
+            const volatile TrUnit* u = &s->u;
+            if (!ok || u->end) {                          // (the others may be at their first tile: two barriers)
+                const bool any = named_bar_or(1, TR_SOFTMAX, !ok);
+                named_bar_or(1, TR_SOFTMAX, !ok);
+                ok = ok && !any;
                 break;
             }
-            const volatile TrUnit* u = &s->u;
-            if (u->end) break;
             const int n_keys = u->n_keys, prefix = u->prefix, tree = u->tree, rows = u->rows;
             const int npt = (n_keys + TR_BN - 1) / TR_BN, n_tiles = npt + tree;
-            const uint64_t sees = r < rows ? s->sees[(u->block * TR_SPAN + r) % T] : 0ull;
+            if (u->newq) {
+                sees = 0;
+                const int node = (u->block * TR_SPAN + r) % T;
+                for (int n = r < rows && s->depth[node] != 255 ? node : -1; n >= 0; n = s->up[n]) sees |= 1ull << n;
+            }
             const uint32_t tO = tmem + 256 + (k & 1) * RR + wg * COLS + lane_addr;
             float m = -INFINITY, l = 0.0f;
             for (int i = 0; i < n_tiles; ++i, ++g) {
-                // the thread's visible columns: whole pages of the prefix, or the prefix's keys and the nodes that the
-                // query sees (tile_cols is the number of either)
                 const uint32_t tS = tmem + (g & 1) * 128 + part * COLS + lane_addr;
-                uint32_t see[COLS / CH];
-#pragma unroll
-                for (int h = 0; h < COLS / CH; ++h) {
-                    const int c0 = part * COLS + h * CH;
-                    if (i < npt) {
-                        const int left = n_keys - i * TR_BN - c0;
-                        see[h] = left >= CH ? 0xffffffffu : left > 0 ? 0xffffu : 0u;
-                    } else {
-                        const int at = c0 - (prefix & (PAGE - 1));  // the node of the first column (before 0: prefix)
-                        see[h] = at >= 64 ? 0u : at >= 0 ? (uint32_t)(sees >> at) : (uint32_t)(sees << -at) | ((1u << -at) - 1u);
-                    }
-                }
                 wait(c->s_full[g & 1], g >> 1);
                 uint32_t xr[CH];
                 float mx = -INFINITY;
-                auto take = [&](int h) {  // columns h * CH .. of the thread, what is hidden at -inf
-                    tmem_load(tS + h * CH, xr);
+                auto take = [&](int h) {  // 16 columns of the thread, what is hidden at -inf
+                    tmem_ld16(tS + h * CH, xr);
                     tmem_ld_wait();
-                    if (__any_sync(0xffffffffu, (~see[h] << (32 - CH)) != 0u)) {
+                    const int c0 = part * COLS + h * CH;
+                    if (i < npt) {        // whole pages of the prefix
+                        if (n_keys - i * TR_BN > c0) return;
 #pragma unroll
-                        for (int x = 0; x < CH; ++x) xr[x] = (see[h] >> x) & 1u ? xr[x] : 0xff800000u;
+                        for (int x = 0; x < CH; ++x) xr[x] = 0xff800000u;
+                    } else {              // the prefix's keys and the nodes that the query sees
+                        const int at = c0 - (prefix & (PAGE - 1));  // the node of the first column (before 0: prefix)
+                        const uint32_t see = at >= 64 ? 0u : at >= 0 ? (uint32_t)(sees >> at) : (uint32_t)(sees << -at) | ((1u << -at) - 1u);
+#pragma unroll
+                        for (int x = 0; x < CH; ++x) xr[x] = (see >> x) & 1u ? xr[x] : 0xff800000u;
                     }
                 };
                 if (ok) {
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int h = 0; h < COLS / CH; ++h) {
                         take(h);
                         float m0 = mx, m1 = __uint_as_float(xr[1]);
@@ -837,19 +906,19 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                                 break;
                             }
                             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int h = 0; h < COLS / CH; ++h) {
                                 uint32_t rr[CH];
-                                tmem_load(tO + h * CH, rr);
+                                tmem_ld16(tO + h * CH, rr);
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int x = 0; x < CH; ++x) rr[x] = __float_as_uint(__uint_as_float(rr[x]) * c->ex[wg * COLS + h * CH + x]);
-                                tmem_store(tO + h * CH, rr);
+                                tmem_st16(tO + h * CH, rr);
                             }
                             tmem_st_wait();
                         }
                     }
-                    named_bar_sync(1, TR_SOFTMAX);  // the exchange may be written again
+                    // (the exchange is written again behind a barrier)
                 }
                 // P^T's buffer: read by PV of the tile PBUF before this one
                 if (g >= Sh::PBUF) wait(c->pv_done[(g - Sh::PBUF) & 1], (g - Sh::PBUF) >> 1);
@@ -858,7 +927,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 const float2 sc2 = make_float2(scl, scl), nm2 = make_float2(nm, nm);
                 float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
                 uint8_t* prow = sm + Sh::OFF_P + (g % Sh::PBUF) * Sh::P_BYTES;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < COLS / CH; ++h) {
                     if (COLS > CH) take(h);
                     uint32_t pr[CH / 2];
@@ -891,19 +960,19 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 if (named_bar_or(1, TR_SOFTMAX, true)) break;
             }
             // ---- the item's results ----
+            float* ex_sum = reinterpret_cast<float*>(c + 1);
+            if (part) ex_sum[(part - 1) * RR + r] = l;
             wait(c->r_full[k & 1], k >> 1);
-            c->ex[part * RR + r] = l;
             if (named_bar_or(1, TR_SOFTMAX, !ok)) {
                 ok = false;
                 break;
             }
             const size_t row0 = first_row(a, u->b, u->kvh) + u->block * TR_SPAN;
-            const int direct = u->direct, split = u->split, nqp = u->nq & 1;
-            float inv = 0.0f;
+            const int direct = u->direct, split = u->split;
             if (t < RR) {  // part 0 of query t, whole warps
-                float sum = 0.0f;
+                float sum = l, inv = 0.0f;
 #pragma unroll
-                for (int x = 0; x < PARTS; ++x) sum += c->ex[x * RR + r];
+                for (int x = 1; x < PARTS; ++x) sum += ex_sum[(x - 1) * RR + r];
                 bool fail = *reinterpret_cast<const uint64_t*>(c->xbad[k & 1]) != 0;
                 if (tree) {
                     const int off = prefix & (PAGE - 1);
@@ -911,9 +980,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     const uint32_t b1 = __ballot_sync(0xffffffffu, lane + 32 < T && c->kbad[k & 1][off + min(lane + 32, TREE_MAX - 1)]);
                     fail |= (sees & (((uint64_t)b1 << 32) | b0 | c->vbad[k & 1])) != 0;
                 }
-                fail |= c->qbad[nqp][r] != 0;
+                fail |= (c->qbad[u->nq & 1][r >> 2] >> (r & 3)) & 1;
                 const bool empty = sees == 0;
                 if (!empty && !fail && sum > 0.0f) inv = 1.0f / sum;
+                c->ex[r] = inv;  // (the maxima have been read)
                 if (r < rows) {
                     const float lse2 = empty ? -INFINITY : fail ? __int_as_float(0x7fc00000) : m + log2f(sum);
                     if (direct) a.lse[row0 + r] = lse2 * 0.693147180559945309f;
@@ -921,8 +991,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     if (fail && !empty && a.status) atomicOr(a.status, RK_STATUS_RANGE);
                 }
             }
-            named_bar_sync(1, TR_SOFTMAX);  // the sums have been read
-            if (t < RR) c->ex[r] = inv;
             wait(c->o_done[k & 1], k >> 1);
             if (named_bar_or(1, TR_SOFTMAX, !ok)) {
                 ok = false;
@@ -930,22 +998,25 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             }
             tc_fence_after();
             // thread: dim ln of queries wg * COLS ..
-            float* part_o = a.o_part + (row0 * a.n_splits + split) * HEAD_DIM + ln;
-            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + row0 * HEAD_DIM + ln;
-#pragma unroll
+            const size_t step = direct ? HEAD_DIM : (size_t)a.n_splits * HEAD_DIM;
+            float* part_o = a.o_part + (row0 * a.n_splits + split) * HEAD_DIM + wg * COLS * step + ln;
+            __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + (row0 + wg * COLS) * HEAD_DIM + ln;
+#pragma unroll 1
             for (int h = 0; h < COLS / CH; ++h) {
                 uint32_t rr[CH];
-                tmem_load(tO + h * CH, rr);
+                tmem_ld16(tO + h * CH, rr);
                 tmem_ld_wait();
+                const int left = rows - wg * COLS - h * CH;
 #pragma unroll
                 for (int x = 0; x < CH; ++x) {
-                    const int qr = wg * COLS + h * CH + x;
-                    const float f = c->ex[qr];
+                    const float f = c->ex[wg * COLS + h * CH + x];
                     const float y = f == 0.0f ? 0.0f : __uint_as_float(rr[x]) * f;  // (a failed query's O may be NaN)
-                    if (qr < rows) {
-                        if (direct) out[(size_t)qr * HEAD_DIM] = __float2bfloat16_rn(y);
-                        else part_o[(size_t)qr * a.n_splits * HEAD_DIM] = y;
+                    if (x < left) {
+                        if (direct) *out = __float2bfloat16_rn(y);
+                        else *part_o = y;
                     }
+                    out += HEAD_DIM;
+                    part_o += step;
                 }
             }
             tc_fence_before();
