@@ -1184,8 +1184,8 @@ int check_tree_plan(const rk_paged_plan_t* plan) {
 // Where a row's prefix is cut, and the scratch for the parts of the widest row: none where the table holds
 // one part.  Tiles of a call are counted in 32 bits.
 int tree_parts(const rk_paged_plan_t* plan, rk::TreeArgs* a, uint64_t* bytes) {
-    a->zone[0] = {0, 0, 512};
-    a->zone[1] = {32, 16384, 1024};
+    a->zone[0] = {0, 0, 1024};
+    a->zone[1] = {16, 16384, 2048};
     const int64_t cap = (int64_t)plan->W * rk::PAGE;
     const int z = cap > a->zone[1].token;
     const int64_t parts = cap > 0 ? a->zone[z].split + (cap - a->zone[z].token + a->zone[z].size - 1) / a->zone[z].size : 1;

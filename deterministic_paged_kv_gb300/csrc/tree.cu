@@ -62,9 +62,6 @@ constexpr int TR_SLOTS = 3;                               // items published ahe
 constexpr int TR_ROW_STEP = TR_XW * 4;                    // rows between a transform thread's rows
 constexpr int TR_ANCHOR = 8;                              // tiles between exact angles
 constexpr int TR_GROUPS = 32;                             // row groups of the item search
-// setmaxnreg split of the 640 x 96 registers that the CTA launches with
-constexpr int REG_X = 88, REG_S = 120, REG_C = 64;
-static_assert(2 * REG_X + 2 * REG_S + REG_C <= 5 * 96, "register split above the launch's");
 
 template <int RR>
 struct TrShape {
@@ -98,6 +95,15 @@ struct TrSlot {
     uint8_t depth[TREE_MAX];   // 255: unused
 };
 
+// A whole warp waits for a barrier's phase.  The first try suspends the warp as long as any later one; what follows it is
+// a call, not code at each of the forty places that wait.
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, PipeCtl* pc) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, pc)) != 0;
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, PipeCtl* pc) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_longer(bar, parity, pc);
+}
+
 // ------------------------------------------------------------ geometry ----
 
 // A row's prefix in whole pages, and why the row has none (status bits; kv_len 0: -1 and no bit).
@@ -130,14 +136,14 @@ struct TrItems {
     int at, hi;             // the part's first tile, the run's end
     __device__ __forceinline__ int head(int heads) const { return v % heads; }
     __device__ __forceinline__ bool valid(const TreeArgs& a, int heads) const { return v < heads * a.members; }
-    __device__ __forceinline__ void row(const TreeArgs& a) {
+    __device__ void row(const TreeArgs& a) {
         if (b < a.B) {
             n = row_pages16(a, b, kv, bad);
             ns = parts_of(a, n);
         }
     }
     // The first part of run v that there is, or of a later run of this CTA.
-    __device__ void start(const TreeArgs& a, int total, const int* pre, int heads, int run) {
+    __device__ __noinline__ void start(const TreeArgs& a, int total, const int* pre, int heads, int run) {
         for (v = run; v < heads * a.members; v += (int)gridDim.x) {
             const unsigned m = (unsigned)(v / heads), each = (unsigned)total / a.members, rest = (unsigned)total % a.members;
             at = (int)(each * m + rest * m / a.members);
@@ -171,7 +177,7 @@ struct TrItems {
             if (b < a.B && at < hi) return;
         }
     }
-    __device__ __forceinline__ void next(const TreeArgs& a, int total, const int* pre, int heads) {
+    __device__ __noinline__ void next(const TreeArgs& a, int total, const int* pre, int heads) {
         const int from = part_start(a, s) / TR_BN;
         if (++s == ns) {
             at += row_tiles(n) - from;
@@ -218,7 +224,7 @@ __device__ __forceinline__ size_t first_row(const TreeArgs& a, int b, int kvh) {
 
 // An item that nothing is computed for (count threads, i of them): a part that says NaN or -inf,
 // or the results themselves.
-__device__ void write_nothing(const TreeArgs& a, int b, int kvh, int block, int split, bool direct, float lse, int i, int count) {
+__device__ __noinline__ void write_nothing(const TreeArgs& a, int b, int kvh, int block, int split, bool direct, float lse, int i, int count) {
     const int R = a.G * a.T, r0 = block * TR_SPAN, rows = min(TR_SPAN, R - r0);
     if (!direct) {
         float* lp = a.lse_part + ((first_row(a, b, kvh) + r0) * a.n_splits + split);
@@ -264,17 +270,39 @@ __device__ __forceinline__ void tma_load_4d_elect(uint32_t dst, const CUtensorMa
         : "memory");
 }
 
+__device__ __forceinline__ float2 fsub2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "sub.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// Angles of eight rotation pairs as (cos, -sin): with the sine's sign turned a step needs no negation, and a rotation one
+// difference.
+struct Turn {
+    float2 c[4], n[4];
+    // by a fixed step of (dc, -ds = dn, ds): c' = c dc - s ds, -s' = -s dc - c ds
+    __device__ __forceinline__ void step(const float2 (&dc)[4], const float2 (&dn)[4], const float2 (&ds)[4]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 cn = ffma2(n[k], ds[k], fmul2(c[k], dc[k]));
+            n[k] = ffma2(c[k], dn[k], fmul2(n[k], dc[k]));
+            c[k] = cn;
+        }
+    }
+};
 // Eight rotation pairs (16 bf16) in FP32, to FP16 in place: (lo, hi) -> (lo c - hi s, hi c + lo s).  rs, ru: running
 // signed and unsigned maxima of the inputs' bits, the largest positive and (if any is below 0) negative one.
-__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2 (&c2)[4], const float2 (&s2)[4], uint32_t& rs, uint32_t& ru) {
+__device__ __forceinline__ void rotate(uint4& a, uint4& b, const Turn& t, uint32_t& rs, uint32_t& ru) {
     uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         rs = __vimax3_s16x2(rs, x[k], y[k]);
         ru = __vimax3_u16x2(ru, x[k], y[k]);
         const float2 lo = make_float2(bf16lo(x[k]), bf16hi(x[k])), hi = make_float2(bf16lo(y[k]), bf16hi(y[k]));
-        const float2 ns = make_float2(-s2[k].x, -s2[k].y);
-        const float2 u = ffma2(hi, ns, fmul2(lo, c2[k])), v = ffma2(lo, s2[k], fmul2(hi, c2[k]));
+        const float2 u = ffma2(hi, t.n[k], fmul2(lo, t.c[k])), v = fsub2(fmul2(hi, t.c[k]), fmul2(lo, t.n[k]));
         x[k] = pack_f16x2(u.x, u.y);
         y[k] = pack_f16x2(v.x, v.y);
     }
@@ -371,12 +399,9 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     PipeCtl* pc = &c->pipe;
     int done = 0;                                         // softmax: items written
 
-    auto wait_all = [&](uint64_t& bar, int parity) {
-        return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), (uint32_t)(parity & 1), pc)) != 0;
-    };
+    auto wait_all = [&](uint64_t& bar, int parity) { return wait_warp(smem_u32(&bar), (uint32_t)(parity & 1), pc); };
 
     if (warp >= WARP_K) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_C));
         if (warp == WARP_SCHED) {
             // ============================================== scheduler ====
             TrItems it;
@@ -479,9 +504,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 }
                 TrSlot* s = &c->slot[k % TR_SLOTS];
                 const int use = k / TR_SLOTS;
-                int good = 1;
-                if (lane == 0) good = mbar_wait(smem_u32(&c->u_empty[k % TR_SLOTS]), (uint32_t)((use & 1) ^ 1), pc);
-                if (!(ok = __shfl_sync(0xffffffffu, good, 0) != 0)) break;
+                if (!(ok = wait_all(c->u_empty[k % TR_SLOTS], use + 1))) break;
                 s->up[lane] = (int8_t)u0;
                 s->up[lane + 32] = (int8_t)u1;
                 s->depth[lane] = (uint8_t)d0;
@@ -522,7 +545,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 for (int i = 0; i < n_tiles; ++i, ++n) {
                     const int keys = tile_keys(i, u.n_keys, u.prefix, T), np = __shfl_sync(0xffffffffu, keys / PAGE, 0);
                     const int next = page_ids(i + 1);
-                    if (!(ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[st]), phase, pc)))) break;
+                    if (!(ok = wait_warp(smem_u32(&empty[st]), phase, pc))) break;
                     const bool clean = !is_k && i >= npt;
                     const uint32_t lb = smem_u32(clean ? &c->v_land : &full[st]);
                     arrive_expect_tx_elect(lb, (uint32_t)np * 4096);
@@ -673,24 +696,23 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         }
         __syncwarp();
     } else if (warp < TR_XW) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_X));
         // ================================================ transform ====
         // thread: pair-chunk u8 (8 rotation pairs: 16 bytes of each 64-dim half) of rows r0 + ROW_STEP * m
         const int u8 = tid & 7, r0 = tid >> 3;
         constexpr int ROWS = TR_BN / TR_ROW_STEP;
-        float2 dcs[4], dsn[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            rope_cos_sin((uint32_t)TR_ROW_STEP, a.rope_turns[8 * u8 + 2 * e], dcs[e].x, dsn[e].x);
-            rope_cos_sin((uint32_t)TR_ROW_STEP, a.rope_turns[8 * u8 + 2 * e + 1], dcs[e].y, dsn[e].y);
-        }
-        auto angles = [&](uint32_t pos, float2 (&cs)[4], float2 (&sn)[4]) {
+        auto angles = [&](uint32_t pos, Turn& t) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                rope_cos_sin(pos, a.rope_turns[8 * u8 + 2 * e], cs[e].x, sn[e].x);
-                rope_cos_sin(pos, a.rope_turns[8 * u8 + 2 * e + 1], cs[e].y, sn[e].y);
+                rope_cos_sin(pos, a.rope_turns[8 * u8 + 2 * e], t.c[e].x, t.n[e].x);
+                rope_cos_sin(pos, a.rope_turns[8 * u8 + 2 * e + 1], t.c[e].y, t.n[e].y);
+                t.n[e] = make_float2(-t.n[e].x, -t.n[e].y);
             }
         };
+        Turn step;
+        angles((uint32_t)TR_ROW_STEP, step);
+        float2 dsn[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dsn[e] = make_float2(-step.n[e].x, -step.n[e].y);
         // a row's verdict from the eight threads that hold it
         auto any8 = [&](bool x) {
             const uint32_t b = __ballot_sync(0xffffffffu, x);
@@ -705,7 +727,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             if (u->end) break;
             const int n_keys = u->n_keys, prefix = u->prefix, t0 = u->t0, tree = u->tree;
             const int npt = (n_keys + TR_BN - 1) / TR_BN;
-            float2 cs[4], sn[4];
+            Turn at;
             if (u->newq) {
                 // new queries, once the score MMAs have read the ones before: COPIES of them, zeros behind the last
                 const int nq = u->nq, rows = u->rows, base = u->block * TR_SPAN;
@@ -728,9 +750,9 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     uint4 x = lo, y = hi;
                     row(r + TR_ROW_STEP);
                     const int d = r < rows ? s->depth[(base + r) % T] : 255;
-                    angles((uint32_t)(prefix + (d == 255 ? 0 : d)), cs, sn);
+                    angles((uint32_t)(prefix + (d == 255 ? 0 : d)), at);
                     uint32_t rs = 0, ru = 0;
-                    rotate(x, y, cs, sn, rs, ru);
+                    rotate(x, y, at, rs, ru);
 #pragma unroll
                     for (int e = 0; e < Sh::COPIES; ++e) {
                         uint8_t* qt = sm + sw128_off(e * RR + r, u8);
@@ -749,26 +771,26 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             if (!(ok = wait_all(c->r_empty[k & 1], (k >> 1) + 1))) break;
             for (int i = 0; i < npt; ++i, ++g) {
                 const int kst = g % TR_KSTAGES;
-                if ((i & (TR_ANCHOR - 1)) == 0) angles((uint32_t)(t0 + i * TR_BN + r0), cs, sn);
+                if ((i & (TR_ANCHOR - 1)) == 0) angles((uint32_t)(t0 + i * TR_BN + r0), at);
                 if (!(ok = wait_all(c->k_full[kst], g / TR_KSTAGES))) break;
                 uint8_t* kt = sm + Sh::OFF_K + kst * TR_TILE_BYTES;
                 const int keys = min(TR_BN, n_keys - i * TR_BN);
                 // row r0 + 32 m is chunk u8 ^ (r0 & 7) of its 128 bytes for every m
-                uint8_t* at = kt + sw128_off(r0, u8);
-                uint4 lo = *reinterpret_cast<const uint4*>(at), hi = *reinterpret_cast<const uint4*>(at + 16384);
-#pragma unroll 1
-                for (int m = 0; m < ROWS; ++m, at += TR_ROW_STEP * 128) {
+                uint8_t* row = kt + sw128_off(r0, u8);
+                uint4 lo = *reinterpret_cast<const uint4*>(row), hi = *reinterpret_cast<const uint4*>(row + 16384);
+#pragma unroll
+                for (int m = 0; m < ROWS; ++m, row += TR_ROW_STEP * 128) {
                     uint4 x = lo, y = hi;
                     if (m + 1 < ROWS) {  // the next row is read while this one is rotated
-                        lo = *reinterpret_cast<const uint4*>(at + TR_ROW_STEP * 128);
-                        hi = *reinterpret_cast<const uint4*>(at + TR_ROW_STEP * 128 + 16384);
+                        lo = *reinterpret_cast<const uint4*>(row + TR_ROW_STEP * 128);
+                        hi = *reinterpret_cast<const uint4*>(row + TR_ROW_STEP * 128 + 16384);
                     }
                     if (r0 + TR_ROW_STEP * m < keys) {
-                        rotate(x, y, cs, sn, rs, ru);
-                        *reinterpret_cast<uint4*>(at) = x;
-                        *reinterpret_cast<uint4*>(at + 16384) = y;
+                        rotate(x, y, at, rs, ru);
+                        *reinterpret_cast<uint4*>(row) = x;
+                        *reinterpret_cast<uint4*>(row + 16384) = y;
                     }
-                    rope_step(cs, sn, dcs, dsn);
+                    at.step(step.c, step.n, dsn);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -787,10 +809,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     const int d = node < 0 ? node : r < last ? s->depth[node] : 255;
                     uint32_t ns = 0, nu = 0;
                     if (d != 255) {
-                        angles((uint32_t)(prefix + d), cs, sn);
+                        angles((uint32_t)(prefix + d), at);
                         const uint32_t off = sw128_off(r, u8);
                         uint4 lo = *reinterpret_cast<const uint4*>(kt + off), hi = *reinterpret_cast<const uint4*>(kt + 16384 + off);
-                        rotate(lo, hi, cs, sn, ns, nu);
+                        rotate(lo, hi, at, ns, nu);
                         *reinterpret_cast<uint4*>(kt + off) = lo;
                         *reinterpret_cast<uint4*>(kt + 16384 + off) = hi;
                     }
@@ -814,7 +836,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_S));
         // ================================================== softmax ====
         constexpr int COLS = Sh::COLS, PARTS = Sh::PARTS, CH = 16;    // CH: columns at a time
         const int t = tid - 32 * WARP_S0, wg = t >> 7, ln = t & 127;  // warpgroup, lane of tensor memory
@@ -823,21 +844,23 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         const float scl = a.qk_scale_log2;
         int g = 0;                                        // tiles so far
         bool ok = true;
-        // The warps leave the loop together: one whose wait gave up goes on to the next barrier, which tells the others.
+        // The warps leave together: one whose wait gave up goes on to the next barrier, where all of them learn it, and
+        // no way out lies anywhere but behind one.
         auto wait = [&](uint64_t& bar, int parity) {
             if (ok) ok = wait_all(bar, parity);
         };
+        auto failed = [&]() -> bool {
+            if (named_bar_or(1, TR_SOFTMAX, !ok)) ok = false;
+            return !ok;
+        };
         uint64_t sees = 0;                                // the query's node and its ancestors (0: unused)
+#pragma unroll 1
         for (int k = 0;; ++k) {
             TrSlot* s = &c->slot[k % TR_SLOTS];
             wait(c->u_full[k % TR_SLOTS], k / TR_SLOTS);
+            if (failed()) break;
             const volatile TrUnit* u = &s->u;
-            if (!ok || u->end) {                          // (the others may be at their first tile: two barriers)
-                const bool any = named_bar_or(1, TR_SOFTMAX, !ok);
-                named_bar_or(1, TR_SOFTMAX, !ok);
-                ok = ok && !any;
-                break;
-            }
+            if (u->end) break;
             const int n_keys = u->n_keys, prefix = u->prefix, tree = u->tree, rows = u->rows;
             const int npt = (n_keys + TR_BN - 1) / TR_BN, n_tiles = npt + tree;
             if (u->newq) {
@@ -847,107 +870,122 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
             }
             const uint32_t tO = tmem + 256 + (k & 1) * RR + wg * COLS + lane_addr;
             float m = -INFINITY, l = 0.0f;
+            bool gone = false;                            // all of them leave
+#pragma unroll 1
             for (int i = 0; i < n_tiles; ++i, ++g) {
                 const uint32_t tS = tmem + (g & 1) * 128 + part * COLS + lane_addr;
+                const bool whole = i < npt && n_keys - i * TR_BN >= TR_BN;  // every column is a key that all see
                 wait(c->s_full[g & 1], g >> 1);
+                tc_fence_after();
                 uint32_t xr[CH];
-                float mx = -INFINITY;
-                auto take = [&](int h) {  // 16 columns of the thread, what is hidden at -inf
-                    tmem_ld16(tS + h * CH, xr);
+                auto take = [&](int c0) {  // 16 columns from c0 of the thread on, what is hidden at -inf
+                    tmem_ld16(tS + c0, xr);
                     tmem_ld_wait();
-                    const int c0 = part * COLS + h * CH;
-                    if (i < npt) {        // whole pages of the prefix
-                        if (n_keys - i * TR_BN > c0) return;
-#pragma unroll
-                        for (int x = 0; x < CH; ++x) xr[x] = 0xff800000u;
-                    } else {              // the prefix's keys and the nodes that the query sees
+                    if (whole) return;
+                    c0 += part * COLS;
+                    uint32_t see;
+                    if (i < npt) {         // whole pages of the prefix
+                        see = n_keys - i * TR_BN > c0 ? 0xffffu : 0u;
+                    } else {               // the prefix's keys and the nodes that the query sees
                         const int at = c0 - (prefix & (PAGE - 1));  // the node of the first column (before 0: prefix)
-                        const uint32_t see = at >= 64 ? 0u : at >= 0 ? (uint32_t)(sees >> at) : (uint32_t)(sees << -at) | ((1u << -at) - 1u);
-#pragma unroll
-                        for (int x = 0; x < CH; ++x) xr[x] = (see >> x) & 1u ? xr[x] : 0xff800000u;
+                        see = at >= 64 ? 0u : at >= 0 ? (uint32_t)(sees >> at) : (uint32_t)(sees << -at) | ((1u << -at) - 1u);
                     }
+#pragma unroll
+                    for (int x = 0; x < CH; ++x) xr[x] = (see >> x) & 1u ? xr[x] : 0xff800000u;
                 };
-                if (ok) {
-                    tc_fence_after();
+                auto largest = [&](float mx) {
+                    float m0 = mx, m1 = __uint_as_float(xr[1]);
+#pragma unroll
+                    for (int x = 0; x < CH; x += 4) {
+                        m0 = fmaxf(fmaxf(m0, __uint_as_float(xr[x])), __uint_as_float(xr[x + 2]));
+                        m1 = fmaxf(fmaxf(m1, __uint_as_float(xr[x + 1])), __uint_as_float(xr[x + 3]));
+                    }
+                    return fmaxf(m0, m1);
+                };
+                // A tile's weights are made with the maximum as it is.  Where some query's has grown by too much (and
+                // at an item's first tile, which has none yet) the maxima are exchanged and the tile is done again.
+                float sum = 0.0f;
+                bool again = i == 0;
+                float mt = -INFINITY;
+                if (i == 0 && ok) {
 #pragma unroll 1
-                    for (int h = 0; h < COLS / CH; ++h) {
+                    for (int h = 0; h < COLS; h += CH) {
                         take(h);
-                        float m0 = mx, m1 = __uint_as_float(xr[1]);
-#pragma unroll
-                        for (int x = 0; x < CH; x += 4) {
-                            m0 = fmaxf(fmaxf(m0, __uint_as_float(xr[x])), __uint_as_float(xr[x + 2]));
-                            m1 = fmaxf(fmaxf(m1, __uint_as_float(xr[x + 1])), __uint_as_float(xr[x + 3]));
-                        }
-                        mx = fmaxf(m0, m1);
+                        mt = largest(mt);
                     }
+                    mt *= scl;
                 }
-                float mt = mx * scl;
-                if (named_bar_or(1, TR_SOFTMAX, mt > m + TR_SLACK || !ok)) {
-                    // some query's maximum moves (or a wait gave up)
-                    c->ex[part * RR + r] = mt;
-                    if (named_bar_or(1, TR_SOFTMAX, !ok)) {
-                        ok = false;
-                        break;
-                    }
+                while (true) {
+                    if (again) {
+                        c->ex[part * RR + r] = mt;
+                        if ((gone = failed())) break;
 #pragma unroll
-                    for (int x = 0; x < PARTS; ++x) mt = fmaxf(mt, c->ex[x * RR + r]);
-                    float alpha = 1.0f;
-                    if (mt > m + TR_SLACK) {
-                        alpha = ex2(m - mt);  // 0 for the first
-                        m = mt;
-                    }
-                    l *= alpha;
-                    if (i > 0) {
-                        if (named_bar_or(1, TR_SOFTMAX, alpha != 1.0f)) {  // (and the maxima have been read)
-                            if (part == 0) c->ex[r] = alpha;
+                        for (int x = 0; x < PARTS; ++x) mt = fmaxf(mt, c->ex[x * RR + r]);
+                        float alpha = 1.0f;
+                        if (mt > m + TR_SLACK) {
+                            alpha = ex2(m - mt);  // 0 for the first
+                            m = mt;
+                        }
+                        l *= alpha;
+                        if (i > 0) {              // O^T, once PV of the tile before is in it: dim ln of COLS queries
                             wait(c->pv_done[(g - 1) & 1], (g - 1) >> 1);
-                            if (named_bar_or(1, TR_SOFTMAX, !ok)) {
-                                ok = false;
-                                break;
-                            }
+                            if ((gone = failed())) break;  // (the maxima have been read)
+                            if (part == 0) c->ex[r] = alpha;
+                            named_bar_sync(1, TR_SOFTMAX);
                             tc_fence_after();
 #pragma unroll 1
-                            for (int h = 0; h < COLS / CH; ++h) {
+                            for (int h = 0; h < COLS; h += CH) {
                                 uint32_t rr[CH];
-                                tmem_ld16(tO + h * CH, rr);
+                                tmem_ld16(tO + h, rr);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int x = 0; x < CH; ++x) rr[x] = __float_as_uint(__uint_as_float(rr[x]) * c->ex[wg * COLS + h * CH + x]);
-                                tmem_st16(tO + h * CH, rr);
+                                for (int x = 0; x < CH; ++x) rr[x] = __float_as_uint(__uint_as_float(rr[x]) * c->ex[wg * COLS + h + x]);
+                                tmem_st16(tO + h, rr);
                             }
                             tmem_st_wait();
                         }
                     }
-                    // (the exchange is written again behind a barrier)
-                }
-                // P^T's buffer: read by PV of the tile PBUF before this one
-                if (g >= Sh::PBUF) wait(c->pv_done[(g - Sh::PBUF) & 1], (g - Sh::PBUF) >> 1);
-                if (!ok) continue;  // leaves at the next barrier, with the others
-                const float nm = m == -INFINITY ? 0.0f : -m;
-                const float2 sc2 = make_float2(scl, scl), nm2 = make_float2(nm, nm);
-                float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
-                uint8_t* prow = sm + Sh::OFF_P + (g % Sh::PBUF) * Sh::P_BYTES;
+                    const float nm = m == -INFINITY ? 0.0f : -m;
+                    const float2 sc2 = make_float2(scl, scl), nm2 = make_float2(nm, nm);
+                    float2 acc0 = make_float2(0.0f, 0.0f), acc1 = acc0;
+                    mt = -INFINITY;
+                    constexpr int CW = COLS < 32 ? COLS : 32;  // columns whose weights wait in registers for P^T's buffer
 #pragma unroll 1
-                for (int h = 0; h < COLS / CH; ++h) {
-                    if (COLS > CH) take(h);
-                    uint32_t pr[CH / 2];
+                    for (int h = 0; ok && h < COLS; h += CW) {
+                        uint32_t pr[CW / 2];
 #pragma unroll
-                    for (int x = 0; x < CH; x += 4) {
-                        const float2 t0 = ffma2(make_float2(__uint_as_float(xr[x]), __uint_as_float(xr[x + 1])), sc2, nm2);
-                        const float2 t1 = ffma2(make_float2(__uint_as_float(xr[x + 2]), __uint_as_float(xr[x + 3])), sc2, nm2);
-                        const float2 e0 = make_float2(ex2(t0.x), ex2(t0.y)), e1 = make_float2(ex2(t1.x), ex2(t1.y));
-                        acc0 = fadd2(acc0, e0);
-                        acc1 = fadd2(acc1, e1);
-                        pr[x >> 1] = pack_bf16x2(e0.x, e0.y);
-                        pr[(x >> 1) + 1] = pack_bf16x2(e1.x, e1.y);
+                        for (int e = 0; e < CW; e += CH) {
+                            take(h + e);
+                            mt = largest(mt);
+#pragma unroll
+                            for (int x = 0; x < CH; x += 4) {
+                                const float2 t0 = ffma2(make_float2(__uint_as_float(xr[x]), __uint_as_float(xr[x + 1])), sc2, nm2);
+                                const float2 t1 = ffma2(make_float2(__uint_as_float(xr[x + 2]), __uint_as_float(xr[x + 3])), sc2, nm2);
+                                const float2 e0 = make_float2(ex2(t0.x), ex2(t0.y)), e1 = make_float2(ex2(t1.x), ex2(t1.y));
+                                acc0 = fadd2(acc0, e0);
+                                acc1 = fadd2(acc1, e1);
+                                pr[(e + x) >> 1] = pack_bf16x2(e0.x, e0.y);
+                                pr[((e + x) >> 1) + 1] = pack_bf16x2(e1.x, e1.y);
+                            }
+                        }
+                        // P^T's buffer: read by PV of the tile PBUF before this one
+                        if (h == 0 && g >= Sh::PBUF) wait(c->pv_done[(g - Sh::PBUF) & 1], (g - Sh::PBUF) >> 1);
+                        const int col = part * COLS + h;   // chunks of 8 keys of the query's row
+                        uint8_t* prow = sm + Sh::OFF_P + (g % Sh::PBUF) * Sh::P_BYTES + (col >> 6) * (RR * 128);
+                        if (ok) {
+#pragma unroll
+                            for (int x = 0; x < CW / 8; ++x)
+                                *reinterpret_cast<uint4*>(prow + sw128_off(r, ((col & 63) >> 3) + x)) =
+                                    make_uint4(pr[4 * x], pr[4 * x + 1], pr[4 * x + 2], pr[4 * x + 3]);
+                        }
                     }
-                    const int col = part * COLS + h * CH;  // chunks of 8 keys of the query's row of P^T
-#pragma unroll
-                    for (int x = 0; x < CH / 8; ++x)
-                        *reinterpret_cast<uint4*>(prow + (col >> 6) * (RR * 128) + sw128_off(r, ((col & 63) >> 3) + x)) =
-                            make_uint4(pr[4 * x], pr[4 * x + 1], pr[4 * x + 2], pr[4 * x + 3]);
+                    sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                    mt *= scl;
+                    again = named_bar_or(1, TR_SOFTMAX, mt > m + TR_SLACK || !ok);
+                    if (!again) break;
                 }
-                l += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+                if (gone) break;
+                l += sum;
                 tc_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -956,17 +994,12 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     mbar_arrive(smem_u32(&c->p_ready[g % Sh::PBUF]));
                 }
             }
-            if (!ok) {
-                if (named_bar_or(1, TR_SOFTMAX, true)) break;
-            }
+            if (gone) break;
             // ---- the item's results ----
             float* ex_sum = reinterpret_cast<float*>(c + 1);
             if (part) ex_sum[(part - 1) * RR + r] = l;
             wait(c->r_full[k & 1], k >> 1);
-            if (named_bar_or(1, TR_SOFTMAX, !ok)) {
-                ok = false;
-                break;
-            }
+            if (failed()) break;
             const size_t row0 = first_row(a, u->b, u->kvh) + u->block * TR_SPAN;
             const int direct = u->direct, split = u->split;
             if (t < RR) {  // part 0 of query t, whole warps
@@ -992,24 +1025,21 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 }
             }
             wait(c->o_done[k & 1], k >> 1);
-            if (named_bar_or(1, TR_SOFTMAX, !ok)) {
-                ok = false;
-                break;
-            }
+            if (failed()) break;
             tc_fence_after();
             // thread: dim ln of queries wg * COLS ..
             const size_t step = direct ? HEAD_DIM : (size_t)a.n_splits * HEAD_DIM;
             float* part_o = a.o_part + (row0 * a.n_splits + split) * HEAD_DIM + wg * COLS * step + ln;
             __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out) + (row0 + wg * COLS) * HEAD_DIM + ln;
 #pragma unroll 1
-            for (int h = 0; h < COLS / CH; ++h) {
+            for (int h = 0; h < COLS; h += CH) {
                 uint32_t rr[CH];
-                tmem_ld16(tO + h * CH, rr);
+                tmem_ld16(tO + h, rr);
                 tmem_ld_wait();
-                const int left = rows - wg * COLS - h * CH;
+                const int left = rows - wg * COLS - h;
 #pragma unroll
                 for (int x = 0; x < CH; ++x) {
-                    const float f = c->ex[wg * COLS + h * CH + x];
+                    const float f = c->ex[wg * COLS + h + x];
                     const float y = f == 0.0f ? 0.0f : __uint_as_float(rr[x]) * f;  // (a failed query's O may be NaN)
                     if (x < left) {
                         if (direct) *out = __float2bfloat16_rn(y);
