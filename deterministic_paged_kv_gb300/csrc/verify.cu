@@ -12,12 +12,15 @@
 // The last token is argmax r(v) / race(v): of independent exponential draws of rates r(v) the first to ring, which
 // has the distribution r; unlike an inverse of the cumulative sum it does not depend on an order of summation.
 //
+// Its keys are compared as logarithms, log2 w - log2 race, in the same pass as the sum where what is left is known
+// before it (p itself, or p without the children's tokens), so the usual last node needs no second pass.
+//
 // Work: a cluster of 1 to 16 CTAs (by the batch) walks a row, reading only the nodes that the walk
 // reaches.  A pass deals the vocabulary in chunks of 8 to the lanes of 64 virtual warps, a lane's chunks in
-// ascending order (running maximum and sum), and adds the warps up in a fixed tree, so a row's results depend on
-// its data and V alone: not on the cluster, nor on how a row lies in memory (a row that does not start at 16
-// bytes is read in whole vectors and shifted).  A warp pushes its partial results into every CTA's
-// shared memory; behind one cluster barrier a pass every warp adds them up and decides for itself.
+// ascending order (each chunk's own maximum and sum, joined to the lane's), and joins lanes and warps in a fixed tree, so a
+// row's results depend on its data and V alone: not on the cluster, nor on how a row lies in memory (a row that does
+// not start at 16 bytes is read in whole vectors and shifted).  A warp pushes its partial results into every CTA's
+// shared memory; behind one cluster barrier a pass every warp joins them and decides for itself.
 // Bound by bytes for many rows and by the chain of passes for few: a round trip to memory, a barrier and
 // a few shuffles each.
 #include <algorithm>
@@ -30,18 +33,22 @@ namespace rk {
 
 namespace {
 
-constexpr int VF_WARPS = 64;                 // virtual warps of a pass
-constexpr int VF_BLOCK = VF_WARPS * 32 * 8;  // tokens that they take in one round
-constexpr int VF_MAX_THREADS = 512;
-constexpr int VF_BITS = 8192;                // chunks with a child's token, by number modulo this
+constexpr int VF_WARPS = 64;            // virtual warps of a pass
+constexpr int VF_STEP = VF_WARPS * 32;  // chunks that they take in one round
+constexpr int VF_MAX_THREADS = 256;
 
-struct VfPart {
-    float m, s;   // largest logit and sum of weights relative to it; or a sum; or the largest key
-    int v, bad;   // a token that has the largest, or its chunk's first; a value that is none was met
+struct alignas(32) VfPart {
+    float m, s;    // largest logit and sum of weights relative to it; or a sum alone
+    int v;         // first token of the chunk that has the largest logit
+    int bad;       // a value that is none was met
+    float key;     // largest key of the race (relative to m, as the weights)
+    int kv;        // its token, or its chunk's first
+    int pad[2];
 };
 struct VfShared {
     VfPart part[2][VF_WARPS];
-    uint32_t child[VF_BITS / 32];
+    int par[64], tok[64];  // the row's tree
+    float coin[64];
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -52,64 +59,104 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// 16 bytes into the same place of another CTA of the cluster.
-__device__ __forceinline__ void push(const void* at, uint32_t rank, const VfPart& x) {
+// Into the same place of another CTA of the cluster.
+__device__ __forceinline__ void push(const VfPart* at, uint32_t rank, const VfPart& x) {
     asm volatile(
         "{\n\t.reg .b32 ra;\n\tmapa.shared::cluster.u32 ra, %0, %1;\n\t"
-        "st.shared::cluster.v4.b32 [ra], {%2, %3, %4, %5};\n\t}" ::"r"(smem_u32(at)),
-        "r"(rank), "r"(__float_as_uint(x.m)), "r"(__float_as_uint(x.s)), "r"(x.v), "r"(x.bad)
+        "st.shared::cluster.v4.b32 [ra], {%2, %3, %4, %5};\n\t"
+        "st.shared::cluster.v2.b32 [ra + 16], {%6, %7};\n\t}" ::"r"(smem_u32(at)),
+        "r"(rank), "r"(__float_as_uint(x.m)), "r"(__float_as_uint(x.s)), "r"(x.v), "r"(x.bad), "r"(__float_as_uint(x.key)), "r"(x.kv)
         : "memory");
 }
 
-// Eight values of a row from element 8 j on, those past the end as `fill`.
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Largest of a warp's values (a NaN is left out), in every lane.
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Eight values of a row from element 8 j on, those past the end as `fill`: asked for, and then taken apart.  (A row
+// that does not start at 16 bytes is put together as it arrives; other rows' chunks can be on their way several at a time.)
 template <bool F32>
-__device__ __forceinline__ void load8(const char* row, unsigned j, int V, float fill, float (&x)[8]) {
-    constexpr int SIZE = F32 ? 4 : 2, VECS = F32 ? 2 : 1;
-    const size_t v0 = (size_t)j * 8;
-    const char* at = row + v0 * SIZE;
-    if (v0 + 8 > (size_t)V) {
+struct Chunk {
+    static constexpr int SIZE = F32 ? 4 : 2, VECS = F32 ? 2 : 1;
+    uint32_t w[VECS * 4];
+    __device__ __forceinline__ void fetch(const char* row, unsigned j, int V, float fill) {
+        const size_t v0 = (size_t)j * 8;
+        const char* at = row + v0 * SIZE;
+        const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u;  // the same for every chunk
+        if (v0 + 8 > (size_t)V) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = fill;
-            if (v0 + e < (size_t)V)
-                x[e] = F32 ? __ldg(reinterpret_cast<const float*>(at) + e) : bf16lo(__ldg(reinterpret_cast<const unsigned short*>(at) + e));
+            for (int e = 0; e < 8; ++e) {
+                const bool in = v0 + e < (size_t)V;
+                if constexpr (F32) {
+                    w[e] = in ? __ldg(reinterpret_cast<const uint32_t*>(at) + e) : __float_as_uint(fill);
+                } else {
+                    const uint32_t x = in ? __ldg(reinterpret_cast<const unsigned short*>(at) + e) : __float_as_uint(fill) >> 16;
+                    w[e / 2] = e & 1 ? w[e / 2] | x << 16 : x;
+                }
+            }
+        } else if (off == 0) {
+#pragma unroll
+            for (int e = 0; e < VECS; ++e) reinterpret_cast<uint4*>(w)[e] = __ldg(reinterpret_cast<const uint4*>(at) + e);
+        } else {
+            // (the vector behind the last whole one holds some of the chunk too, so it may be read)
+            uint32_t x[VECS * 4 + 4];
+#pragma unroll
+            for (int e = 0; e <= VECS; ++e) reinterpret_cast<uint4*>(x)[e] = __ldg(reinterpret_cast<const uint4*>(at - off) + e);
+            if (off & 4)
+#pragma unroll
+                for (int e = 0; e + 1 < VECS * 4 + 4; ++e) x[e] = x[e + 1];
+            if (off & 8)
+#pragma unroll
+                for (int e = 0; e + 2 < VECS * 4 + 4; ++e) x[e] = x[e + 2];
+#pragma unroll
+            for (int e = 0; e < VECS * 4; ++e) w[e] = __funnelshift_r(x[e], x[e + 1], (off & 2) * 8);
         }
-        return;
     }
-    const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(at) & 15u;  // the same for every chunk of the row
-    const uint4* vec = reinterpret_cast<const uint4*>(at - off);
-    uint32_t w[VECS * 4 + 4];
+    // (whole and at 16 bytes)
+    __device__ __forceinline__ void load(const char* row, unsigned j) {
+        const uint4* at = reinterpret_cast<const uint4*>(row) + (size_t)j * VECS;
 #pragma unroll
-    for (int e = 0; e <= VECS; ++e) {
-        // (the vector behind the last holds some of the chunk where there is an offset, so it may be read)
-        const uint4 y = e < VECS || off ? __ldg(vec + e) : make_uint4(0, 0, 0, 0);
-        w[4 * e] = y.x;
-        w[4 * e + 1] = y.y;
-        w[4 * e + 2] = y.z;
-        w[4 * e + 3] = y.w;
+        for (int e = 0; e < VECS; ++e) reinterpret_cast<uint4*>(w)[e] = __ldg(at + e);
     }
-    if (off & 4)
+    __device__ __forceinline__ void fill(float x) {
 #pragma unroll
-        for (int e = 0; e + 1 < VECS * 4 + 4; ++e) w[e] = w[e + 1];
-    if (off & 8)
+        for (int e = 0; e < VECS * 4; ++e) w[e] = F32 ? __float_as_uint(x) : __float_as_uint(x) >> 16 | (__float_as_uint(x) & 0xffff0000u);
+    }
+    // The largest (a NaN is left out).
+    __device__ __forceinline__ float max() const {
+        if constexpr (F32) {
+            float x = __uint_as_float(w[0]);
 #pragma unroll
-        for (int e = 0; e + 2 < VECS * 4 + 4; ++e) w[e] = w[e + 2];
-    if constexpr (F32) {
+            for (int e = 1; e < 8; ++e) x = fmaxf(x, __uint_as_float(w[e]));
+            return x;
+        } else {
+            uint32_t x = w[0];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
-    } else {
+            for (int e = 1; e < 4; ++e) asm("max.bf16x2 %0, %0, %1;" : "+r"(x) : "r"(w[e]));
+            return fmaxf(bf16lo(x), bf16hi(x));
+        }
+    }
+    __device__ __forceinline__ void take(float2 (&x)[4]) const {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t u = __funnelshift_r(w[e], w[e + 1], (off & 2) * 8);
-            x[2 * e] = bf16lo(u);
-            x[2 * e + 1] = bf16hi(u);
+            if constexpr (F32) x[e] = make_float2(__uint_as_float(w[2 * e]), __uint_as_float(w[2 * e + 1]));
+            else x[e] = make_float2(bf16lo(w[e]), bf16hi(w[e]));
         }
     }
-}
+};
 
 // All of a row's walk (see the head of the file).
 template <bool F32>
-__global__ void __launch_bounds__(VF_MAX_THREADS) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ VfShared sh;
     const uint32_t rank = cluster_rank();
     const int ctas = a.cluster, b = blockIdx.x / ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -122,30 +169,28 @@ __global__ void __launch_bounds__(VF_MAX_THREADS) verify_kernel(const __grid_con
     const unsigned chunks = ((unsigned)V + 7) / 8;
     const bool probs = a.draft_probs != nullptr;
 
-    // ---- the row's tree: nodes lane and lane + 32 of every warp ----
-    int par[2], tok[2];
-    float coin[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int n = lane + 32 * e;
-        par[e] = n < T ? a.parents[node0 + n] : TREE_UNUSED;
-        tok[e] = n < T ? a.draft_tokens[node0 + n] : 0;
-        coin[e] = n < T ? a.coins[node0 + n] : 0.0f;
+    // ---- the row's tree ----
+    if (tid < 64) {
+        sh.par[tid] = tid < T ? a.parents[node0 + tid] : TREE_UNUSED;
+        sh.tok[tid] = tid < T ? a.draft_tokens[node0 + tid] : 0;
+        sh.coin[tid] = tid < T ? a.coins[node0 + tid] : 0.0f;
     }
     const float temp = a.temperature[b];
     const bool greedy = temp == 0.0f;
-    for (int i = tid; i < VF_BITS / 32; i += blockDim.x) sh.child[i] = 0;
-    {
-        // The last draw's numbers on their way to L2, and in a small batch the nodes' logits (each CTA its share).
-        auto fetch = [&](const char* p, size_t bytes) {
-            for (size_t i = ((size_t)rank * blockDim.x + tid) * 128; i < bytes; i += (size_t)ctas * blockDim.x * 128)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
-        };
-        if (a.prefetch_nodes) fetch(logits + node0 * V * SIZE, (size_t)T * V * SIZE);
+    // On its way to L2 (each CTA its share).
+    auto fetch = [&](const char* p, size_t bytes) {
+        for (size_t i = ((size_t)rank * blockDim.x + tid) * 128; i < bytes; i += (size_t)ctas * blockDim.x * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+    };
+    if (a.prefetch_nodes) {
+        fetch(logits + node0 * V * SIZE, (size_t)T * V * SIZE);
         if (!greedy) fetch(race, (size_t)V * 4);
     }
-    auto of = [&](const int (&x)[2], int n) {  // node n's value
-        const int lo = __shfl_sync(0xffffffffu, x[0], n & 31), hi = __shfl_sync(0xffffffffu, x[1], n & 31);
+    __syncthreads();
+    // (nodes lane and lane + 32 are a lane's)
+    auto of = [&](float lo, float hi, int n) {  // node n's value
+        lo = __shfl_sync(0xffffffffu, lo, n & 31);
+        hi = __shfl_sync(0xffffffffu, hi, n & 31);
         return n & 32 ? hi : lo;
     };
     auto ballot = [&](bool lo, bool hi) {
@@ -157,19 +202,20 @@ __global__ void __launch_bounds__(VF_MAX_THREADS) verify_kernel(const __grid_con
         bool wrong[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int n = lane + 32 * e, up = of(par, par[e] & 63);
-            wrong[e] = par[e] < TREE_UNUSED || par[e] >= n || (par[e] >= 0 && up == TREE_UNUSED) ||
-                       (n > 0 && par[e] != TREE_UNUSED && (tok[e] < 0 || tok[e] >= V));
+            const int n = lane + 32 * e, p = sh.par[n];
+            wrong[e] = p < TREE_UNUSED || p >= n || (p >= 0 && sh.par[p] == TREE_UNUSED) ||
+                       (n > 0 && p != TREE_UNUSED && (sh.tok[n] < 0 || sh.tok[n] >= V));
         }
         if (ballot(wrong[0], wrong[1])) bad |= RK_STATUS_TREE;
     }
-    const bool rootless = !bad && of(par, 0) == TREE_UNUSED;
+    const bool rootless = !bad && sh.par[0] == TREE_UNUSED;
     const float scale = greedy ? 1.0f : temp, chi = (float)(1.4426950408889634074 / (double)scale);
     const bool writes = rank == 0 && warp == 0;
 
-    // ---- a pass: f(chunk, part) for a lane's chunks, join(x, y) of two parts; the result in every lane ----
+    // ---- a pass: f(warp, part) for the lanes of a virtual warp, join(x, y) of two parts, and all(x) of a warp's; the
+    // result in every lane ----
     int pass = 0;
-    auto sweep = [&](VfPart zero, auto f, auto join) {
+    auto sweep = [&](VfPart zero, auto f, auto join, auto all) {
         VfPart* buf = sh.part[pass & 1];
         ++pass;
 #pragma unroll 1
@@ -177,15 +223,7 @@ __global__ void __launch_bounds__(VF_MAX_THREADS) verify_kernel(const __grid_con
             const int vw = (int)rank * mine + w;
             VfPart x = zero;
             f(vw, x);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                VfPart y;
-                y.m = __shfl_xor_sync(0xffffffffu, x.m, o);
-                y.s = __shfl_xor_sync(0xffffffffu, x.s, o);
-                y.v = __shfl_xor_sync(0xffffffffu, x.v, o);
-                y.bad = __shfl_xor_sync(0xffffffffu, x.bad, o);
-                join(x, y);
-            }
+            all(x);
             if (ctas == 1) {
                 if (lane == 0) buf[vw] = x;
             } else if (lane < ctas) {
@@ -196,32 +234,30 @@ __global__ void __launch_bounds__(VF_MAX_THREADS) verify_kernel(const __grid_con
         else cluster_barrier();
         VfPart x = buf[lane];
         join(x, buf[lane + 32]);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            VfPart y;
-            y.m = __shfl_xor_sync(0xffffffffu, x.m, o);
-            y.s = __shfl_xor_sync(0xffffffffu, x.s, o);
-            y.v = __shfl_xor_sync(0xffffffffu, x.v, o);
-            y.bad = __shfl_xor_sync(0xffffffffu, x.bad, o);
-            join(x, y);
-        }
+        all(x);
         return x;
     };
-    // the largest key, the lowest token of equal ones
-    auto join_max = [](VfPart& x, const VfPart& y) {
-        if (y.m > x.m || (y.m == x.m && y.v < x.v)) {
-            x.m = y.m;
-            x.v = y.v;
+    auto first_of = [](float& m, int& v, float m2, int v2) {  // the larger, the lower token of equal ones
+        if (m2 > m || (m2 == m && v2 < v)) {
+            m = m2;
+            v = v2;
         }
-        x.bad |= y.bad;
     };
-    auto join_sum = [](VfPart& x, const VfPart& y) { x.s += y.s; };
-
+    auto first_of_all = [](float& m, int& v) {
+        const float x = warp_max(m);
+        v = __reduce_min_sync(0xffffffffu, m == x ? v : INT32_MAX);
+        m = x;
+    };
+    auto sum_of_all = [](float& s) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    };
     int at = 0, n_acc = 0;
     while (!bad && !rootless) {
         const char* row = logits + (node0 + at) * V * SIZE;
         const char* q = reinterpret_cast<const char*>(a.draft_probs + (probs ? (node0 + at) * V : 0));
-        auto logit = [&](int v) {
+        auto logit = [&](int v) {  // (of a token that there is)
+            v = min(v, V - 1);
             return F32 ? __ldg(reinterpret_cast<const float*>(row) + v) : bf16lo(__ldg(reinterpret_cast<const unsigned short*>(row) + v));
         };
         // ---- the children: their logits and draft probabilities (on their way while the row is read) ----
@@ -229,72 +265,145 @@ __global__ void __launch_bounds__(VF_MAX_THREADS) verify_kernel(const __grid_con
         float lx[2], qx[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            kid[e] = par[e] == at;
-            lx[e] = kid[e] ? logit(tok[e]) : 0.0f;
-            qx[e] = kid[e] && probs && !greedy ? __ldg(reinterpret_cast<const float*>(q) + tok[e]) : 1.0f;
+            const int x = sh.tok[lane + 32 * e];
+            kid[e] = sh.par[lane + 32 * e] == at;
+            lx[e] = kid[e] ? logit(x) : 0.0f;
+            qx[e] = kid[e] && probs && !greedy ? __ldg(reinterpret_cast<const float*>(q) + x) : 1.0f;
         }
         uint64_t kids = ballot(kid[0], kid[1]);
         const bool leave = !greedy && !probs && kids;  // the sum goes without the children's tokens
+        const bool run = !greedy && (!probs || !kids); // the race is run along
         bool dup[2] = {false, false};                  // has a child before it the same token
         if (leave) {
-            if (warp == 0) {
-                for (int e = 0; e < 2; ++e)
-                    if (kid[e]) atomicOr(&sh.child[(tok[e] / 8 % VF_BITS) / 32], 1u << (tok[e] / 8 % 32));
-            }
-            for (uint64_t left = kids; left; left &= left - 1) {
-                const int n = __ffsll((long long)left) - 1, x = of(tok, n);
+            for (uint64_t rest = kids; rest; rest &= rest - 1) {
+                const int n = __ffsll((long long)rest) - 1, x = sh.tok[n];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) dup[e] |= kid[e] && lane + 32 * e > n && tok[e] == x;
+                for (int e = 0; e < 2; ++e) dup[e] |= kid[e] && lane + 32 * e > n && sh.tok[lane + 32 * e] == x;
             }
-            __syncthreads();
         }
-        // tokens of chunk j that children have, as eight bits
+        // Whether the lanes of virtual warp vw meet a child's token at all, and the tokens of chunk j that
+        // are children's, as eight bits (whole warps call the first).
+        auto meets = [&](int vw) {
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) hit |= kid[e] && (unsigned)sh.tok[lane + 32 * e] / 8 % VF_STEP / 32 == (unsigned)vw;
+            return leave && __any_sync(0xffffffffu, hit);
+        };
         auto taken = [&](unsigned j) -> uint32_t {
             uint32_t hit = 0;
-            for (uint64_t left = kids; left; left &= left - 1) {
-                const int x = of(tok, __ffsll((long long)left) - 1);
+            for (uint64_t rest = kids; rest; rest &= rest - 1) {
+                const int x = sh.tok[__ffsll((long long)rest) - 1];
                 if ((unsigned)x / 8 == j) hit |= 1u << (x & 7);
             }
             return hit;
         };
-        // (whole warps call it: the lists of children lie in lanes)
-        auto out_of = [&](unsigned j) -> uint32_t {
-            const bool maybe = leave && ((sh.child[(j % VF_BITS) / 32] >> (j % 32)) & 1u);
-            return __any_sync(0xffffffffu, maybe) ? taken(j) : 0u;
-        };
-        // ---- the row's maximum, where it is, and the sum ----
-        VfPart z = sweep({-INFINITY, 0.0f, INT32_MAX, 0},
-                         [&](int vw, VfPart& x) {
-#pragma unroll 2
-                             for (unsigned j0 = vw * 32; j0 < chunks; j0 += VF_WARPS * 32) {
-                                 const unsigned j = j0 + lane;
-                                 float l[8];
-                                 load8<F32>(row, j, V, -INFINITY, l);  // (past the end: no address is formed beyond the row)
-                                 const float top = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
-                                 if (top > x.m) {
-                                     x.s *= ex2((x.m - top) * chi);
-                                     x.m = top;
-                                     x.v = (int)(j * 8);
-                                 }
-                                 const float m = x.m == -INFINITY ? 0.0f : x.m;
-                                 const uint32_t hit = out_of(j);
-                                 float s = 0.0f;
+        auto at16 = [](const char* row) { return (reinterpret_cast<uintptr_t>(row) & 15u) == 0; };
+        auto whole = [&](unsigned j) { return j - lane + 32 <= (unsigned)V / 8; };  // a warp's chunks up to lane 31's
+        constexpr int GROUP = F32 ? 2 : 4;  // chunks asked for at a time
+        auto ask = [&](auto& c, const char* from, unsigned j, float fill) {
+            constexpr int N = sizeof(c) / sizeof(c[0]);
+            if (at16(from) && whole(j + (N - 1) * VF_STEP)) {
 #pragma unroll
-                                 for (int e = 0; e < 8; ++e) {
-                                     const float w = ex2((l[e] - m) * chi);
-                                     s += (hit >> e) & 1u ? 0.0f : w;
-                                 }
-                                 x.s += s;
-                             }
-                         },
-                         [&](VfPart& x, const VfPart& y) {
-                             const float top = fmaxf(x.m, y.m);
-                             const float fx = x.m == -INFINITY ? 0.0f : ex2((x.m - top) * chi), fy = y.m == -INFINITY ? 0.0f : ex2((y.m - top) * chi);
-                             const float sx = x.s * fx, sy = y.s * fy;
-                             x.s = __fadd_rn(sx, sy);
-                             if (y.m > x.m || (y.m == x.m && y.v < x.v)) x.v = y.v;
-                             x.m = top;
-                         });
+                for (int u = 0; u < N; ++u) c[u].load(from, j + u * VF_STEP);
+            } else {
+#pragma unroll
+                for (int u = 0; u < N; ++u) {
+                    if (u == 0 || j + u * VF_STEP - lane < chunks) c[u].fetch(from, j + u * VF_STEP, V, fill);
+                    else c[u].fill(fill);
+                }
+            }
+        };
+        // ---- the row's maximum (greedy: the first chunk that has it), the sum, and the race ----
+        VfPart z = sweep(
+            {-INFINITY, 0.0f, INT32_MAX, 0, -INFINITY, INT32_MAX},
+            [&](int vw, VfPart& x) {
+                const bool some = meets(vw);
+#pragma unroll 1
+                for (unsigned j0 = vw * 32 + lane; j0 - lane < chunks; j0 += GROUP * VF_STEP) {
+                    Chunk<F32> c[GROUP];
+                    ask(c, row, j0, -INFINITY);
+                    float big = x.m;
+#pragma unroll
+                    for (int u = 0; u < GROUP; ++u) big = fmaxf(big, c[u].max());
+                    if (big > x.m) {
+                        const float g = (x.m - big) * chi;
+                        x.s *= ex2(g);
+                        x.key = fmaxf(x.key + g, -INFINITY);  // (never NaN)
+                        x.m = big;
+                        if (greedy)
+#pragma unroll
+                            for (int u = GROUP - 1; u >= 0; --u)
+                                if (c[u].max() == big) x.v = (int)(j0 + u * VF_STEP) * 8;
+                    }
+                    const float m = big == -INFINITY ? 0.0f : big;
+                    float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int u = 0; u < GROUP; ++u) {
+                        const unsigned j = j0 + u * VF_STEP;
+                        if (j - lane >= chunks) break;
+                        Chunk<true> rc;
+                        if (run) {
+                            if (at16(race) && whole(j)) rc.load(race, j);
+                            else rc.fetch(race, j, V, 1.0f);
+                        }
+                        float2 d[4];
+                        c[u].take(d);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d[e] = fmul2(fadd2(d[e], make_float2(-m, -m)), make_float2(chi, chi));
+                        if (some) {
+                            const uint32_t hit = taken(j);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if ((hit >> (2 * e)) & 1u) d[e].x = -INFINITY;
+                                if ((hit >> (2 * e)) & 2u) d[e].y = -INFINITY;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s2 = fadd2(s2, make_float2(ex2(d[e].x), ex2(d[e].y)));
+                        if (run) {
+                            float2 r[4];
+                            rc.take(r);
+                            float key = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                d[e] = make_float2(d[e].x - lg2(r[e].x), d[e].y - lg2(r[e].y));
+                                key = fmaxf(key, fmaxf(d[e].x, d[e].y));
+                            }
+                            if (key > x.key) {  // (seldom)
+                                x.key = key;
+                                int at8 = 7;
+#pragma unroll
+                                for (int e = 3; e >= 0; --e) {
+                                    if (d[e].y == key) at8 = 2 * e + 1;
+                                    if (d[e].x == key) at8 = 2 * e;
+                                }
+                                x.kv = (int)(j * 8) + at8;
+                            }
+                        }
+                    }
+                    x.s += s2.x + s2.y;
+                }
+            },
+            [&](VfPart& x, const VfPart& y) {
+                const float top = fmaxf(x.m, y.m);
+                const float gx = x.m == top ? 0.0f : (x.m - top) * chi, gy = y.m == top ? 0.0f : (y.m - top) * chi;
+                x.s = __fadd_rn(__fmul_rn(x.s, ex2(gx)), __fmul_rn(y.s, ex2(gy)));
+                first_of(x.m, x.v, y.m, y.v);
+                x.key = fmaxf(x.key + gx, -INFINITY);
+                first_of(x.key, x.kv, fmaxf(y.key + gy, -INFINITY), y.kv);
+            },
+            [&](VfPart& x) {
+                const float own = x.m;
+                if (greedy) first_of_all(x.m, x.v);
+                else x.m = warp_max(x.m);
+                const float g = own == x.m ? 0.0f : (own - x.m) * chi;
+                x.s *= ex2(g);
+                sum_of_all(x.s);
+                if (run) {
+                    x.key = fmaxf(x.key + g, -INFINITY);
+                    first_of_all(x.key, x.kv);
+                }
+            });
         const float top = z.m;
         auto weight = [&](float l) { return ex2((l - top) * chi); };
         // ---- what is left when each child is tried, if the ones before it were rejected (drafts without probabilities) ----
@@ -306,8 +415,7 @@ __global__ void __launch_bounds__(VF_MAX_THREADS) verify_kernel(const __grid_con
             for (uint64_t rest = kids; rest;) {
                 const int n = 63 - __clzll((long long)rest);
                 rest ^= 1ull << n;
-                const float lo = __shfl_sync(0xffffffffu, dup[0] ? 0.0f : w[0], n & 31), hi = __shfl_sync(0xffffffffu, dup[1] ? 0.0f : w[1], n & 31);
-                Z += n & 32 ? hi : lo;
+                Z += of(dup[0] ? 0.0f : w[0], dup[1] ? 0.0f : w[1], n);
                 if (n == lane) left[0] = Z;
                 if (n == lane + 32) left[1] = Z;
             }
@@ -320,18 +428,27 @@ __global__ void __launch_bounds__(VF_MAX_THREADS) verify_kernel(const __grid_con
         auto logp = [&](float l) { return (l - top) / scale - lnZ; };
         if (n_acc == 0 && writes && lane == 0) a.path[node0] = 0;
         const int here = n_acc++;
-        int best = z.v;  // the first token of the chunk that has the maximum
+        int best = 0;
         if (greedy) {
-            const bool hit = lane < 8 && best + lane < V && logit(min(best + lane, V - 1)) == top;
+            best = z.v;  // the first token of the chunk that has the maximum
+            const bool hit = lane < 8 && best + lane < V && logit(best + lane) == top;
             best += __ffs(__ballot_sync(0xffffffffu, hit)) - 1;
         }
+        auto race_at = [&](int v) { return __ldg(reinterpret_cast<const float*>(race) + min(v, V - 1)); };
+        auto first_lane = [](bool x) { return __ffs(__ballot_sync(0xffffffffu, x)) - 1; };
         // ---- the children in order ----
         int took = -1;
         float aq = 0.0f, S = 1.0f;
+        // the key of a token of what is left (all: of p), -inf where it has no part in it
+        auto left_key = [&](int all, float l, float d, float r) {
+            if (all) return (l - top) * chi - lg2(r);
+            const float k = fmaf(weight(l), inv, -aq * d);
+            return k > 0.0f ? lg2(k) - lg2(r) : -INFINITY;
+        };
         if (!probs || greedy) {
             bool yes[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) yes[e] = kid[e] && (greedy ? tok[e] == best : !dup[e] && coin[e] * left[e] < w[e]);
+            for (int e = 0; e < 2; ++e) yes[e] = kid[e] && (greedy ? sh.tok[lane + 32 * e] == best : !dup[e] && sh.coin[lane + 32 * e] * left[e] < w[e]);
             const uint64_t hit = ballot(yes[0], yes[1]);
             if (hit) took = __ffsll((long long)hit) - 1;
         } else {
@@ -340,91 +457,111 @@ __global__ void __launch_bounds__(VF_MAX_THREADS) verify_kernel(const __grid_con
                 rest &= rest - 1;
                 bool yes[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) yes[e] = lane + 32 * e == n && coin[e] * qx[e] * S < fmaxf(fmaf(w[e], inv, -aq * qx[e]), 0.0f);
+                for (int e = 0; e < 2; ++e) yes[e] = lane + 32 * e == n && sh.coin[n] * qx[e] * S < fmaxf(fmaf(w[e], inv, -aq * qx[e]), 0.0f);
                 if (ballot(yes[0], yes[1])) {
                     took = n;
                     break;
                 }
                 aq += S;
                 if (!rest) break;
-                const VfPart y = sweep({0.0f, 0.0f, 0, 0},
-                                       [&](int vw, VfPart& x) {
-#pragma unroll 2
-                                           for (unsigned j0 = vw * 32; j0 < chunks; j0 += VF_WARPS * 32) {
-                                               float l[8], d[8];
-                                               load8<F32>(row, j0 + lane, V, -INFINITY, l);
-                                               load8<true>(q, j0 + lane, V, 0.0f, d);
-                                               float s = 0.0f;
+                const VfPart y = sweep(
+                    {0.0f, 0.0f, 0, 0, 0.0f, 0},
+                    [&](int vw, VfPart& x) {
+#pragma unroll 1
+                        for (unsigned j0 = vw * 32 + lane; j0 - lane < chunks; j0 += GROUP * VF_STEP) {
+                            Chunk<F32> c[GROUP];
+                            Chunk<true> qc[GROUP];
+                            ask(c, row, j0, -INFINITY);
+                            ask(qc, q, j0, 0.0f);
 #pragma unroll
-                                               for (int e = 0; e < 8; ++e) {
-                                                   const float r = fmaf(weight(l[e]), inv, -aq * d[e]);
-                                                   s += fmaf(r, 0.0f, fmaxf(r, 0.0f));  // NaN where q is none or infinite
-                                               }
-                                               x.s += s;
-                                           }
-                                       },
-                                       join_sum);
+                            for (int u = 0; u < GROUP; ++u) {
+                                if (j0 + u * VF_STEP - lane >= chunks) break;
+                                float2 l[4], d[4], s = make_float2(0.0f, 0.0f), none = s;
+                                c[u].take(l);
+                                qc[u].take(d);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 r = ffma2(make_float2(weight(l[e].x), weight(l[e].y)), make_float2(inv, inv),
+                                                           fmul2(d[e], make_float2(-aq, -aq)));
+                                    s = fadd2(s, make_float2(fmaxf(r.x, 0.0f), fmaxf(r.y, 0.0f)));
+                                    none = ffma2(r, make_float2(0.0f, 0.0f), none);  // NaN where q is none or infinite
+                                }
+                                s = fadd2(s, none);
+                                x.s += s.x + s.y;
+                            }
+                        }
+                    },
+                    [](VfPart& x, const VfPart& y) { x.s += y.s; }, [&](VfPart& x) { sum_of_all(x.s); });
                 S = y.s;
                 if (!(S >= 0.0f)) bad |= RK_STATUS_RANGE;
             }
             if (bad) break;
         }
         if (took >= 0) {
-            if (leave && warp == 0) {  // the bits of these children go (the pass that read them lies behind a barrier)
-                for (int e = 0; e < 2; ++e)
-                    if (kid[e]) sh.child[(tok[e] / 8 % VF_BITS) / 32] = 0;
-            }
-            const int x = of(tok, took);
-            const float lo = __shfl_sync(0xffffffffu, lx[0], took & 31), hi = __shfl_sync(0xffffffffu, lx[1], took & 31);
+            const float l = of(lx[0], lx[1], took);
             if (writes && lane == 0) {
-                a.tokens[node0 + here] = x;
-                a.logprobs[node0 + here] = logp(took & 32 ? hi : lo);
+                a.tokens[node0 + here] = sh.tok[took];
+                a.logprobs[node0 + here] = logp(l);
                 a.path[node0 + here + 1] = took;
             }
             at = took;
             continue;
         }
         // ---- the last token: of what is left, or of p where that is nothing ----
-        int last = best;
-        for (int all = 0; !greedy && all < 2; ++all) {
-            const VfPart y = sweep({-1.0f, 0.0f, INT32_MAX, 0},
-                                   [&](int vw, VfPart& x) {
-#pragma unroll 2
-                                       for (unsigned j0 = vw * 32; j0 < chunks; j0 += VF_WARPS * 32) {
-                                           const unsigned j = j0 + lane;
-                                           float l[8], r[8], d[8];
-                                           load8<F32>(row, j, V, -INFINITY, l);
-                                           load8<true>(race, j, V, 1.0f, r);
-                                           const bool minus = probs && !all && aq > 0.0f;
-                                           if (minus) load8<true>(q, j, V, 0.0f, d);
-                                           const uint32_t hit = all ? 0u : out_of(j);
+        int last = greedy ? best : INT32_MAX;
+        if (run) last = z.kv;
+        for (int all = run; last >= V && all < 2; ++all) {
+            const VfPart y = sweep(
+                {0.0f, 0.0f, 0, 0, -INFINITY, INT32_MAX},
+                [&](int vw, VfPart& x) {
+#pragma unroll 1
+                    for (unsigned j0 = vw * 32 + lane; j0 - lane < chunks; j0 += 2 * VF_STEP) {
+                        Chunk<F32> c[2];
+                        Chunk<true> rc[2], qc[2];
+                        ask(c, row, j0, -INFINITY);
+                        ask(rc, race, j0, 1.0f);
+                        if (!all) ask(qc, q, j0, 0.0f);
 #pragma unroll
-                                           for (int e = 0; e < 8; ++e) {
-                                               float k = weight(l[e]);
-                                               if (minus) {
-                                                   k = fmaf(k, inv, -aq * d[e]);
-                                                   if (!(fabsf(k) < INFINITY)) x.bad = 1;
-                                               }
-                                               if ((hit >> e) & 1u) k = 0.0f;
-                                               if (k > 0.0f) {
-                                                   k = __fdividef(k, r[e]);
-                                                   if (k > x.m) {
-                                                       x.m = k;
-                                                       x.v = (int)(j * 8) + e;
-                                                   }
-                                               }
-                                           }
-                                       }
-                                   },
-                                   join_max);
+                        for (int u = 0; u < 2; ++u) {
+                            if (j0 + u * VF_STEP - lane >= chunks) break;
+                            float2 l[4], r[4], d[4];
+                            c[u].take(l);
+                            rc[u].take(r);
+                            if (!all) qc[u].take(d);
+                            float key = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                key = fmaxf(key, left_key(all, l[e].x, d[e].x, r[e].x));
+                                key = fmaxf(key, left_key(all, l[e].y, d[e].y, r[e].y));
+                                if (!all && !(fabsf(d[e].x) < INFINITY && fabsf(d[e].y) < INFINITY)) x.bad = 1;
+                            }
+                            if (key > x.key) {
+                                x.key = key;
+                                x.kv = (int)((j0 + u * VF_STEP) * 8);
+                            }
+                        }
+                    }
+                },
+                [&](VfPart& x, const VfPart& y) {
+                    first_of(x.key, x.kv, y.key, y.kv);
+                    x.bad |= y.bad;
+                },
+                [&](VfPart& x) {
+                    first_of_all(x.key, x.kv);
+                    x.bad = __any_sync(0xffffffffu, x.bad);
+                });
             if (y.bad) bad |= RK_STATUS_RANGE;
-            if (y.v < V || bad) {
-                last = y.v;
-                break;
+            if (bad) break;
+            if (y.kv < V) {
+                const int v = min(y.kv + (lane & 7), V - 1);
+                const float d = all ? 0.0f : __ldg(reinterpret_cast<const float*>(q) + v);
+                last = y.kv + first_lane(lane < 8 && y.kv + lane < V && left_key(all, logit(v), d, race_at(v)) == y.key);
             }
         }
-        if (bad) break;
-        if (last >= V || last < 0) last = best;
+        if (bad || last >= V) {  // (no draw of the race is a number that is not negative)
+            bad |= RK_STATUS_RANGE;
+            break;
+        }
         if (writes && lane == 0) {
             a.tokens[node0 + here] = last;
             a.logprobs[node0 + here] = logp(logit(last));
