@@ -242,15 +242,22 @@ __global__ void __launch_bounds__(TAB_THREADS) tokens_kernel(const __grid_consta
 // ---- the inverse: tokens leave the rows' ends, emptied pages go back to the pool ----
 //
 // One prefix sum over the rows, of the pages that come free; then each freed page finds its
-// row by bisection and moves to its place.  The CTAs of a launch are one cluster: each sums the
-// rows for itself and moves a share of the pages, and when all have read the lengths and taken,
-// the first writes the new ones (which may be the same arrays).
+// row by bisection and moves to its place.  Large tables take two launches, many CTAs that each sum
+// the rows for themselves and move a share of the pages, and one that writes the new lengths and
+// taken (which may be the arrays that the others read) when those are done.
+// Bound by latency: launch, one round of loads, the scan, the pages' loads and stores.  1024 rows that free
+// 260000 pages: 7.7 us (one CTA 205, a cluster of 8 CTAs 35); 64 rows of up to 500 pages that free 130: 5.6 us,
+// 4.7 by one CTA, which takes tables of up to 4096 entries.
+//
+// MOVE: the pages; WRITE: the lengths and taken.
+template <bool MOVE, bool WRITE>
 __global__ void __launch_bounds__(TAB_THREADS) trim_kernel(const __grid_constant__ TrimArgs a) {
     extern __shared__ int32_t rows[];
     __shared__ long long sh[64];
     int32_t* s_first = rows;        // a row's first freed page, counted over the batch
     int32_t* s_left = rows + a.B;   // the pages that it keeps
     int32_t* s_len = rows + 2 * a.B;  // its length after the drop
+    if constexpr (!WRITE) griddep_launch_dependents();
     const int tid = threadIdx.x, ctas = (int)gridDim.x, cta = (int)blockIdx.x;
     const int per = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;
     const int r0 = min(a.B, tid * per), r1 = min(a.B, r0 + per);
@@ -299,7 +306,7 @@ __global__ void __launch_bounds__(TAB_THREADS) trim_kernel(const __grid_constant
     }
     __syncthreads();
     const int total = (int)all, base = taken - total;
-    for (int i = cta * (int)blockDim.x + tid; i < total; i += ctas * (int)blockDim.x) {
+    for (int i = MOVE ? cta * (int)blockDim.x + tid : total; i < total; i += ctas * (int)blockDim.x) {
         int lo = 0, hi = a.B;  // the last row that starts at or before page i (rows that free none share a start)
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -312,10 +319,9 @@ __global__ void __launch_bounds__(TAB_THREADS) trim_kernel(const __grid_constant
         a.pool[base + i] = page;
         *e = -1;
     }
-    __syncthreads();
-    if (ctas > 1)  // every CTA has read the lengths and taken
-        asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-    if (cta == 0) {
+    if constexpr (WRITE) {
+        if constexpr (!MOVE) griddep_wait();
+        __syncthreads();
         for (int r = tid; r < a.B; r += (int)blockDim.x) a.kv_lens_out[r] = s_len[r];
         if (tid == 0) *a.taken_out = taken - total;
     }
@@ -333,23 +339,31 @@ cudaError_t launch_trim(const TrimArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(configured.load() & bit)) {
-        e = cudaFuncSetAttribute(trim_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * TAB_MAX_ROWS * 4);
-        if (e != cudaSuccess) return e;
+        for (const void* f : {(const void*)trim_kernel<true, true>, (const void*)trim_kernel<true, false>, (const void*)trim_kernel<false, true>}) {
+            e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * TAB_MAX_ROWS * 4);
+            if (e != cudaSuccess) return e;
+        }
         configured.fetch_or(bit);
     }
-    const bool small = (long long)a.B * a.W <= 4 * TAB_THREADS;
+    const long long pages = (long long)a.B * a.W;  // that may come free
+    if (pages <= 4 * TAB_THREADS) {
+        trim_kernel<true, true><<<1, a.B <= 128 ? 128 : TAB_THREADS, smem, stream>>>(a);
+        return cudaGetLastError();
+    }
+    trim_kernel<true, false><<<(unsigned)std::min<long long>(152, (pages + TAB_THREADS - 1) / TAB_THREADS), TAB_THREADS, smem, stream>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(small ? 1 : 8);
-    cfg.blockDim = dim3(small && a.B <= 128 ? 128 : TAB_THREADS);
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(TAB_THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = small ? 1 : 8;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, trim_kernel, a);
+    return cudaLaunchKernelEx(&cfg, trim_kernel<false, true>, a);
 }
 
 cudaError_t launch_tables(const TablesArgs& a, cudaStream_t stream) {

@@ -689,7 +689,8 @@ int rk_paged_attn_tree(const rk_paged_plan_t *plan, const void *q, const void *k
  *   logprobs_d    fp32 [B, T]: ln p of those tokens (temperature 0: with 1); 0 behind
  * Status: RK_STATUS_TREE (parents, a used node's token outside [0, V)), RK_STATUS_RANGE (a
  * temperature that is negative, not finite or below 2^-64; at a node that the walk reaches, logits
- * that are NaN, +inf or all -inf; draft probabilities that are NaN or not finite, where they are read): the row keeps
+ * that are NaN, +inf or all -inf; draft probabilities that are NaN or not finite, where they are read;
+ * a race without a number in it): the row keeps
  * nothing: n_accepted 0, n_drop T, tokens and path -1, logprobs NaN.
  * A row whose node 0 is unused gives n_accepted 0, n_drop 0 without a status.
  * Sums are FP32 in an order that V alone fixes: a row's results do not depend on the batch.
@@ -734,11 +735,12 @@ int rk_paged_kv_compact(const rk_paged_plan_t *plan, const int32_t *path_d, cons
  *   block_table_d int32 [B, W], in place: the freed entries become -1, no other is touched
  *   kv_lens_out_d int32 [B] (it and taken_out_d may be the array that they follow)
  * The other arrays must not overlap each other.  A row stays as it was, and the status word says why, if its
- * length is negative or passes W * 16 or its n_drop is not in [0, kv_len] (RK_STATUS_KVLEN), if a
- * page id that it would free is outside [0, num_pages) (RK_STATUS_PAGE_OOB), or if the pages of the rows
- * up to it (rows without a place left out) are more than taken while it frees one (RK_STATUS_POOL; also
- * taken outside [0, n_pool], which leaves no place).
- * Plan: B, W, num_pages (B at most 16384, else RK_E_UNSUPPORTED).  No allocation, no host synchronisation.
+ * length is negative or passes W * 16 or its n_drop is not in [0, kv_len] (RK_STATUS_KVLEN), or if the
+ * pages of the rows up to it (rows without a place left out) are more than taken while it frees one
+ * (RK_STATUS_POOL; also taken outside [0, n_pool], which leaves no place).  A freed entry outside
+ * [0, num_pages) goes into the pool like the others, with RK_STATUS_PAGE_OOB.
+ * Plan: B, W, num_pages (B at most 16384, else RK_E_UNSUPPORTED).  One launch, or two for tables of more than
+ * 4096 entries; no allocation, no host synchronisation.
  * Errors: RK_E_ARG (null or misaligned pointer, negative n_pool), RK_E_DEVICE, RK_E_CUDA.
  */
 int rk_paged_tables_trim(const rk_paged_plan_t *plan, const int32_t *n_drop_d, const int32_t *kv_lens_d, int32_t *pool_d,
