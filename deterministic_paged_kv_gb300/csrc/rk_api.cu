@@ -1189,11 +1189,11 @@ int tree_parts(const rk_paged_plan_t* plan, rk::TreeArgs* a, uint64_t* bytes) {
     // a part is cheap to merge.  In us, for 1 row of 777 and 32 queries / 64 x 4096 and 32 / 20 ragged rows and 104 / 8 x
     // 2048 and 256 / 2 rows past 100000 and 64: all 1024 20.0 / 202 / 117 / 58.6 / 163, 512 first 17.1 / 205 / 120 /
     // 61.6 / 165, all 512 16.5 / 209 / 139 / 65.7 / 178 (2048 from 16384 on: no difference).
-    a->zone[0] = {0, 0, R <= 64 ? 512 : 1024};
-    a->zone[1] = {1024 / a->zone[0].size, 1024, 1024};
+    a->zone[0] = {0, 0, R <= 64 ? 9 : 10};
+    a->zone[1] = {1024 >> a->zone[0].shift, 1024, 10};
     const int64_t cap = (int64_t)plan->W * rk::PAGE;
     const int z = cap > a->zone[1].token;
-    const int64_t parts = cap > 0 ? a->zone[z].split + (cap - a->zone[z].token + a->zone[z].size - 1) / a->zone[z].size : 1;
+    const int64_t parts = cap > 0 ? a->zone[z].split + ((cap - a->zone[z].token + (1 << a->zone[z].shift) - 1) >> a->zone[z].shift) : 1;
     if ((double)plan->B * plan->Hkv * blocks * ((double)cap / 128 + 2) > 2147483647.0 ||
         (double)plan->B * plan->Hkv * parts * R > 2147483647.0)
         return fail(RK_E_UNSUPPORTED, "B %d x Hkv %d x W %d: too many", plan->B, plan->Hkv, plan->W);

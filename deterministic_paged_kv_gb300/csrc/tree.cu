@@ -107,20 +107,23 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, PipeCtl
 // ------------------------------------------------------------ geometry ----
 
 // A row's prefix in whole pages, and why the row has none (status bits; kv_len 0: -1 and no bit).
-__device__ __forceinline__ int row_pages16(const TreeArgs& a, int b, int& kv, int& bad) {
+template <class A>
+__device__ __forceinline__ int row_pages16(const A& a, int b, int& kv, int& bad) {
     kv = a.kv_lens[b];
     bad = kv < 0 || kv > a.W * PAGE || (kv > 0 && kv < a.T) ? RK_STATUS_KVLEN : 0;
     return bad || kv == 0 ? -1 : (kv - a.T) & ~(PAGE - 1);
 }
 // Parts of a row with n prefix keys in whole pages (one where there are none).
-__device__ __forceinline__ int parts_of(const TreeArgs& a, int n) {
+template <class A>
+__device__ __forceinline__ int parts_of(const A& a, int n) {
     if (n <= 0) return 1;
     const int z = n > a.zone[1].token;
-    return a.zone[z].split + (n - a.zone[z].token + a.zone[z].size - 1) / a.zone[z].size;
+    return a.zone[z].split + ((n - a.zone[z].token + (1 << a.zone[z].shift) - 1) >> a.zone[z].shift);
 }
-__device__ __forceinline__ int part_start(const TreeArgs& a, int s) {
+template <class A>
+__device__ __forceinline__ int part_start(const A& a, int s) {
     const int z = s >= a.zone[1].split;
-    return a.zone[z].token + (s - a.zone[z].split) * a.zone[z].size;
+    return a.zone[z].token + ((s - a.zone[z].split) << a.zone[z].shift);
 }
 // Tiles of a row: its prefix's and the tree's (one for a row without keys, which is an item too).
 __device__ __forceinline__ int row_tiles(int n) { return n < 0 ? 1 : (n + TR_BN - 1) / TR_BN + 1; }
@@ -131,45 +134,51 @@ __device__ __forceinline__ int row_tiles(int n) { return n < 0 ? 1 : (n + TR_BN 
 // neighbours, at about the same time.  Run v of all is run v / heads of head v % heads; CTA c has the runs
 // c, c + grid, ...
 struct TrItems {
-    int v, b, s;            // run, row, part
+    int v, m, kvh, block;   // run: the m-th of its head and block of queries
+    int b, s;               // row, part
     int kv, n, ns, bad;     // the row's length, prefix keys in whole pages, parts, status
     int at, hi;             // the part's first tile, the run's end
-    __device__ __forceinline__ int head(int heads) const { return v % heads; }
     __device__ __forceinline__ bool valid(const TreeArgs& a, int heads) const { return v < heads * a.members; }
-    __device__ void row(const TreeArgs& a) {
+    // (divisions that need no metadata)
+    __device__ __forceinline__ void place(int run, int heads, int blocks) {
+        v = run;
+        m = v / heads;
+        const int h = v - m * heads;
+        kvh = blocks == 1 ? h : h / blocks;
+        block = h - kvh * blocks;
+    }
+    __device__ __forceinline__ void row(const TreeArgs& a) {
         if (b < a.B) {
             n = row_pages16(a, b, kv, bad);
             ns = parts_of(a, n);
         }
     }
     // The first part of run v that there is, or of a later run of this CTA.
-    __device__ __noinline__ void start(const TreeArgs& a, int total, const int* pre, int heads, int run) {
-        for (v = run; v < heads * a.members; v += (int)gridDim.x) {
-            const unsigned m = (unsigned)(v / heads), each = (unsigned)total / a.members, rest = (unsigned)total % a.members;
-            at = (int)(each * m + rest * m / a.members);
-            hi = (int)(each * (m + 1) + rest * (m + 1) / a.members);
-            const int per = (a.B + TR_GROUPS - 1) / TR_GROUPS, groups = (a.B + per - 1) / per;
-            int lo = 0, top = groups;
-            while (top - lo > 1) {
-                const int mid = (lo + top) >> 1;
-                if (pre[mid] <= at) lo = mid;
-                else top = mid;
-            }
+    __device__ __forceinline__ void find(const TreeArgs& a, int total, const int* pre, int heads, int blocks) {
+#pragma unroll 1
+        for (; valid(a, heads); place(v + (int)gridDim.x, heads, blocks)) {
+            at = min(total, (int)((uint64_t)(unsigned)total * (a.share * (unsigned)m) >> 32));
+            hi = min(total, (int)((uint64_t)(unsigned)total * (a.share * (unsigned)(m + 1)) >> 32));
+            if (at >= hi) continue;
+            const int per = (a.B + TR_GROUPS - 1) / TR_GROUPS;
+            int lo = 0;  // the last group that begins at or before the tile (those without rows begin at the total)
+#pragma unroll 1
+            for (int half = TR_GROUPS / 2; half; half >>= 1)
+                if (pre[lo + half] <= at) lo += half;
             b = lo * per;
-            int base = pre[lo];
-            for (;;) {
+            int base = pre[lo], rt;
+#pragma unroll 1
+            for (;; base += rt, ++b) {
                 row(a);
-                const int rt = row_tiles(n);
+                rt = row_tiles(n);
                 if (at - base < rt || b + 1 >= a.B) break;
-                base += rt;
-                ++b;
             }
             const int tile = at - base;
             s = tile ? parts_of(a, min(max(n, 0), tile * TR_BN)) : 0;  // the first part that starts at this tile or later
             if (s < ns) {
                 at = base + part_start(a, s) / TR_BN;
             } else {
-                at = base + row_tiles(n);
+                at = base + rt;
                 s = 0;
                 ++b;
                 row(a);
@@ -177,17 +186,20 @@ struct TrItems {
             if (b < a.B && at < hi) return;
         }
     }
-    __device__ __noinline__ void next(const TreeArgs& a, int total, const int* pre, int heads) {
-        const int from = part_start(a, s) / TR_BN;
+    // To the next part; true: of another run, to be found.
+    __device__ __forceinline__ bool next(const TreeArgs& a, int heads, int blocks) {
+        at -= part_start(a, s) / TR_BN;
         if (++s == ns) {
-            at += row_tiles(n) - from;
+            at += row_tiles(n);
             s = 0;
             ++b;
             row(a);
         } else {
-            at += part_start(a, s) / TR_BN - from;
+            at += part_start(a, s) / TR_BN;
         }
-        if (b >= a.B || at >= hi) start(a, total, pre, heads, v + (int)gridDim.x);
+        const bool over = b >= a.B || at >= hi;
+        if (over) place(v + (int)gridDim.x, heads, blocks);
+        return over;
     }
 };
 
@@ -368,6 +380,8 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         tmem_alloc(smem_u32(&c->tmem_base), Sh::TMEM_COLS);
         tmem_relinquish();
     }
+    TrItems it;                                           // the scheduler's
+    if (warp == WARP_SCHED) it.place((int)blockIdx.x, heads, blocks);
     {
         // Tiles before each group of `per` rows: a group to sixteen threads.
         const int per = (a.B + TR_GROUPS - 1) / TR_GROUPS;
@@ -379,18 +393,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
         if ((tid & 15) == 0 && (tid >> 4) < TR_GROUPS) c->pre[tid >> 4] = cnt;
-        __syncthreads();
-        if (warp == 0) {
-            const int own = c->pre[lane];
-            int v = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int t = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += t;
-            }
-            c->pre[lane] = v - own;
-            if (lane == 31) c->total = v;
-        }
     }
     tc_fence_before();
     __syncthreads();
@@ -404,17 +406,33 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
     if (warp >= WARP_K) {
         if (warp == WARP_SCHED) {
             // ============================================== scheduler ====
-            TrItems it;
-            it.start(a, c->total, c->pre, heads, (int)blockIdx.x);
+            {
+                // Sums to offsets, by the warp that needs them: nothing else waits for them.
+                const int own = c->pre[lane];
+                int sum = own;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int t = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += t;
+                }
+                c->pre[lane] = sum - own;
+                if (lane == 31) c->total = sum;
+                __syncwarp();
+            }
             int k = 0, nq = -1, tree_row = -1;            // published items, queries; row whose tree is in registers
             int up0[2] = {-1, -1}, deep[2] = {255, 255};  // of nodes lane, lane + 32
             int tree_bad = 0;
             int lb = -1, lv = -1;                         // queries of the item before
-            bool ok = true;
+            bool ok = true, past = false;                 // past: `it` is done with
             // checks the item `it`; 0: to be published
             auto judge = [&]() -> int {
                 int bad = it.bad;
                 if (bad || it.n < 0) return bad;
+                // page ids of the item's keys (up to 69; most on their way while the tree is looked at)
+                const int t0 = part_start(a, it.s), end = it.s + 1 < it.ns ? part_start(a, it.s + 1) : it.kv;
+                const int32_t* bt = a.block_table + (size_t)it.b * a.W;
+                const int p0 = t0 / PAGE + lane, p1 = (end + PAGE - 1) / PAGE;
+                const int first = p0 < p1 ? __ldg(bt + p0) : 0, second = p0 + 32 < p1 ? __ldg(bt + p0 + 32) : 0;
                 if (tree_row != it.b) {
                     tree_row = it.b;
                     int p[2], up[2];
@@ -438,7 +456,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     tree_bad = __any_sync(0xffffffffu, wrong) ? RK_STATUS_TREE : 0;
                     // depths: steps to `up`, twice as far up with every turn
 #pragma unroll 1
-                    for (int turn = 0; turn < 6 && !tree_bad; ++turn) {
+                    for (int turn = 0; turn < 6 && !tree_bad && __any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0); ++turn) {
                         int add[2], far[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
@@ -456,38 +474,32 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                         if (p[e] == TREE_UNUSED) deep[e] = 255;
                 }
                 bad |= tree_bad;
-                // page ids of the item's keys
-                const int t0 = part_start(a, it.s), end = it.s + 1 < it.ns ? part_start(a, it.s + 1) : it.kv;
-                const int32_t* bt = a.block_table + (size_t)it.b * a.W;
-                int oob = 0;
-                for (int i = t0 / PAGE + lane; i < (end + PAGE - 1) / PAGE; i += 32) {
-                    const int pg = __ldg(bt + i);
-                    oob |= (pg < 0) | (pg >= a.num_pages);
-                }
+                int oob = (unsigned)first >= (unsigned)a.num_pages || (unsigned)second >= (unsigned)a.num_pages;
+                for (int i = p0 + 64; i < p1; i += 32) oob |= (unsigned)__ldg(bt + i) >= (unsigned)a.num_pages;
                 if (__any_sync(0xffffffffu, oob)) bad |= RK_STATUS_PAGE_OOB;
                 return bad;
             };
-            // goes on to the next item that has something to compute, writing those that have not
-            auto settle = [&]() {
-                while (it.valid(a, heads)) {
-                    const int bad = judge();
-                    if (!bad && it.n >= 0) return;
-                    if (bad && lane == 0 && a.status) atomicOr(a.status, bad);
-                    const int h = it.head(heads);
-                    write_nothing(a, it.b, h / blocks, h % blocks, it.s, it.ns == 1, bad ? __int_as_float(0x7fc00000) : -INFINITY, lane, 32);
-                    it.next(a, c->total, c->pre, heads);
-                }
-            };
+#pragma unroll 1
             while (ok) {
-                settle();
+                // the next item that has something to compute; those that have not are written here
+#pragma unroll 1
+                for (;; past = true) {
+                    if (!past || it.next(a, heads, blocks)) it.find(a, c->total, c->pre, heads, blocks);
+                    if (!it.valid(a, heads)) break;
+                    const int bad = judge();
+                    if (!bad && it.n >= 0) break;
+                    if (bad && lane == 0 && a.status) atomicOr(a.status, bad);
+                    write_nothing(a, it.b, it.kvh, it.block, it.s, it.ns == 1, bad ? __int_as_float(0x7fc00000) : -INFINITY, lane, 32);
+                }
+                past = true;
                 TrUnit u;
                 std::memset(&u, 0, sizeof u);
                 u.end = !it.valid(a, heads);
                 const int u0 = up0[0], u1 = up0[1], d0 = deep[0], d1 = deep[1];
                 if (!u.end) {
                     u.b = it.b;
-                    u.kvh = it.head(heads) / blocks;
-                    u.block = it.head(heads) % blocks;
+                    u.kvh = it.kvh;
+                    u.block = it.block;
                     u.split = it.s;
                     u.t0 = part_start(a, it.s);
                     u.tree = it.s + 1 == it.ns;
@@ -500,7 +512,6 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     u.nq = nq;
                     lb = it.b;
                     lv = it.v;
-                    it.next(a, c->total, c->pre, heads);
                 }
                 TrSlot* s = &c->slot[k % TR_SLOTS];
                 const int use = k / TR_SLOTS;
@@ -1074,15 +1085,18 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
         if (tid == 32 * WARP_S0) *reinterpret_cast<int*>(c->ex) = done;
         __syncthreads();
         int skip = *reinterpret_cast<const int*>(c->ex);
-        TrItems it;
-        for (it.start(a, c->total, c->pre, heads, (int)blockIdx.x); it.valid(a, heads); it.next(a, c->total, c->pre, heads)) {
+        it.place((int)blockIdx.x, heads, blocks);
+        bool found = false;
+#pragma unroll 1
+        for (;; found = true) {
+            if (!found || it.next(a, heads, blocks)) it.find(a, c->total, c->pre, heads, blocks);
+            if (!it.valid(a, heads)) break;
             const bool publishes = it.n >= 0 && !it.bad;
             if (publishes && skip > 0) {
                 --skip;
                 continue;
             }
-            const int h = it.head(heads);
-            write_nothing(a, it.b, h / blocks, h % blocks, it.s, it.ns == 1, __int_as_float(0x7fc00000), tid, TR_THREADS);
+            write_nothing(a, it.b, it.kvh, it.block, it.s, it.ns == 1, __int_as_float(0x7fc00000), tid, TR_THREADS);
         }
         if (tid == 0 && a.status) atomicOr(a.status, RK_STATUS_TIMEOUT);
     }
@@ -1201,6 +1215,7 @@ cudaError_t launch_tree(const CUtensorMap& km, const CUtensorMap& vm, const Tree
     const int R = a.G * a.T, heads = a.Hkv * ((R + TR_SPAN - 1) / TR_SPAN);
     TreeArgs r = a;
     r.members = (int)std::min<long long>(std::max(1, sms / heads), (long long)a.B * a.n_splits);
+    r.share = ((1ull << 32) + r.members - 1) / r.members;
     const unsigned grid = (unsigned)std::min(sms, heads * r.members);
     if (R <= 32) tree_kernel<32><<<grid, TR_THREADS, tr_smem_bytes<32>(), stream>>>(km, vm, r);
     else if (R <= 64) tree_kernel<64><<<grid, TR_THREADS, tr_smem_bytes<64>(), stream>>>(km, vm, r);

@@ -24,10 +24,11 @@ struct TreeArgs {
     int32_t timeout_drill;
     // where a row's prefix is cut: zones of equal parts from a token (and part) on; with more than one part to
     // the widest row: partial O / l [B, Hq, T, n_splits, D] and log2-domain LSE [B, Hq, T, n_splits]
-    struct {
-        int32_t split, token, size;
+    struct Zone {
+        int32_t split, token, shift;  // parts of 2^shift tokens
     } zone[2];
     int32_t members;              // runs that a head's items are dealt to (set at the launch)
+    uint64_t share;               // 2^32 / members, rounded up (set at the launch)
     int32_t n_splits;
     float* o_part;
     float* lse_part;
