@@ -52,7 +52,6 @@ struct VerifyArgs {
     int32_t* status;
     int32_t B, T, V, f32;
     int32_t cluster;              // CTAs of a row, a power of two up to 16 (set at the launch)
-    int32_t prefetch_nodes;       // whether all nodes' logits are fetched to L2 at the start (set at the launch)
 };
 
 // Accepted nodes' K and V to the slots behind the prefix.

@@ -17,12 +17,17 @@
 //
 // Work: a cluster of 1 to 16 CTAs (by the batch) walks a row, reading only the nodes that the walk
 // reaches.  A pass deals the vocabulary in chunks of 8 to the lanes of 64 virtual warps, a lane's chunks in
-// ascending order (each chunk's own maximum and sum, joined to the lane's), and joins lanes and warps in a fixed tree, so a
+// ascending order (in groups of four or two, with the lane's running maximum), and joins lanes and warps in a fixed tree, so a
 // row's results depend on its data and V alone: not on the cluster, nor on how a row lies in memory (a row that does
 // not start at 16 bytes is read in whole vectors and shifted).  A warp pushes its partial results into every CTA's
 // shared memory; behind one cluster barrier a pass every warp joins them and decides for itself.
-// Bound by bytes for many rows and by the chain of passes for few: a round trip to memory, a barrier and
-// a few shuffles each.
+//
+// What bounds it: for few rows the chain of passes, 2.3 us each at V = 32000 (a load, two joins, a cluster barrier, and the
+// node's own numbers): a row of 4 nodes 11 us.  For many rows the instructions of a pass and what its warps wait for:
+// 64 rows of 8 accepted nodes at V = 131072 71 us, 7 us a pass whose 17 MB take 2.5; with rows that end early and draft
+// probabilities 42 (55 with nothing of it in L2).  128 virtual warps gave 50 there, 32 gave 43 and 42 instead of 30 for
+// 20 rows in FP32; asking for a group while the one before is summed changed nothing, nor did fetching the next node or
+// all nodes of a small batch to L2 ahead.
 #include <algorithm>
 #include <atomic>
 
@@ -169,6 +174,8 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
     const unsigned chunks = ((unsigned)V + 7) / 8;
     const bool probs = a.draft_probs != nullptr;
 
+    // (no CTA writes into another before that one runs)
+    if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;");
     // ---- the row's tree ----
     if (tid < 64) {
         sh.par[tid] = tid < T ? a.parents[node0 + tid] : TREE_UNUSED;
@@ -177,16 +184,8 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
     }
     const float temp = a.temperature[b];
     const bool greedy = temp == 0.0f;
-    // On its way to L2 (each CTA its share).
-    auto fetch = [&](const char* p, size_t bytes) {
-        for (size_t i = ((size_t)rank * blockDim.x + tid) * 128; i < bytes; i += (size_t)ctas * blockDim.x * 128)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
-    };
-    if (a.prefetch_nodes) {
-        fetch(logits + node0 * V * SIZE, (size_t)T * V * SIZE);
-        if (!greedy) fetch(race, (size_t)V * 4);
-    }
     __syncthreads();
+    if (ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     // (nodes lane and lane + 32 are a lane's)
     auto of = [&](float lo, float hi, int n) {  // node n's value
         lo = __shfl_sync(0xffffffffu, lo, n & 31);
@@ -598,9 +597,11 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
         configured.fetch_or(bit);
     }
     VerifyArgs r = a;
+    // As many CTAs to a row as have room at two to an SM, all at once.  Chains of 8 accepted nodes, at most 152 CTAs / 304
+    // / 608: 64 x 131072 112 / 71 / 89 us, 20 x 131072 46 / 35 / 35, 64 x 32000 45 / 34 / 50; rows of mixed lengths,
+    // where a waiting cluster takes the room of one that is done, 42 with 304 and 40 with 608.
     r.cluster = 16;
     while (r.cluster > 1 && (long long)a.B * r.cluster > 304) r.cluster /= 2;
-    r.prefetch_nodes = (double)a.B * a.T * a.V * (a.f32 ? 4 : 2) <= 16e6;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * r.cluster));
     cfg.blockDim = dim3((unsigned)std::min(VF_MAX_THREADS, 32 * VF_WARPS / r.cluster));
