@@ -438,11 +438,10 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
         // ---- the children in order ----
         int took = -1;
         float aq = 0.0f, S = 1.0f;
-        // the key of a token of what is left (all: of p), -inf where it has no part in it
-        auto left_key = [&](int all, float l, float d, float r) {
-            if (all) return (l - top) * chi - lg2(r);
-            const float k = fmaf(weight(l), inv, -aq * d);
-            return k > 0.0f ? lg2(k) - lg2(r) : -INFINITY;
+        // the key of a token of what is left (p's own weights: own), -inf where it has no part in it
+        auto left_key = [&](bool own, float l, float d, float r) {
+            const float w = weight(l), k = own ? w : fmaf(w, inv, -aq * d);
+            return k > 0.0f ? (own ? (l - top) * chi : lg2(k)) - lg2(r) : -INFINITY;
         };
         if (!probs || greedy) {
             bool yes[2];
@@ -508,31 +507,36 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
         }
         // ---- the last token: of what is left, or of p where that is nothing ----
         int last = greedy ? best : INT32_MAX;
-        if (run) last = z.kv;
-        for (int all = run; last >= V && all < 2; ++all) {
+        // (the race along with the sum compares tokens with their lanes' maxima, so one that weighs nothing can win it
+        // where its draw is 0; then it is run again)
+        if (run && z.kv < V && weight(logit(z.kv)) > 0.0f) last = z.kv;
+        for (int all = !kids; last >= V && all < 2; ++all) {
+            const bool own = all || !probs;
             const VfPart y = sweep(
                 {0.0f, 0.0f, 0, 0, -INFINITY, INT32_MAX},
                 [&](int vw, VfPart& x) {
+                    const bool some = !all && meets(vw);
 #pragma unroll 1
                     for (unsigned j0 = vw * 32 + lane; j0 - lane < chunks; j0 += 2 * VF_STEP) {
                         Chunk<F32> c[2];
                         Chunk<true> rc[2], qc[2];
                         ask(c, row, j0, -INFINITY);
                         ask(rc, race, j0, 1.0f);
-                        if (!all) ask(qc, q, j0, 0.0f);
+                        if (!own) ask(qc, q, j0, 0.0f);
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             if (j0 + u * VF_STEP - lane >= chunks) break;
                             float2 l[4], r[4], d[4];
                             c[u].take(l);
                             rc[u].take(r);
-                            if (!all) qc[u].take(d);
+                            if (!own) qc[u].take(d);
+                            const uint32_t hit = some ? taken(j0 + u * VF_STEP) : 0u;
                             float key = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                key = fmaxf(key, left_key(all, l[e].x, d[e].x, r[e].x));
-                                key = fmaxf(key, left_key(all, l[e].y, d[e].y, r[e].y));
-                                if (!all && !(fabsf(d[e].x) < INFINITY && fabsf(d[e].y) < INFINITY)) x.bad = 1;
+                                if (!((hit >> (2 * e)) & 1u)) key = fmaxf(key, left_key(own, l[e].x, d[e].x, r[e].x));
+                                if (!((hit >> (2 * e)) & 2u)) key = fmaxf(key, left_key(own, l[e].y, d[e].y, r[e].y));
+                                if (!own && !(fabsf(d[e].x) < INFINITY && fabsf(d[e].y) < INFINITY)) x.bad = 1;
                             }
                             if (key > x.key) {
                                 x.key = key;
@@ -553,8 +557,9 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
             if (bad) break;
             if (y.kv < V) {
                 const int v = min(y.kv + (lane & 7), V - 1);
-                const float d = all ? 0.0f : __ldg(reinterpret_cast<const float*>(q) + v);
-                last = y.kv + first_lane(lane < 8 && y.kv + lane < V && left_key(all, logit(v), d, race_at(v)) == y.key);
+                const float d = own ? 0.0f : __ldg(reinterpret_cast<const float*>(q) + v);
+                const uint32_t hit = !all && leave ? taken((unsigned)y.kv / 8) : 0u;
+                last = y.kv + first_lane(lane < 8 && y.kv + lane < V && !((hit >> lane) & 1u) && left_key(own, logit(v), d, race_at(v)) == y.key);
             }
         }
         if (bad || last >= V) {  // (no draw of the race is a number that is not negative)

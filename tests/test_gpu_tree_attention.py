@@ -338,3 +338,44 @@ def test_many_rows_are_those_of_small_batches(B, T, Hq, Hkv, hi):
         assert _equal([x[lo:lo + 9].contiguous() for x in whole], _run(part))
     few = {k: v[-20:].contiguous() if k in ("q", "block_table", "kv_lens", "parents") else v for k, v in c.items()}
     _near([x[-20:] for x in whole], ref.attention(few))
+
+
+def test_two_calls_at_once_and_two_graphs_with_one_scratch():
+    """Calls on two streams with no order between them, each with its own scratch; two captured graphs that
+    share a scratch and are replayed one after the other."""
+    cases = [ref.case(61, [900, 30, 1500], 6, 8, 2, ["tree"]), ref.case(62, [2500, 1100], 20, 8, 4, ["tree", "star"])]
+    want = [_run(c) for c in cases]
+    plans = [_plan(c) for c in cases]
+    need = [binding.tree_scratch_bytes(p) for p in plans]
+    assert min(need) > 0
+    dev = [{k: v.cuda() for k, v in c.items()} for c in cases]
+    outs = [(torch.empty_like(d["q"]), torch.empty(d["q"].shape[:3], device="cuda")) for d in dev]
+
+    def call(i, scratch):
+        d = dev[i]
+        binding.attn_tree(plans[i], d["q"], d["k_cache"], d["v_cache"], d["block_table"], d["kv_lens"], d["parents"], *outs[i], scratch)
+
+    own = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in need]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                call(i, own[i])
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert _equal(want[i], [x.cpu() for x in outs[i]])
+    shared = torch.empty(max(need), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for i in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(i, shared[:need[i]])
+        graphs.append(g)
+    for o in outs:
+        o[0].zero_()
+    for i in (0, 1, 1, 0, 1, 0):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert _equal(want[i], [x.cpu() for x in outs[i]])

@@ -247,3 +247,74 @@ def test_captured_and_on_another_stream():
     torch.cuda.synchronize()
     got = _run(c, stream=s)
     assert all(torch.equal(want[k].view(i32), got[k].view(i32)) for k in want)
+
+
+@pytest.mark.parametrize("probs", [False, True])
+@pytest.mark.parametrize("low", [-math.inf, -3.3895e38, -1.0e4])
+@pytest.mark.parametrize("V", [300, 40000])
+def test_draws_of_zero_choose_no_token_that_weighs_nothing(V, low, probs):
+    """Masked tokens with a draw of 0 in the race: the results of a race in which their draws are 1."""
+    c = ref.verify_case(47, 8, 5, V, BF, probs, ["tree", "star"])
+    c["logits"][:, :, V // 3:] = low
+    c["race"][:, V // 3:] = 1.0
+    want = _run(c)
+    _check(c, want)
+    c["race"][:, V // 3:] = 0.0
+    got = _run(c)
+    assert all(torch.equal(want[k].view(i32), got[k].view(i32)) for k in want)
+    assert (got["tokens"] < V // 3).all()
+
+
+def test_a_race_without_numbers_is_refused_where_it_is_read():
+    c = ref.verify_case(53, 3, 3, 500, F32, False, ["chain"], temps=(1.0, 1.0, 0.0))
+    want = _run(c)
+    c["race"][0] = math.nan
+    c["race"][2] = math.nan   # greedy: not read
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    got = _run(c, status=st)
+    assert int(st.item()) == binding.STATUS_RANGE
+    assert int(got["n_accepted"][0]) == 0 and got["tokens"][0].tolist() == [-1] * 3 and got["logprobs"][0].isnan().all()
+    assert all(torch.equal(want[k][1:].view(i32), got[k][1:].view(i32)) for k in want)
+
+
+def test_two_captured_calls_at_once():
+    """Two graphs replayed on two streams with no order between them, over and over."""
+    cases = [ref.verify_case(59 + i, 24, 6, V, BF, probs, ["tree", "chain"]) for i, (V, probs) in enumerate(((50000, True), (3001, False)))]
+    want = [_run(c) for c in cases]
+    streams, graphs, outs, keep = [], [], [], []
+    for c in cases:
+        B, T, V = c["logits"].shape
+        d = {k: None if v is None else v.cuda() for k, v in c.items()}
+        o = {k: torch.zeros_like(v, device="cuda") for k, v in want[0].items()}
+        p = binding.plan(B, T, 1, 1, 128, 16, 1, 1)
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            binding.verify_tree(p, d["logits"], d["draft_tokens"], d["parents"], d["coins"], d["race"], d["temperature"],
+                                o["n_accepted"], o["n_drop"], o["path"], o["tokens"], o["logprobs"], draft_probs=d["draft_probs"])
+        streams.append(torch.cuda.Stream())
+        graphs.append(g)
+        outs.append(o)
+        keep.append(d)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w[k].view(i32), o[k].cpu().view(i32)) for k in w)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_hundred_and_more_rows_and_the_smallest_vocabularies(dtype):
+    """Every number of CTAs to a row, and vocabularies that fill no chunk."""
+    for B, T, V in ((305, 3, 70), (160, 4, 5000), (80, 2, 17), (2, 3, 1), (5, 4, 2), (40, 3, 7), (30, 2, 9)):
+        c = ref.verify_case(61 + B, B, T, V, dtype, B % 2 == 0, ["tree", "chain"]) if V >= 3 else None
+        if c is None:
+            g = torch.Generator().manual_seed(V)
+            c = {"logits": torch.randn((B, T, V), generator=g).to(dtype), "draft_probs": None,
+                 "draft_tokens": torch.randint(0, V, (B, T), generator=g, dtype=torch.int64).to(i32),
+                 "parents": torch.arange(-1, T - 1, dtype=i32).expand(B, T).contiguous(), "coins": torch.rand((B, T), generator=g),
+                 "race": torch.rand((B, V), generator=g) + 0.1, "temperature": torch.ones(B)}
+        _check(c, _run(c))
