@@ -281,7 +281,10 @@ const char* rk_paged_policy(void) {
            "q8_decode=fixed_splits_of_512_tokens_and_1024_from_16384_or_of_split_tokens,ordered_fp32_merge,"
            "score_mma=q_in_4_e4m3_parts_fp32_acc,pv_mma=weights_in_3_e4m3_parts_fp32_acc;"
            "q8_prefill=split_kv_disabled,prefill_tile_as_above,score_mma=fp16_operands_fp32_acc,"
-           "pv_mma=fp16_operands_fp32_acc";
+           "pv_mma=fp16_operands_fp32_acc;"
+           "tree=fixed_splits_of_1024_tokens_or_512_before_1024_with_up_to_64_queries_per_kv_head,ordered_fp32_merge,"
+           "score_mma=fp16_operands_fp32_acc,pv_mma=bf16_operands_fp32_acc;"
+           "verify=fp32_sums_of_64_fixed_parts,race_in_fp32_logarithms";
 }
 
 int rk_paged_plan(rk_paged_plan_t* plan, int32_t B, int32_t Sq, int32_t Hq, int32_t Hkv, int32_t D,

@@ -178,3 +178,15 @@ def test_trim_statement():
     got, said = ref.trim([17, 20], [40, 20], [3, 4, 5, 6, 7, 0, 1, 2], 5, bt, 8)
     assert not said and got["kv_lens"] == [23, 0] and got["taken"] == 2
     assert got["block_table"].tolist() == [[3, 4, -1, -1], [-1, -1, -1, -1]] and got["pool"].tolist() == [3, 4, 5, 6, 7, 0, 1, 2]
+
+
+def test_policy_names_the_speculative_step(rk):
+    pol = dict(kv.split("=", 1) for kv in rk.policy().split(";"))
+    assert pol["split_kv"] == "disabled"  # of the calls that it was said of before
+    assert "512_before_1024_with_up_to_64" in pol["tree"] and "1024_tokens" in pol["tree"] and "ordered_fp32_merge" in pol["tree"]
+    assert "64_fixed_parts" in pol["verify"]
+    # the parts that the scratch size tells: of 512 tokens before token 1024 with up to 64 queries a head, else of 1024
+    for T, heads, want in ((64, 1, {512: 0, 528: 2, 1024: 2, 1040: 3, 2048: 3, 2064: 4}), (33, 2, {1024: 0, 1040: 2, 2048: 2, 2064: 3})):
+        for tokens, parts in want.items():
+            p = rk.plan(1, T, heads, 1, 128, 16, 1, tokens // 16)
+            assert rk.tree_scratch_bytes(p) == parts * T * heads * (128 + 1) * 4, (T, tokens)
