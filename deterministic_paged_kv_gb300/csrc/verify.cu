@@ -17,17 +17,18 @@
 //
 // Work: a cluster of 1 to 16 CTAs (by the batch) walks a row, reading only the nodes that the walk
 // reaches.  A pass deals the vocabulary in chunks of 8 to the lanes of 64 virtual warps, a lane's chunks in
-// ascending order (in groups of four or two, with the lane's running maximum), and joins lanes and warps in a fixed tree, so a
+// ascending order (in groups of one, two or four, with the lane's running maximum), and joins lanes and warps in a fixed tree, so a
 // row's results depend on its data and V alone: not on the cluster, nor on how a row lies in memory (a row that does
 // not start at 16 bytes is read in whole vectors and shifted).  A warp pushes its partial results into every CTA's
 // shared memory; behind one cluster barrier a pass every warp joins them and decides for itself.
 //
-// What bounds it: for few rows the chain of passes, 2.3 us each at V = 32000 (a load, two joins, a cluster barrier, and the
-// node's own numbers): a row of 4 nodes 11 us.  For many rows the instructions of a pass and what its warps wait for:
-// 64 rows of 8 accepted nodes at V = 131072 71 us, 7 us a pass whose 17 MB take 2.5; with rows that end early and draft
-// probabilities 42 (55 with nothing of it in L2).  128 virtual warps gave 50 there, 32 gave 43 and 42 instead of 30 for
-// 20 rows in FP32; asking for a group while the one before is summed changed nothing, nor did fetching the next node or
-// all nodes of a small batch to L2 ahead.
+// What bounds it: for few rows the chain of passes, 2.2 us each at V = 32000 (a load, two joins, a cluster barrier, and the
+// node's own numbers): a row of 4 nodes 11 us.  For many rows what the warps of a pass wait for, and its exponentials:
+// 64 rows of 8 accepted nodes at V = 131072 59 us, 7 us a pass, whose 17 MB take 2.5 and whose exponentials take as
+// much.  Of a pass's 12700 cycles the first chunks' way is 1500, a group of four chunks 1100 (four of them), the joins and
+// pushes of two virtual warps 1200, the barrier 1300, the last join 750, the decision 1200.  With rows that end early and
+// draft probabilities 37 us (46 with nothing of it in L2).  Measured against that: chunks asked for only when the
+// ones before are summed 71 and 42; 128 virtual warps 20% slower, 32 in FP32 40%; rows fetched to L2 ahead, no change.
 #include <algorithm>
 #include <atomic>
 
@@ -159,8 +160,8 @@ struct Chunk {
     }
 };
 
-// All of a row's walk (see the head of the file).
-template <bool F32>
+// All of a row's walk (see the head of the file).  GROUP: chunks asked for at a time.
+template <bool F32, int GROUP>
 __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ VfShared sh;
     const uint32_t rank = cluster_rank();
@@ -211,6 +212,8 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
     const float scale = greedy ? 1.0f : temp, chi = (float)(1.4426950408889634074 / (double)scale);
     const bool writes = rank == 0 && warp == 0;
 
+    const unsigned first_chunk = ((unsigned)rank * mine + warp) * 32;  // of this warp
+    const int end = ((int)rank + 1) * mine;
     // ---- a pass: f(warp, part) for the lanes of a virtual warp, join(x, y) of two parts, and all(x) of a warp's; the
     // result in every lane ----
     int pass = 0;
@@ -259,15 +262,35 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
             v = min(v, V - 1);
             return F32 ? __ldg(reinterpret_cast<const float*>(row) + v) : bf16lo(__ldg(reinterpret_cast<const unsigned short*>(row) + v));
         };
+        auto at16 = [](const char* row) { return (reinterpret_cast<uintptr_t>(row) & 15u) == 0; };
+        auto whole = [&](unsigned j) { return j - lane + 32 <= (unsigned)V / 8; };  // a warp's chunks up to lane 31's
+        auto ask = [&](auto& c, const char* from, unsigned j, float fill) {
+            constexpr int N = sizeof(c) / sizeof(c[0]);
+            if (at16(from) && whole(j + (N - 1) * VF_STEP)) {
+#pragma unroll
+                for (int u = 0; u < N; ++u) c[u].load(from, j + u * VF_STEP);
+            } else {
+#pragma unroll
+                for (int u = 0; u < N; ++u) {
+                    if (at16(from) && whole(j + u * VF_STEP)) c[u].load(from, j + u * VF_STEP);
+                    else if (u == 0 || j + u * VF_STEP - lane < chunks) c[u].fetch(from, j + u * VF_STEP, V, fill);
+                    else c[u].fill(fill);
+                }
+            }
+        };
+        Chunk<F32> next[GROUP];  // the row's first chunks, and then those behind the ones that are summed, on their way
+        if (first_chunk < chunks) ask(next, row, first_chunk + lane, -INFINITY);
         // ---- the children: their logits and draft probabilities (on their way while the row is read) ----
         bool kid[2];
-        float lx[2], qx[2];
+        uint32_t lraw[2];  // (asked for unconditionally, of some token: a branch would wait for them)
+        float qraw[2];
+        const float* from = probs ? reinterpret_cast<const float*>(q) : reinterpret_cast<const float*>(race);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int x = sh.tok[lane + 32 * e];
+            const int x = max(0, min(sh.tok[lane + 32 * e], V - 1));
             kid[e] = sh.par[lane + 32 * e] == at;
-            lx[e] = kid[e] ? logit(x) : 0.0f;
-            qx[e] = kid[e] && probs && !greedy ? __ldg(reinterpret_cast<const float*>(q) + x) : 1.0f;
+            lraw[e] = F32 ? __ldg(reinterpret_cast<const uint32_t*>(row) + x) : __ldg(reinterpret_cast<const unsigned short*>(row) + x);
+            qraw[e] = __ldg(from + x);
         }
         uint64_t kids = ballot(kid[0], kid[1]);
         const bool leave = !greedy && !probs && kids;  // the sum goes without the children's tokens
@@ -296,22 +319,6 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
             }
             return hit;
         };
-        auto at16 = [](const char* row) { return (reinterpret_cast<uintptr_t>(row) & 15u) == 0; };
-        auto whole = [&](unsigned j) { return j - lane + 32 <= (unsigned)V / 8; };  // a warp's chunks up to lane 31's
-        constexpr int GROUP = F32 ? 2 : 4;  // chunks asked for at a time
-        auto ask = [&](auto& c, const char* from, unsigned j, float fill) {
-            constexpr int N = sizeof(c) / sizeof(c[0]);
-            if (at16(from) && whole(j + (N - 1) * VF_STEP)) {
-#pragma unroll
-                for (int u = 0; u < N; ++u) c[u].load(from, j + u * VF_STEP);
-            } else {
-#pragma unroll
-                for (int u = 0; u < N; ++u) {
-                    if (u == 0 || j + u * VF_STEP - lane < chunks) c[u].fetch(from, j + u * VF_STEP, V, fill);
-                    else c[u].fill(fill);
-                }
-            }
-        };
         // ---- the row's maximum (greedy: the first chunk that has it), the sum, and the race ----
         VfPart z = sweep(
             {-INFINITY, 0.0f, INT32_MAX, 0, -INFINITY, INT32_MAX},
@@ -320,7 +327,13 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
 #pragma unroll 1
                 for (unsigned j0 = vw * 32 + lane; j0 - lane < chunks; j0 += GROUP * VF_STEP) {
                     Chunk<F32> c[GROUP];
-                    ask(c, row, j0, -INFINITY);
+#pragma unroll
+                    for (int u = 0; u < GROUP; ++u) c[u] = next[u];
+                    {
+                        unsigned j = j0 + GROUP * VF_STEP;
+                        if (j - lane >= chunks) j = vw + warps < end ? (vw + warps) * 32 + lane : ~0u;
+                        if (j < chunks + 31 && j - lane < chunks) ask(next, row, j, -INFINITY);
+                    }
                     float big = x.m;
 #pragma unroll
                     for (int u = 0; u < GROUP; ++u) big = fmaxf(big, c[u].max());
@@ -387,9 +400,12 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                 const float top = fmaxf(x.m, y.m);
                 const float gx = x.m == top ? 0.0f : (x.m - top) * chi, gy = y.m == top ? 0.0f : (y.m - top) * chi;
                 x.s = __fadd_rn(__fmul_rn(x.s, ex2(gx)), __fmul_rn(y.s, ex2(gy)));
-                first_of(x.m, x.v, y.m, y.v);
-                x.key = fmaxf(x.key + gx, -INFINITY);
-                first_of(x.key, x.kv, fmaxf(y.key + gy, -INFINITY), y.kv);
+                if (greedy) first_of(x.m, x.v, y.m, y.v);
+                x.m = top;
+                if (run) {
+                    x.key = fmaxf(x.key + gx, -INFINITY);
+                    first_of(x.key, x.kv, fmaxf(y.key + gy, -INFINITY), y.kv);
+                }
             },
             [&](VfPart& x) {
                 const float own = x.m;
@@ -406,7 +422,10 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
         const float top = z.m;
         auto weight = [&](float l) { return ex2((l - top) * chi); };
         // ---- what is left when each child is tried, if the ones before it were rejected (drafts without probabilities) ----
-        float w[2], left[2] = {1.0f, 1.0f};
+        float lx[2], w[2], left[2] = {1.0f, 1.0f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) lx[e] = F32 ? __uint_as_float(lraw[e]) : bf16lo(lraw[e]);
+        const float* qx = qraw;
 #pragma unroll
         for (int e = 0; e < 2; ++e) w[e] = kid[e] ? weight(lx[e]) : 0.0f;
         float Z = z.s;
@@ -438,10 +457,14 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
         // ---- the children in order ----
         int took = -1;
         float aq = 0.0f, S = 1.0f;
-        // the key of a token of what is left (p's own weights: own), -inf where it has no part in it
-        auto left_key = [&](bool own, float l, float d, float r) {
-            const float w = weight(l), k = own ? w : fmaf(w, inv, -aq * d);
-            return k > 0.0f ? (own ? (l - top) * chi : lg2(k)) - lg2(r) : -INFINITY;
+        // the key of a token of what is left, or by p's own weights; -inf where it has no part in it
+        auto own_key = [&](float l, float r) {
+            const float t = (l - top) * chi;
+            return ex2(t) > 0.0f ? t - lg2(r) : -INFINITY;
+        };
+        auto left_key = [&](float l, float d, float r) {
+            const float k = fmaf(weight(l), inv, -aq * d);
+            return k > 0.0f ? lg2(k) - lg2(r) : -INFINITY;
         };
         if (!probs || greedy) {
             bool yes[2];
@@ -530,13 +553,24 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                             c[u].take(l);
                             rc[u].take(r);
                             if (!own) qc[u].take(d);
-                            const uint32_t hit = some ? taken(j0 + u * VF_STEP) : 0u;
                             float key = -INFINITY;
+                            if (own) {
+                                if (some) {
+                                    const uint32_t hit = taken(j0 + u * VF_STEP);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (!((hit >> (2 * e)) & 1u)) key = fmaxf(key, left_key(own, l[e].x, d[e].x, r[e].x));
-                                if (!((hit >> (2 * e)) & 2u)) key = fmaxf(key, left_key(own, l[e].y, d[e].y, r[e].y));
-                                if (!own && !(fabsf(d[e].x) < INFINITY && fabsf(d[e].y) < INFINITY)) x.bad = 1;
+                                    for (int e = 0; e < 4; ++e) {
+                                        if ((hit >> (2 * e)) & 1u) l[e].x = -INFINITY;
+                                        if ((hit >> (2 * e)) & 2u) l[e].y = -INFINITY;
+                                    }
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) key = fmaxf(key, fmaxf(own_key(l[e].x, r[e].x), own_key(l[e].y, r[e].y)));
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    key = fmaxf(key, fmaxf(left_key(l[e].x, d[e].x, r[e].x), left_key(l[e].y, d[e].y, r[e].y)));
+                                    if (!(fabsf(d[e].x) < INFINITY && fabsf(d[e].y) < INFINITY)) x.bad = 1;
+                                }
                             }
                             if (key > x.key) {
                                 x.key = key;
@@ -559,7 +593,8 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                 const int v = min(y.kv + (lane & 7), V - 1);
                 const float d = own ? 0.0f : __ldg(reinterpret_cast<const float*>(q) + v);
                 const uint32_t hit = !all && leave ? taken((unsigned)y.kv / 8) : 0u;
-                last = y.kv + first_lane(lane < 8 && y.kv + lane < V && !((hit >> lane) & 1u) && left_key(own, logit(v), d, race_at(v)) == y.key);
+                last = y.kv + first_lane(lane < 8 && y.kv + lane < V && !((hit >> lane) & 1u) &&
+                                           (own ? own_key(logit(v), race_at(v)) : left_key(logit(v), d, race_at(v))) == y.key);
             }
         }
         if (bad || last >= V) {  // (no draw of the race is a number that is not negative)
@@ -597,14 +632,14 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(configured.load() & bit)) {
-        if ((e = cudaFuncSetAttribute(verify_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
-        if ((e = cudaFuncSetAttribute(verify_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+        for (const void* f : {(const void*)verify_kernel<false, 2>, (const void*)verify_kernel<false, 4>, (const void*)verify_kernel<true, 1>})
+            if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
     VerifyArgs r = a;
     // As many CTAs to a row as have room at two to an SM, all at once.  Chains of 8 accepted nodes, at most 152 CTAs / 304
-    // / 608: 64 x 131072 112 / 71 / 89 us, 20 x 131072 46 / 35 / 35, 64 x 32000 45 / 34 / 50; rows of mixed lengths,
-    // where a waiting cluster takes the room of one that is done, 42 with 304 and 40 with 608.
+    // / 608: 64 x 131072 86 / 59 / 78 us, 20 x 131072 44 / 33 / 33, 64 x 32000 36 / 29 / 45; rows of mixed lengths,
+    // where a waiting cluster takes the room of one that is done, 54 / 37 / 37.
     r.cluster = 16;
     while (r.cluster > 1 && (long long)a.B * r.cluster > 304) r.cluster /= 2;
     cudaLaunchConfig_t cfg = {};
@@ -617,7 +652,10 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return a.f32 ? cudaLaunchKernelEx(&cfg, verify_kernel<true>, r) : cudaLaunchKernelEx(&cfg, verify_kernel<false>, r);
+    // Chunks of a lane, asked for at a time: in BF16 up to two where that is all.  64 x 32000 29 us with 2, 33 with 4; 64 x
+    // 131072 69 and 59; in FP32 20 x 100003 30.1 with 1, 30.8 with 2.
+    if (a.f32) return cudaLaunchKernelEx(&cfg, verify_kernel<true, 1>, r);
+    return a.V <= 2 * 8 * VF_STEP ? cudaLaunchKernelEx(&cfg, verify_kernel<false, 2>, r) : cudaLaunchKernelEx(&cfg, verify_kernel<false, 4>, r);
 }
 
 }  // namespace rk
