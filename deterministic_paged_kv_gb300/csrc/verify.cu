@@ -12,8 +12,10 @@
 // The last token is argmax r(v) / race(v): of independent exponential draws of rates r(v) the first to ring, which
 // has the distribution r; unlike an inverse of the cumulative sum it does not depend on an order of summation.
 //
-// Its keys are compared as logarithms, log2 w - log2 race, in the same pass as the sum where what is left is known
-// before it (p itself, or p without the children's tokens), so the usual last node needs no second pass.
+// Its keys are compared as logarithms, log2 w - log2 race, at a node without children in the same pass as the sum, so that
+// a walk that accepts a whole path needs no second pass there.  (Drafts without probabilities: run along at every node it
+// saved a pass of 2 to 4 us where the walk ends early, and cost 0.6 to 3 us a node where it does not: 64 x 131072, 8
+// accepted nodes 87 us, and 63 without; 20 trees of 13 x 100003 in FP32 44, and 34.)
 //
 // Work: a cluster of 1 to 16 CTAs (by the batch) walks a row, reading only the nodes that the walk
 // reaches.  A pass deals the vocabulary in chunks of 8 to the lanes of 64 virtual warps, a lane's chunks in
@@ -24,10 +26,10 @@
 //
 // What bounds it: for few rows the chain of passes, 2.2 us each at V = 32000 (a load, two joins, a cluster barrier, and the
 // node's own numbers): a row of 4 nodes 11 us.  For many rows what the warps of a pass wait for, and its exponentials:
-// 64 rows of 8 accepted nodes at V = 131072 59 us, 7 us a pass, whose 17 MB take 2.5 and whose exponentials take as
+// 64 rows of 8 accepted nodes at V = 131072 59 us (63 without probabilities), 7 us a pass, whose 17 MB take 2.5 and whose exponentials take as
 // much.  Of a pass's 12700 cycles the first chunks' way is 1500, a group of four chunks 1100 (four of them), the joins and
 // pushes of two virtual warps 1200, the barrier 1300, the last join 750, the decision 1200.  With rows that end early and
-// draft probabilities 37 us (46 with nothing of it in L2).  Measured against that: chunks asked for only when the
+// draft probabilities 37 us (44 with nothing of it in L2).  Measured against that: chunks asked for only when the
 // ones before are summed 71 and 42; 128 virtual warps 20% slower, 32 in FP32 40%; rows fetched to L2 ahead, no change.
 #include <algorithm>
 #include <atomic>
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
         }
         uint64_t kids = ballot(kid[0], kid[1]);
         const bool leave = !greedy && !probs && kids;  // the sum goes without the children's tokens
-        const bool run = !greedy && (!probs || !kids); // the race is run along
+        const bool run = !greedy && !kids;             // the race is run along
         bool dup[2] = {false, false};                  // has a child before it the same token
         if (leave) {
             for (uint64_t rest = kids; rest; rest &= rest - 1) {
