@@ -37,6 +37,17 @@
 // Loops are rolled: twenty warps in six roles go through their code once a tile, and code of some hundred
 // instructions in a row was fetched anew each time (an MMA issued every 150 cycles, a wait on a barrier that had
 // completed took 300).
+//
+// Roundings: q and K to FP16 after the rotation (2^-11, as in the other BF16 calls; lse moves by 1e-5 to 1e-4), weights to BF16
+// for P V (2^-9 each, and their sum is of the unrounded ones), out once to BF16; scores, maxima, sums, O and parts FP32.
+//
+// What bounds it (one GB300, in a replayed graph, merge included): 64 rows of 4096 and 8 nodes, 32 queries a head, 201 us =
+// 5.4 TB/s, 80% of a copy's; 2 rows past 100000 and 64 queries 163 us, 79%: DRAM, the first load after 8500 cycles
+// (4.5 us; instructions fetched for the first time, 170 cycles to a line of 8) and the merge (84 MB written and read, 12 us).
+// 20 rows of 90 to 9001 and 104 queries 114 us, 8 rows of 2048 and 256 queries 56 us: the chain of a tile, 3700 cycles: S
+// 250, its first half 1000, PV of the tile before 400, the second half 1300, the vote 700; 2500 of them are issued
+// instructions of a quarter of the SM, and shared memory moves 288 KB (2300 cycles).  One row of 777 15 us: latency, 4.5 to the
+// first load, 4 tiles of 1.2, merge.
 #include <algorithm>
 #include <atomic>
 #include <cstring>
