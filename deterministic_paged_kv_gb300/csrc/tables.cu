@@ -242,9 +242,9 @@ __global__ void __launch_bounds__(TAB_THREADS) tokens_kernel(const __grid_consta
 // ---- the inverse: tokens leave the rows' ends, emptied pages go back to the pool ----
 //
 // One prefix sum over the rows, of the pages that come free; then each freed page finds its
-// row by bisection and moves to its place.  Large tables take two launches, many CTAs that each sum
-// the rows for themselves and move a share of the pages, and one that writes the new lengths and
-// taken (which may be the arrays that the others read) when those are done.
+// row by bisection and moves to its place.  Large tables take many CTAs, which each sum the rows for
+// themselves and move a share of the pages; the first writes the new lengths and taken.  Where these are the
+// arrays that the others read, a second launch writes them when those are done.
 // Bound by latency: launch, one round of loads, the scan, the pages' loads and stores.  1024 rows that free
 // 260000 pages: 7.7 us (one CTA 205, a cluster of 8 CTAs 35); 64 rows of up to 500 pages that free 130: 5.6 us,
 // 4.7 by one CTA, which takes tables of up to 4096 entries.
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(TAB_THREADS) trim_kernel(const __grid_constant
         a.pool[base + i] = page;
         *e = -1;
     }
-    if constexpr (WRITE) {
+    if (WRITE && cta == 0) {
         if constexpr (!MOVE) griddep_wait();
         __syncthreads();
         for (int r = tid; r < a.B; r += (int)blockDim.x) a.kv_lens_out[r] = s_len[r];
@@ -350,7 +350,12 @@ cudaError_t launch_trim(const TrimArgs& a, cudaStream_t stream) {
         trim_kernel<true, true><<<1, a.B <= 128 ? 128 : TAB_THREADS, smem, stream>>>(a);
         return cudaGetLastError();
     }
-    trim_kernel<true, false><<<(unsigned)std::min<long long>(152, (pages + TAB_THREADS - 1) / TAB_THREADS), TAB_THREADS, smem, stream>>>(a);
+    const unsigned grid = (unsigned)std::min<long long>(152, (pages + TAB_THREADS - 1) / TAB_THREADS);
+    if (a.kv_lens_out != a.kv_lens && a.taken_out != a.taken) {
+        trim_kernel<true, true><<<grid, TAB_THREADS, smem, stream>>>(a);
+        return cudaGetLastError();
+    }
+    trim_kernel<true, false><<<grid, TAB_THREADS, smem, stream>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};

@@ -57,6 +57,8 @@ struct VfShared {
     VfPart part[2][VF_WARPS];
     int par[64], tok[64];  // the row's tree
     float coin[64];
+    int path[64], took[64];  // the walk's nodes and the tokens behind them; those tokens' logits, the maxima and sums
+    float l[64], top[64], sum[64];
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -444,10 +446,17 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
             bad |= RK_STATUS_RANGE;
             break;
         }
-        const float lnZ = logf(Z), inv = 1.0f / Z;
-        auto logp = [&](float l) { return (l - top) / scale - lnZ; };
-        if (n_acc == 0 && writes && lane == 0) a.path[node0] = 0;
+        const float inv = probs ? 1.0f / Z : 0.0f;
         const int here = n_acc++;
+        auto note = [&](int token, float l) {
+            if (writes && lane == 0) {
+                sh.path[here] = at;
+                sh.took[here] = token;
+                sh.l[here] = l;
+                sh.top[here] = top;
+                sh.sum[here] = Z;
+            }
+        };
         int best = 0;
         if (greedy) {
             best = z.v;  // the first token of the chunk that has the maximum
@@ -521,12 +530,7 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
             if (bad) break;
         }
         if (took >= 0) {
-            const float l = of(lx[0], lx[1], took);
-            if (writes && lane == 0) {
-                a.tokens[node0 + here] = sh.tok[took];
-                a.logprobs[node0 + here] = logp(l);
-                a.path[node0 + here + 1] = took;
-            }
+            note(sh.tok[took], of(lx[0], lx[1], took));
             at = took;
             continue;
         }
@@ -603,19 +607,17 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
             bad |= RK_STATUS_RANGE;
             break;
         }
-        if (writes && lane == 0) {
-            a.tokens[node0 + here] = last;
-            a.logprobs[node0 + here] = logp(logit(last));
-        }
+        note(last, logit(last));
         break;
     }
     if (writes) {
         if (bad && lane == 0 && a.status) atomicOr(a.status, bad);
         const int n = bad || rootless ? 0 : n_acc;
-        for (int i = n + lane; i < T; i += 32) {
-            a.path[node0 + i] = -1;
-            a.tokens[node0 + i] = -1;
-            a.logprobs[node0 + i] = bad ? NAN : 0.0f;
+        __syncwarp();
+        for (int i = lane; i < T; i += 32) {
+            a.path[node0 + i] = i < n ? sh.path[i] : -1;
+            a.tokens[node0 + i] = i < n ? sh.took[i] : -1;
+            a.logprobs[node0 + i] = i < n ? (sh.l[i] - sh.top[i]) / scale - logf(sh.sum[i]) : bad ? NAN : 0.0f;
         }
         if (lane == 0) {
             a.n_accepted[b] = n;

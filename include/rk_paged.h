@@ -739,8 +739,8 @@ int rk_paged_kv_compact(const rk_paged_plan_t *plan, const int32_t *path_d, cons
  * pages of the rows up to it (rows without a place left out) are more than taken while it frees one
  * (RK_STATUS_POOL; also taken outside [0, n_pool], which leaves no place).  A freed entry outside
  * [0, num_pages) goes into the pool like the others, with RK_STATUS_PAGE_OOB.
- * Plan: B, W, num_pages (B at most 16384, else RK_E_UNSUPPORTED).  One launch, or two for tables of more than
- * 4096 entries; no allocation, no host synchronisation.
+ * Plan: B, W, num_pages (B at most 16384, else RK_E_UNSUPPORTED).  One launch, or two in place for tables of
+ * more than 4096 entries; no allocation, no host synchronisation.
  * Errors: RK_E_ARG (null or misaligned pointer, negative n_pool), RK_E_DEVICE, RK_E_CUDA.
  */
 int rk_paged_tables_trim(const rk_paged_plan_t *plan, const int32_t *n_drop_d, const int32_t *kv_lens_d, int32_t *pool_d,
