@@ -379,3 +379,9 @@ def test_two_calls_at_once_and_two_graphs_with_one_scratch():
     torch.cuda.synchronize()
     for i in (0, 1):
         assert _equal(want[i], [x.cpu() for x in outs[i]])
+
+
+@pytest.mark.parametrize("lens,T,Hq,Hkv", [([40, 1200], 3, 160, 160), ([70, 300, 9], 20, 640, 80), ([5], 64, 512, 64)])
+def test_more_heads_than_a_grid_has_blocks(lens, T, Hq, Hkv):
+    c = ref.case(67, lens, T, Hq, Hkv, ["tree", "chain"])
+    _near(_run(c), ref.attention(c))

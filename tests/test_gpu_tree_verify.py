@@ -318,3 +318,37 @@ def test_a_hundred_and_more_rows_and_the_smallest_vocabularies(dtype):
                  "parents": torch.arange(-1, T - 1, dtype=i32).expand(B, T).contiguous(), "coins": torch.rand((B, T), generator=g),
                  "race": torch.rand((B, V), generator=g) + 0.1, "temperature": torch.ones(B)}
         _check(c, _run(c))
+
+
+def test_verify_offsets_past_32_bits():
+    """The last row of a batch whose logits and probabilities pass 2^31 elements: the bits of the row alone."""
+    B, T, V = 36, 64, 1000003
+    assert B * T * V > 2 ** 31
+    c = ref.verify_case(71, 1, T, 2003, BF, True, ["tree"], temps=(1.0,))
+    small = c["logits"].shape[2]
+    lg = torch.zeros((B, T, V), dtype=BF, device="cuda")
+    lg[-1] = -40.0
+    lg[-1, :, -small:] = c["logits"][0].cuda()
+    q = torch.zeros((B, T, V), device="cuda")
+    q[-1, :, -small:] = c["draft_probs"][0].cuda()
+    par = torch.full((B, T), -2, dtype=i32)
+    par[-1] = c["parents"][0]
+    tok = torch.zeros((B, T), dtype=i32)
+    tok[-1] = c["draft_tokens"][0] + (V - small)
+    race = torch.ones((B, V), device="cuda")
+    race[-1, -small:] = c["race"][0].cuda()
+    coins, temp = torch.zeros((B, T)), torch.ones(B)
+    coins[-1] = c["coins"][0]
+
+    def go(rows):
+        n = len(range(B)[rows])
+        p = binding.plan(n, T, 1, 1, 128, 16, 1, 1)
+        o = [torch.full(s, 99, dtype=i32, device="cuda") for s in ((n,), (n,), (n, T), (n, T))] + [torch.full((n, T), 9.0, device="cuda")]
+        binding.verify_tree(p, lg[rows], tok[rows].cuda(), par[rows].cuda(), coins[rows].cuda(), race[rows], temp[rows].cuda(), *o,
+                            draft_probs=q[rows])
+        return [x.cpu() for x in o]
+
+    every, alone = go(slice(0, B)), go(slice(B - 1, B))
+    assert int(alone[0][0]) >= 1 and (every[0][:-1] == 0).all()
+    assert (alone[3][0, :int(alone[0][0])] >= V - small).all()
+    assert all(torch.equal(x[-1:].view(i32), y.view(i32)) for x, y in zip(every, alone))
