@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(TAB_THREADS) tokens_kernel(const __grid_consta
 // themselves and move a share of the pages; the first writes the new lengths and taken.  Where these are the
 // arrays that the others read, a second launch writes them when those are done.
 // Bound by latency: launch, one round of loads, the scan, the pages' loads and stores.  1024 rows that free
-// 260000 pages: 7.7 us (one CTA 205, a cluster of 8 CTAs 35); 64 rows of up to 500 pages that free 130: 5.6 us,
-// 4.7 by one CTA, which takes tables of up to 4096 entries.
+// 260000 pages: 7.3 us (in place 7.7; one CTA 205, a cluster of 8 CTAs 35); 64 rows of up to 500 pages that free 130: 5.2 us
+// (in place 5.6), 4.7 by one CTA, which takes tables of up to 4096 entries.
 //
 // MOVE: the pages; WRITE: the lengths and taken.
 template <bool MOVE, bool WRITE>

@@ -20,7 +20,7 @@
 // Work: a cluster of 1 to 16 CTAs (by the batch) walks a row, reading only the nodes that the walk
 // reaches.  A pass deals the vocabulary in chunks of 8 to the lanes of 64 virtual warps, a lane's chunks in
 // ascending order (in groups of one, two or four, with the lane's running maximum), and joins lanes and warps in a fixed tree, so a
-// row's results depend on its data and V alone: not on the cluster, nor on how a row lies in memory (a row that does
+// row's results depend on its data, type and V alone: not on the cluster, nor on how a row lies in memory (a row that does
 // not start at 16 bytes is read in whole vectors and shifted).  A warp pushes its partial results into every CTA's
 // shared memory; behind one cluster barrier a pass every warp joins them and decides for itself.
 //

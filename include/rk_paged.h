@@ -693,7 +693,7 @@ int rk_paged_attn_tree(const rk_paged_plan_t *plan, const void *q, const void *k
  * a race without a number in it): the row keeps
  * nothing: n_accepted 0, n_drop T, tokens and path -1, logprobs NaN.
  * A row whose node 0 is unused gives n_accepted 0, n_drop 0 without a status.
- * Sums are FP32 in an order that V alone fixes: a row's results do not depend on the batch.
+ * Sums are FP32 in an order that V and the type fix: a row's results do not depend on the batch.
  * Plan: B, Sq.  One launch, no allocation, no host synchronisation.  Errors: RK_E_ARG (V < 1,
  * logits_type, null or misaligned pointer: 2 or 4 bytes), RK_E_UNSUPPORTED (T), RK_E_DEVICE, RK_E_CUDA.
  */
