@@ -25,26 +25,28 @@
 // cycles a tile in the one warp that had rows, where the tile's bytes take 3034).  P^T goes to shared memory
 // as the N operand of O^T = V^T P^T, whose lanes are the output dims.
 //
-// Roles (640 threads):
-//   warps 0-7    transform: rotate new queries and each K tile in place in shared memory (FP32, angles
+// Roles (512 threads):
+//   warps 0-3    transform: rotate new queries and each K tile in place in shared memory (FP32, angles
 //                from exact anchors and steps), FP16 for the score MMA;
-//   warps 8-15   softmax: online, in the log2 domain; the running maximum moves when some query's grows by
+//   warps 4-11   softmax: online, in the log2 domain; the running maximum moves when some query's grows by
 //                more than 8 (a vote of the 256 threads says so; then the maxima are exchanged and O^T is
 //                rescaled); P as BF16; epilogue, a thread one dim of RR / 2 queries;
-//   warps 16, 18 TMA producers of K and V pages; warp 18 cleans the tree's V tile;
-//   warp 17      MMA issuer: S of the next tile before PV of this one (S, and O^T by item, have two buffers);
-//   warp 19      scheduler: walks the items, checks their metadata, publishes them.
-// Loops are rolled: twenty warps in six roles go through their code once a tile, and code of some hundred
+//   warps 12, 14 TMA producers of K and V pages; warp 14 cleans the tree's V tile;
+//   warp 13      MMA issuer: S of the next tile before PV of this one (S, and O^T by item, have two buffers);
+//   warp 15      scheduler: walks the items, checks their metadata, publishes them.
+// Four warps transform: with 8 (640 threads, 96 registers) 64 rows of 4096 took 202 us where they take 199, with 16 270; 4
+// softmax warps instead of 8 took 197 there, and 128 instead of 113 for 104 queries a head.
+// Loops are rolled: sixteen warps in six roles go through their code once a tile, and code of some hundred
 // instructions in a row was fetched anew each time (an MMA issued every 150 cycles, a wait on a barrier that had
 // completed took 300).
 //
 // Roundings: q and K to FP16 after the rotation (2^-11, as in the other BF16 calls; lse moves by 1e-5 to 1e-4), weights to BF16
 // for P V (2^-9 each, and their sum is of the unrounded ones), out once to BF16; scores, maxima, sums, O and parts FP32.
 //
-// What bounds it (one GB300, in a replayed graph, merge included): 64 rows of 4096 and 8 nodes, 32 queries a head, 201 us =
-// 5.4 TB/s, 80% of a copy's; 2 rows past 100000 and 64 queries 163 us, 79%: DRAM, the first load after 8500 cycles
+// What bounds it (one GB300, in a replayed graph, merge included): 64 rows of 4096 and 8 nodes, 32 queries a head, 199 us =
+// 5.45 TB/s, 80% of a copy's; 2 rows past 100000 and 64 queries 160 us, 80%: DRAM, the first load after 8500 cycles
 // (4.5 us; instructions fetched for the first time, 170 cycles to a line of 8) and the merge (84 MB written and read, 12 us).
-// 20 rows of 90 to 9001 and 104 queries 114 us, 8 rows of 2048 and 256 queries 56 us: the chain of a tile, 3700 cycles: S
+// 20 rows of 90 to 9001 and 104 queries 113 us, 8 rows of 2048 and 256 queries 55.5 us: the chain of a tile, 3700 cycles: S
 // 250, its first half 1000, PV of the tile before 400, the second half 1300, the vote 700; 2500 of them are issued
 // instructions of a quarter of the SM, and shared memory moves 288 KB (2300 cycles).  One row of 777 15 us: latency, 4.5 to the
 // first load, 4 tiles of 1.2, merge.
@@ -59,7 +61,7 @@ namespace rk {
 
 namespace {
 
-constexpr int TR_XW = 8, TR_SW = 8;                       // transform and softmax warps
+constexpr int TR_XW = 4, TR_SW = 8;                       // transform and softmax warps
 constexpr int TR_SOFTMAX = TR_SW * 32;
 constexpr int WARP_S0 = TR_XW, WARP_K = WARP_S0 + TR_SW, WARP_MMA = WARP_K + 1, WARP_V = WARP_K + 2, WARP_SCHED = WARP_K + 3;
 constexpr int TR_THREADS = (WARP_SCHED + 1) * 32;
@@ -71,7 +73,7 @@ constexpr int TR_TREE_ROWS = 80;                          // keys of the tree's 
 constexpr float TR_SLACK = 8.0f;                          // the running max moves when it grows by more (log2)
 constexpr int TR_SLOTS = 3;                               // items published ahead
 constexpr int TR_ROW_STEP = TR_XW * 4;                    // rows between a transform thread's rows
-constexpr int TR_ANCHOR = 8;                              // tiles between exact angles
+constexpr int TR_ANCHOR = 4;                              // tiles between exact angles
 constexpr int TR_GROUPS = 32;                             // row groups of the item search
 
 template <int RR>
@@ -227,7 +229,7 @@ struct TrCtrl {
     int total;                        // tiles of the batch's rows (of one KV head and block)
     int pre[TR_GROUPS];               // tiles before each group of rows
     uint64_t vbad[2];                 // nodes whose V is not finite, by item parity
-    uint8_t xbad[2][TR_XW];           // a transform warp met a prefix key out of range
+    alignas(4) uint8_t xbad[2][TR_XW];  // a transform warp met a prefix key out of range
     uint8_t kbad[2][TR_TREE_ROWS];    // keys of the tree's tile out of range
     uint8_t qbad[2][TR_SPAN / 4];     // queries out of range, four to a byte, by the queries' parity
     alignas(16) TrSlot slot[TR_SLOTS];
@@ -797,10 +799,10 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 if (!(ok = wait_all(c->k_full[kst], g / TR_KSTAGES))) break;
                 uint8_t* kt = sm + Sh::OFF_K + kst * TR_TILE_BYTES;
                 const int keys = min(TR_BN, n_keys - i * TR_BN);
-                // row r0 + 32 m is chunk u8 ^ (r0 & 7) of its 128 bytes for every m
+                // row r0 + 16 m is chunk u8 ^ (r0 & 7) of its 128 bytes for every m
                 uint8_t* row = kt + sw128_off(r0, u8);
                 uint4 lo = *reinterpret_cast<const uint4*>(row), hi = *reinterpret_cast<const uint4*>(row + 16384);
-#pragma unroll
+#pragma unroll 2
                 for (int m = 0; m < ROWS; ++m, row += TR_ROW_STEP * 128) {
                     uint4 x = lo, y = hi;
                     if (m + 1 < ROWS) {  // the next row is read while this one is rotated
@@ -1028,7 +1030,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                 float sum = l, inv = 0.0f;
 #pragma unroll
                 for (int x = 1; x < PARTS; ++x) sum += ex_sum[(x - 1) * RR + r];
-                bool fail = *reinterpret_cast<const uint64_t*>(c->xbad[k & 1]) != 0;
+                bool fail = *reinterpret_cast<const uint32_t*>(c->xbad[k & 1]) != 0;
                 if (tree) {
                     const int off = prefix & (PAGE - 1);
                     const uint32_t b0 = __ballot_sync(0xffffffffu, lane < T && c->kbad[k & 1][off + min(lane, TREE_MAX - 1)]);
