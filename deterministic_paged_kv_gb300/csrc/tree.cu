@@ -75,6 +75,11 @@ constexpr int TR_SLOTS = 3;                               // items published ahe
 constexpr int TR_ROW_STEP = TR_XW * 4;                    // rows between a transform thread's rows
 constexpr int TR_ANCHOR = 4;                              // tiles between exact angles
 constexpr int TR_GROUPS = 32;                             // row groups of the item search
+// Sets of queries whose flags are kept.  The transform writes a set's in the set's first item e, after r_empty of item
+// e - 1, which says that the results of items up to e - 3 are written.  Items e - 2 and e - 1, whose flags may still be
+// read (with one tile each their scores, and so q_empty, run two items ahead of their results), hold at most the two
+// sets before it.
+constexpr int TR_QSETS = 3;
 
 template <int RR>
 struct TrShape {
@@ -231,7 +236,7 @@ struct TrCtrl {
     uint64_t vbad[2];                 // nodes whose V is not finite, by item parity
     alignas(4) uint8_t xbad[2][TR_XW];  // a transform warp met a prefix key out of range
     uint8_t kbad[2][TR_TREE_ROWS];    // keys of the tree's tile out of range
-    uint8_t qbad[2][TR_SPAN / 4];     // queries out of range, four to a byte, by the queries' parity
+    uint8_t qbad[TR_QSETS][TR_SPAN / 4];  // queries out of range, four to a byte, by the set of queries
     alignas(16) TrSlot slot[TR_SLOTS];
     // exchange of the softmax threads: maxima, or scales of O^T, or an item's factors (its sums, of all parts
     // but the first, lie behind this block)
@@ -785,7 +790,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     }
                     const uint32_t bad = __ballot_sync(0xffffffffu, too_large(rs, ru));
                     if (lane == 0)
-                        c->qbad[nq & 1][r >> 2] = (uint8_t)(((bad & 0xffu) != 0) | ((bad & 0xff00u) != 0) << 1 | ((bad & 0xff0000u) != 0) << 2 | (bad >> 24 != 0) << 3);
+                        c->qbad[nq % TR_QSETS][r >> 2] = (uint8_t)(((bad & 0xffu) != 0) | ((bad & 0xff00u) != 0) << 1 | ((bad & 0xff0000u) != 0) << 2 | (bad >> 24 != 0) << 3);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1037,7 +1042,7 @@ __global__ void __launch_bounds__(TR_THREADS, 1)
                     const uint32_t b1 = __ballot_sync(0xffffffffu, lane + 32 < T && c->kbad[k & 1][off + min(lane + 32, TREE_MAX - 1)]);
                     fail |= (sees & (((uint64_t)b1 << 32) | b0 | c->vbad[k & 1])) != 0;
                 }
-                fail |= (c->qbad[u->nq & 1][r >> 2] >> (r & 3)) & 1;
+                fail |= (c->qbad[u->nq % TR_QSETS][r >> 2] >> (r & 3)) & 1;
                 const bool empty = sees == 0;
                 if (!empty && !fail && sum > 0.0f) inv = 1.0f / sum;
                 c->ex[r] = inv;  // (the maxima have been read)
