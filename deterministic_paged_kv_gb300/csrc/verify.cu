@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                 }
             });
         const float top = z.m;
-        auto weight = [&](float l) { return ex2((l - top) * chi); };
+        auto weight = [&](float l) { return ex2(__fmul_rn(__fsub_rn(l, top), chi)); };
         // ---- what is left when each child is tried, if the ones before it were rejected (drafts without probabilities) ----
         float lx[2], w[2], left[2] = {1.0f, 1.0f};
 #pragma unroll
@@ -457,25 +457,31 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                 sh.sum[here] = Z;
             }
         };
+        // A sweep says in which chunk its token lies; the token is the first of those that have the chunk's value again, from
+        // the same operations (none of them: no token, which fails the row).
+        auto token_of = [&](int first, bool has) {
+            const uint32_t hit = __ballot_sync(0xffffffffu, lane < 8 && first + lane < V && has);
+            return hit ? first + __ffs(hit) - 1 : INT32_MAX;
+        };
         int best = 0;
-        if (greedy) {
-            best = z.v;  // the first token of the chunk that has the maximum
-            const bool hit = lane < 8 && best + lane < V && logit(best + lane) == top;
-            best += __ffs(__ballot_sync(0xffffffffu, hit)) - 1;
+        if (greedy) best = token_of(z.v, logit(z.v + (lane & 7)) == top);
+        if (best >= V) {
+            bad |= RK_STATUS_RANGE;
+            break;
         }
         auto race_at = [&](int v) { return __ldg(reinterpret_cast<const float*>(race) + min(v, V - 1)); };
-        auto first_lane = [](bool x) { return __ffs(__ballot_sync(0xffffffffu, x)) - 1; };
         // ---- the children in order ----
         int took = -1;
         float aq = 0.0f, S = 1.0f;
-        // the key of a token of what is left, or by p's own weights; -inf where it has no part in it
+        // the key of a token of what is left, or by p's own weights; -inf where it has no part in it.  (Rounded as written: the
+        // token is found by its key, so no compiler may join a product and a difference at one place and not at the other.)
         auto own_key = [&](float l, float r) {
-            const float t = (l - top) * chi;
-            return ex2(t) > 0.0f ? t - lg2(r) : -INFINITY;
+            const float t = __fmul_rn(__fsub_rn(l, top), chi);
+            return ex2(t) > 0.0f ? __fsub_rn(t, lg2(r)) : -INFINITY;
         };
         auto left_key = [&](float l, float d, float r) {
-            const float k = fmaf(weight(l), inv, -aq * d);
-            return k > 0.0f ? lg2(k) - lg2(r) : -INFINITY;
+            const float k = fmaf(weight(l), inv, __fmul_rn(-aq, d));
+            return k > 0.0f ? __fsub_rn(lg2(k), lg2(r)) : -INFINITY;
         };
         if (!probs || greedy) {
             bool yes[2];
@@ -599,8 +605,9 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                 const int v = min(y.kv + (lane & 7), V - 1);
                 const float d = own ? 0.0f : __ldg(reinterpret_cast<const float*>(q) + v);
                 const uint32_t hit = !all && leave ? taken((unsigned)y.kv / 8) : 0u;
-                last = y.kv + first_lane(lane < 8 && y.kv + lane < V && !((hit >> lane) & 1u) &&
-                                           (own ? own_key(logit(v), race_at(v)) : left_key(logit(v), d, race_at(v))) == y.key);
+                last = token_of(y.kv, !((hit >> (lane & 7)) & 1u) &&
+                                          (own ? own_key(logit(v), race_at(v)) : left_key(logit(v), d, race_at(v))) == y.key);
+                if (last >= V) break;
             }
         }
         if (bad || last >= V) {  // (no draw of the race is a number that is not negative)

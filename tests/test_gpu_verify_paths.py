@@ -1,0 +1,71 @@
+"""GPU tests of rk_paged_verify_tree: the last token by each of its ways (the race run along with the sum, a sweep of
+its own, the largest logit), which all have to find the token itself and not only its place."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import tree_ref as ref
+from deterministic_paged_kv_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+i32 = torch.int32
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from deterministic_paged_kv_gb300 import build
+    build.build()
+    binding.load()
+
+
+def _run(c):
+    B, T, V = c["logits"].shape
+    d = {k: None if v is None else v.cuda() for k, v in c.items()}
+    p = binding.plan(B, T, 1, 1, 128, 16, 1, 1)
+    z = lambda *s: torch.full(s, 99, dtype=i32, device="cuda")  # noqa: E731
+    o = [z(B), z(B), z(B, T), z(B, T), torch.full((B, T), 99.0, device="cuda")]
+    st = torch.zeros(1, dtype=i32, device="cuda")
+    binding.verify_tree(p, d["logits"], d["draft_tokens"], d["parents"], d["coins"], d["race"], d["temperature"], *o,
+                        draft_probs=d["draft_probs"], status=st)
+    assert int(st.item()) == 0
+    return [x.cpu() for x in o]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [1, 5, 8, 9, 1000, 4099, 40000])
+def test_the_last_token_of_every_way(V, dtype):
+    """A child of probability 0 is refused and leaves p as it is, so the race without children, the one behind a
+    refused child and, with draft probabilities that are 0 but there, the one over the residual draw the same token: the one
+    that 64 bits say.  Temperatures whose factor is no power of two."""
+    B, T = 96, 2
+    g = torch.Generator().manual_seed(V)
+    x = (torch.randn((B, T, V + 1), generator=g) * 3).to(dtype)
+    x[:, :, V] = -math.inf  # the child's token
+    temp = torch.rand(B, generator=g) + 0.3
+    temp[::8] = 0.0
+    race = (-torch.log1p(-torch.rand((B, V + 1), generator=g))).clamp(min=2.0 ** -40)
+    c = {"logits": x, "draft_probs": None, "draft_tokens": torch.full((B, T), V, dtype=i32), "coins": torch.rand((B, T), generator=g),
+         "race": race, "temperature": temp, "parents": torch.tensor([[-1, ref.UNUSED]] * B, dtype=i32)}
+    key = x[:, 0].double() / torch.where(temp > 0, temp, torch.ones(())).double()[:, None]
+    key = torch.where((temp > 0)[:, None], key - race.double().log(), key)
+    best = key.max(-1)
+    two = key.topk(2, -1).values
+    # keys are FP32: a token within 2^-16 of the largest may be the one that is chosen (greedy: equal ones, the lowest)
+    sure = ((two[:, 0] - two[:, 1] > 2.0 ** -16) | (temp == 0)).numpy()
+    first = np.array([int((key[b] == best.values[b]).nonzero()[0]) for b in range(B)])
+    assert sure.mean() > 0.9
+    runs = [_run(c)]
+    c["parents"] = torch.tensor([[-1, 0]] * B, dtype=i32)
+    runs.append(_run(c))
+    q = torch.zeros((B, T, V + 1))
+    q[:, :, V] = 1.0
+    c["draft_probs"] = q
+    runs.append(_run(c))
+    for n, drop, path, tok, logp in runs:
+        assert (n == 1).all() and (path[:, 0] == 0).all()
+        assert np.array_equal(tok[:, 0].numpy()[sure], first[sure])
+        assert ((tok[:, 0] >= 0) & (tok[:, 0] < V)).all() and torch.isfinite(logp[:, 0]).all()
