@@ -93,7 +93,9 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 // Eight values of a row from element 8 j on, those past the end as `fill`: asked for, and then taken apart.  (A row
-// that does not start at 16 bytes is put together as it arrives; other rows' chunks can be on their way several at a time.)
+// that does not start at 16 bytes is put together as it arrives, from whole vectors where these lie within the row and
+// value by value at its ends, so that nothing outside the caller's array is read; other rows' chunks can be on their way
+// several at a time.)
 template <bool F32>
 struct Chunk {
     static constexpr int SIZE = F32 ? 4 : 2, VECS = F32 ? 2 : 1;
@@ -102,7 +104,7 @@ struct Chunk {
         const size_t v0 = (size_t)j * 8;
         const char* at = row + v0 * SIZE;
         const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u;  // the same for every chunk
-        if (v0 + 8 > (size_t)V) {
+        if (j + (off != 0) >= (unsigned)V / 8 || (off != 0 && j == 0)) {  // (a shifted chunk's vectors reach into both neighbours)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const bool in = v0 + e < (size_t)V;
@@ -117,7 +119,6 @@ struct Chunk {
 #pragma unroll
             for (int e = 0; e < VECS; ++e) reinterpret_cast<uint4*>(w)[e] = __ldg(reinterpret_cast<const uint4*>(at) + e);
         } else {
-            // (the vector behind the last whole one holds some of the chunk too, so it may be read)
             uint32_t x[VECS * 4 + 4];
 #pragma unroll
             for (int e = 0; e <= VECS; ++e) reinterpret_cast<uint4*>(x)[e] = __ldg(reinterpret_cast<const uint4*>(at - off) + e);

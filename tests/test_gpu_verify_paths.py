@@ -69,3 +69,55 @@ def test_the_last_token_of_every_way(V, dtype):
         assert (n == 1).all() and (path[:, 0] == 0).all()
         assert np.array_equal(tok[:, 0].numpy()[sure], first[sure])
         assert ((tok[:, 0] >= 0) & (tok[:, 0] < V)).all() and torch.isfinite(logp[:, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [1, 7, 8, 9, 15, 16, 17, 23, 24, 25, 40, 1003])
+def test_arrays_that_begin_and_end_anywhere_among_others(V, dtype):
+    """Logits, probabilities and draws cut out of larger arrays of NaN, at every element of 16 bytes: the bits of
+    arrays of their own."""
+    B, T = 5, 3
+    c = ref.verify_case(400 + V, B, T, V, dtype, True, ["tree", "chain"]) if V >= 3 else {
+        "logits": torch.zeros((B, T, V), dtype=dtype), "draft_probs": torch.ones((B, T, V)), "draft_tokens": torch.zeros((B, T), dtype=i32),
+        "parents": torch.tensor([[-1, 0, 1]] * B, dtype=i32), "coins": torch.rand((B, T), generator=torch.Generator().manual_seed(1)),
+        "race": torch.ones((B, V)), "temperature": torch.ones(B)}
+    for probs in (True, False):
+        if not probs:
+            c = dict(c, draft_probs=None)
+        want = _run(c)
+        for off in range(1, 8):
+            d = dict(c)
+            for k in ("logits", "draft_probs", "race"):
+                if d[k] is None:
+                    continue
+                n = d[k].numel()
+                flat = torch.full((n + 16,), math.nan, dtype=d[k].dtype, device="cuda")
+                flat[off:off + n] = d[k].cuda().view(-1)
+                d[k] = flat[off:off + n].view(d[k].shape)
+            assert all(torch.equal(x.view(i32), y.view(i32)) for x, y in zip(want, _run(d)))
+
+
+def test_a_captured_call_replayed_with_new_inputs():
+    """One captured call; every input changes in place between its replays and the outputs are spoilt before each."""
+    B, T, V = 12, 6, 3001
+    cases = [ref.verify_case(500 + i, B, T, V, BF, True, shapes, temps=temps)
+             for i, (shapes, temps) in enumerate(((["tree"], (1.0, 0.7)), (["chain", "star"], (0.0, 1.3)), (["forest", "none"], (1.0, 0.0))))]
+    for c in cases:  # (a walk begins at node 0: a forest's first node may be unused)
+        c["draft_tokens"] = c["draft_tokens"].clamp(0, V - 1)
+    want = [_run(c) for c in cases]
+    d = {k: v.cuda() for k, v in cases[0].items()}
+    p = binding.plan(B, T, 1, 1, 128, 16, 1, 1)
+    o = [torch.zeros(x.shape, dtype=x.dtype, device="cuda") for x in want[0]]
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        binding.verify_tree(p, d["logits"], d["draft_tokens"], d["parents"], d["coins"], d["race"], d["temperature"], *o,
+                            draft_probs=d["draft_probs"])
+    for i in (0, 1, 2, 1, 0):
+        for k in d:
+            d[k].copy_(cases[i][k])
+        for x in o:
+            x.fill_(-99)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x.view(i32), y.cpu().view(i32)) for x, y in zip(want[i], o))
