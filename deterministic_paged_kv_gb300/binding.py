@@ -18,7 +18,7 @@ Names mirror the C ABI in ``include/rk_paged.h``:
 ``tables_extend`` (rk_paged_tables_extend), ``kv_append_q8`` (rk_paged_kv_append_q8),
 ``decode_q8_scratch_bytes`` (rk_paged_decode_q8_scratch_bytes), ``attn_decode_q8``
 (rk_paged_attn_decode_q8), ``attn_prefill_q8`` (rk_paged_attn_prefill_q8),
-``tree_scratch_bytes`` (rk_paged_tree_scratch_bytes), ``attn_tree`` (rk_paged_attn_tree),
+``tree_rows`` (rk_paged_tree_rows), ``tree_scratch_bytes`` (rk_paged_tree_scratch_bytes), ``attn_tree`` (rk_paged_attn_tree),
 ``verify_tree`` (rk_paged_verify_tree), ``kv_compact`` (rk_paged_kv_compact),
 ``tables_trim`` (rk_paged_tables_trim),
 ``last_error``, ``policy``, ``abi_version``.
@@ -129,6 +129,8 @@ def load(path: str | None = None):
             [ctypes.c_uint64, vp, vp]
         lib.rk_paged_attn_prefill_q8.restype = ctypes.c_int
         lib.rk_paged_attn_prefill_q8.argtypes = [ctypes.POINTER(Plan)] + [vp] * 12
+        lib.rk_paged_tree_rows.restype = ctypes.c_int
+        lib.rk_paged_tree_rows.argtypes = [ctypes.POINTER(Plan)] + [vp] * 7
         lib.rk_paged_tree_scratch_bytes.restype = ctypes.c_int
         lib.rk_paged_tree_scratch_bytes.argtypes = [ctypes.POINTER(Plan), ctypes.POINTER(ctypes.c_uint64)]
         lib.rk_paged_attn_tree.restype = ctypes.c_int
@@ -573,6 +575,16 @@ def attn_prefill_q8(p: Plan, q, k_cache, v_cache, k_scale, v_scale, block_table,
     """rk_paged_attn_prefill_q8 on device tensors: causal chunked prefill over the 8-bit cache."""
     ptr = _attn_q8(p, q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, position_ids, out, lse, status)
     _check(load().rk_paged_attn_prefill_q8(ctypes.byref(p), *ptr, _raw_stream(stream)))
+
+
+def tree_rows(p: Plan, qo_indptr, kv_lens, parents, tree_lens, tree_parents, status=None, stream=None):
+    """rk_paged_tree_rows: the lengths ``tree_lens`` [B] and parents ``tree_parents`` [B, Sq] that a speculative
+    step's calls take between ``tables_extend`` (``qo_indptr`` [B + 1], ``kv_lens`` [B] after it) and ``tables_trim``:
+    a row that did not get its Sq tokens has length 0 and no nodes.  ``tree_parents`` may be ``parents``.  All int32."""
+    i32, B, T = _types().i32, p.B, p.Sq
+    ptr = _with_status([(qo_indptr, i32, (B + 1,), "qo_indptr"), (kv_lens, i32, (B,), "kv_lens"), (parents, i32, (B, T), "parents"),
+                        (tree_lens, i32, (B,), "tree_lens"), (tree_parents, i32, (B, T), "tree_parents")], status)
+    _check(load().rk_paged_tree_rows(ctypes.byref(p), *ptr, _raw_stream(stream)))
 
 
 def tree_scratch_bytes(p: Plan) -> int:

@@ -38,6 +38,7 @@ cudaError_t launch_prefill_q8(const AttnQ8Args& a, cudaStream_t stream);
 cudaError_t launch_tree(const CUtensorMap& km, const CUtensorMap& vm, const TreeArgs& a, cudaStream_t stream);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_compact(const CompactArgs& a, cudaStream_t stream);
+cudaError_t launch_tree_rows(const TreeRowsArgs& a, cudaStream_t stream);
 cudaError_t launch_trim(const TrimArgs& a, cudaStream_t stream);
 }  // namespace rk
 
@@ -1208,6 +1209,35 @@ int tree_parts(const rk_paged_plan_t* plan, rk::TreeArgs* a, uint64_t* bytes) {
 }  // namespace
 
 extern "C" {
+
+int rk_paged_tree_rows(const rk_paged_plan_t* plan, const int32_t* qo_indptr_d, const int32_t* kv_lens_d,
+                       const int32_t* parents_d, int32_t* tree_lens_d, int32_t* tree_parents_d, int32_t* status_d,
+                       rk_stream_t stream) {
+    g_err.clear();
+    int rc = check_tree_plan(plan);
+    if (rc) return rc;
+    if (plan->B == 0) return RK_OK;
+    const void* all[] = {qo_indptr_d, kv_lens_d, parents_d, tree_lens_d, tree_parents_d, status_d};
+    for (int i = 0; i < 5; ++i)
+        if (!all[i]) return fail(RK_E_ARG, "null device pointer");
+    for (const void* p : all)
+        if (!aligned(p, 4)) return fail(RK_E_ARG, "every array must be 4-byte aligned");
+    if (tree_lens_d == kv_lens_d) return fail(RK_E_ARG, "tree_lens must not be kv_lens, which the trim needs as they are");
+    if ((rc = check_device())) return rc;
+    rk::TreeRowsArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.qo_indptr = qo_indptr_d;
+    a.kv_lens = kv_lens_d;
+    a.parents = parents_d;
+    a.tree_lens = tree_lens_d;
+    a.tree_parents = tree_parents_d;
+    a.status = status_d;
+    a.B = plan->B;
+    a.T = plan->Sq;
+    cudaError_t e = rk::launch_tree_rows(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(RK_E_CUDA, "tree rows launch: %s", cudaGetErrorString(e));
+    return RK_OK;
+}
 
 int rk_paged_tree_scratch_bytes(const rk_paged_plan_t* plan, uint64_t* bytes) {
     g_err.clear();

@@ -239,6 +239,20 @@ __global__ void __launch_bounds__(TAB_THREADS) tokens_kernel(const __grid_consta
     if (bad && a.status) atomicOr(a.status, bad);
 }
 
+// ---- a speculative step's rows: one that got no tokens has no tree ----
+//
+// A node to a thread.  Bound by latency: launch, one load behind the other, a store.
+__global__ void __launch_bounds__(256) tree_rows_kernel(const __grid_constant__ TreeRowsArgs a) {
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (long long)a.B * a.T) return;
+    const int b = (int)(i / a.T), n = a.qo_indptr[b + 1] - a.qo_indptr[b];
+    const int parent = a.parents[i];
+    a.tree_parents[i] = n == a.T ? parent : TREE_UNUSED;
+    if (i != (long long)b * a.T) return;
+    a.tree_lens[b] = n == a.T ? a.kv_lens[b] : 0;
+    if (n != a.T && n != 0 && a.status) atomicOr(a.status, RK_STATUS_TREE);
+}
+
 // ---- the inverse: tokens leave the rows' ends, emptied pages go back to the pool ----
 //
 // One prefix sum over the rows, of the pages that come free; then each freed page finds its
@@ -330,6 +344,14 @@ __global__ void __launch_bounds__(TAB_THREADS) trim_kernel(const __grid_constant
 }
 
 }  // namespace
+
+cudaError_t launch_tree_rows(const TreeRowsArgs& a, cudaStream_t stream) {
+    const long long blocks = ((long long)a.B * a.T + 255) / 256;
+    if (blocks <= 0) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    tree_rows_kernel<<<(unsigned)blocks, 256, 0, stream>>>(a);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_trim(const TrimArgs& a, cudaStream_t stream) {
     const int smem = 3 * a.B * 4;

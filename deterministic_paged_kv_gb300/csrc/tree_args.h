@@ -66,6 +66,17 @@ struct CompactArgs {
     int32_t B, T, Hkv, W, num_pages;
 };
 
+// Which rows have a tree: those that got its T tokens.
+struct TreeRowsArgs {
+    const int32_t* qo_indptr;     // [B + 1]
+    const int32_t* kv_lens;       // [B], nodes included
+    const int32_t* parents;       // [B, T]
+    int32_t* tree_lens;           // [B]
+    int32_t* tree_parents;        // [B, T] (may be parents)
+    int32_t* status;
+    int32_t B, T;
+};
+
 // Dropped tokens' lengths and pages.
 struct TrimArgs {
     const int32_t* n_drop;        // [B]

@@ -609,7 +609,8 @@ int rk_paged_attn_prefill_q8(const rk_paged_plan_t *plan, const void *q, const v
  * cache, judged by the model in one pass, of which one path is kept.  In the order
  * of a step:
  *
- *   rk_paged_tables_extend   pages for the T nodes of every row (n_new = T)
+ *   rk_paged_tables_extend   pages for the T nodes of every row (n_new = T; 0: an idle row)
+ *   rk_paged_tree_rows       lengths and parents for this step: a row that got no tokens has no tree
  *   rk_paged_kv_append       a layer's K and V of the nodes, in their order
  *   rk_paged_attn_tree       that layer's attention
  *   rk_paged_verify_tree     which nodes are accepted, and the token behind them
@@ -628,9 +629,32 @@ int rk_paged_attn_prefill_q8(const rk_paged_plan_t *plan, const void *q, const v
  *   Row b's node n lies in slot prefix + n with prefix = kv_lens_d[b] - T, and stands at
  *   position prefix + depth(n); a root's depth is 0.  A row of kv_len 0 has no nodes.
  * A row whose parents are not as above fails with RK_STATUS_TREE.
+ *
+ * A row can be idle, or rk_paged_tables_extend can refuse it (no page left, the end of its table): then its
+ * last T tokens are no nodes but tokens that it keeps, and a step that took them for nodes would write over
+ * them and drop them.  So every call between the extension and the trim gets the lengths and parents of
+ * rk_paged_tree_rows, in which such a row has length 0 and no nodes: append and compaction leave it alone,
+ * the attention gives 0 and -inf, the verification n_accepted = n_drop = 0.  The trim gets the rows' own
+ * lengths.  (rk_paged_kv_append reports RK_STATUS_KVLEN for a row of length 0: give it no status word, or one of its
+ * own; rk_paged_attn_tree reports what is wrong with the lengths and pages of rows that have a tree.)
  */
 #define RK_PAGED_TREE_MAX_NODES 64
 #define RK_PAGED_TREE_UNUSED (-2)
+
+/*
+ * rk_paged_tree_rows -- which rows of a step have a tree.
+ *   qo_indptr_d   int32 [B + 1], of rk_paged_tables_extend: row b got qo_indptr[b + 1] - qo_indptr[b] tokens
+ *   kv_lens_d     int32 [B], after it
+ *   tree_lens_d   int32 [B]: kv_len of a row that got T tokens, else 0 (not the array kv_lens_d)
+ *   tree_parents_d  int32 [B, T]: the parents of such a row, else RK_PAGED_TREE_UNUSED (may be parents_d)
+ * The other arrays must not overlap each other.  A row that got a number of tokens that is neither T nor 0
+ * has no tree either, with RK_STATUS_TREE; what to do with its tokens is the caller's.
+ * Plan: B, Sq.  One launch, no allocation, no host synchronisation.  Errors: RK_E_ARG (null or misaligned
+ * pointer, tree_lens_d that is kv_lens_d), RK_E_UNSUPPORTED (T), RK_E_DEVICE, RK_E_CUDA.
+ */
+int rk_paged_tree_rows(const rk_paged_plan_t *plan, const int32_t *qo_indptr_d, const int32_t *kv_lens_d,
+                       const int32_t *parents_d, int32_t *tree_lens_d, int32_t *tree_parents_d, int32_t *status_d,
+                       rk_stream_t stream);
 
 /*
  * rk_paged_attn_tree -- attention of the nodes: node n sees the prefix (keys 0 ..
