@@ -202,7 +202,8 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
         const uint64_t y = __ballot_sync(0xffffffffu, hi);
         return y << 32 | __ballot_sync(0xffffffffu, lo);
     };
-    int bad = !(greedy || (temp >= 5.421010862427522e-20f && temp < INFINITY)) ? RK_STATUS_RANGE : 0;
+    // (a row without a root has no use for a temperature)
+    int bad = !(greedy || (temp >= 5.421010862427522e-20f && temp < INFINITY) || sh.par[0] == TREE_UNUSED) ? RK_STATUS_RANGE : 0;
     {
         bool wrong[2];
 #pragma unroll

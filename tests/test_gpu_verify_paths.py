@@ -121,3 +121,14 @@ def test_a_captured_call_replayed_with_new_inputs():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x.view(i32), y.cpu().view(i32)) for x, y in zip(want[i], o))
+
+
+@pytest.mark.parametrize("temp", [math.nan, -1.0, math.inf, 1e-30])
+def test_a_row_without_a_root_drops_nothing_whatever_its_temperature(temp):
+    """An idle row's temperature may be anything: its tokens are not nodes, and none is dropped."""
+    c = ref.verify_case(600, 4, 5, 100, F32, False, ["chain", "none"])
+    want = _run(c)
+    c["temperature"][1::2] = temp
+    got = _run(c)  # (no status)
+    assert all(torch.equal(x.view(i32), y.view(i32)) for x, y in zip(want, got))
+    assert got[0][1::2].tolist() == [0, 0] and got[1][1::2].tolist() == [0, 0]
