@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(TAB_THREADS) tokens_kernel(const __grid_consta
 
 // ---- a speculative step's rows: one that got no tokens has no tree ----
 //
-// A node to a thread.  Bound by latency: launch, one load behind the other, a store.
+// A node to a thread.  Bound by latency: launch, one load behind the other, a store; 64 rows of 8 nodes 1.6 us in a
+// replayed graph, 1024 rows of 64 1.8.
 __global__ void __launch_bounds__(256) tree_rows_kernel(const __grid_constant__ TreeRowsArgs a) {
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= (long long)a.B * a.T) return;

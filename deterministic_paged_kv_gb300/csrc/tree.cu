@@ -44,12 +44,13 @@
 // for P V (2^-9 each, and their sum is of the unrounded ones), out once to BF16; scores, maxima, sums, O and parts FP32.
 //
 // What bounds it (one GB300, in a replayed graph, merge included): 64 rows of 4096 and 8 nodes, 32 queries a head, 199 us =
-// 5.45 TB/s, 80% of a copy's; 2 rows past 100000 and 64 queries 160 us, 80%: DRAM, the first load after 8500 cycles
-// (4.5 us; instructions fetched for the first time, 170 cycles to a line of 8) and the merge (84 MB written and read, 12 us).
-// 20 rows of 90 to 9001 and 104 queries 113 us, 8 rows of 2048 and 256 queries 55.5 us: the chain of a tile, 3700 cycles: S
-// 250, its first half 1000, PV of the tile before 400, the second half 1300, the vote 700; 2500 of them are issued
-// instructions of a quarter of the SM, and shared memory moves 288 KB (2300 cycles).  One row of 777 15 us: latency, 4.5 to the
-// first load, 4 tiles of 1.2, merge.
+// 5.45 TB/s, 80% of a copy's; 2 rows past 100000 and 64 queries 160 us, 80%: DRAM, the first load after 7000 cycles
+// (3.7 us; instructions fetched for the first time, 170 cycles to a line of 8) and the merge (84 MB written and read, 12 us).
+// 20 rows of 90 to 9001 and 104 queries 113 us, 8 rows of 2048 and 256 queries 55.5 us: the chain of a tile, 3200 cycles: S
+// 300, its first half 880, PV of the tile before 230, the second half 1000 to 1100, the vote 200 to 600 (the last warp's share is the
+// larger one), to the next wait 350; the rotation of its keys takes four warps 2000 to 2400 of them, and shared memory moves
+// 288 KB (2300 cycles).  53% of the issue slots are used.  One row of 777 15 us: latency, 3.3 to the first load, 4 tiles of 1.2,
+// merge.
 #include <algorithm>
 #include <atomic>
 #include <cstring>
@@ -146,7 +147,7 @@ __device__ __forceinline__ int part_start(const A& a, int s) {
 // Tiles of a row: its prefix's and the tree's (one for a row without keys, which is an item too).
 __device__ __forceinline__ int row_tiles(int n) { return n < 0 ? 1 : (n + TR_BN - 1) / TR_BN + 1; }
 
-// The items of a KV head and pair of q-tiles are its rows' parts in order of row and part; they are dealt
+// The items of a KV head and block of 128 queries are its rows' parts in order of row and part; they are dealt
 // to `members` runs of equal numbers of tiles (a part belongs to the run that its first tile lies in), the same
 // for every head, so that the CTAs of a row's heads read its pages, in which a token's heads are
 // neighbours, at about the same time.  Run v of all is run v / heads of head v % heads; CTA c has the runs

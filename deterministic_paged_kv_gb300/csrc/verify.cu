@@ -29,7 +29,8 @@
 // 64 rows of 8 accepted nodes at V = 131072 59 us (63 without probabilities), 7 us a pass, whose 17 MB take 2.5 and whose exponentials take as
 // much.  Of a pass's 12700 cycles the first chunks' way is 1500, a group of four chunks 1100 (four of them), the joins and
 // pushes of two virtual warps 1200, the barrier 1300, the last join 750, the decision 1200.  With rows that end early and
-// draft probabilities 37 us (44 with nothing of it in L2).  Measured against that: chunks asked for only when the
+// draft probabilities 37 us (44 with nothing of it in L2).  FP32 logits with draft probabilities, all nodes accepted: 64 x 8 x 131072
+// 95 us and 20 x 13 x 100003 101, of which their bytes take 40 and 15.  Measured against that: chunks asked for only when the
 // ones before are summed 71 and 42; 128 virtual warps 20% slower, 32 in FP32 40%; rows fetched to L2 ahead, no change.
 #include <algorithm>
 #include <atomic>
@@ -665,8 +666,10 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    // Chunks of a lane, asked for at a time: in BF16 up to two where that is all.  64 x 32000 29 us with 2, 33 with 4; 64 x
-    // 131072 69 and 59; in FP32 20 x 100003 30.1 with 1, 30.8 with 2.
+    // Chunks of a lane, asked for at a time: in BF16 up to two where that is all (two rounds of VF_STEP chunks).  64 rows of 8
+    // accepted nodes by 2 / by 4 in us: V = 16384 29.3 / 31.6, 32768 33.0 / 36.4, 40000 41.3 / 39.2, 65536 44.7 / 42.1, 98304
+    // 57.7 / 57.0, 131072 69.7 / 62.4; one row 32768 20.2 / 21.3, 65536 23.4 / 22.7, 131072 31.2 / 29.6.  In FP32 20 x 100003
+    // 30.1 with 1, 30.8 with 2.
     if (a.f32) return cudaLaunchKernelEx(&cfg, verify_kernel<true, 1>, r);
     return a.V <= 2 * 8 * VF_STEP ? cudaLaunchKernelEx(&cfg, verify_kernel<false, 2>, r) : cudaLaunchKernelEx(&cfg, verify_kernel<false, 4>, r);
 }

@@ -666,7 +666,10 @@ int rk_paged_tree_rows(const rk_paged_plan_t *plan, const int32_t *qo_indptr_d, 
  *   scratch       DEVICE, 16-byte aligned, at least rk_paged_tree_scratch_bytes bytes;
  *                nothing in it needs initialising; may be NULL where that is 0.  Two calls
  *                in flight at once must not share it (two captured graphs that may run at once
- *                included).
+ *                included).  It holds the widest row's parts, as the table's width W allows them:
+ *                516 * B * Hq * T * parts bytes, with W * 16 tokens in parts of 1024 (512 before token 1024
+ *                with up to 64 queries T * Hq / Hkv).  64 rows, 32 heads, 8 nodes: 51 MB at W = 258 and 1.1 GB at
+ *                W = 8192; 64 nodes 8.7 GB there.  A table no wider than the longest row needs less.
  * A row's keys are cut at fixed offsets, the parts are reduced apart and merged in FP32 in
  * ascending order (the policy of rk_paged_attn_decode_split), so a row's result depends on
  * its own length, tree and data, and not on the batch, the table's width or the grid.
