@@ -97,11 +97,21 @@ __device__ __forceinline__ float warp_max(float x) {
 // that does not start at 16 bytes is put together as it arrives, from whole vectors where these lie within the row and
 // value by value at its ends, so that nothing outside the caller's array is read; other rows' chunks can be on their way
 // several at a time.)
-template <bool F32>
+// EVEN: every row starts at 16 bytes and is whole chunks.
+template <bool F32, bool EVEN>
 struct Chunk {
-    static constexpr int SIZE = F32 ? 4 : 2, VECS = F32 ? 2 : 1;
+    static constexpr int VECS = F32 ? 2 : 1;
     uint32_t w[VECS * 4];
-    __device__ __forceinline__ void fetch(const char* row, unsigned j, int V, float fill) {
+    __device__ __forceinline__ void fetch(const char* row, unsigned j, int V, float x) {
+        if constexpr (EVEN) {
+            if (j < (unsigned)V / 8) load(row, j);
+            else fill(x);
+        } else {
+            fetch_any(row, j, V, x);
+        }
+    }
+    __device__ __forceinline__ void fetch_any(const char* row, unsigned j, int V, float fill) {
+        constexpr int SIZE = F32 ? 4 : 2;
         const size_t v0 = (size_t)j * 8;
         const char* at = row + v0 * SIZE;
         const uint32_t off = (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u;  // the same for every chunk
@@ -166,8 +176,9 @@ struct Chunk {
     }
 };
 
-// All of a row's walk (see the head of the file).  GROUP: chunks asked for at a time.
-template <bool F32, int GROUP>
+// All of a row's walk (see the head of the file).  GROUP: chunks asked for at a time; EVEN: every row of the arrays starts
+// at 16 bytes and is whole chunks.
+template <bool F32, int GROUP, bool EVEN>
 __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_constant__ VerifyArgs a) {
     __shared__ VfShared sh;
     const uint32_t rank = cluster_rank();
@@ -273,7 +284,10 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
         auto whole = [&](unsigned j) { return j - lane + 32 <= (unsigned)V / 8; };  // a warp's chunks up to lane 31's
         auto ask = [&](auto& c, const char* from, unsigned j, float fill) {
             constexpr int N = sizeof(c) / sizeof(c[0]);
-            if (at16(from) && whole(j + (N - 1) * VF_STEP)) {
+            if constexpr (EVEN) {
+#pragma unroll
+                for (int u = 0; u < N; ++u) c[u].fetch(from, j + u * VF_STEP, V, fill);
+            } else if (at16(from) && whole(j + (N - 1) * VF_STEP)) {
 #pragma unroll
                 for (int u = 0; u < N; ++u) c[u].load(from, j + u * VF_STEP);
             } else {
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                 }
             }
         };
-        Chunk<F32> next[GROUP];  // the row's first chunks, and then those behind the ones that are summed, on their way
+        Chunk<F32, EVEN> next[GROUP];  // the row's first chunks, and then those behind the ones that are summed, on their way
         if (first_chunk < chunks) ask(next, row, first_chunk + lane, -INFINITY);
         // ---- the children: their logits and draft probabilities (on their way while the row is read) ----
         bool kid[2];
@@ -333,7 +347,7 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                 const bool some = meets(vw);
 #pragma unroll 1
                 for (unsigned j0 = vw * 32 + lane; j0 - lane < chunks; j0 += GROUP * VF_STEP) {
-                    Chunk<F32> c[GROUP];
+                    Chunk<F32, EVEN> c[GROUP];
 #pragma unroll
                     for (int u = 0; u < GROUP; ++u) c[u] = next[u];
                     {
@@ -345,7 +359,7 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
 #pragma unroll
                     for (int u = 0; u < GROUP; ++u) big = fmaxf(big, c[u].max());
                     if (big > x.m) {
-                        const float g = (x.m - big) * chi;
+                        const float g = __fmul_rn(x.m - big, chi);
                         x.s *= ex2(g);
                         x.key = fmaxf(x.key + g, -INFINITY);  // (never NaN)
                         x.m = big;
@@ -360,9 +374,9 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                     for (int u = 0; u < GROUP; ++u) {
                         const unsigned j = j0 + u * VF_STEP;
                         if (j - lane >= chunks) break;
-                        Chunk<true> rc;
+                        Chunk<true, EVEN> rc;
                         if (run) {
-                            if (at16(race) && whole(j)) rc.load(race, j);
+                            if (!EVEN && at16(race) && whole(j)) rc.load(race, j);
                             else rc.fetch(race, j, V, 1.0f);
                         }
                         float2 d[4];
@@ -405,7 +419,7 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
             },
             [&](VfPart& x, const VfPart& y) {
                 const float top = fmaxf(x.m, y.m);
-                const float gx = x.m == top ? 0.0f : (x.m - top) * chi, gy = y.m == top ? 0.0f : (y.m - top) * chi;
+                const float gx = x.m == top ? 0.0f : __fmul_rn(x.m - top, chi), gy = y.m == top ? 0.0f : __fmul_rn(y.m - top, chi);
                 x.s = __fadd_rn(__fmul_rn(x.s, ex2(gx)), __fmul_rn(y.s, ex2(gy)));
                 if (greedy) first_of(x.m, x.v, y.m, y.v);
                 x.m = top;
@@ -418,7 +432,7 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                 const float own = x.m;
                 if (greedy) first_of_all(x.m, x.v);
                 else x.m = warp_max(x.m);
-                const float g = own == x.m ? 0.0f : (own - x.m) * chi;
+                const float g = own == x.m ? 0.0f : __fmul_rn(own - x.m, chi);
                 x.s *= ex2(g);
                 sum_of_all(x.s);
                 if (run) {
@@ -510,8 +524,8 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                     [&](int vw, VfPart& x) {
 #pragma unroll 1
                         for (unsigned j0 = vw * 32 + lane; j0 - lane < chunks; j0 += GROUP * VF_STEP) {
-                            Chunk<F32> c[GROUP];
-                            Chunk<true> qc[GROUP];
+                            Chunk<F32, EVEN> c[GROUP];
+                            Chunk<true, EVEN> qc[GROUP];
                             ask(c, row, j0, -INFINITY);
                             ask(qc, q, j0, 0.0f);
 #pragma unroll
@@ -556,8 +570,8 @@ __global__ void __launch_bounds__(VF_MAX_THREADS, 2) verify_kernel(const __grid_
                     const bool some = !all && meets(vw);
 #pragma unroll 1
                     for (unsigned j0 = vw * 32 + lane; j0 - lane < chunks; j0 += 2 * VF_STEP) {
-                        Chunk<F32> c[2];
-                        Chunk<true> rc[2], qc[2];
+                        Chunk<F32, EVEN> c[2];
+                        Chunk<true, EVEN> rc[2], qc[2];
                         ask(c, row, j0, -INFINITY);
                         ask(rc, race, j0, 1.0f);
                         if (!own) ask(qc, q, j0, 0.0f);
@@ -646,7 +660,9 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? (1ull << dev) : 0;
     if (!bit || !(configured.load() & bit)) {
-        for (const void* f : {(const void*)verify_kernel<false, 2>, (const void*)verify_kernel<false, 4>, (const void*)verify_kernel<true, 1>})
+        for (const void* f : {(const void*)verify_kernel<false, 2, false>, (const void*)verify_kernel<false, 4, false>,
+                              (const void*)verify_kernel<true, 1, false>, (const void*)verify_kernel<false, 2, true>,
+                              (const void*)verify_kernel<false, 4, true>, (const void*)verify_kernel<true, 1, true>})
             if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
@@ -667,11 +683,21 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     // Chunks of a lane, asked for at a time: in BF16 up to two where that is all (two rounds of VF_STEP chunks).  64 rows of 8
-    // accepted nodes by 2 / by 4 in us: V = 16384 29.3 / 31.6, 32768 33.0 / 36.4, 40000 41.3 / 39.2, 65536 44.7 / 42.1, 98304
-    // 57.7 / 57.0, 131072 69.7 / 62.4; one row 32768 20.2 / 21.3, 65536 23.4 / 22.7, 131072 31.2 / 29.6.  In FP32 20 x 100003
+    // accepted nodes by 2 / by 4 in us: V = 16384 27.5 / 28.8, 32768 32.3 / 33.9, 40000 40.4 / 36.5, 65536 44.5 / 42.1, 98304
+    // 57.5 / 54.6, 131072 70.0 / 62.2; one row 32768 19.4 / 20.1, 40000 20.9 / 20.8, 131072 30.1 / 29.4.  In FP32 20 x 100003
     // 30.1 with 1, 30.8 with 2.
-    if (a.f32) return cudaLaunchKernelEx(&cfg, verify_kernel<true, 1>, r);
-    return a.V <= 2 * 8 * VF_STEP ? cudaLaunchKernelEx(&cfg, verify_kernel<false, 2>, r) : cudaLaunchKernelEx(&cfg, verify_kernel<false, 4>, r);
+    // Rows that all start at 16 bytes and are whole chunks do without the code for the ends of others: one row of 8 x 32000
+    // 12.4 us a call, 13.6 with it; 64 x 8 x 131072 45.8 and 46.3.  (Every product that is added to is rounded by itself, so
+    // that both have the same bits.)
+    const bool two = a.V <= 2 * 8 * VF_STEP;
+    const bool even = a.V % 8 == 0 && ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.draft_probs) |
+                                        reinterpret_cast<uintptr_t>(a.race)) & 15u) == 0;
+    if (even) {
+        if (a.f32) return cudaLaunchKernelEx(&cfg, verify_kernel<true, 1, true>, r);
+        return two ? cudaLaunchKernelEx(&cfg, verify_kernel<false, 2, true>, r) : cudaLaunchKernelEx(&cfg, verify_kernel<false, 4, true>, r);
+    }
+    if (a.f32) return cudaLaunchKernelEx(&cfg, verify_kernel<true, 1, false>, r);
+    return two ? cudaLaunchKernelEx(&cfg, verify_kernel<false, 2, false>, r) : cudaLaunchKernelEx(&cfg, verify_kernel<false, 4, false>, r);
 }
 
 }  // namespace rk

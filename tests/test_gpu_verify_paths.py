@@ -72,7 +72,7 @@ def test_the_last_token_of_every_way(V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("V", [1, 7, 8, 9, 15, 16, 17, 23, 24, 25, 40, 1003])
+@pytest.mark.parametrize("V", [1, 7, 8, 9, 15, 16, 17, 23, 24, 25, 40, 1003, 16392, 40000])
 def test_arrays_that_begin_and_end_anywhere_among_others(V, dtype):
     """Logits, probabilities and draws cut out of larger arrays of NaN, at every element of 16 bytes: the bits of
     arrays of their own."""
