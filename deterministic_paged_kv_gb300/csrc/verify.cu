@@ -21,7 +21,7 @@
 // reaches.  A pass deals the vocabulary in chunks of 8 to the lanes of 64 virtual warps, a lane's chunks in
 // ascending order (in groups of one, two or four, with the lane's running maximum), and joins lanes and warps in a fixed tree, so a
 // row's results depend on its data, type and V alone: not on the cluster, nor on how a row lies in memory (a row that does
-// not start at 16 bytes is read in whole vectors and shifted).  A warp pushes its partial results into every CTA's
+// not start at 16 bytes is read in whole vectors and shifted, and its ends value by value).  A warp pushes its partial results into every CTA's
 // shared memory; behind one cluster barrier a pass every warp joins them and decides for itself.
 //
 // What bounds it: for few rows the chain of passes, 2.2 us each at V = 32000 (a load, two joins, a cluster barrier, and the
@@ -29,8 +29,8 @@
 // 64 rows of 8 accepted nodes at V = 131072 59 us (63 without probabilities), 7 us a pass, whose 17 MB take 2.5 and whose exponentials take as
 // much.  Of a pass's 12700 cycles the first chunks' way is 1500, a group of four chunks 1100 (four of them), the joins and
 // pushes of two virtual warps 1200, the barrier 1300, the last join 750, the decision 1200.  With rows that end early and
-// draft probabilities 37 us (44 with nothing of it in L2).  FP32 logits with draft probabilities, all nodes accepted: 64 x 8 x 131072
-// 95 us and 20 x 13 x 100003 101, of which their bytes take 40 and 15.  Measured against that: chunks asked for only when the
+// draft probabilities 36 us (43 with nothing of it in L2).  FP32 logits with draft probabilities, all nodes accepted: 64 x 8 x 131072
+// 94 us and 20 x 13 x 100003 102, of which their bytes take 40 and 15.  Measured against that: chunks asked for only when the
 // ones before are summed 71 and 42; 128 virtual warps 20% slower, 32 in FP32 40%; rows fetched to L2 ahead, no change.
 #include <algorithm>
 #include <atomic>
