@@ -132,3 +132,18 @@ def test_a_row_without_a_root_drops_nothing_whatever_its_temperature(temp):
     got = _run(c)  # (no status)
     assert all(torch.equal(x.view(i32), y.view(i32)) for x, y in zip(want, got))
     assert got[0][1::2].tolist() == [0, 0] and got[1][1::2].tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("which", ["logits", "draft_probs", "race"])
+@pytest.mark.parametrize("V", [1000, 4096, 33000])
+def test_one_array_alone_off_its_alignment(V, which, dtype):
+    """Rows of whole chunks of which one array does not start at 16 bytes, with children refused and accepted."""
+    c = ref.verify_case(700 + V, 20, 5, V, dtype, True, ["tree", "star"])
+    c["coins"][::3] = 0.999
+    want = _run(c)
+    n = c[which].numel()
+    flat = torch.full((n + 8,), math.nan, dtype=c[which].dtype, device="cuda")
+    flat[1:n + 1] = c[which].cuda().view(-1)
+    got = _run(dict(c, **{which: flat[1:n + 1].view(c[which].shape)}))
+    assert all(torch.equal(x.view(i32), y.view(i32)) for x, y in zip(want, got))
